@@ -12,6 +12,9 @@ error.
 "Debajo del capó: CUTLASS en Hopper" (7minutos.es):
 q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state,
 final_state, cu_seqlens.
+
+The operators around the recurrence (RMS normalisation, short convolution,
+state-space scan) are in ``layer`` and are offered here as well.
 """
 from __future__ import annotations
 
@@ -22,13 +25,18 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import layer
 from ._build import LIB as LIB_PATH
 from ._build import build
+from .layer import (conv_bwd, conv_bwd_workspace_size, conv_decode, conv_fwd, rms_norm, rmsnorm_bwd,
+                    rmsnorm_bwd_workspace_size, rmsnorm_fwd, rmsnorm_quant, short_conv, ssm_decode)
 
 __all__ = ["fwd", "fwd_noalloc", "noalloc_max_workspace", "decode", "bwd", "bwd_workspace_size",
            "kda_attention", "KdaFunction", "workspace_size", "chain_segments_for",
            "pipelined_for", "KdaArgumentError", "library", "KdaError", "build", "LIB_PATH", "KDA_BF16",
-           "KDA_FP32"]
+           "KDA_FP32",
+           "rmsnorm_fwd", "rmsnorm_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "rms_norm",
+           "conv_fwd", "conv_decode", "conv_bwd", "conv_bwd_workspace_size", "short_conv", "ssm_decode"]
 
 KDA_BF16 = 1
 KDA_FP32 = 2
@@ -107,6 +115,7 @@ def library() -> ctypes.CDLL:
             lib.kda_bwd_workspace_size.argtypes = [ctypes.POINTER(KdaDesc)]
             lib.kda_status_string.restype = ctypes.c_char_p
             lib.kda_status_string.argtypes = [ctypes.c_int]
+            layer._declare(lib)
             _lib = lib
     return _lib
 

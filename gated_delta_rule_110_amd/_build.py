@@ -11,8 +11,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_intra.hip", "kda_chain.hip", "kda_fused.hip", "kda_segment.hip", "kda_decode.hip", "kda_bwd.hip",
-           "kda_api.hip"]
-HEADERS = [os.path.join(CSRC, "kda_common.h"), os.path.join(CSRC, "kda_intra_body.h"), os.path.join(INCLUDE, "kda.h")]
+           "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm_decode.hip", "kda_layer_api.hip"]
+HEADERS = [os.path.join(CSRC, "kda_common.h"), os.path.join(CSRC, "kda_intra_body.h"),
+           os.path.join(CSRC, "kda_layer_args.h"), os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_layer.h")]
 
 # -packed-fp32-ops off: hipcc must not emit packed fp32 VALU instructions.
 HIPCC_FLAGS = [

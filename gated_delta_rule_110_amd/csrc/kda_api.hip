@@ -184,12 +184,12 @@ extern "C" const char *kda_status_string(kda_status_t s) {
     switch (s) {
         case KDA_OK: return "ok";
         case KDA_ERR_NULL: return "a required pointer is NULL";
-        case KDA_ERR_SHAPE: return "invalid shape (B, H >= 1, T >= 0; num_seqs == B, or B == 1 with cu_seqlens)";
-        case KDA_ERR_UNSUPPORTED: return "unsupported head dimension (K and V must be 128)";
-        case KDA_ERR_PARAM: return "invalid parameter (lower_bound must be finite and in [-5, 0]; scale finite)";
-        case KDA_ERR_DTYPE: return "state dtype must be KDA_BF16 or KDA_FP32";
+        case KDA_ERR_SHAPE: return "invalid shape (B, H >= 1, T >= 0; num_seqs == B, or B == 1 with cu_seqlens; strides >= 0)";
+        case KDA_ERR_UNSUPPORTED: return "unsupported head dimension (K and V must be 128; a scan's P and N 64 or 128, a convolution's W 2, 3 or 4)";
+        case KDA_ERR_PARAM: return "invalid parameter (lower_bound must be finite and in [-5, 0]; scale finite; eps finite and positive)";
+        case KDA_ERR_DTYPE: return "state and parameter dtypes must be KDA_BF16 or KDA_FP32";
         case KDA_ERR_ALIGN: return "misaligned pointer (tensors 16 bytes, workspace 256 bytes)";
-        case KDA_ERR_WORKSPACE: return "workspace smaller than kda_fwd_workspace_size()";
+        case KDA_ERR_WORKSPACE: return "workspace smaller than the call's workspace size function asks for";
         case KDA_ERR_HIP: return "HIP launch error";
         case KDA_ERR_SCRATCH: return "workspace need exceeds the static scratch of kda_fwd_noalloc (kda_fwd_noalloc_max_workspace() bytes)";
     }

@@ -1,0 +1,483 @@
+// kda_conv.hip -- the short causal depthwise convolution (gfx950): prompts,
+// one token per sequence, and the gradient.
+//
+//   pre_t = bias + sum_k w_k x_{t - (W - 1) + k},   out_t = pre_t or silu(pre_t)
+//
+// per channel, the W - 1 inputs before a sequence's first token coming from its
+// state.  Two operations per loaded value and tap: bound by memory traffic (x
+// once, out once).  A lane holds 8 neighbouring channels (16 bytes per token
+// and access, 1 KiB per wave) and walks over a run of tokens with the last
+// W - 1 inputs in registers, so that x is read once plus W - 1 rows per run.
+// Where the channel count, a stride or an address does not allow 16-byte
+// accesses, the same code runs with one channel per lane.
+#include "kda_layer_args.h"
+
+using namespace kda;
+
+namespace {
+
+constexpr int kLanes = 64;       // channel groups per workgroup (one wave wide)
+constexpr int kWaves = 4;        // token runs per workgroup
+constexpr int kRun = 16;         // tokens per run, forward: their loads are all in flight together
+constexpr int kBwdRun = 32;      // tokens per run, gradient
+constexpr int64_t kMaxGridY = 65535;
+
+template <int kC>
+__device__ __forceinline__ void load_c(const uint16_t *p, float *o) {
+    if constexpr (kC == 8) unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), o);
+    else o[0] = bf16_bits_to_f32(*p);
+}
+template <int kC>
+__device__ __forceinline__ void store_c(uint16_t *p, const float *v) {
+    if constexpr (kC == 8)
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    else *p = f32_to_bf16_bits(v[0]);
+}
+// kC entries of a state or parameter row of either type.
+template <int kC>
+__device__ __forceinline__ void load_any_c(const void *p, int64_t i, int f32, float *o) {
+    if constexpr (kC == 8) {
+        if (f32) {
+            const float4 a = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+            const float4 b = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + 4);
+            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+            o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        } else {
+            load_c<8>(reinterpret_cast<const uint16_t *>(p) + i, o);
+        }
+    } else {
+        o[0] = load_any(p, i, f32);
+    }
+}
+template <int kC>
+__device__ __forceinline__ void store_f32_c(float *p, const float *v) {
+    if constexpr (kC == 8) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        p[0] = v[0];
+    }
+}
+template <int kC>
+__device__ __forceinline__ void store_any_c(void *p, int64_t i, int f32, const float *v) {
+    if (f32) store_f32_c<kC>(reinterpret_cast<float *>(p) + i, v);
+    else store_c<kC>(reinterpret_cast<uint16_t *>(p) + i, v);
+}
+
+// The lane's filter: w[k][e] for channel c + e.
+template <int kC, int kW>
+__device__ __forceinline__ void load_filter(const ConvArgs &a, int64_t c, float (&w)[kW][kC], float (&b)[kC]) {
+#pragma unroll
+    for (int e = 0; e < kC; ++e) {
+        b[e] = a.bias ? load_any(a.bias, c + e, a.w_f32) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) w[k][e] = load_any(a.w, (c + e) * kW + k, a.w_f32);
+    }
+}
+
+// Sequences of a batch: their first token and the one behind their last, in
+// the flat order b T + t.  Lengths are clamped to the batch's tokens.
+struct Seqs {
+    const int64_t *cu;
+    int64_t T, N, total;
+    __device__ __forceinline__ int64_t begin(int64_t n) const { return cu ? clamp(cu[n]) : n * T; }
+    __device__ __forceinline__ int64_t end(int64_t n) const { return cu ? clamp(cu[n + 1]) : (n + 1) * T; }
+    __device__ __forceinline__ int64_t clamp(int64_t v) const { return v < 0 ? 0 : v > total ? total : v; }
+    // The sequence that holds token t, or N if none does (t behind the last):
+    // the first n with end(n) > t, by halving.
+    __device__ __forceinline__ int64_t of(int64_t t) const {
+        if (!cu) return t / T;
+        int64_t lo = 0, hi = N;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
+        }
+        return lo;
+    }
+};
+__device__ __forceinline__ Seqs seqs_of(const ConvArgs &a) { return Seqs{a.cu, a.T, a.N, a.B * a.T}; }
+
+// Row of x (or dy) of the flat token t.
+__device__ __forceinline__ int64_t row_of(int64_t t, int64_t T, int64_t sb, int64_t st) {
+    const int64_t b = t / T;
+    return b * sb + (t - b * T) * st;
+}
+
+// Input number pos (may be negative: from the state) of sequence n.
+template <int kC, int kW>
+__device__ __forceinline__ void input_at(const ConvArgs &a, int64_t n, int64_t begin, int64_t pos, int64_t c, float *o) {
+    if (pos >= 0) {
+        load_c<kC>(a.x + row_of(begin + pos, a.T, a.xb, a.xt) + c, o);
+    } else if (a.h0 && pos >= -(kW - 1)) {
+        load_any_c<kC>(a.h0, (n * (kW - 1) + (kW - 1) + pos) * a.D + c, a.h0_f32, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kC; ++e) o[e] = 0.f;
+    }
+}
+
+template <int kC, int kW>
+__device__ __forceinline__ void convolve(const float (&w)[kW][kC], const float (&b)[kC], const float (&win)[kW][kC],
+                                         float *pre) {
+#pragma unroll
+    for (int e = 0; e < kC; ++e) {
+        float p = b[e];
+#pragma unroll
+        for (int k = 0; k < kW; ++k) p += w[k][e] * win[k][e];
+        pre[e] = p;
+    }
+}
+
+template <int kC, int kW>
+__global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
+    const int64_t c = ((int64_t)blockIdx.x * kLanes + (threadIdx.x & 63)) * kC;
+    if (c >= a.D) return;
+    const Seqs sq = seqs_of(a);
+    float w[kW][kC], b[kC];
+    load_filter<kC, kW>(a, c, w, b);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    for (int64_t t0 = ((int64_t)blockIdx.y * kWaves + wave) * kRun; t0 < sq.total;
+         t0 += (int64_t)gridDim.y * kWaves * kRun) {
+        const int64_t stop = t0 + kRun < sq.total ? t0 + kRun : sq.total;
+        int64_t n = sq.of(t0);
+        if (n >= sq.N) return;  // behind the last sequence, and so are later runs
+        float x[kRun][kC];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            if (t0 + i < stop) load_c<kC>(a.x + row_of(t0 + i, a.T, a.xb, a.xt) + c, x[i]);
+        // win[k]: the input k steps after the oldest one that t0 needs
+        float win[kW][kC];
+        int64_t begin = sq.begin(n), next = sq.end(n);
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, t0 - begin - (kW - 1) + k, c, win[k]);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int64_t t = t0 + i;
+            if (t >= stop) break;
+            if (t >= next) {  // the next sequence that has tokens
+                do { ++n; } while (n < sq.N && sq.end(n) <= t);
+                if (n >= sq.N) break;
+                begin = sq.begin(n);
+                next = sq.end(n);
+#pragma unroll
+                for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, t - begin - (kW - 1) + k, c, win[k]);
+            }
+            float pre[kC];
+#pragma unroll
+            for (int e = 0; e < kC; ++e) win[kW - 1][e] = x[i][e];
+            convolve<kC, kW>(w, b, win, pre);
+            if (a.silu) {
+#pragma unroll
+                for (int e = 0; e < kC; ++e) pre[e] *= sigmoid(pre[e]);
+            }
+            store_c<kC>(a.out + t * a.D + c, pre);
+#pragma unroll
+            for (int k = 0; k < kW - 1; ++k)
+#pragma unroll
+                for (int e = 0; e < kC; ++e) win[k][e] = win[k + 1][e];
+        }
+    }
+}
+
+// The final states: the last W - 1 inputs of every sequence.  A thread reads
+// all its entries before it writes them, so that ht may be h0; it is launched
+// after the convolution, which reads h0.
+template <int kC, int kW>
+__global__ __launch_bounds__(256) void kda_conv_state_kernel(ConvArgs a) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kC;
+    if (c >= a.D) return;
+    const Seqs sq = seqs_of(a);
+    for (int64_t n = blockIdx.y; n < sq.N; n += gridDim.y) {
+        const int64_t begin = sq.begin(n), len = sq.end(n) > begin ? sq.end(n) - begin : 0;
+        float v[kW - 1][kC];
+#pragma unroll
+        for (int j = 0; j < kW - 1; ++j) input_at<kC, kW>(a, n, begin, len - (kW - 1) + j, c, v[j]);
+#pragma unroll
+        for (int j = 0; j < kW - 1; ++j) store_any_c<kC>(a.ht, (n * (kW - 1) + j) * a.D + c, a.ht_f32, v[j]);
+    }
+}
+
+// One token per sequence: output and shifted state in one launch.
+template <int kC, int kW>
+__global__ __launch_bounds__(64) void kda_conv_decode_kernel(ConvArgs a) {
+    const int64_t c = ((int64_t)blockIdx.x * 64 + threadIdx.x) * kC;
+    if (c >= a.D) return;
+    for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
+        float win[kW][kC], w[kW][kC], b[kC], pre[kC];
+        load_c<kC>(a.x + n * a.xb + c, win[kW - 1]);
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, 0, k - (kW - 1), c, win[k]);
+        load_filter<kC, kW>(a, c, w, b);
+        convolve<kC, kW>(w, b, win, pre);
+        if (a.silu) {
+#pragma unroll
+            for (int e = 0; e < kC; ++e) pre[e] *= sigmoid(pre[e]);
+        }
+        store_c<kC>(a.out + n * a.D + c, pre);
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) store_any_c<kC>(a.ht, (n * (kW - 1) + k) * a.D + c, a.ht_f32, win[k + 1]);
+    }
+}
+
+// ---- gradient ----------------------------------------------------------------
+//
+//   dpre_t = d_out_t act'(pre_t),   dx_t = sum_k w_k dpre_{t + (W - 1) - k}
+//   (tokens of the same sequence) + d_final_state,   dw_k = sum_t dpre_t x_{t - (W - 1) + k}
+//
+// A wave walks over its run and W - 1 tokens further, computing pre again; each
+// dpre is added to the W pending dx entries it reaches (pend[k] is that of
+// token t - (W - 1) + k), and the oldest one is written.  At the end of a
+// sequence the pending ones are complete.
+
+// The derivative of the activation, times g.  For silu, with s = sigmoid(p):
+// s (1 + p (1 - s)).
+__device__ __forceinline__ float act_grad(float p, float g, int silu) {
+    if (!silu) return g;
+    const float s = sigmoid(p);
+    return g * s * (1.0f + p * (1.0f - s));
+}
+
+template <int kC, int kW>
+struct BwdWalk {
+    const ConvArgs &a;
+    const Seqs &sq;
+    int64_t c, t0, stop;      // the run whose dx this wave writes
+    int64_t n, begin, next;
+    float pend[kW][kC];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kW; ++k)
+#pragma unroll
+            for (int e = 0; e < kC; ++e) pend[k][e] = 0.f;
+    }
+    // dx of token t, complete but for the final state's share.
+    __device__ __forceinline__ void emit(int64_t t, const float *v) {
+        if (t < t0 || t >= stop || t < begin) return;
+        float o[kC];
+#pragma unroll
+        for (int e = 0; e < kC; ++e) o[e] = v[e];
+        const int64_t j = t - (next - (kW - 1));
+        if (a.dht && j >= 0) {
+            float d[kC];
+            load_any_c<kC>(a.dht, (n * (kW - 1) + j) * a.D + c, a.ht_f32, d);
+#pragma unroll
+            for (int e = 0; e < kC; ++e) o[e] += d[e];
+        }
+        store_c<kC>(a.dx + t * a.D + c, o);
+    }
+    // After the last token, t - 1, of a sequence or of the walk.
+    __device__ __forceinline__ void flush(int64_t t) {
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) emit(t - (kW - 1) + k, pend[k]);
+    }
+};
+
+template <int kC, int kW>
+__global__ __launch_bounds__(kLanes *kWaves) void kda_conv_bwd_kernel(ConvArgs a) {
+    __shared__ float red[kWaves][kW + 1][kC][kLanes];
+    const int lane = threadIdx.x & 63;
+    const int64_t c = ((int64_t)blockIdx.x * kLanes + lane) * kC;
+    const bool in = c < a.D;
+    const Seqs sq = seqs_of(a);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    float dw[kW + 1][kC];
+#pragma unroll
+    for (int k = 0; k <= kW; ++k)
+#pragma unroll
+        for (int e = 0; e < kC; ++e) dw[k][e] = 0.f;
+    if (in) {
+        float w[kW][kC], b[kC];
+        load_filter<kC, kW>(a, c, w, b);
+        for (int64_t t0 = ((int64_t)blockIdx.y * kWaves + wave) * kBwdRun; t0 < sq.total;
+             t0 += (int64_t)gridDim.y * kWaves * kBwdRun) {
+            BwdWalk<kC, kW> s{a, sq, c, t0, t0 + kBwdRun < sq.total ? t0 + kBwdRun : sq.total, sq.of(t0), 0, 0, {}};
+            if (s.n >= sq.N) break;
+            s.clear();
+            s.begin = sq.begin(s.n);
+            s.next = sq.end(s.n);
+            float win[kW][kC];
+#pragma unroll
+            for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, s.n, s.begin, t0 - s.begin - (kW - 1) + k, c, win[k]);
+            int64_t t = t0;
+            for (; t < s.stop + kW - 1; ++t) {
+                if (t >= s.next) {
+                    s.flush(t);
+                    s.clear();
+                    if (t >= s.stop) break;
+                    do { ++s.n; } while (s.n < sq.N && sq.end(s.n) <= t);
+                    if (s.n >= sq.N) break;
+                    s.begin = sq.begin(s.n);
+                    s.next = sq.end(s.n);
+#pragma unroll
+                    for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, s.n, s.begin, t - s.begin - (kW - 1) + k, c, win[k]);
+                }
+                float g[kC], pre[kC];
+                load_c<kC>(a.x + row_of(t, a.T, a.xb, a.xt) + c, win[kW - 1]);
+                load_c<kC>(a.dy + row_of(t, a.T, a.db_, a.dt_) + c, g);
+                convolve<kC, kW>(w, b, win, pre);
+#pragma unroll
+                for (int e = 0; e < kC; ++e) {
+                    const float d = act_grad(pre[e], g[e], a.silu);
+                    // pend[k] is token t - (W - 1) + k, which tap k of token t reads
+#pragma unroll
+                    for (int k = 0; k < kW; ++k) s.pend[k][e] += w[k][e] * d;
+                    if (t < s.stop) {
+#pragma unroll
+                        for (int k = 0; k < kW; ++k) dw[k][e] += d * win[k][e];
+                        dw[kW][e] += d;
+                    }
+                }
+                s.emit(t - (kW - 1), s.pend[0]);
+#pragma unroll
+                for (int k = 0; k < kW - 1; ++k)
+#pragma unroll
+                    for (int e = 0; e < kC; ++e) {
+                        win[k][e] = win[k + 1][e];
+                        s.pend[k][e] = s.pend[k + 1][e];
+                    }
+#pragma unroll
+                for (int e = 0; e < kC; ++e) s.pend[kW - 1][e] = 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= kW; ++k)
+#pragma unroll
+        for (int e = 0; e < kC; ++e) red[wave][k][e][lane] = dw[k][e];
+    __syncthreads();
+    if (!in) return;
+    for (int k = wave; k <= kW; k += kWaves) {
+        float v[kC];
+#pragma unroll
+        for (int e = 0; e < kC; ++e) {
+            v[e] = red[0][k][e][lane];
+#pragma unroll
+            for (int q = 1; q < kWaves; ++q) v[e] += red[q][k][e][lane];
+        }
+        store_f32_c<kC>(a.part + ((int64_t)blockIdx.y * (kW + 1) + k) * a.D + c, v);
+    }
+}
+
+// dweight and dbias: the sum of the partial sums, in a fixed order.  A workgroup
+// takes 64 channels of one tap, 4 waves over the parts.
+template <int kW>
+__global__ __launch_bounds__(256) void kda_conv_bwd_sum_kernel(ConvArgs a) {
+    __shared__ float s[4][64];
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, k = blockIdx.y;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float v = 0.f;
+    if (c < a.D)
+        for (int64_t p = q; p < a.parts; p += 4) v += a.part[(p * (kW + 1) + k) * a.D + c];
+    s[q][lane] = v;
+    __syncthreads();
+    if (q != 0 || c >= a.D) return;
+    v = s[0][lane] + s[1][lane] + s[2][lane] + s[3][lane];
+    if (k < kW) a.dw[c * kW + k] = v;
+    else if (a.dbias) a.dbias[c] = v;
+}
+
+// The initial state's gradient: entry m (input m - (W - 1)) reaches the tokens
+// p <= m through tap m - p, and, in a sequence shorter than W - 1, the final
+// state's entry m - length.
+template <int kC, int kW>
+__global__ __launch_bounds__(64) void kda_conv_bwd_state_kernel(ConvArgs a) {
+    const int64_t c = ((int64_t)blockIdx.x * 64 + threadIdx.x) * kC;
+    if (c >= a.D) return;
+    const Seqs sq = seqs_of(a);
+    float w[kW][kC], b[kC];
+    load_filter<kC, kW>(a, c, w, b);
+    for (int64_t n = blockIdx.y; n < sq.N; n += gridDim.y) {
+        const int64_t begin = sq.begin(n), len = sq.end(n) > begin ? sq.end(n) - begin : 0;
+        float d[kW - 1][kC];
+#pragma unroll
+        for (int m = 0; m < kW - 1; ++m) {
+#pragma unroll
+            for (int e = 0; e < kC; ++e) d[m][e] = 0.f;
+            if (a.dht && m >= len) load_any_c<kC>(a.dht, (n * (kW - 1) + m - len) * a.D + c, a.ht_f32, d[m]);
+        }
+#pragma unroll
+        for (int p = 0; p < kW - 1; ++p) {
+            if (p >= len) break;
+            float win[kW][kC], g[kC], pre[kC];
+#pragma unroll
+            for (int k = 0; k < kW; ++k) input_at<kC, kW>(a, n, begin, p - (kW - 1) + k, c, win[k]);
+            load_c<kC>(a.dy + row_of(begin + p, a.T, a.db_, a.dt_) + c, g);
+            convolve<kC, kW>(w, b, win, pre);
+#pragma unroll
+            for (int e = 0; e < kC; ++e) {
+                const float dp = act_grad(pre[e], g[e], a.silu);
+#pragma unroll
+                for (int m = p; m < kW - 1; ++m) d[m][e] += w[m - p][e] * dp;
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kW - 1; ++m) store_f32_c<kC>(a.dh0 + (n * (kW - 1) + m) * a.D + c, d[m]);
+    }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// 16-byte accesses to every tensor of the call (states and partial sums have
+// rows of D entries, so D a multiple of 8 keeps them aligned too).
+bool vector_channels(const ConvArgs &a) {
+    return a.D % 8 == 0 && a.xb % 8 == 0 && a.xt % 8 == 0 && a.db_ % 8 == 0 && a.dt_ % 8 == 0 && aligned16(a.x) &&
+           aligned16(a.out) && aligned16(a.h0) && aligned16(a.ht) && aligned16(a.dy) && aligned16(a.dht) &&
+           aligned16(a.dx) && aligned16(a.dh0);
+}
+
+unsigned blocks_x(int64_t D, int kC, int lanes) { return (unsigned)((D + (int64_t)kC * lanes - 1) / ((int64_t)kC * lanes)); }
+unsigned blocks_y(int64_t n, int64_t per) {
+    const int64_t b = (n + per - 1) / per;
+    return (unsigned)(b < 1 ? 1 : b < kMaxGridY ? b : kMaxGridY);
+}
+
+template <int kC, int kW>
+hipError_t launch_conv(const ConvArgs &a, hipStream_t s) {
+    if (a.B * a.T > 0)
+        hipLaunchKernelGGL((kda_conv_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), blocks_y(a.B * a.T, kRun * kWaves)),
+                           dim3(kLanes * kWaves), 0, s, a);
+    if (a.ht)
+        hipLaunchKernelGGL((kda_conv_state_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 256), blocks_y(a.N, 1)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int kC, int kW>
+hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s) {
+    ConvArgs b = a;
+    if (a.B * a.T > 0)
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), (unsigned)a.parts),
+                           dim3(kLanes * kWaves), 0, s, a);
+    else b.parts = 0;
+    hipLaunchKernelGGL((kda_conv_bwd_sum_kernel<kW>), dim3(blocks_x(a.D, 1, 64), kW + 1), dim3(256), 0, s, b);
+    if (a.dh0)
+        hipLaunchKernelGGL((kda_conv_bwd_state_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 64), blocks_y(a.N, 1)), dim3(64), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int kC, int kW>
+hipError_t launch_decode(const ConvArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((kda_conv_decode_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 64), blocks_y(a.N, 1)), dim3(64), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+#define KDA_CONV_DISPATCH(fn)                                                          \
+    if (vector_channels(a)) return W == 2 ? fn<8, 2>(a, s) : W == 3 ? fn<8, 3>(a, s) : fn<8, 4>(a, s); \
+    return W == 2 ? fn<1, 2>(a, s) : W == 3 ? fn<1, 3>(a, s) : fn<1, 4>(a, s)
+
+hipError_t kda_launch_conv(const ConvArgs &a, int W, hipStream_t s) { KDA_CONV_DISPATCH(launch_conv); }
+
+hipError_t kda_launch_conv_decode(const ConvArgs &a, int W, hipStream_t s) { KDA_CONV_DISPATCH(launch_decode); }
+
+// Workgroups along the tokens of the gradient, each of which writes a partial
+// sum of dweight and dbias.
+int64_t kda_conv_parts(int64_t B, int64_t T, int64_t D) {
+    (void)D;
+    const int64_t n = (B * T + kBwdRun * kWaves - 1) / (kBwdRun * kWaves);
+    return n < 1 ? 1 : n < 256 ? n : 256;
+}
+
+hipError_t kda_launch_conv_bwd(const ConvArgs &a, int W, hipStream_t s) { KDA_CONV_DISPATCH(launch_conv_bwd); }

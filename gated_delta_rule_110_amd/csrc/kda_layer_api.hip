@@ -1,0 +1,342 @@
+// kda_layer_api.hip -- the C ABI of the layer operators (include/kda_layer.h):
+// validation, workspaces, launches.
+#include <math.h>
+#include <stdlib.h>
+#include <new>
+#include <vector>
+#include "kda_layer.h"
+#include "kda_layer_args.h"
+
+using namespace kda;
+
+namespace {
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool dtype_ok(int32_t d) { return d == KDA_BF16 || d == KDA_FP32; }
+size_t width(int32_t d) { return d == KDA_FP32 ? 4 : 2; }
+
+// Sizes beyond these are refused, so that no product of a call's sizes passes
+// 63 bits (rows and columns) or a grid's 2^31 - 1 workgroups.
+constexpr int64_t kMaxTokens = int64_t(1) << 40;
+constexpr int64_t kMaxColumns = int64_t(1) << 22;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxSeqs = 0x7fffffff;
+
+bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
+
+// The workspace of a call: the caller's, or one taken on the stream and given
+// back behind the call's kernels.
+class Workspace {
+public:
+    Workspace(void *given, size_t bytes, size_t need, hipStream_t s) : p_(given), s_(s) {
+        if (need == 0) return;
+        if (given) {
+            status_ = !aligned(given, 256) ? KDA_ERR_ALIGN : bytes < need ? KDA_ERR_WORKSPACE : KDA_OK;
+        } else {
+            owned_ = hipMallocAsync(&p_, need, s) == hipSuccess;
+            if (!owned_) status_ = KDA_ERR_HIP;
+        }
+    }
+    ~Workspace() {
+        if (owned_) (void)hipFreeAsync(p_, s_);
+    }
+    Workspace(const Workspace &) = delete;
+    Workspace &operator=(const Workspace &) = delete;
+    kda_status_t status() const { return status_; }
+    char *at(size_t off) const { return static_cast<char *>(p_) + off; }
+
+private:
+    void *p_;
+    hipStream_t s_;
+    bool owned_ = false;
+    kda_status_t status_ = KDA_OK;
+};
+
+kda_status_t of_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+
+// KDA_VALIDATE=1: the contents of cu_seqlens, read back to the host.
+kda_status_t validate_cu(const int64_t *cu, int64_t N, int64_t T, hipStream_t stream) {
+    const char *e = getenv("KDA_VALIDATE");
+    if (!cu || !(e && e[0] == '1' && e[1] == 0)) return KDA_OK;
+    int64_t *h = new (std::nothrow) int64_t[(size_t)N + 1];
+    if (!h) return KDA_ERR_HIP;
+    kda_status_t st = KDA_OK;
+    if (hipMemcpyAsync(h, cu, sizeof(int64_t) * (size_t)(N + 1), hipMemcpyDeviceToHost, stream) != hipSuccess ||
+        hipStreamSynchronize(stream) != hipSuccess) {
+        st = KDA_ERR_HIP;
+    } else {
+        if (h[0] != 0 || h[N] > T) st = KDA_ERR_SHAPE;
+        for (int64_t n = 0; n < N && st == KDA_OK; ++n)
+            if (h[n + 1] < h[n]) st = KDA_ERR_SHAPE;
+    }
+    delete[] h;
+    return st;
+}
+
+// ---- RMS normalisation ----
+
+kda_status_t check_norm(const kda_rmsnorm_desc_t *d) {
+    if (d->rows < 0 || d->D < 1 || d->rows > kMaxTokens || d->D > kMaxColumns) return KDA_ERR_SHAPE;
+    if (!(d->eps > 0.0f) || !isfinite(d->eps)) return KDA_ERR_PARAM;
+    if (!stride_ok(d->x_stride)) return KDA_ERR_SHAPE;
+    if (!dtype_ok(d->weight_dtype)) return KDA_ERR_DTYPE;
+    return KDA_OK;
+}
+
+kda_status_t norm_impl(const void *x, const void *residual, const void *weight, void *residual_out, void *out,
+                       float *scales, int quant, const kda_rmsnorm_desc_t *d, hipStream_t stream) {
+    if (!d || !weight) return KDA_ERR_NULL;
+    const kda_status_t st = check_norm(d);
+    if (st != KDA_OK) return st;
+    if (d->rows > 0 && (!x || !out || (quant && !scales))) return KDA_ERR_NULL;
+    if (residual_out && !residual) return KDA_ERR_NULL;
+    if (residual && !dtype_ok(d->residual_dtype)) return KDA_ERR_DTYPE;
+    if (residual && !stride_ok(d->residual_stride)) return KDA_ERR_SHAPE;
+    if (!aligned(x, 2) || (!quant && !aligned(out, 2)) || !aligned(scales, 4) || !aligned(weight, width(d->weight_dtype)) ||
+        (residual && (!aligned(residual, width(d->residual_dtype)) || !aligned(residual_out, width(d->residual_dtype)))))
+        return KDA_ERR_ALIGN;
+    NormArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.res = residual; a.w = weight; a.res_out = residual_out; a.out = out; a.scales = scales;
+    a.rows = d->rows; a.D = d->D; a.xs = d->x_stride; a.rs = d->residual_stride;
+    a.groups = d->group ? (d->D + d->group - 1) / d->group : 1;
+    a.eps = d->eps;
+    a.res_f32 = d->residual_dtype == KDA_FP32;
+    a.w_f32 = d->weight_dtype == KDA_FP32;
+    a.quant = !quant ? 0 : d->group ? 2 : 1;
+    return of_hip(kda_launch_rmsnorm(a, stream));
+}
+
+// ---- short convolution ----
+
+struct ConvShape {
+    ConvArgs a;
+    size_t need;
+};
+
+kda_status_t check_conv(const kda_conv_desc_t *d, bool packed) {
+    if (d->B < 1 || d->T < 0 || d->D < 1 || d->num_seqs < 1) return KDA_ERR_SHAPE;
+    if (d->B > kMaxSeqs || d->num_seqs > kMaxSeqs || d->T > kMaxTokens / d->B || d->D > kMaxColumns) return KDA_ERR_SHAPE;
+    if (packed ? d->B != 1 : d->num_seqs != d->B) return KDA_ERR_SHAPE;
+    if (d->W < 2 || d->W > 4) return KDA_ERR_UNSUPPORTED;
+    if (d->silu != 0 && d->silu != 1) return KDA_ERR_PARAM;
+    if (!stride_ok(d->x_stride_b) || !stride_ok(d->x_stride_t)) return KDA_ERR_SHAPE;
+    if (!dtype_ok(d->weight_dtype)) return KDA_ERR_DTYPE;
+    return KDA_OK;
+}
+
+// What the three calls have in common.
+kda_status_t conv_args(const void *x, const void *weight, const void *bias, const void *h0, const void *ht,
+                       const int64_t *cu, const kda_conv_desc_t *d, ConvArgs &a) {
+    if (!d || !weight) return KDA_ERR_NULL;
+    const kda_status_t st = check_conv(d, cu != nullptr);
+    if (st != KDA_OK) return st;
+    if (d->T > 0 && !x) return KDA_ERR_NULL;
+    if (h0 && !dtype_ok(d->initial_state_dtype)) return KDA_ERR_DTYPE;
+    if (ht && !dtype_ok(d->final_state_dtype)) return KDA_ERR_DTYPE;
+    if (!aligned(x, 2) || !aligned(weight, width(d->weight_dtype)) || !aligned(bias, width(d->weight_dtype)) ||
+        (h0 && !aligned(h0, width(d->initial_state_dtype))) || (ht && !aligned(ht, width(d->final_state_dtype))) ||
+        !aligned(cu, 8))
+        return KDA_ERR_ALIGN;
+    a = ConvArgs{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.w = weight; a.bias = bias; a.h0 = h0; a.cu = cu;
+    a.B = d->B; a.T = d->T; a.D = d->D; a.N = d->num_seqs;
+    a.xb = d->x_stride_b; a.xt = d->x_stride_t;
+    a.silu = d->silu;
+    a.w_f32 = d->weight_dtype == KDA_FP32;
+    a.h0_f32 = d->initial_state_dtype == KDA_FP32;
+    a.ht_f32 = d->final_state_dtype == KDA_FP32;
+    return KDA_OK;
+}
+
+// ---- state-space scan ----
+
+kda_status_t check_ssm(const kda_ssm_desc_t *d, bool packed) {
+    if (d->B < 1 || d->T < 0 || d->H < 1 || d->G < 1 || d->num_seqs < 1) return KDA_ERR_SHAPE;
+    if (d->H > 65535 || d->H % d->G != 0) return KDA_ERR_SHAPE;
+    if (d->B > kMaxSeqs || d->num_seqs > kMaxSeqs || d->T > (int64_t(1) << 31) / d->B) return KDA_ERR_SHAPE;
+    if (packed ? d->B != 1 : d->num_seqs != d->B) return KDA_ERR_SHAPE;
+    if ((d->P != 64 && d->P != 128) || (d->N != 64 && d->N != 128)) return KDA_ERR_UNSUPPORTED;
+    const int64_t strides[] = {d->x_stride_b, d->x_stride_t, d->dt_stride_b, d->dt_stride_t,
+                               d->b_stride_b, d->b_stride_t, d->c_stride_b, d->c_stride_t};
+    for (int64_t s : strides)
+        if (!stride_ok(s)) return KDA_ERR_SHAPE;
+    // x, B and C are read 16 bytes at a time
+    for (int64_t s : {d->x_stride_b, d->x_stride_t, d->b_stride_b, d->b_stride_t, d->c_stride_b, d->c_stride_t})
+        if (s % 8 != 0) return KDA_ERR_ALIGN;
+    if (d->piece_chunks < 0) return KDA_ERR_PARAM;
+    return KDA_OK;
+}
+
+kda_status_t ssm_args(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+                      const float *dt_bias, const float *D, const void *h0, const void *ht, const int64_t *cu,
+                      const kda_ssm_desc_t *d, SsmArgs &a) {
+    if (!d || !A_log) return KDA_ERR_NULL;
+    const kda_status_t st = check_ssm(d, cu != nullptr);
+    if (st != KDA_OK) return st;
+    if (d->T > 0 && (!x || !dt || !Bm || !Cm)) return KDA_ERR_NULL;
+    if (h0 && !dtype_ok(d->initial_state_dtype)) return KDA_ERR_DTYPE;
+    if (ht && !dtype_ok(d->final_state_dtype)) return KDA_ERR_DTYPE;
+    if (!aligned(x, 16) || !aligned(Bm, 16) || !aligned(Cm, 16) || !aligned(h0, 16) || !aligned(ht, 16) || !aligned(dt, 2) ||
+        !aligned(A_log, 4) || !aligned(dt_bias, 4) || !aligned(D, 4) || !aligned(cu, 8))
+        return KDA_ERR_ALIGN;
+    a = SsmArgs{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.dt = static_cast<const uint16_t *>(dt);
+    a.Bm = static_cast<const uint16_t *>(Bm);
+    a.Cm = static_cast<const uint16_t *>(Cm);
+    a.A_log = A_log; a.dt_bias = dt_bias; a.D = D; a.h0 = h0; a.cu = cu;
+    a.B = d->B; a.T = d->T; a.H = d->H; a.P = d->P; a.G = d->G; a.N = d->N; a.num_seqs = d->num_seqs;
+    a.xb = d->x_stride_b; a.xt = d->x_stride_t;
+    a.dtb = d->dt_stride_b; a.dtt = d->dt_stride_t;
+    a.bb = d->b_stride_b; a.bt = d->b_stride_t;
+    a.cb = d->c_stride_b; a.ct = d->c_stride_t;
+    a.h0_f32 = d->initial_state_dtype == KDA_FP32;
+    a.ht_f32 = d->final_state_dtype == KDA_FP32;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" kda_status_t kda_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *residual_out,
+                                        void *out, const kda_rmsnorm_desc_t *desc, hipStream_t stream) {
+    return norm_impl(x, residual, weight, residual_out, out, nullptr, 0, desc, stream);
+}
+
+extern "C" kda_status_t kda_rmsnorm_quant(const void *x, const void *residual, const void *weight,
+                                          void *residual_out, void *out_q, float *scales,
+                                          const kda_rmsnorm_desc_t *desc, hipStream_t stream) {
+    if (desc && desc->group != 0 && desc->group != 128) return KDA_ERR_PARAM;
+    return norm_impl(x, residual, weight, residual_out, out_q, scales, 1, desc, stream);
+}
+
+namespace {
+struct NormBwdLayout {
+    size_t off_rstd, off_part, total;
+    int64_t parts;
+};
+NormBwdLayout norm_bwd_layout(const kda_rmsnorm_desc_t *d) {
+    NormBwdLayout l{};
+    l.parts = kda_rmsnorm_parts(d->rows, d->D);
+    l.off_rstd = 0;
+    l.off_part = align_up((size_t)d->rows * 4, 256);
+    l.total = align_up(l.off_part + (size_t)l.parts * (size_t)d->D * 4, 256);
+    return l;
+}
+}  // namespace
+
+extern "C" size_t kda_rmsnorm_bwd_workspace_size(const kda_rmsnorm_desc_t *desc) {
+    if (!desc || desc->rows < 0 || desc->D < 1 || desc->rows > kMaxTokens || desc->D > kMaxColumns) return 0;
+    return norm_bwd_layout(desc).total;
+}
+
+extern "C" kda_status_t kda_rmsnorm_bwd(const void *h, const void *weight, const void *d_out,
+                                        const void *d_residual_out, void *dx, float *dresidual, float *dweight,
+                                        const kda_rmsnorm_desc_t *desc, hipStream_t stream) {
+    if (!desc || !weight || !dweight) return KDA_ERR_NULL;
+    kda_status_t st = check_norm(desc);
+    if (st != KDA_OK) return st;
+    if (desc->rows > 0 && (!h || !d_out || !dx)) return KDA_ERR_NULL;
+    if (!dtype_ok(desc->residual_dtype)) return KDA_ERR_DTYPE;
+    if (dresidual && desc->residual_dtype != KDA_FP32) return KDA_ERR_DTYPE;
+    if (!stride_ok(desc->d_out_stride) || (d_residual_out && !stride_ok(desc->d_residual_stride))) return KDA_ERR_SHAPE;
+    const size_t hw = width(desc->residual_dtype);
+    if (!aligned(h, hw) || !aligned(d_residual_out, hw) || !aligned(d_out, 2) || !aligned(dx, 2) || !aligned(dresidual, 4) ||
+        !aligned(dweight, 4) || !aligned(weight, width(desc->weight_dtype)))
+        return KDA_ERR_ALIGN;
+    const NormBwdLayout l = norm_bwd_layout(desc);
+    Workspace ws(desc->workspace, desc->workspace_bytes, l.total, stream);
+    if (ws.status() != KDA_OK) return ws.status();
+    NormBwdArgs a{};
+    a.h = h; a.w = weight; a.dy = static_cast<const uint16_t *>(d_out); a.dres = d_residual_out;
+    a.dx = static_cast<uint16_t *>(dx); a.dresidual = dresidual; a.dw = dweight;
+    a.rstd = reinterpret_cast<float *>(ws.at(l.off_rstd));
+    a.part = reinterpret_cast<float *>(ws.at(l.off_part));
+    a.rows = desc->rows; a.D = desc->D; a.hs = desc->x_stride; a.ds = desc->d_out_stride;
+    a.rs = desc->d_residual_stride; a.parts = l.parts;
+    a.eps = desc->eps;
+    a.h_f32 = desc->residual_dtype == KDA_FP32;
+    a.w_f32 = desc->weight_dtype == KDA_FP32;
+    return of_hip(kda_launch_rmsnorm_bwd(a, stream));
+}
+
+extern "C" kda_status_t kda_conv_fwd(const void *x, const void *weight, const void *bias, const void *initial_state,
+                                     void *final_state, const int64_t *cu_seqlens, void *out,
+                                     const kda_conv_desc_t *desc, hipStream_t stream) {
+    ConvArgs a;
+    kda_status_t st = conv_args(x, weight, bias, initial_state, final_state, cu_seqlens, desc, a);
+    if (st != KDA_OK) return st;
+    if (desc->T > 0 && !out) return KDA_ERR_NULL;
+    if (!aligned(out, 2)) return KDA_ERR_ALIGN;
+    if (final_state && final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype)
+        return KDA_ERR_DTYPE;
+    st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
+    if (st != KDA_OK) return st;
+    a.ht = final_state;
+    a.out = static_cast<uint16_t *>(out);
+    return of_hip(kda_launch_conv(a, (int)desc->W, stream));
+}
+
+extern "C" kda_status_t kda_conv_decode(const void *x, const void *weight, const void *bias,
+                                        const void *initial_state, void *final_state, void *out,
+                                        const kda_conv_desc_t *desc, hipStream_t stream) {
+    ConvArgs a;
+    const kda_status_t st = conv_args(x, weight, bias, initial_state, final_state, nullptr, desc, a);
+    if (st != KDA_OK) return st;
+    if (desc->T != 1) return KDA_ERR_SHAPE;
+    if (!out || !final_state) return KDA_ERR_NULL;
+    if (!aligned(out, 2)) return KDA_ERR_ALIGN;
+    if (final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype) return KDA_ERR_DTYPE;
+    a.ht = final_state;
+    a.out = static_cast<uint16_t *>(out);
+    return of_hip(kda_launch_conv_decode(a, (int)desc->W, stream));
+}
+
+extern "C" size_t kda_conv_bwd_workspace_size(const kda_conv_desc_t *desc) {
+    if (!desc || (check_conv(desc, false) != KDA_OK && check_conv(desc, true) != KDA_OK)) return 0;
+    return align_up((size_t)kda_conv_parts(desc->B, desc->T, desc->D) * (size_t)(desc->W + 1) * (size_t)desc->D * 4, 256);
+}
+
+extern "C" kda_status_t kda_conv_bwd(const void *x, const void *weight, const void *bias, const void *initial_state,
+                                     const int64_t *cu_seqlens, const void *d_out, const void *d_final_state,
+                                     void *dx, float *dweight, float *dbias, float *d_initial_state,
+                                     const kda_conv_desc_t *desc, hipStream_t stream) {
+    ConvArgs a;
+    kda_status_t st = conv_args(x, weight, bias, initial_state, d_final_state, cu_seqlens, desc, a);
+    if (st != KDA_OK) return st;
+    if (!dweight || (desc->T > 0 && (!d_out || !dx))) return KDA_ERR_NULL;
+    if (!stride_ok(desc->d_out_stride_b) || !stride_ok(desc->d_out_stride_t)) return KDA_ERR_SHAPE;
+    if (!aligned(d_out, 2) || !aligned(dx, 2) || !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(d_initial_state, 4))
+        return KDA_ERR_ALIGN;
+    st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
+    if (st != KDA_OK) return st;
+    Workspace ws(desc->workspace, desc->workspace_bytes, kda_conv_bwd_workspace_size(desc), stream);
+    if (ws.status() != KDA_OK) return ws.status();
+    a.dy = static_cast<const uint16_t *>(d_out);
+    a.db_ = desc->d_out_stride_b; a.dt_ = desc->d_out_stride_t;
+    a.dht = d_final_state;
+    a.dx = static_cast<uint16_t *>(dx);
+    a.dw = dweight; a.dbias = dbias; a.dh0 = d_initial_state;
+    a.part = reinterpret_cast<float *>(ws.at(0));
+    a.parts = kda_conv_parts(desc->B, desc->T, desc->D);
+    return of_hip(kda_launch_conv_bwd(a, (int)desc->W, stream));
+}
+
+extern "C" kda_status_t kda_ssm_decode(const void *x, const void *dt, const void *Bm, const void *Cm,
+                                       const float *A_log, const float *dt_bias, const float *D,
+                                       const void *initial_state, void *final_state, void *out,
+                                       const kda_ssm_desc_t *desc, hipStream_t stream) {
+    SsmArgs a;
+    const kda_status_t st = ssm_args(x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, final_state, nullptr, desc, a);
+    if (st != KDA_OK) return st;
+    if (desc->T != 1) return KDA_ERR_SHAPE;
+    if (desc->num_seqs > 0x7fffffff / (desc->H * (desc->P / 64))) return KDA_ERR_SHAPE;
+    if (!out || !final_state) return KDA_ERR_NULL;
+    if (!aligned(out, 16)) return KDA_ERR_ALIGN;
+    if (final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype) return KDA_ERR_DTYPE;
+    a.ht = final_state;
+    a.out = static_cast<uint16_t *>(out);
+    return of_hip(kda_launch_ssm_decode(a, stream));
+}

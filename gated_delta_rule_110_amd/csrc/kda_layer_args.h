@@ -1,0 +1,106 @@
+// kda_layer_args.h -- kernel arguments and launchers of the layer operators
+// (include/kda_layer.h): RMS normalisation, short convolution, state-space scan.
+#pragma once
+#include "kda_common.h"
+
+namespace kda {
+
+struct NormArgs {
+    const uint16_t *x;         // bf16 rows, xs elements apart
+    const void *res;           // residual rows (bf16 or fp32), rs elements apart, or nullptr
+    const void *w;             // [D]
+    void *res_out;             // contiguous, of the residual's type, or nullptr
+    void *out;                 // bf16 or e4m3, contiguous
+    float *scales;             // quantised output: [rows, ceil(D / group)] or [rows, 1]
+    int64_t rows, D, xs, rs;
+    int64_t groups;            // scales per row
+    float eps;
+    int res_f32, w_f32;
+    int quant;                 // 0: bf16, 1: e4m3 with one scale per row, 2: one per 128 columns
+};
+
+struct NormBwdArgs {
+    const void *h;             // bf16 or fp32 rows, hs elements apart
+    const void *w;
+    const uint16_t *dy;        // rows ds elements apart
+    const void *dres;          // of h's type, rows rs elements apart, or nullptr
+    uint16_t *dx;
+    float *dresidual;          // or nullptr
+    float *dw;
+    float *part;               // [parts, D] partial sums of dw
+    float *rstd;               // [rows] (the scalar path)
+    int64_t rows, D, hs, ds, rs;
+    int64_t parts;
+    float eps;
+    int h_f32, w_f32;
+};
+
+// Packed batches: cu with the lengths; otherwise sequence n is batch row n of T tokens.
+struct ConvArgs {
+    const uint16_t *x;
+    const void *w, *bias;      // [D, W], [D] or nullptr
+    const void *h0;            // [N, W - 1, D] or nullptr
+    void *ht;
+    const int64_t *cu;
+    uint16_t *out;
+    int64_t B, T, D, N, xb, xt;
+    int silu, w_f32, h0_f32, ht_f32;
+    // gradient
+    const uint16_t *dy;
+    int64_t db_, dt_;          // strides of dy
+    const void *dht;           // of ht's type, or nullptr
+    uint16_t *dx;
+    float *dw, *dbias, *dh0;
+    float *part;               // [parts, W + 1, D] partial sums of dw and dbias
+    int64_t parts;
+};
+
+struct SsmArgs {
+    const uint16_t *x, *dt, *Bm, *Cm;
+    const float *A_log, *dt_bias, *D;
+    const void *h0;
+    void *ht;
+    const int64_t *cu;
+    uint16_t *out;
+    int64_t B, T, H, P, G, N, num_seqs;
+    int64_t xb, xt, dtb, dtt, bb, bt, cb, ct;
+    int h0_f32, ht_f32;
+};
+
+// fp32 -> two bf16 in one word (round to nearest even), low half first.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+}
+
+// A parameter or state entry of either type.
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int f32) {
+    return f32 ? reinterpret_cast<const float *>(p)[i] : bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int64_t i, int f32, float v) {
+    if (f32) reinterpret_cast<float *>(p)[i] = v;
+    else reinterpret_cast<uint16_t *>(p)[i] = f32_to_bf16_bits(v);
+}
+
+// softplus(x) = max(x, 0) + log1p(e^-|x|) in fp32, relative precision kept at
+// the small end: for t = e^-|x| below 2^-6 the series t - t^2/2 + t^3/3 - t^4/4
+// (relative error below 1e-7), above it the hardware log2 of 1 + t.
+__device__ __forceinline__ float softplus(float x) {
+    const float t = fast_exp(-fabsf(x));
+    const float series = t * (1.0f - t * (0.5f - t * (0.33333334f - 0.25f * t)));
+    const float l = t < 0.015625f ? series : fast_log(1.0f + t);
+    return fmaxf(x, 0.0f) + l;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
+
+}  // namespace kda
+
+hipError_t kda_launch_rmsnorm(const kda::NormArgs &a, hipStream_t s);
+// Partial dweight rows the gradient writes for these shapes.
+int64_t kda_rmsnorm_parts(int64_t rows, int64_t D);
+hipError_t kda_launch_rmsnorm_bwd(const kda::NormBwdArgs &a, hipStream_t s);
+hipError_t kda_launch_conv(const kda::ConvArgs &a, int W, hipStream_t s);
+hipError_t kda_launch_conv_decode(const kda::ConvArgs &a, int W, hipStream_t s);
+int64_t kda_conv_parts(int64_t B, int64_t T, int64_t D);
+hipError_t kda_launch_conv_bwd(const kda::ConvArgs &a, int W, hipStream_t s);
+hipError_t kda_launch_ssm_decode(const kda::SsmArgs &a, hipStream_t s);

@@ -1,0 +1,87 @@
+// kda_ssm_decode.hip -- one step of the selective state-space scan per
+// sequence (gfx950).
+//
+//   S' = exp(-exp(A_log) dt) S + dt x B^T,   y = S' C + D x,   dt = softplus(. + dt_bias)
+//
+// The state is read once, updated in registers and written once, in fp32
+// arithmetic: the step is bound by the state's memory traffic (64 KiB in and
+// out per head of 64 x 128 fp32).
+//
+// A workgroup of 256 threads takes kRows rows (channels) of one head's state; a
+// thread holds 4 neighbouring columns of every 256 / (N / 4)-th row, so that a
+// row is one contiguous access of N / 4 lanes, whose shares of S' C are added by
+// lane exchanges.
+#include "kda_layer_args.h"
+
+using namespace kda;
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ f4 load_state4(const void *p, int64_t i, int f32) {
+    if (f32) return *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(p) + i);
+    const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
+    return f4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+              __uint_as_float(v.y & 0xffff0000u)};
+}
+__device__ __forceinline__ void store_state4(void *p, int64_t i, int f32, f4 v) {
+    if (f32) *reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i) = v;
+    else
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
+template <int kN, int kRows>
+__global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a) {
+    constexpr int kCols = kN / 4;                // threads per row
+    constexpr int kStep = kThreads / kCols;      // rows per pass
+    constexpr int kPass = kRows / kStep;
+    static_assert(kRows % kStep == 0, "whole passes");
+    const int share = (int)(a.P / kRows);
+    const int64_t unit = blockIdx.x / share;     // (sequence, head)
+    const int p0 = (int)(blockIdx.x - unit * share) * kRows;
+    const int64_t n = unit / a.H, h = unit - n * a.H;
+    const int64_t g = h / (a.H / a.G);
+    const int q = threadIdx.x % kCols, r = threadIdx.x / kCols;
+    const int64_t base = (unit * a.P + p0 + r) * kN + 4 * q;
+    f4 S[kPass];
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+        S[i] = a.h0 ? load_state4(a.h0, base + (int64_t)i * kStep * kN, a.h0_f32) : f4{0.f, 0.f, 0.f, 0.f};
+    const f4 Bv = load_state4(a.Bm, n * a.bb + g * kN + 4 * q, 0);
+    const f4 Cv = load_state4(a.Cm, n * a.cb + g * kN + 4 * q, 0);
+    const float raw = bf16_bits_to_f32(a.dt[n * a.dtb + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f);
+    const float dt = softplus(raw);
+    const float decay = fast_exp(-fast_exp(a.A_log[h]) * dt);
+    const float Dh = a.D ? a.D[h] : 0.f;
+    const uint16_t *x = a.x + n * a.xb + h * a.P + p0;
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+        const float xv = bf16_bits_to_f32(x[i * kStep + r]);
+        const float dx = dt * xv;
+        float y = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            S[i][e] = decay * S[i][e] + dx * Bv[e];
+            y += S[i][e] * Cv[e];
+        }
+        store_state4(a.ht, base + (int64_t)i * kStep * kN, a.ht_f32, S[i]);
+#pragma unroll
+        for (int m = kCols / 2; m >= 1; m >>= 1) y += __shfl_xor(y, m);
+        if (q == 0) a.out[unit * a.P + p0 + i * kStep + r] = f32_to_bf16_bits(y + Dh * xv);
+    }
+}
+
+template <int kN, int kRows>
+hipError_t launch(const SsmArgs &a, hipStream_t s) {
+    const int64_t blocks = a.num_seqs * a.H * (a.P / kRows);
+    hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kRows>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t kda_launch_ssm_decode(const SsmArgs &a, hipStream_t s) {
+    return a.N == 128 ? launch<128, 64>(a, s) : launch<64, 64>(a, s);
+}

@@ -1,0 +1,537 @@
+"""The operators around and beside the KDA recurrence (``include/kda_layer.h``):
+RMS normalisation with the residual's addition (bf16 or e4m3 output), the short
+causal convolution and the selective state-space scan, each with its gradient,
+and with a single-token step where generation has one.
+
+As for the recurrence, the functions only marshal arguments: they check types,
+devices and shapes, allocate outputs and workspaces that the caller does not
+pass, and call libkda on torch's current HIP stream of the inputs' device.
+Activations are bf16; they may be slices of wider tensors (only their last
+dimensions have to be contiguous).  Tensors that a call writes are contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+_P = ctypes.c_void_p
+_I = ctypes.c_int64
+_BF16, _FP32 = 1, 2
+_STATE_DTYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
+
+
+class KdaRmsnormDesc(ctypes.Structure):
+    _fields_ = [("rows", _I), ("D", _I), ("x_stride", _I), ("residual_stride", _I),
+                ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("group", _I), ("d_out_stride", _I), ("d_residual_stride", _I), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class KdaConvDesc(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("W", _I), ("num_seqs", _I), ("x_stride_b", _I), ("x_stride_t", _I),
+                ("d_out_stride_b", _I), ("d_out_stride_t", _I), ("silu", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("initial_state_dtype", ctypes.c_int32),
+                ("final_state_dtype", ctypes.c_int32), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class KdaSsmDesc(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("H", _I), ("P", _I), ("G", _I), ("N", _I), ("num_seqs", _I),
+                ("x_stride_b", _I), ("x_stride_t", _I), ("dt_stride_b", _I), ("dt_stride_t", _I),
+                ("b_stride_b", _I), ("b_stride_t", _I), ("c_stride_b", _I), ("c_stride_t", _I),
+                ("d_out_stride_b", _I), ("d_out_stride_t", _I), ("initial_state_dtype", ctypes.c_int32),
+                ("final_state_dtype", ctypes.c_int32), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("piece_chunks", _I)]
+
+
+def _declare(lib) -> None:
+    """Argument types of the layer operators (called once, when the library is loaded)."""
+    N, C, S = (ctypes.POINTER(t) for t in (KdaRmsnormDesc, KdaConvDesc, KdaSsmDesc))
+    for name, n, desc in (("kda_rmsnorm_fwd", 5, N), ("kda_rmsnorm_quant", 6, N), ("kda_rmsnorm_bwd", 7, N),
+                          ("kda_conv_fwd", 7, C), ("kda_conv_decode", 6, C), ("kda_conv_bwd", 11, C),
+                          ("kda_ssm_decode", 10, S)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, [_P] * n + [desc, _P]
+    for name, desc, kind in (("kda_rmsnorm_bwd_workspace_size", N, ctypes.c_size_t),
+                             ("kda_conv_bwd_workspace_size", C, ctypes.c_size_t)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = kind, [desc]
+
+
+def _library():
+    from . import library
+
+    return library()
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(dev: torch.device, **tensors) -> None:
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a HIP device")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+
+
+def _bf16(**tensors) -> None:
+    for name, t in tensors.items():
+        if t.dtype != torch.bfloat16:
+            raise ValueError("%s must be bfloat16, got %s" % (name, t.dtype))
+
+
+def _param(t: Optional[torch.Tensor], name: str, shape: tuple, fp32_only: bool = False) -> None:
+    if t is None:
+        return
+    if t.dtype not in _STATE_DTYPES or (fp32_only and t.dtype != torch.float32):
+        raise ValueError("%s must be %s, got %s" % (name, "float32" if fp32_only else "bf16 or fp32", t.dtype))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, list(shape)))
+
+
+def _output(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, dev) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, list(shape), dev))
+    return t
+
+
+def _state_code(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else _STATE_DTYPES[t.dtype]
+
+
+def _overlap(a: Optional[torch.Tensor], b: Optional[torch.Tensor]) -> bool:
+    """Whether two tensors' memory overlaps (their spans, strides included)."""
+    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
+        return False
+
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _apart(written: dict, read: dict, same: tuple = ()) -> None:
+    """Refuses outputs that overlap an input or each other, but for the pairs in
+    ``same``, which may be one and the same memory."""
+    done = []
+    for w, a in written.items():
+        for r, b in list(read.items()) + done:
+            if _overlap(a, b):
+                if (w, r) in same and a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and b.is_contiguous():
+                    continue
+                raise ValueError("%s overlaps %s" % (w, r))
+        done.append((w, a))
+
+
+def _workspace(t: Optional[torch.Tensor], need: int, dev, d) -> Optional[torch.Tensor]:
+    if t is None:
+        t = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError("workspace must be a contiguous tensor of %d bytes on %s" % (need, dev))
+    d.workspace = t.data_ptr()
+    d.workspace_bytes = t.numel() * t.element_size()
+    return t
+
+
+def _call(fn, dev, *args) -> None:
+    """``fn(*args, stream)`` on the current stream of ``dev``."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        from . import _raise_status
+
+        _raise_status(_library(), st)
+
+
+# ---- RMS normalisation ---------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, D: int) -> Tuple[int, int]:
+    """(number of rows, elements between them) of [..., D] with even row strides."""
+    if t.dim() == 0 or t.shape[-1] != D:
+        raise ValueError("%s must be [..., %d]" % (name, D))
+    if t.stride(-1) != 1 and D > 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    rows, stride, span = 1, D, None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if span is not None and n > 0 and s != span:
+            raise ValueError("%s must have rows at one stride (call .contiguous())" % name)
+        if span is None:
+            stride = s
+        rows, span = rows * n, s * n
+    return rows, stride
+
+
+def _rmsnorm_args(x, weight, eps, residual, residual_out, group=0):
+    _bf16(x=x)
+    D = x.shape[-1] if x.dim() else 0
+    if D < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    rows, xs = _rows(x, "x", D)
+    _param(weight, "weight", (D,))
+    rs = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype not in _STATE_DTYPES:
+            raise ValueError("residual must be bf16 or fp32 of x's shape")
+        rs = _rows(residual, "residual", D)[1]
+    _on_device(x.device, weight=weight, residual=residual)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    else:
+        residual_out = _output(residual_out, "residual_out", x.shape, residual.dtype, x.device)
+    return KdaRmsnormDesc(rows, D, xs, rs, _state_code(residual), _STATE_DTYPES[weight.dtype], float(eps), group), residual_out
+
+
+def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """RMS normalisation of ``h = x + residual`` over the last dimension:
+    ``h / sqrt(mean(h^2) + eps) * weight``.  Returns ``(out, residual_out)``.
+
+    x: bf16 [..., D]; weight: bf16 or fp32 [D]; residual: bf16 or fp32 of x's
+    shape, or None; out: bf16, allocated if None (it may be x); residual_out: h
+    in the residual's type, allocated if None (it may be the residual); None
+    without a residual."""
+    d, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out)
+    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
+    _apart({"out": out, "residual_out": residual_out}, {"x": x, "residual": residual, "weight": weight},
+           (("out", "x"), ("residual_out", "residual")))
+    _call(_library().kda_rmsnorm_fwd, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
+          out.data_ptr(), d)
+    return out, residual_out
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                  group: int = 0, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                  residual_out: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """``rmsnorm_fwd`` with an 8-bit output: returns ``(q, scales, residual_out)``
+    with q in ``torch.float8_e4m3fn`` and fp32 scales, the value of an entry
+    being ``q * scale``.  group 0: one scale per row, [..., 1]; group 128: one
+    per 128 columns, [..., ceil(D / 128)].  A scale is the group's largest
+    magnitude / 448 (at least 2^-126)."""
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (one scale per row) or 128")
+    d, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out, group)
+    out = _output(out, "out", x.shape, torch.float8_e4m3fn, x.device)
+    n = -(-d.D // group) if group else 1
+    scales = _output(scales, "scales", (*x.shape[:-1], n), torch.float32, x.device)
+    _apart({"out": out, "residual_out": residual_out, "scales": scales}, {"x": x, "residual": residual, "weight": weight},
+           (("residual_out", "residual"),))
+    _call(_library().kda_rmsnorm_quant, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
+          out.data_ptr(), scales.data_ptr(), d)
+    return out, scales, residual_out
+
+
+def rmsnorm_bwd_workspace_size(rows: int, D: int) -> int:
+    """Workspace bytes ``rmsnorm_bwd`` needs."""
+    return int(_library().kda_rmsnorm_bwd_workspace_size(KdaRmsnormDesc(rows, D)))
+
+
+def rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, eps: float, d_out: torch.Tensor,
+                d_residual_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                outputs: Optional[dict] = None) -> dict:
+    """Gradient of ``rmsnorm_fwd`` for the loss gradients d_out (bf16) and
+    d_residual_out (of h's type, or None for zeros).  h: what the forward
+    returned as residual_out, or x where it had no residual (bf16 or fp32).
+    Returns a dict: dx (bf16; the gradient of x), dresidual (that of the
+    residual: the fp32 gradient when h is fp32, dx itself when it is bf16, None
+    without d_residual_out and a bf16 h) and dweight (fp32 [D]).  outputs: None,
+    or a dict of tensors of those names to write into."""
+    if h.dtype not in _STATE_DTYPES:
+        raise ValueError("h must be bf16 or fp32, got %s" % h.dtype)
+    _bf16(d_out=d_out)
+    D = h.shape[-1] if h.dim() else 0
+    if D < 1 or d_out.shape != h.shape:
+        raise ValueError("h must be [..., D] and d_out of its shape")
+    rows, hs = _rows(h, "h", D)
+    ds = _rows(d_out, "d_out", D)[1]
+    rs = 0
+    if d_residual_out is not None:
+        if d_residual_out.shape != h.shape or d_residual_out.dtype != h.dtype:
+            raise ValueError("d_residual_out must be of h's shape and type")
+        rs = _rows(d_residual_out, "d_residual_out", D)[1]
+    _param(weight, "weight", (D,))
+    dev = h.device
+    _on_device(dev, weight=weight, d_out=d_out, d_residual_out=d_residual_out)
+    given = outputs or {}
+    dx = _output(given.get("dx"), "dx", h.shape, torch.bfloat16, dev)
+    dres = _output(given.get("dresidual"), "dresidual", h.shape, torch.float32, dev) if h.dtype == torch.float32 else None
+    dw = _output(given.get("dweight"), "dweight", (D,), torch.float32, dev)
+    d = KdaRmsnormDesc(rows, D, hs, 0, _STATE_DTYPES[h.dtype], _STATE_DTYPES[weight.dtype], float(eps), 0, ds, rs)
+    lib = _library()
+    ws = _workspace(workspace, lib.kda_rmsnorm_bwd_workspace_size(d), dev, d)
+    _apart({"dx": dx, "dresidual": dres, "dweight": dw, "workspace": ws},
+           {"h": h, "weight": weight, "d_out": d_out, "d_residual_out": d_residual_out})
+    _call(lib.kda_rmsnorm_bwd, dev, h.data_ptr(), weight.data_ptr(), d_out.data_ptr(), _ptr(d_residual_out),
+          dx.data_ptr(), _ptr(dres), dw.data_ptr(), d)
+    return {"dx": dx, "dresidual": dres if dres is not None else dx if d_residual_out is not None else None,
+            "dweight": dw}
+
+
+class RmsnormFunction(torch.autograd.Function):
+    """``rmsnorm_fwd`` with ``rmsnorm_bwd`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        out, res = rmsnorm_fwd(x, weight, eps, residual=residual)
+        ctx.save_for_backward(x if res is None else res, weight)
+        ctx.eps, ctx.with_residual = float(eps), res is not None
+        return out, res
+
+    @staticmethod
+    def backward(ctx, d_out, d_res):
+        h, weight = ctx.saved_tensors
+        if d_res is not None:
+            d_res = d_res.to(h.dtype).contiguous()
+        if d_out is None:
+            d_out = torch.zeros(h.shape, dtype=torch.bfloat16, device=h.device)
+        g = rmsnorm_bwd(h, weight, ctx.eps, d_out.to(torch.bfloat16).contiguous(), d_residual_out=d_res)
+        dres = None
+        if ctx.with_residual:
+            dres = g["dresidual"] if g["dresidual"] is not None else g["dx"]
+        return g["dx"], g["dweight"].to(weight.dtype), dres, None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``rmsnorm_fwd`` as an autograd operation: returns ``(out, residual_out)``
+    and backpropagates into x, weight and the residual."""
+    return RmsnormFunction.apply(x, weight, residual, eps)
+
+
+# ---- short causal convolution ----------------------------------------------------
+
+def _tokens(t: torch.Tensor, name: str, inner: tuple) -> Tuple[int, int]:
+    """Batch and token strides of [B, T, *inner] with contiguous inner dimensions."""
+    want, n = [], 1
+    for s in reversed(inner):
+        want.append(n)
+        n *= s
+    for size, st, w in zip(reversed(t.shape[2:]), reversed(t.stride()[2:]), want):
+        if size > 1 and st != w:
+            raise ValueError("%s must be contiguous in its dimensions behind [B, T]" % name)
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _num_seqs(cu_seqlens: Optional[torch.Tensor], B: int) -> int:
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a 1-D int64 tensor of at least 2 entries")
+    if B != 1:
+        raise ValueError("with cu_seqlens the batch size must be 1")
+    return cu_seqlens.numel() - 1
+
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _conv_args(x, weight, bias, activation, initial_state, final_state, cu_seqlens, final_name="final_state"):
+    _bf16(x=x)
+    if x.dim() != 3 or x.shape[0] < 1 or x.shape[2] < 1:
+        raise ValueError("x must be [B, T, D]")
+    B, T, D = x.shape
+    if weight.dim() != 2 or weight.shape[1] not in (2, 3, 4):
+        raise ValueError("weight must be [D, W] with W = 2, 3 or 4")
+    W = weight.shape[1]
+    _param(weight, "weight", (D, W))
+    _param(bias, "bias", (D,))
+    if bias is not None and bias.dtype != weight.dtype:
+        raise ValueError("bias must have weight's dtype")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be None or 'silu'")
+    N = _num_seqs(cu_seqlens, B)
+    _param(initial_state, "initial_state", (N, W - 1, D))
+    _param(final_state, final_name, (N, W - 1, D))
+    _on_device(x.device, weight=weight, bias=bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
+               **{final_name: final_state})
+    sb, st = _tokens(x, "x", (D,))
+    return KdaConvDesc(B, T, D, W, N, sb, st, 0, 0, _ACTIVATIONS[activation], _STATE_DTYPES[weight.dtype],
+                       _state_code(initial_state), _state_code(final_state))
+
+
+def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+             activation: Optional[str] = "silu", initial_state: Optional[torch.Tensor] = None,
+             final_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The short causal depthwise convolution over the tokens of every sequence
+    (``kda_conv_fwd``).  Returns ``(out, final_state)``.
+
+    x: bf16 [B, T, D]; weight: bf16 or fp32 [D, W], W = 2, 3 or 4, the last tap
+    on the current token; bias: [D] of the weight's type, or None; activation:
+    None or "silu"; initial_state, final_state: bf16 or fp32 [N, W - 1, D], the
+    inputs before and behind the tokens, oldest first, or None (zeros / not
+    wanted; final_state may be initial_state); cu_seqlens: int64 [N + 1] on the
+    device (then B == 1) or None; out: bf16 [B, T, D], allocated if None."""
+    d = _conv_args(x, weight, bias, activation, initial_state, final_state, cu_seqlens)
+    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
+    _apart({"out": out, "final_state": final_state},
+           {"x": x, "weight": weight, "bias": bias, "initial_state": initial_state, "cu_seqlens": cu_seqlens},
+           (("final_state", "initial_state"),))
+    _call(_library().kda_conv_fwd, x.device, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
+          _ptr(final_state), _ptr(cu_seqlens), out.data_ptr(), d)
+    return out, final_state
+
+
+def conv_decode(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                activation: Optional[str] = "silu", initial_state: Optional[torch.Tensor] = None,
+                final_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per sequence of ``conv_fwd`` (``kda_conv_decode``): x is
+    [N, 1, D].  final_state is required; passing the initial state updates it in
+    place.  Returns ``(out, final_state)``."""
+    if final_state is None:
+        raise ValueError("final_state must be given (it may be initial_state)")
+    if x.dim() != 3 or x.shape[1] != 1:
+        raise ValueError("x must be [N, 1, D]")
+    d = _conv_args(x, weight, bias, activation, initial_state, final_state, None)
+    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
+    _apart({"out": out, "final_state": final_state},
+           {"x": x, "weight": weight, "bias": bias, "initial_state": initial_state}, (("final_state", "initial_state"),))
+    _call(_library().kda_conv_decode, x.device, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
+          final_state.data_ptr(), out.data_ptr(), d)
+    return out, final_state
+
+
+def conv_bwd_workspace_size(B: int, T: int, D: int, W: int) -> int:
+    """Workspace bytes ``conv_bwd`` needs."""
+    return int(_library().kda_conv_bwd_workspace_size(KdaConvDesc(B, T, D, W, B, 0, 0, 0, 0, 0, _FP32)))
+
+
+def conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], activation: Optional[str],
+             d_out: torch.Tensor, d_final_state: Optional[torch.Tensor] = None,
+             initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+             with_d_initial: Optional[bool] = None, workspace: Optional[torch.Tensor] = None,
+             outputs: Optional[dict] = None) -> dict:
+    """Gradient of ``conv_fwd`` for the loss gradients d_out (bf16 [B, T, D]) and
+    d_final_state (bf16 or fp32 [N, W - 1, D], or None).  Returns a dict: dx
+    (bf16), dweight (fp32 [D, W]), dbias (fp32 [D], None without a bias),
+    d_initial_state (fp32 [N, W - 1, D]; None unless wanted, by default where an
+    initial_state is given).  Rows of dx behind a packed batch's last sequence
+    are left as they were.  outputs: None, or a dict of tensors of those names
+    to write into."""
+    d = _conv_args(x, weight, bias, activation, initial_state, d_final_state, cu_seqlens, "d_final_state")
+    _bf16(d_out=d_out)
+    if d_out.shape != x.shape:
+        raise ValueError("d_out must be of x's shape")
+    dev = x.device
+    _on_device(dev, d_out=d_out)
+    d.d_out_stride_b, d.d_out_stride_t = _tokens(d_out, "d_out", (d.D,))
+    given = outputs or {}
+    f32 = torch.float32
+    if with_d_initial is None:
+        with_d_initial = initial_state is not None
+    res = {"dx": _output(given.get("dx"), "dx", x.shape, torch.bfloat16, dev),
+           "dweight": _output(given.get("dweight"), "dweight", (d.D, d.W), f32, dev),
+           "dbias": None if bias is None else _output(given.get("dbias"), "dbias", (d.D,), f32, dev),
+           "d_initial_state": _output(given.get("d_initial_state"), "d_initial_state", (d.num_seqs, d.W - 1, d.D), f32, dev)
+           if with_d_initial else None}
+    lib = _library()
+    ws = _workspace(workspace, lib.kda_conv_bwd_workspace_size(d), dev, d)
+    _apart({**res, "workspace": ws}, {"x": x, "weight": weight, "bias": bias, "d_out": d_out, "d_final_state": d_final_state,
+                                      "initial_state": initial_state, "cu_seqlens": cu_seqlens})
+    _call(lib.kda_conv_bwd, dev, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
+          d_out.data_ptr(), _ptr(d_final_state), res["dx"].data_ptr(), res["dweight"].data_ptr(), _ptr(res["dbias"]),
+          _ptr(res["d_initial_state"]), d)
+    return res
+
+
+def _grad_dx(cu_seqlens: Optional[torch.Tensor], shape, dev) -> Optional[torch.Tensor]:
+    """Zeros for a packed batch (rows behind its last sequence get no gradient), else None."""
+    return None if cu_seqlens is None else torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+
+
+class ConvFunction(torch.autograd.Function):
+    """``conv_fwd`` with ``conv_bwd`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, activation, cu_seqlens, final_dtype):
+        N, W = _num_seqs(cu_seqlens, x.shape[0]), weight.shape[1]
+        final = None if final_dtype is None else torch.empty((N, W - 1, x.shape[2]), dtype=final_dtype, device=x.device)
+        out, final = conv_fwd(x, weight, bias, activation, initial_state, final, cu_seqlens,
+                              out=_grad_dx(cu_seqlens, x.shape, x.device))
+        ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
+        ctx.activation = activation
+        return out, final
+
+    @staticmethod
+    def backward(ctx, d_out, d_final):
+        x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
+        if d_out is None:
+            d_out = torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
+        want = initial_state is not None and ctx.needs_input_grad[3]
+        g = conv_bwd(x, weight, bias, ctx.activation, d_out.to(torch.bfloat16).contiguous(),
+                     d_final_state=None if d_final is None else d_final.contiguous(), initial_state=initial_state,
+                     cu_seqlens=cu_seqlens, with_d_initial=want,
+                     outputs={"dx": _grad_dx(cu_seqlens, x.shape, x.device)})
+        return (g["dx"], g["dweight"].to(weight.dtype), None if bias is None else g["dbias"].to(bias.dtype),
+                g["d_initial_state"].to(initial_state.dtype) if want else None, None, None, None)
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               activation: Optional[str] = "silu", initial_state: Optional[torch.Tensor] = None,
+               final_state_dtype: Optional[torch.dtype] = None, cu_seqlens: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``conv_fwd`` as an autograd operation: returns ``(out, final_state)``, the
+    final state in ``final_state_dtype`` or None, and backpropagates into x,
+    weight, bias and the initial state.  Rows behind a packed batch's last
+    sequence are zero, in the output and in x's gradient."""
+    return ConvFunction.apply(x, weight, bias, initial_state, activation, cu_seqlens, final_state_dtype)
+
+
+# ---- selective state-space scan ----------------------------------------------------
+
+def _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks=0,
+              final_name="final_state"):
+    _bf16(x=x, dt=dt, B=B, C=C)
+    if x.dim() != 4 or B.dim() != 4:
+        raise ValueError("x must be [B, T, H, P] and B [B, T, G, N]")
+    nb, T, H, P = x.shape
+    G, S = B.shape[2:]
+    if nb < 1 or H < 1 or G < 1 or H % G or tuple(B.shape[:2]) != (nb, T) or C.shape != B.shape or \
+            tuple(dt.shape) != (nb, T, H):
+        raise ValueError("shape mismatch among x, dt, B and C (H must be a multiple of G)")
+    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
+        _param(t, name, (H,), fp32_only=True)
+    N = _num_seqs(cu_seqlens, nb)
+    _param(initial_state, "initial_state", (N, H, P, S))
+    _param(final_state, final_name, (N, H, P, S))
+    _on_device(x.device, dt=dt, B=B, C=C, A_log=A_log, dt_bias=dt_bias, D=D, initial_state=initial_state,
+               cu_seqlens=cu_seqlens, **{final_name: final_state})
+    return KdaSsmDesc(nb, T, H, P, G, S, N, *_tokens(x, "x", (H, P)), *_tokens(dt, "dt", (H,)), *_tokens(B, "B", (G, S)),
+                      *_tokens(C, "C", (G, S)), 0, 0, _state_code(initial_state), _state_code(final_state), None, 0,
+                      int(piece_chunks))
+
+
+def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
+               dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+               initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One step of ``ssm_fwd`` per sequence (``kda_ssm_decode``): T = 1.
+    final_state is required; passing the initial state updates it in place.
+    Returns ``(out, final_state)``."""
+    if final_state is None:
+        raise ValueError("final_state must be given (it may be initial_state)")
+    if x.dim() != 4 or x.shape[1] != 1:
+        raise ValueError("x must be [N, 1, H, P]")
+    d = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, None)
+    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
+    _apart({"out": out, "final_state": final_state},
+           {"x": x, "dt": dt, "B": B, "C": C, "A_log": A_log, "dt_bias": dt_bias, "D": D, "initial_state": initial_state},
+           (("final_state", "initial_state"),))
+    _call(_library().kda_ssm_decode, x.device, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
+          _ptr(dt_bias), _ptr(D), _ptr(initial_state), final_state.data_ptr(), out.data_ptr(), d)
+    return out, final_state
