@@ -192,6 +192,7 @@ extern "C" const char *kda_status_string(kda_status_t s) {
         case KDA_ERR_WORKSPACE: return "workspace smaller than the call's workspace size function asks for";
         case KDA_ERR_HIP: return "HIP launch error";
         case KDA_ERR_SCRATCH: return "workspace need exceeds the static scratch of kda_fwd_noalloc (kda_fwd_noalloc_max_workspace() bytes)";
+        case KDA_ERR_OVERLAP: return "a written tensor overlaps a read one or another written one";
     }
     return "unknown status";
 }

@@ -25,6 +25,44 @@ constexpr int64_t kMaxSeqs = 0x7fffffff;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
+// The memory a call touches: every written tensor has to lie apart from all
+// others, but for a read tensor that it may be one and the same as.
+class Memory {
+public:
+    // `bytes` from the first element to behind the last (0: nothing is touched).
+    void read(const void *p, size_t bytes) { add(p, bytes, false, nullptr); }
+    void write(const void *p, size_t bytes, const void *may_be = nullptr) { add(p, bytes, true, may_be); }
+    bool clash() const {
+        for (int i = 0; i < n_; ++i)
+            for (int j = 0; j < n_; ++j) {
+                const Span &w = s_[i], &o = s_[j];
+                if (i == j || !w.written || w.a >= o.b || o.a >= w.b) continue;
+                if (!o.written && w.may_be == o.a && w.a == o.a && w.b == o.b) continue;
+                return true;
+            }
+        return false;
+    }
+
+private:
+    struct Span {
+        uintptr_t a, b, may_be;
+        bool written;
+    };
+    void add(const void *p, size_t bytes, bool written, const void *may_be) {
+        if (!p || !bytes) return;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        s_[n_++] = Span{a, a + bytes, reinterpret_cast<uintptr_t>(may_be), written};
+    }
+    Span s_[24];  // more than any call has tensors
+    int n_ = 0;
+};
+
+// Bytes from the first element of [n0, n1, inner] with strides s0, s1 to behind its last.
+size_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner, size_t w) {
+    if (n0 <= 0 || n1 <= 0 || inner <= 0) return 0;
+    return (size_t)((n0 - 1) * s0 + (n1 - 1) * s1 + inner) * w;
+}
+
 // The workspace of a call: the caller's, or one taken on the stream and given
 // back behind the call's kernels.
 class Workspace {
@@ -96,11 +134,21 @@ kda_status_t norm_impl(const void *x, const void *residual, const void *weight, 
     if (!aligned(x, 2) || (!quant && !aligned(out, 2)) || !aligned(scales, 4) || !aligned(weight, width(d->weight_dtype)) ||
         (residual && (!aligned(residual, width(d->residual_dtype)) || !aligned(residual_out, width(d->residual_dtype)))))
         return KDA_ERR_ALIGN;
+    const size_t n = (size_t)d->rows * (size_t)d->D, rw = width(d->residual_dtype);
+    const int64_t groups = d->group ? (d->D + d->group - 1) / d->group : 1;
+    Memory m;
+    m.read(x, extent(1, 0, d->rows, d->x_stride, d->D, 2));
+    if (residual) m.read(residual, extent(1, 0, d->rows, d->residual_stride, d->D, rw));
+    m.read(weight, (size_t)d->D * width(d->weight_dtype));
+    m.write(out, n * (quant ? 1 : 2), quant ? nullptr : x);
+    m.write(residual_out, n * rw, residual);
+    m.write(scales, (size_t)d->rows * (size_t)groups * 4);
+    if (m.clash()) return KDA_ERR_OVERLAP;
     NormArgs a{};
     a.x = static_cast<const uint16_t *>(x);
     a.res = residual; a.w = weight; a.res_out = residual_out; a.out = out; a.scales = scales;
     a.rows = d->rows; a.D = d->D; a.xs = d->x_stride; a.rs = d->residual_stride;
-    a.groups = d->group ? (d->D + d->group - 1) / d->group : 1;
+    a.groups = groups;
     a.eps = d->eps;
     a.res_f32 = d->residual_dtype == KDA_FP32;
     a.w_f32 = d->weight_dtype == KDA_FP32;
@@ -151,6 +199,20 @@ kda_status_t conv_args(const void *x, const void *weight, const void *bias, cons
     return KDA_OK;
 }
 
+// What the three calls read; the states' bytes are the same for both.
+size_t conv_state_bytes(const kda_conv_desc_t *d, int32_t dtype) {
+    return (size_t)d->num_seqs * (size_t)(d->W - 1) * (size_t)d->D * width(dtype);
+}
+void conv_reads(Memory &m, const void *x, const void *weight, const void *bias, const void *h0, const int64_t *cu,
+                const kda_conv_desc_t *d) {
+    m.read(x, extent(d->B, d->x_stride_b, d->T, d->x_stride_t, d->D, 2));
+    m.read(weight, (size_t)(d->D * d->W) * width(d->weight_dtype));
+    m.read(bias, (size_t)d->D * width(d->weight_dtype));
+    m.read(h0, conv_state_bytes(d, d->initial_state_dtype));
+    m.read(cu, (size_t)(d->num_seqs + 1) * 8);
+}
+size_t conv_token_bytes(const kda_conv_desc_t *d) { return (size_t)(d->B * d->T) * (size_t)d->D * 2; }
+
 // ---- state-space scan ----
 
 kda_status_t check_ssm(const kda_ssm_desc_t *d, bool packed) {
@@ -196,6 +258,21 @@ kda_status_t ssm_args(const void *x, const void *dt, const void *Bm, const void 
     a.h0_f32 = d->initial_state_dtype == KDA_FP32;
     a.ht_f32 = d->final_state_dtype == KDA_FP32;
     return KDA_OK;
+}
+
+size_t ssm_state_bytes(const kda_ssm_desc_t *d, int32_t dtype) {
+    return (size_t)d->num_seqs * (size_t)d->H * (size_t)(d->P * d->N) * width(dtype);
+}
+size_t ssm_out_bytes(const kda_ssm_desc_t *d) { return (size_t)(d->B * d->T) * (size_t)(d->H * d->P) * 2; }
+void ssm_reads(Memory &m, const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+               const float *dt_bias, const float *D, const void *h0, const int64_t *cu, const kda_ssm_desc_t *d) {
+    m.read(x, extent(d->B, d->x_stride_b, d->T, d->x_stride_t, d->H * d->P, 2));
+    m.read(dt, extent(d->B, d->dt_stride_b, d->T, d->dt_stride_t, d->H, 2));
+    m.read(Bm, extent(d->B, d->b_stride_b, d->T, d->b_stride_t, d->G * d->N, 2));
+    m.read(Cm, extent(d->B, d->c_stride_b, d->T, d->c_stride_t, d->G * d->N, 2));
+    for (const float *p : {A_log, dt_bias, D}) m.read(p, (size_t)d->H * 4);
+    m.read(h0, ssm_state_bytes(d, d->initial_state_dtype));
+    m.read(cu, (size_t)(d->num_seqs + 1) * 8);
 }
 
 }  // namespace
@@ -247,6 +324,17 @@ extern "C" kda_status_t kda_rmsnorm_bwd(const void *h, const void *weight, const
         !aligned(dweight, 4) || !aligned(weight, width(desc->weight_dtype)))
         return KDA_ERR_ALIGN;
     const NormBwdLayout l = norm_bwd_layout(desc);
+    const size_t n = (size_t)desc->rows * (size_t)desc->D;
+    Memory m;
+    m.read(h, extent(1, 0, desc->rows, desc->x_stride, desc->D, hw));
+    m.read(weight, (size_t)desc->D * width(desc->weight_dtype));
+    m.read(d_out, extent(1, 0, desc->rows, desc->d_out_stride, desc->D, 2));
+    m.read(d_residual_out, extent(1, 0, desc->rows, desc->d_residual_stride, desc->D, hw));
+    m.write(dx, n * 2);
+    m.write(dresidual, n * 4);
+    m.write(dweight, (size_t)desc->D * 4);
+    m.write(desc->workspace, l.total);
+    if (m.clash()) return KDA_ERR_OVERLAP;
     Workspace ws(desc->workspace, desc->workspace_bytes, l.total, stream);
     if (ws.status() != KDA_OK) return ws.status();
     NormBwdArgs a{};
@@ -270,8 +358,11 @@ extern "C" kda_status_t kda_conv_fwd(const void *x, const void *weight, const vo
     if (st != KDA_OK) return st;
     if (desc->T > 0 && !out) return KDA_ERR_NULL;
     if (!aligned(out, 2)) return KDA_ERR_ALIGN;
-    if (final_state && final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype)
-        return KDA_ERR_DTYPE;
+    Memory m;
+    conv_reads(m, x, weight, bias, initial_state, cu_seqlens, desc);
+    m.write(out, conv_token_bytes(desc));
+    m.write(final_state, conv_state_bytes(desc, desc->final_state_dtype), initial_state);
+    if (m.clash()) return KDA_ERR_OVERLAP;
     st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
     if (st != KDA_OK) return st;
     a.ht = final_state;
@@ -288,7 +379,11 @@ extern "C" kda_status_t kda_conv_decode(const void *x, const void *weight, const
     if (desc->T != 1) return KDA_ERR_SHAPE;
     if (!out || !final_state) return KDA_ERR_NULL;
     if (!aligned(out, 2)) return KDA_ERR_ALIGN;
-    if (final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype) return KDA_ERR_DTYPE;
+    Memory m;
+    conv_reads(m, x, weight, bias, initial_state, nullptr, desc);
+    m.write(out, conv_token_bytes(desc));
+    m.write(final_state, conv_state_bytes(desc, desc->final_state_dtype), initial_state);
+    if (m.clash()) return KDA_ERR_OVERLAP;
     a.ht = final_state;
     a.out = static_cast<uint16_t *>(out);
     return of_hip(kda_launch_conv_decode(a, (int)desc->W, stream));
@@ -310,6 +405,16 @@ extern "C" kda_status_t kda_conv_bwd(const void *x, const void *weight, const vo
     if (!stride_ok(desc->d_out_stride_b) || !stride_ok(desc->d_out_stride_t)) return KDA_ERR_SHAPE;
     if (!aligned(d_out, 2) || !aligned(dx, 2) || !aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(d_initial_state, 4))
         return KDA_ERR_ALIGN;
+    Memory m;
+    conv_reads(m, x, weight, bias, initial_state, cu_seqlens, desc);
+    m.read(d_out, extent(desc->B, desc->d_out_stride_b, desc->T, desc->d_out_stride_t, desc->D, 2));
+    m.read(d_final_state, conv_state_bytes(desc, desc->final_state_dtype));
+    m.write(dx, conv_token_bytes(desc));
+    m.write(dweight, (size_t)(desc->D * desc->W) * 4);
+    m.write(dbias, (size_t)desc->D * 4);
+    m.write(d_initial_state, conv_state_bytes(desc, KDA_FP32));
+    m.write(desc->workspace, kda_conv_bwd_workspace_size(desc));
+    if (m.clash()) return KDA_ERR_OVERLAP;
     st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
     if (st != KDA_OK) return st;
     Workspace ws(desc->workspace, desc->workspace_bytes, kda_conv_bwd_workspace_size(desc), stream);
@@ -335,7 +440,11 @@ extern "C" kda_status_t kda_ssm_decode(const void *x, const void *dt, const void
     if (desc->num_seqs > 0x7fffffff / (desc->H * (desc->P / 64))) return KDA_ERR_SHAPE;
     if (!out || !final_state) return KDA_ERR_NULL;
     if (!aligned(out, 16)) return KDA_ERR_ALIGN;
-    if (final_state == initial_state && desc->initial_state_dtype != desc->final_state_dtype) return KDA_ERR_DTYPE;
+    Memory m;
+    ssm_reads(m, x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, nullptr, desc);
+    m.write(out, ssm_out_bytes(desc));
+    m.write(final_state, ssm_state_bytes(desc, desc->final_state_dtype), initial_state);
+    if (m.clash()) return KDA_ERR_OVERLAP;
     a.ht = final_state;
     a.out = static_cast<uint16_t *>(out);
     return of_hip(kda_launch_ssm_decode(a, stream));

@@ -20,6 +20,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int64
 _BF16, _FP32 = 1, 2
 _STATE_DTYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
+_FP32_ONLY = {torch.float32: _FP32}
+_INT64_ONLY = {torch.int64: 0}
 
 
 class KdaRmsnormDesc(ctypes.Structure):
@@ -69,80 +71,55 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _on_device(dev: torch.device, **tensors) -> None:
-    if dev.type != "cuda":
+def _bf16(t: torch.Tensor, name: str, dev: int) -> None:
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s must be bfloat16, got %s" % (name, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, dev))
+
+
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("inputs must be on a HIP device")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    return dev
 
 
-def _bf16(**tensors) -> None:
-    for name, t in tensors.items():
-        if t.dtype != torch.bfloat16:
-            raise ValueError("%s must be bfloat16, got %s" % (name, t.dtype))
-
-
-def _param(t: Optional[torch.Tensor], name: str, shape: tuple, fp32_only: bool = False) -> None:
+def _whole(t: Optional[torch.Tensor], name: str, shape: tuple, dev: int, dtypes=_STATE_DTYPES) -> int:
+    """Checks a contiguous parameter, state or index tensor; its type's code (0 for None)."""
     if t is None:
-        return
-    if t.dtype not in _STATE_DTYPES or (fp32_only and t.dtype != torch.float32):
-        raise ValueError("%s must be %s, got %s" % (name, "float32" if fp32_only else "bf16 or fp32", t.dtype))
-    if tuple(t.shape) != shape or not t.is_contiguous():
+        return 0
+    code = dtypes.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(k) for k in dtypes), t.dtype))
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous tensor of shape %s" % (name, list(shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, dev))
+    return code
 
 
-def _output(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, dev) -> torch.Tensor:
+def _output(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, dev: int) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, list(shape), dev))
+    _whole(t, name, shape, dev, {dtype: 1})
     return t
 
 
-def _state_code(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else _STATE_DTYPES[t.dtype]
-
-
-def _overlap(a: Optional[torch.Tensor], b: Optional[torch.Tensor]) -> bool:
-    """Whether two tensors' memory overlaps (their spans, strides included)."""
-    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
-        return False
-
-    def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
-
-
-def _apart(written: dict, read: dict, same: tuple = ()) -> None:
-    """Refuses outputs that overlap an input or each other, but for the pairs in
-    ``same``, which may be one and the same memory."""
-    done = []
-    for w, a in written.items():
-        for r, b in list(read.items()) + done:
-            if _overlap(a, b):
-                if (w, r) in same and a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and b.is_contiguous():
-                    continue
-                raise ValueError("%s overlaps %s" % (w, r))
-        done.append((w, a))
-
-
-def _workspace(t: Optional[torch.Tensor], need: int, dev, d) -> Optional[torch.Tensor]:
+def _workspace(t: Optional[torch.Tensor], need: int, dev: int, d) -> Optional[torch.Tensor]:
     if t is None:
         t = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise ValueError("workspace must be a contiguous tensor of %d bytes on %s" % (need, dev))
+    elif t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError("workspace must be a contiguous tensor of %d bytes on cuda:%d" % (need, dev))
     d.workspace = t.data_ptr()
     d.workspace_bytes = t.numel() * t.element_size()
     return t
 
 
-def _call(fn, dev, *args) -> None:
-    """``fn(*args, stream)`` on the current stream of ``dev``."""
+def _call(fn, dev: int, *args) -> None:
+    """``fn(*args, stream)`` on the current stream of device ``dev``."""
     stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -157,41 +134,43 @@ def _call(fn, dev, *args) -> None:
 
 def _rows(t: torch.Tensor, name: str, D: int) -> Tuple[int, int]:
     """(number of rows, elements between them) of [..., D] with even row strides."""
-    if t.dim() == 0 or t.shape[-1] != D:
-        raise ValueError("%s must be [..., %d]" % (name, D))
-    if t.stride(-1) != 1 and D > 1:
+    if t.is_contiguous():
+        return t.numel() // D, D
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and D > 1:
         raise ValueError("%s must be contiguous along its last dimension" % name)
     rows, stride, span = 1, D, None
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
-        if span is not None and n > 0 and s != span:
-            raise ValueError("%s must have rows at one stride (call .contiguous())" % name)
         if span is None:
             stride = s
+        elif s != span:
+            raise ValueError("%s must have rows at one stride (call .contiguous())" % name)
         rows, span = rows * n, s * n
     return rows, stride
 
 
 def _rmsnorm_args(x, weight, eps, residual, residual_out, group=0):
-    _bf16(x=x)
-    D = x.shape[-1] if x.dim() else 0
+    """(descriptor, device, residual_out)"""
+    dev = _device_of(x)
+    _bf16(x, "x", dev)
+    shape = x.shape
+    D = shape[-1] if shape else 0
     if D < 1:
         raise ValueError("x must be [..., D] with D >= 1")
     rows, xs = _rows(x, "x", D)
-    _param(weight, "weight", (D,))
-    rs = 0
+    wcode = _whole(weight, "weight", (D,), dev)
+    rs = rcode = 0
     if residual is not None:
-        if residual.shape != x.shape or residual.dtype not in _STATE_DTYPES:
-            raise ValueError("residual must be bf16 or fp32 of x's shape")
+        rcode = _STATE_DTYPES.get(residual.dtype, 0)
+        if residual.shape != shape or not rcode or residual.get_device() != dev:
+            raise ValueError("residual must be bf16 or fp32, of x's shape and on its device")
         rs = _rows(residual, "residual", D)[1]
-    _on_device(x.device, weight=weight, residual=residual)
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-    else:
-        residual_out = _output(residual_out, "residual_out", x.shape, residual.dtype, x.device)
-    return KdaRmsnormDesc(rows, D, xs, rs, _state_code(residual), _STATE_DTYPES[weight.dtype], float(eps), group), residual_out
+        residual_out = _output(residual_out, "residual_out", shape, residual.dtype, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    return KdaRmsnormDesc(rows, D, xs, rs, rcode, wcode, eps, group), dev, residual_out
 
 
 def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -204,11 +183,9 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
     shape, or None; out: bf16, allocated if None (it may be x); residual_out: h
     in the residual's type, allocated if None (it may be the residual); None
     without a residual."""
-    d, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out)
-    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
-    _apart({"out": out, "residual_out": residual_out}, {"x": x, "residual": residual, "weight": weight},
-           (("out", "x"), ("residual_out", "residual")))
-    _call(_library().kda_rmsnorm_fwd, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
+    d, dev, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out)
+    out = _output(out, "out", x.shape, torch.bfloat16, dev)
+    _call(_library().kda_rmsnorm_fwd, dev, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
           out.data_ptr(), d)
     return out, residual_out
 
@@ -224,13 +201,11 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: O
     magnitude / 448 (at least 2^-126)."""
     if group not in (0, 128):
         raise ValueError("group must be 0 (one scale per row) or 128")
-    d, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out, group)
-    out = _output(out, "out", x.shape, torch.float8_e4m3fn, x.device)
-    n = -(-d.D // group) if group else 1
-    scales = _output(scales, "scales", (*x.shape[:-1], n), torch.float32, x.device)
-    _apart({"out": out, "residual_out": residual_out, "scales": scales}, {"x": x, "residual": residual, "weight": weight},
-           (("residual_out", "residual"),))
-    _call(_library().kda_rmsnorm_quant, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
+    d, dev, residual_out = _rmsnorm_args(x, weight, eps, residual, residual_out, group)
+    shape = x.shape
+    out = _output(out, "out", shape, torch.float8_e4m3fn, dev)
+    scales = _output(scales, "scales", shape[:-1] + (-(-shape[-1] // group) if group else 1,), torch.float32, dev)
+    _call(_library().kda_rmsnorm_quant, dev, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
           out.data_ptr(), scales.data_ptr(), d)
     return out, scales, residual_out
 
@@ -250,31 +225,29 @@ def rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, eps: float, d_out: torch.
     residual: the fp32 gradient when h is fp32, dx itself when it is bf16, None
     without d_residual_out and a bf16 h) and dweight (fp32 [D]).  outputs: None,
     or a dict of tensors of those names to write into."""
-    if h.dtype not in _STATE_DTYPES:
+    dev = _device_of(h)
+    hcode = _STATE_DTYPES.get(h.dtype, 0)
+    if not hcode:
         raise ValueError("h must be bf16 or fp32, got %s" % h.dtype)
-    _bf16(d_out=d_out)
-    D = h.shape[-1] if h.dim() else 0
-    if D < 1 or d_out.shape != h.shape:
+    _bf16(d_out, "d_out", dev)
+    shape = h.shape
+    D = shape[-1] if shape else 0
+    if D < 1 or d_out.shape != shape:
         raise ValueError("h must be [..., D] and d_out of its shape")
     rows, hs = _rows(h, "h", D)
     ds = _rows(d_out, "d_out", D)[1]
     rs = 0
     if d_residual_out is not None:
-        if d_residual_out.shape != h.shape or d_residual_out.dtype != h.dtype:
-            raise ValueError("d_residual_out must be of h's shape and type")
+        if d_residual_out.shape != shape or d_residual_out.dtype != h.dtype or d_residual_out.get_device() != dev:
+            raise ValueError("d_residual_out must be of h's shape and type and on its device")
         rs = _rows(d_residual_out, "d_residual_out", D)[1]
-    _param(weight, "weight", (D,))
-    dev = h.device
-    _on_device(dev, weight=weight, d_out=d_out, d_residual_out=d_residual_out)
+    d = KdaRmsnormDesc(rows, D, hs, 0, hcode, _whole(weight, "weight", (D,), dev), eps, 0, ds, rs)
     given = outputs or {}
-    dx = _output(given.get("dx"), "dx", h.shape, torch.bfloat16, dev)
-    dres = _output(given.get("dresidual"), "dresidual", h.shape, torch.float32, dev) if h.dtype == torch.float32 else None
+    dx = _output(given.get("dx"), "dx", shape, torch.bfloat16, dev)
+    dres = _output(given.get("dresidual"), "dresidual", shape, torch.float32, dev) if hcode == _FP32 else None
     dw = _output(given.get("dweight"), "dweight", (D,), torch.float32, dev)
-    d = KdaRmsnormDesc(rows, D, hs, 0, _STATE_DTYPES[h.dtype], _STATE_DTYPES[weight.dtype], float(eps), 0, ds, rs)
     lib = _library()
-    ws = _workspace(workspace, lib.kda_rmsnorm_bwd_workspace_size(d), dev, d)
-    _apart({"dx": dx, "dresidual": dres, "dweight": dw, "workspace": ws},
-           {"h": h, "weight": weight, "d_out": d_out, "d_residual_out": d_residual_out})
+    ws = _workspace(workspace, lib.kda_rmsnorm_bwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
     _call(lib.kda_rmsnorm_bwd, dev, h.data_ptr(), weight.data_ptr(), d_out.data_ptr(), _ptr(d_residual_out),
           dx.data_ptr(), _ptr(dres), dw.data_ptr(), d)
     return {"dx": dx, "dresidual": dres if dres is not None else dx if d_residual_out is not None else None,
@@ -314,53 +287,53 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
 
 # ---- short causal convolution ----------------------------------------------------
 
-def _tokens(t: torch.Tensor, name: str, inner: tuple) -> Tuple[int, int]:
-    """Batch and token strides of [B, T, *inner] with contiguous inner dimensions."""
-    want, n = [], 1
-    for s in reversed(inner):
-        want.append(n)
-        n *= s
-    for size, st, w in zip(reversed(t.shape[2:]), reversed(t.stride()[2:]), want):
-        if size > 1 and st != w:
+def _tokens(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """Batch and token strides of [B, T, ...] with contiguous further dimensions."""
+    shape, strides = t.shape, t.stride()
+    n = 1
+    for i in range(len(shape) - 1, 1, -1):
+        if shape[i] > 1 and strides[i] != n:
             raise ValueError("%s must be contiguous in its dimensions behind [B, T]" % name)
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+        n *= shape[i]
+    return (strides[0] if shape[0] > 1 else 0), (strides[1] if shape[1] > 1 else 0)
 
 
-def _num_seqs(cu_seqlens: Optional[torch.Tensor], B: int) -> int:
+def _num_seqs(cu_seqlens: Optional[torch.Tensor], B: int, dev: Optional[int] = None) -> int:
     if cu_seqlens is None:
         return B
-    if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
+    n = cu_seqlens.numel()
+    if cu_seqlens.dim() != 1 or n < 2:
         raise ValueError("cu_seqlens must be a 1-D int64 tensor of at least 2 entries")
     if B != 1:
         raise ValueError("with cu_seqlens the batch size must be 1")
-    return cu_seqlens.numel() - 1
+    if dev is not None:
+        _whole(cu_seqlens, "cu_seqlens", (n,), dev, _INT64_ONLY)
+    return n - 1
 
 
 _ACTIVATIONS = {None: 0, "silu": 1}
 
 
 def _conv_args(x, weight, bias, activation, initial_state, final_state, cu_seqlens, final_name="final_state"):
-    _bf16(x=x)
+    """(descriptor, device)"""
+    dev = _device_of(x)
+    _bf16(x, "x", dev)
     if x.dim() != 3 or x.shape[0] < 1 or x.shape[2] < 1:
         raise ValueError("x must be [B, T, D]")
     B, T, D = x.shape
     if weight.dim() != 2 or weight.shape[1] not in (2, 3, 4):
         raise ValueError("weight must be [D, W] with W = 2, 3 or 4")
     W = weight.shape[1]
-    _param(weight, "weight", (D, W))
-    _param(bias, "bias", (D,))
-    if bias is not None and bias.dtype != weight.dtype:
+    wcode = _whole(weight, "weight", (D, W), dev)
+    if bias is not None and _whole(bias, "bias", (D,), dev) != wcode:
         raise ValueError("bias must have weight's dtype")
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be None or 'silu'")
-    N = _num_seqs(cu_seqlens, B)
-    _param(initial_state, "initial_state", (N, W - 1, D))
-    _param(final_state, final_name, (N, W - 1, D))
-    _on_device(x.device, weight=weight, bias=bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
-               **{final_name: final_state})
-    sb, st = _tokens(x, "x", (D,))
-    return KdaConvDesc(B, T, D, W, N, sb, st, 0, 0, _ACTIVATIONS[activation], _STATE_DTYPES[weight.dtype],
-                       _state_code(initial_state), _state_code(final_state))
+    N = _num_seqs(cu_seqlens, B, dev)
+    sb, st = _tokens(x, "x")
+    return KdaConvDesc(B, T, D, W, N, sb, st, 0, 0, _ACTIVATIONS[activation], wcode,
+                       _whole(initial_state, "initial_state", (N, W - 1, D), dev),
+                       _whole(final_state, final_name, (N, W - 1, D), dev)), dev
 
 
 def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -376,12 +349,9 @@ def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     inputs before and behind the tokens, oldest first, or None (zeros / not
     wanted; final_state may be initial_state); cu_seqlens: int64 [N + 1] on the
     device (then B == 1) or None; out: bf16 [B, T, D], allocated if None."""
-    d = _conv_args(x, weight, bias, activation, initial_state, final_state, cu_seqlens)
-    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
-    _apart({"out": out, "final_state": final_state},
-           {"x": x, "weight": weight, "bias": bias, "initial_state": initial_state, "cu_seqlens": cu_seqlens},
-           (("final_state", "initial_state"),))
-    _call(_library().kda_conv_fwd, x.device, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
+    d, dev = _conv_args(x, weight, bias, activation, initial_state, final_state, cu_seqlens)
+    out = _output(out, "out", x.shape, torch.bfloat16, dev)
+    _call(_library().kda_conv_fwd, dev, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
           _ptr(final_state), _ptr(cu_seqlens), out.data_ptr(), d)
     return out, final_state
 
@@ -397,11 +367,9 @@ def conv_decode(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
         raise ValueError("final_state must be given (it may be initial_state)")
     if x.dim() != 3 or x.shape[1] != 1:
         raise ValueError("x must be [N, 1, D]")
-    d = _conv_args(x, weight, bias, activation, initial_state, final_state, None)
-    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
-    _apart({"out": out, "final_state": final_state},
-           {"x": x, "weight": weight, "bias": bias, "initial_state": initial_state}, (("final_state", "initial_state"),))
-    _call(_library().kda_conv_decode, x.device, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
+    d, dev = _conv_args(x, weight, bias, activation, initial_state, final_state, None)
+    out = _output(out, "out", x.shape, torch.bfloat16, dev)
+    _call(_library().kda_conv_decode, dev, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state),
           final_state.data_ptr(), out.data_ptr(), d)
     return out, final_state
 
@@ -423,13 +391,11 @@ def conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     initial_state is given).  Rows of dx behind a packed batch's last sequence
     are left as they were.  outputs: None, or a dict of tensors of those names
     to write into."""
-    d = _conv_args(x, weight, bias, activation, initial_state, d_final_state, cu_seqlens, "d_final_state")
-    _bf16(d_out=d_out)
+    d, dev = _conv_args(x, weight, bias, activation, initial_state, d_final_state, cu_seqlens, "d_final_state")
+    _bf16(d_out, "d_out", dev)
     if d_out.shape != x.shape:
         raise ValueError("d_out must be of x's shape")
-    dev = x.device
-    _on_device(dev, d_out=d_out)
-    d.d_out_stride_b, d.d_out_stride_t = _tokens(d_out, "d_out", (d.D,))
+    d.d_out_stride_b, d.d_out_stride_t = _tokens(d_out, "d_out")
     given = outputs or {}
     f32 = torch.float32
     if with_d_initial is None:
@@ -440,9 +406,7 @@ def conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
            "d_initial_state": _output(given.get("d_initial_state"), "d_initial_state", (d.num_seqs, d.W - 1, d.D), f32, dev)
            if with_d_initial else None}
     lib = _library()
-    ws = _workspace(workspace, lib.kda_conv_bwd_workspace_size(d), dev, d)
-    _apart({**res, "workspace": ws}, {"x": x, "weight": weight, "bias": bias, "d_out": d_out, "d_final_state": d_final_state,
-                                      "initial_state": initial_state, "cu_seqlens": cu_seqlens})
+    ws = _workspace(workspace, lib.kda_conv_bwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
     _call(lib.kda_conv_bwd, dev, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
           d_out.data_ptr(), _ptr(d_final_state), res["dx"].data_ptr(), res["dweight"].data_ptr(), _ptr(res["dbias"]),
           _ptr(res["d_initial_state"]), d)
@@ -496,24 +460,22 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 
 def _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks=0,
               final_name="final_state"):
-    _bf16(x=x, dt=dt, B=B, C=C)
+    """(descriptor, device)"""
+    dev = _device_of(x)
+    _bf16(x, "x", dev), _bf16(dt, "dt", dev), _bf16(B, "B", dev), _bf16(C, "C", dev)
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError("x must be [B, T, H, P] and B [B, T, G, N]")
     nb, T, H, P = x.shape
-    G, S = B.shape[2:]
-    if nb < 1 or H < 1 or G < 1 or H % G or tuple(B.shape[:2]) != (nb, T) or C.shape != B.shape or \
-            tuple(dt.shape) != (nb, T, H):
+    nb2, T2, G, S = shape = B.shape
+    if nb < 1 or H < 1 or G < 1 or H % G or nb2 != nb or T2 != T or C.shape != shape or dt.shape != (nb, T, H):
         raise ValueError("shape mismatch among x, dt, B and C (H must be a multiple of G)")
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
-        _param(t, name, (H,), fp32_only=True)
-    N = _num_seqs(cu_seqlens, nb)
-    _param(initial_state, "initial_state", (N, H, P, S))
-    _param(final_state, final_name, (N, H, P, S))
-    _on_device(x.device, dt=dt, B=B, C=C, A_log=A_log, dt_bias=dt_bias, D=D, initial_state=initial_state,
-               cu_seqlens=cu_seqlens, **{final_name: final_state})
-    return KdaSsmDesc(nb, T, H, P, G, S, N, *_tokens(x, "x", (H, P)), *_tokens(dt, "dt", (H,)), *_tokens(B, "B", (G, S)),
-                      *_tokens(C, "C", (G, S)), 0, 0, _state_code(initial_state), _state_code(final_state), None, 0,
-                      int(piece_chunks))
+    _whole(A_log, "A_log", (H,), dev, _FP32_ONLY)
+    _whole(dt_bias, "dt_bias", (H,), dev, _FP32_ONLY)
+    _whole(D, "D", (H,), dev, _FP32_ONLY)
+    N = _num_seqs(cu_seqlens, nb, dev)
+    return KdaSsmDesc(nb, T, H, P, G, S, N, *_tokens(x, "x"), *_tokens(dt, "dt"), *_tokens(B, "B"), *_tokens(C, "C"), 0, 0,
+                      _whole(initial_state, "initial_state", (N, H, P, S), dev),
+                      _whole(final_state, final_name, (N, H, P, S), dev), None, 0, piece_chunks), dev
 
 
 def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
@@ -527,11 +489,8 @@ def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tens
         raise ValueError("final_state must be given (it may be initial_state)")
     if x.dim() != 4 or x.shape[1] != 1:
         raise ValueError("x must be [N, 1, H, P]")
-    d = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, None)
-    out = _output(out, "out", x.shape, torch.bfloat16, x.device)
-    _apart({"out": out, "final_state": final_state},
-           {"x": x, "dt": dt, "B": B, "C": C, "A_log": A_log, "dt_bias": dt_bias, "D": D, "initial_state": initial_state},
-           (("final_state", "initial_state"),))
-    _call(_library().kda_ssm_decode, x.device, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
+    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, None)
+    out = _output(out, "out", x.shape, torch.bfloat16, dev)
+    _call(_library().kda_ssm_decode, dev, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
           _ptr(dt_bias), _ptr(D), _ptr(initial_state), final_state.data_ptr(), out.data_ptr(), d)
     return out, final_state

@@ -56,7 +56,8 @@ typedef enum {
     KDA_ERR_ALIGN = 6,       /* a tensor pointer not 16-byte aligned (workspace: 256) */
     KDA_ERR_WORKSPACE = 7,   /* workspace_bytes smaller than kda_fwd_workspace_size() */
     KDA_ERR_HIP = 8,         /* a HIP launch error                                 */
-    KDA_ERR_SCRATCH = 9      /* kda_fwd_noalloc: the call needs more workspace than its static scratch */
+    KDA_ERR_SCRATCH = 9,     /* kda_fwd_noalloc: the call needs more workspace than its static scratch */
+    KDA_ERR_OVERLAP = 10     /* kda_layer.h: a written tensor overlaps a read one or another written one */
 } kda_status_t;
 
 /* Shapes and the caller-owned workspace of one call.

@@ -19,7 +19,9 @@
  * (stated at each call) are contiguous, tokens are `*_stride_t` apart and batch
  * rows `*_stride_b` apart, so that slices of a wider projection need no copy.
  * Inputs may overlap or be broadcast (stride 0).  Every tensor that a call
- * writes is contiguous.
+ * writes is contiguous and lies apart from everything else that the call
+ * touches (KDA_ERR_OVERLAP), but for the pairs that may be one tensor, as
+ * stated at the calls.
  *
  * Packed batches.  With cu_seqlens (int64 [num_seqs + 1], cu[0] = 0, never
  * falling, cu[num_seqs] <= T), B is 1 and sequence n holds the tokens
