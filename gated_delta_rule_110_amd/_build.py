@@ -11,9 +11,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_intra.hip", "kda_chain.hip", "kda_fused.hip", "kda_segment.hip", "kda_decode.hip", "kda_bwd.hip",
-           "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm_decode.hip", "kda_layer_api.hip"]
+           "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm.hip", "kda_ssm_decode.hip",
+           "kda_layer_api.hip"]
 HEADERS = [os.path.join(CSRC, "kda_common.h"), os.path.join(CSRC, "kda_intra_body.h"),
-           os.path.join(CSRC, "kda_layer_args.h"), os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_layer.h")]
+           os.path.join(CSRC, "kda_layer_args.h"), os.path.join(CSRC, "kda_ssm_common.h"), os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_layer.h")]
 
 # -packed-fp32-ops off: hipcc must not emit packed fp32 VALU instructions.
 HIPCC_FLAGS = [
@@ -32,14 +33,16 @@ def hipcc() -> str:
 
 # Per-source additions.  The state chain keeps its MFMA accumulators in
 # ordinary VGPRs: the state update multiplies them by the decay every chunk, and
-# accumulator-register copies around that multiply would sit on the serial path.
+# accumulator-register copies around that multiply would sit on the serial path
+# (the same in the state-space scan).
 # The intra-chunk kernel is scheduled for instruction-level parallelism (it
 # runs two workgroups per CU and spends much of each one's life on dependent
 # chains): 1.2% faster than the default scheduler over 10 paired runs.
 # The backward's per-chunk kernel runs one workgroup per CU (its LDS), so it may
 # use the whole register file; in this form its overflow goes to accumulator
 # registers rather than to scratch memory.
-EXTRA_FLAGS = {"kda_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+EXTRA_FLAGS = {"kda_ssm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kda_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kda_fused.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],
                "kda_intra.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]}

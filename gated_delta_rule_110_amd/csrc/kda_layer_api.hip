@@ -22,6 +22,9 @@ constexpr int64_t kMaxTokens = int64_t(1) << 40;
 constexpr int64_t kMaxColumns = int64_t(1) << 22;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxSeqs = 0x7fffffff;
+constexpr int64_t kMaxScanTokens = (int64_t(1) << 31) - 128;  // pieces and chunks are counted in 32 bits
+// Workgroups of 256 threads in one launch: its work-items are counted in 32 bits.
+constexpr int64_t kMaxGroups = int64_t(1) << 23;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
@@ -218,7 +221,7 @@ size_t conv_token_bytes(const kda_conv_desc_t *d) { return (size_t)(d->B * d->T)
 kda_status_t check_ssm(const kda_ssm_desc_t *d, bool packed) {
     if (d->B < 1 || d->T < 0 || d->H < 1 || d->G < 1 || d->num_seqs < 1) return KDA_ERR_SHAPE;
     if (d->H > 65535 || d->H % d->G != 0) return KDA_ERR_SHAPE;
-    if (d->B > kMaxSeqs || d->num_seqs > kMaxSeqs || d->T > (int64_t(1) << 31) / d->B) return KDA_ERR_SHAPE;
+    if (d->B > kMaxSeqs || d->num_seqs > kMaxSeqs || d->T > kMaxScanTokens / d->B) return KDA_ERR_SHAPE;
     if (packed ? d->B != 1 : d->num_seqs != d->B) return KDA_ERR_SHAPE;
     if ((d->P != 64 && d->P != 128) || (d->N != 64 && d->N != 128)) return KDA_ERR_UNSUPPORTED;
     const int64_t strides[] = {d->x_stride_b, d->x_stride_t, d->dt_stride_b, d->dt_stride_t,
@@ -273,6 +276,101 @@ void ssm_reads(Memory &m, const void *x, const void *dt, const void *Bm, const v
     for (const float *p : {A_log, dt_bias, D}) m.read(p, (size_t)d->H * 4);
     m.read(h0, ssm_state_bytes(d, d->initial_state_dtype));
     m.read(cu, (size_t)(d->num_seqs + 1) * 8);
+}
+
+// How a call's sequences are cut into pieces, and its workspace.
+struct SsmPlan {
+    int64_t cps, pps, pieces, chunks;   // chunks / pieces per sequence (not packed); both in all (bounds when packed)
+    int pc;                             // chunks per piece
+    size_t off_piece, off_chunk, off_state, off_decay, total;
+};
+
+// Workgroups a launch should have: two rounds of the two that fit each of the
+// 256 CUs.  Fewer than kMinPiece chunks per piece would leave a piece's state
+// (32 KiB of fp32 per 64 channels and 128 entries) larger than its tokens.
+constexpr int64_t kWantGroups = 1024;
+constexpr int64_t kMinPiece = 4;
+
+kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
+    const int64_t units = d->H * (d->P / 64);
+    p = SsmPlan{};
+    p.cps = packed ? 0 : (d->T + 63) / 64;
+    const int64_t all = packed ? d->T / 64 + 1 : d->B * p.cps;
+    int64_t pc = d->piece_chunks;
+    if (pc == 0) {
+        pc = (all * units + kWantGroups - 1) / kWantGroups;
+        if (pc < kMinPiece) pc = kMinPiece;
+        // chains that fill the GPU by themselves are not cut
+        if (!packed && d->B * units >= kWantGroups / 2) pc = p.cps;
+    }
+    const int64_t top = packed ? all : p.cps;
+    if (pc > top) pc = top;
+    if (pc < 1) pc = 1;
+    p.chunks = packed ? d->T / 64 + d->num_seqs : d->B * p.cps;
+    p.pps = packed ? 0 : (p.cps + pc - 1) / pc;
+    p.pieces = packed ? d->T / (64 * pc) + d->num_seqs : d->B * p.pps;
+    p.pc = (int)pc;
+    if ((p.pieces + 7) / 8 * 8 > kMaxGroups / units || p.chunks > 0x7fffffff) return KDA_ERR_SHAPE;
+    size_t o = 0;
+    if (packed) {
+        p.off_piece = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
+        p.off_chunk = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
+    }
+    if (packed || p.pps > 1) {
+        p.off_state = o; o = align_up(o + (size_t)p.pieces * (size_t)d->H * (size_t)(d->P * d->N) * 4, 256);
+        p.off_decay = o; o = align_up(o + (size_t)p.pieces * (size_t)d->H * 4, 256);
+    }
+    p.total = o;
+    return KDA_OK;
+}
+
+// The larger of the packed and unpacked needs, where both are possible.
+template <typename F>
+int64_t over_plans(const kda_ssm_desc_t *d, F f) {
+    int64_t best = -1;
+    if (!d) return best;
+    for (bool packed : {false, true}) {
+        SsmPlan p;
+        if (check_ssm(d, packed) != KDA_OK || plan_ssm(d, packed, p) != KDA_OK) continue;
+        const int64_t v = f(p);
+        best = v > best ? v : best;
+    }
+    return best;
+}
+
+SsmChainArgs chain_args(const SsmArgs &a, const SsmPlan &p, const Workspace &ws) {
+    SsmChainArgs c{};
+    c.x = a.x; c.k = a.Bm; c.c = a.Cm; c.dt = a.dt;
+    c.xb = a.xb; c.xt = a.xt; c.kb = a.bb; c.kt = a.bt; c.cb = a.cb; c.ct = a.ct; c.dtb = a.dtb; c.dtt = a.dtt;
+    c.A_log = a.A_log; c.dt_bias = a.dt_bias; c.D = a.D;
+    c.cu = a.cu;
+    c.T = a.T; c.H = a.H; c.P = a.P; c.G = a.G; c.seqs = a.num_seqs;
+    c.pieces = p.pieces; c.chunks = p.chunks; c.pps = p.pps; c.cps = p.cps; c.pc = p.pc;
+    if (a.cu) {
+        c.piece_off = reinterpret_cast<const int32_t *>(ws.at(p.off_piece));
+        c.chunk_off = reinterpret_cast<const int32_t *>(ws.at(p.off_chunk));
+    }
+    if (a.cu || p.pps > 1) {
+        c.state = reinterpret_cast<float *>(ws.at(p.off_state));
+        c.decay = reinterpret_cast<float *>(ws.at(p.off_decay));
+    }
+    return c;
+}
+
+hipError_t launch_table(const SsmArgs &a, const SsmPlan &p, const Workspace &ws, hipStream_t s) {
+    if (!a.cu) return hipSuccess;
+    return kda_launch_ssm_table(a.cu, a.num_seqs, a.T, p.pc, p.pieces, p.chunks, reinterpret_cast<int32_t *>(ws.at(p.off_piece)),
+                                reinterpret_cast<int32_t *>(ws.at(p.off_chunk)), s);
+}
+
+// The states entering the pieces, and the final states of empty sequences.
+// Nothing to do for sequences of one piece each.
+hipError_t launch_entering(const SsmChainArgs &c, int N, bool reverse, hipStream_t s) {
+    if (!c.cu && c.pps == 1) return hipSuccess;
+    hipError_t e = hipSuccess;
+    if (c.T > 0) e = kda_launch_ssm_pieces(c, N, reverse, s);
+    if (e == hipSuccess) e = kda_launch_ssm_scan(c, N, reverse, s);
+    return e;
 }
 
 }  // namespace
@@ -437,7 +535,6 @@ extern "C" kda_status_t kda_ssm_decode(const void *x, const void *dt, const void
     const kda_status_t st = ssm_args(x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, final_state, nullptr, desc, a);
     if (st != KDA_OK) return st;
     if (desc->T != 1) return KDA_ERR_SHAPE;
-    if (desc->num_seqs > 0x7fffffff / (desc->H * (desc->P / 64))) return KDA_ERR_SHAPE;
     if (!out || !final_state) return KDA_ERR_NULL;
     if (!aligned(out, 16)) return KDA_ERR_ALIGN;
     Memory m;
@@ -448,4 +545,49 @@ extern "C" kda_status_t kda_ssm_decode(const void *x, const void *dt, const void
     a.ht = final_state;
     a.out = static_cast<uint16_t *>(out);
     return of_hip(kda_launch_ssm_decode(a, stream));
+}
+
+extern "C" size_t kda_ssm_fwd_workspace_size(const kda_ssm_desc_t *desc) {
+    const int64_t n = over_plans(desc, [](const SsmPlan &p) { return (int64_t)p.total; });
+    return n > 0 ? (size_t)n : 0;
+}
+
+extern "C" int64_t kda_ssm_piece_chunks(const kda_ssm_desc_t *desc) {
+    SsmPlan p;
+    const bool packed = desc && desc->num_seqs != desc->B;
+    if (!desc || check_ssm(desc, packed) != KDA_OK || plan_ssm(desc, packed, p) != KDA_OK) return -1;
+    return p.pc;
+}
+
+extern "C" kda_status_t kda_ssm_fwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+                                    const float *dt_bias, const float *D, const void *initial_state,
+                                    void *final_state, const int64_t *cu_seqlens, void *out,
+                                    const kda_ssm_desc_t *desc, hipStream_t stream) {
+    SsmArgs a;
+    kda_status_t st = ssm_args(x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, desc, a);
+    if (st != KDA_OK) return st;
+    if (desc->T > 0 && !out) return KDA_ERR_NULL;
+    if (!aligned(out, 16)) return KDA_ERR_ALIGN;
+    SsmPlan p;
+    st = plan_ssm(desc, cu_seqlens != nullptr, p);
+    if (st != KDA_OK) return st;
+    Memory m;
+    ssm_reads(m, x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, cu_seqlens, desc);
+    m.write(out, ssm_out_bytes(desc));
+    m.write(final_state, ssm_state_bytes(desc, desc->final_state_dtype), initial_state);
+    m.write(desc->workspace, p.total);
+    if (m.clash()) return KDA_ERR_OVERLAP;
+    st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
+    if (st != KDA_OK) return st;
+    Workspace ws(desc->workspace, desc->workspace_bytes, p.total, stream);
+    if (ws.status() != KDA_OK) return ws.status();
+    SsmChainArgs c = chain_args(a, p, ws);
+    c.h0 = initial_state; c.h0_f32 = a.h0_f32;
+    c.ht = final_state; c.ht_f32 = a.ht_f32;
+    c.out = static_cast<uint16_t *>(out);
+    const int N = (int)desc->N;
+    hipError_t e = launch_table(a, p, ws, stream);
+    if (e == hipSuccess) e = launch_entering(c, N, false, stream);
+    if (e == hipSuccess && desc->T > 0) e = kda_launch_ssm_chain(c, N, stream);
+    return of_hip(e);
 }

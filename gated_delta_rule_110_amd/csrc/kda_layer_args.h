@@ -67,6 +67,51 @@ struct SsmArgs {
     int h0_f32, ht_f32;
 };
 
+// The scan's state chains.  A piece is up to `pc` 64-token chunks of one
+// sequence, walked through in order by one workgroup per (head, 64 channels).
+// The tables of a packed batch give the first piece and the first chunk of
+// every sequence; otherwise every sequence has `pps` pieces and `cps` chunks.
+struct SsmChainArgs {
+    const uint16_t *x;         // [tokens, H, P]: x, or d_out backwards
+    const uint16_t *k;         // [tokens, G, N]: B, or C backwards
+    const uint16_t *c;         // C (outputs only)
+    const uint16_t *dt;
+    int64_t xb, xt, kb, kt, cb, ct, dtb, dtt;
+    const float *A_log, *dt_bias, *D;
+    const int64_t *cu;
+    const int32_t *piece_off, *chunk_off;
+    int64_t T, H, P, G, seqs;
+    int64_t pieces, chunks;    // of the batch (upper bounds when packed)
+    int64_t pps, cps;
+    int pc;
+    const void *h0;            // state at the chains' start, or nullptr
+    void *ht;                  // state at their end, or nullptr
+    int h0_f32, ht_f32;
+    float *state;              // [pieces, H, P, N]: every piece's own state, then the one entering it
+    float *decay;              // [pieces, H]: log2 of a piece's decay
+    float *save;               // [chunks, H, P / 64, 64 N]: state entering every chunk (kda_ssm.hip)
+    uint16_t *out;
+};
+
+// The scan's gradient, chunk by chunk, from the states entering every chunk
+// (hs) and the gradients of those leaving it (ds).
+struct SsmGradArgs {
+    const uint16_t *x, *Bm, *Cm, *dt, *dy;
+    int64_t xb, xt, bb, bt, cb, ct, dtb, dtt, yb, yt;
+    const float *A_log, *dt_bias, *D;
+    const int64_t *cu;
+    const int32_t *chunk_off;
+    int64_t T, H, P, G, seqs;
+    int64_t chunks, cps;
+    int share;                 // heads of a group per workgroup
+    int shares;                // workgroups per chunk and group
+    const float *hs, *ds;
+    uint16_t *dx, *ddt, *dB, *dC;
+    float *part;               // [2][shares][chunks][G][64][N]: dB, dC (with more than one share)
+    float *psum;               // [chunks][H][4]: the parameters' gradients
+    float *dA_log, *ddt_bias, *dD;
+};
+
 // fp32 -> two bf16 in one word (round to nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
@@ -104,3 +149,17 @@ hipError_t kda_launch_conv_decode(const kda::ConvArgs &a, int W, hipStream_t s);
 int64_t kda_conv_parts(int64_t B, int64_t T, int64_t D);
 hipError_t kda_launch_conv_bwd(const kda::ConvArgs &a, int W, hipStream_t s);
 hipError_t kda_launch_ssm_decode(const kda::SsmArgs &a, hipStream_t s);
+// The tables of a packed batch: first piece and first chunk of every sequence.
+hipError_t kda_launch_ssm_table(const int64_t *cu, int64_t N, int64_t T, int pc, int64_t most_pieces,
+                                int64_t most_chunks, int32_t *piece_off, int32_t *chunk_off, hipStream_t s);
+// The pieces' own states, from zero (all but a sequence's last piece in walking order).
+hipError_t kda_launch_ssm_pieces(const kda::SsmChainArgs &a, int N, bool reverse, hipStream_t s);
+// The state entering every piece from the pieces' own ones, and the final
+// states of sequences without tokens.
+hipError_t kda_launch_ssm_scan(const kda::SsmChainArgs &a, int N, bool reverse, hipStream_t s);
+// The chains from the entering states, keeping the state entering every chunk
+// (and, reversed, giving the initial state's gradient).
+hipError_t kda_launch_ssm_save(const kda::SsmChainArgs &a, int N, bool reverse, hipStream_t s);
+hipError_t kda_launch_ssm_grad(const kda::SsmGradArgs &a, int N, hipStream_t s);
+// The chains from the entering states: outputs and final states.
+hipError_t kda_launch_ssm_chain(const kda::SsmChainArgs &a, int N, hipStream_t s);

@@ -1,0 +1,492 @@
+// kda_ssm.hip -- the selective state-space scan over whole sequences (gfx950).
+//
+// In chunks of 64 tokens, with a_t = -exp(A_log) dt_t and G_i = sum_{t <= i} a_t
+// within the chunk, the recurrence S_t = e^{a_t} S_{t-1} + dt_t x_t B_t^T becomes
+//
+//   y_i   = e^{G_i} S C_i + sum_{j <= i} M_ij x_j,   M_ij = e^{G_i - G_j} dt_j (C_i . B_j) + [i = j] D
+//   S     <- e^{G_63} S + sum_j w_j x_j B_j^T,        w_j  = e^{G_63 - G_j} dt_j
+//
+// four products on the matrix cores per chunk and head (C B^T, M x, C S^T, the
+// update), with every decay at most 1, so that nothing overflows.
+//
+// x, B and C are bf16, exact as operands.  What is computed in fp32 and then
+// needed as an operand is split into bf16 parts: M and S into two (together
+// 2^-17: their products only reach the bf16 output), the weighted x into three
+// (2^-25, fp32's own step: they add up in the fp32 state).  States, decays and
+// sums stay in fp32.
+//
+// Work.  Chains are serial over chunks but independent over heads and over
+// blocks of 64 channels, and 64 x N states leave most of the GPU idle for a
+// single prompt; so sequences are cut into pieces: a first pass walks through
+// each piece from a zero state (kPieces: B and x only), a scan joins the states
+// of the pieces in fp32, and the second pass starts each piece from the state
+// that enters it.  With one piece per sequence only the last pass runs.
+//
+// A workgroup of four waves holds the state of 64 channels in registers, 16
+// channels a wave: S^T as MFMA accumulators, tile t of 16 state rows by the
+// wave's channels, rows numbered so that a pair of tiles is at once the operand
+// of the next product (rows 4 g + e of tiles 2 q and 2 q + 1 stand for n = 32 q +
+// 8 g + e and + 4).  B, C and x of the chunk are staged in LDS row by row; the
+// operands that run along tokens are read back with the transposing LDS read.
+#include "kda_ssm_common.h"
+
+using namespace kda;
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Passes over a piece.
+constexpr int kPieces = 0;    // from zero: the piece's own state and its decay
+constexpr int kOutputs = 1;   // outputs and final states
+constexpr int kSave = 2;      // the state entering every chunk, for the gradient
+
+// One piece: its sequence, tokens and place.
+struct Piece {
+    int64_t n, index;          // sequence; number of the piece in the batch
+    int64_t row0, t0;          // batch row and token of its first token
+    int count;                 // tokens
+    int64_t chunk0;            // number of its first chunk in the batch
+    bool first, last;          // of its sequence
+    bool valid;
+};
+
+__device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) {
+    Piece p;
+    p.index = index;
+    p.valid = false;
+    int64_t begin = 0, len = a.T, k;
+    if (index >= a.pieces) return p;
+    if (a.cu) {
+        if (index >= a.piece_off[a.seqs]) return p;
+        p.n = seq_of_slot(a.piece_off, a.seqs, index);
+        k = index - a.piece_off[p.n];
+        begin = clamp_to(a.cu[p.n], a.T);
+        len = clamp_to(a.cu[p.n + 1], a.T) - begin;
+        p.row0 = 0;
+        p.chunk0 = a.chunk_off[p.n] + k * a.pc;
+    } else {
+        p.n = index / a.pps;
+        k = index - p.n * a.pps;
+        p.row0 = p.n;
+        p.chunk0 = p.n * a.cps + k * a.pc;
+    }
+    const int64_t from = k * a.pc * kL, size = (int64_t)a.pc * kL;
+    p.t0 = begin + from;
+    p.count = (int)(len - from < size ? len - from : size);
+    p.first = k == 0;
+    p.last = from + size >= len;
+    p.valid = p.count > 0;
+    return p;
+}
+
+// Workgroups to (piece, head, channel block).  Workgroups go to the 8 XCDs in
+// turn; all heads of a piece are given to one XCD, whose L2 then serves B and C
+// of the piece to the heads that share them.
+__device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int64_t &h, int64_t &pb) {
+    const int64_t units = a.H * (a.P / kPB);
+    const int64_t i = blockIdx.x >> 3;
+    const int64_t u = i % units;
+    piece = (i / units) * 8 + (blockIdx.x & 7);
+    h = u / (a.P / kPB);
+    pb = u - h * (a.P / kPB);
+}
+int64_t grid_size(const SsmChainArgs &a) { return (a.pieces + 7) / 8 * 8 * a.H * (a.P / kPB); }
+
+template <int kN, bool kOut>
+struct __align__(16) ChainSmem {
+    uint16_t k[kL * kPitch<kN>];
+    uint16_t c[kOut ? kL * kPitch<kN> : 8];
+    uint16_t x[kL * kXPitch];
+    uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
+    float g[kL], gr[kL];                        // log2 of the decay from the chunk's start, and what rounding it left
+    float dt[kL];
+};
+
+// 8 consecutive state entries of either type.
+__device__ __forceinline__ void load_state8(const void *p, int64_t i, int f32, float *o) {
+    if (f32) {
+        const float4 a = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+        const float4 b = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + 4);
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    } else {
+        unpack_bf16x8(*reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i), o);
+    }
+}
+__device__ __forceinline__ void store_state8(void *p, int64_t i, int f32, const f4 &lo, const f4 &hi) {
+    if (f32) {
+        float *q = reinterpret_cast<float *>(p) + i;
+        *reinterpret_cast<f4 *>(q) = lo;
+        *reinterpret_cast<f4 *>(q + 4) = hi;
+    } else {
+        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p) + i) =
+            make_uint4(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]));
+    }
+}
+
+// kReverse: the chains of the gradient of the state, from the last token to the
+// first: D <- e^{G_63} D + sum_i e^{G_i} d_out_i C_i^T.
+template <int kN, int kPass, bool kReverse>
+__global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs a) {
+    constexpr bool kOut = kPass == kOutputs;
+    // The states that the gradient reads are kept as accumulators hold them, 16
+    // bytes a lane: those of the scan as S (rows: channels), so that a pair of
+    // tiles is an operand along channels, those of its gradient as here, S^T.
+    constexpr bool kSwapped = kPass == kSave && !kReverse;
+    constexpr int kTiles = kN / 16, kQ = kN / 32;
+    __shared__ ChainSmem<kN, kOut> sm;
+    int64_t index, h, pb;
+    place(a, index, h, pb);
+    const Piece p = piece_of(a, index);
+    if (!p.valid) return;
+    if (kPass == kPieces && (kReverse ? p.first : p.last)) return;  // nothing follows it
+
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int64_t grp = h / (a.H / a.G);
+    const float nA2 = -fast_exp(a.A_log[h]) * kLog2e;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float Dh = kOut && a.D ? a.D[h] : 0.f;
+    const uint16_t *xrow = a.x + p.row0 * a.xb + p.t0 * a.xt + h * a.P + pb * kPB;
+    const uint16_t *krow = a.k + p.row0 * a.kb + p.t0 * a.kt + grp * kN;
+    const uint16_t *crow = kOut ? a.c + p.row0 * a.cb + p.t0 * a.ct + grp * kN : nullptr;
+    const uint16_t *drow = a.dt + p.row0 * a.dtb + p.t0 * a.dtt + h;
+    uint16_t *orow = kOut ? a.out + ((p.row0 * a.T + p.t0) * a.H + h) * a.P + pb * kPB : nullptr;
+    // this lane's rows of a state tensor: channel 16 w + r, entries 32 q + 8 g ..
+    const int64_t sbase = (h * a.P + pb * kPB + 16 * w + r) * kN + 8 * g;
+    const int64_t sseq = p.n * a.H * a.P * kN + sbase, spiece = p.index * a.H * a.P * kN + sbase;
+
+    // ---- the state at the start
+    f4 S[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) S[t] = f4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (kPass != kPieces) {
+        const bool whole = p.first && p.last;  // a single piece starts from the initial state itself
+        const void *src = whole ? a.h0 : a.state;
+        const int f32 = whole ? a.h0_f32 : 1;
+        const int64_t from = whole ? p.n : p.index;
+        if (src) {
+            if constexpr (kSwapped) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[t][e] = load_any(src, ((from * a.H + h) * a.P + pb * kPB + 16 * w + 4 * g + e) * kN + 16 * t + r, f32);
+            } else {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    float v[8];
+                    load_state8(src, (whole ? sseq : spiece) + 32 * q, f32, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[2 * q][e] = v[e];
+                        S[2 * q + 1][e] = v[4 + e];
+                    }
+                }
+            }
+        }
+    }
+
+    const int chunks = (p.count + kL - 1) / kL;
+    Rows<kN, kThreads> rk, rc;
+    Rows<kPB, kThreads> rx;
+    float rdt = 0.f;
+    auto fetch = [&](int i) {
+        const int c = kReverse ? chunks - 1 - i : i;
+        const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
+        const int64_t t = (int64_t)c * kL;
+        rk.load(krow + t * a.kt, a.kt, rows);
+        if constexpr (kOut) rc.load(crow + t * a.ct, a.ct, rows);
+        rx.load(xrow + t * a.xt, a.xt, rows);
+        if (w == 0) rdt = lane < rows ? bf16_bits_to_f32(drow[(t + lane) * a.dtt]) : 0.f;
+    };
+    fetch(0);
+    float total = 0.f;
+    for (int i = 0; i < chunks; ++i) {
+        const int c = kReverse ? chunks - 1 - i : i;
+        const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
+        if constexpr (kPass == kSave) {
+            if (p.chunk0 + c < a.chunks) {
+                f4 *dst = reinterpret_cast<f4 *>(a.save) +
+                          (((p.chunk0 + c) * a.H + h) * (a.P / kPB) + pb) * (kPB * kN / 4) + w * kTiles * 64 + lane;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) dst[t * 64] = S[t];
+            }
+            if (i + 1 == chunks && !(kReverse && p.first && a.ht)) break;  // what leaves the piece is not needed
+        }
+        if (i) __syncthreads();  // the chunk before is done with
+        rk.store(sm.k, kPitch<kN>);
+        if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
+        rx.store(sm.x, kXPitch);
+        if (w == 0) step_sizes(rdt, lane < rows, bias, nA2, sm.g, sm.gr, sm.dt);
+        __syncthreads();
+        if (i + 1 < chunks) fetch(i + 1);
+        const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1];
+
+        // x along tokens, for this wave's channels
+        s8 xf[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const uint16_t *q = sm.x + (32 * kb + 4 * g + (r >> 2)) * kXPitch + 16 * w + 4 * (r & 3);
+            xf[kb] = join(read_tr(q), read_tr(q + 16 * kXPitch));
+        }
+
+        if constexpr (kOut) {
+            // ---- M for the token rows 16 w .. 16 w + 15, as B C^T: lane = row i,
+            // its entries the columns j that an operand holds
+            const int ti = 16 * w + r;
+            s8 cf[kQ];
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) cf[q] = lds8(sm.c + ti * kPitch<kN> + 32 * q + 8 * g);
+            const float gi = sm.g[ti], gir = sm.gr[ti];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                if (2 * kb > w) break;
+                float m[8];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int jt = 2 * kb + half;
+                    f4 acc = {0.f, 0.f, 0.f, 0.f};
+                    if (jt <= w) {
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q)
+                            acc = mfma16x16x32_bf16(lds8(sm.k + (16 * jt + r) * kPitch<kN> + 32 * q + 8 * g), cf[q], acc);
+                    }
+                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.g[16 * jt + 4 * g]);
+                    const float4 rj = *reinterpret_cast<const float4 *>(&sm.gr[16 * jt + 4 * g]);
+                    const float4 dj = *reinterpret_cast<const float4 *>(&sm.dt[16 * jt + 4 * g]);
+                    const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, rv[4] = {rj.x, rj.y, rj.z, rj.w};
+                    const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tj = 16 * jt + 4 * g + e;
+                        const float v = acc[e] * (__builtin_amdgcn_exp2f((gi - gv[e]) + (gir - rv[e])) * dv[e]);
+                        m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
+                    }
+                }
+                s8 hi, lo;
+                split2(m, hi, lo);
+                *reinterpret_cast<s8 *>(&sm.m[(((0 * 4 + w) * 2 + kb) * 64 + lane) * 8]) = hi;
+                *reinterpret_cast<s8 *>(&sm.m[(((1 * 4 + w) * 2 + kb) * 64 + lane) * 8]) = lo;
+            }
+            // ---- outputs, transposed: lane = token, entries 4 neighbouring channels
+            s8 sh[kQ], sl[kQ];
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = S[2 * q][e];
+                    v[4 + e] = S[2 * q + 1][e];
+                }
+                split2(v, sh[q], sl[q]);
+            }
+            f4 y[4];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                y[it] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    const s8 cv = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
+                    y[it] = mfma16x16x32_bf16(sh[q], cv, y[it]);
+                    y[it] = mfma16x16x32_bf16(sl[q], cv, y[it]);
+                }
+                const float d = __builtin_amdgcn_exp2f(sm.g[16 * it + r]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[it][e] *= d;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    if (2 * kb > it) break;
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((0 * 4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((1 * 4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+                }
+                const int t = 16 * it + r;
+                if (t < rows)
+                    *reinterpret_cast<uint2 *>(orow + ((int64_t)c * kL + t) * a.H * a.P + 16 * w + 4 * g) =
+                        make_uint2(pack_bf16(y[it][0], y[it][1]), pack_bf16(y[it][2], y[it][3]));
+            }
+        }
+
+        // ---- the state at the chunk's end
+        const float dl = __builtin_amdgcn_exp2f(gl);
+        total += gl;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] *= dl;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            float v[8];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tj = 32 * kb + 16 * half + 4 * g + e;
+                    const float wj = kReverse ? __builtin_amdgcn_exp2f(sm.g[tj])
+                                              : __builtin_amdgcn_exp2f((gl - sm.g[tj]) + (glr - sm.gr[tj])) * sm.dt[tj];
+                    v[4 * half + e] = wj * bf16_bits_to_f32((uint16_t)xf[kb][4 * half + e]);
+                }
+            s8 x0, x1, x2;
+            split3(v, x0, x1, x2);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int col = kSwapped ? 16 * t + 4 * (r & 3) : 32 * (t >> 1) + 8 * (r & 3) + 4 * (t & 1);
+                const uint16_t *q = sm.k + (32 * kb + 4 * g + (r >> 2)) * kPitch<kN> + col;
+                const s8 kv = join(read_tr(q), read_tr(q + 16 * kPitch<kN>));
+                if constexpr (kSwapped) {
+                    S[t] = mfma16x16x32_bf16(x0, kv, S[t]);
+                    S[t] = mfma16x16x32_bf16(x1, kv, S[t]);
+                    S[t] = mfma16x16x32_bf16(x2, kv, S[t]);
+                } else {
+                    S[t] = mfma16x16x32_bf16(kv, x0, S[t]);
+                    S[t] = mfma16x16x32_bf16(kv, x1, S[t]);
+                    S[t] = mfma16x16x32_bf16(kv, x2, S[t]);
+                }
+            }
+        }
+    }
+
+    // ---- the state at the end
+    void *dst = kPass == kPieces ? a.state : kSwapped ? nullptr : (kReverse ? p.first : p.last) ? a.ht : nullptr;
+    if (dst) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+            store_state8(dst, (kPass == kPieces ? spiece : sseq) + 32 * q, kPass == kPieces ? 1 : a.ht_f32, S[2 * q], S[2 * q + 1]);
+    }
+    if (kPass == kPieces && threadIdx.x == 0 && pb == 0) a.decay[p.index * a.H + h] = total;
+}
+
+// The states entering the pieces of every sequence with several of them, in
+// place of the pieces' own states: E_0 = h0, E_{k+1} = 2^decay_k E_k + own_k (last
+// to first when reversed).  Sequences without tokens get their final state here.
+// One thread per 4 entries of a head's state.
+template <int kN, bool kReverse>
+__global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) {
+    const int64_t size = a.P * kN;
+    const int64_t per = size / (4 * kThreads);
+    for (int64_t u = blockIdx.x; u < a.seqs * a.H * per; u += gridDim.x) {
+        const int64_t part = u % per, nh = u / per;
+        const int64_t n = nh / a.H, h = nh - n * a.H;
+        const int64_t off = part * 4 * kThreads + threadIdx.x * 4;
+        int64_t first, count;
+        if (a.cu) {
+            first = a.piece_off[n];
+            count = a.piece_off[n + 1] - first;
+        } else {
+            first = n * a.pps;
+            count = a.pps;
+        }
+        if (count == 1) continue;
+        f4 E = {0.f, 0.f, 0.f, 0.f};
+        if (a.h0)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[e] = load_any(a.h0, nh * size + off + e, a.h0_f32);
+        if (count == 0) {
+            if (a.ht)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) store_any(a.ht, nh * size + off + e, a.ht_f32, E[e]);
+            continue;
+        }
+        for (int64_t i = 0; i < count; ++i) {
+            const int64_t k = first + (kReverse ? count - 1 - i : i);
+            f4 *s = reinterpret_cast<f4 *>(a.state + (k * a.H + h) * size + off);
+            f4 own = {0.f, 0.f, 0.f, 0.f};
+            float d = 0.f;
+            if (i + 1 < count) {
+                own = *s;
+                d = __builtin_amdgcn_exp2f(a.decay[k * a.H + h]);
+            }
+            *s = E;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) E[e] = d * E[e] + own[e];
+        }
+    }
+}
+
+// First piece and first chunk of every sequence of a packed batch: running sums
+// over the sequences by one workgroup.  Lengths that overlap (which no batch
+// has) could add up to more pieces than the workspace holds: the tables end there.
+__global__ __launch_bounds__(1024) void kda_ssm_table_kernel(const int64_t *cu, int64_t N, int64_t T, int pc,
+                                                             int64_t most_pieces, int64_t most_chunks,
+                                                             int32_t *piece_off, int32_t *chunk_off) {
+    __shared__ int64_t sp[1024], sc[1024];
+    const int tid = threadIdx.x;
+    int64_t pieces = 0, chunks = 0;
+    for (int64_t base = 0; base < N; base += 1024) {
+        const int64_t n = base + tid;
+        int64_t c = 0, p = 0;
+        if (n < N) {
+            const int64_t len = clamp_to(cu[n + 1], T) - clamp_to(cu[n], T);
+            c = len > 0 ? (len + kL - 1) / kL : 0;
+            p = (c + pc - 1) / pc;
+        }
+        sp[tid] = p;
+        sc[tid] = c;
+        __syncthreads();
+        for (int d = 1; d < 1024; d <<= 1) {
+            const int64_t vp = tid >= d ? sp[tid - d] : 0, vc = tid >= d ? sc[tid - d] : 0;
+            __syncthreads();
+            sp[tid] += vp;
+            sc[tid] += vc;
+            __syncthreads();
+        }
+        if (n < N) {
+            piece_off[n] = (int32_t)clamp_to(pieces + sp[tid] - p, most_pieces);
+            chunk_off[n] = (int32_t)clamp_to(chunks + sc[tid] - c, most_chunks);
+        }
+        pieces += sp[1023];
+        chunks += sc[1023];
+        __syncthreads();
+    }
+    if (tid == 0) {
+        piece_off[N] = (int32_t)clamp_to(pieces, most_pieces);
+        chunk_off[N] = (int32_t)clamp_to(chunks, most_chunks);
+    }
+}
+
+template <int kN, int kPass, bool kReverse>
+hipError_t launch(const SsmChainArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((kda_ssm_chain_kernel<kN, kPass, kReverse>), dim3((unsigned)grid_size(a)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t kda_launch_ssm_table(const int64_t *cu, int64_t N, int64_t T, int pc, int64_t most_pieces,
+                                int64_t most_chunks, int32_t *piece_off, int32_t *chunk_off, hipStream_t s) {
+    hipLaunchKernelGGL(kda_ssm_table_kernel, dim3(1), dim3(1024), 0, s, cu, N, T, pc, most_pieces, most_chunks, piece_off,
+                       chunk_off);
+    return hipGetLastError();
+}
+
+hipError_t kda_launch_ssm_pieces(const SsmChainArgs &a, int N, bool reverse, hipStream_t s) {
+    if (N == 128) return reverse ? launch<128, kPieces, true>(a, s) : launch<128, kPieces, false>(a, s);
+    return reverse ? launch<64, kPieces, true>(a, s) : launch<64, kPieces, false>(a, s);
+}
+
+hipError_t kda_launch_ssm_scan(const SsmChainArgs &a, int N, bool reverse, hipStream_t s) {
+    const int64_t units = a.seqs * a.H * (a.P * N / (4 * kThreads));
+    const unsigned grid = (unsigned)(units < (1 << 16) ? units : (1 << 16));
+    if (N == 128) {
+        if (reverse) hipLaunchKernelGGL((kda_ssm_scan_kernel<128, true>), dim3(grid), dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((kda_ssm_scan_kernel<128, false>), dim3(grid), dim3(kThreads), 0, s, a);
+    } else {
+        if (reverse) hipLaunchKernelGGL((kda_ssm_scan_kernel<64, true>), dim3(grid), dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((kda_ssm_scan_kernel<64, false>), dim3(grid), dim3(kThreads), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t kda_launch_ssm_save(const SsmChainArgs &a, int N, bool reverse, hipStream_t s) {
+    if (N == 128) return reverse ? launch<128, kSave, true>(a, s) : launch<128, kSave, false>(a, s);
+    return reverse ? launch<64, kSave, true>(a, s) : launch<64, kSave, false>(a, s);
+}
+
+hipError_t kda_launch_ssm_chain(const SsmChainArgs &a, int N, hipStream_t s) {
+    return N == 128 ? launch<128, kOutputs, false>(a, s) : launch<64, kOutputs, false>(a, s);
+}

@@ -33,14 +33,15 @@ __device__ __forceinline__ void store_state4(void *p, int64_t i, int f32, f4 v) 
 }
 
 template <int kN, int kRows>
-__global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a) {
+__global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int64_t base_block) {
     constexpr int kCols = kN / 4;                // threads per row
     constexpr int kStep = kThreads / kCols;      // rows per pass
     constexpr int kPass = kRows / kStep;
     static_assert(kRows % kStep == 0, "whole passes");
     const int share = (int)(a.P / kRows);
-    const int64_t unit = blockIdx.x / share;     // (sequence, head)
-    const int p0 = (int)(blockIdx.x - unit * share) * kRows;
+    const int64_t block = base_block + blockIdx.x;
+    const int64_t unit = block / share;          // (sequence, head)
+    const int p0 = (int)(block - unit * share) * kRows;
     const int64_t n = unit / a.H, h = unit - n * a.H;
     const int64_t g = h / (a.H / a.G);
     const int q = threadIdx.x % kCols, r = threadIdx.x / kCols;
@@ -75,9 +76,15 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a) {
 
 template <int kN, int kRows>
 hipError_t launch(const SsmArgs &a, hipStream_t s) {
+    constexpr int64_t kMost = int64_t(1) << 23;  // a launch's work-items are counted in 32 bits
     const int64_t blocks = a.num_seqs * a.H * (a.P / kRows);
-    hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kRows>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+    for (int64_t b = 0; b < blocks; b += kMost) {
+        const int64_t n = blocks - b < kMost ? blocks - b : kMost;
+        hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kRows>), dim3((unsigned)n), dim3(kThreads), 0, s, a, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -52,11 +52,12 @@ def _declare(lib) -> None:
     N, C, S = (ctypes.POINTER(t) for t in (KdaRmsnormDesc, KdaConvDesc, KdaSsmDesc))
     for name, n, desc in (("kda_rmsnorm_fwd", 5, N), ("kda_rmsnorm_quant", 6, N), ("kda_rmsnorm_bwd", 7, N),
                           ("kda_conv_fwd", 7, C), ("kda_conv_decode", 6, C), ("kda_conv_bwd", 11, C),
-                          ("kda_ssm_decode", 10, S)):
+                          ("kda_ssm_fwd", 11, S), ("kda_ssm_decode", 10, S)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, [_P] * n + [desc, _P]
     for name, desc, kind in (("kda_rmsnorm_bwd_workspace_size", N, ctypes.c_size_t),
-                             ("kda_conv_bwd_workspace_size", C, ctypes.c_size_t)):
+                             ("kda_conv_bwd_workspace_size", C, ctypes.c_size_t),
+                             ("kda_ssm_fwd_workspace_size", S, ctypes.c_size_t), ("kda_ssm_piece_chunks", S, _I)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = kind, [desc]
 
@@ -476,6 +477,56 @@ def _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seq
     return KdaSsmDesc(nb, T, H, P, G, S, N, *_tokens(x, "x"), *_tokens(dt, "dt"), *_tokens(B, "B"), *_tokens(C, "C"), 0, 0,
                       _whole(initial_state, "initial_state", (N, H, P, S), dev),
                       _whole(final_state, final_name, (N, H, P, S), dev), None, 0, piece_chunks), dev
+
+
+def _ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks) -> KdaSsmDesc:
+    d = KdaSsmDesc(B, T, H, P, G, N, B if num_seqs is None else num_seqs)
+    d.piece_chunks = piece_chunks
+    return d
+
+
+def ssm_workspace_size(B: int, T: int, H: int, P: int, G: int, N: int, num_seqs: Optional[int] = None,
+                       piece_chunks: int = 0) -> int:
+    """Workspace bytes ``ssm_fwd`` needs for these shapes."""
+    return int(_library().kda_ssm_fwd_workspace_size(_ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks)))
+
+
+def ssm_piece_chunks(B: int, T: int, H: int, P: int, G: int, N: int, num_seqs: Optional[int] = None,
+                     piece_chunks: int = 0) -> int:
+    """64-token chunks per piece of a state chain for these shapes."""
+    n = int(_library().kda_ssm_piece_chunks(_ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks)))
+    if n < 0:
+        raise ValueError("invalid shapes")
+    return n
+
+
+def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
+            dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+            initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+            cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None, piece_chunks: int = 0
+            ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The selective state-space scan (``kda_ssm_fwd``).  Returns ``(out, final_state)``.
+
+    x: bf16 [B, T, H, P], P = 64 or 128; dt: bf16 [B, T, H], before the bias and
+    the softplus; B, C: bf16 [B, T, G, N], N = 64 or 128, each group shared by
+    H / G consecutive heads; A_log: fp32 [H]; dt_bias, D: fp32 [H] or None (zero);
+    initial_state, final_state: bf16 or fp32 [num_seqs, H, P, N] or None (zeros /
+    not wanted; final_state may be initial_state); cu_seqlens: int64
+    [num_seqs + 1] on the device (then the batch size is 1) or None; out: bf16
+    [B, T, H, P], allocated if None; workspace: uint8 of at least
+    ``ssm_workspace_size`` bytes, allocated if None; piece_chunks: 0 or the
+    chunks per piece (``kda_ssm_desc_t::piece_chunks``).
+
+    A NaN or infinity in a token reaches its sequence's outputs from the start of
+    its 64-token chunk on, and no other sequence."""
+    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks)
+    out = _output(out, "out", x.shape, torch.bfloat16, dev)
+    lib = _library()
+    ws = _workspace(workspace, lib.kda_ssm_fwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    _call(lib.kda_ssm_fwd, dev, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
+          _ptr(dt_bias), _ptr(D), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), out.data_ptr(), d)
+    return out, final_state
 
 
 def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,

@@ -153,11 +153,20 @@ typedef struct {
     int64_t piece_chunks;
 } kda_ssm_desc_t;
 
+/* Bytes of workspace kda_ssm_fwd needs for these shapes (0 if they are invalid;
+ * with B = 1 enough for a packed batch too), and the chunks per piece it uses
+ * (-1 if they are invalid).  Host arithmetic. */
+size_t kda_ssm_fwd_workspace_size(const kda_ssm_desc_t *desc);
+int64_t kda_ssm_piece_chunks(const kda_ssm_desc_t *desc);
+
 /* x, dt, B, C: bf16; A_log: fp32 [H]; dt_bias: fp32 [H] or NULL (zeros); D: fp32
- * [H] or NULL (no skip term); initial_state, final_state: [num_seqs, H, P, N],
- * initial_state or NULL (zeros); out: bf16 [B, T, H, P].
- *
- * One token per sequence (T = 1, num_seqs = B), in one launch and without a
+ * [H] or NULL (no skip term); initial_state, final_state: [num_seqs, H, P, N] or
+ * NULL, final_state may be initial_state when the types match; out: bf16
+ * [B, T, H, P]. */
+kda_status_t kda_ssm_fwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+                         const float *dt_bias, const float *D, const void *initial_state, void *final_state,
+                         const int64_t *cu_seqlens, void *out, const kda_ssm_desc_t *desc, hipStream_t stream);
+/* One token per sequence (T = 1, num_seqs = B), in one launch and without a
  * workspace; final_state (required) may be initial_state. */
 kda_status_t kda_ssm_decode(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
                             const float *dt_bias, const float *D, const void *initial_state, void *final_state,
