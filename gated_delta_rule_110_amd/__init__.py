@@ -29,8 +29,8 @@ from . import layer
 from ._build import LIB as LIB_PATH
 from ._build import build
 from .layer import (conv_bwd, conv_bwd_workspace_size, conv_decode, conv_fwd, rms_norm, rmsnorm_bwd,
-                    rmsnorm_bwd_workspace_size, rmsnorm_fwd, rmsnorm_quant, short_conv, ssm_decode, ssm_fwd,
-                    ssm_piece_chunks, ssm_workspace_size)
+                    rmsnorm_bwd_workspace_size, rmsnorm_fwd, rmsnorm_quant, short_conv, ssm_bwd,
+                    ssm_bwd_workspace_size, ssm_decode, ssm_fwd, ssm_piece_chunks, ssm_scan, ssm_workspace_size)
 
 __all__ = ["fwd", "fwd_noalloc", "noalloc_max_workspace", "decode", "bwd", "bwd_workspace_size",
            "kda_attention", "KdaFunction", "workspace_size", "chain_segments_for",
@@ -38,7 +38,7 @@ __all__ = ["fwd", "fwd_noalloc", "noalloc_max_workspace", "decode", "bwd", "bwd_
            "KDA_FP32",
            "rmsnorm_fwd", "rmsnorm_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "rms_norm",
            "conv_fwd", "conv_decode", "conv_bwd", "conv_bwd_workspace_size", "short_conv", "ssm_fwd", "ssm_decode",
-           "ssm_workspace_size", "ssm_piece_chunks"]
+           "ssm_bwd", "ssm_scan", "ssm_workspace_size", "ssm_bwd_workspace_size", "ssm_piece_chunks"]
 
 KDA_BF16 = 1
 KDA_FP32 = 2

@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_intra.hip", "kda_chain.hip", "kda_fused.hip", "kda_segment.hip", "kda_decode.hip", "kda_bwd.hip",
-           "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm.hip", "kda_ssm_decode.hip",
+           "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm.hip", "kda_ssm_bwd.hip", "kda_ssm_decode.hip",
            "kda_layer_api.hip"]
 HEADERS = [os.path.join(CSRC, "kda_common.h"), os.path.join(CSRC, "kda_intra_body.h"),
            os.path.join(CSRC, "kda_layer_args.h"), os.path.join(CSRC, "kda_ssm_common.h"), os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_layer.h")]
@@ -42,6 +42,7 @@ def hipcc() -> str:
 # use the whole register file; in this form its overflow goes to accumulator
 # registers rather than to scratch memory.
 EXTRA_FLAGS = {"kda_ssm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kda_ssm_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kda_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kda_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kda_fused.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],

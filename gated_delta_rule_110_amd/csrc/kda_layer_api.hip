@@ -324,6 +324,38 @@ kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     return KDA_OK;
 }
 
+// The gradient's workspace: the forward's, then the states and the sums.
+struct SsmBwdPlan {
+    SsmPlan p;
+    int share, shares;                  // heads of a group per workgroup, workgroups per chunk and group
+    size_t off_hs, off_ds, off_psum, off_part, total;
+};
+
+// Two rounds of the one gradient workgroup that fits each CU: with few chunks,
+// the heads of a group are shared out, and the shares' dB and dC added up.
+constexpr int64_t kWantGradGroups = 512;
+
+kda_status_t plan_ssm_bwd(const kda_ssm_desc_t *d, bool packed, SsmBwdPlan &b) {
+    const kda_status_t st = plan_ssm(d, packed, b.p);
+    if (st != KDA_OK) return st;
+    const int64_t heads = d->H / d->G, chunks = b.p.chunks, groups = chunks * d->G;
+    int64_t shares = groups > 0 ? (kWantGradGroups + groups - 1) / groups : 1;
+    if (shares > heads) shares = heads;
+    const int64_t share = (heads + shares - 1) / shares;
+    b.share = (int)share;
+    b.shares = (int)((heads + share - 1) / share);
+    if (groups > kMaxGroups / 2 / b.shares) return KDA_ERR_SHAPE;
+    const size_t states = (size_t)chunks * (size_t)d->H * (size_t)(d->P * d->N) * 4;
+    size_t o = b.p.total;
+    b.off_hs = o; o = align_up(o + states, 256);
+    b.off_ds = o; o = align_up(o + states, 256);
+    b.off_psum = o; o = align_up(o + (size_t)chunks * (size_t)d->H * 16, 256);
+    b.off_part = o;
+    if (b.shares > 1) o = align_up(o + 2 * (size_t)b.shares * (size_t)groups * (size_t)(64 * d->N) * 4, 256);
+    b.total = o;
+    return KDA_OK;
+}
+
 // The larger of the packed and unpacked needs, where both are possible.
 template <typename F>
 int64_t over_plans(const kda_ssm_desc_t *d, F f) {
@@ -589,5 +621,86 @@ extern "C" kda_status_t kda_ssm_fwd(const void *x, const void *dt, const void *B
     hipError_t e = launch_table(a, p, ws, stream);
     if (e == hipSuccess) e = launch_entering(c, N, false, stream);
     if (e == hipSuccess && desc->T > 0) e = kda_launch_ssm_chain(c, N, stream);
+    return of_hip(e);
+}
+
+extern "C" size_t kda_ssm_bwd_workspace_size(const kda_ssm_desc_t *desc) {
+    size_t best = 0;
+    if (!desc) return 0;
+    for (bool packed : {false, true}) {
+        SsmBwdPlan b;
+        if (check_ssm(desc, packed) != KDA_OK || plan_ssm_bwd(desc, packed, b) != KDA_OK) continue;
+        best = b.total > best ? b.total : best;
+    }
+    return best;
+}
+
+extern "C" kda_status_t kda_ssm_bwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+                                    const float *dt_bias, const float *D, const void *initial_state,
+                                    const int64_t *cu_seqlens, const void *d_out, const void *d_final_state, void *dx,
+                                    void *ddt, void *dB, void *dC, float *dA_log, float *ddt_bias, float *dD,
+                                    float *d_initial_state, const kda_ssm_desc_t *desc, hipStream_t stream) {
+    SsmArgs a;
+    kda_status_t st = ssm_args(x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, d_final_state, cu_seqlens, desc, a);
+    if (st != KDA_OK) return st;
+    if (!dA_log || (desc->T > 0 && (!d_out || !dx || !ddt || !dB || !dC))) return KDA_ERR_NULL;
+    if (!stride_ok(desc->d_out_stride_b) || !stride_ok(desc->d_out_stride_t)) return KDA_ERR_SHAPE;
+    if (desc->d_out_stride_b % 8 || desc->d_out_stride_t % 8 || !aligned(d_out, 16) || !aligned(dx, 16) || !aligned(ddt, 2) ||
+        !aligned(dB, 16) || !aligned(dC, 16) || !aligned(dA_log, 4) || !aligned(ddt_bias, 4) || !aligned(dD, 4) ||
+        !aligned(d_initial_state, 16))
+        return KDA_ERR_ALIGN;
+    SsmBwdPlan b;
+    st = plan_ssm_bwd(desc, cu_seqlens != nullptr, b);
+    if (st != KDA_OK) return st;
+    const size_t tokens = (size_t)(desc->B * desc->T), bc = tokens * (size_t)(desc->G * desc->N) * 2;
+    Memory m;
+    ssm_reads(m, x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, cu_seqlens, desc);
+    m.read(d_out, extent(desc->B, desc->d_out_stride_b, desc->T, desc->d_out_stride_t, desc->H * desc->P, 2));
+    m.read(d_final_state, ssm_state_bytes(desc, desc->final_state_dtype));
+    m.write(dx, ssm_out_bytes(desc));
+    m.write(ddt, tokens * (size_t)desc->H * 2);
+    m.write(dB, bc);
+    m.write(dC, bc);
+    for (float *q : {dA_log, ddt_bias, dD}) m.write(q, (size_t)desc->H * 4);
+    m.write(d_initial_state, ssm_state_bytes(desc, KDA_FP32));
+    m.write(desc->workspace, b.total);
+    if (m.clash()) return KDA_ERR_OVERLAP;
+    st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
+    if (st != KDA_OK) return st;
+    Workspace ws(desc->workspace, desc->workspace_bytes, b.total, stream);
+    if (ws.status() != KDA_OK) return ws.status();
+
+    const int N = (int)desc->N;
+    SsmChainArgs f = chain_args(a, b.p, ws);     // the states
+    f.h0 = initial_state; f.h0_f32 = a.h0_f32;
+    f.save = reinterpret_cast<float *>(ws.at(b.off_hs));
+    SsmChainArgs r = f;                          // their gradients: from d_out and C, last token first
+    r.x = static_cast<const uint16_t *>(d_out); r.xb = desc->d_out_stride_b; r.xt = desc->d_out_stride_t;
+    r.k = a.Cm; r.kb = a.cb; r.kt = a.ct;
+    r.h0 = d_final_state; r.h0_f32 = a.ht_f32;
+    r.ht = d_initial_state; r.ht_f32 = 1;
+    r.save = reinterpret_cast<float *>(ws.at(b.off_ds));
+    SsmGradArgs g{};
+    g.x = a.x; g.Bm = a.Bm; g.Cm = a.Cm; g.dt = a.dt; g.dy = static_cast<const uint16_t *>(d_out);
+    g.xb = a.xb; g.xt = a.xt; g.bb = a.bb; g.bt = a.bt; g.cb = a.cb; g.ct = a.ct; g.dtb = a.dtb; g.dtt = a.dtt;
+    g.yb = desc->d_out_stride_b; g.yt = desc->d_out_stride_t;
+    g.A_log = A_log; g.dt_bias = dt_bias; g.D = D;
+    g.cu = cu_seqlens; g.chunk_off = f.chunk_off;
+    g.T = a.T; g.H = a.H; g.P = a.P; g.G = a.G; g.seqs = a.num_seqs;
+    g.chunks = b.p.chunks; g.cps = b.p.cps;
+    g.share = b.share; g.shares = b.shares;
+    g.hs = f.save; g.ds = r.save;
+    g.dx = static_cast<uint16_t *>(dx); g.ddt = static_cast<uint16_t *>(ddt);
+    g.dB = static_cast<uint16_t *>(dB); g.dC = static_cast<uint16_t *>(dC);
+    g.psum = reinterpret_cast<float *>(ws.at(b.off_psum));
+    g.part = reinterpret_cast<float *>(ws.at(b.off_part));
+    g.dA_log = dA_log; g.ddt_bias = ddt_bias; g.dD = dD;
+
+    hipError_t e = launch_table(a, b.p, ws, stream);
+    if (e == hipSuccess) e = launch_entering(f, N, false, stream);
+    if (e == hipSuccess && desc->T > 0) e = kda_launch_ssm_save(f, N, false, stream);
+    if (e == hipSuccess) e = launch_entering(r, N, true, stream);
+    if (e == hipSuccess && desc->T > 0) e = kda_launch_ssm_save(r, N, true, stream);
+    if (e == hipSuccess) e = kda_launch_ssm_grad(g, N, stream);
     return of_hip(e);
 }

@@ -1,0 +1,480 @@
+// kda_ssm_bwd.hip -- the gradient of the selective state-space scan, chunk by
+// chunk (gfx950).
+//
+// The chains of kda_ssm.hip leave, for every chunk of 64 tokens, the state S
+// entering it and the gradient D of the state leaving it.  With G, dt and w as
+// there, XD_ij = d_out_i . x_j and the masked decays L_ij = e^{G_i - G_j}, j <= i,
+//
+//   M_ij = L_ij dt_j (C_i . B_j) + [i = j] Dskip,    W_ij = L_ij dt_j XD_ij
+//   dx_j = sum_i M_ij d_out_i + w_j D B_j
+//   dB_j = sum_i W_ij C_i     + w_j D^T x_j
+//   dC_i = sum_j W_ij B_j     + e^{G_i} S^T d_out_i
+//
+// and with Q_ij = L_ij (C_i . B_j) XD_ij, F_j = w_j x_j^T D B_j, R_i = e^{G_i} d_out_i^T S C_i
+// the gradient of a_t collects every pair (i, j) whose decay runs over token t:
+//
+//   da_t  = e^{G_63} <D, S> + sum_{j < t} F_j + sum_{i >= t} R_i + sum_{i >= t > j} Q_ij dt_j
+//   ddt_t = -exp(A_log) da_t + sum_i Q_it + F_t / dt_t,
+//
+// the double sum as suffix sums of (row sum - column sum) of Q_ij dt_j over i > j,
+// in 64 bits: the pairs behind t cancel up to the rounding of the row and column
+// sums (the diagonal, which would cancel too, is left out).
+//
+// One workgroup of 8 waves takes a chunk, a group of B and C and a share of its
+// heads, one head and 64 channels after the other: C B^T is computed once for
+// all of them, and dB and dC add up in registers.  The products' fp32 operands
+// (M, W, S, D) are split into two bf16 parts (2^-17); x, B, C and d_out are
+// exact.  Bound by LDS reads and by the latency of its phases at one workgroup
+// per CU (150 KiB of LDS).
+#include "kda_ssm_common.h"
+
+using namespace kda;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = 8;
+constexpr int kMPitch = kL + 16;
+
+template <int kN>
+struct __align__(16) GradSmem {
+    uint16_t b[kL * kPitch<kN>], c[kL * kPitch<kN>];
+    uint16_t x[kL * kXPitch], dy[kL * kXPitch];
+    uint16_t m[2][kL * kMPitch], wm[2][kL * kMPitch];  // M and W, two parts, rows i
+    uint16_t d[2][kPB * kPitch<kN>];                   // D, two parts, rows = channels
+    float g[kL], gr[kL], dt[kL];
+    float colq[4][kL], rowe[2][kL], qd[kL], f[4][kL], rr[kN / 16][kL];
+    float xs[kN / 16], dd[4];
+};
+
+// Operand fragments from LDS.  Along a row: 8 neighbouring entries, or in the
+// order of a pair of accumulator tiles (4 g + e, 16 + 4 g + e).  Along rows: by the
+// transposing read, in that order too.
+__device__ __forceinline__ s8 along(const uint16_t *row, int q, int g) { return lds8(row + 32 * q + 8 * g); }
+__device__ __forceinline__ s8 along_pair(const uint16_t *row, int q, int g) {
+    return join(*reinterpret_cast<const s4 *>(row + 32 * q + 4 * g), *reinterpret_cast<const s4 *>(row + 32 * q + 16 + 4 * g));
+}
+__device__ __forceinline__ s8 across(const uint16_t *base, int pitch, int q, int col, int r, int g) {
+    const uint16_t *p = base + (32 * q + 4 * g + (r >> 2)) * pitch + col + 4 * (r & 3);
+    return join(read_tr(p), read_tr(p + 16 * pitch));
+}
+
+// Sum over the 16 lanes of a row, in its last lane.
+__device__ __forceinline__ float row16_sum(float v) {
+    v += dpp_row_shr_zero(v, 8);
+    v += dpp_row_shr_zero(v, 4);
+    v += dpp_row_shr_zero(v, 2);
+    v += dpp_row_shr_zero(v, 1);
+    return v;
+}
+// Sum over the four 16-lane rows, in every lane.
+__device__ __forceinline__ float rows_sum(float v) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+    return v;
+}
+__device__ __forceinline__ double wave_scan(double v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+__device__ __forceinline__ void add_to(float *p, float v, bool more) { *p = more ? *p + v : v; }
+
+// Tokens of chunk number i of the batch.
+struct Chunk {
+    int64_t row0, t0;
+    int rows;
+};
+__device__ __forceinline__ bool chunk_of(const SsmGradArgs &a, int64_t i, Chunk &c) {
+    int64_t begin = 0, len = a.T, k;
+    if (a.cu) {
+        if (i >= a.chunk_off[a.seqs]) return false;
+        const int64_t n = seq_of_slot(a.chunk_off, a.seqs, i);
+        k = i - a.chunk_off[n];
+        begin = clamp_to(a.cu[n], a.T);
+        len = clamp_to(a.cu[n + 1], a.T) - begin;
+        c.row0 = 0;
+    } else {
+        if (i >= a.seqs * a.cps) return false;
+        c.row0 = i / a.cps;
+        k = i - c.row0 * a.cps;
+    }
+    c.t0 = begin + k * kL;
+    const int64_t left = len - k * kL;
+    c.rows = (int)(left < kL ? left : kL);
+    return c.rows > 0;
+}
+
+template <int kN>
+__global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
+    constexpr int kTiles = kN / 16, kQ = kN / 32;
+    constexpr int kJ = 4 * kTiles / kWaves;      // token tiles of dB and dC per wave
+    __shared__ GradSmem<kN> sm;
+    const int64_t per = a.G * a.shares;
+    const int64_t chunk = blockIdx.x / per;
+    const int64_t grp = (blockIdx.x - chunk * per) / a.shares;
+    const int share = (int)(blockIdx.x - chunk * per - grp * a.shares);
+    Chunk ck;
+    if (chunk >= a.chunks || !chunk_of(a, chunk, ck)) return;
+    const int rows = ck.rows;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int it = w & 3, kb = w >> 2;           // this wave's tiles of the 64 x 64 products
+    const int nt = w % kTiles, j0 = w / kTiles * kJ;
+    const int64_t heads = a.H / a.G;             // of the group
+    const int64_t h0 = grp * heads + (int64_t)share * a.share;
+    const int64_t h1 = (share + 1) * (int64_t)a.share < heads ? h0 + a.share : grp * heads + heads;
+    const int64_t pbs = a.P / kPB;
+    const uint16_t *xrow = a.x + ck.row0 * a.xb + ck.t0 * a.xt;
+    const uint16_t *yrow = a.dy + ck.row0 * a.yb + ck.t0 * a.yt;
+    const int64_t trow = ck.row0 * a.T + ck.t0;  // row of the contiguous outputs
+
+    {
+        Rows<kN, kThreads> rb, rc;
+        rb.load(a.Bm + ck.row0 * a.bb + ck.t0 * a.bt + grp * kN, a.bt, rows);
+        rc.load(a.Cm + ck.row0 * a.cb + ck.t0 * a.ct + grp * kN, a.ct, rows);
+        rb.store(sm.b, kPitch<kN>);
+        rc.store(sm.c, kPitch<kN>);
+    }
+    __syncthreads();
+    f4 cb[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // (C_i . B_j): lane = i, entries j
+    if (2 * kb <= it) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                cb[half] = mfma16x16x32_bf16(along(sm.b + (32 * kb + 16 * half + r) * kPitch<kN>, q, g),
+                                             along(sm.c + (16 * it + r) * kPitch<kN>, q, g), cb[half]);
+    }
+    f4 dB[kJ], dC[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) dB[j] = dC[j] = f4{0.f, 0.f, 0.f, 0.f};
+
+    for (int64_t h = h0; h < h1; ++h) {
+        const float A = -fast_exp(a.A_log[h]);
+        const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        const float Dh = a.D ? a.D[h] : 0.f;
+        float raw = 0.f;
+        for (int64_t pb = 0; pb < pbs; ++pb) {
+            const bool more = pb > 0;            // sums over channels go on
+            const int64_t unit = (chunk * a.H + h) * pbs + pb;
+            const f4 *hs = reinterpret_cast<const f4 *>(a.hs) + unit * (kPB * kN / 4);
+            const f4 *ds = reinterpret_cast<const f4 *>(a.ds) + unit * (kPB * kN / 4);
+            f4 S[4];                             // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
+            {
+                Rows<kPB, kThreads> rx, ry;
+                rx.load(xrow + h * a.P + pb * kPB, a.xt, rows);
+                ry.load(yrow + h * a.P + pb * kPB, a.yt, rows);
+                f4 D[kN / 32];
+#pragma unroll
+                for (int i = 0; i < kN / 32; ++i) D[i] = ds[i * kThreads + threadIdx.x];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) S[t] = hs[(t * kTiles + nt) * 64 + lane];
+                if (w == 0 && !more) {
+                    raw = lane < rows ? bf16_bits_to_f32(a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h]) : 0.f;
+                    step_sizes(raw, lane < rows, bias, A * kLog2e, sm.g, sm.gr, sm.dt);
+                }
+                rx.store(sm.x, kXPitch);
+                ry.store(sm.dy, kXPitch);
+#pragma unroll
+                for (int i = 0; i < kN / 32; ++i) {
+                    // tile t of the channels 16 p + r: entries 32 (t / 2) + 8 g + 4 (t % 2) ..
+                    const int tile = (i * kThreads + (int)threadIdx.x) >> 6, p = tile / kTiles, t = tile % kTiles;
+                    const int at = (16 * p + r) * kPitch<kN> + 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+                    s4 hi, lo;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        short u, v;
+                        split_bf16(D[i][e], u, v);
+                        hi[e] = u;
+                        lo[e] = v;
+                    }
+                    *reinterpret_cast<s4 *>(&sm.d[0][at]) = hi;
+                    *reinterpret_cast<s4 *>(&sm.d[1][at]) = lo;
+                }
+            }
+            __syncthreads();
+            const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1];
+
+            // ---- M, W, Q: 64 x 64, lane = i, entries j
+            if (2 * kb <= it) {
+                const int ti = 16 * it + r;
+                const float gi = sm.g[ti], gir = sm.gr[ti];
+                float rowe = 0.f, dd = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int jt = 2 * kb + half;
+                    f4 xd = {0.f, 0.f, 0.f, 0.f};
+                    if (jt <= it) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kXPitch, q, g), along(sm.dy + ti * kXPitch, q, g), xd);
+                    }
+                    s4 m0, m1, w0, w1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tj = 16 * jt + 4 * g + e;
+                        const float dtj = sm.dt[tj];
+                        const float l = tj <= ti ? __builtin_amdgcn_exp2f((gi - sm.g[tj]) + (gir - sm.gr[tj])) : 0.f;
+                        const float lc = tj <= ti ? l * cb[half][e] : 0.f;
+                        const float wv = tj <= ti ? l * dtj * xd[e] : 0.f;
+                        const float qv = tj < ti ? lc * xd[e] : 0.f;
+                        rowe += qv * dtj;
+                        if (tj == ti) {
+                            dd += xd[e];
+                            add_to(&sm.qd[ti], lc * xd[e], more);
+                        }
+                        short u, v;
+                        split_bf16(lc * dtj + (tj == ti ? Dh : 0.f), u, v);
+                        m0[e] = u;
+                        m1[e] = v;
+                        split_bf16(wv, u, v);
+                        w0[e] = u;
+                        w1[e] = v;
+                        const float col = row16_sum(qv);
+                        if (r == 15 && jt <= it) add_to(&sm.colq[it][tj], col, more);
+                    }
+                    const int at = ti * kMPitch + 16 * jt + 4 * g;
+                    *reinterpret_cast<s4 *>(&sm.m[0][at]) = m0;
+                    *reinterpret_cast<s4 *>(&sm.m[1][at]) = m1;
+                    *reinterpret_cast<s4 *>(&sm.wm[0][at]) = w0;
+                    *reinterpret_cast<s4 *>(&sm.wm[1][at]) = w1;
+                }
+                rowe = rows_sum(rowe);
+                if (g == 0) add_to(&sm.rowe[kb][ti], rowe, more);
+                if (kb == it >> 1) {             // the wave with the diagonal tile
+                    dd = wave_sum(dd);
+                    if (lane == 0) add_to(&sm.dd[it], dd, more);
+                }
+            }
+            __syncthreads();
+
+            // ---- dx, transposed: lane = token, entries 4 neighbouring channels
+            {
+                const int pt = w & 3, half = w >> 2;
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    const int jt = 2 * half + jj, tj = 16 * jt + r;
+                    f4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) {
+                        const s8 bv = along(sm.b + tj * kPitch<kN>, q, g);
+                        u = mfma16x16x32_bf16(along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
+                        u = mfma16x16x32_bf16(along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
+                    }
+                    const s4 xv = *reinterpret_cast<const s4 *>(sm.x + tj * kXPitch + 16 * pt + 4 * g);
+                    float f = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)xv[e]) * u[e];
+                    f = rows_sum(f);
+                    if (g == 0) add_to(&sm.f[pt][tj], f, more);
+                    const float wj = __builtin_amdgcn_exp2f((gl - sm.g[tj]) + (glr - sm.gr[tj])) * sm.dt[tj];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[e] *= wj;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (q < half) continue;  // i before j
+                        const s8 yv = across(sm.dy, kXPitch, q, 16 * pt, r, g);
+                        u = mfma16x16x32_bf16(yv, across(sm.m[0], kMPitch, q, 16 * jt, r, g), u);
+                        u = mfma16x16x32_bf16(yv, across(sm.m[1], kMPitch, q, 16 * jt, r, g), u);
+                    }
+                    if (tj < rows)
+                        *reinterpret_cast<uint2 *>(a.dx + ((trow + tj) * a.H + h) * a.P + pb * kPB + 16 * pt + 4 * g) =
+                            make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+                }
+            }
+
+            // ---- dB and dC, transposed: lane = token, entries 4 neighbouring state entries
+            {
+                s8 Dv[2][2], Sv[2][2];
+                float xs = 0.f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) Dv[k][q] = across(sm.d[k], kPitch<kN>, q, 16 * nt, r, g);
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = S[2 * q][e];
+                        v[4 + e] = S[2 * q + 1][e];
+                    }
+                    split2(v, Sv[0][q], Sv[1][q]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) + bf16_bits_to_f32((uint16_t)Dv[1][q][e]));
+                }
+                xs = wave_sum(xs);
+                if (lane == 0 && j0 == 0) add_to(&sm.xs[nt], xs, more);
+                s8 Ct[2], Bt[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    Ct[q] = across(sm.c, kPitch<kN>, q, 16 * nt, r, g);
+                    Bt[q] = across(sm.b, kPitch<kN>, q, 16 * nt, r, g);
+                }
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int tt = j0 + j, t = 16 * tt + r;
+                    f4 u = {0.f, 0.f, 0.f, 0.f}, v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const s8 xv = along_pair(sm.x + t * kXPitch, q, g), yv = along_pair(sm.dy + t * kXPitch, q, g);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            u = mfma16x16x32_bf16(Dv[k][q], xv, u);
+                            v = mfma16x16x32_bf16(Sv[k][q], yv, v);
+                        }
+                    }
+                    const s4 cv = *reinterpret_cast<const s4 *>(sm.c + t * kPitch<kN> + 16 * nt + 4 * g);
+                    float f = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)cv[e]) * v[e];
+                    f = rows_sum(f);
+                    if (g == 0) add_to(&sm.rr[nt][t], f, more);
+                    const float gt = sm.g[t];
+                    const float wt = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.gr[t])) * sm.dt[t];
+                    const float et = __builtin_amdgcn_exp2f(gt);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dB[j][e] += wt * u[e];
+                        dC[j][e] += et * v[e];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (2 * q + 1 >= tt) {   // i from token tile tt on
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                dB[j] = mfma16x16x32_bf16(Ct[q], across(sm.wm[k], kMPitch, q, 16 * tt, r, g), dB[j]);
+                        }
+                        if (2 * q <= tt) {       // j up to it
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                dC[j] = mfma16x16x32_bf16(Bt[q], along_pair(sm.wm[k] + t * kMPitch, q, g), dC[j]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- step sizes and parameters, lane = token
+        if (w == 0) {
+            const int t = lane;
+            float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= t >> 4) colq += sm.colq[i][t];
+                f += sm.f[i][t];
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                rr += sm.rr[i][t];
+                xs += sm.xs[i];
+            }
+            const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1], gt = sm.g[t], dt = sm.dt[t];
+            const float rowe = sm.rowe[0][t] + (t >= 32 ? sm.rowe[1][t] : 0.f);
+            const float wd = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.gr[t]));
+            rr *= __builtin_amdgcn_exp2f(gt);
+            xs *= __builtin_amdgcn_exp2f(gl);
+            const double z = (double)rr + ((double)rowe - (double)dt * (double)colq);
+            const double F = (double)wd * (double)dt * (double)f;
+            const double zi = wave_scan(z), fi = wave_scan(F);
+            const double total = __shfl(zi, 63);
+            const float da = (float)((double)xs + (fi - F) + (total - zi + z));
+            const float ddt = A * da + (colq + sm.qd[t]) + wd * f;
+            const float draw = t < rows ? ddt * sigmoid(raw + bias) : 0.f;
+            if (t < rows) a.ddt[(trow + t) * a.H + h] = f32_to_bf16_bits(draw);
+            const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
+            if (lane == 0) {
+                float *o = a.psum + (chunk * a.H + h) * 4;
+                o[0] = dA;
+                o[1] = db;
+                o[2] = (sm.dd[0] + sm.dd[1]) + (sm.dd[2] + sm.dd[3]);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+        const int t = 16 * (j0 + j) + r, n = 16 * nt + 4 * g;
+        if (t >= rows) continue;
+        if (a.shares == 1) {
+            const int64_t o = ((trow + t) * a.G + grp) * kN + n;
+            *reinterpret_cast<uint2 *>(a.dB + o) = make_uint2(pack_bf16(dB[j][0], dB[j][1]), pack_bf16(dB[j][2], dB[j][3]));
+            *reinterpret_cast<uint2 *>(a.dC + o) = make_uint2(pack_bf16(dC[j][0], dC[j][1]), pack_bf16(dC[j][2], dC[j][3]));
+        } else {
+            const int64_t one = a.chunks * a.G * kL * kN;  // a share of one of the two
+            const int64_t o = ((chunk * a.G + grp) * kL + t) * kN + n;
+            *reinterpret_cast<f4 *>(a.part + share * one + o) = dB[j];
+            *reinterpret_cast<f4 *>(a.part + (a.shares + share) * one + o) = dC[j];
+        }
+    }
+}
+
+// dB and dC from the shares, in order: one workgroup per chunk and group.
+template <int kN>
+__global__ __launch_bounds__(256) void kda_ssm_grad_join_kernel(SsmGradArgs a) {
+    const int64_t chunk = blockIdx.x / a.G, grp = blockIdx.x - chunk * a.G;
+    Chunk ck;
+    if (chunk >= a.chunks || !chunk_of(a, chunk, ck)) return;
+    const int64_t one = a.chunks * a.G * kL * kN;
+    for (int i = threadIdx.x; i < 2 * ck.rows * kN / 4; i += 256) {
+        const int which = i / (ck.rows * kN / 4), at = i - which * (ck.rows * kN / 4);
+        const int t = at / (kN / 4), n = 4 * (at % (kN / 4));
+        const float *src = a.part + which * a.shares * one + ((chunk * a.G + grp) * kL + t) * kN + n;
+        f4 v = *reinterpret_cast<const f4 *>(src);
+        for (int s = 1; s < a.shares; ++s) v += *reinterpret_cast<const f4 *>(src + s * one);
+        uint16_t *dst = (which ? a.dC : a.dB) + ((ck.row0 * a.T + ck.t0 + t) * a.G + grp) * kN + n;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+}
+
+// dA_log, ddt_bias and dD: the chunks' sums, in a fixed order and in 64 bits.
+__global__ __launch_bounds__(256) void kda_ssm_grad_params_kernel(SsmGradArgs a) {
+    __shared__ double s[3][256];
+    const int64_t h = blockIdx.x;
+    const int64_t chunks = a.cu ? clamp_to(a.chunk_off[a.seqs], a.chunks) : a.chunks;
+    double v[3] = {0.0, 0.0, 0.0};
+    for (int64_t c = threadIdx.x; c < chunks; c += 256)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) v[k] += (double)a.psum[(c * a.H + h) * 4 + k];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k][threadIdx.x] = v[k];
+    __syncthreads();
+    for (int d = 128; d >= 1; d >>= 1) {
+        if ((int)threadIdx.x < d)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) s[k][threadIdx.x] += s[k][threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        a.dA_log[h] = (float)s[0][0];
+        if (a.ddt_bias) a.ddt_bias[h] = (float)s[1][0];
+        if (a.dD) a.dD[h] = (float)s[2][0];
+    }
+}
+
+template <int kN>
+hipError_t launch(const SsmGradArgs &a, hipStream_t s) {
+    if (a.chunks > 0 && a.T > 0) {
+        hipLaunchKernelGGL((kda_ssm_grad_kernel<kN>), dim3((unsigned)(a.chunks * a.G * a.shares)), dim3(kThreads), 0, s, a);
+        if (a.shares > 1)
+            hipLaunchKernelGGL((kda_ssm_grad_join_kernel<kN>), dim3((unsigned)(a.chunks * a.G)), dim3(256), 0, s, a);
+    }
+    hipLaunchKernelGGL(kda_ssm_grad_params_kernel, dim3((unsigned)a.H), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t kda_launch_ssm_grad(const SsmGradArgs &a, int N, hipStream_t s) {
+    return N == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}

@@ -52,12 +52,14 @@ def _declare(lib) -> None:
     N, C, S = (ctypes.POINTER(t) for t in (KdaRmsnormDesc, KdaConvDesc, KdaSsmDesc))
     for name, n, desc in (("kda_rmsnorm_fwd", 5, N), ("kda_rmsnorm_quant", 6, N), ("kda_rmsnorm_bwd", 7, N),
                           ("kda_conv_fwd", 7, C), ("kda_conv_decode", 6, C), ("kda_conv_bwd", 11, C),
-                          ("kda_ssm_fwd", 11, S), ("kda_ssm_decode", 10, S)):
+                          ("kda_ssm_fwd", 11, S), ("kda_ssm_decode", 10, S),
+                          ("kda_ssm_bwd", 19, S)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, [_P] * n + [desc, _P]
     for name, desc, kind in (("kda_rmsnorm_bwd_workspace_size", N, ctypes.c_size_t),
                              ("kda_conv_bwd_workspace_size", C, ctypes.c_size_t),
-                             ("kda_ssm_fwd_workspace_size", S, ctypes.c_size_t), ("kda_ssm_piece_chunks", S, _I)):
+                             ("kda_ssm_fwd_workspace_size", S, ctypes.c_size_t), ("kda_ssm_piece_chunks", S, _I),
+                             ("kda_ssm_bwd_workspace_size", S, ctypes.c_size_t)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = kind, [desc]
 
@@ -414,9 +416,9 @@ def conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     return res
 
 
-def _grad_dx(cu_seqlens: Optional[torch.Tensor], shape, dev) -> Optional[torch.Tensor]:
-    """Zeros for a packed batch (rows behind its last sequence get no gradient), else None."""
-    return None if cu_seqlens is None else torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+def _packed_zeros(cu_seqlens: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
+    """Zeros for a packed batch (rows behind its last sequence are not written), else None."""
+    return None if cu_seqlens is None else torch.zeros(like.shape, dtype=torch.bfloat16, device=like.device)
 
 
 class ConvFunction(torch.autograd.Function):
@@ -427,7 +429,7 @@ class ConvFunction(torch.autograd.Function):
         N, W = _num_seqs(cu_seqlens, x.shape[0]), weight.shape[1]
         final = None if final_dtype is None else torch.empty((N, W - 1, x.shape[2]), dtype=final_dtype, device=x.device)
         out, final = conv_fwd(x, weight, bias, activation, initial_state, final, cu_seqlens,
-                              out=_grad_dx(cu_seqlens, x.shape, x.device))
+                              out=_packed_zeros(cu_seqlens, x))
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.activation = activation
         return out, final
@@ -441,7 +443,7 @@ class ConvFunction(torch.autograd.Function):
         g = conv_bwd(x, weight, bias, ctx.activation, d_out.to(torch.bfloat16).contiguous(),
                      d_final_state=None if d_final is None else d_final.contiguous(), initial_state=initial_state,
                      cu_seqlens=cu_seqlens, with_d_initial=want,
-                     outputs={"dx": _grad_dx(cu_seqlens, x.shape, x.device)})
+                     outputs={"dx": _packed_zeros(cu_seqlens, x)})
         return (g["dx"], g["dweight"].to(weight.dtype), None if bias is None else g["dbias"].to(bias.dtype),
                 g["d_initial_state"].to(initial_state.dtype) if want else None, None, None, None)
 
@@ -545,3 +547,90 @@ def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tens
     _call(_library().kda_ssm_decode, dev, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
           _ptr(dt_bias), _ptr(D), _ptr(initial_state), final_state.data_ptr(), out.data_ptr(), d)
     return out, final_state
+
+
+def ssm_bwd_workspace_size(B: int, T: int, H: int, P: int, G: int, N: int, num_seqs: Optional[int] = None,
+                           piece_chunks: int = 0) -> int:
+    """Workspace bytes ``ssm_bwd`` needs for these shapes."""
+    return int(_library().kda_ssm_bwd_workspace_size(_ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks)))
+
+
+def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
+            dt_bias: Optional[torch.Tensor], D: Optional[torch.Tensor], d_out: torch.Tensor,
+            d_final_state: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+            cu_seqlens: Optional[torch.Tensor] = None, with_d_initial: Optional[bool] = None,
+            workspace: Optional[torch.Tensor] = None, outputs: Optional[dict] = None, piece_chunks: int = 0) -> dict:
+    """Gradient of ``ssm_fwd`` (``kda_ssm_bwd``) for the loss gradients d_out (bf16
+    [B, T, H, P]) and d_final_state (bf16 or fp32 [num_seqs, H, P, N], or None).
+    Returns a dict: dx, ddt, dB and dC (bf16, of their inputs' shapes), dA_log,
+    ddt_bias and dD (fp32 [H]; the latter two None where the input is) and
+    d_initial_state (fp32 [num_seqs, H, P, N]; None unless wanted, by default
+    where an initial_state is given).  Rows behind a packed batch's last sequence
+    are left as they were.  outputs: None, or a dict of tensors of those names to
+    write into.  The workspace holds 8 P N bytes per 64-token chunk and head."""
+    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, d_final_state, cu_seqlens, piece_chunks,
+                       "d_final_state")
+    _bf16(d_out, "d_out", dev)
+    if d_out.shape != x.shape:
+        raise ValueError("d_out must be of x's shape")
+    d.d_out_stride_b, d.d_out_stride_t = _tokens(d_out, "d_out")
+    given = outputs or {}
+    bf16, f32, H = torch.bfloat16, torch.float32, (d.H,)
+    if with_d_initial is None:
+        with_d_initial = initial_state is not None
+    res = {"dx": _output(given.get("dx"), "dx", x.shape, bf16, dev),
+           "ddt": _output(given.get("ddt"), "ddt", dt.shape, bf16, dev),
+           "dB": _output(given.get("dB"), "dB", B.shape, bf16, dev),
+           "dC": _output(given.get("dC"), "dC", B.shape, bf16, dev),
+           "dA_log": _output(given.get("dA_log"), "dA_log", H, f32, dev),
+           "ddt_bias": None if dt_bias is None else _output(given.get("ddt_bias"), "ddt_bias", H, f32, dev),
+           "dD": None if D is None else _output(given.get("dD"), "dD", H, f32, dev),
+           "d_initial_state": _output(given.get("d_initial_state"), "d_initial_state", (d.num_seqs, d.H, d.P, d.N), f32, dev)
+           if with_d_initial else None}
+    lib = _library()
+    ws = _workspace(workspace, lib.kda_ssm_bwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    _call(lib.kda_ssm_bwd, dev, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(), _ptr(dt_bias),
+          _ptr(D), _ptr(initial_state), _ptr(cu_seqlens), d_out.data_ptr(), _ptr(d_final_state), res["dx"].data_ptr(),
+          res["ddt"].data_ptr(), res["dB"].data_ptr(), res["dC"].data_ptr(), res["dA_log"].data_ptr(),
+          _ptr(res["ddt_bias"]), _ptr(res["dD"]), _ptr(res["d_initial_state"]), d)
+    return res
+
+
+class SsmFunction(torch.autograd.Function):
+    """``ssm_fwd`` with ``ssm_bwd`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens, final_dtype):
+        N = _num_seqs(cu_seqlens, x.shape[0])
+        final = None
+        if final_dtype is not None:
+            final = torch.empty((N, *x.shape[2:], B.shape[-1]), dtype=final_dtype, device=x.device)
+        out, final = ssm_fwd(x, dt, B, C, A_log, dt_bias, D, initial_state, final, cu_seqlens,
+                             out=_packed_zeros(cu_seqlens, x))
+        ctx.save_for_backward(x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens)
+        return out, final
+
+    @staticmethod
+    def backward(ctx, d_out, d_final):
+        x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens = ctx.saved_tensors
+        if d_out is None:
+            d_out = torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
+        want = initial_state is not None and ctx.needs_input_grad[7]
+        g = ssm_bwd(x, dt, B, C, A_log, dt_bias, D, d_out.to(torch.bfloat16).contiguous(),
+                    d_final_state=None if d_final is None else d_final.contiguous(), initial_state=initial_state,
+                    cu_seqlens=cu_seqlens, with_d_initial=want,
+                    outputs={"dx": _packed_zeros(cu_seqlens, x), "ddt": _packed_zeros(cu_seqlens, dt),
+                             "dB": _packed_zeros(cu_seqlens, B), "dC": _packed_zeros(cu_seqlens, C)})
+        return (g["dx"], g["ddt"], g["dB"], g["dC"], g["dA_log"], g["ddt_bias"], g["dD"],
+                g["d_initial_state"].to(initial_state.dtype) if want else None, None, None)
+
+
+def ssm_scan(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
+             dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+             initial_state: Optional[torch.Tensor] = None, final_state_dtype: Optional[torch.dtype] = None,
+             cu_seqlens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``ssm_fwd`` as an autograd operation: returns ``(out, final_state)``, the
+    final state in ``final_state_dtype`` or None, and backpropagates into x, dt,
+    B, C, A_log, dt_bias, D and the initial state.  Rows behind a packed batch's
+    last sequence are zero, in the output and in the gradients."""
+    return SsmFunction.apply(x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens, final_state_dtype)

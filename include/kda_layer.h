@@ -153,10 +153,11 @@ typedef struct {
     int64_t piece_chunks;
 } kda_ssm_desc_t;
 
-/* Bytes of workspace kda_ssm_fwd needs for these shapes (0 if they are invalid;
- * with B = 1 enough for a packed batch too), and the chunks per piece it uses
- * (-1 if they are invalid).  Host arithmetic. */
+/* Bytes of workspace kda_ssm_fwd and kda_ssm_bwd need for these shapes (0 if they
+ * are invalid; with B = 1 enough for a packed batch too), and the chunks per piece
+ * they use (-1 if they are invalid).  Host arithmetic. */
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_desc_t *desc);
+size_t kda_ssm_bwd_workspace_size(const kda_ssm_desc_t *desc);
 int64_t kda_ssm_piece_chunks(const kda_ssm_desc_t *desc);
 
 /* x, dt, B, C: bf16; A_log: fp32 [H]; dt_bias: fp32 [H] or NULL (zeros); D: fp32
@@ -171,6 +172,19 @@ kda_status_t kda_ssm_fwd(const void *x, const void *dt, const void *Bm, const vo
 kda_status_t kda_ssm_decode(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
                             const float *dt_bias, const float *D, const void *initial_state, void *final_state,
                             void *out, const kda_ssm_desc_t *desc, hipStream_t stream);
+/* The gradient of <d_out, out> + <d_final_state, final_state>.  d_out: bf16;
+ * d_final_state: of final_state_dtype, or NULL for zeros.  dx [B, T, H, P], ddt
+ * [B, T, H], dB and dC [B, T, G, N]: bf16; dA_log, ddt_bias, dD: fp32 [H]
+ * (ddt_bias and dD may be NULL); d_initial_state: fp32 [num_seqs, H, P, N] or
+ * NULL.  The forward's states are computed again, and the state entering every
+ * chunk and the gradient of the one leaving it are held in the workspace (2 x 4 P N
+ * bytes per chunk and head). */
+kda_status_t kda_ssm_bwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
+                         const float *dt_bias, const float *D, const void *initial_state,
+                         const int64_t *cu_seqlens, const void *d_out, const void *d_final_state, void *dx,
+                         void *ddt, void *dB, void *dC, float *dA_log, float *ddt_bias, float *dD,
+                         float *d_initial_state, const kda_ssm_desc_t *desc, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

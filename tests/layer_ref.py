@@ -83,6 +83,8 @@ def check_norm(got, ref, rel, label):
 
 
 def grads(loss, leaves):
+    if not loss.requires_grad:  # no token and no state reaches it
+        return [None if t is None else torch.zeros_like(t) for t in leaves]
     got = torch.autograd.grad(loss, [t for t in leaves if t is not None], allow_unused=True)
     it = iter(got)
     out = []
