@@ -65,15 +65,20 @@ __device__ __forceinline__ void store_any_c(void *p, int64_t i, int f32, const f
     else store_c<kC>(reinterpret_cast<uint16_t *>(p) + i, v);
 }
 
-// The lane's filter: w[k][e] for channel c + e.
+// The lane's filter: w[k][e] for channel c + e.  With 8 channels its kC kW
+// entries are one 16-byte aligned piece.
 template <int kC, int kW>
 __device__ __forceinline__ void load_filter(const ConvArgs &a, int64_t c, float (&w)[kW][kC], float (&b)[kC]) {
+    float f[kW * kC];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) load_any_c<kC>(a.w, c * kW + i * kC, a.w_f32, &f[i * kC]);
 #pragma unroll
     for (int e = 0; e < kC; ++e) {
-        b[e] = a.bias ? load_any(a.bias, c + e, a.w_f32) : 0.f;
+        b[e] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kW; ++k) w[k][e] = load_any(a.w, (c + e) * kW + k, a.w_f32);
+        for (int k = 0; k < kW; ++k) w[k][e] = f[e * kW + k];
     }
+    if (a.bias) load_any_c<kC>(a.bias, c, a.w_f32, b);
 }
 
 // Sequences of a batch: their first token and the one behind their last, in
@@ -129,6 +134,37 @@ __device__ __forceinline__ void convolve(const float (&w)[kW][kC], const float (
     }
 }
 
+// A wave's run of tokens: within one batch row (of T tokens, the packed batch
+// being one row), so that its rows are one stride apart.
+struct Run {
+    int64_t b, t0, stop;      // batch row; flat tokens t0 .. stop - 1
+};
+__device__ __forceinline__ Run run_of(int64_t u, int64_t runs, int64_t T, int len) {
+    Run r;
+    r.b = u / runs;
+    r.t0 = r.b * T + (u - r.b * runs) * len;
+    r.stop = r.t0 + len < (r.b + 1) * T ? r.t0 + len : (r.b + 1) * T;
+    return r;
+}
+
+template <int kC, int kW>
+__device__ __forceinline__ void conv_token(const float (&w)[kW][kC], const float (&b)[kC], float (&win)[kW][kC],
+                                           const float (&x)[kC], int silu, uint16_t *out) {
+    float pre[kC];
+#pragma unroll
+    for (int e = 0; e < kC; ++e) win[kW - 1][e] = x[e];
+    convolve<kC, kW>(w, b, win, pre);
+    if (silu) {
+#pragma unroll
+        for (int e = 0; e < kC; ++e) pre[e] *= sigmoid(pre[e]);
+    }
+    store_c<kC>(out, pre);
+#pragma unroll
+    for (int k = 0; k < kW - 1; ++k)
+#pragma unroll
+        for (int e = 0; e < kC; ++e) win[k][e] = win[k + 1][e];
+}
+
 template <int kC, int kW>
 __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
     const int64_t c = ((int64_t)blockIdx.x * kLanes + (threadIdx.x & 63)) * kC;
@@ -137,24 +173,29 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
     float w[kW][kC], b[kC];
     load_filter<kC, kW>(a, c, w, b);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    for (int64_t t0 = ((int64_t)blockIdx.y * kWaves + wave) * kRun; t0 < sq.total;
-         t0 += (int64_t)gridDim.y * kWaves * kRun) {
-        const int64_t stop = t0 + kRun < sq.total ? t0 + kRun : sq.total;
-        int64_t n = sq.of(t0);
+    const int64_t runs = (a.T + kRun - 1) / kRun;
+    for (int64_t u = (int64_t)blockIdx.y * kWaves + wave; u < a.B * runs; u += (int64_t)gridDim.y * kWaves) {
+        const Run run = run_of(u, runs, a.T, kRun);
+        int64_t n = sq.of(run.t0);
         if (n >= sq.N) return;  // behind the last sequence, and so are later runs
-        float x[kRun][kC];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-            if (t0 + i < stop) load_c<kC>(a.x + row_of(t0 + i, a.T, a.xb, a.xt) + c, x[i]);
-        // win[k]: the input k steps after the oldest one that t0 needs
-        float win[kW][kC];
+        const uint16_t *xp = a.x + run.b * a.xb + (run.t0 - run.b * a.T) * a.xt + c;
+        uint16_t *op = a.out + run.t0 * a.D + c;
         int64_t begin = sq.begin(n), next = sq.end(n);
+        float win[kW][kC];     // win[k]: the input k steps after the oldest one that the token needs
+        if (run.t0 + kRun <= next && run.t0 + kRun <= run.stop) {
+            // the run lies within one sequence: all its loads in flight together
+            float x[kRun][kC];
 #pragma unroll
-        for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, t0 - begin - (kW - 1) + k, c, win[k]);
+            for (int i = 0; i < kRun; ++i) load_c<kC>(xp + i * a.xt, x[i]);
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const int64_t t = t0 + i;
-            if (t >= stop) break;
+            for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, run.t0 - begin - (kW - 1) + k, c, win[k]);
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) conv_token<kC, kW>(w, b, win, x[i], a.silu, op + i * a.D);
+            continue;
+        }
+#pragma unroll
+        for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, run.t0 - begin - (kW - 1) + k, c, win[k]);
+        for (int64_t t = run.t0; t < run.stop; ++t) {
             if (t >= next) {  // the next sequence that has tokens
                 do { ++n; } while (n < sq.N && sq.end(n) <= t);
                 if (n >= sq.N) break;
@@ -163,19 +204,9 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
 #pragma unroll
                 for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, n, begin, t - begin - (kW - 1) + k, c, win[k]);
             }
-            float pre[kC];
-#pragma unroll
-            for (int e = 0; e < kC; ++e) win[kW - 1][e] = x[i][e];
-            convolve<kC, kW>(w, b, win, pre);
-            if (a.silu) {
-#pragma unroll
-                for (int e = 0; e < kC; ++e) pre[e] *= sigmoid(pre[e]);
-            }
-            store_c<kC>(a.out + t * a.D + c, pre);
-#pragma unroll
-            for (int k = 0; k < kW - 1; ++k)
-#pragma unroll
-                for (int e = 0; e < kC; ++e) win[k][e] = win[k + 1][e];
+            float x[kC];
+            load_c<kC>(xp + (t - run.t0) * a.xt, x);
+            conv_token<kC, kW>(w, b, win, x, a.silu, op + (t - run.t0) * a.D);
         }
     }
 }
@@ -290,9 +321,13 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_bwd_kernel(ConvArgs a
     if (in) {
         float w[kW][kC], b[kC];
         load_filter<kC, kW>(a, c, w, b);
-        for (int64_t t0 = ((int64_t)blockIdx.y * kWaves + wave) * kBwdRun; t0 < sq.total;
-             t0 += (int64_t)gridDim.y * kWaves * kBwdRun) {
-            BwdWalk<kC, kW> s{a, sq, c, t0, t0 + kBwdRun < sq.total ? t0 + kBwdRun : sq.total, sq.of(t0), 0, 0, {}};
+        const int64_t runs = (a.T + kBwdRun - 1) / kBwdRun;
+        for (int64_t v = (int64_t)blockIdx.y * kWaves + wave; v < a.B * runs; v += (int64_t)gridDim.y * kWaves) {
+            const Run run = run_of(v, runs, a.T, kBwdRun);
+            const int64_t t0 = run.t0;
+            const uint16_t *xp = a.x + run.b * a.xb + (t0 - run.b * a.T) * a.xt + c;
+            const uint16_t *yp = a.dy + run.b * a.db_ + (t0 - run.b * a.T) * a.dt_ + c;
+            BwdWalk<kC, kW> s{a, sq, c, t0, run.stop, sq.of(t0), 0, 0, {}};
             if (s.n >= sq.N) break;
             s.clear();
             s.begin = sq.begin(s.n);
@@ -314,8 +349,8 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_bwd_kernel(ConvArgs a
                     for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, s.n, s.begin, t - s.begin - (kW - 1) + k, c, win[k]);
                 }
                 float g[kC], pre[kC];
-                load_c<kC>(a.x + row_of(t, a.T, a.xb, a.xt) + c, win[kW - 1]);
-                load_c<kC>(a.dy + row_of(t, a.T, a.db_, a.dt_) + c, g);
+                load_c<kC>(xp + (t - t0) * a.xt, win[kW - 1]);
+                load_c<kC>(yp + (t - t0) * a.dt_, g);
                 convolve<kC, kW>(w, b, win, pre);
 #pragma unroll
                 for (int e = 0; e < kC; ++e) {
@@ -424,7 +459,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 bool vector_channels(const ConvArgs &a) {
     return a.D % 8 == 0 && a.xb % 8 == 0 && a.xt % 8 == 0 && a.db_ % 8 == 0 && a.dt_ % 8 == 0 && aligned16(a.x) &&
            aligned16(a.out) && aligned16(a.h0) && aligned16(a.ht) && aligned16(a.dy) && aligned16(a.dht) &&
-           aligned16(a.dx) && aligned16(a.dh0);
+           aligned16(a.dx) && aligned16(a.dh0) && aligned16(a.w) && aligned16(a.bias);
 }
 
 unsigned blocks_x(int64_t D, int kC, int lanes) { return (unsigned)((D + (int64_t)kC * lanes - 1) / ((int64_t)kC * lanes)); }
@@ -436,7 +471,7 @@ unsigned blocks_y(int64_t n, int64_t per) {
 template <int kC, int kW>
 hipError_t launch_conv(const ConvArgs &a, hipStream_t s) {
     if (a.B * a.T > 0)
-        hipLaunchKernelGGL((kda_conv_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), blocks_y(a.B * a.T, kRun * kWaves)),
+        hipLaunchKernelGGL((kda_conv_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), blocks_y(a.B * ((a.T + kRun - 1) / kRun), kWaves)),
                            dim3(kLanes * kWaves), 0, s, a);
     if (a.ht)
         hipLaunchKernelGGL((kda_conv_state_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 256), blocks_y(a.N, 1)), dim3(256), 0, s, a);
@@ -476,7 +511,7 @@ hipError_t kda_launch_conv_decode(const ConvArgs &a, int W, hipStream_t s) { KDA
 // sum of dweight and dbias.
 int64_t kda_conv_parts(int64_t B, int64_t T, int64_t D) {
     (void)D;
-    const int64_t n = (B * T + kBwdRun * kWaves - 1) / (kBwdRun * kWaves);
+    const int64_t n = (B * ((T + kBwdRun - 1) / kBwdRun) + kWaves - 1) / kWaves;
     return n < 1 ? 1 : n < 256 ? n : 256;
 }
 
