@@ -5,11 +5,11 @@
 //
 // per channel, the W - 1 inputs before a sequence's first token coming from its
 // state.  Two operations per loaded value and tap: bound by memory traffic (x
-// once, out once).  A lane holds 8 neighbouring channels (16 bytes per token
-// and access, 1 KiB per wave) and walks over a run of tokens with the last
-// W - 1 inputs in registers, so that x is read once plus W - 1 rows per run.
-// Where the channel count, a stride or an address does not allow 16-byte
-// accesses, the same code runs with one channel per lane.
+// once, out once).  A lane holds 4 neighbouring channels (8 bytes per token and
+// access, 512 per wave) and walks over a run of tokens with the last W - 1
+// inputs in registers, so that x is read once plus W - 1 rows per run.  Where the
+// channel count, a stride or an address does not allow such accesses, the same
+// code runs with one channel per lane.
 #include "kda_layer_args.h"
 
 using namespace kda;
@@ -22,41 +22,61 @@ constexpr int kRun = 16;         // tokens per run, forward: their loads are all
 constexpr int kBwdRun = 32;      // tokens per run, gradient
 constexpr int64_t kMaxGridY = 65535;
 
+// kC neighbouring bf16 values as loaded, until they are used.
+template <int kC> struct Raw;
+template <> struct Raw<8> {
+    uint4 v;
+    __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float *o) const { unpack_bf16x8(v, o); }
+};
+template <> struct Raw<4> {
+    uint2 v;
+    __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void get(float *o) const {
+        o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+        o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+};
+template <> struct Raw<1> {
+    uint16_t v;
+    __device__ __forceinline__ void load(const uint16_t *p) { v = *p; }
+    __device__ __forceinline__ void get(float *o) const { o[0] = bf16_bits_to_f32(v); }
+};
 template <int kC>
 __device__ __forceinline__ void load_c(const uint16_t *p, float *o) {
-    if constexpr (kC == 8) unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), o);
-    else o[0] = bf16_bits_to_f32(*p);
+    Raw<kC> r;
+    r.load(p);
+    r.get(o);
 }
 template <int kC>
 __device__ __forceinline__ void store_c(uint16_t *p, const float *v) {
     if constexpr (kC == 8)
         *reinterpret_cast<uint4 *>(p) =
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    else if constexpr (kC == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     else *p = f32_to_bf16_bits(v[0]);
 }
 // kC entries of a state or parameter row of either type.
 template <int kC>
 __device__ __forceinline__ void load_any_c(const void *p, int64_t i, int f32, float *o) {
-    if constexpr (kC == 8) {
-        if (f32) {
-            const float4 a = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-            const float4 b = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + 4);
-            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-            o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-        } else {
-            load_c<8>(reinterpret_cast<const uint16_t *>(p) + i, o);
+    if constexpr (kC == 1) {
+        o[0] = load_any(p, i, f32);
+    } else if (f32) {
+#pragma unroll
+        for (int j = 0; j < kC; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i + j);
+            o[j] = a.x; o[j + 1] = a.y; o[j + 2] = a.z; o[j + 3] = a.w;
         }
     } else {
-        o[0] = load_any(p, i, f32);
+        load_c<kC>(reinterpret_cast<const uint16_t *>(p) + i, o);
     }
 }
 template <int kC>
 __device__ __forceinline__ void store_f32_c(float *p, const float *v) {
-    if constexpr (kC == 8) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        p[0] = v[0];
+    if constexpr (kC == 1) p[0] = v[0];
+    else {
+#pragma unroll
+        for (int j = 0; j < kC; j += 4) *reinterpret_cast<float4 *>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
 }
 template <int kC>
@@ -65,8 +85,8 @@ __device__ __forceinline__ void store_any_c(void *p, int64_t i, int f32, const f
     else store_c<kC>(reinterpret_cast<uint16_t *>(p) + i, v);
 }
 
-// The lane's filter: w[k][e] for channel c + e.  With 8 channels its kC kW
-// entries are one 16-byte aligned piece.
+// The lane's filter: w[k][e] for channel c + e.  With several channels its kC kW
+// entries are one aligned piece.
 template <int kC, int kW>
 __device__ __forceinline__ void load_filter(const ConvArgs &a, int64_t c, float (&w)[kW][kC], float (&b)[kC]) {
     float f[kW * kC];
@@ -165,16 +185,35 @@ __device__ __forceinline__ void conv_token(const float (&w)[kW][kC], const float
         for (int e = 0; e < kC; ++e) win[k][e] = win[k + 1][e];
 }
 
+// The final state of sequence n: its last W - 1 inputs.  All are read before
+// the first is written, so that ht may be h0 once nothing else reads that.
 template <int kC, int kW>
-__global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
+__device__ __forceinline__ void final_state(const ConvArgs &a, const Seqs &sq, int64_t n, int64_t c) {
+    const int64_t begin = sq.begin(n), len = sq.end(n) > begin ? sq.end(n) - begin : 0;
+    float v[kW - 1][kC];
+#pragma unroll
+    for (int j = 0; j < kW - 1; ++j) input_at<kC, kW>(a, n, begin, len - (kW - 1) + j, c, v[j]);
+#pragma unroll
+    for (int j = 0; j < kW - 1; ++j) store_any_c<kC>(a.ht, (n * (kW - 1) + j) * a.D + c, a.ht_f32, v[j]);
+}
+
+// The first state_blocks workgroups along y write final states instead.
+template <int kC, int kW>
+__global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a, int state_blocks) {
     const int64_t c = ((int64_t)blockIdx.x * kLanes + (threadIdx.x & 63)) * kC;
     if (c >= a.D) return;
     const Seqs sq = seqs_of(a);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if ((int)blockIdx.y < state_blocks) {
+        for (int64_t n = (int64_t)blockIdx.y * kWaves + wave; n < sq.N; n += (int64_t)state_blocks * kWaves)
+            final_state<kC, kW>(a, sq, n, c);
+        return;
+    }
+    const int64_t by = blockIdx.y - state_blocks, blocks = gridDim.y - state_blocks;
     float w[kW][kC], b[kC];
     load_filter<kC, kW>(a, c, w, b);
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t runs = (a.T + kRun - 1) / kRun;
-    for (int64_t u = (int64_t)blockIdx.y * kWaves + wave; u < a.B * runs; u += (int64_t)gridDim.y * kWaves) {
+    for (int64_t u = by * kWaves + wave; u < a.B * runs; u += blocks * kWaves) {
         const Run run = run_of(u, runs, a.T, kRun);
         int64_t n = sq.of(run.t0);
         if (n >= sq.N) return;  // behind the last sequence, and so are later runs
@@ -211,22 +250,14 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_kernel(ConvArgs a) {
     }
 }
 
-// The final states: the last W - 1 inputs of every sequence.  A thread reads
-// all its entries before it writes them, so that ht may be h0; it is launched
-// after the convolution, which reads h0.
+// Final states in a launch of their own, for ht the same as h0.
 template <int kC, int kW>
-__global__ __launch_bounds__(256) void kda_conv_state_kernel(ConvArgs a) {
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kC;
+__global__ __launch_bounds__(kLanes *kWaves) void kda_conv_state_kernel(ConvArgs a) {
+    const int64_t c = ((int64_t)blockIdx.x * kLanes + (threadIdx.x & 63)) * kC;
     if (c >= a.D) return;
     const Seqs sq = seqs_of(a);
-    for (int64_t n = blockIdx.y; n < sq.N; n += gridDim.y) {
-        const int64_t begin = sq.begin(n), len = sq.end(n) > begin ? sq.end(n) - begin : 0;
-        float v[kW - 1][kC];
-#pragma unroll
-        for (int j = 0; j < kW - 1; ++j) input_at<kC, kW>(a, n, begin, len - (kW - 1) + j, c, v[j]);
-#pragma unroll
-        for (int j = 0; j < kW - 1; ++j) store_any_c<kC>(a.ht, (n * (kW - 1) + j) * a.D + c, a.ht_f32, v[j]);
-    }
+    for (int64_t n = (int64_t)blockIdx.y * kWaves + (threadIdx.x >> 6); n < sq.N; n += (int64_t)gridDim.y * kWaves)
+        final_state<kC, kW>(a, sq, n, c);
 }
 
 // One token per sequence: output and shifted state in one launch.
@@ -336,6 +367,8 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_bwd_kernel(ConvArgs a
 #pragma unroll
             for (int k = 0; k < kW - 1; ++k) input_at<kC, kW>(a, s.n, s.begin, t0 - s.begin - (kW - 1) + k, c, win[k]);
             int64_t t = t0;
+            // unrolled: the next tokens' loads go out while this one is computed
+#pragma unroll 4
             for (; t < s.stop + kW - 1; ++t) {
                 if (t >= s.next) {
                     s.flush(t);
@@ -396,19 +429,20 @@ __global__ __launch_bounds__(kLanes *kWaves) void kda_conv_bwd_kernel(ConvArgs a
 }
 
 // dweight and dbias: the sum of the partial sums, in a fixed order.  A workgroup
-// takes 64 channels of one tap, 4 waves over the parts.
+// takes 64 channels of one tap, 16 waves over the parts.
 template <int kW>
-__global__ __launch_bounds__(256) void kda_conv_bwd_sum_kernel(ConvArgs a) {
-    __shared__ float s[4][64];
+__global__ __launch_bounds__(1024) void kda_conv_bwd_sum_kernel(ConvArgs a) {
+    __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, k = blockIdx.y;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float v = 0.f;
     if (c < a.D)
-        for (int64_t p = q; p < a.parts; p += 4) v += a.part[(p * (kW + 1) + k) * a.D + c];
+        for (int64_t p = q; p < a.parts; p += 16) v += a.part[(p * (kW + 1) + k) * a.D + c];
     s[q][lane] = v;
     __syncthreads();
     if (q != 0 || c >= a.D) return;
-    v = s[0][lane] + s[1][lane] + s[2][lane] + s[3][lane];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += s[i][lane];
     if (k < kW) a.dw[c * kW + k] = v;
     else if (a.dbias) a.dbias[c] = v;
 }
@@ -454,8 +488,8 @@ __global__ __launch_bounds__(64) void kda_conv_bwd_state_kernel(ConvArgs a) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// 16-byte accesses to every tensor of the call (states and partial sums have
-// rows of D entries, so D a multiple of 8 keeps them aligned too).
+// Wide accesses to every tensor of the call (states and partial sums have rows
+// of D entries, so D a multiple of 8 keeps them aligned too).
 bool vector_channels(const ConvArgs &a) {
     return a.D % 8 == 0 && a.xb % 8 == 0 && a.xt % 8 == 0 && a.db_ % 8 == 0 && a.dt_ % 8 == 0 && aligned16(a.x) &&
            aligned16(a.out) && aligned16(a.h0) && aligned16(a.ht) && aligned16(a.dy) && aligned16(a.dht) &&
@@ -468,13 +502,23 @@ unsigned blocks_y(int64_t n, int64_t per) {
     return (unsigned)(b < 1 ? 1 : b < kMaxGridY ? b : kMaxGridY);
 }
 
+// Sequences per workgroup of final states: with few, one wave each.
+constexpr int kMaxStateBlocks = 1024;
+
 template <int kC, int kW>
 hipError_t launch_conv(const ConvArgs &a, hipStream_t s) {
-    if (a.B * a.T > 0)
-        hipLaunchKernelGGL((kda_conv_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), blocks_y(a.B * ((a.T + kRun - 1) / kRun), kWaves)),
-                           dim3(kLanes * kWaves), 0, s, a);
-    if (a.ht)
-        hipLaunchKernelGGL((kda_conv_state_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 256), blocks_y(a.N, 1)), dim3(256), 0, s, a);
+    const unsigned x = blocks_x(a.D, kC, kLanes);
+    // where the final state replaces the initial one, the tokens read that first
+    const bool apart = a.ht && (a.ht == a.h0 || a.B * a.T == 0);
+    unsigned states = a.ht ? blocks_y(a.N, kWaves) : 0;
+    if (states > kMaxStateBlocks) states = kMaxStateBlocks;
+    if (a.B * a.T > 0) {
+        const unsigned y = blocks_y(a.B * ((a.T + kRun - 1) / kRun), kWaves);
+        const unsigned first = apart ? 0 : states;
+        hipLaunchKernelGGL((kda_conv_kernel<kC, kW>), dim3(x, first + (y < kMaxGridY - first ? y : (unsigned)kMaxGridY - first)),
+                           dim3(kLanes * kWaves), 0, s, a, (int)first);
+    }
+    if (apart) hipLaunchKernelGGL((kda_conv_state_kernel<kC, kW>), dim3(x, states), dim3(kLanes * kWaves), 0, s, a);
     return hipGetLastError();
 }
 
@@ -485,7 +529,7 @@ hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((kda_conv_bwd_kernel<kC, kW>), dim3(blocks_x(a.D, kC, kLanes), (unsigned)a.parts),
                            dim3(kLanes * kWaves), 0, s, a);
     else b.parts = 0;
-    hipLaunchKernelGGL((kda_conv_bwd_sum_kernel<kW>), dim3(blocks_x(a.D, 1, 64), kW + 1), dim3(256), 0, s, b);
+    hipLaunchKernelGGL((kda_conv_bwd_sum_kernel<kW>), dim3(blocks_x(a.D, 1, 64), kW + 1), dim3(1024), 0, s, b);
     if (a.dh0)
         hipLaunchKernelGGL((kda_conv_bwd_state_kernel<kC, kW>), dim3(blocks_x(a.D, kC, 64), blocks_y(a.N, 1)), dim3(64), 0, s, a);
     return hipGetLastError();
@@ -499,8 +543,14 @@ hipError_t launch_decode(const ConvArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// Channels per lane where 16- and 8-byte accesses are possible.  4 rather than 8:
+// half the registers (filter, window, pending sums), twice the waves; the same
+// for prompts (90 us at 4 x 2048 x 12288, 114 against 120 us packed), 66 against
+// 79 us for the gradient at 8192 x 4352.
+constexpr int kVec = 4;
+
 #define KDA_CONV_DISPATCH(fn)                                                          \
-    if (vector_channels(a)) return W == 2 ? fn<8, 2>(a, s) : W == 3 ? fn<8, 3>(a, s) : fn<8, 4>(a, s); \
+    if (vector_channels(a)) return W == 2 ? fn<kVec, 2>(a, s) : W == 3 ? fn<kVec, 3>(a, s) : fn<kVec, 4>(a, s); \
     return W == 2 ? fn<1, 2>(a, s) : W == 3 ? fn<1, 3>(a, s) : fn<1, 4>(a, s)
 
 hipError_t kda_launch_conv(const ConvArgs &a, int W, hipStream_t s) { KDA_CONV_DISPATCH(launch_conv); }

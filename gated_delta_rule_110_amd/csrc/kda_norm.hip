@@ -407,20 +407,26 @@ __global__ __launch_bounds__(kBlock) void kda_rmsnorm_bwd_weight_kernel(NormBwdA
     }
 }
 
-// dweight = the sum of the partial sums: 64 columns per workgroup, 16 threads per
-// column, in a fixed order.
+// dweight = the sum of the partial sums, in a fixed order: 16 columns per
+// workgroup, 64 threads per column.
 __global__ __launch_bounds__(1024) void kda_rmsnorm_bwd_sum_kernel(NormBwdArgs a) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float s[64][17];
+    const int col = threadIdx.x & 15, q = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
     float v = 0.f;
     if (c < a.D)
-        for (int64_t p = q; p < a.parts; p += 16) v += a.part[p * a.D + c];
-    s[q][lane] = v;
+        for (int64_t p = q; p < a.parts; p += 64) v += a.part[p * a.D + c];
+    s[q][col] = v;
+    __syncthreads();
+    if (q < 8) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += s[q + 8 * i][col];
+        s[q][col] = v;
+    }
     __syncthreads();
     if (q == 0 && c < a.D) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) v += s[i][lane];
+        for (int i = 1; i < 8; ++i) v += s[i][col];
         a.dw[c] = v;
     }
 }
@@ -522,6 +528,6 @@ hipError_t kda_launch_rmsnorm_bwd(const NormBwdArgs &a, hipStream_t s) {
     } else {
         b.parts = 0;
     }
-    hipLaunchKernelGGL(kda_rmsnorm_bwd_sum_kernel, dim3((unsigned)((a.D + 63) / 64)), dim3(1024), 0, s, b);
+    hipLaunchKernelGGL(kda_rmsnorm_bwd_sum_kernel, dim3((unsigned)((a.D + 15) / 16)), dim3(1024), 0, s, b);
     return hipGetLastError();
 }
