@@ -21,6 +21,7 @@ size_t width(int32_t d) { return d == KDA_FP32 ? 4 : 2; }
 constexpr int64_t kMaxTokens = int64_t(1) << 40;
 constexpr int64_t kMaxColumns = int64_t(1) << 22;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;
 constexpr int64_t kMaxSeqs = 0x7fffffff;
 constexpr int64_t kMaxScanTokens = (int64_t(1) << 31) - 128;  // pieces and chunks are counted in 32 bits
 // Workgroups of 256 threads in one launch: its work-items are counted in 32 bits.
@@ -228,6 +229,9 @@ kda_status_t check_ssm(const kda_ssm_desc_t *d, bool packed) {
                                d->b_stride_b, d->b_stride_t, d->c_stride_b, d->c_stride_t};
     for (int64_t s : strides)
         if (!stride_ok(s)) return KDA_ERR_SHAPE;
+    // the offsets of a chunk's tokens are kept in 32 bits
+    for (int64_t s : {d->x_stride_t, d->dt_stride_t, d->b_stride_t, d->c_stride_t})
+        if (s >= kMaxTokenStride) return KDA_ERR_SHAPE;
     // x, B and C are read 16 bytes at a time
     for (int64_t s : {d->x_stride_b, d->x_stride_t, d->b_stride_b, d->b_stride_t, d->c_stride_b, d->c_stride_t})
         if (s % 8 != 0) return KDA_ERR_ALIGN;
@@ -644,7 +648,8 @@ extern "C" kda_status_t kda_ssm_bwd(const void *x, const void *dt, const void *B
     kda_status_t st = ssm_args(x, dt, Bm, Cm, A_log, dt_bias, D, initial_state, d_final_state, cu_seqlens, desc, a);
     if (st != KDA_OK) return st;
     if (!dA_log || (desc->T > 0 && (!d_out || !dx || !ddt || !dB || !dC))) return KDA_ERR_NULL;
-    if (!stride_ok(desc->d_out_stride_b) || !stride_ok(desc->d_out_stride_t)) return KDA_ERR_SHAPE;
+    if (!stride_ok(desc->d_out_stride_b) || !stride_ok(desc->d_out_stride_t) || desc->d_out_stride_t >= kMaxTokenStride)
+        return KDA_ERR_SHAPE;
     if (desc->d_out_stride_b % 8 || desc->d_out_stride_t % 8 || !aligned(d_out, 16) || !aligned(dx, 16) || !aligned(ddt, 2) ||
         !aligned(dB, 16) || !aligned(dC, 16) || !aligned(dA_log, 4) || !aligned(ddt_bias, 4) || !aligned(dD, 4) ||
         !aligned(d_initial_state, 16))

@@ -191,18 +191,30 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
     const int chunks = (p.count + kL - 1) / kL;
     Rows<kN, kThreads> rk, rc;
     Rows<kPB, kThreads> rx;
+    rk.init(a.kt, kPitch<kN>);
+    if constexpr (kOut) rc.init(a.ct, kPitch<kN>);
+    rx.init(a.xt, kXPitch);
+    const uint32_t doff = (uint32_t)lane * (uint32_t)a.dtt * 2;
+    // byte offset of this lane's output: token lane % 16, 4 channels
+    const uint32_t ostep = (uint32_t)(a.H * a.P) * 2;
+    const uint32_t ooff = (uint32_t)r * ostep + (16 * w + 4 * g) * 2;
     float rdt = 0.f;
     auto fetch = [&](int i) {
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
         const int64_t t = (int64_t)c * kL;
-        rk.load(krow + t * a.kt, a.kt, rows);
-        if constexpr (kOut) rc.load(crow + t * a.ct, a.ct, rows);
-        rx.load(xrow + t * a.xt, a.xt, rows);
-        if (w == 0) rdt = lane < rows ? bf16_bits_to_f32(drow[(t + lane) * a.dtt]) : 0.f;
+        if (w == 0) {
+            rdt = 0.f;
+            if (lane < rows)
+                rdt = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + t * a.dtt) + doff));
+        }
+        rx.load(xrow + t * a.xt, rows);
+        rk.load(krow + t * a.kt, rows);
+        if constexpr (kOut) rc.load(crow + t * a.ct, rows);
     };
     fetch(0);
     float total = 0.f;
+    // Barriers here order LDS traffic only: the next chunk's loads stay in flight.
     for (int i = 0; i < chunks; ++i) {
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
@@ -215,12 +227,12 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
             }
             if (i + 1 == chunks && !(kReverse && p.first && a.ht)) break;  // what leaves the piece is not needed
         }
-        if (i) __syncthreads();  // the chunk before is done with
+        if (i) lds_barrier();  // the chunk before is done with
+        if (w == 0) step_sizes(rdt, lane < rows, bias, nA2, sm.g, sm.gr, sm.dt);
+        rx.store(sm.x, kXPitch);
         rk.store(sm.k, kPitch<kN>);
         if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
-        rx.store(sm.x, kXPitch);
-        if (w == 0) step_sizes(rdt, lane < rows, bias, nA2, sm.g, sm.gr, sm.dt);
-        __syncthreads();
+        lds_barrier();
         if (i + 1 < chunks) fetch(i + 1);
         const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1];
 
@@ -296,7 +308,8 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[it][e] *= d;
             }
-            __syncthreads();
+            lds_barrier();
+            char *orows = reinterpret_cast<char *>(orow + (int64_t)c * kL * a.H * a.P);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
 #pragma unroll
@@ -307,8 +320,8 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
                 }
                 const int t = 16 * it + r;
                 if (t < rows)
-                    *reinterpret_cast<uint2 *>(orow + ((int64_t)c * kL + t) * a.H * a.P + 16 * w + 4 * g) =
-                        make_uint2(pack_bf16(y[it][0], y[it][1]), pack_bf16(y[it][2], y[it][3]));
+                    *reinterpret_cast<uint2 *>(orows + 16 * it * ostep + ooff) =
+                        make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
             }
         }
 

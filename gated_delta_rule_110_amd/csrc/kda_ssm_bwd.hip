@@ -78,15 +78,6 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
     return v;
 }
-__device__ __forceinline__ double wave_scan(double v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
 __device__ __forceinline__ void add_to(float *p, float v, bool more) { *p = more ? *p + v : v; }
 
 // Tokens of chunk number i of the batch.
@@ -140,8 +131,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 
     {
         Rows<kN, kThreads> rb, rc;
-        rb.load(a.Bm + ck.row0 * a.bb + ck.t0 * a.bt + grp * kN, a.bt, rows);
-        rc.load(a.Cm + ck.row0 * a.cb + ck.t0 * a.ct + grp * kN, a.ct, rows);
+        rb.init(a.bt, kPitch<kN>);
+        rc.init(a.ct, kPitch<kN>);
+        rb.load(a.Bm + ck.row0 * a.bb + ck.t0 * a.bt + grp * kN, rows);
+        rc.load(a.Cm + ck.row0 * a.cb + ck.t0 * a.ct + grp * kN, rows);
         rb.store(sm.b, kPitch<kN>);
         rc.store(sm.c, kPitch<kN>);
     }
@@ -172,8 +165,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             f4 S[4];                             // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
             {
                 Rows<kPB, kThreads> rx, ry;
-                rx.load(xrow + h * a.P + pb * kPB, a.xt, rows);
-                ry.load(yrow + h * a.P + pb * kPB, a.yt, rows);
+                rx.init(a.xt, kXPitch);
+                ry.init(a.yt, kXPitch);
+                rx.load(xrow + h * a.P + pb * kPB, rows);
+                ry.load(yrow + h * a.P + pb * kPB, rows);
                 f4 D[kN / 32];
 #pragma unroll
                 for (int i = 0; i < kN / 32; ++i) D[i] = ds[i * kThreads + threadIdx.x];

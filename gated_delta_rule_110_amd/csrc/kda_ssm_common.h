@@ -31,51 +31,99 @@ __device__ __forceinline__ s8 lds8(const uint16_t *p) { return *reinterpret_cast
 
 __device__ __forceinline__ int64_t clamp_to(int64_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? hi : v; }
 
-// Rows of kN (or 64) bf16 values to registers and on to LDS: 16 bytes a thread.
+// 64 token rows of kCols bf16 values to registers and on to LDS, 16 bytes a
+// thread and pass.  A row's address is a uniform one plus 32 bits a thread
+// (the host refuses token strides of 2^24 entries and more).
 template <int kCols, int kThreads>
 struct Rows {
     static constexpr int kPer = kThreads / (kCols / 8);  // rows per pass
     static constexpr int kPass = kL / kPer;
     uint4 v[kPass];
-    __device__ __forceinline__ void load(const uint16_t *base, int64_t stride, int rows) {
-        const int c = threadIdx.x % (kCols / 8), r = threadIdx.x / (kCols / 8);
+    uint32_t off;                                        // bytes from a pass's first row
+    int64_t step;                                        // bytes between the passes
+    int r, lds;
+    __device__ __forceinline__ void init(int64_t stride, int pitch) {
+        const int c = threadIdx.x % (kCols / 8);
+        r = threadIdx.x / (kCols / 8);
+        off = ((uint32_t)r * (uint32_t)stride + 8 * c) * 2;
+        step = kPer * stride * 2;
+        lds = r * pitch + 8 * c;
+    }
+    __device__ __forceinline__ void load(const uint16_t *base, int rows) {
+        const char *p = reinterpret_cast<const char *>(base);
+        if (rows >= kL) {
 #pragma unroll
-        for (int i = 0; i < kPass; ++i) {
-            const int t = i * kPer + r;
-            v[i] = make_uint4(0, 0, 0, 0);  // rows behind the sequence count as zero
-            if (t < rows) v[i] = *reinterpret_cast<const uint4 *>(base + t * stride + 8 * c);
+            for (int i = 0; i < kPass; ++i) v[i] = *reinterpret_cast<const uint4 *>(p + i * step + off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPass; ++i) {
+                v[i] = make_uint4(0, 0, 0, 0);           // rows behind the sequence count as zero
+                if (i * kPer + r < rows) v[i] = *reinterpret_cast<const uint4 *>(p + i * step + off);
+            }
         }
     }
-    __device__ __forceinline__ void store(uint16_t *lds, int pitch) const {
-        const int c = threadIdx.x % (kCols / 8), r = threadIdx.x / (kCols / 8);
+    __device__ __forceinline__ void store(uint16_t *to, int pitch) const {
 #pragma unroll
-        for (int i = 0; i < kPass; ++i) *reinterpret_cast<uint4 *>(lds + (i * kPer + r) * pitch + 8 * c) = v[i];
+        for (int i = 0; i < kPass; ++i) *reinterpret_cast<uint4 *>(to + i * kPer * pitch + lds) = v[i];
     }
 };
 
-// Two- and three-part bf16 splits of fp32 values, 8 at a time.
+// Splits of fp32 values into two or three bf16 parts, each rounded to nearest
+// and the next taken from what it left, two values at a time.
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t round_pair(float &a, float &b) {
+    const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
+    a -= __uint_as_float(h << 16);
+    b -= __uint_as_float(h & 0xffff0000u);
+    return h;
+}
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
+}
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void split2(const float *x, s8 &hi, s8 &lo) {
+    u4v h, l;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        short h, l;
-        split_bf16(x[j], h, l);
-        hi[j] = h;
-        lo[j] = l;
+    for (int j = 0; j < 4; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
+        h[j] = round_pair(a, b);
+        l[j] = pack_pair(a, b);
     }
+    hi = __builtin_bit_cast(s8, h);
+    lo = __builtin_bit_cast(s8, l);
 }
-__device__ __forceinline__ float bf16_rest(float x, short &hi) {
-    hi = (short)f32_to_bf16_bits(x);
-    return x - bf16_bits_to_f32((uint16_t)hi);
-}
-__device__ __forceinline__ void split3(const float *x, s8 &a, s8 &b, s8 &c) {
+__device__ __forceinline__ void split3(const float *x, s8 &p, s8 &q, s8 &r) {
+    u4v h, m, l;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        short h, m;
-        const float r = bf16_rest(bf16_rest(x[j], h), m);
-        a[j] = h;
-        b[j] = m;
-        c[j] = (short)f32_to_bf16_bits(r);
+    for (int j = 0; j < 4; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
+        h[j] = round_pair(a, b);
+        m[j] = round_pair(a, b);
+        l[j] = pack_pair(a, b);
     }
+    p = __builtin_bit_cast(s8, h);
+    q = __builtin_bit_cast(s8, m);
+    r = __builtin_bit_cast(s8, l);
+}
+
+// Inclusive running sum over the 64 lanes, in 64 bits: within rows of 16 lanes,
+// then the rows before (lane moves only, no LDS).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double lane_move(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRows, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan(double v) {
+    v += lane_move<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: lanes without a source add 0
+    v += lane_move<0x112, 0xf>(v);
+    v += lane_move<0x114, 0xf>(v);
+    v += lane_move<0x118, 0xf>(v);
+    v += lane_move<0x142, 0xa>(v);  // the last lane of rows 0 and 2 to rows 1 and 3
+    v += lane_move<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
+    return v;
 }
 
 // The chunk's step sizes and running log-decays, by wave 0, lane = token.  The
@@ -84,13 +132,8 @@ __device__ __forceinline__ void split3(const float *x, s8 &a, s8 &b, s8 &c) {
 // where the steps are large), and would lose the low bits of fp32 otherwise.
 __device__ __forceinline__ void step_sizes(float raw, bool live, float bias, float nA2, float *g, float *gr, float *dts) {
     const float dt = live ? softplus(raw + bias) : 0.f;
-    double s = (double)nA2 * (double)dt;
+    const double s = wave_scan((double)nA2 * (double)dt);
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(s, d);
-        if (lane >= d) s += o;
-    }
     const float hi = (float)s;
     g[lane] = hi;
     gr[lane] = (float)(s - (double)hi);

@@ -138,7 +138,7 @@ size_t kda_conv_bwd_workspace_size(const kda_conv_desc_t *desc);
 typedef struct {
     int64_t B, T, H, P, G, N;               /* P and N are 64 or 128; H is a multiple of G */
     int64_t num_seqs;
-    int64_t x_stride_b, x_stride_t;         /* x [B, T, H, P] */
+    int64_t x_stride_b, x_stride_t;         /* x [B, T, H, P]; token strides are below 2^24 here */
     int64_t dt_stride_b, dt_stride_t;       /* dt [B, T, H] */
     int64_t b_stride_b, b_stride_t;         /* B [B, T, G, N] */
     int64_t c_stride_b, c_stride_t;         /* C [B, T, G, N] */

@@ -144,7 +144,7 @@ def test_ssm_checks(lib):
         assert ssm(lib, which, B=0) == SHAPE and ssm(lib, which, T=-1) == SHAPE and ssm(lib, which, num_seqs=1) == SHAPE
         assert ssm(lib, which, G=3) == SHAPE and ssm(lib, which, H=0) == SHAPE and ssm(lib, which, T=1 << 33) == SHAPE
         assert ssm(lib, which, P=32) == UNSUPPORTED and ssm(lib, which, N=256) == UNSUPPORTED
-        assert ssm(lib, which, x_stride_t=-8) == SHAPE and ssm(lib, which, x_stride_t=257) == ALIGN
+        assert ssm(lib, which, x_stride_t=-8) == SHAPE and ssm(lib, which, b_stride_t=1 << 24) == SHAPE and ssm(lib, which, x_stride_t=257) == ALIGN
         assert ssm(lib, which, piece_chunks=-1) == PARAM
         assert ssm(lib, which, initial_state_dtype=0) == DTYPE and ssm(lib, which, final_state_dtype=3) == DTYPE
         for k in ("x", "B", "C", "h0") + need[:1]:
