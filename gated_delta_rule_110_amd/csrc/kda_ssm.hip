@@ -93,15 +93,22 @@ __device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int
 }
 int64_t grid_size(const SsmChainArgs &a) { return (a.pieces + 7) / 8 * 8 * a.H * (a.P / kPB); }
 
+constexpr int kMEntries = 2 * 4 * 2 * 64 * 8;
+
 template <int kN, bool kOut>
 struct __align__(16) ChainSmem {
     uint16_t k[kL * kPitch<kN>];
-    uint16_t c[kOut ? kL * kPitch<kN> : 8];
+    // C; then, when every wave is done with it, M in two parts as operands:
+    // [part][row tile][k block][lane][8]
+    uint16_t c[kOut ? (kL * kPitch<kN> > kMEntries ? kL * kPitch<kN> : kMEntries) : 8];
     uint16_t x[kL * kXPitch];
-    uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
-    float g[kL], gr[kL];                        // log2 of the decay from the chunk's start, and what rounding it left
-    float dt[kL];
+    Steps s;
+    float before[kOut ? 4 : 1][kL];             // decay from token j to the start of a row tile, times dt_j
 };
+
+// LDS written by a wave's lanes is read by others of the same wave: a wave's LDS
+// accesses are in order, so only the compiler has to keep theirs.
+__device__ __forceinline__ void wave_sync() { asm volatile("" ::: "memory"); }
 
 // 8 consecutive state entries of either type.
 __device__ __forceinline__ void load_state8(const void *p, int64_t i, int f32, float *o) {
@@ -128,7 +135,7 @@ __device__ __forceinline__ void store_state8(void *p, int64_t i, int f32, const 
 // kReverse: the chains of the gradient of the state, from the last token to the
 // first: D <- e^{G_63} D + sum_i e^{G_i} d_out_i C_i^T.
 template <int kN, int kPass, bool kReverse>
-__global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs a) {
+__global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_chain_kernel(SsmChainArgs a) {
     constexpr bool kOut = kPass == kOutputs;
     // The states that the gradient reads are kept as accumulators hold them, 16
     // bytes a lane: those of the scan as S (rows: channels), so that a pair of
@@ -198,15 +205,15 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
     // byte offset of this lane's output: token lane % 16, 4 channels
     const uint32_t ostep = (uint32_t)(a.H * a.P) * 2;
     const uint32_t ooff = (uint32_t)r * ostep + (16 * w + 4 * g) * 2;
-    float rdt = 0.f;
+    uint32_t rdt = 0;            // as loaded: used, and so waited for, only when its chunk begins
     auto fetch = [&](int i) {
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
         const int64_t t = (int64_t)c * kL;
         if (w == 0) {
-            rdt = 0.f;
+            rdt = 0;
             if (lane < rows)
-                rdt = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + t * a.dtt) + doff));
+                rdt = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + t * a.dtt) + doff);
         }
         rx.load(xrow + t * a.xt, rows);
         rk.load(krow + t * a.kt, rows);
@@ -228,13 +235,13 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
             if (i + 1 == chunks && !(kReverse && p.first && a.ht)) break;  // what leaves the piece is not needed
         }
         if (i) lds_barrier();  // the chunk before is done with
-        if (w == 0) step_sizes(rdt, lane < rows, bias, nA2, sm.g, sm.gr, sm.dt);
+        if (w == 0) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s);
         rx.store(sm.x, kXPitch);
         rk.store(sm.k, kPitch<kN>);
         if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
         lds_barrier();
         if (i + 1 < chunks) fetch(i + 1);
-        const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1];
+        const float gl = sm.s.g[kL - 1];
 
         // x along tokens, for this wave's channels
         s8 xf[2];
@@ -244,46 +251,65 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
             xf[kb] = join(read_tr(q), read_tr(q + 16 * kXPitch));
         }
 
+        f4 y[4];
         if constexpr (kOut) {
-            // ---- M for the token rows 16 w .. 16 w + 15, as B C^T: lane = row i,
-            // its entries the columns j that an operand holds
+            // ---- M for the token rows 16 w .. 16 w + 15, as B C^T: lane = row i, its
+            // entries the columns j that an operand holds.  Tiles left of the diagonal
+            // take their decays as a product around the tile's first row, both factors
+            // at most 1; the diagonal tile takes the exponentials themselves.
             const int ti = 16 * w + r;
-            s8 cf[kQ];
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) cf[q] = lds8(sm.c + ti * kPitch<kN> + 32 * q + 8 * g);
-            const float gi = sm.g[ti], gir = sm.gr[ti];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                if (2 * kb > w) break;
-                float m[8];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int jt = 2 * kb + half;
-                    f4 acc = {0.f, 0.f, 0.f, 0.f};
-                    if (jt <= w) {
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q)
-                            acc = mfma16x16x32_bf16(lds8(sm.k + (16 * jt + r) * kPitch<kN> + 32 * q + 8 * g), cf[q], acc);
-                    }
-                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.g[16 * jt + 4 * g]);
-                    const float4 rj = *reinterpret_cast<const float4 *>(&sm.gr[16 * jt + 4 * g]);
-                    const float4 dj = *reinterpret_cast<const float4 *>(&sm.dt[16 * jt + 4 * g]);
-                    const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, rv[4] = {rj.x, rj.y, rj.z, rj.w};
-                    const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tj = 16 * jt + 4 * g + e;
-                        const float v = acc[e] * (__builtin_amdgcn_exp2f((gi - gv[e]) + (gir - rv[e])) * dv[e]);
-                        m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
-                    }
-                }
-                s8 hi, lo;
-                split2(m, hi, lo);
-                *reinterpret_cast<s8 *>(&sm.m[(((0 * 4 + w) * 2 + kb) * 64 + lane) * 8]) = hi;
-                *reinterpret_cast<s8 *>(&sm.m[(((1 * 4 + w) * 2 + kb) * 64 + lane) * 8]) = lo;
+            const float gi = sm.s.g[ti], gir = sm.s.gr[ti];
+            float upto = 1.f;
+            if (w > 0) {
+                const float g0 = sm.s.g[16 * w - 1], g0r = sm.s.gr[16 * w - 1];
+                sm.before[w][lane] = __builtin_amdgcn_exp2f((g0 - sm.s.g[lane]) + (g0r - sm.s.gr[lane])) * sm.s.dt[lane];
+                upto = __builtin_amdgcn_exp2f((gi - g0) + (gir - g0r));
+                wave_sync();
             }
-            // ---- outputs, transposed: lane = token, entries 4 neighbouring channels
-            s8 sh[kQ], sl[kQ];
+            s8 m0[2], m1[2];
+            {
+                f4 cb[4];
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) cb[jt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    const s8 cv = lds8(sm.c + ti * kPitch<kN> + 32 * q + 8 * g);
+#pragma unroll
+                    for (int jt = 0; jt < 4; ++jt)
+                        if (jt <= w) cb[jt] = mfma16x16x32_bf16(lds8(sm.k + (16 * jt + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[jt]);
+                }
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    if (2 * kb > w) break;
+                    float m[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int jt = 2 * kb + half;
+                        if (jt < w) {
+                            const float4 bj = *reinterpret_cast<const float4 *>(&sm.before[w][16 * jt + 4 * g]);
+                            const float bv[4] = {bj.x, bj.y, bj.z, bj.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) m[4 * half + e] = cb[jt][e] * (upto * bv[e]);
+                        } else if (jt == w) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int tj = 16 * jt + 4 * g + e;
+                                const float v = cb[jt][e] *
+                                    (__builtin_amdgcn_exp2f((gi - sm.s.g[tj]) + (gir - sm.s.gr[tj])) * sm.s.dt[tj]);
+                                m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) m[4 * half + e] = 0.f;
+                        }
+                    }
+                    split2(m, m0[kb], m1[kb]);
+                }
+            }
+            // ---- outputs from the entering state, transposed: lane = token, entries 4
+            // neighbouring channels
+#pragma unroll
+            for (int it = 0; it < 4; ++it) y[it] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
                 float v[8];
@@ -292,19 +318,25 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
                     v[e] = S[2 * q][e];
                     v[4 + e] = S[2 * q + 1][e];
                 }
-                split2(v, sh[q], sl[q]);
+                s8 hi, lo;
+                split2(v, hi, lo);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const s8 cv = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
+                    y[it] = mfma16x16x32_bf16(hi, cv, y[it]);
+                    y[it] = mfma16x16x32_bf16(lo, cv, y[it]);
+                }
             }
-            f4 y[4];
+            lds_barrier();  // C is done with
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                if (2 * kb > w) break;
+                *reinterpret_cast<s8 *>(&sm.c[((w * 2 + kb) * 64 + lane) * 8]) = m0[kb];
+                *reinterpret_cast<s8 *>(&sm.c[(((4 + w) * 2 + kb) * 64 + lane) * 8]) = m1[kb];
+            }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                y[it] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < kQ; ++q) {
-                    const s8 cv = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
-                    y[it] = mfma16x16x32_bf16(sh[q], cv, y[it]);
-                    y[it] = mfma16x16x32_bf16(sl[q], cv, y[it]);
-                }
-                const float d = __builtin_amdgcn_exp2f(sm.g[16 * it + r]);
+                const float d = sm.s.from[16 * it + r];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[it][e] *= d;
             }
@@ -315,12 +347,12 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     if (2 * kb > it) break;
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((0 * 4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((1 * 4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.c[((it * 2 + kb) * 64 + lane) * 8]), y[it]);
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.c[(((4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
                 }
                 const int t = 16 * it + r;
                 if (t < rows)
-                    *reinterpret_cast<uint2 *>(orows + 16 * it * ostep + ooff) =
+                    *reinterpret_cast<uint2 *>(orows + (ooff + 16 * it * ostep)) =
                         make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
             }
         }
@@ -336,14 +368,13 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
         for (int kb = 0; kb < 2; ++kb) {
             float v[8];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+                const float *wp = kReverse ? sm.s.from : sm.s.w;
+                const float4 wj = *reinterpret_cast<const float4 *>(wp + 32 * kb + 16 * half + 4 * g);
+                const float wv[4] = {wj.x, wj.y, wj.z, wj.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tj = 32 * kb + 16 * half + 4 * g + e;
-                    const float wj = kReverse ? __builtin_amdgcn_exp2f(sm.g[tj])
-                                              : __builtin_amdgcn_exp2f((gl - sm.g[tj]) + (glr - sm.gr[tj])) * sm.dt[tj];
-                    v[4 * half + e] = wj * bf16_bits_to_f32((uint16_t)xf[kb][4 * half + e]);
-                }
+                for (int e = 0; e < 4; ++e) v[4 * half + e] = wv[e] * bf16_bits_to_f32((uint16_t)xf[kb][4 * half + e]);
+            }
             s8 x0, x1, x2;
             split3(v, x0, x1, x2);
 #pragma unroll
@@ -377,7 +408,10 @@ __global__ __launch_bounds__(kThreads, 2) void kda_ssm_chain_kernel(SsmChainArgs
 // The states entering the pieces of every sequence with several of them, in
 // place of the pieces' own states: E_0 = h0, E_{k+1} = 2^decay_k E_k + own_k (last
 // to first when reversed).  Sequences without tokens get their final state here.
-// One thread per 4 entries of a head's state.
+// One thread per 4 entries of a head's state; the loads of kBatch pieces are in
+// flight together, the sums wait for nothing else.
+constexpr int kBatch = 8;
+
 template <int kN, bool kReverse>
 __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) {
     const int64_t size = a.P * kN;
@@ -405,18 +439,30 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) 
                 for (int e = 0; e < 4; ++e) store_any(a.ht, nh * size + off + e, a.ht_f32, E[e]);
             continue;
         }
-        for (int64_t i = 0; i < count; ++i) {
-            const int64_t k = first + (kReverse ? count - 1 - i : i);
-            f4 *s = reinterpret_cast<f4 *>(a.state + (k * a.H + h) * size + off);
-            f4 own = {0.f, 0.f, 0.f, 0.f};
-            float d = 0.f;
-            if (i + 1 < count) {
-                own = *s;
-                d = __builtin_amdgcn_exp2f(a.decay[k * a.H + h]);
-            }
-            *s = E;
+        f4 *state = reinterpret_cast<f4 *>(a.state + h * size + off);
+        const int64_t step = a.H * size / 4;
+        for (int64_t i0 = 0; i0 < count; i0 += kBatch) {
+            f4 own[kBatch];
+            float d[kBatch];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) E[e] = d * E[e] + own[e];
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t k = first + (kReverse ? count - 1 - i0 - i : i0 + i);
+                own[i] = f4{0.f, 0.f, 0.f, 0.f};
+                d[i] = 0.f;
+                if (i0 + i + 1 < count) {
+                    own[i] = state[k * step];
+                    d[i] = a.decay[k * a.H + h];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t k = first + (kReverse ? count - 1 - i0 - i : i0 + i);
+                if (i0 + i >= count) break;
+                state[k * step] = E;
+                const float m = __builtin_amdgcn_exp2f(d[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) E[e] = m * E[e] + own[i][e];
+            }
         }
     }
 }

@@ -42,7 +42,7 @@ struct __align__(16) GradSmem {
     uint16_t x[kL * kXPitch], dy[kL * kXPitch];
     uint16_t m[2][kL * kMPitch], wm[2][kL * kMPitch];  // M and W, two parts, rows i
     uint16_t d[2][kPB * kPitch<kN>];                   // D, two parts, rows = channels
-    float g[kL], gr[kL], dt[kL];
+    Steps s;
     float colq[4][kL], rowe[2][kL], qd[kL], f[4][kL], rr[kN / 16][kL];
     float xs[kN / 16], dd[4];
 };
@@ -169,41 +169,45 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 ry.init(a.yt, kXPitch);
                 rx.load(xrow + h * a.P + pb * kPB, rows);
                 ry.load(yrow + h * a.P + pb * kPB, rows);
-                f4 D[kN / 32];
+                // D: a thread takes pairs of tiles of one 16-channel row, 8 neighbouring
+                // entries of one channel
+                constexpr int kPairs = kN / 64;
+                const int dq = w % kQ, dp = w / kQ;
+                f4 D[2 * kPairs];
 #pragma unroll
-                for (int i = 0; i < kN / 32; ++i) D[i] = ds[i * kThreads + threadIdx.x];
+                for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        D[2 * i + k] = ds[((dp + i * (kWaves / kQ)) * kTiles + 2 * dq + k) * 64 + lane];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) S[t] = hs[(t * kTiles + nt) * 64 + lane];
                 if (w == 0 && !more) {
                     raw = lane < rows ? bf16_bits_to_f32(a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h]) : 0.f;
-                    step_sizes(raw, lane < rows, bias, A * kLog2e, sm.g, sm.gr, sm.dt);
+                    step_sizes(raw, lane < rows, bias, A * kLog2e, sm.s);
                 }
                 rx.store(sm.x, kXPitch);
                 ry.store(sm.dy, kXPitch);
 #pragma unroll
-                for (int i = 0; i < kN / 32; ++i) {
-                    // tile t of the channels 16 p + r: entries 32 (t / 2) + 8 g + 4 (t % 2) ..
-                    const int tile = (i * kThreads + (int)threadIdx.x) >> 6, p = tile / kTiles, t = tile % kTiles;
-                    const int at = (16 * p + r) * kPitch<kN> + 32 * (t >> 1) + 8 * g + 4 * (t & 1);
-                    s4 hi, lo;
+                for (int i = 0; i < kPairs; ++i) {
+                    float v[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        short u, v;
-                        split_bf16(D[i][e], u, v);
-                        hi[e] = u;
-                        lo[e] = v;
+                        v[e] = D[2 * i][e];
+                        v[4 + e] = D[2 * i + 1][e];
                     }
-                    *reinterpret_cast<s4 *>(&sm.d[0][at]) = hi;
-                    *reinterpret_cast<s4 *>(&sm.d[1][at]) = lo;
+                    s8 hi, lo;
+                    split2(v, hi, lo);
+                    const int at = (16 * (dp + i * (kWaves / kQ)) + r) * kPitch<kN> + 32 * dq + 8 * g;
+                    *reinterpret_cast<s8 *>(&sm.d[0][at]) = hi;
+                    *reinterpret_cast<s8 *>(&sm.d[1][at]) = lo;
                 }
             }
             __syncthreads();
-            const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1];
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
-                const float gi = sm.g[ti], gir = sm.gr[ti];
+                const float gi = sm.s.g[ti], gir = sm.s.gr[ti];
                 float rowe = 0.f, dd = 0.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -215,11 +219,16 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                             xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kXPitch, q, g), along(sm.dy + ti * kXPitch, q, g), xd);
                     }
                     s4 m0, m1, w0, w1;
+                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.s.g[16 * jt + 4 * g]);
+                    const float4 rj = *reinterpret_cast<const float4 *>(&sm.s.gr[16 * jt + 4 * g]);
+                    const float4 dj = *reinterpret_cast<const float4 *>(&sm.s.dt[16 * jt + 4 * g]);
+                    const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, rv[4] = {rj.x, rj.y, rj.z, rj.w};
+                    const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int tj = 16 * jt + 4 * g + e;
-                        const float dtj = sm.dt[tj];
-                        const float l = tj <= ti ? __builtin_amdgcn_exp2f((gi - sm.g[tj]) + (gir - sm.gr[tj])) : 0.f;
+                        const float dtj = dv[e];
+                        const float l = tj <= ti ? __builtin_amdgcn_exp2f((gi - gv[e]) + (gir - rv[e])) : 0.f;
                         const float lc = tj <= ti ? l * cb[half][e] : 0.f;
                         const float wv = tj <= ti ? l * dtj * xd[e] : 0.f;
                         const float qv = tj < ti ? lc * xd[e] : 0.f;
@@ -272,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)xv[e]) * u[e];
                     f = rows_sum(f);
                     if (g == 0) add_to(&sm.f[pt][tj], f, more);
-                    const float wj = __builtin_amdgcn_exp2f((gl - sm.g[tj]) + (glr - sm.gr[tj])) * sm.dt[tj];
+                    const float wj = sm.s.w[tj];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) u[e] *= wj;
 #pragma unroll
@@ -334,9 +343,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)cv[e]) * v[e];
                     f = rows_sum(f);
                     if (g == 0) add_to(&sm.rr[nt][t], f, more);
-                    const float gt = sm.g[t];
-                    const float wt = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.gr[t])) * sm.dt[t];
-                    const float et = __builtin_amdgcn_exp2f(gt);
+                    const float wt = sm.s.w[t], et = sm.s.from[t];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         dB[j][e] += wt * u[e];
@@ -374,11 +381,11 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 rr += sm.rr[i][t];
                 xs += sm.xs[i];
             }
-            const float gl = sm.g[kL - 1], glr = sm.gr[kL - 1], gt = sm.g[t], dt = sm.dt[t];
+            const float gl = sm.s.g[kL - 1], glr = sm.s.gr[kL - 1], gt = sm.s.g[t], dt = sm.s.dt[t];
             const float rowe = sm.rowe[0][t] + (t >= 32 ? sm.rowe[1][t] : 0.f);
-            const float wd = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.gr[t]));
-            rr *= __builtin_amdgcn_exp2f(gt);
-            xs *= __builtin_amdgcn_exp2f(gl);
+            const float wd = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.s.gr[t]));
+            rr *= sm.s.from[t];
+            xs *= sm.s.from[kL - 1];
             const double z = (double)rr + ((double)rowe - (double)dt * (double)colq);
             const double F = (double)wd * (double)dt * (double)f;
             const double zi = wave_scan(z), fi = wave_scan(F);

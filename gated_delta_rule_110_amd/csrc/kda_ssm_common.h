@@ -11,10 +11,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-// LDS rows are padded: 64 bytes behind the N values of B and C, 32 behind the
-// 64 channels of x, so that the 16 rows (and 4-row groups of the transposing
-// read) of one access spread over the banks.
-template <int kN> constexpr int kPitch = kN + 32;
+// LDS rows are padded by 32 bytes, so that the 16 rows (and 4-row groups of the
+// transposing read) of one access spread over the banks.
+template <int kN> constexpr int kPitch = kN + 16;
 constexpr int kXPitch = kPB + 16;
 
 // The transposing read: within 16 lanes, lane l gives the address of 4 values
@@ -126,18 +125,29 @@ __device__ __forceinline__ double wave_scan(double v) {
     return v;
 }
 
-// The chunk's step sizes and running log-decays, by wave 0, lane = token.  The
-// sums run in 64 bits and are kept as a rounded value and its rest: decays
-// between neighbours far into a chunk are differences of large sums (hundreds,
-// where the steps are large), and would lose the low bits of fp32 otherwise.
-__device__ __forceinline__ void step_sizes(float raw, bool live, float bias, float nA2, float *g, float *gr, float *dts) {
+// The chunk's step sizes and running log-decays (base 2), by one wave, lane =
+// token.  The sums run in 64 bits and are kept as a rounded value and its rest:
+// decays between neighbours far into a chunk are differences of large sums
+// (hundreds, where the steps are large), and would lose the low bits of fp32.
+struct Steps {
+    float g[kL], gr[kL];          // log2 of the decay from the chunk's start: value and rest
+    float dt[kL];
+    float from[kL];               // the decay itself, from the chunk's start
+    float w[kL];                  // the decay to the chunk's end, times dt
+};
+__device__ __forceinline__ void step_sizes(float raw, bool live, float bias, float nA2, Steps &o) {
     const float dt = live ? softplus(raw + bias) : 0.f;
     const double s = wave_scan((double)nA2 * (double)dt);
     const int lane = threadIdx.x & 63;
     const float hi = (float)s;
-    g[lane] = hi;
-    gr[lane] = (float)(s - (double)hi);
-    dts[lane] = dt;
+    const uint64_t u = __builtin_bit_cast(uint64_t, s);
+    const uint64_t e = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    o.g[lane] = hi;
+    o.gr[lane] = (float)(s - (double)hi);
+    o.dt[lane] = dt;
+    o.from[lane] = __builtin_amdgcn_exp2f(hi);
+    o.w[lane] = __builtin_amdgcn_exp2f((float)(__builtin_bit_cast(double, e) - s)) * dt;
 }
 
 }  // namespace kda
