@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = 8;
-constexpr int kMPitch = kL + 16;
+constexpr int kMPitch = kL + 8;
 
 template <int kN>
 struct __align__(16) GradSmem {
@@ -152,57 +152,66 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 #pragma unroll
     for (int j = 0; j < kJ; ++j) dB[j] = dC[j] = f4{0.f, 0.f, 0.f, 0.f};
 
-    for (int64_t h = h0; h < h1; ++h) {
+    // The next head's (or channel block's) tensors are loaded while one is computed;
+    // barriers order LDS traffic only, so that the loads stay in flight across them.
+    constexpr int kPairs = kN / 64;              // pairs of D's tiles per thread, 8 neighbouring entries each
+    const int dq = w % kQ, dp = w / kQ;
+    const int units = (int)((h1 - h0) * pbs);
+    Rows<kPB, kThreads> rx, ry;
+    rx.init(a.xt, kXPitch);
+    ry.init(a.yt, kXPitch);
+    f4 D[2 * kPairs], Sn[4];
+    uint32_t rawn = 0;
+    auto fetch = [&](int u) {
+        const int64_t h = h0 + u / pbs, pb = u % pbs;
+        const int64_t unit = (chunk * a.H + h) * pbs + pb;
+        const f4 *hs = reinterpret_cast<const f4 *>(a.hs) + unit * (kPB * kN / 4);
+        const f4 *ds = reinterpret_cast<const f4 *>(a.ds) + unit * (kPB * kN / 4);
+        rx.load(xrow + h * a.P + pb * kPB, rows);
+        ry.load(yrow + h * a.P + pb * kPB, rows);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) D[2 * i + k] = ds[((dp + i * (kWaves / kQ)) * kTiles + 2 * dq + k) * 64 + lane];
+        // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
+#pragma unroll
+        for (int t = 0; t < 4; ++t) Sn[t] = hs[(t * kTiles + nt) * 64 + lane];
+        if (w == 0 && pb == 0) rawn = lane < rows ? a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h] : 0;
+    };
+    fetch(0);
+    float raw = 0.f;
+    for (int u = 0; u < units; ++u) {
+        const int64_t h = h0 + u / pbs, pb = u % pbs;
         const float A = -fast_exp(a.A_log[h]);
         const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         const float Dh = a.D ? a.D[h] : 0.f;
-        float raw = 0.f;
-        for (int64_t pb = 0; pb < pbs; ++pb) {
-            const bool more = pb > 0;            // sums over channels go on
-            const int64_t unit = (chunk * a.H + h) * pbs + pb;
-            const f4 *hs = reinterpret_cast<const f4 *>(a.hs) + unit * (kPB * kN / 4);
-            const f4 *ds = reinterpret_cast<const f4 *>(a.ds) + unit * (kPB * kN / 4);
-            f4 S[4];                             // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
-            {
-                Rows<kPB, kThreads> rx, ry;
-                rx.init(a.xt, kXPitch);
-                ry.init(a.yt, kXPitch);
-                rx.load(xrow + h * a.P + pb * kPB, rows);
-                ry.load(yrow + h * a.P + pb * kPB, rows);
-                // D: a thread takes pairs of tiles of one 16-channel row, 8 neighbouring
-                // entries of one channel
-                constexpr int kPairs = kN / 64;
-                const int dq = w % kQ, dp = w / kQ;
-                f4 D[2 * kPairs];
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        D[2 * i + k] = ds[((dp + i * (kWaves / kQ)) * kTiles + 2 * dq + k) * 64 + lane];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) S[t] = hs[(t * kTiles + nt) * 64 + lane];
-                if (w == 0 && !more) {
-                    raw = lane < rows ? bf16_bits_to_f32(a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h]) : 0.f;
-                    step_sizes(raw, lane < rows, bias, A * kLog2e, sm.s);
-                }
-                rx.store(sm.x, kXPitch);
-                ry.store(sm.dy, kXPitch);
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = D[2 * i][e];
-                        v[4 + e] = D[2 * i + 1][e];
-                    }
-                    s8 hi, lo;
-                    split2(v, hi, lo);
-                    const int at = (16 * (dp + i * (kWaves / kQ)) + r) * kPitch<kN> + 32 * dq + 8 * g;
-                    *reinterpret_cast<s8 *>(&sm.d[0][at]) = hi;
-                    *reinterpret_cast<s8 *>(&sm.d[1][at]) = lo;
-                }
+        const bool more = pb > 0;                // sums over channels go on
+        f4 S[4];
+        {
+            if (w == 0 && !more) {
+                raw = bf16_bits_to_f32(rawn);
+                step_sizes(raw, lane < rows, bias, A * kLog2e, sm.s);
             }
-            __syncthreads();
+            rx.store(sm.x, kXPitch);
+            ry.store(sm.dy, kXPitch);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = D[2 * i][e];
+                    v[4 + e] = D[2 * i + 1][e];
+                }
+                s8 hi, lo;
+                split2(v, hi, lo);
+                const int at = (16 * (dp + i * (kWaves / kQ)) + r) * kPitch<kN> + 32 * dq + 8 * g;
+                *reinterpret_cast<s8 *>(&sm.d[0][at]) = hi;
+                *reinterpret_cast<s8 *>(&sm.d[1][at]) = lo;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[t] = Sn[t];
+            lds_barrier();
+            if (u + 1 < units) fetch(u + 1);
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
             if (2 * kb <= it) {
@@ -260,7 +269,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     if (lane == 0) add_to(&sm.dd[it], dd, more);
                 }
             }
-            __syncthreads();
+            lds_barrier();
 
             // ---- dx, transposed: lane = token, entries 4 neighbouring channels
             {
@@ -364,11 +373,11 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     }
                 }
             }
-            __syncthreads();
+            lds_barrier();
         }
 
         // ---- step sizes and parameters, lane = token
-        if (w == 0) {
+        if (w == 0 && pb + 1 == pbs) {
             const int t = lane;
             float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
 #pragma unroll

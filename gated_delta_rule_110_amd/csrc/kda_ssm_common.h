@@ -11,10 +11,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-// LDS rows are padded by 32 bytes, so that the 16 rows (and 4-row groups of the
-// transposing read) of one access spread over the banks.
+// LDS rows are padded, so that the 16 rows (and 4-row groups of the transposing
+// read) of one access spread over the banks: by 32 bytes, rows of 64 values, which
+// are also read 8 bytes at a time, by 16.
 template <int kN> constexpr int kPitch = kN + 16;
-constexpr int kXPitch = kPB + 16;
+constexpr int kXPitch = kPB + 8;
 
 // The transposing read: within 16 lanes, lane l gives the address of 4 values
 // and receives, as entry e, value l % 4 of those that lane 4 e + l / 4 addressed.
