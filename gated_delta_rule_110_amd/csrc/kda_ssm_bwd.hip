@@ -36,15 +36,21 @@ constexpr int kThreads = 512;
 constexpr int kWaves = 8;
 constexpr int kMPitch = kL + 8;
 
+// A head's sums over channels and state entries, shares of its step sizes' gradient.
+template <int kN>
+struct Sums {
+    float colq[4][kL], rowe[2][kL], qd[kL], f[4][kL], rr[kN / 16][kL];
+    float xs[kN / 16], dd[4];
+};
+
 template <int kN>
 struct __align__(16) GradSmem {
     uint16_t b[kL * kPitch<kN>], c[kL * kPitch<kN>];
     uint16_t x[kL * kXPitch], dy[kL * kXPitch];
     uint16_t m[2][kL * kMPitch], wm[2][kL * kMPitch];  // M and W, two parts, rows i
     uint16_t d[2][kPB * kPitch<kN>];                   // D, two parts, rows = channels
-    Steps s;
-    float colq[4][kL], rowe[2][kL], qd[kL], f[4][kL], rr[kN / 16][kL];
-    float xs[kN / 16], dd[4];
+    Steps s[3];                                        // of the head before, this one and the next
+    Sums<kN> sum[2];                                   // of the head before and this one
 };
 
 // Operand fragments from LDS.  Along a row: 8 neighbouring entries, or in the
@@ -161,7 +167,6 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     rx.init(a.xt, kXPitch);
     ry.init(a.yt, kXPitch);
     f4 D[2 * kPairs], Sn[4];
-    uint32_t rawn = 0;
     auto fetch = [&](int u) {
         const int64_t h = h0 + u / pbs, pb = u % pbs;
         const int64_t unit = (chunk * a.H + h) * pbs + pb;
@@ -176,22 +181,70 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
 #pragma unroll
         for (int t = 0; t < 4; ++t) Sn[t] = hs[(t * kTiles + nt) * 64 + lane];
-        if (w == 0 && pb == 0) rawn = lane < rows ? a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h] : 0;
     };
+    // The work per token of a head, lane = token: its step sizes ahead of its
+    // turn, and the sums' gradients behind it, each by a wave that the 64 x 64
+    // products leave idle.
+    auto raw_dt = [&](int64_t h) -> uint32_t {
+        return h < h1 && lane < rows ? a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h] : 0;
+    };
+    auto steps_of = [&](int64_t h, uint32_t raw) {
+        step_sizes(bf16_bits_to_f32(raw), lane < rows, a.dt_bias ? a.dt_bias[h] : 0.f, -fast_exp(a.A_log[h]) * kLog2e,
+                   sm.s[(h - h0) % 3]);
+    };
+    auto finish = [&](int64_t h, uint32_t raw_bits) {
+        const Steps &st = sm.s[(h - h0) % 3];
+        const Sums<kN> &su = sm.sum[(h - h0) & 1];
+        const float A = -fast_exp(a.A_log[h]);
+        const float raw = bf16_bits_to_f32(raw_bits) + (a.dt_bias ? a.dt_bias[h] : 0.f);
+        const int t = lane;
+        float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= t >> 4) colq += su.colq[i][t];
+            f += su.f[i][t];
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            rr += su.rr[i][t];
+            xs += su.xs[i];
+        }
+        const float gl = st.g[kL - 1], glr = st.gr[kL - 1], dt = st.dt[t];
+        const float rowe = su.rowe[0][t] + (t >= 32 ? su.rowe[1][t] : 0.f);
+        const float wd = __builtin_amdgcn_exp2f((gl - st.g[t]) + (glr - st.gr[t]));
+        rr *= st.from[t];
+        xs *= st.from[kL - 1];
+        const double z = (double)rr + ((double)rowe - (double)dt * (double)colq);
+        const double F = (double)wd * (double)dt * (double)f;
+        const double zi = wave_scan(z), fi = wave_scan(F);
+        const double total = __shfl(zi, 63);
+        const float da = (float)((double)xs + (fi - F) + (total - zi + z));
+        const float ddt = A * da + (colq + su.qd[t]) + wd * f;
+        const float draw = t < rows ? ddt * sigmoid(raw) : 0.f;
+        if (t < rows) a.ddt[(trow + t) * a.H + h] = f32_to_bf16_bits(draw);
+        const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
+        if (lane == 0) {
+            float *o = a.psum + (chunk * a.H + h) * 4;
+            o[0] = dA;
+            o[1] = db;
+            o[2] = (su.dd[0] + su.dd[1]) + (su.dd[2] + su.dd[3]);
+        }
+    };
+    constexpr int kFinisher = 4, kStepper = 5;   // waves without a tile below the diagonal
+    uint32_t raw = 0;                            // finisher: of this head; stepper: of the next one
+    if (w == kStepper) {
+        steps_of(h0, raw_dt(h0));
+        raw = raw_dt(h0 + 1);
+    }
     fetch(0);
-    float raw = 0.f;
     for (int u = 0; u < units; ++u) {
         const int64_t h = h0 + u / pbs, pb = u % pbs;
-        const float A = -fast_exp(a.A_log[h]);
-        const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         const float Dh = a.D ? a.D[h] : 0.f;
         const bool more = pb > 0;                // sums over channels go on
+        const Steps &st = sm.s[(h - h0) % 3];
+        Sums<kN> &su = sm.sum[(h - h0) & 1];
         f4 S[4];
         {
-            if (w == 0 && !more) {
-                raw = bf16_bits_to_f32(rawn);
-                step_sizes(raw, lane < rows, bias, A * kLog2e, sm.s);
-            }
             rx.store(sm.x, kXPitch);
             ry.store(sm.dy, kXPitch);
 #pragma unroll
@@ -214,9 +267,17 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             if (u + 1 < units) fetch(u + 1);
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
+            if (w == kFinisher && !more) {
+                if (h > h0) finish(h - 1, raw);
+                raw = raw_dt(h);
+            }
+            if (w == kStepper && !more && h + 1 < h1) {
+                steps_of(h + 1, raw);
+                raw = raw_dt(h + 2);
+            }
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
-                const float gi = sm.s.g[ti], gir = sm.s.gr[ti];
+                const float gi = st.g[ti], gir = st.gr[ti];
                 float rowe = 0.f, dd = 0.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -228,9 +289,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                             xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kXPitch, q, g), along(sm.dy + ti * kXPitch, q, g), xd);
                     }
                     s4 m0, m1, w0, w1;
-                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.s.g[16 * jt + 4 * g]);
-                    const float4 rj = *reinterpret_cast<const float4 *>(&sm.s.gr[16 * jt + 4 * g]);
-                    const float4 dj = *reinterpret_cast<const float4 *>(&sm.s.dt[16 * jt + 4 * g]);
+                    const float4 gj = *reinterpret_cast<const float4 *>(&st.g[16 * jt + 4 * g]);
+                    const float4 rj = *reinterpret_cast<const float4 *>(&st.gr[16 * jt + 4 * g]);
+                    const float4 dj = *reinterpret_cast<const float4 *>(&st.dt[16 * jt + 4 * g]);
                     const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, rv[4] = {rj.x, rj.y, rj.z, rj.w};
                     const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
 #pragma unroll
@@ -244,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         rowe += qv * dtj;
                         if (tj == ti) {
                             dd += xd[e];
-                            add_to(&sm.qd[ti], lc * xd[e], more);
+                            add_to(&su.qd[ti], lc * xd[e], more);
                         }
                         short u, v;
                         split_bf16(lc * dtj + (tj == ti ? Dh : 0.f), u, v);
@@ -254,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         w0[e] = u;
                         w1[e] = v;
                         const float col = row16_sum(qv);
-                        if (r == 15 && jt <= it) add_to(&sm.colq[it][tj], col, more);
+                        if (r == 15 && jt <= it) add_to(&su.colq[it][tj], col, more);
                     }
                     const int at = ti * kMPitch + 16 * jt + 4 * g;
                     *reinterpret_cast<s4 *>(&sm.m[0][at]) = m0;
@@ -263,10 +324,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     *reinterpret_cast<s4 *>(&sm.wm[1][at]) = w1;
                 }
                 rowe = rows_sum(rowe);
-                if (g == 0) add_to(&sm.rowe[kb][ti], rowe, more);
+                if (g == 0) add_to(&su.rowe[kb][ti], rowe, more);
                 if (kb == it >> 1) {             // the wave with the diagonal tile
                     dd = wave_sum(dd);
-                    if (lane == 0) add_to(&sm.dd[it], dd, more);
+                    if (lane == 0) add_to(&su.dd[it], dd, more);
                 }
             }
             lds_barrier();
@@ -289,8 +350,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)xv[e]) * u[e];
                     f = rows_sum(f);
-                    if (g == 0) add_to(&sm.f[pt][tj], f, more);
-                    const float wj = sm.s.w[tj];
+                    if (g == 0) add_to(&su.f[pt][tj], f, more);
+                    const float wj = st.w[tj];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) u[e] *= wj;
 #pragma unroll
@@ -326,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) + bf16_bits_to_f32((uint16_t)Dv[1][q][e]));
                 }
                 xs = wave_sum(xs);
-                if (lane == 0 && j0 == 0) add_to(&sm.xs[nt], xs, more);
+                if (lane == 0 && j0 == 0) add_to(&su.xs[nt], xs, more);
                 s8 Ct[2], Bt[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -351,8 +412,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)cv[e]) * v[e];
                     f = rows_sum(f);
-                    if (g == 0) add_to(&sm.rr[nt][t], f, more);
-                    const float wt = sm.s.w[t], et = sm.s.from[t];
+                    if (g == 0) add_to(&su.rr[nt][t], f, more);
+                    const float wt = st.w[t], et = st.from[t];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         dB[j][e] += wt * u[e];
@@ -375,43 +436,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             }
             lds_barrier();
         }
-
-        // ---- step sizes and parameters, lane = token
-        if (w == 0 && pb + 1 == pbs) {
-            const int t = lane;
-            float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i >= t >> 4) colq += sm.colq[i][t];
-                f += sm.f[i][t];
-            }
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                rr += sm.rr[i][t];
-                xs += sm.xs[i];
-            }
-            const float gl = sm.s.g[kL - 1], glr = sm.s.gr[kL - 1], gt = sm.s.g[t], dt = sm.s.dt[t];
-            const float rowe = sm.rowe[0][t] + (t >= 32 ? sm.rowe[1][t] : 0.f);
-            const float wd = __builtin_amdgcn_exp2f((gl - gt) + (glr - sm.s.gr[t]));
-            rr *= sm.s.from[t];
-            xs *= sm.s.from[kL - 1];
-            const double z = (double)rr + ((double)rowe - (double)dt * (double)colq);
-            const double F = (double)wd * (double)dt * (double)f;
-            const double zi = wave_scan(z), fi = wave_scan(F);
-            const double total = __shfl(zi, 63);
-            const float da = (float)((double)xs + (fi - F) + (total - zi + z));
-            const float ddt = A * da + (colq + sm.qd[t]) + wd * f;
-            const float draw = t < rows ? ddt * sigmoid(raw + bias) : 0.f;
-            if (t < rows) a.ddt[(trow + t) * a.H + h] = f32_to_bf16_bits(draw);
-            const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
-            if (lane == 0) {
-                float *o = a.psum + (chunk * a.H + h) * 4;
-                o[0] = dA;
-                o[1] = db;
-                o[2] = (sm.dd[0] + sm.dd[1]) + (sm.dd[2] + sm.dd[3]);
-            }
-        }
     }
+    if (w == kFinisher) finish(h1 - 1, raw);
 
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
