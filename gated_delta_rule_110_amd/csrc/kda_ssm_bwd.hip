@@ -73,17 +73,18 @@ __device__ __forceinline__ float row16_sum(float v) {
     v += dpp_row_shr_zero(v, 1);
     return v;
 }
-// Sum over the four 16-lane rows, in every lane.
+// Sum over the four 16-lane rows, in every lane: the halves, then the rows, of
+// the wave exchanged (lane moves only, no LDS).
 __device__ __forceinline__ float rows_sum(float v) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
+    const uint32_t u = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float s = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    const uint32_t x = __float_as_uint(s);
+    const auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-    return v;
-}
+// Sum over the wave, in the last lane of every row.
+__device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
 __device__ __forceinline__ void add_to(float *p, float v, bool more) { *p = more ? *p + v : v; }
 
 // Tokens of chunk number i of the batch.
@@ -127,10 +128,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int it = w & 3, kb = w >> 2;           // this wave's tiles of the 64 x 64 products
     const int nt = w % kTiles, j0 = w / kTiles * kJ;
-    const int64_t heads = a.H / a.G;             // of the group
-    const int64_t h0 = grp * heads + (int64_t)share * a.share;
-    const int64_t h1 = (share + 1) * (int64_t)a.share < heads ? h0 + a.share : grp * heads + heads;
-    const int64_t pbs = a.P / kPB;
+    const int H = (int)a.H, heads = H / (int)a.G;  // of the group
+    const int h0 = (int)grp * heads + share * a.share;
+    const int count = heads - share * a.share < a.share ? heads - share * a.share : a.share;
+    const int pbs = a.P == 2 * kPB ? 2 : 1, shift = pbs - 1;
     const uint16_t *xrow = a.x + ck.row0 * a.xb + ck.t0 * a.xt;
     const uint16_t *yrow = a.dy + ck.row0 * a.yb + ck.t0 * a.yt;
     const int64_t trow = ck.row0 * a.T + ck.t0;  // row of the contiguous outputs
@@ -162,18 +163,18 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     // barriers order LDS traffic only, so that the loads stay in flight across them.
     constexpr int kPairs = kN / 64;              // pairs of D's tiles per thread, 8 neighbouring entries each
     const int dq = w % kQ, dp = w / kQ;
-    const int units = (int)((h1 - h0) * pbs);
+    const int units = count << shift;
     Rows<kPB, kThreads> rx, ry;
     rx.init(a.xt, kXPitch);
     ry.init(a.yt, kXPitch);
     f4 D[2 * kPairs], Sn[4];
     auto fetch = [&](int u) {
-        const int64_t h = h0 + u / pbs, pb = u % pbs;
-        const int64_t unit = (chunk * a.H + h) * pbs + pb;
+        const int h = h0 + (u >> shift), pb = u & shift;
+        const int64_t unit = ((chunk * H + h) << shift) + pb;
         const f4 *hs = reinterpret_cast<const f4 *>(a.hs) + unit * (kPB * kN / 4);
         const f4 *ds = reinterpret_cast<const f4 *>(a.ds) + unit * (kPB * kN / 4);
-        rx.load(xrow + h * a.P + pb * kPB, rows);
-        ry.load(yrow + h * a.P + pb * kPB, rows);
+        rx.load(xrow + ((h << shift) + pb) * kPB, rows);
+        ry.load(yrow + ((h << shift) + pb) * kPB, rows);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i)
 #pragma unroll
@@ -185,18 +186,27 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     // The work per token of a head, lane = token: its step sizes ahead of its
     // turn, and the sums' gradients behind it, each by a wave that the 64 x 64
     // products leave idle.
-    auto raw_dt = [&](int64_t h) -> uint32_t {
-        return h < h1 && lane < rows ? a.dt[ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h] : 0;
+    // Head number i of the share: what these need from memory, loaded a head ahead.
+    struct Head {
+        uint32_t raw;
+        float A_log, bias;
     };
-    auto steps_of = [&](int64_t h, uint32_t raw) {
-        step_sizes(bf16_bits_to_f32(raw), lane < rows, a.dt_bias ? a.dt_bias[h] : 0.f, -fast_exp(a.A_log[h]) * kLog2e,
-                   sm.s[(h - h0) % 3]);
+    const uint16_t *drow = a.dt + ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h0;
+    auto head = [&](int i) -> Head {
+        Head o{0, 0.f, 0.f};
+        if (i < count) {
+            if (lane < rows) o.raw = drow[i];
+            o.A_log = a.A_log[h0 + i];
+            if (a.dt_bias) o.bias = a.dt_bias[h0 + i];
+        }
+        return o;
     };
-    auto finish = [&](int64_t h, uint32_t raw_bits) {
-        const Steps &st = sm.s[(h - h0) % 3];
-        const Sums<kN> &su = sm.sum[(h - h0) & 1];
-        const float A = -fast_exp(a.A_log[h]);
-        const float raw = bf16_bits_to_f32(raw_bits) + (a.dt_bias ? a.dt_bias[h] : 0.f);
+    auto steps_of = [&](const Head &o, Steps &to) {
+        step_sizes(bf16_bits_to_f32(o.raw), lane < rows, o.bias, -fast_exp(o.A_log) * kLog2e, to);
+    };
+    auto finish = [&](int i, const Head &o, const Steps &st, const Sums<kN> &su) {
+        const float A = -fast_exp(o.A_log);
+        const float raw = bf16_bits_to_f32(o.raw) + o.bias;
         const int t = lane;
         float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
 #pragma unroll
@@ -221,28 +231,30 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         const float da = (float)((double)xs + (fi - F) + (total - zi + z));
         const float ddt = A * da + (colq + su.qd[t]) + wd * f;
         const float draw = t < rows ? ddt * sigmoid(raw) : 0.f;
-        if (t < rows) a.ddt[(trow + t) * a.H + h] = f32_to_bf16_bits(draw);
+        if (t < rows) a.ddt[(trow + t) * H + h0 + i] = f32_to_bf16_bits(draw);
         const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
-        if (lane == 0) {
-            float *o = a.psum + (chunk * a.H + h) * 4;
-            o[0] = dA;
-            o[1] = db;
-            o[2] = (su.dd[0] + su.dd[1]) + (su.dd[2] + su.dd[3]);
+        if (lane == 63) {
+            float *p = a.psum + (chunk * H + h0 + i) * 4;
+            p[0] = dA;
+            p[1] = db;
+            p[2] = (su.dd[0] + su.dd[1]) + (su.dd[2] + su.dd[3]);
         }
     };
     constexpr int kFinisher = 4, kStepper = 5;   // waves without a tile below the diagonal
-    uint32_t raw = 0;                            // finisher: of this head; stepper: of the next one
+    Head own{0, 0.f, 0.f};                       // finisher: this head; stepper: the next one
     if (w == kStepper) {
-        steps_of(h0, raw_dt(h0));
-        raw = raw_dt(h0 + 1);
+        steps_of(head(0), sm.s[0]);
+        own = head(1);
     }
     fetch(0);
+    int slot = 0;                                // of this head's step sizes
     for (int u = 0; u < units; ++u) {
-        const int64_t h = h0 + u / pbs, pb = u % pbs;
+        const int i = u >> shift, h = h0 + i, pb = u & shift;
         const float Dh = a.D ? a.D[h] : 0.f;
         const bool more = pb > 0;                // sums over channels go on
-        const Steps &st = sm.s[(h - h0) % 3];
-        Sums<kN> &su = sm.sum[(h - h0) & 1];
+        if (u > 0 && !more) slot = slot == 2 ? 0 : slot + 1;
+        const Steps &st = sm.s[slot];
+        Sums<kN> &su = sm.sum[i & 1];
         f4 S[4];
         {
             rx.store(sm.x, kXPitch);
@@ -268,12 +280,12 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
             if (w == kFinisher && !more) {
-                if (h > h0) finish(h - 1, raw);
-                raw = raw_dt(h);
+                if (i > 0) finish(i - 1, own, sm.s[slot == 0 ? 2 : slot - 1], sm.sum[(i - 1) & 1]);
+                own = head(i);
             }
-            if (w == kStepper && !more && h + 1 < h1) {
-                steps_of(h + 1, raw);
-                raw = raw_dt(h + 2);
+            if (w == kStepper && !more && i + 1 < count) {
+                steps_of(own, sm.s[slot == 2 ? 0 : slot + 1]);
+                own = head(i + 2);
             }
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
@@ -327,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 if (g == 0) add_to(&su.rowe[kb][ti], rowe, more);
                 if (kb == it >> 1) {             // the wave with the diagonal tile
                     dd = wave_sum(dd);
-                    if (lane == 0) add_to(&su.dd[it], dd, more);
+                    if (lane == 63) add_to(&su.dd[it], dd, more);
                 }
             }
             lds_barrier();
@@ -362,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         u = mfma16x16x32_bf16(yv, across(sm.m[1], kMPitch, q, 16 * jt, r, g), u);
                     }
                     if (tj < rows)
-                        *reinterpret_cast<uint2 *>(a.dx + ((trow + tj) * a.H + h) * a.P + pb * kPB + 16 * pt + 4 * g) =
+                        *reinterpret_cast<uint2 *>(a.dx + ((((trow + tj) * H + h) << shift) + pb) * kPB + 16 * pt + 4 * g) =
                             make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
                 }
             }
@@ -387,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) + bf16_bits_to_f32((uint16_t)Dv[1][q][e]));
                 }
                 xs = wave_sum(xs);
-                if (lane == 0 && j0 == 0) add_to(&su.xs[nt], xs, more);
+                if (lane == 63 && j0 == 0) add_to(&su.xs[nt], xs, more);
                 s8 Ct[2], Bt[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -437,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             lds_barrier();
         }
     }
-    if (w == kFinisher) finish(h1 - 1, raw);
+    if (w == kFinisher) finish(count - 1, own, sm.s[slot], sm.sum[(count - 1) & 1]);
 
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
