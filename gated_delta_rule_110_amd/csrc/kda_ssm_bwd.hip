@@ -34,7 +34,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = 8;
-constexpr int kMPitch = kL + 8;
+// Rows of x, d_out and W are read 8 bytes at a time as well as transposed: 16
+// bytes of padding serve the former; M is only read transposed.
+constexpr int kRowPitch = kL + 8;
+constexpr int kMPitch = kL + 16;
 
 // A head's sums over channels and state entries, shares of its step sizes' gradient.
 template <int kN>
@@ -46,8 +49,8 @@ struct Sums {
 template <int kN>
 struct __align__(16) GradSmem {
     uint16_t b[kL * kPitch<kN>], c[kL * kPitch<kN>];
-    uint16_t x[kL * kXPitch], dy[kL * kXPitch];
-    uint16_t m[2][kL * kMPitch], wm[2][kL * kMPitch];  // M and W, two parts, rows i
+    uint16_t x[kL * kRowPitch], dy[kL * kRowPitch];
+    uint16_t m[2][kL * kMPitch], wm[2][kL * kRowPitch]; // M and W, two parts, rows i
     uint16_t d[2][kPB * kPitch<kN>];                   // D, two parts, rows = channels
     Steps s[3];                                        // of the head before, this one and the next
     Sums<kN> sum[2];                                   // of the head before and this one
@@ -165,8 +168,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     const int dq = w % kQ, dp = w / kQ;
     const int units = count << shift;
     Rows<kPB, kThreads> rx, ry;
-    rx.init(a.xt, kXPitch);
-    ry.init(a.yt, kXPitch);
+    rx.init(a.xt, kRowPitch);
+    ry.init(a.yt, kRowPitch);
     f4 D[2 * kPairs], Sn[4];
     auto fetch = [&](int u) {
         const int h = h0 + (u >> shift), pb = u & shift;
@@ -257,8 +260,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         Sums<kN> &su = sm.sum[i & 1];
         f4 S[4];
         {
-            rx.store(sm.x, kXPitch);
-            ry.store(sm.dy, kXPitch);
+            rx.store(sm.x, kRowPitch);
+            ry.store(sm.dy, kRowPitch);
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
                 float v[8];
@@ -298,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     if (jt <= it) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kXPitch, q, g), along(sm.dy + ti * kXPitch, q, g), xd);
+                            xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kRowPitch, q, g), along(sm.dy + ti * kRowPitch, q, g), xd);
                     }
                     s4 m0, m1, w0, w1;
                     const float4 gj = *reinterpret_cast<const float4 *>(&st.g[16 * jt + 4 * g]);
@@ -329,11 +332,11 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         const float col = row16_sum(qv);
                         if (r == 15 && jt <= it) add_to(&su.colq[it][tj], col, more);
                     }
-                    const int at = ti * kMPitch + 16 * jt + 4 * g;
+                    const int at = ti * kMPitch + 16 * jt + 4 * g, wat = ti * kRowPitch + 16 * jt + 4 * g;
                     *reinterpret_cast<s4 *>(&sm.m[0][at]) = m0;
                     *reinterpret_cast<s4 *>(&sm.m[1][at]) = m1;
-                    *reinterpret_cast<s4 *>(&sm.wm[0][at]) = w0;
-                    *reinterpret_cast<s4 *>(&sm.wm[1][at]) = w1;
+                    *reinterpret_cast<s4 *>(&sm.wm[0][wat]) = w0;
+                    *reinterpret_cast<s4 *>(&sm.wm[1][wat]) = w1;
                 }
                 rowe = rows_sum(rowe);
                 if (g == 0) add_to(&su.rowe[kb][ti], rowe, more);
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         u = mfma16x16x32_bf16(along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
                         u = mfma16x16x32_bf16(along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
                     }
-                    const s4 xv = *reinterpret_cast<const s4 *>(sm.x + tj * kXPitch + 16 * pt + 4 * g);
+                    const s4 xv = *reinterpret_cast<const s4 *>(sm.x + tj * kRowPitch + 16 * pt + 4 * g);
                     float f = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)xv[e]) * u[e];
@@ -369,7 +372,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if (q < half) continue;  // i before j
-                        const s8 yv = across(sm.dy, kXPitch, q, 16 * pt, r, g);
+                        const s8 yv = across(sm.dy, kRowPitch, q, 16 * pt, r, g);
                         u = mfma16x16x32_bf16(yv, across(sm.m[0], kMPitch, q, 16 * jt, r, g), u);
                         u = mfma16x16x32_bf16(yv, across(sm.m[1], kMPitch, q, 16 * jt, r, g), u);
                     }
@@ -412,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     f4 u = {0.f, 0.f, 0.f, 0.f}, v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const s8 xv = along_pair(sm.x + t * kXPitch, q, g), yv = along_pair(sm.dy + t * kXPitch, q, g);
+                        const s8 xv = along_pair(sm.x + t * kRowPitch, q, g), yv = along_pair(sm.dy + t * kRowPitch, q, g);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             u = mfma16x16x32_bf16(Dv[k][q], xv, u);
@@ -436,12 +439,12 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         if (2 * q + 1 >= tt) {   // i from token tile tt on
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                dB[j] = mfma16x16x32_bf16(Ct[q], across(sm.wm[k], kMPitch, q, 16 * tt, r, g), dB[j]);
+                                dB[j] = mfma16x16x32_bf16(Ct[q], across(sm.wm[k], kRowPitch, q, 16 * tt, r, g), dB[j]);
                         }
                         if (2 * q <= tt) {       // j up to it
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                dC[j] = mfma16x16x32_bf16(Bt[q], along_pair(sm.wm[k] + t * kMPitch, q, g), dC[j]);
+                                dC[j] = mfma16x16x32_bf16(Bt[q], along_pair(sm.wm[k] + t * kRowPitch, q, g), dC[j]);
                         }
                     }
                 }
@@ -468,21 +471,26 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     }
 }
 
-// dB and dC from the shares, in order: one workgroup per chunk and group.
+// dB and dC from the shares, in order: kJoin workgroups per chunk and group, for
+// dB (the first half of them) and dC.
+constexpr int kJoin = 8;
+
 template <int kN>
 __global__ __launch_bounds__(256) void kda_ssm_grad_join_kernel(SsmGradArgs a) {
-    const int64_t chunk = blockIdx.x / a.G, grp = blockIdx.x - chunk * a.G;
+    const int64_t block = blockIdx.x / kJoin;
+    const int64_t chunk = block / a.G, grp = block - chunk * a.G;
     Chunk ck;
     if (chunk >= a.chunks || !chunk_of(a, chunk, ck)) return;
+    const int part = blockIdx.x % kJoin, which = part / (kJoin / 2);
     const int64_t one = a.chunks * a.G * kL * kN;
-    for (int i = threadIdx.x; i < 2 * ck.rows * kN / 4; i += 256) {
-        const int which = i / (ck.rows * kN / 4), at = i - which * (ck.rows * kN / 4);
-        const int t = at / (kN / 4), n = 4 * (at % (kN / 4));
-        const float *src = a.part + which * a.shares * one + ((chunk * a.G + grp) * kL + t) * kN + n;
+    const float *from = a.part + which * a.shares * one + (chunk * a.G + grp) * kL * kN;
+    uint16_t *to = (which ? a.dC : a.dB) + ((ck.row0 * a.T + ck.t0) * a.G + grp) * kN;
+    for (int i = (part % (kJoin / 2)) * 256 + threadIdx.x; i < ck.rows * kN / 4; i += kJoin / 2 * 256) {
+        const int t = i / (kN / 4), n = 4 * (i % (kN / 4));
+        const float *src = from + t * kN + n;
         f4 v = *reinterpret_cast<const f4 *>(src);
         for (int s = 1; s < a.shares; ++s) v += *reinterpret_cast<const f4 *>(src + s * one);
-        uint16_t *dst = (which ? a.dC : a.dB) + ((ck.row0 * a.T + ck.t0 + t) * a.G + grp) * kN + n;
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        *reinterpret_cast<uint2 *>(to + t * a.G * kN + n) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
     }
 }
 
@@ -516,7 +524,7 @@ hipError_t launch(const SsmGradArgs &a, hipStream_t s) {
     if (a.chunks > 0 && a.T > 0) {
         hipLaunchKernelGGL((kda_ssm_grad_kernel<kN>), dim3((unsigned)(a.chunks * a.G * a.shares)), dim3(kThreads), 0, s, a);
         if (a.shares > 1)
-            hipLaunchKernelGGL((kda_ssm_grad_join_kernel<kN>), dim3((unsigned)(a.chunks * a.G)), dim3(256), 0, s, a);
+            hipLaunchKernelGGL((kda_ssm_grad_join_kernel<kN>), dim3((unsigned)(a.chunks * a.G * kJoin)), dim3(256), 0, s, a);
     }
     hipLaunchKernelGGL(kda_ssm_grad_params_kernel, dim3((unsigned)a.H), dim3(256), 0, s, a);
     return hipGetLastError();

@@ -11,11 +11,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-// LDS rows are padded, so that the 16 rows (and 4-row groups of the transposing
-// read) of one access spread over the banks: by 32 bytes, rows of 64 values, which
-// are also read 8 bytes at a time, by 16.
+// LDS rows are padded by 32 bytes, so that the 16 rows (and the 8-row groups of
+// the transposing read) of one access spread over the banks.
 template <int kN> constexpr int kPitch = kN + 16;
-constexpr int kXPitch = kPB + 8;
+constexpr int kXPitch = kPB + 16;
 
 // The transposing read: within 16 lanes, lane l gives the address of 4 values
 // and receives, as entry e, value l % 4 of those that lane 4 e + l / 4 addressed.
@@ -43,8 +42,9 @@ struct Rows {
     int64_t step;                                        // bytes between the passes
     int r, lds;
     __device__ __forceinline__ void init(int64_t stride, int pitch) {
-        const int c = threadIdx.x % (kCols / 8);
-        r = threadIdx.x / (kCols / 8);
+        const int thread = threadIdx.x % kThreads;       // larger workgroups: a set of rows per kThreads of them
+        const int c = thread % (kCols / 8);
+        r = thread / (kCols / 8);
         off = ((uint32_t)r * (uint32_t)stride + 8 * c) * 2;
         step = kPer * stride * 2;
         lds = r * pitch + 8 * c;
