@@ -40,6 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kPieces = 0;    // from zero: the piece's own state and its decay
 constexpr int kOutputs = 1;   // outputs and final states
 constexpr int kSave = 2;      // the state entering every chunk, for the gradient
+constexpr int kStepper = 3;   // the wave that takes the step sizes
 
 // One piece: its sequence, tokens and place.
 struct Piece {
@@ -93,17 +94,17 @@ __device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int
 }
 int64_t grid_size(const SsmChainArgs &a) { return (a.pieces + 7) / 8 * 8 * a.H * (a.P / kPB); }
 
-constexpr int kMEntries = 2 * 4 * 2 * 64 * 8;
+// M's 16 x 32 units, (row tile, half of the columns), by the wave that computes
+// them: at most 3 of the 10 tiles on or below the diagonal each.
 
 template <int kN, bool kOut>
 struct __align__(16) ChainSmem {
     uint16_t k[kL * kPitch<kN>];
-    // C; then, when every wave is done with it, M in two parts as operands:
-    // [part][row tile][k block][lane][8]
-    uint16_t c[kOut ? (kL * kPitch<kN> > kMEntries ? kL * kPitch<kN> : kMEntries) : 8];
+    uint16_t c[kOut ? kL * kPitch<kN> : 8];
     uint16_t x[kL * kXPitch];
-    Steps s;
-    float before[kOut ? 4 : 1][kL];             // decay from token j to the start of a row tile, times dt_j
+    uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
+    Steps s[2];                                 // of this chunk and the next
+    float before[kOut ? 8 : 1][kL];             // by unit: decay from token j to the start of the row tile, times dt_j
 };
 
 // LDS written by a wave's lanes is read by others of the same wave: a wave's LDS
@@ -164,6 +165,33 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     const int64_t sbase = (h * a.P + pb * kPB + 16 * w + r) * kN + 8 * g;
     const int64_t sseq = p.n * a.H * a.P * kN + sbase, spiece = p.index * a.H * a.P * kN + sbase;
 
+    const int chunks = (p.count + kL - 1) / kL;
+    Rows<kN, kThreads> rk, rc;
+    Rows<kPB, kThreads> rx;
+    rk.init(a.kt, kPitch<kN>);
+    if constexpr (kOut) rc.init(a.ct, kPitch<kN>);
+    rx.init(a.xt, kXPitch);
+    const uint32_t doff = (uint32_t)lane * (uint32_t)a.dtt * 2;
+    // byte offset of this lane's output: token lane % 16, 4 channels
+    const uint32_t ostep = (uint32_t)(a.H * a.P) * 2;
+    const uint32_t ooff = (uint32_t)r * ostep + (16 * w + 4 * g) * 2;
+    uint32_t rdt = 0;
+    // step sizes of the piece's chunk c, as loaded: used, and so waited for, later
+    auto raw_dt = [&](int c) -> uint32_t {
+        if (c >= chunks || lane >= p.count - c * kL) return 0;
+        return *reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + (int64_t)c * kL * a.dtt) + doff);
+    };
+    auto fetch = [&](int i) {
+        const int c = kReverse ? chunks - 1 - i : i;
+        const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
+        const int64_t t = (int64_t)c * kL;
+        if (!kOut && w == kStepper) rdt = raw_dt(c);
+        rx.load(xrow + t * a.xt, rows);
+        rk.load(krow + t * a.kt, rows);
+        if constexpr (kOut) rc.load(crow + t * a.ct, rows);
+    };
+    fetch(0);
+
     // ---- the state at the start
     f4 S[kTiles];
 #pragma unroll
@@ -195,36 +223,38 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
     }
 
-    const int chunks = (p.count + kL - 1) / kL;
-    Rows<kN, kThreads> rk, rc;
-    Rows<kPB, kThreads> rx;
-    rk.init(a.kt, kPitch<kN>);
-    if constexpr (kOut) rc.init(a.ct, kPitch<kN>);
-    rx.init(a.xt, kXPitch);
-    const uint32_t doff = (uint32_t)lane * (uint32_t)a.dtt * 2;
-    // byte offset of this lane's output: token lane % 16, 4 channels
-    const uint32_t ostep = (uint32_t)(a.H * a.P) * 2;
-    const uint32_t ooff = (uint32_t)r * ostep + (16 * w + 4 * g) * 2;
-    uint32_t rdt = 0;            // as loaded: used, and so waited for, only when its chunk begins
-    auto fetch = [&](int i) {
-        const int c = kReverse ? chunks - 1 - i : i;
-        const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
-        const int64_t t = (int64_t)c * kL;
-        if (w == 0) {
-            rdt = 0;
-            if (lane < rows)
-                rdt = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + t * a.dtt) + doff);
-        }
-        rx.load(xrow + t * a.xt, rows);
-        rk.load(krow + t * a.kt, rows);
-        if constexpr (kOut) rc.load(crow + t * a.ct, rows);
+    // The outputs of the chunk before: token 16 it + r, 4 channels.
+    uint2 out[4];
+    char *oput = reinterpret_cast<char *>(orow);
+    auto put = [&](int rows) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+            if (16 * it + r < rows) *reinterpret_cast<uint2 *>(oput + (ooff + 16 * it * ostep)) = out[it];
+        oput += (int64_t)kL * ostep;
     };
-    fetch(0);
+    const int u0 = w < 2 ? 3 : w == 2 ? 2 : 1, k0 = w == 1, u1 = w == 0 ? 0 : w == 1 ? 2 : -1, k1 = w == 1;
     float total = 0.f;
+    // Outputs: the next chunk's step sizes are taken beside this one's M, by a wave
+    // with few of its tiles.
+    if (kOut && w == kStepper) {
+        step_sizes(bf16_bits_to_f32(raw_dt(0)), lane < p.count, bias, nA2, sm.s[0]);
+        rdt = raw_dt(1);
+    }
     // Barriers here order LDS traffic only: the next chunk's loads stay in flight.
     for (int i = 0; i < chunks; ++i) {
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
+        const bool leave = kPass == kSave && i + 1 == chunks && !(kReverse && p.first && a.ht);
+        if (i && !leave) lds_barrier();  // the chunk before is done with
+        if (!leave) {
+            if (!kOut && w == kStepper) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s[i & 1]);
+            rx.store(sm.x, kXPitch);
+            rk.store(sm.k, kPitch<kN>);
+            if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
+            lds_barrier();
+        }
+        // What goes to memory goes out here, behind the wait for this chunk's loads and
+        // before the next one's: the next wait, which counts both, comes a chunk later.
         if constexpr (kPass == kSave) {
             if (p.chunk0 + c < a.chunks) {
                 f4 *dst = reinterpret_cast<f4 *>(a.save) +
@@ -232,16 +262,14 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) dst[t * 64] = S[t];
             }
-            if (i + 1 == chunks && !(kReverse && p.first && a.ht)) break;  // what leaves the piece is not needed
+            if (leave) break;            // what leaves the piece is not needed
         }
-        if (i) lds_barrier();  // the chunk before is done with
-        if (w == 0) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s);
-        rx.store(sm.x, kXPitch);
-        rk.store(sm.k, kPitch<kN>);
-        if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
-        lds_barrier();
+        if constexpr (kOut) {
+            if (i > 0) put(kL);
+        }
         if (i + 1 < chunks) fetch(i + 1);
-        const float gl = sm.s.g[kL - 1];
+        const Steps &st = sm.s[i & 1];
+        const float gl = st.g[kL - 1];
 
         // x along tokens, for this wave's channels
         s8 xf[2];
@@ -253,59 +281,62 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 
         f4 y[4];
         if constexpr (kOut) {
-            // ---- M for the token rows 16 w .. 16 w + 15, as B C^T: lane = row i, its
-            // entries the columns j that an operand holds.  Tiles left of the diagonal
-            // take their decays as a product around the tile's first row, both factors
-            // at most 1; the diagonal tile takes the exponentials themselves.
-            const int ti = 16 * w + r;
-            const float gi = sm.s.g[ti], gir = sm.s.gr[ti];
-            float upto = 1.f;
-            if (w > 0) {
-                const float g0 = sm.s.g[16 * w - 1], g0r = sm.s.gr[16 * w - 1];
-                sm.before[w][lane] = __builtin_amdgcn_exp2f((g0 - sm.s.g[lane]) + (g0r - sm.s.gr[lane])) * sm.s.dt[lane];
-                upto = __builtin_amdgcn_exp2f((gi - g0) + (gir - g0r));
-                wave_sync();
-            }
-            s8 m0[2], m1[2];
-            {
-                f4 cb[4];
-#pragma unroll
-                for (int jt = 0; jt < 4; ++jt) cb[jt] = f4{0.f, 0.f, 0.f, 0.f};
+            // ---- M, unit by unit, as B C^T: lane = row i, its entries the columns j that an
+            // operand holds.  Tiles left of the diagonal take their decays as a product
+            // around the tile's first row, both factors at most 1; the diagonal tile
+            // takes the exponentials themselves.
+            auto unit = [&](const int it, const int kb, float *before) {
+                const int ti = 16 * it + r;
+                const float gi = st.g[ti], gir = st.gr[ti];
+                float upto = 1.f;
+                if (it > 0) {
+                    const float g0 = st.g[16 * it - 1], g0r = st.gr[16 * it - 1];
+                    before[lane] = __builtin_amdgcn_exp2f((g0 - st.g[lane]) + (g0r - st.gr[lane])) * st.dt[lane];
+                    upto = __builtin_amdgcn_exp2f((gi - g0) + (gir - g0r));
+                    wave_sync();
+                }
+                f4 cb[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                const bool two = 2 * kb < it;
 #pragma unroll
                 for (int q = 0; q < kQ; ++q) {
                     const s8 cv = lds8(sm.c + ti * kPitch<kN> + 32 * q + 8 * g);
-#pragma unroll
-                    for (int jt = 0; jt < 4; ++jt)
-                        if (jt <= w) cb[jt] = mfma16x16x32_bf16(lds8(sm.k + (16 * jt + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[jt]);
+                    cb[0] = mfma16x16x32_bf16(lds8(sm.k + (32 * kb + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[0]);
+                    if (two) cb[1] = mfma16x16x32_bf16(lds8(sm.k + (32 * kb + 16 + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[1]);
                 }
+                float m[8];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    if (2 * kb > w) break;
-                    float m[8];
+                for (int half = 0; half < 2; ++half) {
+                    const int jt = 2 * kb + half;
+                    if (jt < it) {
+                        const float4 bj = *reinterpret_cast<const float4 *>(&before[16 * jt + 4 * g]);
+                        const float bv[4] = {bj.x, bj.y, bj.z, bj.w};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int jt = 2 * kb + half;
-                        if (jt < w) {
-                            const float4 bj = *reinterpret_cast<const float4 *>(&sm.before[w][16 * jt + 4 * g]);
-                            const float bv[4] = {bj.x, bj.y, bj.z, bj.w};
+                        for (int e = 0; e < 4; ++e) m[4 * half + e] = cb[half][e] * (upto * bv[e]);
+                    } else if (jt == it) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) m[4 * half + e] = cb[jt][e] * (upto * bv[e]);
-                        } else if (jt == w) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int tj = 16 * jt + 4 * g + e;
-                                const float v = cb[jt][e] *
-                                    (__builtin_amdgcn_exp2f((gi - sm.s.g[tj]) + (gir - sm.s.gr[tj])) * sm.s.dt[tj]);
-                                m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) m[4 * half + e] = 0.f;
+                        for (int e = 0; e < 4; ++e) {
+                            const int tj = 16 * jt + 4 * g + e;
+                            const float v = cb[half][e] *
+                                (__builtin_amdgcn_exp2f((gi - st.g[tj]) + (gir - st.gr[tj])) * st.dt[tj]);
+                            m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
                         }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[4 * half + e] = 0.f;
                     }
-                    split2(m, m0[kb], m1[kb]);
                 }
+                s8 hi, lo;
+                split2(m, hi, lo);
+                *reinterpret_cast<s8 *>(&sm.m[((it * 2 + kb) * 64 + lane) * 8]) = hi;
+                *reinterpret_cast<s8 *>(&sm.m[(((4 + it) * 2 + kb) * 64 + lane) * 8]) = lo;
+            };
+            if (w == kStepper) {
+                if (i + 1 < chunks)
+                    step_sizes(bf16_bits_to_f32(rdt), lane < p.count - (i + 1) * kL, bias, nA2, sm.s[(i + 1) & 1]);
+                rdt = raw_dt(i + 2);
             }
+            unit(u0, k0, sm.before[w]);
+            if (u1 >= 0) unit(u1, k1, sm.before[4 + w]);
             // ---- outputs from the entering state, transposed: lane = token, entries 4
             // neighbouring channels
 #pragma unroll
@@ -327,33 +358,22 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                     y[it] = mfma16x16x32_bf16(lo, cv, y[it]);
                 }
             }
-            lds_barrier();  // C is done with
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                if (2 * kb > w) break;
-                *reinterpret_cast<s8 *>(&sm.c[((w * 2 + kb) * 64 + lane) * 8]) = m0[kb];
-                *reinterpret_cast<s8 *>(&sm.c[(((4 + w) * 2 + kb) * 64 + lane) * 8]) = m1[kb];
-            }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                const float d = sm.s.from[16 * it + r];
+                const float d = st.from[16 * it + r];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[it][e] *= d;
             }
             lds_barrier();
-            char *orows = reinterpret_cast<char *>(orow + (int64_t)c * kL * a.H * a.P);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     if (2 * kb > it) break;
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.c[((it * 2 + kb) * 64 + lane) * 8]), y[it]);
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.c[(((4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[((it * 2 + kb) * 64 + lane) * 8]), y[it]);
+                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
                 }
-                const int t = 16 * it + r;
-                if (t < rows)
-                    *reinterpret_cast<uint2 *>(orows + (ooff + 16 * it * ostep)) =
-                        make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
+                out[it] = make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
             }
         }
 
@@ -369,7 +389,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
             float v[8];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float *wp = kReverse ? sm.s.from : sm.s.w;
+                const float *wp = kReverse ? st.from : st.w;
                 const float4 wj = *reinterpret_cast<const float4 *>(wp + 32 * kb + 16 * half + 4 * g);
                 const float wv[4] = {wj.x, wj.y, wj.z, wj.w};
 #pragma unroll
@@ -394,6 +414,8 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
             }
         }
     }
+
+    if constexpr (kOut) put(p.count - (chunks - 1) * kL);
 
     // ---- the state at the end
     void *dst = kPass == kPieces ? a.state : kSwapped ? nullptr : (kReverse ? p.first : p.last) ? a.ht : nullptr;
