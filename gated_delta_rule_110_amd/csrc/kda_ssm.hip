@@ -143,6 +143,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     // tiles is an operand along channels, those of its gradient as here, S^T.
     constexpr bool kSwapped = kPass == kSave && !kReverse;
     constexpr int kTiles = kN / 16, kQ = kN / 32;
+    constexpr int kGroup = kOut ? 4 : 1;  // state tiles updated side by side, as registers allow
     __shared__ ChainSmem<kN, kOut> sm;
     int64_t index, h, pb;
     place(a, index, h, pb);
@@ -351,12 +352,14 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                 }
                 s8 hi, lo;
                 split2(v, hi, lo);
+                // products into one accumulator are four apart: none waits for the one before
+                s8 cv[4];
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const s8 cv = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
-                    y[it] = mfma16x16x32_bf16(hi, cv, y[it]);
-                    y[it] = mfma16x16x32_bf16(lo, cv, y[it]);
-                }
+                for (int it = 0; it < 4; ++it) cv[it] = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) y[it] = mfma16x16x32_bf16(hi, cv[it], y[it]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) y[it] = mfma16x16x32_bf16(lo, cv[it], y[it]);
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -366,15 +369,15 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
             }
             lds_barrier();
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    if (2 * kb > it) break;
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[((it * 2 + kb) * 64 + lane) * 8]), y[it]);
-                    y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
-                }
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int it = 2 * kb; it < 4; ++it)
+                        y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
                 out[it] = make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
-            }
         }
 
         // ---- the state at the chunk's end
@@ -395,22 +398,22 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[4 * half + e] = wv[e] * bf16_bits_to_f32((uint16_t)xf[kb][4 * half + e]);
             }
-            s8 x0, x1, x2;
-            split3(v, x0, x1, x2);
+            s8 xs[3];
+            split3(v, xs[0], xs[1], xs[2]);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const int col = kSwapped ? 16 * t + 4 * (r & 3) : 32 * (t >> 1) + 8 * (r & 3) + 4 * (t & 1);
-                const uint16_t *q = sm.k + (32 * kb + 4 * g + (r >> 2)) * kPitch<kN> + col;
-                const s8 kv = join(read_tr(q), read_tr(q + 16 * kPitch<kN>));
-                if constexpr (kSwapped) {
-                    S[t] = mfma16x16x32_bf16(x0, kv, S[t]);
-                    S[t] = mfma16x16x32_bf16(x1, kv, S[t]);
-                    S[t] = mfma16x16x32_bf16(x2, kv, S[t]);
-                } else {
-                    S[t] = mfma16x16x32_bf16(kv, x0, S[t]);
-                    S[t] = mfma16x16x32_bf16(kv, x1, S[t]);
-                    S[t] = mfma16x16x32_bf16(kv, x2, S[t]);
+            for (int t0 = 0; t0 < kTiles; t0 += kGroup) {
+                s8 kv[kGroup];
+#pragma unroll
+                for (int t = t0; t < t0 + kGroup; ++t) {
+                    const int col = kSwapped ? 16 * t + 4 * (r & 3) : 32 * (t >> 1) + 8 * (r & 3) + 4 * (t & 1);
+                    const uint16_t *q = sm.k + (32 * kb + 4 * g + (r >> 2)) * kPitch<kN> + col;
+                    kv[t - t0] = join(read_tr(q), read_tr(q + 16 * kPitch<kN>));
                 }
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int t = t0; t < t0 + kGroup; ++t)
+                        S[t] = kSwapped ? mfma16x16x32_bf16(xs[part], kv[t - t0], S[t]) : mfma16x16x32_bf16(kv[t - t0], xs[part], S[t]);
             }
         }
     }

@@ -350,35 +350,54 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             // ---- dx, transposed: lane = token, entries 4 neighbouring channels
             {
                 const int pt = w & 3, half = w >> 2;
+                // both token tiles side by side, the parts in accumulators of their own: four
+                // products between any two of one chain
+                f4 u[2][2];
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) u[jj][0] = u[jj][1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    const s8 d0 = along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), d1 = along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g);
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        const s8 bv = along(sm.b + (32 * half + 16 * jj + r) * kPitch<kN>, q, g);
+                        u[jj][0] = mfma16x16x32_bf16(d0, bv, u[jj][0]);
+                        u[jj][1] = mfma16x16x32_bf16(d1, bv, u[jj][1]);
+                    }
+                }
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
-                    const int jt = 2 * half + jj, tj = 16 * jt + r;
-                    f4 u = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int q = 0; q < kQ; ++q) {
-                        const s8 bv = along(sm.b + tj * kPitch<kN>, q, g);
-                        u = mfma16x16x32_bf16(along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
-                        u = mfma16x16x32_bf16(along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g), bv, u);
-                    }
+                    const int tj = 32 * half + 16 * jj + r;
                     const s4 xv = *reinterpret_cast<const s4 *>(sm.x + tj * kRowPitch + 16 * pt + 4 * g);
                     float f = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)xv[e]) * u[e];
-                    f = rows_sum(f);
-                    if (g == 0) add_to(&su.f[pt][tj], f, more);
                     const float wj = st.w[tj];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) u[e] *= wj;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (q < half) continue;  // i before j
-                        const s8 yv = across(sm.dy, kRowPitch, q, 16 * pt, r, g);
-                        u = mfma16x16x32_bf16(yv, across(sm.m[0], kMPitch, q, 16 * jt, r, g), u);
-                        u = mfma16x16x32_bf16(yv, across(sm.m[1], kMPitch, q, 16 * jt, r, g), u);
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = u[jj][0][e] + u[jj][1][e];
+                        f += bf16_bits_to_f32((uint16_t)xv[e]) * v;
+                        u[jj][0][e] = v * wj;
+                        u[jj][1][e] = 0.f;
                     }
+                    f = rows_sum(f);
+                    if (g == 0) add_to(&su.f[pt][tj], f, more);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (q < half) continue;      // i before j
+                    const s8 yv = across(sm.dy, kRowPitch, q, 16 * pt, r, g);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj)
+                            u[jj][k] = mfma16x16x32_bf16(yv, across(sm.m[k], kMPitch, q, 32 * half + 16 * jj, r, g), u[jj][k]);
+                }
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    const int tj = 32 * half + 16 * jj + r;
+                    const f4 v = u[jj][0] + u[jj][1];
                     if (tj < rows)
                         *reinterpret_cast<uint2 *>(a.dx + ((((trow + tj) * H + h) << shift) + pb) * kPB + 16 * pt + 4 * g) =
-                            make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+                            make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
                 }
             }
 
@@ -460,8 +479,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         if (t >= rows) continue;
         if (a.shares == 1) {
             const int64_t o = ((trow + t) * a.G + grp) * kN + n;
-            *reinterpret_cast<uint2 *>(a.dB + o) = make_uint2(pack_bf16(dB[j][0], dB[j][1]), pack_bf16(dB[j][2], dB[j][3]));
-            *reinterpret_cast<uint2 *>(a.dC + o) = make_uint2(pack_bf16(dC[j][0], dC[j][1]), pack_bf16(dC[j][2], dC[j][3]));
+            *reinterpret_cast<uint2 *>(a.dB + o) = make_uint2(pack_pair(dB[j][0], dB[j][1]), pack_pair(dB[j][2], dB[j][3]));
+            *reinterpret_cast<uint2 *>(a.dC + o) = make_uint2(pack_pair(dC[j][0], dC[j][1]), pack_pair(dC[j][2], dC[j][3]));
         } else {
             const int64_t one = a.chunks * a.G * kL * kN;  // a share of one of the two
             const int64_t o = ((chunk * a.G + grp) * kL + t) * kN + n;

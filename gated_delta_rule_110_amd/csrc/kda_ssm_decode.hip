@@ -10,7 +10,8 @@
 // A workgroup of 256 threads takes kRows rows (channels) of one head's state; a
 // thread holds 4 neighbouring columns of every 256 / (N / 4)-th row, so that a
 // row is one contiguous access of N / 4 lanes, whose shares of S' C are added by
-// lane exchanges.
+// lane exchanges.  32 rows, so that a few sequences fill the GPU (one sequence of
+// 64 heads of 64 x 128 fp32: 4.3 us against 5.6 with 64 rows).
 #include "kda_layer_args.h"
 
 using namespace kda;
@@ -18,21 +19,38 @@ using namespace kda;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRows = 32;
 
+// The new state is stored with the non-temporal hint: it displaces less of what
+// the caches still hold of the state being read (64 sequences of 64 heads, 128 MiB
+// into another tensor: 45 us against 54; in place 41 against 44).  States that do
+// not fit the 256 MB Infinity Cache at all are read past it as well (256
+// sequences, 512 MiB, in place: 181 us against 199); at 256 MiB and below that
+// costs more than it gives (128 sequences: 93 us against 79).
+constexpr int64_t kStreamBytes = 384ll << 20;
+
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+
+template <bool kStream, typename T>
+__device__ __forceinline__ T state_load(const T *p) {
+    if constexpr (kStream) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool kStream>
 __device__ __forceinline__ f4 load_state4(const void *p, int64_t i, int f32) {
-    if (f32) return *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(p) + i);
-    const uint2 v = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i);
-    return f4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-              __uint_as_float(v.y & 0xffff0000u)};
+    if (f32) return state_load<kStream>(reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(p) + i));
+    const u2v v = state_load<kStream>(reinterpret_cast<const u2v *>(reinterpret_cast<const uint16_t *>(p) + i));
+    return f4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
+              __uint_as_float(v[1] & 0xffff0000u)};
 }
 __device__ __forceinline__ void store_state4(void *p, int64_t i, int f32, f4 v) {
-    if (f32) *reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i) = v;
+    if (f32) __builtin_nontemporal_store(v, reinterpret_cast<f4 *>(reinterpret_cast<float *>(p) + i));
     else
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
-            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        __builtin_nontemporal_store(u2v{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])},
+                                    reinterpret_cast<u2v *>(reinterpret_cast<uint16_t *>(p) + i));
 }
 
-template <int kN, int kRows>
+template <int kN, bool kStream>
 __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int64_t base_block) {
     constexpr int kCols = kN / 4;                // threads per row
     constexpr int kStep = kThreads / kCols;      // rows per pass
@@ -49,9 +67,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int
     f4 S[kPass];
 #pragma unroll
     for (int i = 0; i < kPass; ++i)
-        S[i] = a.h0 ? load_state4(a.h0, base + (int64_t)i * kStep * kN, a.h0_f32) : f4{0.f, 0.f, 0.f, 0.f};
-    const f4 Bv = load_state4(a.Bm, n * a.bb + g * kN + 4 * q, 0);
-    const f4 Cv = load_state4(a.Cm, n * a.cb + g * kN + 4 * q, 0);
+        S[i] = a.h0 ? load_state4<kStream>(a.h0, base + (int64_t)i * kStep * kN, a.h0_f32) : f4{0.f, 0.f, 0.f, 0.f};
+    const f4 Bv = load_state4<false>(a.Bm, n * a.bb + g * kN + 4 * q, 0);
+    const f4 Cv = load_state4<false>(a.Cm, n * a.cb + g * kN + 4 * q, 0);
     const float raw = bf16_bits_to_f32(a.dt[n * a.dtb + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f);
     const float dt = softplus(raw);
     const float decay = fast_exp(-fast_exp(a.A_log[h]) * dt);
@@ -74,13 +92,13 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int
     }
 }
 
-template <int kN, int kRows>
+template <int kN, bool kStream>
 hipError_t launch(const SsmArgs &a, hipStream_t s) {
     constexpr int64_t kMost = int64_t(1) << 23;  // a launch's work-items are counted in 32 bits
     const int64_t blocks = a.num_seqs * a.H * (a.P / kRows);
     for (int64_t b = 0; b < blocks; b += kMost) {
         const int64_t n = blocks - b < kMost ? blocks - b : kMost;
-        hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kRows>), dim3((unsigned)n), dim3(kThreads), 0, s, a, b);
+        hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kStream>), dim3((unsigned)n), dim3(kThreads), 0, s, a, b);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -90,5 +108,7 @@ hipError_t launch(const SsmArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t kda_launch_ssm_decode(const SsmArgs &a, hipStream_t s) {
-    return a.N == 128 ? launch<128, 64>(a, s) : launch<64, 64>(a, s);
+    const bool stream = a.num_seqs * a.H * a.P * a.N * (a.h0_f32 ? 4 : 2) >= kStreamBytes;
+    if (a.N == 128) return stream ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return stream ? launch<64, true>(a, s) : launch<64, false>(a, s);
 }

@@ -49,6 +49,8 @@ class KdaSsmDesc(ctypes.Structure):
 
 def _declare(lib) -> None:
     """Argument types of the layer operators (called once, when the library is loaded)."""
+    global _lib
+    _lib = lib
     N, C, S = (ctypes.POINTER(t) for t in (KdaRmsnormDesc, KdaConvDesc, KdaSsmDesc))
     for name, n, desc in (("kda_rmsnorm_fwd", 5, N), ("kda_rmsnorm_quant", 6, N), ("kda_rmsnorm_bwd", 7, N),
                           ("kda_conv_fwd", 7, C), ("kda_conv_decode", 6, C), ("kda_conv_bwd", 11, C),
@@ -64,10 +66,15 @@ def _declare(lib) -> None:
         fn.restype, fn.argtypes = kind, [desc]
 
 
-def _library():
-    from . import library
+_lib = None
 
-    return library()
+
+def _library():
+    if _lib is None:
+        from . import library
+
+        return library()
+    return _lib
 
 
 def _ptr(t: Optional[torch.Tensor]):
