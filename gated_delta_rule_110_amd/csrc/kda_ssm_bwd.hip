@@ -16,9 +16,11 @@
 //   da_t  = e^{G_63} <D, S> + sum_{j < t} F_j + sum_{i >= t} R_i + sum_{i >= t > j} Q_ij dt_j
 //   ddt_t = -exp(A_log) da_t + sum_i Q_it + F_t / dt_t,
 //
-// the double sum as suffix sums of (row sum - column sum) of Q_ij dt_j over i > j,
-// in 64 bits: the pairs behind t cancel up to the rounding of the row and column
-// sums (the diagonal, which would cancel too, is left out).
+// the double sum, for t in the 16-token tile s, as the column sums of the row tiles
+// behind s over j < t, the row sums left of tile s over i >= t in s, and within the
+// diagonal tile as suffix sums of (row sum - column sum), where the pairs behind t
+// cancel: within one tile only, since over a chunk the rounding of what cancels
+// would show in the gradients of A_log and dt_bias.
 //
 // One workgroup of 8 waves takes a chunk, a group of B and C and a share of its
 // heads, one head and 64 channels after the other: C B^T is computed once for
@@ -42,7 +44,7 @@ constexpr int kMPitch = kL + 16;
 // A head's sums over channels and state entries, shares of its step sizes' gradient.
 template <int kN>
 struct Sums {
-    float colq[4][kL], rowe[2][kL], qd[kL], f[4][kL], rr[kN / 16][kL];
+    float colq[4][kL], rowe[2][kL], rowd[kL], qd[kL], f[4][kL], rr[kN / 16][kL];
     float xs[kN / 16], dd[4];
 };
 
@@ -88,6 +90,14 @@ __device__ __forceinline__ float rows_sum(float v) {
 }
 // Sum over the wave, in the last lane of every row.
 __device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
+// Sum over this lane and those behind it in its row of 16, in 64 bits.
+__device__ __forceinline__ double row_suffix(double v) {
+    v += lane_move<0x101, 0xf>(v);
+    v += lane_move<0x102, 0xf>(v);
+    v += lane_move<0x104, 0xf>(v);
+    v += lane_move<0x108, 0xf>(v);
+    return v;
+}
 __device__ __forceinline__ void add_to(float *p, float v, bool more) { *p = more ? *p + v : v; }
 
 // Tokens of chunk number i of the batch.
@@ -223,15 +233,23 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             xs += su.xs[i];
         }
         const float gl = st.g[kL - 1], glr = st.gr[kL - 1], dt = st.dt[t];
-        const float rowe = su.rowe[0][t] + (t >= 32 ? su.rowe[1][t] : 0.f);
         const float wd = __builtin_amdgcn_exp2f((gl - st.g[t]) + (glr - st.gr[t]));
         rr *= st.from[t];
         xs *= st.from[kL - 1];
-        const double z = (double)rr + ((double)rowe - (double)dt * (double)colq);
-        const double F = (double)wd * (double)dt * (double)f;
+        const double z = rr, F = (double)wd * (double)dt * (double)f;
         const double zi = wave_scan(z), fi = wave_scan(F);
         const double total = __shfl(zi, 63);
-        const float da = (float)((double)xs + (fi - F) + (total - zi + z));
+        const int tile = t >> 4;
+        double over = (double)su.rowe[0][t] + (double)(t >= 32 ? su.rowe[1][t] : 0.f) +
+                      ((double)su.rowd[t] - (double)dt * (double)su.colq[tile][t]);
+        over = row_suffix(over);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {            // row tiles behind t's, columns before t
+            const double v = tile < i ? (double)dt * (double)su.colq[i][t] : 0.0;
+            const double before = wave_scan(v) - v;
+            over += tile < i ? before : 0.0;
+        }
+        const float da = (float)((double)xs + (fi - F) + (total - zi + z) + over);
         const float ddt = A * da + (colq + su.qd[t]) + wd * f;
         const float draw = t < rows ? ddt * sigmoid(raw) : 0.f;
         if (t < rows) a.ddt[(trow + t) * H + h0 + i] = f32_to_bf16_bits(draw);
@@ -293,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
                 const float gi = st.g[ti], gir = st.gr[ti];
-                float rowe = 0.f, dd = 0.f;
+                float rowe = 0.f, rowd = 0.f, dd = 0.f;  // row sums left of the diagonal tile and in it
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int jt = 2 * kb + half;
@@ -317,7 +335,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         const float lc = tj <= ti ? l * cb[half][e] : 0.f;
                         const float wv = tj <= ti ? l * dtj * xd[e] : 0.f;
                         const float qv = tj < ti ? lc * xd[e] : 0.f;
-                        rowe += qv * dtj;
+                        if (jt == it) rowd += qv * dtj;
+                        else rowe += qv * dtj;
                         if (tj == ti) {
                             dd += xd[e];
                             add_to(&su.qd[ti], lc * xd[e], more);
@@ -343,6 +362,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 if (kb == it >> 1) {             // the wave with the diagonal tile
                     dd = wave_sum(dd);
                     if (lane == 63) add_to(&su.dd[it], dd, more);
+                    rowd = rows_sum(rowd);
+                    if (g == 0) add_to(&su.rowd[ti], rowd, more);
                 }
             }
             lds_barrier();
