@@ -24,10 +24,10 @@
 //
 // One workgroup of 8 waves takes a chunk, a group of B and C and a share of its
 // heads, one head and 64 channels after the other: C B^T is computed once for
-// all of them, and dB and dC add up in registers.  The products' fp32 operands
-// (M, W, S, D) are split into two bf16 parts (2^-17); x, B, C and d_out are
-// exact.  Bound by LDS reads and by the latency of its phases at one workgroup
-// per CU (150 KiB of LDS).
+// all of them, and dB and dC add up in registers.  The products' fp32 operands are
+// split into bf16 parts: M and W into two (2^-17; they reach bf16 gradients only),
+// S and D into three (2^-25) where F and R come from, which add up in the fp32
+// gradients of A_log and dt_bias; x, B, C and d_out are exact.
 #include "kda_ssm_common.h"
 
 using namespace kda;
@@ -53,7 +53,7 @@ struct __align__(16) GradSmem {
     uint16_t b[kL * kPitch<kN>], c[kL * kPitch<kN>];
     uint16_t x[kL * kRowPitch], dy[kL * kRowPitch];
     uint16_t m[2][kL * kMPitch], wm[2][kL * kRowPitch]; // M and W, two parts, rows i
-    uint16_t d[2][kPB * kPitch<kN>];                   // D, two parts, rows = channels
+    uint16_t d[3][kPB * kPitch<kN>];                   // D, three parts, rows = channels
     Steps s[3];                                        // of the head before, this one and the next
     Sums<kN> sum[2];                                   // of the head before and this one
 };
@@ -288,11 +288,12 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     v[e] = D[2 * i][e];
                     v[4 + e] = D[2 * i + 1][e];
                 }
-                s8 hi, lo;
-                split2(v, hi, lo);
+                s8 d0, d1, d2;
+                split3(v, d0, d1, d2);
                 const int at = (16 * (dp + i * (kWaves / kQ)) + r) * kPitch<kN> + 32 * dq + 8 * g;
-                *reinterpret_cast<s8 *>(&sm.d[0][at]) = hi;
-                *reinterpret_cast<s8 *>(&sm.d[1][at]) = lo;
+                *reinterpret_cast<s8 *>(&sm.d[0][at]) = d0;
+                *reinterpret_cast<s8 *>(&sm.d[1][at]) = d1;
+                *reinterpret_cast<s8 *>(&sm.d[2][at]) = d2;
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) S[t] = Sn[t];
@@ -378,12 +379,14 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 for (int jj = 0; jj < 2; ++jj) u[jj][0] = u[jj][1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < kQ; ++q) {
-                    const s8 d0 = along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), d1 = along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g);
+                    const s8 d0 = along(sm.d[0] + (16 * pt + r) * kPitch<kN>, q, g), d1 = along(sm.d[1] + (16 * pt + r) * kPitch<kN>, q, g),
+                             d2 = along(sm.d[2] + (16 * pt + r) * kPitch<kN>, q, g);
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj) {
                         const s8 bv = along(sm.b + (32 * half + 16 * jj + r) * kPitch<kN>, q, g);
                         u[jj][0] = mfma16x16x32_bf16(d0, bv, u[jj][0]);
                         u[jj][1] = mfma16x16x32_bf16(d1, bv, u[jj][1]);
+                        u[jj][1] = mfma16x16x32_bf16(d2, bv, u[jj][1]);
                     }
                 }
 #pragma unroll
@@ -424,22 +427,24 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
 
             // ---- dB and dC, transposed: lane = token, entries 4 neighbouring state entries
             {
-                s8 Dv[2][2], Sv[2][2];
+                s8 Dv[2][2], Sv[3][2];
                 float xs = 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) Dv[k][q] = across(sm.d[k], kPitch<kN>, q, 16 * nt, r, g);
+                    const s8 rest = across(sm.d[2], kPitch<kN>, q, 16 * nt, r, g);
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         v[e] = S[2 * q][e];
                         v[4 + e] = S[2 * q + 1][e];
                     }
-                    split2(v, Sv[0][q], Sv[1][q]);
+                    split3(v, Sv[0][q], Sv[1][q], Sv[2][q]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) + bf16_bits_to_f32((uint16_t)Dv[1][q][e]));
+                        xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) +
+                                      (bf16_bits_to_f32((uint16_t)Dv[1][q][e]) + bf16_bits_to_f32((uint16_t)rest[e])));
                 }
                 xs = wave_sum(xs);
                 if (lane == 63 && j0 == 0) add_to(&su.xs[nt], xs, more);
@@ -461,6 +466,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                             u = mfma16x16x32_bf16(Dv[k][q], xv, u);
                             v = mfma16x16x32_bf16(Sv[k][q], yv, v);
                         }
+                        v = mfma16x16x32_bf16(Sv[2][q], yv, v);
                     }
                     const s4 cv = *reinterpret_cast<const s4 *>(sm.c + t * kPitch<kN> + 16 * nt + 4 * g);
                     float f = 0.f;
