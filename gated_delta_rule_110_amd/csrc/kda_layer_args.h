@@ -126,14 +126,36 @@ __device__ __forceinline__ void store_any(void *p, int64_t i, int f32, float v) 
     else reinterpret_cast<uint16_t *>(p)[i] = f32_to_bf16_bits(v);
 }
 
-// softplus(x) = max(x, 0) + log1p(e^-|x|) in fp32, relative precision kept at
-// the small end: for t = e^-|x| below 2^-6 the series t - t^2/2 + t^3/3 - t^4/4
-// (relative error below 1e-7), above it the hardware log2 of 1 + t.
+// e^x with the rounding of x log2(e) made good: the hardware's exp2 of the rounded
+// product alone is off by |x| 2^-24, relative, which a step size of e^-7 would show.
+__device__ __forceinline__ float exact_exp(float x) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e) = kHi + kLo
+    const float p = x * kHi;
+    const float rest = __builtin_fmaf(x, kHi, -p) + x * kLo;
+    const float e = __builtin_amdgcn_exp2f(p);
+    return fabsf(p) < 200.0f ? __builtin_fmaf(e, rest * 0.693147182f, e) : e;  // beyond: 0 or infinity
+}
+
+// softplus(x) = max(x, 0) + log1p(t), t = e^-|x| <= 1, to about 2^-23 relative:
+// log1p(t) = 2 atanh(z) with z = t / (2 + t) <= 1/3, by the series to z^15 (the next
+// term is below 2^-27 relative).
 __device__ __forceinline__ float softplus(float x) {
-    const float t = fast_exp(-fabsf(x));
-    const float series = t * (1.0f - t * (0.5f - t * (0.33333334f - 0.25f * t)));
-    const float l = t < 0.015625f ? series : fast_log(1.0f + t);
+    const float t = exact_exp(-fabsf(x));
+    const float z = t * fast_rcp(2.0f + t), q = z * z;
+    float s = 1.0f / 15.0f;
+    s = __builtin_fmaf(s, q, 1.0f / 13.0f);
+    s = __builtin_fmaf(s, q, 1.0f / 11.0f);
+    s = __builtin_fmaf(s, q, 1.0f / 9.0f);
+    s = __builtin_fmaf(s, q, 1.0f / 7.0f);
+    s = __builtin_fmaf(s, q, 1.0f / 5.0f);
+    s = __builtin_fmaf(s, q, 1.0f / 3.0f);
+    const float l = 2.0f * __builtin_fmaf(z * q, s, z);
     return fmaxf(x, 0.0f) + l;
+}
+// The derivative of softplus: 1 / (1 + e^-x), with e^-|x|, so that it is as good.
+__device__ __forceinline__ float exact_sigmoid(float x) {
+    const float t = exact_exp(-fabsf(x));
+    return (x < 0.f ? t : 1.0f) * fast_rcp(1.0f + t);
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }

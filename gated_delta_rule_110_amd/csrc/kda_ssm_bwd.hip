@@ -215,10 +215,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         return o;
     };
     auto steps_of = [&](const Head &o, Steps &to) {
-        step_sizes(bf16_bits_to_f32(o.raw), lane < rows, o.bias, -fast_exp(o.A_log) * kLog2e, to);
+        step_sizes(bf16_bits_to_f32(o.raw), lane < rows, o.bias, -exact_exp(o.A_log) * kLog2e, to);
     };
     auto finish = [&](int i, const Head &o, const Steps &st, const Sums<kN> &su) {
-        const float A = -fast_exp(o.A_log);
+        const float A = -exact_exp(o.A_log);
         const float raw = bf16_bits_to_f32(o.raw) + o.bias;
         const int t = lane;
         float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         }
         const float da = (float)((double)xs + (fi - F) + (total - zi + z) + over);
         const float ddt = A * da + (colq + su.qd[t]) + wd * f;
-        const float draw = t < rows ? ddt * sigmoid(raw) : 0.f;
+        const float draw = t < rows ? ddt * exact_sigmoid(raw) : 0.f;
         if (t < rows) a.ddt[(trow + t) * H + h0 + i] = f32_to_bf16_bits(draw);
         const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
         if (lane == 63) {

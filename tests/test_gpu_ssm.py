@@ -72,6 +72,23 @@ def test_decode(N, H, P, G, S, state):
         assert torch.equal(y2, y) and torch.equal(st, fin)
 
 
+@pytest.mark.parametrize("step", [True, False])
+def test_small_step_sizes_keep_their_precision(step):
+    """With x = B = 1 the state after one token is dt = softplus(dt_bias) itself.  Its roundings: the
+    hardware's exp2 and reciprocal are good to 2^-23, the sums and products between them and the state's
+    own products round six times at 2^-24, and log1p's relative change is at most 1.1 times its
+    argument's (z = 1/3): 6.5 * 2^-23 in all, below 8 * 2^-23."""
+    H, P, S = 61, 64, 64
+    bias = torch.linspace(-14, 16, H)
+    x = torch.ones(1, 1, H, P, dtype=BF, device="cuda")
+    bc = torch.ones(1, 1, 1, S, dtype=BF, device="cuda")
+    fin = torch.empty(1, H, P, S, dtype=F32, device="cuda")
+    (kda.ssm_decode if step else kda.ssm_fwd)(x, torch.zeros(1, 1, H, dtype=BF, device="cuda"), bc, bc,
+                                              torch.zeros(H, device="cuda"), bias.cuda(), final_state=fin)
+    want = torch.nn.functional.softplus(bias.double(), threshold=100)[None, :, None, None]
+    assert float(((fin.double().cpu() - want).abs() / want).max()) <= 8 * 2.0 ** -23
+
+
 def test_decode_extremes():
     """Step sizes from far below to far above one: no overflow, the state replaced or kept."""
     a, s = make(4, 1, 2, 64, 1, 64, 4, F32, seed=2, params=False)
