@@ -8,6 +8,11 @@ devices and shapes, allocate outputs and workspaces that the caller does not
 pass, and call libkda on torch's current HIP stream of the inputs' device.
 Activations are bf16; they may be slices of wider tensors (only their last
 dimensions have to be contiguous).  Tensors that a call writes are contiguous.
+
+``rms_norm``, ``short_conv`` and ``ssm_scan`` differentiate once.  To capture
+their backward into a HIP graph, let no autograd graph of the same leaves from
+before the capture live (delete the outputs and losses of the warm-up first):
+torch ends such a capture with an error, or ends the process.
 """
 from __future__ import annotations
 
@@ -15,6 +20,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int64
@@ -270,11 +276,13 @@ class RmsnormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         out, res = rmsnorm_fwd(x, weight, eps, residual=residual)
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(x if res is None else res, weight)
         ctx.eps, ctx.with_residual = float(eps), res is not None
         return out, res
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_res):
         h, weight = ctx.saved_tensors
         if d_res is not None:
@@ -439,9 +447,11 @@ class ConvFunction(torch.autograd.Function):
                               out=_packed_zeros(cu_seqlens, x))
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.activation = activation
+        ctx.set_materialize_grads(False)
         return out, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_final):
         x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
         if d_out is None:
@@ -615,9 +625,11 @@ class SsmFunction(torch.autograd.Function):
         out, final = ssm_fwd(x, dt, B, C, A_log, dt_bias, D, initial_state, final, cu_seqlens,
                              out=_packed_zeros(cu_seqlens, x))
         ctx.save_for_backward(x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens)
+        ctx.set_materialize_grads(False)
         return out, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_final):
         x, dt, B, C, A_log, dt_bias, D, initial_state, cu_seqlens = ctx.saved_tensors
         if d_out is None:
