@@ -94,22 +94,39 @@ __device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int
 }
 int64_t grid_size(const SsmChainArgs &a) { return (a.pieces + 7) / 8 * 8 * a.H * (a.P / kPB); }
 
-// M's 16 x 32 units, (row tile, half of the columns), by the wave that computes
-// them: at most 3 of the 10 tiles on or below the diagonal each.
+// The decays that M's tiles left of the diagonal take as products around their
+// row tile's first token, both factors at most 1.
+struct TileDecays {
+    float upto[kL];               // from the token before the row tile to token i
+    float before[3][kL];          // from token j to the token before row tile 1, 2, 3, times dt_j
+};
 
 template <int kN, bool kOut>
 struct __align__(16) ChainSmem {
     uint16_t k[kL * kPitch<kN>];
     uint16_t c[kOut ? kL * kPitch<kN> : 8];
     uint16_t x[kL * kXPitch];
+    uint16_t o[kOut ? kL * kXPitch : 8];        // outputs, on their way to whole rows
     uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
     Steps s[2];                                 // of this chunk and the next
-    float before[kOut ? 8 : 1][kL];             // by unit: decay from token j to the start of the row tile, times dt_j
+    TileDecays t[kOut ? 2 : 1];
 };
 
-// LDS written by a wave's lanes is read by others of the same wave: a wave's LDS
-// accesses are in order, so only the compiler has to keep theirs.
-__device__ __forceinline__ void wave_sync() { asm volatile("" ::: "memory"); }
+// By the wave that wrote the steps, lane = token, from what the lane itself wrote and
+// the tokens before the row tiles (a wave's own LDS accesses are in order).
+__device__ __forceinline__ void tile_decays(const Steps &s, TileDecays &o) {
+    const int lane = threadIdx.x & 63;
+    const float g = s.g[lane], gr = s.gr[lane], dt = s.dt[lane];
+    float up = 1.f;
+#pragma unroll
+    for (int it = 1; it < 4; ++it) {
+        const float g0 = s.g[16 * it - 1], g0r = s.gr[16 * it - 1];
+        // tokens of the tile and behind it: not read, kept finite
+        o.before[it - 1][lane] = lane < 16 * it ? __builtin_amdgcn_exp2f((g0 - g) + (g0r - gr)) * dt : 0.f;
+        if (lane >= 16 * it) up = __builtin_amdgcn_exp2f((g - g0) + (gr - g0r));
+    }
+    o.upto[lane] = up;
+}
 
 // 8 consecutive state entries of either type.
 __device__ __forceinline__ void load_state8(const void *p, int64_t i, int f32, float *o) {
@@ -173,9 +190,6 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     if constexpr (kOut) rc.init(a.ct, kPitch<kN>);
     rx.init(a.xt, kXPitch);
     const uint32_t doff = (uint32_t)lane * (uint32_t)a.dtt * 2;
-    // byte offset of this lane's output: token lane % 16, 4 channels
-    const uint32_t ostep = (uint32_t)(a.H * a.P) * 2;
-    const uint32_t ooff = (uint32_t)r * ostep + (16 * w + 4 * g) * 2;
     uint32_t rdt = 0;
     // step sizes of the piece's chunk c, as loaded: used, and so waited for, later
     auto raw_dt = [&](int c) -> uint32_t {
@@ -224,22 +238,32 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
     }
 
-    // The outputs of the chunk before: token 16 it + r, 4 channels.
-    uint2 out[4];
-    char *oput = reinterpret_cast<char *>(orow);
+    // The outputs of the chunk before, from LDS: 16 bytes a thread, whole rows.
+    uint16_t *oput = orow;
     auto put = [&](int rows) {
+        const int t = threadIdx.x >> 3, c8 = 8 * (threadIdx.x & 7);
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-            if (16 * it + r < rows) *reinterpret_cast<uint2 *>(oput + (ooff + 16 * it * ostep)) = out[it];
-        oput += (int64_t)kL * ostep;
+        for (int i = 0; i < 2; ++i)
+            if (32 * i + t < rows)
+                *reinterpret_cast<uint4 *>(oput + ((uint32_t)(32 * i + t) * (uint32_t)(a.H * a.P) + c8)) =
+                    *reinterpret_cast<const uint4 *>(sm.o + (32 * i + t) * kXPitch + c8);
+        oput += (int64_t)kL * a.H * a.P;
     };
-    const int u0 = w < 2 ? 3 : w == 2 ? 2 : 1, k0 = w == 1, u1 = w == 0 ? 0 : w == 1 ? 2 : -1, k1 = w == 1;
+    // this wave's tiles of M left of the diagonal: rows 1 and 2 of column 0; (2, 1) and
+    // (3, 0); rows 3 of columns 1 and 2
+    const int it0 = w == 0 ? 1 : w == 1 ? 2 : 3, jt0 = w == 0 ? 0 : 1, it1 = w == 0 ? 2 : 3, jt1 = w == 2 ? 2 : 0;
     float total = 0.f;
     // Outputs: the next chunk's step sizes are taken beside this one's M, by a wave
     // with few of its tiles.
     if (kOut && w == kStepper) {
         step_sizes(bf16_bits_to_f32(raw_dt(0)), lane < p.count, bias, nA2, sm.s[0]);
+        tile_decays(sm.s[0], sm.t[0]);
         rdt = raw_dt(1);
+    }
+    if (kOut && w < 2) {  // M's tiles (0, 1) and (2, 3) are zero: half an operand each, both parts
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+            *reinterpret_cast<s4 *>(&sm.m[(((4 * part + 2 * w) * 2 + w) * 64 + lane) * 8 + 4]) = s4{0, 0, 0, 0};
     }
     // Barriers here order LDS traffic only: the next chunk's loads stay in flight.
     for (int i = 0; i < chunks; ++i) {
@@ -270,6 +294,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
         if (i + 1 < chunks) fetch(i + 1);
         const Steps &st = sm.s[i & 1];
+        [[maybe_unused]] const TileDecays &td = sm.t[kOut ? i & 1 : 0];
         const float gl = st.g[kL - 1];
 
         // x along tokens, for this wave's channels
@@ -282,62 +307,61 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 
         f4 y[4];
         if constexpr (kOut) {
-            // ---- M, unit by unit, as B C^T: lane = row i, its entries the columns j that an
-            // operand holds.  Tiles left of the diagonal take their decays as a product
-            // around the tile's first row, both factors at most 1; the diagonal tile
-            // takes the exponentials themselves.
-            auto unit = [&](const int it, const int kb, float *before) {
-                const int ti = 16 * it + r;
-                const float gi = st.g[ti], gir = st.gr[ti];
-                float upto = 1.f;
-                if (it > 0) {
-                    const float g0 = st.g[16 * it - 1], g0r = st.gr[16 * it - 1];
-                    before[lane] = __builtin_amdgcn_exp2f((g0 - st.g[lane]) + (g0r - st.gr[lane])) * st.dt[lane];
-                    upto = __builtin_amdgcn_exp2f((gi - g0) + (gir - g0r));
-                    wave_sync();
+            // ---- M, 16 x 16 tiles as B C^T: lane = row i, its entries 4 columns j, half of an
+            // operand.  Tiles left of the diagonal take their decays as a product
+            // around the tile's first row; the diagonal tiles take the exponentials
+            // themselves.  Each wave has a diagonal tile; two of the others go to each wave
+            // that takes no step sizes.
+            auto scores = [&](const int it, const int jt) {
+                f4 cb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < kQ; ++q)
+                    cb = mfma16x16x32_bf16(lds8(sm.k + (16 * jt + r) * kPitch<kN> + 32 * q + 8 * g),
+                                           lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g), cb);
+                return cb;
+            };
+            auto keep = [&](const int it, const int jt, f4 m) {
+                float v[4] = {m[0], m[1], m[2], m[3]};
+                const uint32_t h0 = round_pair(v[0], v[1]), h1 = round_pair(v[2], v[3]);
+                uint16_t *to = &sm.m[((it * 2 + (jt >> 1)) * 64 + lane) * 8 + 4 * (jt & 1)];
+                *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
+                *reinterpret_cast<uint2 *>(to + 4 * 2 * 64 * 8) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
+            };
+            auto left = [&](const int it, const int jt, f4 cb) {
+                const float upto = td.upto[16 * it + r];
+                const f4 b = *reinterpret_cast<const f4 *>(&td.before[it - 1][16 * jt + 4 * g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cb[e] *= upto * b[e];
+                keep(it, jt, cb);
+            };
+            auto diagonal = [&](f4 cb) {
+                const float gi = st.g[16 * w + r], gir = st.gr[16 * w + r];
+                const f4 gj = *reinterpret_cast<const f4 *>(&st.g[16 * w + 4 * g]);
+                const f4 gjr = *reinterpret_cast<const f4 *>(&st.gr[16 * w + 4 * g]);
+                const f4 dj = *reinterpret_cast<const f4 *>(&st.dt[16 * w + 4 * g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 4 * g + e;
+                    const float v = cb[e] * (__builtin_amdgcn_exp2f((gi - gj[e]) + (gir - gjr[e])) * dj[e]);
+                    cb[e] = j < r ? v : j == r ? v + Dh : 0.f;
                 }
-                f4 cb[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                const bool two = 2 * kb < it;
-#pragma unroll
-                for (int q = 0; q < kQ; ++q) {
-                    const s8 cv = lds8(sm.c + ti * kPitch<kN> + 32 * q + 8 * g);
-                    cb[0] = mfma16x16x32_bf16(lds8(sm.k + (32 * kb + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[0]);
-                    if (two) cb[1] = mfma16x16x32_bf16(lds8(sm.k + (32 * kb + 16 + r) * kPitch<kN> + 32 * q + 8 * g), cv, cb[1]);
-                }
-                float m[8];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int jt = 2 * kb + half;
-                    if (jt < it) {
-                        const float4 bj = *reinterpret_cast<const float4 *>(&before[16 * jt + 4 * g]);
-                        const float bv[4] = {bj.x, bj.y, bj.z, bj.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) m[4 * half + e] = cb[half][e] * (upto * bv[e]);
-                    } else if (jt == it) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tj = 16 * jt + 4 * g + e;
-                            const float v = cb[half][e] *
-                                (__builtin_amdgcn_exp2f((gi - st.g[tj]) + (gir - st.gr[tj])) * st.dt[tj]);
-                            m[4 * half + e] = tj < ti ? v : tj == ti ? v + Dh : 0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) m[4 * half + e] = 0.f;
-                    }
-                }
-                s8 hi, lo;
-                split2(m, hi, lo);
-                *reinterpret_cast<s8 *>(&sm.m[((it * 2 + kb) * 64 + lane) * 8]) = hi;
-                *reinterpret_cast<s8 *>(&sm.m[(((4 + it) * 2 + kb) * 64 + lane) * 8]) = lo;
+                keep(w, w, cb);
             };
             if (w == kStepper) {
-                if (i + 1 < chunks)
-                    step_sizes(bf16_bits_to_f32(rdt), lane < p.count - (i + 1) * kL, bias, nA2, sm.s[(i + 1) & 1]);
+                const f4 d = scores(w, w);
+                if (i + 1 < chunks) {
+                    Steps &next = sm.s[(i + 1) & 1];
+                    step_sizes(bf16_bits_to_f32(rdt), lane < p.count - (i + 1) * kL, bias, nA2, next);
+                    tile_decays(next, sm.t[(i + 1) & 1]);
+                }
                 rdt = raw_dt(i + 2);
+                diagonal(d);
+            } else {
+                const f4 d = scores(w, w), l0 = scores(it0, jt0), l1 = scores(it1, jt1);
+                left(it0, jt0, l0);
+                left(it1, jt1, l1);
+                diagonal(d);
             }
-            unit(u0, k0, sm.before[w]);
-            if (u1 >= 0) unit(u1, k1, sm.before[4 + w]);
             // ---- outputs from the entering state, transposed: lane = token, entries 4
             // neighbouring channels
 #pragma unroll
@@ -367,17 +391,6 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[it][e] *= d;
             }
-            lds_barrier();
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int it = 2 * kb; it < 4; ++it)
-                        y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-                out[it] = make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
         }
 
         // ---- the state at the chunk's end
@@ -416,9 +429,26 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                         S[t] = kSwapped ? mfma16x16x32_bf16(xs[part], kv[t - t0], S[t]) : mfma16x16x32_bf16(kv[t - t0], xs[part], S[t]);
             }
         }
+        // ---- outputs from the chunk's own tokens
+        if constexpr (kOut) {
+            lds_barrier();
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int it = 2 * kb; it < 4; ++it)
+                        y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+                *reinterpret_cast<uint2 *>(sm.o + (16 * it + r) * kXPitch + 16 * w + 4 * g) =
+                    make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
+        }
     }
-
-    if constexpr (kOut) put(p.count - (chunks - 1) * kL);
+    if constexpr (kOut) {
+        lds_barrier();
+        put(p.count - (chunks - 1) * kL);
+    }
 
     // ---- the state at the end
     void *dst = kPass == kPieces ? a.state : kSwapped ? nullptr : (kReverse ? p.first : p.last) ? a.ht : nullptr;
