@@ -105,8 +105,7 @@ template <int kN, bool kOut>
 struct __align__(16) ChainSmem {
     uint16_t k[kL * kPitch<kN>];
     uint16_t c[kOut ? kL * kPitch<kN> : 8];
-    uint16_t x[kL * kXPitch];
-    uint16_t o[kOut ? kL * kXPitch : 8];        // outputs, on their way to whole rows
+    uint16_t x[kL * kXPitch];                   // and then the chunk's outputs, on their way to whole rows
     uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
     Steps s[2];                                 // of this chunk and the next
     TileDecays t[kOut ? 2 : 1];
@@ -196,16 +195,20 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         if (c >= chunks || lane >= p.count - c * kL) return 0;
         return *reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + (int64_t)c * kL * a.dtt) + doff);
     };
-    auto fetch = [&](int i) {
+    // The next chunk's rows, in parts: a dozen loads at once fill the memory pipeline's
+    // queue and hold up what follows (at 8192 x 64 heads, 1500 of 8600 cycles a chunk).
+    constexpr int kX = 1, kK = 2, kC = 4, kAll = 7;
+    auto fetch = [&](int i, const int what) {
+        if (i >= chunks) return;
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
         const int64_t t = (int64_t)c * kL;
         if (!kOut && w == kStepper) rdt = raw_dt(c);
-        rx.load(xrow + t * a.xt, rows);
-        rk.load(krow + t * a.kt, rows);
-        if constexpr (kOut) rc.load(crow + t * a.ct, rows);
+        if (what & kX) rx.load(xrow + t * a.xt, rows);
+        if (what & kK) rk.load(krow + t * a.kt, rows);
+        if (kOut && what & kC) rc.load(crow + t * a.ct, rows);
     };
-    fetch(0);
+    fetch(0, kAll);
 
     // ---- the state at the start
     f4 S[kTiles];
@@ -238,16 +241,21 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
     }
 
-    // The outputs of the chunk before, from LDS: 16 bytes a thread, whole rows.
-    uint16_t *oput = orow;
+    // The outputs of the chunk before: a thread takes them from where it then stores x.
+    constexpr int kHalf = kL / 2;  // rows of a pass over x
+    uint4 out0, out1;
+    const uint32_t orow_step = (uint32_t)(a.H * a.P);
+    const uint32_t ooff = (uint32_t)(threadIdx.x >> 3) * orow_step + 8 * (threadIdx.x & 7);
+    uint16_t *const oplace = sm.x + (threadIdx.x >> 3) * kXPitch + 8 * (threadIdx.x & 7);
+    auto take = [&] {
+        out0 = *reinterpret_cast<const uint4 *>(oplace);
+        out1 = *reinterpret_cast<const uint4 *>(oplace + kHalf * kXPitch);
+    };
     auto put = [&](int rows) {
-        const int t = threadIdx.x >> 3, c8 = 8 * (threadIdx.x & 7);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (32 * i + t < rows)
-                *reinterpret_cast<uint4 *>(oput + ((uint32_t)(32 * i + t) * (uint32_t)(a.H * a.P) + c8)) =
-                    *reinterpret_cast<const uint4 *>(sm.o + (32 * i + t) * kXPitch + c8);
-        oput += (int64_t)kL * a.H * a.P;
+        const int t = threadIdx.x >> 3;
+        if (t < rows) *reinterpret_cast<uint4 *>(orow + ooff) = out0;
+        if (kHalf + t < rows) *reinterpret_cast<uint4 *>(orow + ooff + kHalf * orow_step) = out1;
+        orow += (int64_t)kL * orow_step;
     };
     // this wave's tiles of M left of the diagonal: rows 1 and 2 of column 0; (2, 1) and
     // (3, 0); rows 3 of columns 1 and 2
@@ -273,6 +281,9 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         if (i && !leave) lds_barrier();  // the chunk before is done with
         if (!leave) {
             if (!kOut && w == kStepper) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s[i & 1]);
+            if constexpr (kOut) {
+                if (i) take();
+            }
             rx.store(sm.x, kXPitch);
             rk.store(sm.k, kPitch<kN>);
             if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
@@ -292,7 +303,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         if constexpr (kOut) {
             if (i > 0) put(kL);
         }
-        if (i + 1 < chunks) fetch(i + 1);
+        fetch(i + 1, kOut ? kX : kAll);
         const Steps &st = sm.s[i & 1];
         [[maybe_unused]] const TileDecays &td = sm.t[kOut ? i & 1 : 0];
         const float gl = st.g[kL - 1];
@@ -362,6 +373,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                 left(it1, jt1, l1);
                 diagonal(d);
             }
+            fetch(i + 1, kK);
             // ---- outputs from the entering state, transposed: lane = token, entries 4
             // neighbouring channels
 #pragma unroll
@@ -431,6 +443,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
         // ---- outputs from the chunk's own tokens
         if constexpr (kOut) {
+            fetch(i + 1, kC);
             lds_barrier();
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -441,12 +454,13 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                         y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
 #pragma unroll
             for (int it = 0; it < 4; ++it)
-                *reinterpret_cast<uint2 *>(sm.o + (16 * it + r) * kXPitch + 16 * w + 4 * g) =
+                *reinterpret_cast<uint2 *>(sm.x + (16 * it + r) * kXPitch + 16 * w + 4 * g) =
                     make_uint2(pack_pair(y[it][0], y[it][1]), pack_pair(y[it][2], y[it][3]));
         }
     }
     if constexpr (kOut) {
         lds_barrier();
+        take();
         put(p.count - (chunks - 1) * kL);
     }
 
