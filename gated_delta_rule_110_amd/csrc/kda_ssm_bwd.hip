@@ -70,6 +70,9 @@ __device__ __forceinline__ s8 across(const uint16_t *base, int pitch, int q, int
     return join(read_tr(p), read_tr(p + 16 * pitch));
 }
 
+template <int k> struct Int { static constexpr int value = k; };
+template <bool k> struct Flag { static constexpr bool value = k; };
+
 // Sum over the 16 lanes of a row, in its last lane.
 __device__ __forceinline__ float row16_sum(float v) {
     v += dpp_row_shr_zero(v, 8);
@@ -90,6 +93,20 @@ __device__ __forceinline__ float rows_sum(float v) {
 }
 // Sum over the wave, in the last lane of every row.
 __device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
+// Sum over this lane and those before it.
+__device__ __forceinline__ float wave_scan32(float v) {
+    auto move = [](float x, auto ctrl, auto rows) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value,
+                                                                     decltype(rows)::value, 0xf, false));
+    };
+    v += move(v, Int<0x111>{}, Int<0xf>{});
+    v += move(v, Int<0x112>{}, Int<0xf>{});
+    v += move(v, Int<0x114>{}, Int<0xf>{});
+    v += move(v, Int<0x118>{}, Int<0xf>{});
+    v += move(v, Int<0x142>{}, Int<0xa>{});
+    v += move(v, Int<0x143>{}, Int<0xc>{});
+    return v;
+}
 // Sum over this lane and those behind it in its row of 16, in 64 bits.
 __device__ __forceinline__ double row_suffix(double v) {
     v += lane_move<0x101, 0xf>(v);
@@ -98,7 +115,15 @@ __device__ __forceinline__ double row_suffix(double v) {
     v += lane_move<0x108, 0xf>(v);
     return v;
 }
-__device__ __forceinline__ void add_to(float *p, float v, bool more) { *p = more ? *p + v : v; }
+template <typename T>
+__device__ __forceinline__ void add_to(T *p, T v, bool more) { *p = more ? *p + v : v; }
+
+// Four values in two bf16 parts, `apart` entries from each other.
+__device__ __forceinline__ void keep_pair(float (&v)[4], uint16_t *to, int apart) {
+    const uint32_t h0 = round_pair(v[0], v[1]), h1 = round_pair(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2 *>(to + apart) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
+}
 
 // Tokens of chunk number i of the batch.
 struct Chunk {
@@ -168,6 +193,11 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 cb[half] = mfma16x16x32_bf16(along(sm.b + (32 * kb + 16 * half + r) * kPitch<kN>, q, g),
                                              along(sm.c + (16 * it + r) * kPitch<kN>, q, g), cb[half]);
     }
+    if (kb == 0 && it < 2) {                     // tiles (0, 1) and (2, 3) of M and W are zero
+        float none[4] = {0.f, 0.f, 0.f, 0.f};
+        keep_pair(none, &sm.m[0][(32 * it + r) * kMPitch + 32 * it + 16 + 4 * g], kL * kMPitch);
+        keep_pair(none, &sm.wm[0][(32 * it + r) * kRowPitch + 32 * it + 16 + 4 * g], kL * kRowPitch);
+    }
     f4 dB[kJ], dC[kJ];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) dB[j] = dC[j] = f4{0.f, 0.f, 0.f, 0.f};
@@ -180,21 +210,27 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     Rows<kPB, kThreads> rx, ry;
     rx.init(a.xt, kRowPitch);
     ry.init(a.yt, kRowPitch);
-    f4 D[2 * kPairs], Sn[4];
-    auto fetch = [&](int u) {
+    f4 D[2 * kPairs], S[4];
+    constexpr int kRows = 1, kD = 2, kS = 4, kAll = 7;
+    auto fetch = [&](int u, const int what) {
+        if (u >= units) return;
         const int h = h0 + (u >> shift), pb = u & shift;
         const int64_t unit = ((chunk * H + h) << shift) + pb;
         const f4 *hs = reinterpret_cast<const f4 *>(a.hs) + unit * (kPB * kN / 4);
         const f4 *ds = reinterpret_cast<const f4 *>(a.ds) + unit * (kPB * kN / 4);
-        rx.load(xrow + ((h << shift) + pb) * kPB, rows);
-        ry.load(yrow + ((h << shift) + pb) * kPB, rows);
+        if (what & kRows) {
+            rx.load(xrow + ((h << shift) + pb) * kPB, rows);
+            ry.load(yrow + ((h << shift) + pb) * kPB, rows);
+        }
+        if (what & kD)
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i)
+            for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) D[2 * i + k] = ds[((dp + i * (kWaves / kQ)) * kTiles + 2 * dq + k) * 64 + lane];
+                for (int k = 0; k < 2; ++k) D[2 * i + k] = ds[((dp + i * (kWaves / kQ)) * kTiles + 2 * dq + k) * 64 + lane];
         // rows = channels 16 t + 4 g + e, column = entry 16 nt + r
+        if (what & kS)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) Sn[t] = hs[(t * kTiles + nt) * 64 + lane];
+            for (int t = 0; t < 4; ++t) S[t] = hs[(t * kTiles + nt) * 64 + lane];
     };
     // The work per token of a head, lane = token: its step sizes ahead of its
     // turn, and the sums' gradients behind it, each by a wave that the 64 x 64
@@ -221,10 +257,12 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         const float A = -exact_exp(o.A_log);
         const float raw = bf16_bits_to_f32(o.raw) + o.bias;
         const int t = lane;
-        float colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
+        float cq[4], colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i >= t >> 4) colq += su.colq[i][t];
+            const float v = su.colq[i][t];       // row tiles before t's hold none
+            cq[i] = i >= t >> 4 ? v : 0.f;
+            colq += cq[i];
             f += su.f[i][t];
         }
 #pragma unroll
@@ -241,15 +279,16 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         const double total = __shfl(zi, 63);
         const int tile = t >> 4;
         double over = (double)su.rowe[0][t] + (double)(t >= 32 ? su.rowe[1][t] : 0.f) +
-                      ((double)su.rowd[t] - (double)dt * (double)su.colq[tile][t]);
+                      ((double)su.rowd[t] - (double)dt * (double)(tile == 0 ? cq[0] : tile == 1 ? cq[1] : tile == 2 ? cq[2] : cq[3]));
         over = row_suffix(over);
+        float left = 0.f;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {            // row tiles behind t's, columns before t
-            const double v = tile < i ? (double)dt * (double)su.colq[i][t] : 0.0;
-            const double before = wave_scan(v) - v;
-            over += tile < i ? before : 0.0;
+        for (int i = 1; i < 4; ++i) {            // row tiles behind t's, columns before t: nothing cancels
+            const float v = tile < i ? dt * cq[i] : 0.f;
+            const float before = wave_scan32(v) - v;
+            left += tile < i ? before : 0.f;
         }
-        const float da = (float)((double)xs + (fi - F) + (total - zi + z) + over);
+        const float da = (float)((double)xs + (fi - F) + (total - zi + z) + (over + (double)left));
         const float ddt = A * da + (colq + su.qd[t]) + wd * f;
         const float draw = t < rows ? ddt * exact_sigmoid(raw) : 0.f;
         if (t < rows) a.ddt[(trow + t) * H + h0 + i] = f32_to_bf16_bits(draw);
@@ -267,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         steps_of(head(0), sm.s[0]);
         own = head(1);
     }
-    fetch(0);
+    fetch(0, kAll);
     int slot = 0;                                // of this head's step sizes
     for (int u = 0; u < units; ++u) {
         const int i = u >> shift, h = h0 + i, pb = u & shift;
@@ -276,7 +315,6 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         if (u > 0 && !more) slot = slot == 2 ? 0 : slot + 1;
         const Steps &st = sm.s[slot];
         Sums<kN> &su = sm.sum[i & 1];
-        f4 S[4];
         {
             rx.store(sm.x, kRowPitch);
             ry.store(sm.dy, kRowPitch);
@@ -295,10 +333,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 *reinterpret_cast<s8 *>(&sm.d[1][at]) = d1;
                 *reinterpret_cast<s8 *>(&sm.d[2][at]) = d2;
             }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) S[t] = Sn[t];
             lds_barrier();
-            if (u + 1 < units) fetch(u + 1);
+            fetch(u + 1, kRows);
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
             if (w == kFinisher && !more) {
@@ -312,51 +348,54 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
                 const float gi = st.g[ti], gir = st.gr[ti];
-                float rowe = 0.f, rowd = 0.f, dd = 0.f;  // row sums left of the diagonal tile and in it
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                // One 16 x 16 tile; the sums are returned: of the row, and in the diagonal
+                // tile of Q and of XD at i = j.
+                auto tile = [&](const int half, auto on_diagonal, float &row, float &qd, float &dd) {
+                    constexpr bool kDiagonal = decltype(on_diagonal)::value;
                     const int jt = 2 * kb + half;
                     f4 xd = {0.f, 0.f, 0.f, 0.f};
-                    if (jt <= it) {
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kRowPitch, q, g), along(sm.dy + ti * kRowPitch, q, g), xd);
-                    }
-                    s4 m0, m1, w0, w1;
-                    const float4 gj = *reinterpret_cast<const float4 *>(&st.g[16 * jt + 4 * g]);
-                    const float4 rj = *reinterpret_cast<const float4 *>(&st.gr[16 * jt + 4 * g]);
-                    const float4 dj = *reinterpret_cast<const float4 *>(&st.dt[16 * jt + 4 * g]);
-                    const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, rv[4] = {rj.x, rj.y, rj.z, rj.w};
-                    const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
+                    for (int q = 0; q < 2; ++q)
+                        xd = mfma16x16x32_bf16(along(sm.x + (16 * jt + r) * kRowPitch, q, g), along(sm.dy + ti * kRowPitch, q, g), xd);
+                    const f4 gj = *reinterpret_cast<const f4 *>(&st.g[16 * jt + 4 * g]);
+                    const f4 rj = *reinterpret_cast<const f4 *>(&st.gr[16 * jt + 4 * g]);
+                    const f4 dj = *reinterpret_cast<const f4 *>(&st.dt[16 * jt + 4 * g]);
+                    float m[4], wv[4];
+                    f4 col;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int tj = 16 * jt + 4 * g + e;
-                        const float dtj = dv[e];
-                        const float l = tj <= ti ? __builtin_amdgcn_exp2f((gi - gv[e]) + (gir - rv[e])) : 0.f;
-                        const float lc = tj <= ti ? l * cb[half][e] : 0.f;
-                        const float wv = tj <= ti ? l * dtj * xd[e] : 0.f;
-                        const float qv = tj < ti ? lc * xd[e] : 0.f;
-                        if (jt == it) rowd += qv * dtj;
-                        else rowe += qv * dtj;
-                        if (tj == ti) {
-                            dd += xd[e];
-                            add_to(&su.qd[ti], lc * xd[e], more);
+                        float l = __builtin_amdgcn_exp2f((gi - gj[e]) + (gir - rj[e]));
+                        if (kDiagonal) l = tj <= ti ? l : 0.f;
+                        const float lc = l * cb[half][e];
+                        float qv = lc * xd[e];
+                        m[e] = lc * dj[e];
+                        wv[e] = l * dj[e] * xd[e];
+                        if (kDiagonal) {
+                            // lanes above the diagonal: 0 times what is there could be NaN
+                            const bool is = tj == ti;
+                            m[e] = tj <= ti ? m[e] + (is ? Dh : 0.f) : 0.f;
+                            wv[e] = tj <= ti ? wv[e] : 0.f;
+                            qd += is ? qv : 0.f;
+                            dd += is ? xd[e] : 0.f;
+                            qv = tj < ti ? qv : 0.f;
                         }
-                        short u, v;
-                        split_bf16(lc * dtj + (tj == ti ? Dh : 0.f), u, v);
-                        m0[e] = u;
-                        m1[e] = v;
-                        split_bf16(wv, u, v);
-                        w0[e] = u;
-                        w1[e] = v;
-                        const float col = row16_sum(qv);
-                        if (r == 15 && jt <= it) add_to(&su.colq[it][tj], col, more);
+                        row += qv * dj[e];
+                        col[e] = row16_sum(qv);
                     }
-                    const int at = ti * kMPitch + 16 * jt + 4 * g, wat = ti * kRowPitch + 16 * jt + 4 * g;
-                    *reinterpret_cast<s4 *>(&sm.m[0][at]) = m0;
-                    *reinterpret_cast<s4 *>(&sm.m[1][at]) = m1;
-                    *reinterpret_cast<s4 *>(&sm.wm[0][wat]) = w0;
-                    *reinterpret_cast<s4 *>(&sm.wm[1][wat]) = w1;
+                    if (r == 15) add_to(reinterpret_cast<f4 *>(&su.colq[it][16 * jt + 4 * g]), col, more);
+                    keep_pair(m, &sm.m[0][ti * kMPitch + 16 * jt + 4 * g], kL * kMPitch);
+                    keep_pair(wv, &sm.wm[0][ti * kRowPitch + 16 * jt + 4 * g], kL * kRowPitch);
+                };
+                float rowe = 0.f, rowd = 0.f, qd = 0.f, dd = 0.f, none = 0.f;
+                if (it == 2 * kb) {
+                    tile(0, Flag<true>{}, rowd, qd, dd);
+                } else if (it == 2 * kb + 1) {
+                    tile(0, Flag<false>{}, rowe, none, none);
+                    tile(1, Flag<true>{}, rowd, qd, dd);
+                } else {
+                    tile(0, Flag<false>{}, rowe, none, none);
+                    tile(1, Flag<false>{}, rowe, none, none);
                 }
                 rowe = rows_sum(rowe);
                 if (g == 0) add_to(&su.rowe[kb][ti], rowe, more);
@@ -365,8 +404,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     if (lane == 63) add_to(&su.dd[it], dd, more);
                     rowd = rows_sum(rowd);
                     if (g == 0) add_to(&su.rowd[ti], rowd, more);
+                    if (g == r >> 2) add_to(&su.qd[ti], qd, more);
                 }
             }
+            fetch(u + 1, kD);
             lds_barrier();
 
             // ---- dx, transposed: lane = token, entries 4 neighbouring channels
@@ -389,6 +430,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         u[jj][1] = mfma16x16x32_bf16(d2, bv, u[jj][1]);
                     }
                 }
+                float fs[2];
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
                     const int tj = 32 * half + 16 * jj + r;
@@ -402,9 +444,11 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         u[jj][0][e] = v * wj;
                         u[jj][1][e] = 0.f;
                     }
-                    f = rows_sum(f);
-                    if (g == 0) add_to(&su.f[pt][tj], f, more);
+                    fs[jj] = rows_sum(f);
                 }
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj)
+                    if (g == 0) add_to(&su.f[pt][32 * half + 16 * jj + r], fs[jj], more);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     if (q < half) continue;      // i before j
@@ -448,12 +492,14 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 }
                 xs = wave_sum(xs);
                 if (lane == 63 && j0 == 0) add_to(&su.xs[nt], xs, more);
+                fetch(u + 1, kS);
                 s8 Ct[2], Bt[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     Ct[q] = across(sm.c, kPitch<kN>, q, 16 * nt, r, g);
                     Bt[q] = across(sm.b, kPitch<kN>, q, 16 * nt, r, g);
                 }
+                float rr[kJ];
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) {
                     const int tt = j0 + j, t = 16 * tt + r;
@@ -472,8 +518,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     float f = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)cv[e]) * v[e];
-                    f = rows_sum(f);
-                    if (g == 0) add_to(&su.rr[nt][t], f, more);
+                    rr[j] = rows_sum(f);
                     const float wt = st.w[t], et = st.from[t];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -494,6 +539,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         }
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+                    if (g == 0) add_to(&su.rr[nt][16 * (j0 + j) + r], rr[j], more);
             }
             lds_barrier();
         }
