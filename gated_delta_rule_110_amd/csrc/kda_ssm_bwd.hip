@@ -125,6 +125,27 @@ __device__ __forceinline__ void keep_pair(float (&v)[4], uint16_t *to, int apart
     *reinterpret_cast<uint2 *>(to + apart) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
 }
 
+// p[i], or 0 without p, by a scalar load; i is the same for the whole wave, and nothing
+// here writes the parameters.
+__device__ __forceinline__ float scalar(const float *p, int i) {
+    typedef const __attribute__((address_space(4))) float cf;
+    return p ? reinterpret_cast<cf *>(reinterpret_cast<uintptr_t>(p))[i] : 0.f;
+}
+
+// The derivative of softplus, from its value dt: 1 - e^-dt, for small dt by its series
+// (to dt^8: the next term is below 2^-25 relative at 1/2).
+__device__ __forceinline__ float softplus_slope(float dt) {
+    float s = -1.0f / 8.0f;
+    s = __builtin_fmaf(s, dt, 1.0f) * (1.0f / 7.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * (1.0f / 6.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * (1.0f / 5.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * (1.0f / 4.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * (1.0f / 3.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * (1.0f / 2.0f);
+    s = __builtin_fmaf(-s, dt, 1.0f) * dt;
+    return dt < 0.5f ? s : 1.0f - exact_exp(-dt);
+}
+
 // Tokens of chunk number i of the batch.
 struct Chunk {
     int64_t row0, t0;
@@ -235,27 +256,18 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     // The work per token of a head, lane = token: its step sizes ahead of its
     // turn, and the sums' gradients behind it, each by a wave that the 64 x 64
     // products leave idle.
-    // Head number i of the share: what these need from memory, loaded a head ahead.
-    struct Head {
-        uint32_t raw;
-        float A_log, bias;
+    // Parameters come by scalar loads, and the raw step sizes a head ahead: waits for
+    // vector loads are in order, and one within the products would wait for the rows
+    // just fetched.
+    // Lanes and heads behind the last ones read those again.
+    const uint16_t *drow = a.dt + ck.row0 * a.dtb + (ck.t0 + (lane < rows ? lane : rows - 1)) * a.dtt + h0;
+    auto raw_of = [&](int i) -> uint32_t { return drow[i < count ? i : count - 1]; };
+    auto steps_of = [&](int i, uint32_t raw, Steps &to) {
+        step_sizes(bf16_bits_to_f32((uint16_t)raw), lane < rows, scalar(a.dt_bias, h0 + i),
+                   -exact_exp(scalar(a.A_log, h0 + i)) * kLog2e, to);
     };
-    const uint16_t *drow = a.dt + ck.row0 * a.dtb + (ck.t0 + lane) * a.dtt + h0;
-    auto head = [&](int i) -> Head {
-        Head o{0, 0.f, 0.f};
-        if (i < count) {
-            if (lane < rows) o.raw = drow[i];
-            o.A_log = a.A_log[h0 + i];
-            if (a.dt_bias) o.bias = a.dt_bias[h0 + i];
-        }
-        return o;
-    };
-    auto steps_of = [&](const Head &o, Steps &to) {
-        step_sizes(bf16_bits_to_f32(o.raw), lane < rows, o.bias, -exact_exp(o.A_log) * kLog2e, to);
-    };
-    auto finish = [&](int i, const Head &o, const Steps &st, const Sums<kN> &su) {
-        const float A = -exact_exp(o.A_log);
-        const float raw = bf16_bits_to_f32(o.raw) + o.bias;
+    auto finish = [&](int i, const Steps &st, const Sums<kN> &su) {
+        const float A = -exact_exp(scalar(a.A_log, h0 + i));
         const int t = lane;
         float cq[4], colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
 #pragma unroll
@@ -290,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         }
         const float da = (float)((double)xs + (fi - F) + (total - zi + z) + (over + (double)left));
         const float ddt = A * da + (colq + su.qd[t]) + wd * f;
-        const float draw = t < rows ? ddt * exact_sigmoid(raw) : 0.f;
+        const float draw = t < rows ? ddt * softplus_slope(dt) : 0.f;
         if (t < rows) a.ddt[(trow + t) * H + h0 + i] = f32_to_bf16_bits(draw);
         const float dA = wave_sum(A * dt * da), db = wave_sum(draw);
         if (lane == 63) {
@@ -301,16 +313,16 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
         }
     };
     constexpr int kFinisher = 4, kStepper = 5;   // waves without a tile below the diagonal
-    Head own{0, 0.f, 0.f};                       // finisher: this head; stepper: the next one
+    uint32_t raw = 0;                            // the stepper's, of the next head
     if (w == kStepper) {
-        steps_of(head(0), sm.s[0]);
-        own = head(1);
+        steps_of(0, raw_of(0), sm.s[0]);
+        raw = raw_of(1);
     }
     fetch(0, kAll);
     int slot = 0;                                // of this head's step sizes
     for (int u = 0; u < units; ++u) {
         const int i = u >> shift, h = h0 + i, pb = u & shift;
-        const float Dh = a.D ? a.D[h] : 0.f;
+        const float Dh = scalar(a.D, h);
         const bool more = pb > 0;                // sums over channels go on
         if (u > 0 && !more) slot = slot == 2 ? 0 : slot + 1;
         const Steps &st = sm.s[slot];
@@ -333,17 +345,17 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 *reinterpret_cast<s8 *>(&sm.d[1][at]) = d1;
                 *reinterpret_cast<s8 *>(&sm.d[2][at]) = d2;
             }
+            asm volatile("" : "+v"(raw));       // waited for here, before the rows' loads
             lds_barrier();
             fetch(u + 1, kRows);
 
             // ---- M, W, Q: 64 x 64, lane = i, entries j
             if (w == kFinisher && !more) {
-                if (i > 0) finish(i - 1, own, sm.s[slot == 0 ? 2 : slot - 1], sm.sum[(i - 1) & 1]);
-                own = head(i);
+                if (i > 0) finish(i - 1, sm.s[slot == 0 ? 2 : slot - 1], sm.sum[(i - 1) & 1]);
             }
             if (w == kStepper && !more && i + 1 < count) {
-                steps_of(own, sm.s[slot == 2 ? 0 : slot + 1]);
-                own = head(i + 2);
+                steps_of(i + 1, raw, sm.s[slot == 2 ? 0 : slot + 1]);
+                raw = raw_of(i + 2);
             }
             if (2 * kb <= it) {
                 const int ti = 16 * it + r;
@@ -546,7 +558,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
             lds_barrier();
         }
     }
-    if (w == kFinisher) finish(count - 1, own, sm.s[slot], sm.sum[(count - 1) & 1]);
+    if (w == kFinisher) finish(count - 1, sm.s[slot], sm.sum[(count - 1) & 1]);
 
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
