@@ -183,23 +183,26 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     const int64_t sseq = p.n * a.H * a.P * kN + sbase, spiece = p.index * a.H * a.P * kN + sbase;
 
     const int chunks = (p.count + kL - 1) / kL;
+    // where only the states are kept, what leaves the piece is not needed
+    const bool leave = kPass == kSave && !(kReverse && p.first && a.ht);
+    const int steps = chunks - leave;
     Rows<kN, kThreads> rk, rc;
     Rows<kPB, kThreads> rx;
     rk.init(a.kt, kPitch<kN>);
     if constexpr (kOut) rc.init(a.ct, kPitch<kN>);
     rx.init(a.xt, kXPitch);
-    const uint32_t doff = (uint32_t)lane * (uint32_t)a.dtt * 2;
     uint32_t rdt = 0;
-    // step sizes of the piece's chunk c, as loaded: used, and so waited for, later
+    // step sizes of the piece's chunk c, as loaded: used, and so waited for, later; tokens
+    // behind the last one read it again
     auto raw_dt = [&](int c) -> uint32_t {
-        if (c >= chunks || lane >= p.count - c * kL) return 0;
-        return *reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(drow + (int64_t)c * kL * a.dtt) + doff);
+        const int t = c * kL + lane;
+        return drow[(int64_t)(t < p.count ? t : p.count - 1) * a.dtt];
     };
     // The next chunk's rows, in parts: a dozen loads at once fill the memory pipeline's
     // queue and hold up what follows (at 8192 x 64 heads, 1500 of 8600 cycles a chunk).
     constexpr int kX = 1, kK = 2, kC = 4, kAll = 7;
     auto fetch = [&](int i, const int what) {
-        if (i >= chunks) return;
+        if (i > 0 && i >= steps) return;
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
         const int64_t t = (int64_t)c * kL;
@@ -273,33 +276,29 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         for (int part = 0; part < 2; ++part)
             *reinterpret_cast<s4 *>(&sm.m[(((4 * part + 2 * w) * 2 + w) * 64 + lane) * 8 + 4]) = s4{0, 0, 0, 0};
     }
+    auto keep_state = [&](int c) {
+        if (p.chunk0 + c >= a.chunks) return;
+        f4 *dst = reinterpret_cast<f4 *>(a.save) +
+                  (((p.chunk0 + c) * a.H + h) * (a.P / kPB) + pb) * (kPB * kN / 4) + w * kTiles * 64 + lane;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) dst[t * 64] = S[t];
+    };
     // Barriers here order LDS traffic only: the next chunk's loads stay in flight.
-    for (int i = 0; i < chunks; ++i) {
+    for (int i = 0; i < steps; ++i) {
         const int c = kReverse ? chunks - 1 - i : i;
         const int rows = p.count - c * kL < kL ? p.count - c * kL : kL;
-        const bool leave = kPass == kSave && i + 1 == chunks && !(kReverse && p.first && a.ht);
-        if (i && !leave) lds_barrier();  // the chunk before is done with
-        if (!leave) {
-            if (!kOut && w == kStepper) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s[i & 1]);
-            if constexpr (kOut) {
-                if (i) take();
-            }
-            rx.store(sm.x, kXPitch);
-            rk.store(sm.k, kPitch<kN>);
-            if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
-            lds_barrier();
+        if (i) lds_barrier();                    // the chunk before is done with
+        if (!kOut && w == kStepper) step_sizes(bf16_bits_to_f32(rdt), lane < rows, bias, nA2, sm.s[i & 1]);
+        if constexpr (kOut) {
+            if (i) take();
         }
+        rx.store(sm.x, kXPitch);
+        rk.store(sm.k, kPitch<kN>);
+        if constexpr (kOut) rc.store(sm.c, kPitch<kN>);
+        lds_barrier();
         // What goes to memory goes out here, behind the wait for this chunk's loads and
         // before the next one's: the next wait, which counts both, comes a chunk later.
-        if constexpr (kPass == kSave) {
-            if (p.chunk0 + c < a.chunks) {
-                f4 *dst = reinterpret_cast<f4 *>(a.save) +
-                          (((p.chunk0 + c) * a.H + h) * (a.P / kPB) + pb) * (kPB * kN / 4) + w * kTiles * 64 + lane;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) dst[t * 64] = S[t];
-            }
-            if (leave) break;            // what leaves the piece is not needed
-        }
+        if constexpr (kPass == kSave) keep_state(c);
         if constexpr (kOut) {
             if (i > 0) put(kL);
         }
@@ -462,6 +461,10 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         lds_barrier();
         take();
         put(p.count - (chunks - 1) * kL);
+    }
+
+    if constexpr (kPass == kSave) {
+        if (leave) keep_state(kReverse ? 0 : chunks - 1);
     }
 
     // ---- the state at the end

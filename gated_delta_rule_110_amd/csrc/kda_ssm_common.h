@@ -10,6 +10,7 @@ constexpr int kPB = 64;       // channels per workgroup
 constexpr float kLog2e = 1.4426950408889634f;
 
 typedef short s4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 
 // LDS rows are padded by 32 bytes, so that the 16 rows (and the 8-row groups of
 // the transposing read) of one access spread over the banks.
@@ -31,40 +32,39 @@ __device__ __forceinline__ s8 lds8(const uint16_t *p) { return *reinterpret_cast
 __device__ __forceinline__ int64_t clamp_to(int64_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? hi : v; }
 
 // 64 token rows of kCols bf16 values to registers and on to LDS, 16 bytes a
-// thread and pass.  A row's address is a uniform one plus 32 bits a thread
-// (the host refuses token strides of 2^24 entries and more).
+// thread and pass.  Rows behind the sequence count as zero: they are given an
+// offset outside the buffer, for which the hardware loads zeros.  No branch
+// around the loads: where paths with different loads meet, the compiler has to
+// wait for all that may be in flight, stores included (the outputs' pass over
+// 8192 x 64 heads lost 1500 of 8600 cycles a chunk to that).
 template <int kCols, int kThreads>
 struct Rows {
     static constexpr int kPer = kThreads / (kCols / 8);  // rows per pass
     static constexpr int kPass = kL / kPer;
-    uint4 v[kPass];
+    static constexpr uint32_t kSize = 0x7ffffff0u;       // above 64 rows of 2^24 entries
+    u4v v[kPass];
     uint32_t off;                                        // bytes from a pass's first row
-    int64_t step;                                        // bytes between the passes
+    uint32_t step;                                       // bytes between the passes
     int r, lds;
+    // The host refuses token strides of 2^24 entries and more.
     __device__ __forceinline__ void init(int64_t stride, int pitch) {
         const int thread = threadIdx.x % kThreads;       // larger workgroups: a set of rows per kThreads of them
         const int c = thread % (kCols / 8);
         r = thread / (kCols / 8);
         off = ((uint32_t)r * (uint32_t)stride + 8 * c) * 2;
-        step = kPer * stride * 2;
+        step = kPer * (uint32_t)stride * 2;
         lds = r * pitch + 8 * c;
     }
     __device__ __forceinline__ void load(const uint16_t *base, int rows) {
-        const char *p = reinterpret_cast<const char *>(base);
-        if (rows >= kL) {
+        // a raw buffer of bytes: no stride, no swizzle
+        const auto buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base), 0, kSize, 0x00020000);
 #pragma unroll
-            for (int i = 0; i < kPass; ++i) v[i] = *reinterpret_cast<const uint4 *>(p + i * step + off);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPass; ++i) {
-                v[i] = make_uint4(0, 0, 0, 0);           // rows behind the sequence count as zero
-                if (i * kPer + r < rows) v[i] = *reinterpret_cast<const uint4 *>(p + i * step + off);
-            }
-        }
+        for (int i = 0; i < kPass; ++i)
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(buffer, i * kPer + r < rows ? off : kSize, i * step, 0);
     }
     __device__ __forceinline__ void store(uint16_t *to, int pitch) const {
 #pragma unroll
-        for (int i = 0; i < kPass; ++i) *reinterpret_cast<uint4 *>(to + i * kPer * pitch + lds) = v[i];
+        for (int i = 0; i < kPass; ++i) *reinterpret_cast<u4v *>(to + i * kPer * pitch + lds) = v[i];
     }
 };
 
@@ -81,7 +81,6 @@ __device__ __forceinline__ uint32_t round_pair(float &a, float &b) {
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
 }
-typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void split2(const float *x, s8 &hi, s8 &lo) {
     u4v h, l;
 #pragma unroll
