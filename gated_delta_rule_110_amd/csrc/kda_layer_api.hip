@@ -289,11 +289,17 @@ struct SsmPlan {
     size_t off_piece, off_chunk, off_state, off_decay, total;
 };
 
-// Workgroups a launch should have: two rounds of the two that fit each of the
-// 256 CUs.  Fewer than kMinPiece chunks per piece would leave a piece's state
-// (32 KiB of fp32 per 64 channels and 128 entries) larger than its tokens.
-constexpr int64_t kWantGroups = 1024;
-constexpr int64_t kMinPiece = 4;
+// Workgroups a launch should have: the two that fit each of the 256 CUs, at once
+// and for equal pieces in one round (8192 tokens x 64 heads: 127 us, with two rounds
+// 132 us, with a round and a half 152 us).  Under kFewPieces pieces per sequence, two
+// rounds: the first pass leaves out the last piece, and one of few leaves CUs idle
+// (6 x 4000 tokens x 40 heads: 213 us, with one 285 us).  A packed batch's pieces are
+// uneven, and two rounds even them out (32768 tokens in 17 sequences: 463 us, with one
+// 635 us).
+// Fewer than kMinPiece chunks per piece would leave a piece's state (32 KiB of fp32
+// per 64 channels and 128 entries) larger than its tokens.
+constexpr int64_t kGroups = 512;
+constexpr int64_t kMinPiece = 4, kFewPieces = 4;
 
 kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     const int64_t units = d->H * (d->P / 64);
@@ -302,10 +308,14 @@ kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     const int64_t all = packed ? d->T / 64 + 1 : d->B * p.cps;
     int64_t pc = d->piece_chunks;
     if (pc == 0) {
-        pc = (all * units + kWantGroups - 1) / kWantGroups;
+        if (packed) {
+            pc = (all * units + 2 * kGroups - 1) / (2 * kGroups);
+        } else {                             // chains that fill the GPU by themselves are not cut
+            int64_t pieces = kGroups / std::max<int64_t>(d->B * units, 1);
+            if (pieces > 1 && pieces < kFewPieces) pieces *= 2;
+            pc = pieces > 1 ? (p.cps + pieces - 1) / pieces : p.cps;
+        }
         if (pc < kMinPiece) pc = kMinPiece;
-        // chains that fill the GPU by themselves are not cut
-        if (!packed && d->B * units >= kWantGroups / 2) pc = p.cps;
     }
     const int64_t top = packed ? all : p.cps;
     if (pc > top) pc = top;
@@ -335,16 +345,30 @@ struct SsmBwdPlan {
     size_t off_hs, off_ds, off_psum, off_part, total;
 };
 
-// Two rounds of the one gradient workgroup that fits each CU: with few chunks,
-// the heads of a group are shared out, and the shares' dB and dC added up.
-constexpr int64_t kWantGradGroups = 512;
+// With few chunks the heads of a group are shared out among workgroups, of which one
+// fits each CU, and the shares' dB and dC added up.  In units of a workgroup's time
+// for one head and 64 channels (7 us at 128 entries), a round costs its heads and
+// about one more to begin, and adding up about one per 256 shares (128 chunks x 64
+// heads: 2 shares 491 us, 4 507 us, 8 531 us).
+int64_t grad_shares(int64_t groups, int64_t heads, int64_t blocks) {
+    constexpr int64_t kCus = 256, kMost = 64;
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t s = 1; s <= heads && s <= kMost; ++s) {
+        const int64_t share = (heads + s - 1) / s, all = groups * s;
+        const int64_t cost = (all + kCus - 1) / kCus * (share * blocks + 1) + (s > 1 ? (all + kCus - 1) / kCus : 0);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
 
 kda_status_t plan_ssm_bwd(const kda_ssm_desc_t *d, bool packed, SsmBwdPlan &b) {
     const kda_status_t st = plan_ssm(d, packed, b.p);
     if (st != KDA_OK) return st;
     const int64_t heads = d->H / d->G, chunks = b.p.chunks, groups = chunks * d->G;
-    int64_t shares = groups > 0 ? (kWantGradGroups + groups - 1) / groups : 1;
-    if (shares > heads) shares = heads;
+    const int64_t shares = grad_shares(groups, heads, d->P / 64);
     const int64_t share = (heads + shares - 1) / shares;
     b.share = (int)share;
     b.shares = (int)((heads + share - 1) / share);
