@@ -13,8 +13,8 @@ LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_intra.hip", "kda_chain.hip", "kda_fused.hip", "kda_segment.hip", "kda_decode.hip", "kda_bwd.hip",
            "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm.hip", "kda_ssm_bwd.hip", "kda_ssm_decode.hip",
            "kda_layer_api.hip"]
-HEADERS = [os.path.join(CSRC, "kda_common.h"), os.path.join(CSRC, "kda_intra_body.h"),
-           os.path.join(CSRC, "kda_layer_args.h"), os.path.join(CSRC, "kda_ssm_common.h"), os.path.join(INCLUDE, "kda.h"), os.path.join(INCLUDE, "kda_layer.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("kda_common.h", "kda_intra_body.h", "kda_layer_args.h", "kda_ssm_common.h")] + [
+    os.path.join(INCLUDE, h) for h in ("kda.h", "kda_layer.h")]
 
 # -packed-fp32-ops off: hipcc must not emit packed fp32 VALU instructions.
 HIPCC_FLAGS = [

@@ -9,7 +9,11 @@
 // access, 512 per wave) and walks over a run of tokens with the last W - 1
 // inputs in registers, so that x is read once plus W - 1 rows per run.  Where the
 // channel count, a stride or an address does not allow such accesses, the same
-// code runs with one channel per lane.
+// code runs with one channel per lane.  Measured: 4 x 2048 tokens of 12288 channels
+// 84 us, 32768 packed tokens of 4352 112 us (4.8 and 5.1 TB/s of what has to be read
+// and written; a copy reaches 5.0 to 5.4), the gradient of 8192 x 4352 49 us and 5 for
+// the weights' sum (4.0 TB/s: each run reads W - 1 tokens of its neighbour's again),
+// one token of 64 sequences of 12288 5 us, all of it latency.
 #include "kda_layer_args.h"
 
 using namespace kda;
@@ -24,11 +28,6 @@ constexpr int64_t kMaxGridY = 65535;
 
 // kC neighbouring bf16 values as loaded, until they are used.
 template <int kC> struct Raw;
-template <> struct Raw<8> {
-    uint4 v;
-    __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float *o) const { unpack_bf16x8(v, o); }
-};
 template <> struct Raw<4> {
     uint2 v;
     __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint2 *>(p); }
@@ -50,10 +49,7 @@ __device__ __forceinline__ void load_c(const uint16_t *p, float *o) {
 }
 template <int kC>
 __device__ __forceinline__ void store_c(uint16_t *p, const float *v) {
-    if constexpr (kC == 8)
-        *reinterpret_cast<uint4 *>(p) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    else if constexpr (kC == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    if constexpr (kC == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     else *p = f32_to_bf16_bits(v[0]);
 }
 // kC entries of a state or parameter row of either type.
@@ -544,9 +540,9 @@ hipError_t launch_decode(const ConvArgs &a, hipStream_t s) {
 }  // namespace
 
 // Channels per lane where 16- and 8-byte accesses are possible.  4 rather than 8:
-// half the registers (filter, window, pending sums), twice the waves; the same
-// for prompts (90 us at 4 x 2048 x 12288, 114 against 120 us packed), 66 against
-// 79 us for the gradient at 8192 x 4352.
+// half the registers (filter, window, pending sums), twice the waves: the same time
+// for prompts, 5% less packed (32768 x 4352), 66 against 79 us for the gradient of
+// 8192 x 4352 when they were compared.
 constexpr int kVec = 4;
 
 #define KDA_CONV_DISPATCH(fn)                                                          \

@@ -152,12 +152,6 @@ __device__ __forceinline__ float softplus(float x) {
     const float l = 2.0f * __builtin_fmaf(z * q, s, z);
     return fmaxf(x, 0.0f) + l;
 }
-// The derivative of softplus: 1 / (1 + e^-x), with e^-|x|, so that it is as good.
-__device__ __forceinline__ float exact_sigmoid(float x) {
-    const float t = exact_exp(-fabsf(x));
-    return (x < 0.f ? t : 1.0f) * fast_rcp(1.0f + t);
-}
-
 __device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
 }  // namespace kda

@@ -9,7 +9,10 @@
 //
 // The row is read once and stays in registers between the reduction and the
 // output, so the kernels are bound by the memory traffic of their inputs and
-// outputs.  Everything between load and store is fp32.
+// outputs.  Everything between load and store is fp32.  With rows of 4096: 8191 rows
+// and an fp32 residual 83 us (4.9 TB/s of what has to be read and written; a copy
+// reaches 5.0 to 5.4), the gradient of 8192 rows 51 us and 5 for the weight's sum
+// (4.8 TB/s), 64 rows to e4m3 4.4 us, all of it latency.
 #include "kda_layer_args.h"
 
 using namespace kda;
