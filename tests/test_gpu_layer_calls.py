@@ -147,3 +147,48 @@ def test_autograd_with_unused_outputs_and_twice():
         g = torch.autograd.grad(y.float().square().sum(), leaf1, create_graph=True)[0]
         with pytest.raises(RuntimeError):
             g.float().sum().backward()
+
+
+def packed_calls(cu, T=100):
+    """Each call that takes cu_seqlens, with its outputs the middle one of three in a buffer of zeros."""
+    a, _ = make(1, T, 2, 64, 1, 64, 1, None, seed=6)
+    x = a["x"].flatten(2).contiguous()
+    w = torch.ones(x.shape[2], 4, device="cuda")
+    dy = torch.randn(a["x"].shape, device="cuda").to(BF)
+
+    def guarded(*names):
+        outs = {n: torch.zeros(3, *s[1:], dtype=BF, device="cuda") for n, s in names}
+        return outs, {n: t[1:2] for n, t in outs.items()}
+    conv, ssm = [("dx", x.shape)], [("dx", a["x"].shape), ("ddt", a["dt"].shape), ("dB", a["B"].shape), ("dC", a["C"].shape)]
+    for fn, names in ((lambda o: kda.conv_fwd(x, w, cu_seqlens=cu, out=o["dx"]), conv),
+                      (lambda o: kda.conv_bwd(x, w, None, "silu", x, cu_seqlens=cu, outputs=o), conv),
+                      (lambda o: kda.ssm_fwd(*a.values(), cu_seqlens=cu, out=o["dx"], piece_chunks=1), ssm),
+                      (lambda o: kda.ssm_bwd(*a.values(), dy, cu_seqlens=cu, outputs=o, piece_chunks=1), ssm)):
+        whole, outs = guarded(*names)
+        yield lambda: fn(outs), whole
+
+
+def test_wrong_lengths_stay_inside():
+    """Contents of cu_seqlens that no batch has are clamped on the device: nothing outside the outputs is written."""
+    for cu in ([0, -5, 1000, 50], [70, 20, 90, 30], [0, 1 << 40, 5, 1 << 50], [0, 100] * 20, [100, 0] * 20):
+        for i, (call, whole) in enumerate(packed_calls(torch.tensor(cu, device="cuda"))):
+            say("case lengths %s, call %d" % (cu[:4], i))
+            call()
+            torch.cuda.synchronize()
+            for t in whole.values():
+                assert (t[0] == 0).all() and (t[2] == 0).all()
+
+
+def test_validated_lengths(monkeypatch):
+    """KDA_VALIDATE=1 refuses such contents before anything is launched; a batch's rows may go on behind its
+    last sequence."""
+    monkeypatch.setenv("KDA_VALIDATE", "1")
+    for cu in ([3, 20, 100], [0, 60, 20], [0, 50, 101]):
+        for call, whole in packed_calls(torch.tensor(cu, device="cuda")):
+            with pytest.raises(RuntimeError):
+                call()
+            torch.cuda.synchronize()
+            assert all((t == 0).all() for t in whole.values())
+    for call, whole in packed_calls(torch.tensor([0, 0, 77], device="cuda")):
+        call()
+        assert all(float(t[1, :77].abs().max()) > 0 and (t[1, 77:] == 0).all() for t in whole.values() if t.any())
