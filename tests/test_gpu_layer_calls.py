@@ -192,3 +192,38 @@ def test_validated_lengths(monkeypatch):
     for call, whole in packed_calls(torch.tensor([0, 0, 77], device="cuda")):
         call()
         assert all(float(t[1, :77].abs().max()) > 0 and (t[1, 77:] == 0).all() for t in whole.values() if t.any())
+
+
+def test_more_than_32_bits_of_entries():
+    """Tensors of more than 2^31 entries: their last rows come out as those of a small batch."""
+    rows, D, tail = 530000, 4096, 200
+    assert rows * D > 1 << 31
+    x = torch.zeros(1, rows, D, dtype=BF, device="cuda")
+    x[:, -tail:].normal_()
+    last = x[:, -tail:].contiguous()
+    w, wc = torch.rand(D, device="cuda"), torch.randn(D, 4, device="cuda")
+    say("case 2^31 entries: norm")
+    same([kda.rmsnorm_fwd(x, w, 1e-5)[0][0, -tail:]], [kda.rmsnorm_fwd(last, w, 1e-5)[0][0]])
+    q, s, _ = kda.rmsnorm_quant(x, w, 1e-5)
+    ql, sl, _ = kda.rmsnorm_quant(last, w, 1e-5)
+    same([q[0, -tail:], s[0, -tail:]], [ql[0], sl[0]])
+    same([kda.rmsnorm_bwd(x, w, 1e-5, x)["dx"][0, -tail:]], [kda.rmsnorm_bwd(last, w, 1e-5, last)["dx"][0]])
+    say("case 2^31 entries: convolution")
+    same([kda.conv_fwd(x, wc)[0][0, -tail:]], [kda.conv_fwd(last, wc)[0][0]])
+    same([kda.conv_bwd(x, wc, None, "silu", x)["dx"][0, -tail:]], [kda.conv_bwd(last, wc, None, "silu", last)["dx"][0]])
+    # the scan: zeros leave no state behind, so the tail starts from none in both
+    H, P, S = D // 64, 64, 64
+    g = {"dt": torch.zeros(1, rows, H, dtype=BF, device="cuda"), "B": torch.zeros(1, rows, 1, S, dtype=BF, device="cuda"),
+         "C": torch.zeros(1, rows, 1, S, dtype=BF, device="cuda")}
+    for t in g.values():
+        t[:, -tail:].normal_()
+    A, bias = torch.zeros(H, device="cuda"), torch.full((H,), -3.0, device="cuda")
+    big = [x.unflatten(2, (H, P)), *g.values(), A, bias]
+    small = [t[:, -tail:].contiguous() for t in big[:4]] + [A, bias]
+    say("case 2^31 entries: scan")
+    y, yl = kda.ssm_fwd(*big)[0][0, -tail:].float(), kda.ssm_fwd(*small)[0][0].float()
+    # the chunks begin at other tokens: two roundings to bf16 of sums that agree to 2^-16 of their size
+    assert float((y - yl).abs().max()) <= (2.0 ** -7 + 2.0 ** -15) * float(yl.abs().max())
+    say("case 2^31 entries: scan's gradient")
+    d, dl = kda.ssm_bwd(*big, None, big[0])["dx"][0, -tail:].float(), kda.ssm_bwd(*small, None, small[0])["dx"][0].float()
+    assert float((d - dl).abs().max()) <= (2.0 ** -7 + 2.0 ** -15) * float(dl.abs().max())
