@@ -91,18 +91,29 @@ __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) 
     return p;
 }
 
-// Workgroups to (piece, head, channel block).  Workgroups go to the 8 XCDs in
-// turn; all heads of a piece are given to one XCD, whose L2 then serves B and C
-// of the piece to the heads that share them.
+// Workgroups to (piece, head, channel block).  Workgroups go to the 8 XCDs in turn.
+// Each XCD gets an eighth of the heads, of all pieces, so that uneven pieces load
+// them evenly; with a number of heads that is no multiple of 8 it gets whole pieces.
+// Either way the heads that share B and C find them in its L2.
 __device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int64_t &h, int64_t &pb) {
     const int64_t units = a.H * (a.P / kPB);
-    const int64_t i = blockIdx.x >> 3;
-    const int64_t u = i % units;
-    piece = (i / units) * 8 + (blockIdx.x & 7);
+    const int64_t i = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+    int64_t u;
+    if (units % 8 == 0) {
+        const int64_t own = units / 8;
+        piece = i / own;
+        u = xcd * own + (i - piece * own);
+    } else {
+        u = i % units;
+        piece = (i / units) * 8 + xcd;
+    }
     h = u / (a.P / kPB);
     pb = u - h * (a.P / kPB);
 }
-int64_t grid_size(const SsmChainArgs &a) { return (a.pieces + 7) / 8 * 8 * a.H * (a.P / kPB); }
+int64_t grid_size(const SsmChainArgs &a) {
+    const int64_t units = a.H * (a.P / kPB);
+    return (units % 8 == 0 ? a.pieces : (a.pieces + 7) / 8 * 8) * units;
+}
 
 // The decays that M's tiles left of the diagonal take as products around their
 // row tile's first token, both factors at most 1.
