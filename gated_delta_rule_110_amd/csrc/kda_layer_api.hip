@@ -294,8 +294,8 @@ struct SsmPlan {
 // 132 us, with a round and a half 152 us).  Under kFewPieces pieces per sequence, two
 // rounds: the first pass leaves out the last piece, and one of few leaves CUs idle
 // (6 x 4000 tokens x 40 heads: 213 us, with one 285 us).  A packed batch's pieces are
-// uneven, and two rounds even them out (32768 tokens in 17 sequences: 463 us, with one
-// 635 us).
+// uneven, and two rounds even them out (32768 tokens in 17 sequences: 434 us, with one
+// 488 us, with three 455 us).
 // Fewer than kMinPiece chunks per piece would leave a piece's state (32 KiB of fp32
 // per 64 channels and 128 entries) larger than its tokens.
 constexpr int64_t kGroups = 512;

@@ -66,7 +66,7 @@ __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) 
     Piece p;
     p.index = index;
     p.valid = false;
-    int64_t begin = 0, len = a.T, k;
+    int64_t begin = 0, len = a.T, k, per = a.pc;
     if (index >= a.pieces) return p;
     if (a.cu) {
         if (index >= a.piece_off[a.seqs]) return p;
@@ -74,15 +74,20 @@ __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) 
         k = index - a.piece_off[p.n];
         begin = clamp_to(a.cu[p.n], a.T);
         len = clamp_to(a.cu[p.n + 1], a.T) - begin;
+        if (len <= 0) return p;
+        // as many pieces as of pc chunks, but even ones (1 to 3% less time than with a rest)
+        const uint32_t chunks = (uint32_t)((len + kL - 1) / kL);
+        const uint32_t pieces = (chunks + (uint32_t)a.pc - 1) / (uint32_t)a.pc;
+        per = (chunks + pieces - 1) / pieces;
         p.row0 = 0;
-        p.chunk0 = a.chunk_off[p.n] + k * a.pc;
+        p.chunk0 = a.chunk_off[p.n] + k * per;
     } else {
         p.n = index / a.pps;
         k = index - p.n * a.pps;
         p.row0 = p.n;
-        p.chunk0 = p.n * a.cps + k * a.pc;
+        p.chunk0 = p.n * a.cps + k * per;
     }
-    const int64_t from = k * a.pc * kL, size = (int64_t)a.pc * kL;
+    const int64_t from = k * per * kL, size = per * kL;
     p.t0 = begin + from;
     p.count = (int)(len - from < size ? len - from : size);
     p.first = k == 0;

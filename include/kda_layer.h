@@ -147,7 +147,8 @@ typedef struct {
     void *workspace;
     size_t workspace_bytes;
     /* 64-token chunks per piece of a state chain: 0 for the library's rule
-     * (kda_ssm_piece_chunks), n > 0 for n.  A piece is what one workgroup walks
+     * (kda_ssm_piece_chunks), n > 0 for n (at most n in a packed batch, whose
+     * sequences are cut evenly).  A piece is what one workgroup walks
      * through in order; shorter pieces make more of them, and where a sequence
      * has several, its tokens are read twice (once for the pieces' states). */
     int64_t piece_chunks;
