@@ -22,8 +22,8 @@
 // another.  Per chunk and wave the outputs' pass spends 8800 cycles: 1200 on C S^T and
 // 2000 on the update, both near the matrix cores' rate with two workgroups a CU, 2300
 // on M and 1100 on M x, which wait for LDS and for each other, 1700 on staging and
-// barriers.  32768 packed tokens of 32 heads of 128 x 128: 451 us; 131072 tokens of 4
-// heads of 64 x 64: 98 us.
+// barriers.  32768 packed tokens of 32 heads of 128 x 128: 431 us; 131072 tokens of 4
+// heads of 64 x 64: 97 us.
 //
 // Work.  Chains are serial over chunks but independent over heads and over
 // blocks of 64 channels, and 64 x N states leave most of the GPU idle for a

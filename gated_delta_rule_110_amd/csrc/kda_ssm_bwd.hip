@@ -30,10 +30,10 @@
 // S and D into three (2^-25) where F and R come from, which add up in the fp32
 // gradients of A_log and dt_bias; x, B, C and d_out are exact.
 //
-// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 493 us: 260 here (250, and
+// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 489 us: 260 here (250, and
 // 11 for the sums of shares and parameters), the rest the chains of both directions
-// (40 + 44 the pieces, 8 + 8 their joins, 80 + 83 the chunks' states, 268 MB each,
-// written at 3.4 TB/s).  One workgroup fits a CU, its waves in step; of 16000 cycles a
+// (43 + 45 the pieces, 8 + 8 their joins, 73 + 77 the chunks' states, 268 MB each,
+// written at 3.6 TB/s).  One workgroup fits a CU, its waves in step; of 16000 cycles a
 // head they spend 3300 on M and W, 2300 on dx, 6800 on dB and dC, 2000 on staging and
 // the rest in barriers.  LDS is busy for 46% of the time, the matrix cores for 18%:
 // latency and LDS reads, not memory (0.45 GB, 1.8 TB/s).
