@@ -23,7 +23,7 @@
 // 2000 on the update, both near the matrix cores' rate with two workgroups a CU, 2300
 // on M and 1100 on M x, which wait for LDS and for each other, 1700 on staging and
 // barriers.  32768 packed tokens of 32 heads of 128 x 128: 431 us; 131072 tokens of 4
-// heads of 64 x 64: 97 us.
+// heads of 64 x 64: 94 us.
 //
 // Work.  Chains are serial over chunks but independent over heads and over
 // blocks of 64 channels, and 64 x N states leave most of the GPU idle for a
@@ -507,8 +507,9 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 // place of the pieces' own states: E_0 = h0, E_{k+1} = 2^decay_k E_k + own_k (last
 // to first when reversed).  Sequences without tokens get their final state here.
 // One thread per 4 entries of a head's state; the loads of kBatch pieces are in
-// flight together, the sums wait for nothing else.
+// flight together, and the next ones' while they are added up.
 constexpr int kBatch = 8;
+template <bool k> struct Flag { static constexpr bool value = k; };
 
 template <int kN, bool kReverse>
 __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) {
@@ -539,29 +540,54 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) 
         }
         f4 *state = reinterpret_cast<f4 *>(a.state + h * size + off);
         const int64_t step = a.H * size / 4;
-        for (int64_t i0 = 0; i0 < count; i0 += kBatch) {
-            f4 own[kBatch];
-            float d[kBatch];
+        auto piece = [&](int64_t i) { return first + (kReverse ? count - 1 - i : i); };
+        // Many pieces: no branches around the loads, and the last place read again behind the
+        // last one; few: no loads that nothing takes (nothing takes the last one's state).
+        auto load = [&](int64_t i0, f4 (&own)[kBatch], float (&d)[kBatch], auto many) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int64_t k = first + (kReverse ? count - 1 - i0 - i : i0 + i);
-                own[i] = f4{0.f, 0.f, 0.f, 0.f};
-                d[i] = 0.f;
-                if (i0 + i + 1 < count) {
-                    own[i] = state[k * step];
-                    d[i] = a.decay[k * a.H + h];
-                }
+                const int64_t k = piece(i0 + i < count ? i0 + i : count - 1);
+                if (!decltype(many)::value && i0 + i + 1 >= count) break;
+                own[i] = state[k * step];
+                d[i] = a.decay[k * a.H + h];
             }
+        };
+        auto walk = [&](int64_t i0, const f4 (&own)[kBatch], const float (&d)[kBatch], int n) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int64_t k = first + (kReverse ? count - 1 - i0 - i : i0 + i);
-                if (i0 + i >= count) break;
-                state[k * step] = E;
+                if (i >= n) break;
+                state[piece(i0 + i) * step] = E;
                 const float m = __builtin_amdgcn_exp2f(d[i]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) E[e] = m * E[e] + own[i][e];
             }
+        };
+        f4 own0[kBatch], own1[kBatch];
+        float d0[kBatch], d1[kBatch];
+        int64_t i0 = 0;
+        if (count < 2 * kBatch) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                own0[i] = f4{0.f, 0.f, 0.f, 0.f};
+                d0[i] = 0.f;
+            }
+            for (; i0 < count; i0 += kBatch) {
+                load(i0, own0, d0, Flag<false>{});
+                walk(i0, own0, d0, (int)(count - i0));
+            }
+            continue;
         }
+        load(0, own0, d0, Flag<true>{});
+        for (; i0 + 2 * kBatch <= count; i0 += 2 * kBatch) {
+            load(i0 + kBatch, own1, d1, Flag<true>{});
+            walk(i0, own0, d0, kBatch);
+            load(i0 + 2 * kBatch, own0, d0, Flag<true>{});
+            walk(i0 + kBatch, own1, d1, kBatch);
+        }
+        const int left = (int)(count - i0);      // below 2 kBatch, the first of them loaded
+        if (left > kBatch) load(i0 + kBatch, own1, d1, Flag<true>{});
+        walk(i0, own0, d0, left);
+        if (left > kBatch) walk(i0 + kBatch, own1, d1, left - kBatch);
     }
 }
 

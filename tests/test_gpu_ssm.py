@@ -508,3 +508,28 @@ def test_a_training_and_a_generation_step_together():
         R.check_norm(c.reshape(2, D), rc1, 2.0 ** -8, "one token's convolution")
         R.check_norm(o1[:, 0], ro1, 2.0 ** -8, "one token's output")
         R.check_norm(ss, rs1, 2.0 ** -20, "state after it")
+
+
+@pytest.mark.parametrize("lens", [[64 * 15, 64 * 16, 64 * 17 - 3], [64 * 24, 64 * 31 + 1], [64 * 33, 5, 64 * 8]])
+def test_many_pieces(lens):
+    """The join of the pieces' states at counts around its batches of 8 and 16, against one piece per sequence."""
+    H, P, S = 2, 64, 64
+    T, N = sum(lens), len(lens)
+    a, s = make(1, T, H, P, 1, S, N, F32, seed=41)
+    dy, dfin = loss_grads(a, s, N, 42)
+    cu = torch.tensor(R.bounds(lens), dtype=torch.int64, device="cuda")
+    say("case ssm pieces of one chunk, lengths %s" % lens)
+    got, fin = [], []
+    for pc in (1, 1 << 20):
+        f = torch.empty_like(s)
+        y, _ = kda.ssm_fwd(*a.values(), initial_state=s, final_state=f, cu_seqlens=cu, piece_chunks=pc)
+        g = kda.ssm_bwd(*a.values(), dy, d_final_state=dfin, initial_state=s, cu_seqlens=cu, piece_chunks=pc)
+        torch.cuda.synchronize()
+        got.append(y.float())
+        fin.append((f, g["d_initial_state"], g["dx"].float()))
+    # the joins round each state once more per piece, in fp32, and the decays before it shrink what they round:
+    # within REL of the states, and one rounding to bf16 (two halves) of the outputs
+    for p, q in zip(fin[0][:2], fin[1][:2]):
+        assert float((p - q).norm()) <= REL * float(q.norm())
+    for p, q in ((got[0], got[1]), (fin[0][2], fin[1][2])):
+        assert float((p - q).abs().max()) <= (2.0 ** -8 + GREL) * float(q.abs().max())
