@@ -10,10 +10,9 @@
 // update), with every decay at most 1, so that nothing overflows.
 //
 // x, B and C are bf16, exact as operands.  What is computed in fp32 and then
-// needed as an operand is split into bf16 parts: M and S into two (together
-// 2^-17: their products only reach the bf16 output), the weighted x into three
-// (2^-25, fp32's own step: they add up in the fp32 state).  States, decays and
-// sums stay in fp32.
+// needed as an operand (M, S, the weighted x) is split into three bf16 parts,
+// together 2^-25, half of fp32's own step: the products are those of fp32.  States,
+// decays and sums stay in fp32.
 //
 // What bounds it.  8192 tokens of 64 heads of 64 x 128 take 118 us (36 for the pieces'
 // states, 8 to join them, 74 for the outputs), where the tensors alone would take 27:
@@ -132,7 +131,7 @@ struct __align__(16) ChainSmem {
     uint16_t k[kL * kPitch<kN>];
     uint16_t c[kOut ? kL * kPitch<kN> : 8];
     uint16_t x[kL * kXPitch];                   // and then the chunk's outputs, on their way to whole rows
-    uint16_t m[kOut ? 2 * 4 * 2 * 64 * 8 : 8];  // M, two parts, as operands: [part][row tile][k block][lane][8]
+    uint16_t m[kOut ? kParts * 4 * 2 * 64 * 8 : 8];  // M as operands: [part][row tile][k block][lane][8]
     Steps s[2];                                 // of this chunk and the next
     TileDecays t[kOut ? 2 : 1];
 };
@@ -297,9 +296,9 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         tile_decays(sm.s[0], sm.t[0]);
         rdt = raw_dt(1);
     }
-    if (kOut && w < 2) {  // M's tiles (0, 1) and (2, 3) are zero: half an operand each, both parts
+    if (kOut && w < 2) {  // M's tiles (0, 1) and (2, 3) are zero: half an operand each, all parts
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < kParts; ++part)
             *reinterpret_cast<s4 *>(&sm.m[(((4 * part + 2 * w) * 2 + w) * 64 + lane) * 8 + 4]) = s4{0, 0, 0, 0};
     }
     auto keep_state = [&](int c) {
@@ -358,10 +357,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
             };
             auto keep = [&](const int it, const int jt, f4 m) {
                 float v[4] = {m[0], m[1], m[2], m[3]};
-                const uint32_t h0 = round_pair(v[0], v[1]), h1 = round_pair(v[2], v[3]);
-                uint16_t *to = &sm.m[((it * 2 + (jt >> 1)) * 64 + lane) * 8 + 4 * (jt & 1)];
-                *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
-                *reinterpret_cast<uint2 *>(to + 4 * 2 * 64 * 8) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
+                keep_parts(v, &sm.m[((it * 2 + (jt >> 1)) * 64 + lane) * 8 + 4 * (jt & 1)], 4 * 2 * 64 * 8);
             };
             auto left = [&](const int it, const int jt, f4 cb) {
                 const float upto = td.upto[16 * it + r];
@@ -411,16 +407,16 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                     v[e] = S[2 * q][e];
                     v[4 + e] = S[2 * q + 1][e];
                 }
-                s8 hi, lo;
-                split2(v, hi, lo);
+                s8 sv[kParts];
+                split3(v, sv[0], sv[1], sv[2]);
                 // products into one accumulator are four apart: none waits for the one before
                 s8 cv[4];
 #pragma unroll
                 for (int it = 0; it < 4; ++it) cv[it] = lds8(sm.c + (16 * it + r) * kPitch<kN> + 32 * q + 8 * g);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) y[it] = mfma16x16x32_bf16(hi, cv[it], y[it]);
+                for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                for (int it = 0; it < 4; ++it) y[it] = mfma16x16x32_bf16(lo, cv[it], y[it]);
+                    for (int it = 0; it < 4; ++it) y[it] = mfma16x16x32_bf16(sv[part], cv[it], y[it]);
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -448,7 +444,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[4 * half + e] = wv[e] * bf16_bits_to_f32((uint16_t)xf[kb][4 * half + e]);
             }
-            s8 xs[3];
+            s8 xs[kParts];
             split3(v, xs[0], xs[1], xs[2]);
 #pragma unroll
             for (int t0 = 0; t0 < kTiles; t0 += kGroup) {
@@ -460,7 +456,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
                     kv[t - t0] = join(read_tr(q), read_tr(q + 16 * kPitch<kN>));
                 }
 #pragma unroll
-                for (int part = 0; part < 3; ++part)
+                for (int part = 0; part < kParts; ++part)
 #pragma unroll
                     for (int t = t0; t < t0 + kGroup; ++t)
                         S[t] = kSwapped ? mfma16x16x32_bf16(xs[part], kv[t - t0], S[t]) : mfma16x16x32_bf16(kv[t - t0], xs[part], S[t]);
@@ -473,7 +469,7 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < kParts; ++part)
 #pragma unroll
                     for (int it = 2 * kb; it < 4; ++it)
                         y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);

@@ -25,10 +25,8 @@
 //
 // One workgroup of 8 waves takes a chunk, a group of B and C and a share of its
 // heads, one head and 64 channels after the other: C B^T is computed once for
-// all of them, and dB and dC add up in registers.  The products' fp32 operands are
-// split into bf16 parts: M and W into two (2^-17; they reach bf16 gradients only),
-// S and D into three (2^-25) where F and R come from, which add up in the fp32
-// gradients of A_log and dt_bias; x, B, C and d_out are exact.
+// all of them, and dB and dC add up in registers.  The products' fp32 operands (M, W,
+// S, D) are split into three bf16 parts (2^-25); x, B, C and d_out are exact.
 //
 // What bounds it.  8192 tokens of 64 heads of 64 x 128 take 489 us: 260 here (250, and
 // 11 for the sums of shares and parameters), the rest the chains of both directions
@@ -45,10 +43,21 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = 8;
-// Rows of x, d_out and W are read 8 bytes at a time as well as transposed: 16
-// bytes of padding serve the former; M is only read transposed.
+// Rows of x and d_out are read 8 bytes at a time as well as transposed: 16 bytes of
+// padding serve the former.
 constexpr int kRowPitch = kL + 8;
-constexpr int kMPitch = kL + 16;
+
+// M and W (rows i, columns j) hold their 32-column blocks from the diagonal down: 64
+// rows of columns 0 to 31, then rows 32 to 63 of the others.  Three parts of both would
+// not fit LDS as squares.  A row is 64 bytes, unpadded: its 8-byte groups of columns
+// change places by bits 2 and 3 of the row number, so that both the 8-byte and the
+// transposing reads of 16 rows spread over the banks.
+constexpr int kTriPitch = 32, kTri = 96 * kTriPitch;
+// Place of entry (16 it + r, 16 jt + c), where `at` is that of (r, c) in tile (0, 0).
+__device__ __forceinline__ int tri_at(int r, int c) { return r * kTriPitch + (c ^ ((r & 4) << 2 | (r & 8))); }
+__device__ __forceinline__ int tri_tile(int at, int it, int jt) {
+    return (at ^ (jt & 1) << 4) + (16 * it + 16 * (jt & 2)) * kTriPitch;
+}
 
 // A head's sums over channels and state entries, shares of its step sizes' gradient.
 template <int kN>
@@ -61,8 +70,8 @@ template <int kN>
 struct __align__(16) GradSmem {
     uint16_t b[kL * kPitch<kN>], c[kL * kPitch<kN>];
     uint16_t x[kL * kRowPitch], dy[kL * kRowPitch];
-    uint16_t m[2][kL * kMPitch], wm[2][kL * kRowPitch]; // M and W, two parts, rows i
-    uint16_t d[3][kPB * kPitch<kN>];                   // D, three parts, rows = channels
+    uint16_t m[kParts][kTri], wm[kParts][kTri];        // M and W
+    uint16_t d[kParts][kPB * kPitch<kN>];              // D, rows = channels
     Steps s[3];                                        // of the head before, this one and the next
     Sums<kN> sum[2];                                   // of the head before and this one
 };
@@ -77,6 +86,17 @@ __device__ __forceinline__ s8 along_pair(const uint16_t *row, int q, int g) {
 __device__ __forceinline__ s8 across(const uint16_t *base, int pitch, int q, int col, int r, int g) {
     const uint16_t *p = base + (32 * q + 4 * g + (r >> 2)) * pitch + col + 4 * (r & 3);
     return join(read_tr(p), read_tr(p + 16 * pitch));
+}
+
+// The same of M or W, from the lane's place in a tile: rows 32 q .. of column tile jt, and
+// columns 32 q .. of row tile it.
+__device__ __forceinline__ s8 tri_across(const uint16_t *base, int at, int q, int jt) {
+    const uint16_t *p = base + tri_tile(at, 2 * q, jt);
+    return join(read_tr(p), read_tr(p + 16 * kTriPitch));
+}
+__device__ __forceinline__ s8 tri_along(const uint16_t *base, int at, int it, int q) {
+    return join(*reinterpret_cast<const s4 *>(base + tri_tile(at, it, 2 * q)),
+                *reinterpret_cast<const s4 *>(base + tri_tile(at, it, 2 * q + 1)));
 }
 
 template <int k> struct Int { static constexpr int value = k; };
@@ -136,11 +156,11 @@ __device__ __forceinline__ double row_suffix(double v) {
 template <typename T>
 __device__ __forceinline__ void add_to(T *p, T v, bool more) { *p = more ? *p + v : v; }
 
-// Four values in two bf16 parts, `apart` entries from each other.
-__device__ __forceinline__ void keep_pair(float (&v)[4], uint16_t *to, int apart) {
-    const uint32_t h0 = round_pair(v[0], v[1]), h1 = round_pair(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(to) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2 *>(to + apart) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
+// The same value, as computed here: what follows from it is computed anew rather than kept in
+// registers over the loop over the heads, which has none to spare.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // p[i], or 0 without p, by a scalar load; i is the same for the whole wave, and nothing
@@ -204,7 +224,8 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int it = w & 3, kb = w >> 2;           // this wave's tiles of the 64 x 64 products
-    const int nt = w % kTiles, j0 = w / kTiles * kJ;
+    const int nt = w % kTiles, j0 = kTiles < kWaves ? w / kTiles * kJ : 0;
+    const int along_at = tri_at(r, 4 * g), across_at = tri_at(4 * g + (r >> 2), 4 * (r & 3));  // in M and W
     const int H = (int)a.H, heads = H / (int)a.G;  // of the group
     const int h0 = (int)grp * heads + share * a.share;
     const int count = heads - share * a.share < a.share ? heads - share * a.share : a.share;
@@ -234,8 +255,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     }
     if (kb == 0 && it < 2) {                     // tiles (0, 1) and (2, 3) of M and W are zero
         float none[4] = {0.f, 0.f, 0.f, 0.f};
-        keep_pair(none, &sm.m[0][(32 * it + r) * kMPitch + 32 * it + 16 + 4 * g], kL * kMPitch);
-        keep_pair(none, &sm.wm[0][(32 * it + r) * kRowPitch + 32 * it + 16 + 4 * g], kL * kRowPitch);
+        const int at = tri_tile(along_at, 2 * it, 2 * it + 1);
+        keep_parts(none, &sm.m[0][at], kTri);
+        keep_parts(none, &sm.wm[0][at], kTri);
     }
     f4 dB[kJ], dC[kJ];
 #pragma unroll
@@ -425,8 +447,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                         if (r == 15) add_to(reinterpret_cast<f4 *>(&su.over[16 * jt + 4 * g]), over, more);
                     }
                     if (r == 15) add_to(reinterpret_cast<f4 *>(&su.colq[it][16 * jt + 4 * g]), col, more);
-                    keep_pair(m, &sm.m[0][ti * kMPitch + 16 * jt + 4 * g], kL * kMPitch);
-                    keep_pair(wv, &sm.wm[0][ti * kRowPitch + 16 * jt + 4 * g], kL * kRowPitch);
+                    const int at = tri_tile(along_at, it, jt);
+                    keep_parts(m, &sm.m[0][at], kTri);
+                    keep_parts(wv, &sm.wm[0][at], kTri);
                 };
                 float rowe = 0.f, qd = 0.f, dd = 0.f, none = 0.f;
                 if (it == 2 * kb) {
@@ -493,10 +516,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     if (q < half) continue;      // i before j
                     const s8 yv = across(sm.dy, kRowPitch, q, 16 * pt, r, g);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < kParts; ++k)
 #pragma unroll
                         for (int jj = 0; jj < 2; ++jj)
-                            u[jj][k] = mfma16x16x32_bf16(yv, across(sm.m[k], kMPitch, q, 32 * half + 16 * jj, r, g), u[jj][k]);
+                            u[jj][k > 0] = mfma16x16x32_bf16(yv, tri_across(sm.m[k], across_at, q, 2 * half + jj), u[jj][k > 0]);
                 }
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
@@ -508,36 +531,60 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                 }
             }
 
-            // ---- dB and dC, transposed: lane = token, entries 4 neighbouring state entries
+            // ---- dB and dC, transposed: lane = token, entries 4 neighbouring state entries; one
+            // after the other, so that D's parts and S's are not held together
             {
-                s8 Dv[2][2], Sv[3][2];
+                s8 Dv[kParts][2], Ct[2];
                 float xs = 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
+                    Ct[q] = across(sm.c, kPitch<kN>, q, 16 * nt, r, g);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) Dv[k][q] = across(sm.d[k], kPitch<kN>, q, 16 * nt, r, g);
-                    const s8 rest = across(sm.d[2], kPitch<kN>, q, 16 * nt, r, g);
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = S[2 * q][e];
-                        v[4 + e] = S[2 * q + 1][e];
-                    }
-                    split3(v, Sv[0][q], Sv[1][q], Sv[2][q]);
+                    for (int k = 0; k < kParts; ++k) Dv[k][q] = across(sm.d[k], kPitch<kN>, q, 16 * nt, r, g);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        xs += v[e] * (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) +
-                                      (bf16_bits_to_f32((uint16_t)Dv[1][q][e]) + bf16_bits_to_f32((uint16_t)rest[e])));
+                        xs += S[2 * q + (e >> 2)][e & 3] *
+                              (bf16_bits_to_f32((uint16_t)Dv[0][q][e]) +
+                               (bf16_bits_to_f32((uint16_t)Dv[1][q][e]) + bf16_bits_to_f32((uint16_t)Dv[2][q][e])));
                 }
                 xs = wave_sum(xs);
                 if (lane == 63 && j0 == 0) add_to(&su.xs[nt], xs, more);
-                fetch(u + 1, kS);
-                s8 Ct[2], Bt[2];
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int tt = j0 + j, t = 16 * tt + r;
+                    f4 u = {0.f, 0.f, 0.f, 0.f}, v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const s8 xv = along_pair(sm.x + t * kRowPitch, q, g);
+                        u = mfma16x16x32_bf16(Dv[0][q], xv, u);
+                        v = mfma16x16x32_bf16(Dv[1][q], xv, v);
+                        v = mfma16x16x32_bf16(Dv[2][q], xv, v);
+                    }
+                    const float wt = st.w[t];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dB[j][e] += wt * (u[e] + v[e]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (2 * q + 1 < tt) continue;  // i from token tile tt on
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k)
+                            dB[j] = mfma16x16x32_bf16(Ct[q], tri_across(sm.wm[k], across_at, q, tt), dB[j]);
+                    }
+                }
+            }
+            {
+                const int own = here(lane), r = own & 15, g = own >> 4;
+                const int along_at = tri_at(r, 4 * g);
+                s8 Sv[kParts][2], Bt[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    Ct[q] = across(sm.c, kPitch<kN>, q, 16 * nt, r, g);
                     Bt[q] = across(sm.b, kPitch<kN>, q, 16 * nt, r, g);
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = S[2 * q + (e >> 2)][e & 3];
+                    split3(v, Sv[0][q], Sv[1][q], Sv[2][q]);
                 }
+                fetch(u + 1, kS);
                 float rr[kJ];
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) {
@@ -545,37 +592,27 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
                     f4 u = {0.f, 0.f, 0.f, 0.f}, v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const s8 xv = along_pair(sm.x + t * kRowPitch, q, g), yv = along_pair(sm.dy + t * kRowPitch, q, g);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            u = mfma16x16x32_bf16(Dv[k][q], xv, u);
-                            v = mfma16x16x32_bf16(Sv[k][q], yv, v);
-                        }
+                        const s8 yv = along_pair(sm.dy + t * kRowPitch, q, g);
+                        u = mfma16x16x32_bf16(Sv[0][q], yv, u);
+                        v = mfma16x16x32_bf16(Sv[1][q], yv, v);
                         v = mfma16x16x32_bf16(Sv[2][q], yv, v);
                     }
                     const s4 cv = *reinterpret_cast<const s4 *>(sm.c + t * kPitch<kN> + 16 * nt + 4 * g);
+                    const float et = st.from[t];
                     float f = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f += bf16_bits_to_f32((uint16_t)cv[e]) * v[e];
-                    rr[j] = rows_sum(f);
-                    const float wt = st.w[t], et = st.from[t];
-#pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        dB[j][e] += wt * u[e];
-                        dC[j][e] += et * v[e];
+                        const float s = u[e] + v[e];
+                        f += bf16_bits_to_f32((uint16_t)cv[e]) * s;
+                        dC[j][e] += et * s;
                     }
+                    rr[j] = rows_sum(f);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        if (2 * q + 1 >= tt) {   // i from token tile tt on
+                        if (2 * q > tt) continue;      // j up to token tile tt
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                dB[j] = mfma16x16x32_bf16(Ct[q], across(sm.wm[k], kRowPitch, q, 16 * tt, r, g), dB[j]);
-                        }
-                        if (2 * q <= tt) {       // j up to it
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                dC[j] = mfma16x16x32_bf16(Bt[q], along_pair(sm.wm[k] + t * kRowPitch, q, g), dC[j]);
-                        }
+                        for (int k = 0; k < kParts; ++k)
+                            dC[j] = mfma16x16x32_bf16(Bt[q], tri_along(sm.wm[k], along_at, tt, q), dC[j]);
                     }
                 }
 #pragma unroll

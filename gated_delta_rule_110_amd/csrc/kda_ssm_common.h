@@ -68,8 +68,9 @@ struct Rows {
     }
 };
 
-// Splits of fp32 values into two or three bf16 parts, each rounded to nearest
-// and the next taken from what it left, two values at a time.
+// Splits of fp32 values into three bf16 parts (24 bits, fp32's own), each rounded to
+// nearest and the next taken from what it left, two values at a time.
+constexpr int kParts = 3;
 typedef float f2v __attribute__((ext_vector_type(2)));
 typedef __bf16 b2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t round_pair(float &a, float &b) {
@@ -80,17 +81,6 @@ __device__ __forceinline__ uint32_t round_pair(float &a, float &b) {
 }
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{a, b}, b2v));
-}
-__device__ __forceinline__ void split2(const float *x, s8 &hi, s8 &lo) {
-    u4v h, l;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float a = x[2 * j], b = x[2 * j + 1];
-        h[j] = round_pair(a, b);
-        l[j] = pack_pair(a, b);
-    }
-    hi = __builtin_bit_cast(s8, h);
-    lo = __builtin_bit_cast(s8, l);
 }
 __device__ __forceinline__ void split3(const float *x, s8 &p, s8 &q, s8 &r) {
     u4v h, m, l;
@@ -104,6 +94,15 @@ __device__ __forceinline__ void split3(const float *x, s8 &p, s8 &q, s8 &r) {
     p = __builtin_bit_cast(s8, h);
     q = __builtin_bit_cast(s8, m);
     r = __builtin_bit_cast(s8, l);
+}
+// Four values in their parts, `apart` entries from each other.
+__device__ __forceinline__ void keep_parts(float (&v)[4], uint16_t *to, int apart) {
+#pragma unroll
+    for (int part = 0; part < kParts - 1; ++part) {
+        const uint32_t h0 = round_pair(v[0], v[1]), h1 = round_pair(v[2], v[3]);
+        *reinterpret_cast<uint2 *>(to + part * apart) = make_uint2(h0, h1);
+    }
+    *reinterpret_cast<uint2 *>(to + (kParts - 1) * apart) = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
 }
 
 // Inclusive running sum over the 64 lanes, in 64 bits: within rows of 16 lanes,
