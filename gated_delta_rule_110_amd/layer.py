@@ -56,7 +56,6 @@ class KdaSsmDesc(ctypes.Structure):
 def _declare(lib) -> None:
     """Argument types of the layer operators (called once, when the library is loaded)."""
     global _lib
-    _lib = lib
     N, C, S = (ctypes.POINTER(t) for t in (KdaRmsnormDesc, KdaConvDesc, KdaSsmDesc))
     for name, n, desc in (("kda_rmsnorm_fwd", 5, N), ("kda_rmsnorm_quant", 6, N), ("kda_rmsnorm_bwd", 7, N),
                           ("kda_conv_fwd", 7, C), ("kda_conv_decode", 6, C), ("kda_conv_bwd", 11, C),
@@ -70,6 +69,7 @@ def _declare(lib) -> None:
                              ("kda_ssm_bwd_workspace_size", S, ctypes.c_size_t)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = kind, [desc]
+    _lib = lib  # last: other threads call what they find here
 
 
 _lib = None

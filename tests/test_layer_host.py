@@ -186,3 +186,24 @@ def test_binding_refuses_cpu_tensors():
                 lambda: kda.ssm_fwd(x[..., None], x, x[..., None], x[..., None], w)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_the_library_is_published_with_its_types(monkeypatch):
+    """Another thread may look while the first call declares the functions: it must not find a library whose
+    functions still take anything."""
+    class Function:
+        restype = argtypes = None
+
+    class Library:
+        def __init__(self):
+            self.functions, self.seen = {}, []
+
+        def __getattr__(self, name):
+            self.seen.append(L._lib)
+            return self.functions.setdefault(name, Function())
+
+    fake = Library()
+    monkeypatch.setattr(L, "_lib", None)
+    L._declare(fake)
+    assert fake.seen and all(s is None for s in fake.seen)
+    assert L._lib is fake and all(f.argtypes is not None for f in fake.functions.values())
