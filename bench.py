@@ -113,7 +113,7 @@ def cpu_baseline(w, target_s: float = 10.0):
 # The files each kernel's code and launch depend on: its own source (which
 # holds its launcher and grid), the shared header, the public header and the
 # build flags; for split chains also kda_api.hip, which chooses the segments.
-_COMMON_SOURCES = ["kda_common.h", "../_build.py"]
+_COMMON_SOURCES = ["kda_common.h"]
 KERNEL_SOURCES = {
     "kda_intra_kernel": ["kda_intra.hip", "kda_intra_body.h"],
     "kda_chain_kernel": ["kda_chain.hip"],
@@ -189,6 +189,8 @@ def source_digest(kernel=None) -> str:
     build flags the library is built from: all of them, or those ``kernel`` is
     built and launched from."""
     import hashlib
+
+    from gated_delta_rule_110_amd import _build
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "gated_delta_rule_110_amd", "csrc")
     names = (sorted(os.listdir(csrc)) + ["../../include/kda.h", "../_build.py"] if kernel is None
@@ -199,6 +201,9 @@ def source_digest(kernel=None) -> str:
             h.update(name.encode())
             with open(path, encoding="utf-8") as f:
                 h.update(_code_only(name, f.read()).encode())
+    if kernel is not None:  # the flags of its own sources; those of other kernels' do not matter
+        flags = {n: _build.EXTRA_FLAGS.get(n, []) for n in KERNEL_SOURCES[kernel] if n.endswith(".hip")}
+        h.update(json.dumps([_build.HIPCC_FLAGS, flags], sort_keys=True).encode())
     return h.hexdigest()
 
 

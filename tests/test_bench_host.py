@@ -91,6 +91,22 @@ def test_kernel_digests_cover_their_sources():
     assert bench.source_digest("split_chain") != bench.source_digest("kda_chain_kernel")
 
 
+def test_kernel_digests_cover_their_own_flags(monkeypatch):
+    """A summary is stale when the flags of its kernel's source change, and only then: not when another source is
+    added to the library or built differently."""
+    from gated_delta_rule_110_amd import _build
+
+    before = {k: bench.source_digest(k) for k in bench.KERNEL_SOURCES}
+    monkeypatch.setattr(_build, "SOURCES", _build.SOURCES + ["kda_other.hip"])
+    monkeypatch.setitem(_build.EXTRA_FLAGS, "kda_other.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"])
+    assert before == {k: bench.source_digest(k) for k in bench.KERNEL_SOURCES}
+    monkeypatch.setitem(_build.EXTRA_FLAGS, "kda_decode.hip", ["-O2"])
+    for k, files in bench.KERNEL_SOURCES.items():
+        assert (bench.source_digest(k) != before[k]) == ("kda_decode.hip" in files), k
+    monkeypatch.setattr(_build, "HIPCC_FLAGS", _build.HIPCC_FLAGS + ["-g"])
+    assert not any(bench.source_digest(k) == before[k] for k in bench.KERNEL_SOURCES)
+
+
 def test_digest_ignores_comments_only():
     code = "int f(int x) {  // add one\n  return x + 1; /* done */ }\n"
     assert bench._code_only("a.hip", code) == bench._code_only("a.hip", code.replace("add one", "increment"))
