@@ -134,6 +134,7 @@ struct __align__(16) ChainSmem {
     uint16_t m[kOut ? kParts * 4 * 2 * 64 * 8 : 8];  // M as operands: [part][row tile][k block][lane][8]
     Steps s[2];                                 // of this chunk and the next
     TileDecays t[kOut ? 2 : 1];
+    int special;                                // outputs to be taken again
 };
 
 // By the wave that wrote the steps, lane = token, from what the lane itself wrote and
@@ -174,10 +175,58 @@ __device__ __forceinline__ void store_state8(void *p, int64_t i, int f32, const 
     }
 }
 
+// NaN and infinities in x.  M's zeros above the diagonal carry them to the tokens
+// before, as products of M x do, and to every token of the chunk's last tile, where a
+// test of 4 values a lane finds them.  A piece with any there is walked through again,
+// its waves then leaving them out of M x and adding their products to the tokens from
+// theirs on one by one.  (Doing so at once, behind a test of x, put branches into every
+// chunk: a packed prompt of 32768 tokens x 32 heads 487 us, this way 473, without 464.)
+__device__ __forceinline__ bool is_special(uint32_t bits16) { return (bits16 & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool any_special(const s8 (&x)[2]) {
+    uint32_t full = 0;                           // bit 15 of a half: its exponent has all bits set
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) full |= (__builtin_bit_cast(u4v, x[kb])[j] & 0x7f807f80u) + 0x00800080u;
+    return __builtin_amdgcn_ballot_w64((full & 0x80008000u) != 0) != 0;
+}
+__device__ __forceinline__ void finite_only(s8 (&x)[2]) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[kb][e] = is_special((uint16_t)x[kb][e]) ? (short)0 : x[kb][e];
+}
+// y, lane = token 16 it + r, entries the 4 channels at `x` (token 0), and M as ChainSmem holds it.
+__device__ __forceinline__ void add_special(const uint16_t *m, const uint16_t *x, f4 (&y)[4]) {
+    const int r = threadIdx.x & 15;
+#pragma unroll 1
+    for (int j = 0; j < kL; ++j) {
+        const s4 xj = *reinterpret_cast<const s4 *>(x + j * kXPitch);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= is_special((uint16_t)xj[e]);
+        if (__builtin_amdgcn_ballot_w64(any) == 0) continue;
+        const int jt = j >> 4;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            if (it < jt) continue;
+            float mij = 0.f;
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part)
+                mij += bf16_bits_to_f32(m[(((4 * part + it) * 2 + (jt >> 1)) * 64 + 16 * ((j & 15) >> 2) + r) * 8 + 4 * (jt & 1) + (j & 3)]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (16 * it + r >= j && is_special((uint16_t)xj[e])) y[it][e] += mij * bf16_bits_to_f32((uint16_t)xj[e]);
+        }
+    }
+}
+
 // kReverse: the chains of the gradient of the state, from the last token to the
 // first: D <- e^{G_63} D + sum_i e^{G_i} d_out_i C_i^T.
-template <int kN, int kPass, bool kReverse>
-__global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_chain_kernel(SsmChainArgs a) {
+// With kCausal, a NaN or infinity in x as add_special has it; otherwise returns whether
+// that is needed.
+template <int kN, int kPass, bool kReverse, bool kCausal>
+__device__ __forceinline__ bool walk_piece(const SsmChainArgs &a, ChainSmem<kN, kPass == kOutputs> &sm) {
     constexpr bool kOut = kPass == kOutputs;
     // The states that the gradient reads are kept as accumulators hold them, 16
     // bytes a lane: those of the scan as S (rows: channels), so that a pair of
@@ -185,12 +234,11 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     constexpr bool kSwapped = kPass == kSave && !kReverse;
     constexpr int kTiles = kN / 16, kQ = kN / 32;
     constexpr int kGroup = kOut ? 4 : 1;  // state tiles updated side by side, as registers allow
-    __shared__ ChainSmem<kN, kOut> sm;
     int64_t index, h, pb;
     place(a, index, h, pb);
     const Piece p = piece_of(a, index);
-    if (!p.valid) return;
-    if (kPass == kPieces && (kReverse ? p.first : p.last)) return;  // nothing follows it
+    if (!p.valid) return false;
+    if (kPass == kPieces && (kReverse ? p.first : p.last)) return false;  // nothing follows it
 
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -289,6 +337,8 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
     // (3, 0); rows 3 of columns 1 and 2
     const int it0 = w == 0 ? 1 : w == 1 ? 2 : 3, jt0 = w == 0 ? 0 : 1, it1 = w == 0 ? 2 : 3, jt1 = w == 2 ? 2 : 0;
     float total = 0.f;
+    [[maybe_unused]] bool seen = false;
+    if (kOut && threadIdx.x == 0) sm.special = 0;
     // Outputs: the next chunk's step sizes are taken beside this one's M, by a wave
     // with few of its tiles.
     if (kOut && w == kStepper) {
@@ -465,6 +515,8 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         // ---- outputs from the chunk's own tokens
         if constexpr (kOut) {
             fetch(i + 1, kC);
+            const bool special = kCausal && any_special(xf);
+            if (special) finite_only(xf);
             lds_barrier();
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -473,6 +525,9 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
 #pragma unroll
                     for (int it = 2 * kb; it < 4; ++it)
                         y[it] = mfma16x16x32_bf16(xf[kb], lds8(&sm.m[(((4 * part + it) * 2 + kb) * 64 + lane) * 8]), y[it]);
+            if (special) add_special(sm.m, sm.x + 16 * w + 4 * g, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) seen |= !kCausal && !__builtin_isfinite(y[3][e]);
 #pragma unroll
             for (int it = 0; it < 4; ++it)
                 *reinterpret_cast<uint2 *>(sm.x + (16 * it + r) * kXPitch + 16 * w + 4 * g) =
@@ -480,7 +535,12 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
         }
     }
     if constexpr (kOut) {
+        if (seen) sm.special = 1;
         lds_barrier();
+        if (!kCausal && __builtin_amdgcn_readfirstlane(sm.special)) {
+            lds_barrier();
+            return true;
+        }
         take();
         put(p.count - (chunks - 1) * kL);
     }
@@ -497,6 +557,22 @@ __global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_c
             store_state8(dst, (kPass == kPieces ? spiece : sseq) + 32 * q, kPass == kPieces ? 1 : a.ht_f32, S[2 * q], S[2 * q + 1]);
     }
     if (kPass == kPieces && threadIdx.x == 0 && pb == 0) a.decay[p.index * a.H + h] = total;
+    return false;
+}
+
+template <int kN, int kPass, bool kReverse>
+__global__ __launch_bounds__(kThreads, kPass == kOutputs ? 2 : 4) void kda_ssm_chain_kernel(SsmChainArgs a) {
+    __shared__ ChainSmem<kN, kPass == kOutputs> sm;
+    const bool again = walk_piece<kN, kPass, kReverse, false>(a, sm);
+    if constexpr (kPass == kOutputs) {
+        if (again) {
+            // the arguments are read anew: kept over the first walk, they would take its registers
+            auto p = (const __attribute__((address_space(4))) SsmChainArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+            asm volatile("" : "+s"(p));
+            const SsmChainArgs b = *(const SsmChainArgs *)p;
+            walk_piece<kN, kPass, kReverse, true>(b, sm);
+        }
+    }
 }
 
 // The states entering the pieces of every sequence with several of them, in

@@ -537,8 +537,8 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
     ``ssm_workspace_size`` bytes, allocated if None; piece_chunks: 0 or the
     chunks per piece (``kda_ssm_desc_t::piece_chunks``).
 
-    A NaN or infinity in a token reaches its sequence's outputs from the start of
-    its 64-token chunk on, and no other sequence."""
+    A NaN or infinity in a token reaches its sequence's outputs from that token on,
+    and no other sequence."""
     d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks)
     out = _output(out, "out", x.shape, torch.bfloat16, dev)
     lib = _library()
@@ -584,7 +584,10 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
     d_initial_state (fp32 [num_seqs, H, P, N]; None unless wanted, by default
     where an initial_state is given).  Rows behind a packed batch's last sequence
     are left as they were.  outputs: None, or a dict of tensors of those names to
-    write into.  The workspace holds 8 P N bytes per 64-token chunk and head."""
+    write into.  The workspace holds 8 P N bytes per 64-token chunk and head.
+
+    A NaN or infinity in a token reaches all gradients of its 64-token chunk, those
+    of its sequence that depend on the chunk's and the parameters'."""
     d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, d_final_state, cu_seqlens, piece_chunks,
                        "d_final_state")
     _bf16(d_out, "d_out", dev)

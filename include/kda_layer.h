@@ -164,7 +164,8 @@ int64_t kda_ssm_piece_chunks(const kda_ssm_desc_t *desc);
 /* x, dt, B, C: bf16; A_log: fp32 [H]; dt_bias: fp32 [H] or NULL (zeros); D: fp32
  * [H] or NULL (no skip term); initial_state, final_state: [num_seqs, H, P, N] or
  * NULL, final_state may be initial_state when the types match; out: bf16
- * [B, T, H, P]. */
+ * [B, T, H, P].  A NaN or infinity in a token reaches its sequence's outputs from
+ * that token on, and no other sequence. */
 kda_status_t kda_ssm_fwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
                          const float *dt_bias, const float *D, const void *initial_state, void *final_state,
                          const int64_t *cu_seqlens, void *out, const kda_ssm_desc_t *desc, hipStream_t stream);
@@ -179,7 +180,9 @@ kda_status_t kda_ssm_decode(const void *x, const void *dt, const void *Bm, const
  * (ddt_bias and dD may be NULL); d_initial_state: fp32 [num_seqs, H, P, N] or
  * NULL.  The forward's states are computed again, and the state entering every
  * chunk and the gradient of the one leaving it are held in the workspace (2 x 4 P N
- * bytes per chunk and head). */
+ * bytes per chunk and head).  A NaN or infinity in a token reaches all gradients of
+ * its 64-token chunk, those of its sequence that depend on the chunk's and the
+ * parameters'. */
 kda_status_t kda_ssm_bwd(const void *x, const void *dt, const void *Bm, const void *Cm, const float *A_log,
                          const float *dt_bias, const float *D, const void *initial_state,
                          const int64_t *cu_seqlens, const void *d_out, const void *d_final_state, void *dx,

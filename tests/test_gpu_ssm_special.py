@@ -1,0 +1,77 @@
+"""NaN and infinities in the scan's inputs: a prompt's outputs are those of its tokens taken one
+by one, so one in a token reaches that token and those behind it, never those before."""
+import pytest
+import torch
+
+import gated_delta_rule_110_amd as kda
+from tests.parity import say
+from tests.test_gpu_ssm import make
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+def step_by_step(a, s):
+    st, ys = s.clone(), []
+    for t in range(a["x"].shape[1]):
+        one = [v[:, t:t + 1] if k in ("x", "dt", "B", "C") else v for k, v in a.items()]
+        ys.append(kda.ssm_decode(*one, initial_state=st, final_state=st)[0])
+    return torch.cat(ys, 1), st
+
+
+def check(a, clean, s, label, pc=0):
+    y, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), piece_chunks=pc)
+    want, last = step_by_step(a, s)
+    was, _ = kda.ssm_fwd(*clean.values(), initial_state=s, piece_chunks=pc)
+    ok = want.isfinite()
+    assert torch.equal(y.isfinite(), ok), (label, (y.isfinite() != ok).nonzero()[:5].tolist())
+    assert torch.equal(fin.isfinite(), last.isfinite()), label
+    assert torch.equal(y[ok], was[ok]), label
+
+
+@pytest.mark.parametrize("H,P,G,S", [(2, 64, 1, 64), (4, 128, 2, 128)])
+@pytest.mark.parametrize("t", [0, 5, 15, 16, 40, 63, 64, 100, 129])
+def test_nothing_reaches_the_tokens_before(H, P, G, S, t):
+    clean, s = make(1, 130, H, P, G, S, 1, F32, seed=t)
+    for name, at, value in (("x", (0, t, 1, 7), NAN), ("x", (0, t, 0, P - 1), INF), ("x", (0, t, 1, 16), -INF), ("B", (0, t, 0, 3), NAN),
+                            ("B", (0, t, 0, S - 1), INF), ("C", (0, t, G - 1, 9), NAN), ("C", (0, t, 0, 0), -INF), ("dt", (0, t, 1), NAN),
+                            ("dt", (0, t, 0), INF)):
+        say("case %s = %s at token %d" % (name, value, t))
+        a = {k: v.clone() if k == name else v for k, v in clean.items()}
+        a[name][at] = value
+        check(a, clean, s, (name, value, t), pc=t % 2)
+
+
+def test_several_at_once():
+    clean, s = make(1, 200, 3, 64, 1, 128, 1, F32, seed=3)
+    a = {k: v.clone() if k == "x" else v for k, v in clean.items()}
+    for t, p, v in ((3, 0, INF), (9, 0, -INF), (20, 1, NAN), (20, 2, INF), (63, 3, NAN), (64, 3, NAN), (150, 40, INF), (199, 63, NAN)):
+        a["x"][0, t, t % 3, p] = v
+    check(a, clean, s, "several")
+
+
+def test_padding_that_holds_nan():
+    """A padded batch: what stands behind a row's tokens, in every tensor, leaves their outputs as they are."""
+    lens = [1, 40, 65, 100]
+    a, _ = make(4, 100, 2, 64, 1, 64, 4, None, seed=4)
+    was, _ = kda.ssm_fwd(*a.values())
+    for k in ("x", "dt", "B", "C"):
+        a[k] = a[k].clone()
+        for n, m in enumerate(lens):
+            a[k][n, m:] = NAN
+    y, _ = kda.ssm_fwd(*a.values())
+    for n, m in enumerate(lens):
+        assert torch.equal(y[n, :m], was[n, :m]) and y[n, m:].isnan().all(), n
+
+
+def test_no_step_leaves_everything():
+    """A raw step size of -inf or of the type's lowest value takes no step: the token leaves the state as it was."""
+    a, s = make(1, 70, 2, 64, 1, 64, 1, F32, seed=5)
+    a["dt"][0, 10:20] = -INF
+    a["dt"][0, 30:] = torch.finfo(torch.bfloat16).min
+    check(a, a, s, "no step")
+    keep = {k: v[:, :30] if k in ("x", "dt", "B", "C") else v for k, v in a.items()}
+    _, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s))
+    _, last = kda.ssm_fwd(*keep.values(), initial_state=s, final_state=torch.empty_like(s))
+    assert torch.equal(fin, last)
