@@ -284,9 +284,10 @@ void ssm_reads(Memory &m, const void *x, const void *dt, const void *Bm, const v
 
 // How a call's sequences are cut into pieces, and its workspace.
 struct SsmPlan {
-    int64_t cps, pps, pieces, chunks;   // chunks / pieces per sequence (not packed); both in all (bounds when packed)
+    int64_t cps, pps;                   // chunks / pieces per sequence (not packed)
+    int64_t pieces, chunks, slots;      // in all (bounds when packed); slots: pieces of sequences with several
     int pc;                             // chunks per piece
-    size_t off_piece, off_chunk, off_state, off_decay, total;
+    size_t off_piece, off_chunk, off_slot, off_state, off_decay, total;
 };
 
 // Workgroups a launch should have: the two that fit each of the 256 CUs, at once
@@ -323,17 +324,18 @@ kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     p.chunks = packed ? d->T / 64 + d->num_seqs : d->B * p.cps;
     p.pps = packed ? 0 : (p.cps + pc - 1) / pc;
     p.pieces = packed ? d->T / (64 * pc) + d->num_seqs : d->B * p.pps;
+    // Packed: a sequence of more than 64 pc tokens has under 2 len / (64 pc) pieces.
+    p.slots = packed ? std::min(p.pieces, d->T / (32 * pc)) : p.pps > 1 ? p.pieces : 0;
     p.pc = (int)pc;
     if ((p.pieces + 7) / 8 * 8 > kMaxGroups / units || p.chunks > 0x7fffffff) return KDA_ERR_SHAPE;
     size_t o = 0;
     if (packed) {
         p.off_piece = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
         p.off_chunk = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
+        p.off_slot = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
     }
-    if (packed || p.pps > 1) {
-        p.off_state = o; o = align_up(o + (size_t)p.pieces * (size_t)d->H * (size_t)(d->P * d->N) * 4, 256);
-        p.off_decay = o; o = align_up(o + (size_t)p.pieces * (size_t)d->H * 4, 256);
-    }
+    p.off_state = o; o = align_up(o + (size_t)p.slots * (size_t)d->H * (size_t)(d->P * d->N) * 4, 256);
+    p.off_decay = o; o = align_up(o + (size_t)p.slots * (size_t)d->H * 4, 256);
     p.total = o;
     return KDA_OK;
 }
@@ -405,12 +407,13 @@ SsmChainArgs chain_args(const SsmArgs &a, const SsmPlan &p, const Workspace &ws)
     c.A_log = a.A_log; c.dt_bias = a.dt_bias; c.D = a.D;
     c.cu = a.cu;
     c.T = a.T; c.H = a.H; c.P = a.P; c.G = a.G; c.seqs = a.num_seqs;
-    c.pieces = p.pieces; c.chunks = p.chunks; c.pps = p.pps; c.cps = p.cps; c.pc = p.pc;
+    c.pieces = p.pieces; c.chunks = p.chunks; c.slots = p.slots; c.pps = p.pps; c.cps = p.cps; c.pc = p.pc;
     if (a.cu) {
         c.piece_off = reinterpret_cast<const int32_t *>(ws.at(p.off_piece));
         c.chunk_off = reinterpret_cast<const int32_t *>(ws.at(p.off_chunk));
+        c.slot_off = reinterpret_cast<const int32_t *>(ws.at(p.off_slot));
     }
-    if (a.cu || p.pps > 1) {
+    if (p.slots > 0) {
         c.state = reinterpret_cast<float *>(ws.at(p.off_state));
         c.decay = reinterpret_cast<float *>(ws.at(p.off_decay));
     }
@@ -419,8 +422,9 @@ SsmChainArgs chain_args(const SsmArgs &a, const SsmPlan &p, const Workspace &ws)
 
 hipError_t launch_table(const SsmArgs &a, const SsmPlan &p, const Workspace &ws, hipStream_t s) {
     if (!a.cu) return hipSuccess;
-    return kda_launch_ssm_table(a.cu, a.num_seqs, a.T, p.pc, p.pieces, p.chunks, reinterpret_cast<int32_t *>(ws.at(p.off_piece)),
-                                reinterpret_cast<int32_t *>(ws.at(p.off_chunk)), s);
+    return kda_launch_ssm_table({a.cu, a.num_seqs, a.T, p.pc, p.pieces, p.chunks, p.slots,
+                                 reinterpret_cast<int32_t *>(ws.at(p.off_piece)), reinterpret_cast<int32_t *>(ws.at(p.off_chunk)),
+                                 reinterpret_cast<int32_t *>(ws.at(p.off_slot))}, s);
 }
 
 // The states entering the pieces, and the final states of empty sequences.
@@ -428,7 +432,7 @@ hipError_t launch_table(const SsmArgs &a, const SsmPlan &p, const Workspace &ws,
 hipError_t launch_entering(const SsmChainArgs &c, int N, bool reverse, hipStream_t s) {
     if (!c.cu && c.pps == 1) return hipSuccess;
     hipError_t e = hipSuccess;
-    if (c.T > 0) e = kda_launch_ssm_pieces(c, N, reverse, s);
+    if (c.slots > 0) e = kda_launch_ssm_pieces(c, N, reverse, s);
     if (e == hipSuccess) e = kda_launch_ssm_scan(c, N, reverse, s);
     return e;
 }

@@ -70,7 +70,9 @@ struct SsmArgs {
 // The scan's state chains.  A piece is up to `pc` 64-token chunks of one
 // sequence, walked through in order by one workgroup per (head, 64 channels).
 // The tables of a packed batch give the first piece and the first chunk of
-// every sequence; otherwise every sequence has `pps` pieces and `cps` chunks.
+// every sequence, and the first slot for a piece's state, which only the pieces of
+// sequences with several have; otherwise every sequence has `pps` pieces and `cps`
+// chunks, and the slots are the pieces.
 struct SsmChainArgs {
     const uint16_t *x;         // [tokens, H, P]: x, or d_out backwards
     const uint16_t *k;         // [tokens, G, N]: B, or C backwards
@@ -79,16 +81,16 @@ struct SsmChainArgs {
     int64_t xb, xt, kb, kt, cb, ct, dtb, dtt;
     const float *A_log, *dt_bias, *D;
     const int64_t *cu;
-    const int32_t *piece_off, *chunk_off;
+    const int32_t *piece_off, *chunk_off, *slot_off;
     int64_t T, H, P, G, seqs;
-    int64_t pieces, chunks;    // of the batch (upper bounds when packed)
+    int64_t pieces, chunks, slots;  // of the batch (upper bounds when packed)
     int64_t pps, cps;
     int pc;
     const void *h0;            // state at the chains' start, or nullptr
     void *ht;                  // state at their end, or nullptr
     int h0_f32, ht_f32;
-    float *state;              // [pieces, H, P, N]: every piece's own state, then the one entering it
-    float *decay;              // [pieces, H]: log2 of a piece's decay
+    float *state;              // [slots, H, P, N]: a piece's own state, then the one entering it
+    float *decay;              // [slots, H]: log2 of a piece's decay
     float *save;               // [chunks, H, P / 64, 64 N]: state entering every chunk (kda_ssm.hip)
     uint16_t *out;
 };
@@ -165,9 +167,16 @@ hipError_t kda_launch_conv_decode(const kda::ConvArgs &a, int W, hipStream_t s);
 int64_t kda_conv_parts(int64_t B, int64_t T, int64_t D);
 hipError_t kda_launch_conv_bwd(const kda::ConvArgs &a, int W, hipStream_t s);
 hipError_t kda_launch_ssm_decode(const kda::SsmArgs &a, hipStream_t s);
-// The tables of a packed batch: first piece and first chunk of every sequence.
-hipError_t kda_launch_ssm_table(const int64_t *cu, int64_t N, int64_t T, int pc, int64_t most_pieces,
-                                int64_t most_chunks, int32_t *piece_off, int32_t *chunk_off, hipStream_t s);
+// The tables of a packed batch (SsmChainArgs), [seqs + 1] each; its pieces, chunks and
+// slots are the most that they may count.
+struct SsmTables {
+    const int64_t *cu;
+    int64_t seqs, T;
+    int pc;
+    int64_t pieces, chunks, slots;
+    int32_t *piece_off, *chunk_off, *slot_off;
+};
+hipError_t kda_launch_ssm_table(const SsmTables &a, hipStream_t s);
 // The pieces' own states, from zero (all but a sequence's last piece in walking order).
 hipError_t kda_launch_ssm_pieces(const kda::SsmChainArgs &a, int N, bool reverse, hipStream_t s);
 // The state entering every piece from the pieces' own ones, and the final

@@ -53,7 +53,7 @@ constexpr int kStepper = 3;   // the wave that takes the step sizes
 
 // One piece: its sequence, tokens and place.
 struct Piece {
-    int64_t n, index;          // sequence; number of the piece in the batch
+    int64_t n, slot;           // sequence; slot of the piece's state, where the sequence has several
     int64_t row0, t0;          // batch row and token of its first token
     int count;                 // tokens
     int64_t chunk0;            // number of its first chunk in the batch
@@ -63,7 +63,7 @@ struct Piece {
 
 __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) {
     Piece p;
-    p.index = index;
+    p.slot = index;
     p.valid = false;
     int64_t begin = 0, len = a.T, k, per = a.pc;
     if (index >= a.pieces) return p;
@@ -78,6 +78,8 @@ __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) 
         const uint32_t chunks = (uint32_t)((len + kL - 1) / kL);
         const uint32_t pieces = (chunks + (uint32_t)a.pc - 1) / (uint32_t)a.pc;
         per = (chunks + pieces - 1) / pieces;
+        p.slot = a.slot_off[p.n] + k;
+        if (pieces > 1 && p.slot >= a.slots) return p;  // lengths that no batch has
         p.row0 = 0;
         p.chunk0 = a.chunk_off[p.n] + k * per;
     } else {
@@ -253,7 +255,7 @@ __device__ __forceinline__ bool walk_piece(const SsmChainArgs &a, ChainSmem<kN, 
     uint16_t *orow = kOut ? a.out + ((p.row0 * a.T + p.t0) * a.H + h) * a.P + pb * kPB : nullptr;
     // this lane's rows of a state tensor: channel 16 w + r, entries 32 q + 8 g ..
     const int64_t sbase = (h * a.P + pb * kPB + 16 * w + r) * kN + 8 * g;
-    const int64_t sseq = p.n * a.H * a.P * kN + sbase, spiece = p.index * a.H * a.P * kN + sbase;
+    const int64_t sseq = p.n * a.H * a.P * kN + sbase, spiece = p.slot * a.H * a.P * kN + sbase;
 
     const int chunks = (p.count + kL - 1) / kL;
     // where only the states are kept, what leaves the piece is not needed
@@ -294,7 +296,7 @@ __device__ __forceinline__ bool walk_piece(const SsmChainArgs &a, ChainSmem<kN, 
         const bool whole = p.first && p.last;  // a single piece starts from the initial state itself
         const void *src = whole ? a.h0 : a.state;
         const int f32 = whole ? a.h0_f32 : 1;
-        const int64_t from = whole ? p.n : p.index;
+        const int64_t from = whole ? p.n : p.slot;
         if (src) {
             if constexpr (kSwapped) {
 #pragma unroll
@@ -556,7 +558,7 @@ __device__ __forceinline__ bool walk_piece(const SsmChainArgs &a, ChainSmem<kN, 
         for (int q = 0; q < kQ; ++q)
             store_state8(dst, (kPass == kPieces ? spiece : sseq) + 32 * q, kPass == kPieces ? 1 : a.ht_f32, S[2 * q], S[2 * q + 1]);
     }
-    if (kPass == kPieces && threadIdx.x == 0 && pb == 0) a.decay[p.index * a.H + h] = total;
+    if (kPass == kPieces && threadIdx.x == 0 && pb == 0) a.decay[p.slot * a.H + h] = total;
     return false;
 }
 
@@ -591,20 +593,21 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) 
         const int64_t part = u % per, nh = u / per;
         const int64_t n = nh / a.H, h = nh - n * a.H;
         const int64_t off = part * 4 * kThreads + threadIdx.x * 4;
-        int64_t first, count;
+        int64_t first, count, pieces;
         if (a.cu) {
-            first = a.piece_off[n];
-            count = a.piece_off[n + 1] - first;
+            first = a.slot_off[n];
+            count = a.slot_off[n + 1] - first;
+            pieces = a.piece_off[n + 1] - a.piece_off[n];
         } else {
             first = n * a.pps;
-            count = a.pps;
+            count = pieces = a.pps;
         }
-        if (count == 1) continue;
+        if (pieces > 0 && count < 2) continue;
         f4 E = {0.f, 0.f, 0.f, 0.f};
         if (a.h0)
 #pragma unroll
             for (int e = 0; e < 4; ++e) E[e] = load_any(a.h0, nh * size + off + e, a.h0_f32);
-        if (count == 0) {
+        if (pieces == 0) {
             if (a.ht)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) store_any(a.ht, nh * size + off + e, a.ht_f32, E[e]);
@@ -663,45 +666,46 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_scan_kernel(SsmChainArgs a) 
     }
 }
 
-// First piece and first chunk of every sequence of a packed batch: running sums
+// First piece, chunk and slot of every sequence of a packed batch: running sums
 // over the sequences by one workgroup.  Lengths that overlap (which no batch
-// has) could add up to more pieces than the workspace holds: the tables end there.
-__global__ __launch_bounds__(1024) void kda_ssm_table_kernel(const int64_t *cu, int64_t N, int64_t T, int pc,
-                                                             int64_t most_pieces, int64_t most_chunks,
-                                                             int32_t *piece_off, int32_t *chunk_off) {
-    __shared__ int64_t sp[1024], sc[1024];
+// has) could add up to more than the workspace holds: the tables end there.
+__global__ __launch_bounds__(1024) void kda_ssm_table_kernel(SsmTables a) {
+    __shared__ int64_t sum[3][1024];
+    int32_t *const tables[3] = {a.piece_off, a.chunk_off, a.slot_off};
+    const int64_t most[3] = {a.pieces, a.chunks, a.slots};
     const int tid = threadIdx.x;
-    int64_t pieces = 0, chunks = 0;
-    for (int64_t base = 0; base < N; base += 1024) {
+    int64_t before[3] = {0, 0, 0};
+    for (int64_t base = 0; base < a.seqs; base += 1024) {
         const int64_t n = base + tid;
-        int64_t c = 0, p = 0;
-        if (n < N) {
-            const int64_t len = clamp_to(cu[n + 1], T) - clamp_to(cu[n], T);
-            c = len > 0 ? (len + kL - 1) / kL : 0;
-            p = (c + pc - 1) / pc;
+        int64_t own[3] = {0, 0, 0};
+        if (n < a.seqs) {
+            const int64_t len = clamp_to(a.cu[n + 1], a.T) - clamp_to(a.cu[n], a.T);
+            own[1] = len > 0 ? (len + kL - 1) / kL : 0;
+            own[0] = (own[1] + a.pc - 1) / a.pc;
+            own[2] = own[0] > 1 ? own[0] : 0;
         }
-        sp[tid] = p;
-        sc[tid] = c;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum[k][tid] = own[k];
         __syncthreads();
         for (int d = 1; d < 1024; d <<= 1) {
-            const int64_t vp = tid >= d ? sp[tid - d] : 0, vc = tid >= d ? sc[tid - d] : 0;
+            int64_t v[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[k] = tid >= d ? sum[k][tid - d] : 0;
             __syncthreads();
-            sp[tid] += vp;
-            sc[tid] += vc;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) sum[k][tid] += v[k];
             __syncthreads();
         }
-        if (n < N) {
-            piece_off[n] = (int32_t)clamp_to(pieces + sp[tid] - p, most_pieces);
-            chunk_off[n] = (int32_t)clamp_to(chunks + sc[tid] - c, most_chunks);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (n < a.seqs) tables[k][n] = (int32_t)clamp_to(before[k] + sum[k][tid] - own[k], most[k]);
+            before[k] += sum[k][1023];
         }
-        pieces += sp[1023];
-        chunks += sc[1023];
         __syncthreads();
     }
-    if (tid == 0) {
-        piece_off[N] = (int32_t)clamp_to(pieces, most_pieces);
-        chunk_off[N] = (int32_t)clamp_to(chunks, most_chunks);
-    }
+    if (tid == 0)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) tables[k][a.seqs] = (int32_t)clamp_to(before[k], most[k]);
 }
 
 template <int kN, int kPass, bool kReverse>
@@ -712,10 +716,8 @@ hipError_t launch(const SsmChainArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t kda_launch_ssm_table(const int64_t *cu, int64_t N, int64_t T, int pc, int64_t most_pieces,
-                                int64_t most_chunks, int32_t *piece_off, int32_t *chunk_off, hipStream_t s) {
-    hipLaunchKernelGGL(kda_ssm_table_kernel, dim3(1), dim3(1024), 0, s, cu, N, T, pc, most_pieces, most_chunks, piece_off,
-                       chunk_off);
+hipError_t kda_launch_ssm_table(const SsmTables &a, hipStream_t s) {
+    hipLaunchKernelGGL(kda_ssm_table_kernel, dim3(1), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

@@ -1,11 +1,13 @@
-"""NaN and infinities in the scan's inputs: a prompt's outputs are those of its tokens taken one
-by one, so one in a token reaches that token and those behind it, never those before."""
+"""The scan where calls are out of the ordinary.  NaN and infinities in its inputs: a prompt's
+outputs are those of its tokens taken one by one, so one in a token reaches that token and those
+behind it, never those before.  Packed batches of very short sequences and their workspaces."""
 import pytest
 import torch
 
 import gated_delta_rule_110_amd as kda
+from tests import layer_ref as R
 from tests.parity import say
-from tests.test_gpu_ssm import make
+from tests.test_gpu_ssm import check as check_scan, check_bwd, make
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -75,3 +77,25 @@ def test_no_step_leaves_everything():
     _, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s))
     _, last = kda.ssm_fwd(*keep.values(), initial_state=s, final_state=torch.empty_like(s))
     assert torch.equal(fin, last)
+
+
+@pytest.mark.parametrize("lens,pc", [([65] * 10, 1), ([129, 3, 0, 129, 64, 1, 129], 2), ([1] * 70 + [700] + [2] * 70, 4),
+                                     ([7, 64, 5], 1), ([0, 0], 1)])
+def test_a_workspace_of_exactly_the_size(lens, pc):
+    """Sequences of one and of several pieces among each other, in a workspace that ends where its size says."""
+    a, s = make(1, sum(lens), 2, 64, 1, 128, len(lens), F32, seed=7)
+    cu = torch.tensor(R.bounds(lens), dtype=torch.int64, device="cuda")
+    dy = torch.randn(a["x"].shape, device="cuda").to(torch.bfloat16)
+    for bwd in (False, True):
+        size = kda.ssm_bwd_workspace_size if bwd else kda.ssm_workspace_size
+        need = size(1, sum(lens), 2, 64, 1, 128, num_seqs=len(lens), piece_chunks=pc)
+        ws = torch.full((need + 65536,), 0xa5, dtype=torch.uint8, device="cuda")
+        say("case workspace %s pieces of %d backwards %s" % (lens[:4], pc, bwd))
+        if bwd:
+            g = kda.ssm_bwd(*a.values(), dy, initial_state=s, cu_seqlens=cu, workspace=ws, piece_chunks=pc)
+            check_bwd(a, s, lens, dy, None, g)
+        else:
+            y, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=cu, workspace=ws,
+                                 piece_chunks=pc)
+            check_scan(a, s, lens, y, fin, "exact workspace")
+        assert (ws[need:] == 0xa5).all()

@@ -207,3 +207,17 @@ def test_the_library_is_published_with_its_types(monkeypatch):
     L._declare(fake)
     assert fake.seen and all(s is None for s in fake.seen)
     assert L._lib is fake and all(f.argtypes is not None for f in fake.functions.values())
+
+
+def test_short_sequences_need_no_piece_states(lib):
+    """Only the pieces of sequences with several have a state in the workspace: 4096 sequences of 8 tokens need
+    the tables and the states of a few pieces, forwards, and two states per chunk (and head) for the gradient."""
+    shape = (1, 32768, 64, 64, 1, 128)
+    state = 64 * 64 * 128 * 4
+    pieces = 2 * 32768 // (64 * kda.ssm_piece_chunks(*shape, num_seqs=4096))   # at most, of sequences with several
+    assert kda.ssm_workspace_size(*shape, num_seqs=4096) <= pieces * state + (1 << 20)
+    chunks = 32768 // 64 + 4096
+    # the shares of dB and dC and the parameters' sums are small beside the states
+    assert kda.ssm_bwd_workspace_size(*shape, num_seqs=4096) <= (pieces + 2 * chunks) * state * 9 // 8
+    # sequences of one chunk more than a piece have two pieces each
+    assert kda.ssm_workspace_size(1, 65 * 10, 4, 64, 1, 64, num_seqs=10, piece_chunks=1) >= 20 * 4 * 64 * 64 * 4
