@@ -24,8 +24,6 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxTokenStride = int64_t(1) << 24;
 constexpr int64_t kMaxSeqs = 0x7fffffff;
 constexpr int64_t kMaxScanTokens = (int64_t(1) << 31) - 128;  // pieces and chunks are counted in 32 bits
-// Workgroups of 256 threads in one launch: its work-items are counted in 32 bits.
-constexpr int64_t kMaxGroups = int64_t(1) << 23;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
@@ -235,7 +233,7 @@ kda_status_t check_ssm(const kda_ssm_desc_t *d, bool packed) {
     // x, B and C are read 16 bytes at a time
     for (int64_t s : {d->x_stride_b, d->x_stride_t, d->b_stride_b, d->b_stride_t, d->c_stride_b, d->c_stride_t})
         if (s % 8 != 0) return KDA_ERR_ALIGN;
-    if (d->piece_chunks < 0) return KDA_ERR_PARAM;
+    if (d->piece_chunks < 0 || d->launch_piece < 0) return KDA_ERR_PARAM;
     return KDA_OK;
 }
 
@@ -264,6 +262,7 @@ kda_status_t ssm_args(const void *x, const void *dt, const void *Bm, const void 
     a.cb = d->c_stride_b; a.ct = d->c_stride_t;
     a.h0_f32 = d->initial_state_dtype == KDA_FP32;
     a.ht_f32 = d->final_state_dtype == KDA_FP32;
+    a.launch_cap = d->launch_piece;
     return KDA_OK;
 }
 
@@ -327,7 +326,8 @@ kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     // Packed: a sequence of more than 64 pc tokens has under 2 len / (64 pc) pieces.
     p.slots = packed ? std::min(p.pieces, d->T / (32 * pc)) : p.pps > 1 ? p.pieces : 0;
     p.pc = (int)pc;
-    if ((p.pieces + 7) / 8 * 8 > kMaxGroups / units || p.chunks > 0x7fffffff) return KDA_ERR_SHAPE;
+    // the tables count in 32 bits, and no product of a workspace's sizes passes 63
+    if (p.pieces > kMaxSeqs || p.chunks > kMaxSeqs || p.chunks > kMaxTokens / d->H) return KDA_ERR_SHAPE;
     size_t o = 0;
     if (packed) {
         p.off_piece = o; o = align_up(o + (size_t)(d->num_seqs + 1) * 4, 256);
@@ -374,7 +374,6 @@ kda_status_t plan_ssm_bwd(const kda_ssm_desc_t *d, bool packed, SsmBwdPlan &b) {
     const int64_t share = (heads + shares - 1) / shares;
     b.share = (int)share;
     b.shares = (int)((heads + share - 1) / share);
-    if (groups > kMaxGroups / 2 / b.shares) return KDA_ERR_SHAPE;
     const size_t states = (size_t)chunks * (size_t)d->H * (size_t)(d->P * d->N) * 4;
     size_t o = b.p.total;
     b.off_hs = o; o = align_up(o + states, 256);
@@ -406,6 +405,7 @@ SsmChainArgs chain_args(const SsmArgs &a, const SsmPlan &p, const Workspace &ws)
     c.xb = a.xb; c.xt = a.xt; c.kb = a.bb; c.kt = a.bt; c.cb = a.cb; c.ct = a.ct; c.dtb = a.dtb; c.dtt = a.dtt;
     c.A_log = a.A_log; c.dt_bias = a.dt_bias; c.D = a.D;
     c.cu = a.cu;
+    c.launch_cap = a.launch_cap;
     c.T = a.T; c.H = a.H; c.P = a.P; c.G = a.G; c.seqs = a.num_seqs;
     c.pieces = p.pieces; c.chunks = p.chunks; c.slots = p.slots; c.pps = p.pps; c.cps = p.cps; c.pc = p.pc;
     if (a.cu) {
@@ -718,6 +718,7 @@ extern "C" kda_status_t kda_ssm_bwd(const void *x, const void *dt, const void *B
     g.xb = a.xb; g.xt = a.xt; g.bb = a.bb; g.bt = a.bt; g.cb = a.cb; g.ct = a.ct; g.dtb = a.dtb; g.dtt = a.dtt;
     g.yb = desc->d_out_stride_b; g.yt = desc->d_out_stride_t;
     g.A_log = A_log; g.dt_bias = dt_bias; g.D = D;
+    g.launch_cap = a.launch_cap;
     g.cu = cu_seqlens; g.chunk_off = f.chunk_off;
     g.T = a.T; g.H = a.H; g.P = a.P; g.G = a.G; g.seqs = a.num_seqs;
     g.chunks = b.p.chunks; g.cps = b.p.cps;

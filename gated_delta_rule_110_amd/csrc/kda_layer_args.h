@@ -65,6 +65,7 @@ struct SsmArgs {
     int64_t B, T, H, P, G, N, num_seqs;
     int64_t xb, xt, dtb, dtt, bb, bt, cb, ct;
     int h0_f32, ht_f32;
+    int64_t launch_cap;        // kda_ssm_desc_t::launch_piece
 };
 
 // The scan's state chains.  A piece is up to `pc` 64-token chunks of one
@@ -93,6 +94,7 @@ struct SsmChainArgs {
     float *decay;              // [slots, H]: log2 of a piece's decay
     float *save;               // [chunks, H, P / 64, 64 N]: state entering every chunk (kda_ssm.hip)
     uint16_t *out;
+    int64_t launch_cap, base;  // base: first workgroup of this launch; set by the launcher
 };
 
 // The scan's gradient, chunk by chunk, from the states entering every chunk
@@ -112,7 +114,23 @@ struct SsmGradArgs {
     float *part;               // [2][shares][chunks][G][64][N]: dB, dC (with more than one share)
     float *psum;               // [chunks][H][4]: the parameters' gradients
     float *dA_log, *ddt_bias, *dD;
+    int64_t launch_cap, base;
 };
+
+// Launches of at most 2^23 workgroups (or `cap` of them, kda_ssm_desc_t::launch_piece),
+// since a launch's work-items are counted in 32 bits: calls launch(first workgroup,
+// number) for every one of them.  Their size is a multiple of 8, which keeps the XCD of
+// every workgroup.
+template <typename F>
+inline hipError_t launch_groups(int64_t groups, int64_t cap, F launch) {
+    const int64_t most = (launch_piece(int64_t(1) << 23, cap) + 7) / 8 * 8;
+    for (int64_t base = 0; base < groups; base += most) {
+        launch(base, dim3((unsigned)(groups - base < most ? groups - base : most)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 
 // fp32 -> two bf16 in one word (round to nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

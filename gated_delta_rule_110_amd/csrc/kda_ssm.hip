@@ -103,7 +103,7 @@ __device__ __forceinline__ Piece piece_of(const SsmChainArgs &a, int64_t index) 
 // Either way the heads that share B and C find them in its L2.
 __device__ __forceinline__ void place(const SsmChainArgs &a, int64_t &piece, int64_t &h, int64_t &pb) {
     const int64_t units = a.H * (a.P / kPB);
-    const int64_t i = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+    const int64_t i = (a.base + blockIdx.x) >> 3, xcd = blockIdx.x & 7;
     int64_t u;
     if (units % 8 == 0) {
         const int64_t own = units / 8;
@@ -710,8 +710,11 @@ __global__ __launch_bounds__(1024) void kda_ssm_table_kernel(SsmTables a) {
 
 template <int kN, int kPass, bool kReverse>
 hipError_t launch(const SsmChainArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((kda_ssm_chain_kernel<kN, kPass, kReverse>), dim3((unsigned)grid_size(a)), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+    SsmChainArgs b = a;
+    return launch_groups(grid_size(a), a.launch_cap, [&](int64_t base, dim3 grid) {
+        b.base = base;
+        hipLaunchKernelGGL((kda_ssm_chain_kernel<kN, kPass, kReverse>), grid, dim3(kThreads), 0, s, b);
+    });
 }
 
 }  // namespace

@@ -215,9 +215,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     constexpr int kJ = 4 * kTiles / kWaves;      // token tiles of dB and dC per wave
     __shared__ GradSmem<kN> sm;
     const int64_t per = a.G * a.shares;
-    const int64_t chunk = blockIdx.x / per;
-    const int64_t grp = (blockIdx.x - chunk * per) / a.shares;
-    const int share = (int)(blockIdx.x - chunk * per - grp * a.shares);
+    const int64_t block = a.base + blockIdx.x;
+    const int64_t chunk = block / per;
+    const int64_t grp = (block - chunk * per) / a.shares;
+    const int share = (int)(block - chunk * per - grp * a.shares);
     Chunk ck;
     if (chunk >= a.chunks || !chunk_of(a, chunk, ck)) return;
     const int rows = ck.rows;
@@ -647,11 +648,11 @@ constexpr int kJoin = 8;
 
 template <int kN>
 __global__ __launch_bounds__(256) void kda_ssm_grad_join_kernel(SsmGradArgs a) {
-    const int64_t block = blockIdx.x / kJoin;
+    const int64_t place = a.base + blockIdx.x, block = place / kJoin;
     const int64_t chunk = block / a.G, grp = block - chunk * a.G;
     Chunk ck;
     if (chunk >= a.chunks || !chunk_of(a, chunk, ck)) return;
-    const int part = blockIdx.x % kJoin, which = part / (kJoin / 2);
+    const int part = (int)(place % kJoin), which = part / (kJoin / 2);
     const int64_t one = a.chunks * a.G * kL * kN;
     const float *from = a.part + which * a.shares * one + (chunk * a.G + grp) * kL * kN;
     uint16_t *to = (which ? a.dC : a.dB) + ((ck.row0 * a.T + ck.t0) * a.G + grp) * kN;
@@ -692,9 +693,19 @@ __global__ __launch_bounds__(256) void kda_ssm_grad_params_kernel(SsmGradArgs a)
 template <int kN>
 hipError_t launch(const SsmGradArgs &a, hipStream_t s) {
     if (a.chunks > 0 && a.T > 0) {
-        hipLaunchKernelGGL((kda_ssm_grad_kernel<kN>), dim3((unsigned)(a.chunks * a.G * a.shares)), dim3(kThreads), 0, s, a);
-        if (a.shares > 1)
-            hipLaunchKernelGGL((kda_ssm_grad_join_kernel<kN>), dim3((unsigned)(a.chunks * a.G * kJoin)), dim3(256), 0, s, a);
+        SsmGradArgs b = a;
+        // its workgroups have twice the threads that launch_groups counts with
+        const int64_t cap = launch_piece(int64_t(1) << 22, a.launch_cap);
+        hipError_t e = launch_groups(a.chunks * a.G * a.shares, cap, [&](int64_t base, dim3 grid) {
+            b.base = base;
+            hipLaunchKernelGGL((kda_ssm_grad_kernel<kN>), grid, dim3(kThreads), 0, s, b);
+        });
+        if (e == hipSuccess && a.shares > 1)
+            e = launch_groups(a.chunks * a.G * kJoin, a.launch_cap, [&](int64_t base, dim3 grid) {
+                b.base = base;
+                hipLaunchKernelGGL((kda_ssm_grad_join_kernel<kN>), grid, dim3(256), 0, s, b);
+            });
+        if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(kda_ssm_grad_params_kernel, dim3((unsigned)a.H), dim3(256), 0, s, a);
     return hipGetLastError();

@@ -94,15 +94,9 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int
 
 template <int kN, bool kStream>
 hipError_t launch(const SsmArgs &a, hipStream_t s) {
-    constexpr int64_t kMost = int64_t(1) << 23;  // a launch's work-items are counted in 32 bits
-    const int64_t blocks = a.num_seqs * a.H * (a.P / kRows);
-    for (int64_t b = 0; b < blocks; b += kMost) {
-        const int64_t n = blocks - b < kMost ? blocks - b : kMost;
-        hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kStream>), dim3((unsigned)n), dim3(kThreads), 0, s, a, b);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    return launch_groups(a.num_seqs * a.H * (a.P / kRows), a.launch_cap, [&](int64_t base, dim3 grid) {
+        hipLaunchKernelGGL((kda_ssm_decode_kernel<kN, kStream>), grid, dim3(kThreads), 0, s, a, base);
+    });
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ class KdaSsmDesc(ctypes.Structure):
                 ("b_stride_b", _I), ("b_stride_t", _I), ("c_stride_b", _I), ("c_stride_t", _I),
                 ("d_out_stride_b", _I), ("d_out_stride_t", _I), ("initial_state_dtype", ctypes.c_int32),
                 ("final_state_dtype", ctypes.c_int32), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
-                ("piece_chunks", _I)]
+                ("piece_chunks", _I), ("launch_piece", _I)]
 
 
 def _declare(lib) -> None:
@@ -479,7 +479,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 # ---- selective state-space scan ----------------------------------------------------
 
 def _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks=0,
-              final_name="final_state"):
+              launch_piece=0, final_name="final_state"):
     """(descriptor, device)"""
     dev = _device_of(x)
     _bf16(x, "x", dev), _bf16(dt, "dt", dev), _bf16(B, "B", dev), _bf16(C, "C", dev)
@@ -495,7 +495,7 @@ def _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seq
     N = _num_seqs(cu_seqlens, nb, dev)
     return KdaSsmDesc(nb, T, H, P, G, S, N, *_tokens(x, "x"), *_tokens(dt, "dt"), *_tokens(B, "B"), *_tokens(C, "C"), 0, 0,
                       _whole(initial_state, "initial_state", (N, H, P, S), dev),
-                      _whole(final_state, final_name, (N, H, P, S), dev), None, 0, piece_chunks), dev
+                      _whole(final_state, final_name, (N, H, P, S), dev), None, 0, piece_chunks, launch_piece), dev
 
 
 def _ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks) -> KdaSsmDesc:
@@ -523,7 +523,7 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
             dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
             initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
             cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-            workspace: Optional[torch.Tensor] = None, piece_chunks: int = 0
+            workspace: Optional[torch.Tensor] = None, piece_chunks: int = 0, launch_piece: int = 0
             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The selective state-space scan (``kda_ssm_fwd``).  Returns ``(out, final_state)``.
 
@@ -535,11 +535,13 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
     [num_seqs + 1] on the device (then the batch size is 1) or None; out: bf16
     [B, T, H, P], allocated if None; workspace: uint8 of at least
     ``ssm_workspace_size`` bytes, allocated if None; piece_chunks: 0 or the
-    chunks per piece (``kda_ssm_desc_t::piece_chunks``).
+    chunks per piece (``kda_ssm_desc_t::piece_chunks``); launch_piece:
+    kda_ssm_desc_t::launch_piece (0: the library's launch size).
 
     A NaN or infinity in a token reaches its sequence's outputs from that token on,
     and no other sequence."""
-    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks)
+    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, cu_seqlens, piece_chunks,
+                       launch_piece)
     out = _output(out, "out", x.shape, torch.bfloat16, dev)
     lib = _library()
     ws = _workspace(workspace, lib.kda_ssm_fwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
@@ -551,15 +553,16 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
 def ssm_decode(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor, A_log: torch.Tensor,
                dt_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
                initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
-               out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               out: Optional[torch.Tensor] = None, launch_piece: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """One step of ``ssm_fwd`` per sequence (``kda_ssm_decode``): T = 1.
     final_state is required; passing the initial state updates it in place.
+    launch_piece: kda_ssm_desc_t::launch_piece (0: the library's launch size).
     Returns ``(out, final_state)``."""
     if final_state is None:
         raise ValueError("final_state must be given (it may be initial_state)")
     if x.dim() != 4 or x.shape[1] != 1:
         raise ValueError("x must be [N, 1, H, P]")
-    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, None)
+    d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, final_state, None, 0, launch_piece)
     out = _output(out, "out", x.shape, torch.bfloat16, dev)
     _call(_library().kda_ssm_decode, dev, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), A_log.data_ptr(),
           _ptr(dt_bias), _ptr(D), _ptr(initial_state), final_state.data_ptr(), out.data_ptr(), d)
@@ -576,7 +579,8 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
             dt_bias: Optional[torch.Tensor], D: Optional[torch.Tensor], d_out: torch.Tensor,
             d_final_state: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
             cu_seqlens: Optional[torch.Tensor] = None, with_d_initial: Optional[bool] = None,
-            workspace: Optional[torch.Tensor] = None, outputs: Optional[dict] = None, piece_chunks: int = 0) -> dict:
+            workspace: Optional[torch.Tensor] = None, outputs: Optional[dict] = None, piece_chunks: int = 0,
+            launch_piece: int = 0) -> dict:
     """Gradient of ``ssm_fwd`` (``kda_ssm_bwd``) for the loss gradients d_out (bf16
     [B, T, H, P]) and d_final_state (bf16 or fp32 [num_seqs, H, P, N], or None).
     Returns a dict: dx, ddt, dB and dC (bf16, of their inputs' shapes), dA_log,
@@ -584,12 +588,13 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
     d_initial_state (fp32 [num_seqs, H, P, N]; None unless wanted, by default
     where an initial_state is given).  Rows behind a packed batch's last sequence
     are left as they were.  outputs: None, or a dict of tensors of those names to
-    write into.  The workspace holds 8 P N bytes per 64-token chunk and head.
+    write into; launch_piece: kda_ssm_desc_t::launch_piece (0: the library's launch
+    size).  The workspace holds 8 P N bytes per 64-token chunk and head.
 
     A NaN or infinity in a token reaches all gradients of its 64-token chunk, those
     of its sequence that depend on the chunk's and the parameters'."""
     d, dev = _ssm_args(x, dt, B, C, A_log, dt_bias, D, initial_state, d_final_state, cu_seqlens, piece_chunks,
-                       "d_final_state")
+                       launch_piece, "d_final_state")
     _bf16(d_out, "d_out", dev)
     if d_out.shape != x.shape:
         raise ValueError("d_out must be of x's shape")

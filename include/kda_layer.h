@@ -152,6 +152,8 @@ typedef struct {
      * through in order; shorter pieces make more of them, and where a sequence
      * has several, its tokens are read twice (once for the pieces' states). */
     int64_t piece_chunks;
+    int64_t launch_piece;                   /* most workgroups of one launch, rounded up to a multiple of 8; 0: the
+                                               library's (2^23, so that only very large batches take several) */
 } kda_ssm_desc_t;
 
 /* Bytes of workspace kda_ssm_fwd and kda_ssm_bwd need for these shapes (0 if they

@@ -99,3 +99,40 @@ def test_a_workspace_of_exactly_the_size(lens, pc):
                                  piece_chunks=pc)
             check_scan(a, s, lens, y, fin, "exact workspace")
         assert (ws[need:] == 0xa5).all()
+
+
+@pytest.mark.parametrize("H,P,G", [(3, 64, 1), (8, 128, 2)])
+def test_launches_in_pieces(H, P, G):
+    """launch_piece splits every kernel's grid as a very large batch does: the same results, bit for bit."""
+    lens = [70, 3, 300, 0, 129]
+    a, s = make(1, sum(lens), H, P, G, 64, len(lens), F32, seed=8)
+    cu = torch.tensor(R.bounds(lens), dtype=torch.int64, device="cuda")
+    dy = torch.randn(a["x"].shape, device="cuda").to(torch.bfloat16)
+    one, st = make(20, 1, H, P, G, 64, 20, F32, seed=9)
+
+    def run(cap):
+        y, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=cu, piece_chunks=1,
+                             launch_piece=cap)
+        g = kda.ssm_bwd(*a.values(), dy, initial_state=s, cu_seqlens=cu, piece_chunks=1, launch_piece=cap)
+        return [y, fin, *g.values(), *kda.ssm_decode(*one.values(), initial_state=st, final_state=torch.empty_like(st), launch_piece=cap)]
+    want = run(0)
+    for cap in (1, 16, 40):
+        say("case launches of at most %d" % cap)
+        for i, (t, u) in enumerate(zip(run(cap), want)):
+            assert torch.equal(t, u), (cap, i)
+
+
+def test_more_sequences_than_a_launch_holds():
+    """131073 sequences of one token, 64 heads: more than 2^23 workgroups, packed and as a batch."""
+    n, H, P, S = 131073, 64, 64, 64
+    small, _ = make(1, 64, H, P, 1, S, 64, None, seed=10)
+    args = {k: v.repeat(1, n // 64 + 1, *[1] * (v.dim() - 2))[:, :n] if k in ("x", "dt", "B", "C") else v for k, v in small.items()}
+    cu = torch.arange(n + 1, device="cuda")
+    want, _ = kda.ssm_fwd(*small.values(), cu_seqlens=cu[:65].contiguous())
+    say("case 131073 packed sequences")
+    y, _ = kda.ssm_fwd(*args.values(), cu_seqlens=cu)
+    assert torch.equal(y[0, :64], want[0]) and torch.equal(y[0, n - 1], want[0, (n - 1) % 64])
+    assert torch.equal(y[0, n - 65:n - 1], want[0].roll(-((n - 65) % 64), 0))
+    say("case 131073 batch rows")
+    rows = {k: v.transpose(0, 1) if k in ("x", "dt", "B", "C") else v for k, v in args.items()}
+    assert torch.equal(kda.ssm_fwd(*rows.values())[0][:, 0], y[0])

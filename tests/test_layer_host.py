@@ -221,3 +221,13 @@ def test_short_sequences_need_no_piece_states(lib):
     assert kda.ssm_bwd_workspace_size(*shape, num_seqs=4096) <= (pieces + 2 * chunks) * state * 9 // 8
     # sequences of one chunk more than a piece have two pieces each
     assert kda.ssm_workspace_size(1, 65 * 10, 4, 64, 1, 64, num_seqs=10, piece_chunks=1) >= 20 * 4 * 64 * 64 * 4
+
+
+def test_many_sequences_take_several_launches(lib):
+    """More pieces times heads than one launch holds workgroups is no reason to refuse a call."""
+    n = 131073
+    assert kda.ssm_workspace_size(1, 8 * n, 64, 64, 1, 128, num_seqs=n) > 0
+    assert kda.ssm_bwd_workspace_size(1, 8 * n, 64, 64, 1, 128, num_seqs=n) > 2 * n * 64 * 64 * 128 * 4
+    assert kda.ssm_piece_chunks(n, 8, 64, 64, 1, 128) == 1
+    assert ssm(lib, launch_piece=-1) == PARAM and ssm(lib, "decode", launch_piece=-1) == PARAM
+    assert ssm(lib, "bwd", launch_piece=-1) == PARAM
