@@ -136,3 +136,34 @@ def test_more_sequences_than_a_launch_holds():
     say("case 131073 batch rows")
     rows = {k: v.transpose(0, 1) if k in ("x", "dt", "B", "C") else v for k, v in args.items()}
     assert torch.equal(kda.ssm_fwd(*rows.values())[0][:, 0], y[0])
+
+
+@pytest.mark.parametrize("dtype,N", [(F32, 200), (torch.bfloat16, 400)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_states_larger_than_the_cache(dtype, N, in_place):
+    """A step over states of more than 384 MiB, which are read past the caches: the first and last sequences as
+    those of a small batch."""
+    H, P, S = 64, 64, 128
+    a, _ = make(N, 1, H, P, 1, S, N, None, seed=11)
+    s = torch.randn(N, H, P, S, device="cuda").to(dtype)
+    assert s.numel() * s.element_size() > 384 << 20
+    picks = [0, 1, N // 2, N - 1]
+    few = {k: v[picks].contiguous() if k in ("x", "dt", "B", "C") else v for k, v in a.items()}
+    y, fin = kda.ssm_decode(*few.values(), initial_state=s[picks], final_state=torch.empty_like(s[picks]))
+    say("case %d sequences, %s, in place %s" % (N, dtype, in_place))
+    z, last = kda.ssm_decode(*a.values(), initial_state=s, final_state=s if in_place else torch.empty_like(s))
+    assert torch.equal(z[picks], y) and torch.equal(last[picks], fin)
+    assert last.isfinite().all()
+
+
+def test_a_step_over_more_than_32_bits_of_entries():
+    """A state of more than 2^31 entries: the last sequences as those of a small batch."""
+    H, P, S, N = 64, 128, 128, 2050
+    assert N * H * P * S > 1 << 31
+    a, _ = make(N, 1, H, P, 1, S, N, None, seed=12)
+    s = torch.zeros(N, H, P, S, dtype=torch.bfloat16, device="cuda")
+    s[-2:].normal_()
+    few = {k: v[-2:].contiguous() if k in ("x", "dt", "B", "C") else v for k, v in a.items()}
+    y, fin = kda.ssm_decode(*few.values(), initial_state=s[-2:].clone(), final_state=torch.empty_like(s[-2:]))
+    z, _ = kda.ssm_decode(*a.values(), initial_state=s, final_state=s)
+    assert torch.equal(z[-2:], y) and torch.equal(s[-2:], fin)
