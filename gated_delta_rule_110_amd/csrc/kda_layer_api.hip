@@ -293,8 +293,8 @@ struct SsmPlan {
 // and for equal pieces in one round (8192 tokens x 64 heads: 127 us, with two rounds
 // 132 us, with a round and a half 152 us).  Under kFewPieces pieces per sequence, two
 // rounds: the first pass leaves out the last piece, and one of few leaves CUs idle
-// (6 x 4000 tokens x 40 heads: 213 us, with one 285 us).  A packed batch's pieces are
-// uneven, and two rounds even them out (32768 tokens in 17 sequences: 434 us, with one
+// (6 x 4000 tokens x 40 heads: 213 us, with one 285 us).  The pieces of several packed
+// sequences are uneven, and two rounds even them out (32768 tokens in 17 sequences: 434 us, with one
 // 488 us, with three 455 us).
 // Fewer than kMinPiece chunks per piece would leave a piece's state (32 KiB of fp32
 // per 64 channels and 128 entries) larger than its tokens.
@@ -305,19 +305,19 @@ kda_status_t plan_ssm(const kda_ssm_desc_t *d, bool packed, SsmPlan &p) {
     const int64_t units = d->H * (d->P / 64);
     p = SsmPlan{};
     p.cps = packed ? 0 : (d->T + 63) / 64;
-    const int64_t all = packed ? d->T / 64 + 1 : d->B * p.cps;
+    const bool several = packed && d->num_seqs > 1;
+    const int64_t top = several ? d->T / 64 + 1 : (d->T + 63) / 64;  // chunks of the longest sequence
     int64_t pc = d->piece_chunks;
     if (pc == 0) {
-        if (packed) {
-            pc = (all * units + 2 * kGroups - 1) / (2 * kGroups);
+        if (several) {
+            pc = (top * units + 2 * kGroups - 1) / (2 * kGroups);
         } else {                             // chains that fill the GPU by themselves are not cut
             int64_t pieces = kGroups / std::max<int64_t>(d->B * units, 1);
             if (pieces > 1 && pieces < kFewPieces) pieces *= 2;
-            pc = pieces > 1 ? (p.cps + pieces - 1) / pieces : p.cps;
+            pc = pieces > 1 ? (top + pieces - 1) / pieces : top;
         }
         if (pc < kMinPiece) pc = kMinPiece;
     }
-    const int64_t top = packed ? all : p.cps;
     if (pc > top) pc = top;
     if (pc < 1) pc = 1;
     p.chunks = packed ? d->T / 64 + d->num_seqs : d->B * p.cps;

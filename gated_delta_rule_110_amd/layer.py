@@ -512,7 +512,8 @@ def ssm_workspace_size(B: int, T: int, H: int, P: int, G: int, N: int, num_seqs:
 
 def ssm_piece_chunks(B: int, T: int, H: int, P: int, G: int, N: int, num_seqs: Optional[int] = None,
                      piece_chunks: int = 0) -> int:
-    """64-token chunks per piece of a state chain for these shapes."""
+    """64-token chunks per piece of a state chain for these shapes (at most, in a packed
+    batch of several sequences)."""
     n = int(_library().kda_ssm_piece_chunks(_ssm_shape(B, T, H, P, G, N, num_seqs, piece_chunks)))
     if n < 0:
         raise ValueError("invalid shapes")

@@ -158,7 +158,8 @@ typedef struct {
 
 /* Bytes of workspace kda_ssm_fwd and kda_ssm_bwd need for these shapes (0 if they
  * are invalid; with B = 1 enough for a packed batch too), and the chunks per piece
- * they use (-1 if they are invalid).  Host arithmetic. */
+ * they use (at most, in a packed batch of several sequences; -1 if the shapes are
+ * invalid).  Host arithmetic. */
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_desc_t *desc);
 size_t kda_ssm_bwd_workspace_size(const kda_ssm_desc_t *desc);
 int64_t kda_ssm_piece_chunks(const kda_ssm_desc_t *desc);

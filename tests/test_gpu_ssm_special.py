@@ -167,3 +167,18 @@ def test_a_step_over_more_than_32_bits_of_entries():
     y, fin = kda.ssm_decode(*few.values(), initial_state=s[-2:].clone(), final_state=torch.empty_like(s[-2:]))
     z, _ = kda.ssm_decode(*a.values(), initial_state=s, final_state=s)
     assert torch.equal(z[-2:], y) and torch.equal(s[-2:], fin)
+
+
+@pytest.mark.parametrize("T,H", [(8192, 64), (5000, 4)])
+def test_pieces_as_the_query_says(T, H):
+    """Of a batch row and of a packed batch of one sequence: the pieces that ssm_piece_chunks tells, so that asking for
+    them changes no bit."""
+    a, s = make(1, T, H, 64, 1, 128, 1, F32, seed=13)
+    pc = kda.ssm_piece_chunks(1, T, H, 64, 1, 128)
+    assert kda.ssm_piece_chunks(1, T, H, 64, 1, 128, num_seqs=1) == pc < T // 64
+    cu = torch.tensor([0, T], device="cuda")
+    want = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), piece_chunks=pc)
+    for lens in (None, cu):
+        for n in (0, pc):
+            got = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=lens, piece_chunks=n)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (n, lens)
