@@ -156,6 +156,14 @@ __device__ __forceinline__ float exact_exp(float x) {
     return fabsf(p) < 200.0f ? __builtin_fmaf(e, rest * 0.693147182f, e) : e;  // beyond: 0 or infinity
 }
 
+// The scan's decay rate e^A_log, at most 2^100, so that its products with step sizes (up
+// to 2^20) and their sums over a chunk stay finite, and zero without a step: rates like
+// that leave nothing of a state, whatever the step.
+__device__ __forceinline__ float decay_rate(float A_log) {
+    const float e = exact_exp(A_log);
+    return e > 0x1p100f ? 0x1p100f : e;          // false for NaN
+}
+
 // softplus(x) = max(x, 0) + log1p(t), t = e^-|x| <= 1, to about 2^-23 relative:
 // log1p(t) = 2 atanh(z) with z = t / (2 + t) <= 1/3, by the series to z^15 (the next
 // term is below 2^-27 relative).

@@ -245,7 +245,7 @@ __device__ __forceinline__ bool walk_piece(const SsmChainArgs &a, ChainSmem<kN, 
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int64_t grp = h / (a.H / a.G);
-    const float nA2 = -exact_exp(a.A_log[h]) * kLog2e;
+    const float nA2 = -decay_rate(a.A_log[h]) * kLog2e;
     const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
     const float Dh = kOut && a.D ? a.D[h] : 0.f;
     const uint16_t *xrow = a.x + p.row0 * a.xb + p.t0 * a.xt + h * a.P + pb * kPB;

@@ -305,10 +305,10 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_grad_kernel(SsmGradArgs a) {
     auto raw_of = [&](int i) -> uint32_t { return drow[i < count ? i : count - 1]; };
     auto steps_of = [&](int i, uint32_t raw, Steps &to) {
         step_sizes(bf16_bits_to_f32((uint16_t)raw), lane < rows, scalar(a.dt_bias, h0 + i),
-                   -exact_exp(scalar(a.A_log, h0 + i)) * kLog2e, to);
+                   -decay_rate(scalar(a.A_log, h0 + i)) * kLog2e, to);
     };
     auto finish = [&](int i, const Steps &st, const Sums<kN> &su) {
-        const float A = -exact_exp(scalar(a.A_log, h0 + i));
+        const float A = -decay_rate(scalar(a.A_log, h0 + i));
         const int t = lane;
         float cq[4], colq = 0.f, f = 0.f, rr = 0.f, xs = 0.f;
 #pragma unroll

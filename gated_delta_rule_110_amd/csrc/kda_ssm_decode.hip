@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kThreads) void kda_ssm_decode_kernel(SsmArgs a, int
     const f4 Cv = load_state4<false>(a.Cm, n * a.cb + g * kN + 4 * q, 0);
     const float raw = bf16_bits_to_f32(a.dt[n * a.dtb + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f);
     const float dt = softplus(raw);
-    const float decay = exact_exp(-exact_exp(a.A_log[h]) * dt);
+    const float decay = exact_exp(-decay_rate(a.A_log[h]) * dt);
     const float Dh = a.D ? a.D[h] : 0.f;
     const uint16_t *x = a.x + n * a.xb + h * a.P + p0;
 #pragma unroll

@@ -182,3 +182,24 @@ def test_pieces_as_the_query_says(T, H):
         for n in (0, pc):
             got = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=lens, piece_chunks=n)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (n, lens)
+
+
+@pytest.mark.parametrize("A_log", [20.0, 80.0, 88.0, 100.0, 3e38, INF])
+def test_decay_rates_that_leave_nothing(A_log):
+    """e^A_log far above one, or above fp32: a step leaves nothing of the state before it, prompts as well as
+    single tokens; where there is no step (dt = 0) nothing decays.  The gradients are those of that."""
+    a, s = make(1, 100, 3, 64, 1, 64, 1, F32, seed=14)
+    a["A_log"][1] = A_log
+    a["dt"][0, 50:60] = -INF
+    check(a, a, s, "A_log = %g" % A_log)
+    y, fin = kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s))
+    want, last = step_by_step(a, s)
+    assert y.isfinite().all() and fin.isfinite().all()
+    # no state of that head outlives a token: y = (dt C.B + D) x, as the one-token step has it, once more rounded
+    R.check(y[0, :, 1], R.d(want[0, :, 1]), torch.bfloat16, 2.0 ** -8 * R.d(want[0, :, 1]).abs() + 1e-30, "y")
+    R.check(fin[0, 1], R.d(last[0, 1]), F32, 64 * R.U * R.d(last[0, 1]).abs() + 1e-30, "state")
+    dy = torch.randn(a["x"].shape, device="cuda").to(torch.bfloat16)
+    g = kda.ssm_bwd(*a.values(), dy, d_final_state=torch.randn_like(s), initial_state=s)
+    for k, v in g.items():
+        assert v.isfinite().all(), k
+    assert (g["dA_log"][1] == 0) and (g["d_initial_state"][0, 1] == 0).all()
