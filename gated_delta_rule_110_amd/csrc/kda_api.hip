@@ -186,7 +186,7 @@ extern "C" const char *kda_status_string(kda_status_t s) {
         case KDA_ERR_NULL: return "a required pointer is NULL";
         case KDA_ERR_SHAPE: return "invalid shape (B, H >= 1, T >= 0; num_seqs == B, or B == 1 with cu_seqlens; strides >= 0)";
         case KDA_ERR_UNSUPPORTED: return "unsupported head dimension (K and V must be 128; a scan's P and N 64 or 128, a convolution's W 2, 3 or 4)";
-        case KDA_ERR_PARAM: return "invalid parameter (lower_bound must be finite and in [-5, 0]; scale finite; eps finite and positive)";
+        case KDA_ERR_PARAM: return "invalid parameter (lower_bound must be finite and in [-5, 0]; scale finite; eps finite and at least 2^-126)";
         case KDA_ERR_DTYPE: return "state and parameter dtypes must be KDA_BF16 or KDA_FP32";
         case KDA_ERR_ALIGN: return "misaligned pointer (tensors 16 bytes, workspace 256 bytes)";
         case KDA_ERR_WORKSPACE: return "workspace smaller than the call's workspace size function asks for";

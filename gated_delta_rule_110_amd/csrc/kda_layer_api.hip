@@ -118,7 +118,8 @@ kda_status_t validate_cu(const int64_t *cu, int64_t N, int64_t T, hipStream_t st
 
 kda_status_t check_norm(const kda_rmsnorm_desc_t *d) {
     if (d->rows < 0 || d->D < 1 || d->rows > kMaxTokens || d->D > kMaxColumns) return KDA_ERR_SHAPE;
-    if (!(d->eps > 0.0f) || !isfinite(d->eps)) return KDA_ERR_PARAM;
+    // a smaller eps, which a row of zeros leaves by itself, is zero to the hardware's reciprocal root
+    if (!(d->eps >= 0x1p-126f) || !isfinite(d->eps)) return KDA_ERR_PARAM;
     if (!stride_ok(d->x_stride)) return KDA_ERR_SHAPE;
     if (!dtype_ok(d->weight_dtype)) return KDA_ERR_DTYPE;
     return KDA_OK;

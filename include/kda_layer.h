@@ -53,7 +53,7 @@ typedef struct {
     int64_t x_stride, residual_stride;      /* elements between rows (>= 0) */
     int32_t residual_dtype, weight_dtype;   /* kda_dtype_t; residual_dtype also of residual_out (and, in the
                                                gradient, of h and d_residual_out) */
-    float eps;                              /* > 0, finite */
+    float eps;                              /* finite, >= 2^-126 */
     int64_t group;                          /* quantised output: columns per scale (128), or 0: one scale per row */
     int64_t d_out_stride, d_residual_stride;/* the gradient's inputs */
     void *workspace;                        /* gradient only: >= kda_rmsnorm_bwd_workspace_size(), 256-byte aligned */

@@ -231,3 +231,11 @@ def test_many_sequences_take_several_launches(lib):
     assert kda.ssm_piece_chunks(n, 8, 64, 64, 1, 128) == 1
     assert ssm(lib, launch_piece=-1) == PARAM and ssm(lib, "decode", launch_piece=-1) == PARAM
     assert ssm(lib, "bwd", launch_piece=-1) == PARAM
+
+
+def test_rmsnorm_refuses_subnormal_eps(lib):
+    """A row of zeros leaves eps by itself, and the hardware's reciprocal root takes a subnormal one as zero."""
+    for q in (False, True):
+        assert norm(lib, q, eps=1e-40) == PARAM and norm(lib, q, eps=2.0 ** -127) == PARAM
+    assert norm_bwd(lib, eps=1e-40) == PARAM
+    assert norm(lib, False, {"x": None}, eps=2.0 ** -126) == NULL   # accepted: the next check answers
