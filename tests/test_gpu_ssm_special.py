@@ -203,3 +203,37 @@ def test_decay_rates_that_leave_nothing(A_log):
     for k, v in g.items():
         assert v.isfinite().all(), k
     assert (g["dA_log"][1] == 0) and (g["d_initial_state"][0, 1] == 0).all()
+
+
+def test_special_values_in_place_and_captured():
+    """Pieces that are walked through twice: with the state updated in place, and in a graph whose inputs change
+    between replays."""
+    lens = [200, 0, 65, 300]
+    a, s = make(1, sum(lens), 4, 128, 2, 64, len(lens), F32, seed=15)
+    cu = torch.tensor(R.bounds(lens), dtype=torch.int64, device="cuda")
+    b = {k: v.clone() for k, v in a.items()}
+    b["x"][0, 100, 1, 5], b["x"][0, 400, 3, 70] = NAN, INF
+    bits = lambda y, f: (y.view(torch.int16).clone(), f.view(torch.int32).clone())  # noqa: E731
+    want = {i: bits(*kda.ssm_fwd(*v.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=cu))
+            for i, v in enumerate((a, b))}
+    st = s.clone()
+    got = bits(*kda.ssm_fwd(*b.values(), initial_state=st, final_state=st, cu_seqlens=cu))
+    assert all(torch.equal(g, w) for g, w in zip(got, want[1]))
+    c = {k: v.clone() for k, v in a.items()}
+    out, fin = torch.empty(a["x"].shape, dtype=torch.bfloat16, device="cuda"), torch.empty_like(s)
+    ws = torch.empty(kda.ssm_workspace_size(1, sum(lens), 4, 128, 2, 64, num_seqs=len(lens)), dtype=torch.uint8, device="cuda")
+
+    def call():
+        kda.ssm_fwd(*c.values(), initial_state=s, final_state=fin, cu_seqlens=cu, out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i in (1, 0, 1, 0):
+        c["x"].copy_((a, b)[i]["x"])
+        out.zero_(), fin.zero_(), ws.fill_(255)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, w) for p, w in zip(bits(out, fin), want[i])), i
