@@ -8,12 +8,13 @@
 // once, out once).  A lane holds 4 neighbouring channels (8 bytes per token and
 // access, 512 per wave) and walks over a run of tokens with the last W - 1
 // inputs in registers, so that x is read once plus W - 1 rows per run.  Where the
-// channel count, a stride or an address does not allow such accesses, the same
-// code runs with one channel per lane.  Measured: 4 x 2048 tokens of 12288 channels
+// channel count or a stride is no multiple of 8, or an address none of 16 bytes, the
+// same code runs with one channel per lane.  Measured: 4 x 2048 tokens of 12288 channels
 // 84 us, 32768 packed tokens of 4352 112 us (4.8 and 5.1 TB/s of what has to be read
-// and written; a copy reaches 5.0 to 5.4), the gradient of 8192 x 4352 49 us and 5 for
-// the weights' sum (4.0 TB/s: each run reads W - 1 tokens of its neighbour's again),
-// one token of 64 sequences of 12288 5 us, all of it latency.
+// and written; the runtime's copy reaches 5.1, an elementwise one of a GiB 6.2), the
+// gradient of 8192 x 4352 47 us and 5 for the weights' sum (4.1 TB/s: each run reads
+// W - 1 tokens of its neighbour's again), one token of 64 sequences of 12288 5 us, all
+// of it latency.
 #include "kda_layer_args.h"
 
 using namespace kda;
@@ -484,8 +485,9 @@ __global__ __launch_bounds__(64) void kda_conv_bwd_state_kernel(ConvArgs a) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Wide accesses to every tensor of the call (states and partial sums have rows
-// of D entries, so D a multiple of 8 keeps them aligned too).
+// Wide accesses to every tensor of the call.  Stricter than they need: a lane's 4
+// channels are 8 bytes of bf16 and 16 of fp32, so multiples of 4 channels at 8-byte
+// addresses (fp32: 16) would do (8192 tokens of 4352 channels 31 us, of 4356 45).
 bool vector_channels(const ConvArgs &a) {
     return a.D % 8 == 0 && a.xb % 8 == 0 && a.xt % 8 == 0 && a.db_ % 8 == 0 && a.dt_ % 8 == 0 && aligned16(a.x) &&
            aligned16(a.out) && aligned16(a.h0) && aligned16(a.ht) && aligned16(a.dy) && aligned16(a.dht) &&

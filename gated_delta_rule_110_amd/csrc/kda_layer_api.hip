@@ -291,12 +291,12 @@ struct SsmPlan {
 };
 
 // Workgroups a launch should have: the two that fit each of the 256 CUs, at once
-// and for equal pieces in one round (8192 tokens x 64 heads: 127 us, with two rounds
-// 132 us, with a round and a half 152 us).  Under kFewPieces pieces per sequence, two
+// and for equal pieces in one round (8192 tokens x 64 heads: 122 us, with two rounds
+// 128 us, with a round and a half 131 us).  Under kFewPieces pieces per sequence, two
 // rounds: the first pass leaves out the last piece, and one of few leaves CUs idle
-// (6 x 4000 tokens x 40 heads: 213 us, with one 285 us).  The pieces of several packed
-// sequences are uneven, and two rounds even them out (32768 tokens in 17 sequences: 434 us, with one
-// 488 us, with three 455 us).
+// (6 x 4000 tokens x 40 heads: 215 us, with one 219 us).  The pieces of several packed
+// sequences are uneven, and take two rounds as well (32768 tokens in 17 sequences: 478
+// us, with one 479 us, with three 465 us).
 // Fewer than kMinPiece chunks per piece would leave a piece's state (32 KiB of fp32
 // per 64 channels and 128 entries) larger than its tokens.
 constexpr int64_t kGroups = 512;
@@ -352,7 +352,7 @@ struct SsmBwdPlan {
 // fits each CU, and the shares' dB and dC added up.  In units of a workgroup's time
 // for one head and 64 channels (7 us at 128 entries), a round costs its heads and
 // about one more to begin, and adding up about one per 256 shares (128 chunks x 64
-// heads: 2 shares 491 us, 4 507 us, 8 531 us).
+// heads: 2 shares 510 us, 4 522 us, 8 544 us).
 int64_t grad_shares(int64_t groups, int64_t heads, int64_t blocks) {
     constexpr int64_t kCus = 256, kMost = 64;
     int64_t best = 1, least = INT64_MAX;

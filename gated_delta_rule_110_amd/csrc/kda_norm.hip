@@ -10,9 +10,10 @@
 // The row is read once and stays in registers between the reduction and the
 // output, so the kernels are bound by the memory traffic of their inputs and
 // outputs.  Everything between load and store is fp32.  With rows of 4096: 8191 rows
-// and an fp32 residual 83 us (4.9 TB/s of what has to be read and written; a copy
-// reaches 5.0 to 5.4), the gradient of 8192 rows 51 us and 5 for the weight's sum
-// (4.8 TB/s), 64 rows to e4m3 4.4 us, all of it latency.
+// and an fp32 residual 83 us (4.9 TB/s of what has to be read and written; the
+// runtime's copy reaches 5.1, an elementwise one of a GiB 6.2), the gradient of 8192
+// rows 49 us and 5 for the weight's sum (5.0 TB/s), 64 rows to e4m3 4.3 us, all of it
+// latency.
 #include "kda_layer_args.h"
 
 using namespace kda;
@@ -488,7 +489,8 @@ bool bwd_vector(const NormBwdArgs &a) {
 }  // namespace
 
 // Rows of 8-column groups at 16-byte aligned addresses take the register
-// kernels (up to 16384 columns), all others the scalar one.
+// kernels (up to 16384 columns), all others the scalar one (8192 rows of 4096 columns
+// 42 us, of 4097 186).
 hipError_t kda_launch_rmsnorm(const NormArgs &a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
     const bool vec = vector_rows(a.D, a.xs, a.res ? a.rs : 0, 0) && aligned16(a.x) && aligned16(a.res) &&

@@ -14,15 +14,15 @@
 // together 2^-25, half of fp32's own step: the products are those of fp32.  States,
 // decays and sums stay in fp32.
 //
-// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 118 us (36 for the pieces'
-// states, 8 to join them, 74 for the outputs), where the tensors alone would take 27:
-// the products, in parts, are 84 GFLOP, 35 us of the matrix cores at the clock they
+// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 127 us (39 for the pieces'
+// states, 8 to join them, 80 for the outputs), where the tensors alone would take 23:
+// the products, in parts, are 90 GFLOP, 40 us of the matrix cores at the clock they
 // run at here, and a chunk's four products, its 64 decays and two barriers follow one
-// another.  Per chunk and wave the outputs' pass spends 8800 cycles: 1200 on C S^T and
-// 2000 on the update, both near the matrix cores' rate with two workgroups a CU, 2300
-// on M and 1100 on M x, which wait for LDS and for each other, 1700 on staging and
-// barriers.  32768 packed tokens of 32 heads of 128 x 128: 431 us; 131072 tokens of 4
-// heads of 64 x 64: 94 us.
+// another.  Per chunk and wave the outputs' pass spends 10400 cycles: 2000 on C S^T and
+// 2200 on the update, both near the matrix cores' rate with two workgroups a CU, 2700
+// on M and 1600 on M x, which wait for LDS and for each other, 1900 on staging, stores
+// and barriers.  32768 packed tokens of 32 heads of 128 x 128: 481 us; 131072 tokens of
+// 4 heads of 64 x 64: 99 us.
 //
 // Work.  Chains are serial over chunks but independent over heads and over
 // blocks of 64 channels, and 64 x N states leave most of the GPU idle for a

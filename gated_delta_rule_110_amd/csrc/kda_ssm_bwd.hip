@@ -28,13 +28,14 @@
 // all of them, and dB and dC add up in registers.  The products' fp32 operands (M, W,
 // S, D) are split into three bf16 parts (2^-25); x, B, C and d_out are exact.
 //
-// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 489 us: 260 here (250, and
-// 11 for the sums of shares and parameters), the rest the chains of both directions
-// (43 + 45 the pieces, 8 + 8 their joins, 73 + 77 the chunks' states, 268 MB each,
-// written at 3.6 TB/s).  One workgroup fits a CU, its waves in step; of 16000 cycles a
-// head they spend 3300 on M and W, 2300 on dx, 6800 on dB and dC, 2000 on staging and
-// the rest in barriers.  LDS is busy for 46% of the time, the matrix cores for 18%:
-// latency and LDS reads, not memory (0.45 GB, 1.8 TB/s).
+// What bounds it.  8192 tokens of 64 heads of 64 x 128 take 506 us: 258 here (248, and
+// 10 for the sums of shares and parameters), the rest the chains of both directions
+// (39 + 41 the pieces, 8 + 9 their joins, 73 + 77 the chunks' states, 268 MB each,
+// written at 3.6 TB/s).  One workgroup fits a CU, its waves in step; of 17400 cycles a
+// head they spend 3100 on M and W and 1400 waiting for the slowest there, 2500 on dx,
+// 8000 on dB and dC, 1500 on staging and the rest in barriers.  LDS is busy for 46% of
+// the time, the matrix cores for 24%: latency and LDS reads, not memory (0.45 GB, 1.8
+// TB/s).
 #include "kda_ssm_common.h"
 
 using namespace kda;

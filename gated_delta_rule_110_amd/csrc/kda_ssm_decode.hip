@@ -5,7 +5,9 @@
 //
 // The state is read once, updated in registers and written once, in fp32
 // arithmetic: the step is bound by the state's memory traffic (64 KiB in and
-// out per head of 64 x 128 fp32).
+// out per head of 64 x 128 fp32).  64 sequences of 64 heads, 268 MB: 49 us from states
+// that are not resident and 52 in place (5.5 and 5.1 TB/s), 40 from ones that the
+// caches kept from the step before; 256 sequences 180 us (6.0 TB/s, a copy's rate).
 //
 // A workgroup of 256 threads takes kRows rows (channels) of one head's state; a
 // thread holds 4 neighbouring columns of every 256 / (N / 4)-th row, so that a

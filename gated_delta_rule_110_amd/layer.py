@@ -7,7 +7,9 @@ As for the recurrence, the functions only marshal arguments: they check types,
 devices and shapes, allocate outputs and workspaces that the caller does not
 pass, and call libkda on torch's current HIP stream of the inputs' device.
 Activations are bf16; they may be slices of wider tensors (only their last
-dimensions have to be contiguous).  Tensors that a call writes are contiguous.
+dimensions have to be contiguous; the scan's x, B, C and d_out also have to begin
+at multiples of 16 bytes, with strides that are multiples of 8 elements).  Tensors
+that a call writes are contiguous.
 
 ``rms_norm``, ``short_conv`` and ``ssm_scan`` differentiate once.  To capture
 their backward into a HIP graph, let no autograd graph of the same leaves from

@@ -21,7 +21,14 @@
  * Inputs may overlap or be broadcast (stride 0).  Every tensor that a call
  * writes is contiguous and lies apart from everything else that the call
  * touches (KDA_ERR_OVERLAP), but for the pairs that may be one tensor, as
- * stated at the calls.
+ * stated at the calls.  The norm and the convolution take any stride and any
+ * address that is a multiple of the type's size; the scan reads x, B, C and d_out
+ * 16 bytes at a time, at addresses that are multiples of 16 bytes, with strides that
+ * are multiples of 8 elements (KDA_ERR_ALIGN otherwise), and its other tensors of
+ * more than one dimension, dt and ddt aside, begin at such addresses too.  Strides of
+ * more than 2^40 elements, more than 2^40 rows or tokens, more than 2^22 columns or
+ * channels, and scans of more than 2^31 - 128 tokens, 65535 heads or 2^31 - 1
+ * sequences, pieces or chunks are refused (KDA_ERR_SHAPE).
  *
  * Packed batches.  With cu_seqlens (int64 [num_seqs + 1], cu[0] = 0, never
  * falling, cu[num_seqs] <= T), B is 1 and sequence n holds the tokens
