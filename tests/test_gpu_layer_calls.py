@@ -227,3 +227,29 @@ def test_more_than_32_bits_of_entries():
     say("case 2^31 entries: scan's gradient")
     d, dl = kda.ssm_bwd(*big, None, big[0])["dx"][0, -tail:].float(), kda.ssm_bwd(*small, None, small[0])["dx"][0].float()
     assert float((d - dl).abs().max()) <= (2.0 ** -7 + 2.0 ** -15) * float(dl.abs().max())
+
+
+def test_the_library_takes_its_own_workspace(monkeypatch):
+    """Through the C ABI without a workspace: taken and given back on the stream, with the same results."""
+    from gated_delta_rule_110_amd import layer as L
+
+    lens = [300, 0, 5, 129]
+    a, s = make(1, sum(lens), 4, 64, 1, 128, len(lens), F32, seed=7)
+    cu = torch.tensor(R.bounds(lens), dtype=torch.int64, device="cuda")
+    dy = torch.randn(a["x"].shape, device="cuda").to(BF)
+    x, w, wc = torch.randn(1, 434, 256, device="cuda").to(BF), torch.randn(256, device="cuda"), torch.randn(256, 4, device="cuda")
+    u, odd = torch.randn(70, 256, device="cuda").to(BF), torch.randn(70, 77, device="cuda").to(BF)
+
+    def run():
+        return [t.clone() for t in (*kda.ssm_fwd(*a.values(), initial_state=s, final_state=torch.empty_like(s), cu_seqlens=cu, piece_chunks=1),
+                                    *kda.ssm_bwd(*a.values(), dy, initial_state=s, cu_seqlens=cu, piece_chunks=1).values(),
+                                    *kda.conv_bwd(x, wc, None, "silu", x, cu_seqlens=cu).values(),
+                                    *kda.rmsnorm_bwd(u, w, 1e-5, u).values(), *kda.rmsnorm_bwd(odd, w[:77].clone(), 1e-5, odd).values())
+                if t is not None]
+    want = run()
+    none = []
+    monkeypatch.setattr(L, "_workspace", lambda t, need, dev, d: none.append(need))
+    for rep in range(3):
+        same(run(), want)
+    torch.cuda.synchronize()
+    assert len(none) == 15 and all(n > 0 for n in none)
