@@ -14,7 +14,8 @@ q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state,
 final_state, cu_seqlens.
 
 The operators around the recurrence (RMS normalisation, short convolution,
-state-space scan) are in ``layer`` and are offered here as well.
+state-space scan) are in ``layer``, latent attention with its cache in
+``latent``; both are offered here as well.
 """
 from __future__ import annotations
 
@@ -25,9 +26,10 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import layer
+from . import latent, layer
 from ._build import LIB as LIB_PATH
 from ._build import build
+from .latent import latent_attention, latent_bwd, latent_bwd_workspace_size, latent_fwd, latent_workspace_size
 from .layer import (conv_bwd, conv_bwd_workspace_size, conv_decode, conv_fwd, rms_norm, rmsnorm_bwd,
                     rmsnorm_bwd_workspace_size, rmsnorm_fwd, rmsnorm_quant, short_conv, ssm_bwd,
                     ssm_bwd_workspace_size, ssm_decode, ssm_fwd, ssm_piece_chunks, ssm_scan, ssm_workspace_size)
@@ -38,7 +40,8 @@ __all__ = ["fwd", "fwd_noalloc", "noalloc_max_workspace", "decode", "bwd", "bwd_
            "KDA_FP32",
            "rmsnorm_fwd", "rmsnorm_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "rms_norm",
            "conv_fwd", "conv_decode", "conv_bwd", "conv_bwd_workspace_size", "short_conv", "ssm_fwd", "ssm_decode",
-           "ssm_bwd", "ssm_scan", "ssm_workspace_size", "ssm_bwd_workspace_size", "ssm_piece_chunks"]
+           "ssm_bwd", "ssm_scan", "ssm_workspace_size", "ssm_bwd_workspace_size", "ssm_piece_chunks",
+           "latent_fwd", "latent_bwd", "latent_attention", "latent_workspace_size", "latent_bwd_workspace_size"]
 
 KDA_BF16 = 1
 KDA_FP32 = 2
@@ -118,7 +121,8 @@ def library() -> ctypes.CDLL:
             lib.kda_bwd_workspace_size.argtypes = [ctypes.POINTER(KdaDesc)]
             lib.kda_status_string.restype = ctypes.c_char_p
             lib.kda_status_string.argtypes = [ctypes.c_int]
-            layer._declare(lib)
+            latent._declare(lib)
+            layer._declare(lib)  # publishes the library to both
             _lib = lib
     return _lib
 

@@ -1,0 +1,495 @@
+// kda_latent_bwd.hip -- the gradient of latent attention in its expanded form
+// (kda_latent_bwd in include/kda_latent.h).
+//
+// Two passes over the pairs of queries and keys, each with the sums that it can keep
+// in accumulators, so that nothing is added up in memory in an order left to chance:
+//   dq:  a workgroup has 128 queries and runs through the keys they see,
+//        S^T = K Q^T, dP^T = V dO^T, dQ^T += K^T dS^T          (32 products a 32 x 32 block)
+//   dkv: a workgroup has 128 keys and runs through the queries that see them,
+//        S = Q K^T, dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS   (40 products)
+// with P = e^(scale S - lse) and dS = P (dP - delta).  (One pass would take S and dP
+// once, 52 products instead of 72, but add dQ up in fp32 memory.)  As in the forward a
+// wave has 32 of its own side's tokens in registers, the lane's column, and the other side's come
+// through LDS, 64 at a time; P and dS are fed back as B operands as they stand.  A unit is
+// 32 tokens of the other side: the first products of unit u + 1 run beside the
+// exponentials of unit u.  Every head leaves its part of dk_pe in fp32; they are added up
+// in the order of the heads.
+//
+// Precision: fp32 but for P and dS, rounded to bf16 for the products they enter (2^-9 of
+// each, as large as the outputs' own rounding); delta and lse are fp32.
+#include "kda_latent_common.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kBlock = kLatentBwdBlock;
+
+struct StatArgs {
+    float *lse2, *delta;
+};
+
+// P and dS of unit entries: x in 0 .. 15 a probability, then 16 .. 31 a dS.
+struct Pairs {
+    uint32_t p[8], e[8];
+    float last;
+};
+__device__ __forceinline__ s8 operand_of(const uint32_t (&w)[8], int s) {
+    const u4v v = {w[4 * s], w[4 * s + 1], w[4 * s + 2], w[4 * s + 3]};
+    return __builtin_bit_cast(s8, v);
+}
+
+// ---- dq -----------------------------------------------------------------------------
+
+constexpr int kStages = 3;  // tiles in LDS: two in use, one on its way
+struct DqSmem {
+    uint16_t kn[kStages][kKeys * kNope];
+    uint16_t kp[kStages][kKeys * kPe];
+    uint16_t v[kStages][kKeys * kVal];
+};
+struct DqState {
+    s8 q[kQk / 16], y[kVal / 16];
+    f16v dq[kQk / 32];
+    float lse2, delta;
+};
+struct DqAddr {
+    uint32_t kn, kp, v;      // row operands in buffer 0
+    uint32_t tn, tp;         // column operands
+};
+
+// Slots of a unit: the first products of the next one, S and dP in turn, then dQ's.
+constexpr int kSdSlots = kQk / 16 + kVal / 16;
+__device__ __forceinline__ bool is_s(int n) { return n < 2 * kVal / 16 ? (n & 1) == 0 : true; }
+__device__ __forceinline__ int sd_block(int n) { return n < 2 * kVal / 16 ? n >> 1 : n - kVal / 16; }
+
+template <bool NEXT>
+__device__ __forceinline__ void dq_unit(DqState &f, const DqAddr &at, int buf, int half, int nbuf, int nhalf, f16v &s, f16v &dp,
+                                        f16v &s2, f16v &dp2, float c) {
+    constexpr int kAhead = 4, kFirst = NEXT ? 0 : kSdSlots, kAll = kSdSlots + 2 * kQk / 32;
+    Pairs w;
+    const auto operand = [&](int n) -> s8 {
+        if (n < kSdSlots) {
+            const int ks = sd_block(n);
+            if (!is_s(n)) return row_operand<2 * kVal>(at.v + nbuf * (uint32_t)sizeof(DqSmem::v[0]), nhalf, ks);
+            return ks < kNope / 16 ? row_operand<2 * kNope>(at.kn + nbuf * (uint32_t)sizeof(DqSmem::kn[0]), nhalf, ks)
+                                   : row_operand<2 * kPe>(at.kp + nbuf * (uint32_t)sizeof(DqSmem::kp[0]), nhalf, ks - kNope / 16);
+        }
+        const int m = n - kSdSlots, ks = m / (kQk / 32), dt = m % (kQk / 32);
+        return dt < kNope / 32 ? col_operand<2 * kNope>(at.tn + buf * (uint32_t)sizeof(DqSmem::kn[0]), 2 * half + ks, dt)
+                               : col_operand<2 * kPe>(at.tp + buf * (uint32_t)sizeof(DqSmem::kp[0]), 2 * half + ks, dt - kNope / 32);
+    };
+    const auto pair = [&](int i) {  // dS of entry i
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -f.lse2)) * (dp[i] - f.delta);
+        if (i & 1) w.e[i / 2] = pack2(w.last, e);
+        else w.last = e;
+    };
+    s8 ring[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) ring[(kFirst + n) % kAhead] = operand(kFirst + n);
+    if (NEXT) {
+        s2 = zero16();
+        dp2 = zero16();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pair(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = kFirst; n < kAll; ++n) {
+        const s8 a = ring[n % kAhead];
+        const int m = n - kSdSlots;
+        if (m >= 0) f.dq[m % (kQk / 32)] = mfma32(a, operand_of(w.e, m / (kQk / 32)), f.dq[m % (kQk / 32)]);
+        else if (is_s(n)) s2 = mfma32(a, f.q[sd_block(n)], s2);
+        else dp2 = mfma32(a, f.y[sd_block(n)], dp2);
+        if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
+        if (NEXT && n < 16) pair(n);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+__global__ __launch_bounds__(256, 1) void latent_dq_kernel(LatentArgs a) {
+    __shared__ __attribute__((aligned(1024))) DqSmem sm;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
+    Span sp;
+    if (!span_of(a, unit / a.H, a.causal, sp)) return;
+    const int q_first = sp.block * kBlock + wave * 32;
+    const int block_last = min(sp.lq, (sp.block + 1) * kBlock) - 1;
+    if (block_last < sp.block * kBlock) return;
+    const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
+    const int tiles = (sees(block_last) + kKeys - 1) / kKeys;
+    const int last = min(sp.lq - 1, q_first + 31);
+    const int mine = last < q_first ? 0 : (sees(last) + kKeys - 1) / kKeys;  // of this wave
+    const int whole = sees(q_first) / 32;                                    // units without hidden keys
+
+    const uint16_t *kv = a.kv + sp.b * a.kvb + sp.k0 * a.kvt + h * kKvRow;
+    const uint16_t *pe = a.pe + sp.b * a.peb + sp.k0 * a.pet;
+    const uint32_t kv_bytes = (uint32_t)a.kvt * 2, pe_bytes = (uint32_t)a.pet * 2;
+    const uint32_t off_n = tile_offset<kNope>(tid, kv_bytes), off_p = tile_offset<kPe>(tid, pe_bytes);
+    const uint32_t lds_kn = lds_addr(sm.kn), lds_kp = lds_addr(sm.kp), lds_v = lds_addr(sm.v);
+    const auto copy = [&](int j) {
+        if (j >= tiles) return;
+        const int rows = min(kKeys, sp.lk - j * kKeys), buf = j % kStages;
+        const uint16_t *p = kv + (int64_t)j * kKeys * a.kvt;
+        copy_tile<kNope>(p, rows, kv_bytes, off_n, lds_kn + buf * (uint32_t)sizeof(sm.kn[0]), wave);
+        copy_tile<kPe>(pe + (int64_t)j * kKeys * a.pet, rows, pe_bytes, off_p, lds_kp + buf * (uint32_t)sizeof(sm.kp[0]), wave);
+        copy_tile<kVal>(p + kNope, rows, kv_bytes, off_n, lds_v + buf * (uint32_t)sizeof(sm.v[0]), wave);
+    };
+    copy(0);
+    copy(1);
+
+    DqState f;
+    const int i = q_first + (lane & 31), row = min(i, sp.lq - 1);  // rows behind the last: of no effect, not stored
+    const int seen = sees(i);
+    {
+        const int64_t t = sp.b * a.T + sp.q0 + row;
+        const uint16_t *q = a.q + sp.b * a.qb + (sp.q0 + row) * a.qt + h * kQk + 8 * g;
+        const uint16_t *y = a.dy + sp.b * a.yb + (sp.q0 + row) * a.yt + h * kVal + 8 * g;
+        const uint16_t *o = a.o + sp.b * a.ob + (sp.q0 + row) * a.ot + h * kVal + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < kQk / 16; ++ks) f.q[ks] = *reinterpret_cast<const s8 *>(q + 16 * ks);
+        float d = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < kVal / 16; ++ks) {
+            f.y[ks] = *reinterpret_cast<const s8 *>(y + 16 * ks);
+            const s8 v = *reinterpret_cast<const s8 *>(o + 16 * ks);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d = fmaf(bf16_bits_to_f32((uint16_t)f.y[ks][j]), bf16_bits_to_f32((uint16_t)v[j]), d);
+        }
+        f.delta = pair_sum(d);
+        const float lse = a.lse_in[t * a.H + h];
+        f.lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+        if (g == 0 && i < sp.lq) {
+            float *stat = a.stat + h * a.B * a.T + t;
+            stat[0] = f.lse2;
+            stat[a.H * a.B * a.T] = f.delta;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < kQk / 32; ++d) f.dq[d] = zero16();
+    const DqAddr at = {row_at<2 * kNope>(lds_kn, lane), row_at<2 * kPe>(lds_kp, lane), row_at<2 * kVal>(lds_v, lane),
+                       col_at<2 * kNope>(lds_kn, lane), col_at<2 * kPe>(lds_kp, lane)};
+    const float c = a.scale * kLog2e;
+
+    const auto hide = [&](int u, f16v &s) {
+        if (u < whole) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = u * 32 + 8 * (e / 4) + 4 * g + e % 4 < seen ? s[e] : -INFINITY;
+    };
+    // Tile t is there and tile t - 1 read, whose place the next copies take.
+    const auto begin = [&](int t) {
+        copies_done();
+        copy(t + 1);
+    };
+    int t = 0;
+    if (tiles > 0) copies_done();
+    if (mine > 0) {
+        f16v s0, d0, s1, d1;
+        s0 = d0 = zero16();
+#pragma unroll
+        for (int n = 0; n < kSdSlots; ++n) {
+            const int ks = sd_block(n);
+            if (is_s(n))
+                s0 = mfma32(ks < kNope / 16 ? row_operand<2 * kNope>(at.kn, 0, ks) : row_operand<2 * kPe>(at.kp, 0, ks - kNope / 16),
+                            f.q[ks], s0);
+            else
+                d0 = mfma32(row_operand<2 * kVal>(at.v, 0, ks), f.y[ks], d0);
+            if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        int st = 0;
+        for (; t < mine - 1; ++t) {
+            const int next = st == kStages - 1 ? 0 : st + 1;
+            begin(t + 1);
+            hide(2 * t, s0);
+            dq_unit<true>(f, at, st, 0, st, 1, s0, d0, s1, d1, c);
+            hide(2 * t + 1, s1);
+            dq_unit<true>(f, at, st, 1, next, 0, s1, d1, s0, d0, c);
+            st = next;
+        }
+        hide(2 * t, s0);
+        dq_unit<true>(f, at, st, 0, st, 1, s0, d0, s1, d1, c);
+        hide(2 * t + 1, s1);
+        dq_unit<false>(f, at, st, 1, 0, 0, s1, d1, s0, d0, c);
+        ++t;
+    } else {
+        ++t;
+    }
+    for (; t < tiles; ++t) begin(t);
+
+    if (i >= sp.lq) return;
+    uint16_t *out = a.dq + ((sp.b * a.T + sp.q0 + i) * a.H + h) * kQk + 4 * g;
+#pragma unroll
+    for (int d = 0; d < kQk / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u2v w = {pack2(f.dq[d][4 * e] * a.scale, f.dq[d][4 * e + 1] * a.scale),
+                           pack2(f.dq[d][4 * e + 2] * a.scale, f.dq[d][4 * e + 3] * a.scale)};
+            *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = w;
+        }
+}
+
+// ---- dkv ----------------------------------------------------------------------------
+
+struct DkvSmem {
+    uint16_t qn[kStages][kKeys * kNope];
+    uint16_t qp[kStages][kKeys * kPe];
+    uint16_t y[kStages][kKeys * kVal];
+    float lse2[kStages][kKeys], delta[kStages][kKeys];
+};
+struct DkvState {
+    s8 k[kQk / 16], v[kVal / 16];
+    f16v dk[kQk / 32], dv[kVal / 32];
+};
+struct DkvAddr {
+    uint32_t qn, qp, y;      // row operands in stage 0
+    uint32_t tn, tp, ty;     // column operands
+    uint32_t stat;           // lse2 of the lane's first query
+};
+typedef const __attribute__((address_space(3))) f4 *lds_f4;
+
+template <bool NEXT>
+__device__ __forceinline__ void dkv_unit(DkvState &f, const DkvAddr &at, int st, int half, int nst, int nhalf, f16v &s, f16v &dp,
+                                         f16v &s2, f16v &dp2, float c) {
+    constexpr int kAhead = 4, kFirst = NEXT ? 0 : kSdSlots, kDv = 2 * kVal / 32, kAll = kSdSlots + kDv + 2 * kQk / 32;
+    Pairs w;
+    f4 lse2[4], delta[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t p = at.stat + st * (kKeys * 4) + half * 128 + e * 32;
+        lse2[e] = *reinterpret_cast<lds_f4>(p);
+        delta[e] = *reinterpret_cast<lds_f4>(p + (uint32_t)sizeof(DkvSmem::lse2));
+    }
+    const auto operand = [&](int n) -> s8 {
+        if (n < kSdSlots) {
+            const int ks = sd_block(n);
+            if (!is_s(n)) return row_operand<2 * kVal>(at.y + nst * (uint32_t)sizeof(DkvSmem::y[0]), nhalf, ks);
+            return ks < kNope / 16 ? row_operand<2 * kNope>(at.qn + nst * (uint32_t)sizeof(DkvSmem::qn[0]), nhalf, ks)
+                                   : row_operand<2 * kPe>(at.qp + nst * (uint32_t)sizeof(DkvSmem::qp[0]), nhalf, ks - kNope / 16);
+        }
+        int m = n - kSdSlots;
+        if (m < kDv) return col_operand<2 * kVal>(at.ty + st * (uint32_t)sizeof(DkvSmem::y[0]), 2 * half + m / (kVal / 32), m % (kVal / 32));
+        m -= kDv;
+        const int ks = 2 * half + m / (kQk / 32), dt = m % (kQk / 32);
+        return dt < kNope / 32 ? col_operand<2 * kNope>(at.tn + st * (uint32_t)sizeof(DkvSmem::qn[0]), ks, dt)
+                               : col_operand<2 * kPe>(at.tp + st * (uint32_t)sizeof(DkvSmem::qp[0]), ks, dt - kNope / 32);
+    };
+    // Entry i's probability takes the place of its score.
+    const auto prob = [&](int i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2[i / 4][i % 4]));
+        if (i & 1) w.p[i / 2] = pack2(s[i - 1], s[i]);
+    };
+    const auto pair = [&](int i) {
+        const float e = s[i] * (dp[i] - delta[i / 4][i % 4]);
+        if (i & 1) w.e[i / 2] = pack2(w.last, e);
+        else w.last = e;
+    };
+    s8 ring[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) ring[(kFirst + n) % kAhead] = operand(kFirst + n);
+    if (NEXT) {
+        s2 = zero16();
+        dp2 = zero16();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) prob(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = kFirst; n < kAll; ++n) {
+        const s8 a = ring[n % kAhead];
+        const int m = n - kSdSlots;
+        if (m >= kDv) {
+            const int x = m - kDv;
+            f.dk[x % (kQk / 32)] = mfma32(a, operand_of(w.e, x / (kQk / 32)), f.dk[x % (kQk / 32)]);
+        } else if (m >= 0) {
+            f.dv[m % (kVal / 32)] = mfma32(a, operand_of(w.p, m / (kVal / 32)), f.dv[m % (kVal / 32)]);
+        } else if (is_s(n)) {
+            s2 = mfma32(a, f.k[sd_block(n)], s2);
+        } else {
+            dp2 = mfma32(a, f.v[sd_block(n)], dp2);
+        }
+        if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
+        if (NEXT && n < 16) prob(n);
+        if (m >= 0 && m < kDv) {  // dS, which the products behind these take
+            pair(2 * m);
+            pair(2 * m + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+__global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentArgs a) {
+    __shared__ __attribute__((aligned(1024))) DkvSmem sm;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
+    Span sp;
+    if (!span_of(a, unit / a.H, false, sp)) return;
+    if (sp.block * kBlock >= sp.lk) return;
+    const int k_first = sp.block * kBlock + wave * 32;
+    // The first query that sees key j, and with it all behind it.
+    const int lead = sp.lk - sp.lq;
+    const auto seen_from = [&](int j) { return a.causal ? max(0, j - lead) : 0; };
+    const int first = seen_from(sp.block * kBlock) / kKeys;           // tiles of queries
+    const int tiles = max(first, (sp.lq + kKeys - 1) / kKeys);        // (one behind the last)
+    const int j = k_first + (lane & 31), row = min(j, sp.lk - 1);
+    const int from = seen_from(j);                                    // of the lane's key
+    const int top_key = min(k_first + 31, sp.lk - 1);
+    const int whole = (seen_from(top_key) + 31) / 32;                 // units from here on see all of the wave's keys
+    const int full = sp.lq / 32;                                      // units behind these are not full
+
+    const int64_t tok = sp.b * a.T + sp.q0;
+    const uint16_t *q = a.q + sp.b * a.qb + sp.q0 * a.qt + h * kQk;
+    const uint16_t *y = a.dy + sp.b * a.yb + sp.q0 * a.yt + h * kVal;
+    const float *stat = a.stat + h * a.B * a.T + tok;
+    const uint32_t q_bytes = (uint32_t)a.qt * 2, y_bytes = (uint32_t)a.yt * 2;
+    const uint32_t off_n = tile_offset<kNope>(tid, q_bytes), off_p = tile_offset<kPe>(tid, q_bytes),
+                   off_y = tile_offset<kVal>(tid, y_bytes);
+    const uint32_t lds_qn = lds_addr(sm.qn), lds_qp = lds_addr(sm.qp), lds_y = lds_addr(sm.y), lds_l = lds_addr(sm.lse2),
+                   lds_d = lds_addr(sm.delta);
+    const auto copy = [&](int t) {
+        if (t >= tiles) return;
+        const int rows = min(kKeys, sp.lq - t * kKeys), st = t % kStages;
+        const uint16_t *p = q + (int64_t)t * kKeys * a.qt;
+        copy_tile<kNope>(p, rows, q_bytes, off_n, lds_qn + st * (uint32_t)sizeof(sm.qn[0]), wave);
+        copy_tile<kPe>(p + kNope, rows, q_bytes, off_p, lds_qp + st * (uint32_t)sizeof(sm.qp[0]), wave);
+        copy_tile<kVal>(y + (int64_t)t * kKeys * a.yt, rows, y_bytes, off_y, lds_y + st * (uint32_t)sizeof(sm.y[0]), wave);
+        if (wave < 2) {
+            const float *x = stat + (wave ? a.H * a.B * a.T : 0) + (int64_t)t * kKeys;
+            copy4(buffer_of(x, (uint32_t)rows * 4), (uint32_t)lane * 4, (wave ? lds_d : lds_l) + st * (kKeys * 4));
+        }
+    };
+    copy(first);
+    copy(first + 1);
+
+    DkvState f;
+    {
+        const uint16_t *kv = a.kv + sp.b * a.kvb + (sp.k0 + row) * a.kvt + h * kKvRow + 8 * g;
+        const uint16_t *pe = a.pe + sp.b * a.peb + (sp.k0 + row) * a.pet + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < kQk / 16; ++ks)
+            f.k[ks] = ks < kNope / 16 ? *reinterpret_cast<const s8 *>(kv + 16 * ks)
+                                      : *reinterpret_cast<const s8 *>(pe + 16 * ks - kNope);
+#pragma unroll
+        for (int ks = 0; ks < kVal / 16; ++ks) f.v[ks] = *reinterpret_cast<const s8 *>(kv + kNope + 16 * ks);
+    }
+#pragma unroll
+    for (int d = 0; d < kQk / 32; ++d) f.dk[d] = zero16();
+#pragma unroll
+    for (int d = 0; d < kVal / 32; ++d) f.dv[d] = zero16();
+    const DkvAddr at = {row_at<2 * kNope>(lds_qn, lane), row_at<2 * kPe>(lds_qp, lane), row_at<2 * kVal>(lds_y, lane),
+                        col_at<2 * kNope>(lds_qn, lane), col_at<2 * kPe>(lds_qp, lane), col_at<2 * kVal>(lds_y, lane),
+                        lds_l + 16 * g};
+    const float c = a.scale * kLog2e;
+
+    // Queries that do not see the lane's key, or are none.
+    const auto hide = [&](int u, f16v &s) {
+        if (u >= whole && u < full) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int i = u * 32 + 8 * (e / 4) + 4 * g + e % 4;
+            s[e] = i >= from && i < sp.lq ? s[e] : -INFINITY;
+        }
+    };
+    if (first < tiles) {
+        f16v s0, d0, s1, d1;
+        copies_done();
+        s0 = d0 = zero16();
+        int st = first % kStages;
+#pragma unroll
+        for (int n = 0; n < kSdSlots; ++n) {
+            const int ks = sd_block(n);
+            const uint32_t qn = at.qn + st * (uint32_t)sizeof(sm.qn[0]), qp = at.qp + st * (uint32_t)sizeof(sm.qp[0]);
+            if (is_s(n))
+                s0 = mfma32(ks < kNope / 16 ? row_operand<2 * kNope>(qn, 0, ks) : row_operand<2 * kPe>(qp, 0, ks - kNope / 16), f.k[ks], s0);
+            else
+                d0 = mfma32(row_operand<2 * kVal>(at.y + st * (uint32_t)sizeof(sm.y[0]), 0, ks), f.v[ks], d0);
+            if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int t = first; t < tiles - 1; ++t) {
+            const int next = st == kStages - 1 ? 0 : st + 1;
+            copies_done();  // tile t + 1 is there, and tile t - 1 read
+            copy(t + 2);
+            hide(2 * t, s0);
+            dkv_unit<true>(f, at, st, 0, st, 1, s0, d0, s1, d1, c);
+            hide(2 * t + 1, s1);
+            dkv_unit<true>(f, at, st, 1, next, 0, s1, d1, s0, d0, c);
+            st = next;
+        }
+        hide(2 * tiles - 2, s0);
+        dkv_unit<true>(f, at, st, 0, st, 1, s0, d0, s1, d1, c);
+        hide(2 * tiles - 1, s1);
+        dkv_unit<false>(f, at, st, 1, 0, 0, s1, d1, s0, d0, c);
+    }
+
+    if (j >= sp.lk) return;
+    const int64_t key = sp.b * a.Tk + sp.k0 + j;
+    uint16_t *out = a.dkv + (key * a.H + h) * kKvRow + 4 * g;
+    float *part = a.dpe_part + (h * a.B * a.Tk + key) * kPe + 4 * g;
+#pragma unroll
+    for (int d = 0; d < kQk / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = f.dk[d][4 * e + r] * a.scale;
+            if (d < kNope / 32) {
+                const u2v w = {pack2(x[0], x[1]), pack2(x[2], x[3])};
+                *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = w;
+            } else {
+                *reinterpret_cast<f4 *>(part + 32 * (d - kNope / 32) + 8 * e) = x;
+            }
+        }
+#pragma unroll
+    for (int d = 0; d < kVal / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u2v w = {pack2(f.dv[d][4 * e], f.dv[d][4 * e + 1]), pack2(f.dv[d][4 * e + 2], f.dv[d][4 * e + 3])};
+            *reinterpret_cast<u2v *>(out + kNope + 32 * d + 8 * e) = w;
+        }
+}
+
+// dk_pe: the heads' parts added up, 4 values a thread, heads in order.
+__global__ __launch_bounds__(256) void latent_dpe_kernel(const float *part, uint16_t *dpe, const int64_t *cuk, int64_t seqs, int64_t Tk,
+                                                         int64_t keys, int64_t H, int64_t base) {
+    const int64_t i = (base + blockIdx.x) * 256 + threadIdx.x;
+    const int64_t live = cuk ? clamp64(cuk[seqs], 0, Tk) : keys;
+    if (i >= live * (kPe / 4)) return;
+    const f4 *p = reinterpret_cast<const f4 *>(part) + i;
+    const int64_t step = keys * (kPe / 4);
+    f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int64_t h = 0; h < H; ++h) s += p[h * step];
+    reinterpret_cast<u2v *>(dpe)[i] = u2v{pack2(s[0], s[1]), pack2(s[2], s[3])};
+}
+
+}  // namespace
+
+}  // namespace kda
+
+using namespace kda;
+
+hipError_t kda_launch_latent_dq(const LatentArgs &a, hipStream_t s) {
+    return launch_groups(a.blocks * a.B * a.H, a.launch_cap, [&](int64_t base, dim3 grid) {
+        LatentArgs p = a;
+        p.base = base;
+        hipLaunchKernelGGL(latent_dq_kernel, grid, dim3(256), 0, s, p);
+    });
+}
+
+hipError_t kda_launch_latent_dkv(const LatentArgs &a, hipStream_t s) {
+    return launch_groups(a.blocks * a.B * a.H, a.launch_cap, [&](int64_t base, dim3 grid) {
+        LatentArgs p = a;
+        p.base = base;
+        hipLaunchKernelGGL(latent_dkv_kernel, grid, dim3(256), 0, s, p);
+    });
+}
+
+hipError_t kda_launch_latent_dpe(const LatentArgs &a, hipStream_t s) {
+    const int64_t keys = a.B * a.Tk;
+    return launch_groups((keys * (kPe / 4) + 255) / 256, a.launch_cap, [&](int64_t base, dim3 grid) {
+        hipLaunchKernelGGL(latent_dpe_kernel, grid, dim3(256), 0, s, a.dpe_part, a.dpe, a.cu ? a.cuk : nullptr, a.seqs, a.Tk, keys, a.H,
+                           base);
+    });
+}

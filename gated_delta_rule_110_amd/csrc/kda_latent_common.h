@@ -1,0 +1,178 @@
+// kda_latent_common.h -- device code that the latent attention kernels share:
+// 32 x 32 matrix instructions, tiles in LDS, a block's sequence.
+//
+// Lane l of a wave is (n = l % 32, g = l / 32).  v_mfma_f32_32x32x16_bf16 takes 16
+// values of k: A row n and B column n each in 8 k's of lane group g, and leaves in
+// accumulator i of lane l the row 8 (i / 4) + 4 g + i % 4 of column n.  A product's
+// accumulators are fed back as the B operand of the next one without leaving the
+// lane: for k-block s of 16 rows, accumulators 8 s .. 8 s + 7 of the lane stand for
+// the rows perm(s, g, j) = 16 s + 8 (j / 4) + 4 g + j % 4, and the A operand takes
+// its columns in the same order, which is what two transposing LDS reads of 4 rows
+// each deliver (ds_read_tr16_b64: of 4 rows x 16 columns, lane i of 16 gets column i).
+#pragma once
+#include "kda_latent_args.h"
+
+namespace kda {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef int i4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ f16v mfma32(const s8 &a, const s8 &b, const f16v &c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_b8(a), as_b8(b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f16v zero16() {
+    f16v z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+    return z;
+}
+
+// Two fp32 -> two bf16 in one word (one conversion instruction, round to nearest even).
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const f2v v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2v));
+}
+// Accumulators 8 s .. 8 s + 7 as a B operand.
+__device__ __forceinline__ s8 pack8(const f16v &v, int s) {
+    u4v w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2(v[8 * s + 2 * i], v[8 * s + 2 * i + 1]);
+    return __builtin_bit_cast(s8, w);
+}
+
+// The value of lanes n and n + 32, combined in both.
+__device__ __forceinline__ float pair_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---- tiles in LDS -----------------------------------------------------------------
+// A tile holds rows of 16-byte chunks, 8 (or a multiple) to a row, with chunk c of row
+// r at place c ^ swap(r).  Both reads are then without bank conflicts: 16 bytes of 8
+// neighbouring rows (swap takes 8 values), and the transposing read's 32 bytes of 4
+// rows (swap / 2 takes 4).
+__device__ __forceinline__ int swap(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+
+typedef const __attribute__((address_space(3))) s8 *lds_s8;
+typedef __attribute__((address_space(3))) s4 *lds_s4;
+__device__ __forceinline__ s8 read8(uint32_t at) { return *reinterpret_cast<lds_s8>(at); }
+__device__ __forceinline__ s8 read_tr(uint32_t at, uint32_t step) {
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(at));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(at + step));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Row operand of rows 0 .. 31 of a tile of `row` bytes a row, k-block ks: at
+// row_at(...) ^ 32 ks within 128 bytes, 128 bytes further for every 4 k-blocks, 32
+// rows further for the next rows.
+template <int ROW>
+__device__ __forceinline__ uint32_t row_at(uint32_t base, int lane) {
+    const int n = lane & 31, g = lane >> 5;
+    return base + n * ROW + ((g ^ swap(n)) << 4);
+}
+template <int ROW>
+__device__ __forceinline__ s8 row_operand(uint32_t at, int rows32, int ks) {
+    return read8((at ^ ((ks & 3) << 5)) + (ks >> 2) * 128 + rows32 * 32 * ROW);
+}
+// Column operand: 32 columns from 32 dt, the rows perm(s, g, j) of k-block s.
+template <int ROW>
+__device__ __forceinline__ uint32_t col_at(uint32_t base, int lane) {
+    const int i = lane & 15, c16 = (lane >> 4) & 1, g = lane >> 5;
+    const int r = 4 * g + (i >> 2);
+    return base + r * ROW + (((2 * c16 + ((i & 3) >> 1)) ^ swap(r)) << 4) + (i & 1) * 8;
+}
+template <int ROW>
+__device__ __forceinline__ s8 col_operand(uint32_t at, int s, int dt) {
+    return read_tr((at ^ ((dt & 1) << 6)) + (dt >> 1) * 128 + s * 16 * ROW, 8 * ROW);
+}
+
+// Copies from global memory straight into LDS, 16 bytes a lane: the wave's 64 lanes
+// fill 1 KiB from `lds`.  Lanes whose offset is out of the descriptor's range write
+// zeros.  Issued through inline asm, so that the compiler does not wait for them
+// before other LDS reads; they are waited for by copies_done.
+__device__ __forceinline__ void copy16(const i4v &rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" :: "v"(off), "s"(rsrc), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void copy4(const i4v &rsrc, uint32_t off, uint32_t lds) {  // 256 bytes
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" :: "v"(off), "s"(rsrc), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ i4v buffer_of(const void *p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    i4v r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu));
+    r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+// This wave's copies and LDS accesses are done, and every wave's behind the barrier.
+__device__ __forceinline__ void copies_done() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// `rows` (at most 64) rows of 2 W bytes, `stride` bytes apart, into a tile: for a workgroup of 256 threads, W / 8 chunks
+// a row.  voff: tile_offset's; chunk blocks of 256 are voff + i step.
+template <int W>
+__device__ __forceinline__ uint32_t tile_offset(int tid, uint32_t stride) {
+    constexpr int C = W / 8;
+    const int r = tid / C, c = tid % C;
+    return (uint32_t)r * stride + (uint32_t)((c ^ swap(r)) << 4);
+}
+template <int W>
+__device__ __forceinline__ void copy_tile(const uint16_t *p, int rows, uint32_t stride, uint32_t off, uint32_t lds, int wave) {
+    constexpr int C = W / 8, kRows = 256 / C;
+    const i4v rsrc = buffer_of(p, rows > 0 ? (uint32_t)(rows - 1) * stride + 2 * W : 0u);
+#pragma unroll
+    for (int i = 0; i < kKeys / kRows; ++i)
+        copy16(rsrc, off + (uint32_t)(i * kRows) * stride, lds + i * 4096 + wave * 1024);
+}
+
+// ---- a block's sequence ----------------------------------------------------------
+struct Span {
+    int64_t q0, k0;  // first query and key, in rows of the tensors' token dimension
+    int lq, lk;
+    int64_t b;       // batch row
+    int block;
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+__device__ __forceinline__ void bounds_of(const int64_t *cu, int64_t n, int64_t T, int64_t &first, int &len) {
+    const int64_t lo = clamp64(cu[n], 0, T), hi = clamp64(cu[n + 1], lo, T);
+    first = lo;
+    len = (int)(hi - lo);
+}
+
+// The sequence and block of unit e (a workgroup's number over the heads); false where there is none.
+__device__ __forceinline__ bool span_of(const LatentArgs &a, int64_t e, bool reversed, Span &s) {
+    if (a.table) {
+        if (e >= a.table[0]) return false;
+        const int64_t n = a.table[2 + 2 * e];
+        s.block = a.table[3 + 2 * e];
+        bounds_of(a.cu, n, a.T, s.q0, s.lq);
+        bounds_of(a.cuk, n, a.Tk, s.k0, s.lk);
+        s.b = 0;
+    } else {
+        s.b = e % a.B;
+        s.block = (int)(e / a.B);
+        if (reversed) s.block = (int)a.blocks - 1 - s.block;
+        s.q0 = s.k0 = 0;
+        s.lq = (int)a.T;
+        s.lk = (int)a.Tk;
+    }
+    return true;
+}
+
+}  // namespace kda

@@ -1,0 +1,168 @@
+"""Latent attention (``include/kda_latent.h``): keys and values that come from one
+shared vector a token, in the expanded form for prompts and training and in the
+absorbed form for generation from a paged cache of those vectors; the store into
+that cache; and the pages, slots and offsets of a serving step.
+
+The functions marshal arguments as those of ``layer`` do.  Activations are bf16 and
+may be slices of wider tensors: q and kv have to be contiguous behind their token
+dimension, all of them begin at multiples of 16 bytes and have strides that are
+multiples of 8 elements.  Tensors that a call writes are contiguous.
+
+``latent_attention`` differentiates once.  To capture its backward into a HIP
+graph, let no autograd graph of the same leaves from before the capture live
+(delete the outputs and losses of the warm-up first): torch ends such a capture
+with an error, or ends the process.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from .layer import (_BF16, _FP32, _FP32_ONLY, _I, _INT64_ONLY, _P, _bf16, _call, _device_of, _library, _num_seqs, _output, _ptr,
+                    _tokens, _whole, _workspace)
+
+NOPE, PE, VALUE, LATENT = 128, 64, 128, 512  # a head's own key values, the shared ones, its values, the latent
+
+
+class KdaLatentDesc(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("Tk", _I), ("H", _I), ("num_seqs", _I), ("q_stride_b", _I), ("q_stride_t", _I),
+                ("kv_stride_b", _I), ("kv_stride_t", _I), ("pe_stride_b", _I), ("pe_stride_t", _I), ("out_stride_b", _I),
+                ("out_stride_t", _I), ("d_out_stride_b", _I), ("d_out_stride_t", _I), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("launch_piece", _I)]
+
+
+def _declare(lib) -> None:
+    """Argument types of these functions (called once, when the library is loaded)."""
+    A = ctypes.POINTER(KdaLatentDesc)
+    for name, n, desc in (("kda_latent_fwd", 7, A), ("kda_latent_bwd", 11, A)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, [_P] * n + [desc, _P]
+    for name, desc in (("kda_latent_fwd_workspace_size", A), ("kda_latent_bwd_workspace_size", A)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_size_t, [desc]
+
+
+# ---- the expanded form -----------------------------------------------------------
+
+def _latent_args(q, kv, k_pe, scale, causal, cu, cu_k):
+    """(descriptor, device) of a call's inputs."""
+    dev = _device_of(q)
+    for t, name in ((q, "q"), (kv, "kv"), (k_pe, "k_pe")):
+        _bf16(t, name, dev)
+    if q.dim() != 4 or q.shape[3] != NOPE + PE:
+        raise ValueError("q must be [B, T, H, %d]" % (NOPE + PE))
+    B, T, H = q.shape[:3]
+    if kv.dim() != 4 or kv.shape[0] != B or kv.shape[2:] != (H, NOPE + VALUE):
+        raise ValueError("kv must be [B, Tk, H, %d] with q's B and H" % (NOPE + VALUE))
+    Tk = kv.shape[1]
+    if k_pe.shape != (B, Tk, PE):
+        raise ValueError("k_pe must be [B, Tk, %d] with kv's B and Tk" % PE)
+    n = _num_seqs(cu, B, dev)
+    if cu_k is not None:
+        if cu is None:
+            raise ValueError("cu_seqlens_k without cu_seqlens")
+        _whole(cu_k, "cu_seqlens_k", (n + 1,), dev, _INT64_ONLY)
+    elif cu is not None and T != Tk:
+        raise ValueError("packed queries and keys of different number need cu_seqlens_k")
+    return KdaLatentDesc(B, T, Tk, H, n, *_tokens(q, "q"), *_tokens(kv, "kv"), *_tokens(k_pe, "k_pe"), 0, 0, 0, 0, scale,
+                         int(bool(causal))), dev
+
+
+def latent_workspace_size(B: int, T: int, Tk: int, H: int, num_seqs: Optional[int] = None) -> int:
+    """Workspace bytes ``latent_fwd`` needs for these sizes as a packed batch of num_seqs sequences (0 if it is none)."""
+    return 0 if num_seqs is None else int(_library().kda_latent_fwd_workspace_size(_sizes(B, T, Tk, H, num_seqs)))
+
+
+def _sizes(B, T, Tk, H, n):
+    return KdaLatentDesc(B, T, Tk, H, n, scale=1.0)
+
+
+def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float, causal: bool = True,
+               cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of every head with the keys ``(kv[..., :128], k_pe)``, of which the second part is shared by all
+    heads, and the values ``kv[..., 128:]``.  Returns ``(out, lse)``: bf16 [B, T, H, 128] and the scores' log-sum-exp,
+    fp32 [B, T, H].
+
+    q: bf16 [B, T, H, 192]; kv: bf16 [B, Tk, H, 256]; k_pe: bf16 [B, Tk, 64]; scale: of the scores, above zero;
+    causal: the last query of a sequence sees all its keys, each one before it one less; cu_seqlens, cu_seqlens_k:
+    int64 offsets of a packed batch's queries and keys (B = 1; the keys' are the queries' if None).  A query that
+    sees no key has out 0 and lse -inf."""
+    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
+    out = _output(out, "out", (d.B, d.T, d.H, VALUE), torch.bfloat16, dev)
+    lse = _output(lse, "lse", (d.B, d.T, d.H), torch.float32, dev)
+    ws = None
+    if cu_seqlens is not None:
+        ws = _workspace(workspace, _library().kda_latent_fwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    _call(_library().kda_latent_fwd, dev, q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), _ptr(cu_seqlens), _ptr(cu_seqlens_k),
+          out.data_ptr(), lse.data_ptr(), d)
+    return out, lse
+
+
+def latent_bwd_workspace_size(B: int, T: int, Tk: int, H: int, num_seqs: Optional[int] = None) -> int:
+    """Workspace bytes ``latent_bwd`` needs for these sizes (num_seqs: of a packed batch)."""
+    return int(_library().kda_latent_bwd_workspace_size(_sizes(B, T, Tk, H, B if num_seqs is None else num_seqs)))
+
+
+def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float, out: torch.Tensor, lse: torch.Tensor,
+               d_out: torch.Tensor, causal: bool = True, cu_seqlens: Optional[torch.Tensor] = None,
+               cu_seqlens_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               outputs: Optional[dict] = None) -> dict:
+    """Gradient of ``latent_fwd`` for the loss's gradient d_out (bf16 [B, T, H, 128]), from its inputs and what it
+    returned (out, lse).  Returns a dict of bf16 tensors: dq [B, T, H, 192], dkv [B, Tk, H, 256] and dk_pe [B, Tk, 64],
+    summed over the heads.  outputs: None, or a dict of tensors of those names to write into."""
+    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
+    for t, name in ((out, "out"), (d_out, "d_out")):
+        _bf16(t, name, dev)
+        if t.shape != (d.B, d.T, d.H, VALUE):
+            raise ValueError("%s must be [B, T, H, %d]" % (name, VALUE))
+    _whole(lse, "lse", (d.B, d.T, d.H), dev, _FP32_ONLY)
+    d.out_stride_b, d.out_stride_t = _tokens(out, "out")
+    d.d_out_stride_b, d.d_out_stride_t = _tokens(d_out, "d_out")
+    given = outputs or {}
+    dq = _output(given.get("dq"), "dq", (d.B, d.T, d.H, NOPE + PE), torch.bfloat16, dev)
+    dkv = _output(given.get("dkv"), "dkv", (d.B, d.Tk, d.H, NOPE + VALUE), torch.bfloat16, dev)
+    dpe = _output(given.get("dk_pe"), "dk_pe", (d.B, d.Tk, PE), torch.bfloat16, dev)
+    lib = _library()
+    ws = _workspace(workspace, lib.kda_latent_bwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    _call(lib.kda_latent_bwd, dev, q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), _ptr(cu_seqlens), _ptr(cu_seqlens_k),
+          out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(), dkv.data_ptr(), dpe.data_ptr(), d)
+    return {"dq": dq, "dkv": dkv, "dk_pe": dpe}
+
+
+class LatentFunction(torch.autograd.Function):
+    """``latent_fwd`` with ``latent_bwd`` as its gradient."""
+
+    @staticmethod
+    def forward(ctx, q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k):
+        out, lse = latent_fwd(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
+        if cu_seqlens is not None:  # rows behind the last sequence, which the kernels leave as they were
+            row = torch.arange(out.shape[1], device=out.device)[None, :, None, None]
+            out.masked_fill_(row >= cu_seqlens[-1], 0)
+        ctx.save_for_backward(q, kv, k_pe, out, lse, cu_seqlens, cu_seqlens_k)
+        ctx.scale, ctx.causal = float(scale), bool(causal)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        q, kv, k_pe, out, lse, cu, cu_k = ctx.saved_tensors
+        given = None
+        if cu is not None:
+            given = {"dq": torch.zeros(q.shape, dtype=q.dtype, device=q.device),
+                     "dkv": torch.zeros(kv.shape, dtype=kv.dtype, device=kv.device),
+                     "dk_pe": torch.zeros(k_pe.shape, dtype=k_pe.dtype, device=k_pe.device)}
+        g = latent_bwd(q, kv, k_pe, ctx.scale, out, lse, d_out.to(torch.bfloat16).contiguous(), ctx.causal, cu, cu_k,
+                       outputs=given)
+        return g["dq"], g["dkv"], g["dk_pe"], None, None, None, None
+
+
+def latent_attention(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float, causal: bool = True,
+                     cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``latent_fwd`` as an autograd operation: returns out and backpropagates into q, kv and k_pe.  In a packed
+    batch, rows behind the last sequence are zeros, as are their gradients."""
+    return LatentFunction.apply(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
