@@ -29,7 +29,8 @@ import torch
 from . import latent, layer
 from ._build import LIB as LIB_PATH
 from ._build import build
-from .latent import latent_attention, latent_bwd, latent_bwd_workspace_size, latent_fwd, latent_workspace_size
+from .latent import (latent_attention, latent_bwd, latent_bwd_workspace_size, latent_decode, latent_decode_workspace_size,
+                     latent_fwd, latent_store, latent_workspace_size, page_assign)
 from .layer import (conv_bwd, conv_bwd_workspace_size, conv_decode, conv_fwd, rms_norm, rmsnorm_bwd,
                     rmsnorm_bwd_workspace_size, rmsnorm_fwd, rmsnorm_quant, short_conv, ssm_bwd,
                     ssm_bwd_workspace_size, ssm_decode, ssm_fwd, ssm_piece_chunks, ssm_scan, ssm_workspace_size)
@@ -41,7 +42,8 @@ __all__ = ["fwd", "fwd_noalloc", "noalloc_max_workspace", "decode", "bwd", "bwd_
            "rmsnorm_fwd", "rmsnorm_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "rms_norm",
            "conv_fwd", "conv_decode", "conv_bwd", "conv_bwd_workspace_size", "short_conv", "ssm_fwd", "ssm_decode",
            "ssm_bwd", "ssm_scan", "ssm_workspace_size", "ssm_bwd_workspace_size", "ssm_piece_chunks",
-           "latent_fwd", "latent_bwd", "latent_attention", "latent_workspace_size", "latent_bwd_workspace_size"]
+           "latent_fwd", "latent_bwd", "latent_attention", "latent_workspace_size", "latent_bwd_workspace_size",
+           "latent_decode", "latent_decode_workspace_size", "latent_store", "page_assign"]
 
 KDA_BF16 = 1
 KDA_FP32 = 2

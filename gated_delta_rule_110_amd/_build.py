@@ -12,7 +12,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_intra.hip", "kda_chain.hip", "kda_fused.hip", "kda_segment.hip", "kda_decode.hip", "kda_bwd.hip",
            "kda_api.hip", "kda_norm.hip", "kda_conv.hip", "kda_ssm.hip", "kda_ssm_bwd.hip", "kda_ssm_decode.hip",
-           "kda_layer_api.hip", "kda_latent_fwd.hip", "kda_latent_bwd.hip", "kda_latent_api.hip"]
+           "kda_layer_api.hip", "kda_latent_fwd.hip", "kda_latent_bwd.hip", "kda_latent_decode.hip",
+           "kda_latent_store.hip", "kda_latent_api.hip"]
 HEADERS = [os.path.join(CSRC, h) for h in ("kda_common.h", "kda_intra_body.h", "kda_layer_args.h", "kda_ssm_common.h", "kda_checks.h",
                                                  "kda_latent_args.h", "kda_latent_common.h")] + [
     os.path.join(INCLUDE, h) for h in ("kda.h", "kda_layer.h", "kda_latent.h")]

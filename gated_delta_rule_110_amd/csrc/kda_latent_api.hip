@@ -219,3 +219,198 @@ extern "C" kda_status_t kda_latent_bwd(const void *q, const void *kv, const void
     if (e == hipSuccess) e = kda_launch_latent_dpe(k, stream);
     return of_hip(e);
 }
+
+// ---- the absorbed form ----
+
+namespace {
+
+struct DecodePlan {
+    int rows32;
+    int64_t row_tiles;
+    size_t off_seg, off_stat, off_part, total;
+};
+
+bool page_ok(int64_t size) { return size >= 1 && size <= 65536 && (size & (size - 1)) == 0; }
+int log2_of(int64_t v) {
+    int s = 0;
+    while ((int64_t(1) << s) < v) ++s;
+    return s;
+}
+
+kda_status_t plan_decode(const kda_latent_decode_desc_t *d, DecodePlan &p) {
+    if (d->N < 0 || d->T < 1 || d->H < 1 || d->pages < 0 || d->max_pages < 0) return KDA_ERR_SHAPE;
+    if (!page_ok(d->page_size)) return KDA_ERR_UNSUPPORTED;
+    constexpr int64_t kMaxRows = int64_t(1) << 24;
+    if (d->H > 65535 || d->T > kMaxRows / d->H || d->N > kMaxRows / (d->T * d->H)) return KDA_ERR_SHAPE;
+    if (d->pages > kMaxSeqs || d->max_pages > kMaxSeqs || d->max_pages > kMaxAttention / d->page_size) return KDA_ERR_SHAPE;
+    const int64_t strides[] = {d->ql_stride_n, d->ql_stride_t, d->ql_stride_h, d->qp_stride_n, d->qp_stride_t, d->qp_stride_h};
+    for (int64_t s : strides)
+        if (!stride_ok(s)) return KDA_ERR_SHAPE;
+    for (int64_t s : strides)
+        if (s % 8 != 0) return KDA_ERR_ALIGN;
+    if (!scale_ok(d->scale)) return KDA_ERR_PARAM;
+    const int64_t rows = d->T * d->H;
+    p.rows32 = rows <= 32 ? 1 : 2;
+    p.row_tiles = (rows + 32 * p.rows32 - 1) / (32 * p.rows32);
+    const size_t slots = 2 * (size_t)kLatentGroups, lanes = (size_t)p.rows32 * 32;
+    p.off_seg = 0;
+    p.off_stat = align_up((size_t)(d->N * p.row_tiles) * 8, 256);
+    p.off_part = p.off_stat + align_up(slots * lanes * 8, 256);
+    p.total = p.off_part + slots * lanes * kLat * 4;
+    return KDA_OK;
+}
+
+// Elements from the first to behind the last of [n, t, h, inner].
+size_t extent4(int64_t n, int64_t sn, int64_t t, int64_t st, int64_t h, int64_t sh, int64_t inner) {
+    return n > 0 ? (size_t)((n - 1) * sn + (t - 1) * st + (h - 1) * sh + inner) * 2 : 0;
+}
+
+}  // namespace
+
+extern "C" size_t kda_latent_decode_workspace_size(const kda_latent_decode_desc_t *desc) {
+    DecodePlan p;
+    return desc && plan_decode(desc, p) == KDA_OK ? p.total : 0;
+}
+
+extern "C" kda_status_t kda_latent_decode(const void *q_latent, const void *q_pe, const void *cache, const int64_t *lengths,
+                                          const int32_t *block_table, void *out, float *lse,
+                                          const kda_latent_decode_desc_t *desc, hipStream_t stream) {
+    if (!desc) return KDA_ERR_NULL;
+    DecodePlan p;
+    const kda_status_t st = plan_decode(desc, p);
+    if (st != KDA_OK) return st;
+    const bool any = desc->N > 0;
+    const bool keys = any && desc->pages > 0 && desc->max_pages > 0;
+    if (any && (!q_latent || !q_pe || !lengths || !out)) return KDA_ERR_NULL;
+    if (keys && (!cache || !block_table)) return KDA_ERR_NULL;
+    if (!aligned(q_latent, 16) || !aligned(q_pe, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(lengths, 8) ||
+        !aligned(block_table, 4) || !aligned(lse, 4))
+        return KDA_ERR_ALIGN;
+    const size_t rows = (size_t)(desc->N * desc->T) * (size_t)desc->H;
+    Memory m;
+    m.read(q_latent, extent4(desc->N, desc->ql_stride_n, desc->T, desc->ql_stride_t, desc->H, desc->ql_stride_h, kLat));
+    m.read(q_pe, extent4(desc->N, desc->qp_stride_n, desc->T, desc->qp_stride_t, desc->H, desc->qp_stride_h, kPe));
+    m.read(cache, (size_t)desc->pages * (size_t)desc->page_size * kRow * 2);
+    m.read(lengths, (size_t)desc->N * 8);
+    m.read(block_table, (size_t)(desc->N * desc->max_pages) * 4);
+    m.write(out, rows * kLat * 2);
+    m.write(lse, rows * 4);
+    m.write(desc->workspace, p.total);
+    if (m.clash()) return KDA_ERR_OVERLAP;
+    if (!any) return KDA_OK;
+    Workspace ws(desc->workspace, desc->workspace_bytes, p.total, stream);
+    if (ws.status() != KDA_OK) return ws.status();
+    LatentDecodeArgs a{};
+    a.ql = static_cast<const uint16_t *>(q_latent);
+    a.qp = static_cast<const uint16_t *>(q_pe);
+    a.cache = static_cast<const uint16_t *>(cache);
+    a.qln = desc->ql_stride_n; a.qlt = desc->ql_stride_t; a.qlh = desc->ql_stride_h;
+    a.qpn = desc->qp_stride_n; a.qpt = desc->qp_stride_t; a.qph = desc->qp_stride_h;
+    a.len = lengths; a.table = block_table;
+    a.N = desc->N; a.T = desc->T; a.H = desc->H; a.pages = desc->pages;
+    a.max_pages = keys ? desc->max_pages : 0;  // no cache: no sequence has keys
+    a.page_shift = log2_of(desc->page_size);
+    a.scale = desc->scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.rows32 = p.rows32; a.row_tiles = p.row_tiles;
+    a.groups = kLatentGroups;
+    a.seg = reinterpret_cast<int32_t *>(ws.at(p.off_seg));
+    a.part_stat = reinterpret_cast<float *>(ws.at(p.off_stat));
+    a.part = reinterpret_cast<float *>(ws.at(p.off_part));
+    hipError_t e = kda_launch_latent_decode(a, stream);
+    if (e == hipSuccess) e = kda_launch_latent_join(a, stream);
+    return of_hip(e);
+}
+
+// ---- the cache ----
+
+extern "C" kda_status_t kda_latent_store(const void *latent, const void *k_pe, const void *weight, const int64_t *slots,
+                                         void *cache, void *normed, const kda_latent_store_desc_t *desc, hipStream_t stream) {
+    if (!desc) return KDA_ERR_NULL;
+    if (desc->tokens < 0 || desc->num_slots < 0 || desc->tokens > kMaxTokens || desc->num_slots > kMaxTokens) return KDA_ERR_SHAPE;
+    if (!stride_ok(desc->latent_stride) || !stride_ok(desc->pe_stride)) return KDA_ERR_SHAPE;
+    if (weight && !dtype_ok(desc->weight_dtype)) return KDA_ERR_DTYPE;
+    // a smaller eps is zero to the hardware's reciprocal root
+    if (weight && (!(desc->eps >= 0x1p-126f) || !isfinite(desc->eps))) return KDA_ERR_PARAM;
+    if (desc->latent_stride % 8 != 0 || desc->pe_stride % 8 != 0) return KDA_ERR_ALIGN;
+    if (desc->tokens > 0 && (!latent || !k_pe || !slots || (desc->num_slots > 0 && !cache))) return KDA_ERR_NULL;
+    if (!aligned(latent, 16) || !aligned(k_pe, 16) || !aligned(cache, 16) || !aligned(normed, 16) || !aligned(slots, 8) ||
+        (weight && !aligned(weight, width(desc->weight_dtype))))
+        return KDA_ERR_ALIGN;
+    Memory m;
+    m.read(latent, extent(1, 0, desc->tokens, desc->latent_stride, kLat, 2));
+    m.read(k_pe, extent(1, 0, desc->tokens, desc->pe_stride, kPe, 2));
+    if (weight) m.read(weight, kLat * width(desc->weight_dtype));
+    m.read(slots, (size_t)desc->tokens * 8);
+    m.write(cache, (size_t)desc->num_slots * kRow * 2);
+    m.write(normed, (size_t)desc->tokens * kLat * 2);
+    if (m.clash()) return KDA_ERR_OVERLAP;
+    if (desc->tokens == 0) return KDA_OK;
+    LatentStoreArgs a{};
+    a.latent = static_cast<const uint16_t *>(latent); a.ls = desc->latent_stride;
+    a.pe = static_cast<const uint16_t *>(k_pe); a.ps = desc->pe_stride;
+    a.w = weight; a.w_f32 = desc->weight_dtype == KDA_FP32;
+    a.slots = slots;
+    a.cache = static_cast<uint16_t *>(cache);
+    a.normed = static_cast<uint16_t *>(normed);
+    a.tokens = desc->tokens; a.num_slots = desc->num_slots;
+    a.eps = desc->eps;
+    return of_hip(kda_launch_latent_store(a, stream));
+}
+
+namespace {
+kda_status_t check_pages(const kda_page_desc_t *d) {
+    if (d->N < 0 || d->max_pages < 0 || d->stack < 0 || d->tokens < 0) return KDA_ERR_SHAPE;
+    if (d->N > int64_t(1) << 20 || d->max_pages > kMaxSeqs || d->stack > kMaxSeqs || d->tokens > kMaxSeqs) return KDA_ERR_SHAPE;
+    if (d->N * d->max_pages > kMaxSeqs) return KDA_ERR_SHAPE;
+    return page_ok(d->page_size) ? KDA_OK : KDA_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+extern "C" size_t kda_page_workspace_size(const kda_page_desc_t *desc) {
+    return desc && check_pages(desc) == KDA_OK ? align_up((size_t)(desc->N + 1) * 8, 256) : 0;
+}
+
+extern "C" kda_status_t kda_page_assign(const int64_t *lengths, const int64_t *new_tokens, const uint8_t *ended,
+                                        int32_t *block_table, int32_t *free_pages, const int64_t *free_count, int64_t *slots,
+                                        int64_t *cu_seqlens, int64_t *lengths_out, int64_t *granted, int64_t *free_count_out,
+                                        const kda_page_desc_t *desc, hipStream_t stream) {
+    if (!desc) return KDA_ERR_NULL;
+    const kda_status_t st = check_pages(desc);
+    if (st != KDA_OK) return st;
+    if (!free_count || !free_count_out || !cu_seqlens) return KDA_ERR_NULL;
+    if (desc->N > 0 && (!lengths || !new_tokens || !lengths_out || !granted || (desc->max_pages > 0 && !block_table)))
+        return KDA_ERR_NULL;
+    if ((desc->stack > 0 && !free_pages) || (desc->tokens > 0 && !slots)) return KDA_ERR_NULL;
+    for (const void *q : {(const void *)lengths, (const void *)new_tokens, (const void *)free_count, (const void *)slots,
+                          (const void *)cu_seqlens, (const void *)lengths_out, (const void *)granted, (const void *)free_count_out})
+        if (!aligned(q, 8)) return KDA_ERR_ALIGN;
+    if (!aligned(block_table, 4) || !aligned(free_pages, 4)) return KDA_ERR_ALIGN;
+    const size_t n = (size_t)desc->N, need = kda_page_workspace_size(desc);
+    Memory m;
+    m.read(lengths, n * 8);
+    m.read(new_tokens, n * 8);
+    m.read(ended, n);
+    m.read(free_count, 8);
+    m.write(block_table, n * (size_t)desc->max_pages * 4);
+    m.write(free_pages, (size_t)desc->stack * 4);
+    m.write(slots, (size_t)desc->tokens * 8);
+    m.write(cu_seqlens, (n + 1) * 8);
+    m.write(lengths_out, n * 8, lengths);
+    m.write(granted, n * 8);
+    m.write(free_count_out, 8, free_count);
+    m.write(desc->workspace, need);
+    if (m.clash()) return KDA_ERR_OVERLAP;
+    Workspace ws(desc->workspace, desc->workspace_bytes, need, stream);
+    if (ws.status() != KDA_OK) return ws.status();
+    PageArgs a{};
+    a.len = lengths; a.add = new_tokens; a.ended = ended;
+    a.table = block_table; a.free_pages = free_pages; a.count = free_count;
+    a.slots = slots; a.cu = cu_seqlens; a.len_out = lengths_out; a.granted = granted; a.count_out = free_count_out;
+    a.N = desc->N; a.max_pages = desc->max_pages; a.stack = desc->stack; a.tokens = desc->tokens;
+    a.shift = log2_of(desc->page_size);
+    a.have = reinterpret_cast<int64_t *>(ws.at(0));
+    a.base = a.have + 1;
+    return of_hip(kda_launch_pages(a, stream));
+}

@@ -31,6 +31,49 @@ struct LatentArgs {
     uint16_t *dq, *dkv, *dpe;
 };
 
+struct LatentDecodeArgs {
+    const uint16_t *ql, *qp, *cache;
+    int64_t qln, qlt, qlh, qpn, qpt, qph;
+    const int64_t *len;
+    const int32_t *table;
+    int64_t N, T, H, pages, max_pages;
+    int page_shift;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    int rows32;                // 32-row tiles of a workgroup's rows, 1 or 2
+    int64_t row_tiles;         // row tiles of a sequence
+    int64_t groups;            // workgroups the steps are shared among
+    // What a workgroup leaves of the first (slot 2 w) and the last (slot 2 w + 1) of its
+    // row tiles where others have a part of it: accumulators, and (maximum, sum) of 64 rows.
+    float *part, *part_stat;
+    int32_t *seg;              // [N row_tiles][2]: first slot and last workgroup; (-1, 0): no part, nothing left to do,
+                               // (-2, 0): no keys
+};
+
+struct LatentStoreArgs {
+    const uint16_t *latent, *pe;
+    int64_t ls, ps;            // elements between rows
+    const void *w;             // [512] or nullptr
+    const int64_t *slots;
+    uint16_t *cache, *normed;
+    int64_t tokens, num_slots;
+    int w_f32;
+    float eps;
+};
+
+struct PageArgs {
+    const int64_t *len, *add;
+    const uint8_t *ended;
+    int32_t *table, *free_pages;
+    const int64_t *count;
+    int64_t *slots, *cu, *len_out, *granted, *count_out;
+    int64_t N, max_pages, stack, tokens;
+    int shift;                 // log2 of the page size
+    int64_t *have;             // workspace: [1] pages on the stack once all are back
+    int64_t *base;             // workspace: [N] pages that the requests before take; before that, that they give
+};
+
 }  // namespace kda
 
 // Queries per workgroup of the forward: the caller's table is made for them.
@@ -44,3 +87,9 @@ constexpr int kLatentBwdBlock = 128;  // queries or keys per workgroup
 hipError_t kda_launch_latent_dq(const kda::LatentArgs &a, hipStream_t s);
 hipError_t kda_launch_latent_dkv(const kda::LatentArgs &a, hipStream_t s);
 hipError_t kda_launch_latent_dpe(const kda::LatentArgs &a, hipStream_t s);
+// The absorbed form: the workgroups' parts, then their joining.
+constexpr int64_t kLatentGroups = 256;
+hipError_t kda_launch_latent_decode(const kda::LatentDecodeArgs &a, hipStream_t s);
+hipError_t kda_launch_latent_join(const kda::LatentDecodeArgs &a, hipStream_t s);
+hipError_t kda_launch_latent_store(const kda::LatentStoreArgs &a, hipStream_t s);
+hipError_t kda_launch_pages(const kda::PageArgs &a, hipStream_t s);

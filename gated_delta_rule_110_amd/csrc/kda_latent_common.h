@@ -118,8 +118,13 @@ __device__ __forceinline__ i4v buffer_of(const void *p, uint32_t bytes) {
     return r;
 }
 // This wave's copies and LDS accesses are done, and every wave's behind the barrier.
+// (The wait is a builtin, which the compiler counts: loads of its own from before are
+// not waited for again later, when the next copies are under way.)
 __device__ __forceinline__ void copies_done() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // `rows` (at most 64) rows of 2 W bytes, `stride` bytes apart, into a tile: for a workgroup of 256 threads, W / 8 chunks

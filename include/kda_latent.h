@@ -140,8 +140,8 @@ kda_status_t kda_latent_store(const void *latent, const void *k_pe, const void *
  *   2. Each request needs the pages its new tokens reach beyond those it has.
  *      Running through the requests, one is granted its tokens while the pages needed
  *      so far (by those refused too) do not pass those on the stack; a request that needs
- *      none always is.  A request that would pass max_pages pages is refused and
- *      counts no pages.  Pages come from the stack's end, requests in order.
+ *      none always is.  A request that would pass max_pages pages or `tokens` rows is
+ *      refused and counts no pages.  Pages come from the stack's end, requests in order.
  *   3. cu_seqlens: running sums of new_tokens, the packed batch of the new tokens;
  *      slots: page * page_size + offset of each of its rows, -1 for rows of refused
  *      requests and behind the last; lengths_out: the new lengths; granted: new_tokens
@@ -152,6 +152,8 @@ typedef struct {
     int64_t N, max_pages, page_size;        /* N up to 2^20; page_size: a power of two up to 2^16; N max_pages below 2^31 */
     int64_t stack;                          /* entries of free_pages */
     int64_t tokens;                         /* entries of slots */
+    void *workspace;                        /* >= kda_page_workspace_size(), 256-byte aligned */
+    size_t workspace_bytes;
 } kda_page_desc_t;
 
 /* lengths, new_tokens, lengths_out, granted: int64 [N]; ended: uint8 [N] or NULL;
@@ -162,6 +164,8 @@ kda_status_t kda_page_assign(const int64_t *lengths, const int64_t *new_tokens, 
                              int32_t *block_table, int32_t *free_pages, const int64_t *free_count, int64_t *slots,
                              int64_t *cu_seqlens, int64_t *lengths_out, int64_t *granted, int64_t *free_count_out,
                              const kda_page_desc_t *desc, hipStream_t stream);
+/* Bytes of workspace kda_page_assign needs (0 if the sizes are invalid). */
+size_t kda_page_workspace_size(const kda_page_desc_t *desc);
 
 #ifdef __cplusplus
 }
