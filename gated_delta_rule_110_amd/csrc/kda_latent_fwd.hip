@@ -429,12 +429,27 @@ __global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs a) {
         const int last = min(lq, (i + 1) * a.size) - 1;
         return (max(0, a.causal ? min(lk, last + 1 + lk - lq) : lk) + kKeys - 1) / kKeys;
     };
-    for (int64_t n = wave; n < a.seqs; n += 16) {
-        int lq, lk;
-        lengths(n, lq, lk);
-        const int blocks = ((a.by_keys ? lk : lq) + a.size - 1) / a.size;
-        for (int i = lane; i < blocks; i += 64) atomicAdd(&count[work(lq, lk, i) >> shift], 1);
-    }
+    // visit(sequence, lq, lk, block) for every block.  A wave takes 64 sequences at a time:
+    // lanes run through the blocks of short ones, the wave through those of long ones.
+    constexpr int kShort = 8;
+    const auto each = [&](auto visit) {
+        for (int64_t first = wave * 64; first < a.seqs; first += 1024) {
+            const int64_t n = first + lane;
+            int lq = 0, lk = 0;
+            if (n < a.seqs) lengths(n, lq, lk);
+            const int blocks = ((a.by_keys ? lk : lq) + a.size - 1) / a.size;
+            if (blocks <= kShort)
+                for (int i = 0; i < blocks; ++i) visit(n, lq, lk, i);
+            uint64_t who = __builtin_amdgcn_ballot_w64(blocks > kShort);
+            while (who) {
+                const int m = __builtin_ctzll(who);
+                who &= who - 1;
+                const int q = __shfl(lq, m), k = __shfl(lk, m), all = __shfl(blocks, m);
+                for (int i = lane; i < all; i += 64) visit(first + m, q, k, i);
+            }
+        }
+    };
+    each([&](int64_t, int lq, int lk, int i) { atomicAdd(&count[work(lq, lk, i) >> shift], 1); });
     __syncthreads();
     // each bucket's first entry: the blocks of all larger ones
     const int mine = count[kBuckets - 1 - tid];
@@ -451,17 +466,12 @@ __global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs a) {
     count[kBuckets - 1 - tid] = before + upto - mine;
     if (tid == 1023) a.table[0] = (int)min((int64_t)(before + upto), a.cap);
     __syncthreads();
-    for (int64_t n = wave; n < a.seqs; n += 16) {
-        int lq, lk;
-        lengths(n, lq, lk);
-        const int blocks = ((a.by_keys ? lk : lq) + a.size - 1) / a.size;
-        for (int i = lane; i < blocks; i += 64) {
-            const int at = atomicAdd(&count[work(lq, lk, i) >> shift], 1);
-            if (at >= a.cap) continue;  // sequences that overlap, which valid offsets do not describe
-            a.table[2 + 2 * at] = (int)n;
-            a.table[3 + 2 * at] = i;
-        }
-    }
+    each([&](int64_t n, int lq, int lk, int i) {
+        const int at = atomicAdd(&count[work(lq, lk, i) >> shift], 1);
+        if (at >= a.cap) return;  // sequences that overlap, which valid offsets do not describe
+        a.table[2 + 2 * at] = (int)n;
+        a.table[3 + 2 * at] = i;
+    });
 }
 
 }  // namespace

@@ -51,7 +51,7 @@ def _declare(lib) -> None:
 
 # ---- the expanded form -----------------------------------------------------------
 
-def _latent_args(q, kv, k_pe, scale, causal, cu, cu_k):
+def _latent_args(q, kv, k_pe, scale, causal, cu, cu_k, launch_piece=0):
     """(descriptor, device) of a call's inputs."""
     dev = _device_of(q)
     for t, name in ((q, "q"), (kv, "kv"), (k_pe, "k_pe")):
@@ -72,7 +72,7 @@ def _latent_args(q, kv, k_pe, scale, causal, cu, cu_k):
     elif cu is not None and T != Tk:
         raise ValueError("packed queries and keys of different number need cu_seqlens_k")
     return KdaLatentDesc(B, T, Tk, H, n, *_tokens(q, "q"), *_tokens(kv, "kv"), *_tokens(k_pe, "k_pe"), 0, 0, 0, 0, scale,
-                         int(bool(causal))), dev
+                         int(bool(causal)), None, 0, launch_piece), dev
 
 
 def latent_workspace_size(B: int, T: int, Tk: int, H: int, num_seqs: Optional[int] = None) -> int:
@@ -87,7 +87,7 @@ def _sizes(B, T, Tk, H, n):
 def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float, causal: bool = True,
                cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-               workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+               workspace: Optional[torch.Tensor] = None, launch_piece: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of every head with the keys ``(kv[..., :128], k_pe)``, of which the second part is shared by all
     heads, and the values ``kv[..., 128:]``.  Returns ``(out, lse)``: bf16 [B, T, H, 128] and the scores' log-sum-exp,
     fp32 [B, T, H].
@@ -95,8 +95,9 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: flo
     q: bf16 [B, T, H, 192]; kv: bf16 [B, Tk, H, 256]; k_pe: bf16 [B, Tk, 64]; scale: of the scores, above zero;
     causal: the last query of a sequence sees all its keys, each one before it one less; cu_seqlens, cu_seqlens_k:
     int64 offsets of a packed batch's queries and keys (B = 1; the keys' are the queries' if None).  A query that
-    sees no key has out 0 and lse -inf."""
-    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
+    sees no key has out 0 and lse -inf.  launch_piece: kda_latent_desc_t::launch_piece (0: the library's launch
+    size)."""
+    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k, launch_piece)
     out = _output(out, "out", (d.B, d.T, d.H, VALUE), torch.bfloat16, dev)
     lse = _output(lse, "lse", (d.B, d.T, d.H), torch.float32, dev)
     ws = None
@@ -115,11 +116,11 @@ def latent_bwd_workspace_size(B: int, T: int, Tk: int, H: int, num_seqs: Optiona
 def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: float, out: torch.Tensor, lse: torch.Tensor,
                d_out: torch.Tensor, causal: bool = True, cu_seqlens: Optional[torch.Tensor] = None,
                cu_seqlens_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-               outputs: Optional[dict] = None) -> dict:
+               outputs: Optional[dict] = None, launch_piece: int = 0) -> dict:
     """Gradient of ``latent_fwd`` for the loss's gradient d_out (bf16 [B, T, H, 128]), from its inputs and what it
     returned (out, lse).  Returns a dict of bf16 tensors: dq [B, T, H, 192], dkv [B, Tk, H, 256] and dk_pe [B, Tk, 64],
     summed over the heads.  outputs: None, or a dict of tensors of those names to write into."""
-    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k)
+    d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k, launch_piece)
     for t, name in ((out, "out"), (d_out, "d_out")):
         _bf16(t, name, dev)
         if t.shape != (d.B, d.T, d.H, VALUE):
