@@ -252,6 +252,8 @@ kda_status_t plan_decode(const kda_latent_decode_desc_t *d, DecodePlan &p) {
     const int64_t rows = d->T * d->H;
     p.rows32 = rows <= 32 ? 1 : 2;
     p.row_tiles = (rows + 32 * p.rows32 - 1) / (32 * p.rows32);
+    // a workgroup counts its steps of 32 cached rows in 32 bits
+    if (d->N > 0 && d->max_pages * d->page_size > (int64_t(1) << 43) / (d->N * p.row_tiles)) return KDA_ERR_SHAPE;
     const size_t slots = 2 * (size_t)kLatentGroups, lanes = (size_t)p.rows32 * 32;
     p.off_seg = 0;
     p.off_stat = align_up((size_t)(d->N * p.row_tiles) * 8, 256);

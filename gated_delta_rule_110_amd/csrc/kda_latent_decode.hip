@@ -2,23 +2,22 @@
 // (kda_latent_decode in include/kda_latent.h).
 //
 // All heads of a token read the same cached rows, so a workgroup has 32 or 64 rows of
-// (token, head) and 64 cached rows at a time in LDS, which serve as keys (576 values)
+// (token, head) and 32 cached rows at a time in LDS, which serve as keys (576 values)
 // and as values (their first 512): 1152 bytes for 2 x 64 x 1088 operations a row.  Up to
 // 64 rows the cache's bytes are the bound, beyond that they come from L2.
 //
-// Steps (64 cached rows of one row tile) of all sequences are lined up and shared out
+// Steps (32 cached rows of one row tile) of all sequences are lined up and shared out
 // evenly among 256 workgroups, one a CU, whatever the lengths: each computes the line
 // from the lengths, so that no plan has to be made on the host or launched ahead.  A
 // row tile that ends up in several workgroups is joined by a second kernel from their
 // fp32 accumulators, maxima and sums.
 //
-// Of a step, each of eight waves takes the scores of 16 rows (S^T = K Q^T, queries in
-// registers) and a quarter or half of the keys, leaves their probabilities in LDS, and
-// then takes 64 of the 512 values of all rows (O^T += V^T P^T).  The copies of the next 64
-// rows run meanwhile.  (Four waves of larger tiles, or 32 rows a wave among the scores, need
-// more than the 256 registers that matrix and vector instructions share: what moves
-// between the halves of the file, or to memory and back, then costs more than the LDS reads
-// it saves: 64 rows 12 and 5 us a step.)
+// A workgroup's steps are one stream, across sequences: four waves take the scores of
+// step i (S^T = K Q^T, queries in registers) and leave the probabilities in LDS, four
+// take the outputs of step i - 1 (O^T += V^T P^T, 128 of the 512 values each), and the copies
+// of the steps i + 1 and i + 2 run meanwhile, with one barrier a step.  (Each SIMD has a
+// wave of either kind; waves that do both need more registers than they have, or twice
+// the LDS reads.)  The table's entries are copied into LDS two steps ahead of the rows.
 //
 // Precision: as in the expanded form, probabilities are rounded to bf16, all else is fp32.
 #include "kda_latent_common.h"
@@ -27,16 +26,20 @@ namespace kda {
 
 namespace {
 
-constexpr int kSub = kKeys * 128;              // bytes of 64 values of a tile's rows
+constexpr int kStep = 32;                      // cached rows a step
+constexpr int kSub = kStep * 128;              // bytes of 64 values of a step's rows
 constexpr int kSubs = kRow / 64;
-constexpr int kWaves = kLat / 64;              // each has 64 values among the outputs
+constexpr int kBuffers = 4, kEntries = 8;      // steps in LDS; steps whose table entries are
+constexpr int kOutWaves = 4;
+constexpr int kWaveDims = kLat / kOutWaves;    // values of an output wave
 
 struct DecodeSmem {
-    uint16_t row[2][kSubs][kKeys * 64];
-    uint16_t p[64 * kKeys];                    // [row][key], 16-byte chunk c of row r at c ^ (r % 8)
-    float top[4][64], sum[4][64];              // [group of keys][row]
-    int rise[2], odd;
-    int64_t wave_sum[kWaves];
+    uint16_t row[kBuffers][kSubs][kStep * 64];
+    uint16_t p[2][64 * kStep];                 // [row][key], 16-byte chunk c of row r at c ^ (r / 2 % 4)
+    int32_t entry[kEntries][64];               // page of every row of a step (32 of them)
+    float top[2][64], sum[2][2][64];           // [half of the keys][row]; of two segments
+    int rise[2];
+    int64_t wave_sum[8];
     int64_t begin_n, begin_rest;
 };
 
@@ -46,17 +49,14 @@ __device__ __forceinline__ void copy16_at(const uint16_t *p, uint32_t lds) {
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%c2" :: "v"(p), "{m0}"(lds - OFF), "i"(OFF) : "memory");
 }
 
-// This thread's row (tid / 8) of a tile, chunk tid % 8 of every 128 bytes.
-__device__ __forceinline__ void copy_row(const uint16_t *p, uint32_t lds) {
-    copy16_at<0>(p, lds);
-    copy16_at<128>(p, lds + kSub);
-    copy16_at<256>(p, lds + 2 * kSub);
-    copy16_at<384>(p, lds + 3 * kSub);
-    copy16_at<512>(p, lds + 4 * kSub);
-    copy16_at<640>(p, lds + 5 * kSub);
-    copy16_at<768>(p, lds + 6 * kSub);
-    copy16_at<896>(p, lds + 7 * kSub);
-    copy16_at<1024>(p, lds + 8 * kSub);
+// Waits until at most `left` of the wave's memory operations (the youngest) and none of its LDS
+// accesses are under way, then for the other waves.
+template <int LEFT>
+__device__ __forceinline__ void arrive() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | LEFT);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // The values of lanes n, n + 16, n + 32 and n + 48, combined in all of them.
@@ -69,25 +69,94 @@ __device__ __forceinline__ float quad_sum(float x) {
     return pair_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// R: 32-row tiles of the workgroup's rows, and 16-key tiles of a wave's.
+// Scales from one maximum in use to another.
+__device__ __forceinline__ float rescale(float from, float to) { return to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(from - to); }
+
+// A position in the line of steps.  Lengths are read by scalar loads, which are not
+// counted with the copies.
+typedef const __attribute__((address_space(4))) int64_t *const_i64;
+struct Cursor {
+    int n, rt, t;              // sequence, row tile, step within it
+    int len, steps;            // of the sequence
+};
+__device__ __forceinline__ int length_of(const LatentDecodeArgs &a, int64_t n) {
+    return (int)clamp64(reinterpret_cast<const_i64>(reinterpret_cast<uintptr_t>(a.len))[n], 0, a.max_pages << a.page_shift);
+}
+__device__ __forceinline__ void advance(const LatentDecodeArgs &a, Cursor &x) {
+    if (++x.t < x.steps) return;
+    x.t = 0;
+    if (++x.rt < a.row_tiles) return;
+    x.rt = 0;
+    do {
+        if (++x.n >= a.N) return;  // behind the last step
+        x.len = length_of(a, x.n);
+        x.steps = (x.len + kStep - 1) / kStep;
+    } while (x.steps == 0);
+}
+
+// The copies of a step: this thread's row among the step's, from its table entry.  The
+// score waves take the even 64-value parts, the output waves the odd ones.
+template <bool EVEN>
+__device__ __forceinline__ void copy_step(const LatentDecodeArgs &a, const Cursor &x, int32_t page, int row, int chunk, uint32_t lds) {
+    const int pos = min(x.t * kStep + row, x.len - 1);  // rows behind the length: the last one again
+    const int64_t slot = (clamp64(page, 0, a.pages - 1) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    const uint16_t *p = a.cache + slot * kRow + ((chunk ^ swap(row)) << 3);
+    if (EVEN) {
+        copy16_at<0>(p, lds);
+        copy16_at<256>(p, lds + 2 * kSub);
+        copy16_at<512>(p, lds + 4 * kSub);
+        copy16_at<768>(p, lds + 6 * kSub);
+        copy16_at<1024>(p, lds + 8 * kSub);
+    } else {
+        copy16_at<128>(p, lds + kSub);
+        copy16_at<384>(p, lds + 3 * kSub);
+        copy16_at<640>(p, lds + 5 * kSub);
+        copy16_at<896>(p, lds + 7 * kSub);
+    }
+}
+constexpr int kEvenCopies = 5, kOddCopies = 4;
+
+// What both kinds of waves share: the copies ahead of their work.
+template <bool EVEN>
+struct Feed {
+    Cursor copy, look;         // two and four steps ahead
+    int row, chunk;            // this thread's
+    uint32_t lds;              // its wave's place in a 64-value part of buffer 0
+
+    // Step i's share: copies of step i + 2, entries of step i + 4.
+    __device__ __forceinline__ void ahead(const LatentDecodeArgs &a, DecodeSmem &sm, int i, int count, int tid) {
+        if (i + 4 < count) {
+            if (tid < 64) {
+                const int pos = min(look.t * kStep + (tid & (kStep - 1)), look.len - 1);
+                const int32_t *p = a.table + look.n * a.max_pages + (pos >> a.page_shift);
+                asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(p), "{m0}"(lds_addr(sm.entry[(i + 4) % kEntries])) : "memory");
+            }
+            advance(a, look);
+        }
+        if (i + 2 < count) {
+            copy_step<EVEN>(a, copy, sm.entry[(i + 2) % kEntries][row], row, chunk, lds + (i + 2) % kBuffers * (uint32_t)sizeof(sm.row[0]));
+            advance(a, copy);
+        }
+    }
+};
+
+// R: 32-row tiles of the workgroup's rows, and 16-row tiles of a score wave's.
 template <int R>
 __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs a) {
     __shared__ __attribute__((aligned(1024))) DecodeSmem sm;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5, n16 = lane & 15, g16 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t w = blockIdx.x;
-    constexpr int kRowGroups = 2 * R, kKeyGroups = kWaves / kRowGroups;
-    const int kg = wave / kRowGroups, k0 = kg * 16 * R, my_row = wave % kRowGroups * 16 + n16;  // the lane's among the scores
-    const int64_t top_len = a.max_pages << a.page_shift;
-    const auto length = [&](int64_t n) { return clamp64(a.len[n], 0, top_len); };
-    const auto tiles_of = [&](int64_t n) { return (length(n) + kKeys - 1) / kKeys; };
 
     // The line of steps: sequence after sequence, row tile after row tile.  Thread t sums
     // up an even share of the sequences.
     const int64_t share = (a.N + 511) / 512, n0 = min(a.N, tid * share), n1 = min(a.N, n0 + share);
+    const auto steps_of = [&](int64_t n) {
+        return (clamp64(a.len[n], 0, a.max_pages << a.page_shift) + kStep - 1) / kStep * a.row_tiles;
+    };
     int64_t sum = 0;
     for (int64_t n = n0; n < n1; ++n) {
-        const int64_t t = tiles_of(n) * a.row_tiles;
+        const int64_t t = steps_of(n);
         sum += t;
         if (t == 0 && w == 0)
             for (int64_t r = 0; r < a.row_tiles; ++r) a.seg[2 * (n * a.row_tiles + r)] = -2;
@@ -103,17 +172,18 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < 8; ++i) {
         if (i < wave) upto += sm.wave_sum[i];
         total += sm.wave_sum[i];
     }
     const int64_t per = (total + a.groups - 1) / a.groups;
-    const int64_t first = w * per, end = min(total, first + per);
-    if (first >= end) return;
+    const int64_t first = w * per;
+    const int64_t mine = min(total, first + per) - first;
+    if (mine <= 0) return;
     if (upto - sum <= first && first < upto) {
         int64_t at = upto - sum, n = n0;
         for (;; ++n) {
-            const int64_t t = tiles_of(n) * a.row_tiles;
+            const int64_t t = steps_of(n);
             if (first < at + t) break;
             at += t;
         }
@@ -121,299 +191,329 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         sm.begin_rest = first - at;
     }
     __syncthreads();
+    const int count = __builtin_amdgcn_readfirstlane((int)mine);
+    Cursor at;
+    at.n = __builtin_amdgcn_readfirstlane((int)sm.begin_n);
+    at.len = length_of(a, at.n);
+    at.steps = (at.len + kStep - 1) / kStep;
+    {
+        const int64_t rest = sm.begin_rest;
+        const int rt = rest >> 32 ? (int)(rest / at.steps) : (int)((uint32_t)rest / (uint32_t)at.steps);  // below 2^24 / 32
+        at.rt = __builtin_amdgcn_readfirstlane(rt);
+        at.t = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)rt * at.steps));
+    }
 
+    const uint32_t rows = (uint32_t)(a.T * a.H), H = (uint32_t)a.H;
     const float c = a.scale * kLog2e;
     const uint32_t lds = lds_addr(sm.row), lds_p = lds_addr(sm.p);
-    // operands: a key's values 8 g16 .. of every 32; the values' columns of keys 8 g .. of every
-    // 16 (two reads of 4 keys each); a row's probabilities of those keys
-    const uint32_t at_k = lds + (k0 + n16) * 128 + ((g16 ^ swap(n16)) << 4);
-    const int vr = 8 * g + (n16 >> 2);
-    const uint32_t at_v = lds + wave * kSub + vr * 128 + (((2 * (g16 & 1) + ((n16 & 3) >> 1)) ^ swap(vr)) << 4) + (n16 & 1) * 8;
-    const uint32_t at_p = lds_p + (lane & 31) * 128 + ((g ^ (lane & 7)) << 4);
-    const uint32_t put_p = lds_p + my_row * 128 + (((2 * R * kg + (g16 >> 1)) ^ (n16 & 7)) << 4) + (g16 & 1) * 8;
-    const uint32_t rows = (uint32_t)(a.T * a.H), H = (uint32_t)a.H;
-    int64_t n = __builtin_amdgcn_readfirstlane((int)sm.begin_n), rest = sm.begin_rest, step = first;
-    rest = ((int64_t)__builtin_amdgcn_readfirstlane((int)(rest >> 32)) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane((int)rest);
-    bool opening = true;
-    while (step < end) {
-        // A segment: tiles t0 .. t1 - 1 of row tile rt of sequence n.
-        const int len = (int)length(n), tiles = (len + kKeys - 1) / kKeys;
-        if (tiles * a.row_tiles <= rest) {
-            ++n;
-            rest = 0;
-            continue;
-        }
-        const int rt = (uint64_t)rest >> 32 ? (int)(rest / tiles) : (int)((uint32_t)rest / (uint32_t)tiles);  // below 2^24 / 32
-        const int t0 = (int)(rest - (int64_t)rt * tiles), t1 = (int)min((int64_t)tiles, t0 + (end - step));
-        const bool alone = t0 == 0 && t1 == tiles;
+    // Keys that a row of a row tile sees; rows behind the last stand for it and are not stored.
+    const auto seen_by = [&](const Cursor &x, int row) {
+        const uint32_t i = min((uint32_t)(x.rt * R * 32 + row), rows - 1);
+        return min(max(x.len - (int)a.T + 1 + (int)(i / H), 0), x.len);
+    };
 
-        // Keys that a row sees; rows behind the last stand for it and are not stored.
-        const auto seen_by = [&](int row) {
-            const uint32_t i = min((uint32_t)(rt * R * 32 + row), rows - 1);
-            return min(max(len - (int)a.T + 1 + (int)(i / H), 0), len);
-        };
-        const int all_see = seen_by(0);
-        f16v o[R][2];
-        // Maxima in use: of the row among the scores, and of those among the outputs (lane % 32 of
-        // each 32-row tile).  l: the sum over this lane's keys.
-        float ms, mo[R], l;
-
-        // Where this thread's row of tile t lies; rows behind the length take the last one's place.
-        int32_t page;
-        const auto look_up = [&](int t) {
-            const int pos = min(t * kKeys + (tid >> 3), len - 1);
-            page = a.table[n * a.max_pages + (pos >> a.page_shift)];
-        };
-        const auto copy = [&](int t) {
-            const int pos = min(t * kKeys + (tid >> 3), len - 1);
-            const int64_t slot = (clamp64(page, 0, a.pages - 1) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-            copy_row(a.cache + slot * kRow + (((tid & 7) ^ swap(tid >> 3)) << 3),
-                     lds + (uint32_t)(t & 1) * (uint32_t)sizeof(sm.row[0]) + wave * 1024);
-        };
-
-        look_up(t0);
-        copies_done();  // the last segment's reads, too
-        copy(t0);
-        const int seen = seen_by(my_row);
-        s8 q[kRow / 32];
-        {
-            const uint32_t i = min((uint32_t)(rt * R * 32 + my_row), rows - 1), tok = i / H, head = i - tok * H;
-            const uint16_t *ql = a.ql + n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + 8 * g16;
-            const uint16_t *qp = a.qp + n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + 8 * g16;
+    // The first two steps' copies, by entries that the thread reads itself; the next two's entries.
+    const int my_row = 8 * (wave & 3) + (lane >> 3);
+    Cursor copy = at, look;
+    {
+        int32_t page[2];
+        Cursor x = at;
 #pragma unroll
-            for (int ks = 0; ks < kRow / 32; ++ks)
-                q[ks] = ks < kLat / 32 ? *reinterpret_cast<const s8 *>(ql + 32 * ks) : *reinterpret_cast<const s8 *>(qp + 32 * ks - kLat);
+        for (int i = 0; i < 2; ++i)
+            if (i < count) {
+                page[i] = a.table[x.n * a.max_pages + (min(x.t * kStep + my_row, x.len - 1) >> a.page_shift)];
+                advance(a, x);
+            }
+        look = x;
+        const uint32_t place = lds + (wave & 3) * 1024;
+        for (int i = 2; i < 4 && i < count; ++i) {
+            if (tid < 64) {
+                const int pos = min(look.t * kStep + (tid & (kStep - 1)), look.len - 1);
+                sm.entry[i][tid] = a.table[look.n * a.max_pages + (pos >> a.page_shift)];
+            }
+            advance(a, look);
         }
-
-        // apart: hidden keys' NaNs and infinities are kept from the rows that do not see them
-        // (as in the expanded form: the segment runs again with them added apart).
-        for (int apart = 0; apart < 2; ++apart) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                mo[r] = -INFINITY;
-                o[r][0] = o[r][1] = zero16();
+        for (int i = 0; i < 2; ++i)
+            if (i < count) {
+                if (wave < 4) copy_step<true>(a, copy, page[i], my_row, lane & 7, place + i * (uint32_t)sizeof(sm.row[0]));
+                else copy_step<false>(a, copy, page[i], my_row, lane & 7, place + i * (uint32_t)sizeof(sm.row[0]));
+                advance(a, copy);
             }
-            ms = -INFINITY;
-            l = 0.0f;
-            if (apart) {
-                look_up(t0);
-                copies_done();
-                copy(t0);
-            }
-            look_up(min(t0 + 1, tiles - 1));
+    }
+
+    // Probabilities use the maximum that is in use, which may stay 2^40 behind the true one
+    // (bf16 has fp32's exponents, so that nothing is lost): only a larger step, as at a segment's
+    // start, makes all waves agree on new maxima before they go on.
+    constexpr float kSlack = 40.0f;
+
+    if (wave < 4) {
+        // ---- scores: 16 keys and 16 R rows a wave --------------------------------------
+        Feed<true> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
+        const int kg = wave >> 1, r0 = (wave & 1) * 16 * R;
+        const uint32_t at_k = lds + (kg * 16 + n16) * 128 + ((g16 ^ swap(n16)) << 4);
+        s8 q[R][kRow / 32];
+        int seen[R], all_see = 0, segment = 0;
+        float m[R], l[R];
+        bool fresh = true;
+        if (count > 1) arrive<kEvenCopies>();
+        else arrive<0>();
 #pragma unroll 1
-            for (int t = t0; t < t1; ++t) {
-                copies_done();
-                if (t + 1 < t1) {
-                    copy(t + 1);
-                    look_up(min(t + 2, tiles - 1));
-                }
-                const uint32_t buf = (uint32_t)(t & 1) * (uint32_t)sizeof(sm.row[0]);
-                // scores
-                f4 s[R];
-                {
-                    // One tile of keys has two sums, two have one each: every second product waits for none.
-                    constexpr int kAhead = 6;
-                    const uint32_t k = at_k + buf;
-                    const auto operand = [&](int i) { return read8((k ^ (((i / R) & 1) << 6)) + (i / R >> 1) * kSub + i % R * 16 * 128); };
-                    s8 ring[kAhead];
-                    f4 sums[2];
+        for (int i = 0; i <= count; ++i) {
+            feed.ahead(a, sm, i, count, tid);
+            float part[R];
+            f4 s[R];
+            const bool last = i == count - 1 || at.t == at.steps - 1;
+            const auto probabilities = [&]() {
+                const uint32_t put = lds_p + (i & 1) * (uint32_t)sizeof(sm.p[0]);
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) ring[i] = operand(i);
-                    sums[0] = sums[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int r = 0; r < R; ++r) {
+                    const int row = r0 + 16 * r + n16;
+                    const float x = m[r] == -INFINITY ? 0.0f : m[r];
+                    float e[4];
 #pragma unroll
-                    for (int i = 0; i < R * kRow / 32; ++i) {
-                        sums[i & 1] = mfma16x16x32_bf16(ring[i % kAhead], q[i / R], sums[i & 1]);
-                        if (i + kAhead < R * kRow / 32) ring[i % kAhead] = operand(i + kAhead);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    if (R == 1) s[0] = sums[0] + sums[1];
-                    else {
-                        s[0] = sums[0];
-                        s[R - 1] = sums[1];
+                    for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f(fmaf(s[r][k], c, -x));
+                    part[r] = (e[0] + e[1]) + (e[2] + e[3]);
+                    *reinterpret_cast<__attribute__((address_space(3))) u2v *>(
+                        put + row * 64 + (((2 * kg + (g16 >> 1)) ^ (row >> 1 & 3)) << 4) + (g16 & 1) * 8) = u2v{pack2(e[0], e[1]), pack2(e[2], e[3])};
+                    if (last) {
+                        const float z = quad_sum(l[r] + part[r]);
+                        if (g16 == 0) sm.sum[segment & 1][kg][row] = z;
                     }
                 }
-                if ((t + 1) * kKeys > all_see) {
+            };
+            if (i < count) {
+                if (fresh) {
+                    all_see = seen_by(at, 0);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint32_t x = min((uint32_t)(at.rt * R * 32 + r0 + 16 * r + n16), rows - 1), tok = x / H, head = x - tok * H;
+                        seen[r] = seen_by(at, r0 + 16 * r + n16);
+                        m[r] = -INFINITY;
+                        l[r] = 0.0f;
+                        const uint16_t *ql = a.ql + at.n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + 8 * g16;
+                        const uint16_t *qp = a.qp + at.n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + 8 * g16;
+#pragma unroll
+                        for (int ks = 0; ks < kRow / 32; ++ks)
+                            q[r][ks] = ks < kLat / 32 ? *reinterpret_cast<const s8 *>(ql + 32 * ks)
+                                                      : *reinterpret_cast<const s8 *>(qp + 32 * ks - kLat);
+                    }
+                    // Waited for here, once a segment: at their uses, every step would wait, and with
+                    // them for the copies.
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+                    asm volatile("" ::: "memory");
+                }
+                // One 16-row tile has two sums, two have one each: every second product waits for none.
+                constexpr int kAhead = 5;
+                const uint32_t k = at_k + i % kBuffers * (uint32_t)sizeof(sm.row[0]);
+                const auto operand = [&](int x) { return read8((k ^ ((x & 1) << 6)) + (x >> 1) * kSub); };
+                s8 ring[kAhead];
+                f4 sums[2];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) ring[x] = operand(x);
+                sums[0] = sums[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int x = 0; x < kRow / 32; ++x) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        sums[R == 1 ? x & 1 : r] = mfma16x16x32_bf16(ring[x % kAhead], q[r][x], sums[R == 1 ? x & 1 : r]);
+                    if (x + kAhead < kRow / 32) ring[x % kAhead] = operand(x + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                s[0] = R == 1 ? sums[0] + sums[1] : sums[0];
+                if (R == 2) s[R - 1] = sums[1];
+                if ((at.t + 1) * kStep > all_see) {
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[r][i] = t * kKeys + k0 + 16 * r + 4 * g16 + i < seen ? s[r][i] : -INFINITY;
+                        for (int x = 0; x < 4; ++x) s[r][x] = at.t * kStep + kg * 16 + 4 * g16 + x < seen[r] ? s[r][x] : -INFINITY;
                 }
-                // Probabilities by the maximum in use, which may stay 2^40 behind the true one (bf16
-                // has fp32's exponents, so that nothing is lost): only a larger step, as in a segment's first
-                // tile, makes the waves agree on new maxima first.
-                constexpr float kSlack = 40.0f;
-                float top = -INFINITY;
+                bool need = false;
 #pragma unroll
-                for (int r = 0; r < R; ++r) top = fmaxf(top, fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3])));
-                top = quad_max(top) * c;
-                if (g16 == 0) sm.top[kg][my_row] = top;
-                if (__builtin_amdgcn_ballot_w64(top > ms + kSlack) != 0 && lane == 0) sm.rise[t & 1] = 1;
-                float part;
-                const auto probabilities = [&]() {
-                    const float x = ms == -INFINITY ? 0.0f : ms;
-                    part = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        float e[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(s[r][i], c, -x));
-                        part += (e[0] + e[1]) + (e[2] + e[3]);
-                        *reinterpret_cast<__attribute__((address_space(3))) u2v *>(put_p ^ (r << 5)) = u2v{pack2(e[0], e[1]), pack2(e[2], e[3])};
-                    }
-                };
+                for (int r = 0; r < R; ++r) {
+                    const float top = quad_max(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]))) * c;
+                    if (g16 == 0) sm.top[kg][r0 + 16 * r + n16] = top;
+                    need |= top > m[r] + kSlack;
+                }
+                if (__builtin_amdgcn_ballot_w64(need) != 0 && lane == 0) sm.rise[i & 1] = 1;
                 probabilities();
-                lds_barrier();
-                if (sm.rise[t & 1]) {
-                    const auto risen = [&](float m, int row) {
-#pragma unroll
-                        for (int k = 0; k < kKeyGroups; ++k) m = fmaxf(m, sm.top[k][row]);
-                        return m;
-                    };
-                    const auto factor = [](float from, float to) { return to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(from - to); };
-                    const float xs = risen(ms, my_row);
-                    l *= factor(ms, xs);
-                    ms = xs;
+            }
+            if (i + 2 < count) arrive<kEvenCopies>();
+            else arrive<0>();
+            if (i < count) {
+                if (sm.rise[i & 1]) {
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        const float xo = risen(mo[r], 32 * r + (lane & 31)), f = factor(mo[r], xo);
-                        mo[r] = xo;
-#pragma unroll
-                        for (int d = 0; d < 2; ++d)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[r][d][i] *= f;
+                        const int row = r0 + 16 * r + n16;
+                        const float x = fmaxf(m[r], fmaxf(sm.top[0][row], sm.top[1][row]));
+                        l[r] *= rescale(m[r], x);
+                        m[r] = x;
                     }
                     probabilities();
                     lds_barrier();
-                    if (tid == 0) sm.rise[t & 1] = 0;  // set again two tiles on
+                    if (tid == 0) sm.rise[i & 1] = 0;  // set again two steps on
                 }
-                l += part;
-                if (apart && (t + 1) * kKeys > all_see) {
-                    int sees[R];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) sees[r] = seen_by(32 * r + (lane & 31));
+                for (int r = 0; r < R; ++r) l[r] += part[r];
+                fresh = at.t == at.steps - 1;
+                segment += fresh;
+                advance(a, at);
+            }
+        }
+    } else {
+        // ---- outputs: 128 values of all rows a wave -------------------------------------
+        Feed<false> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
+        const int ow = wave - 4;
+        const int vr = 8 * g + (n16 >> 2);  // keys 8 g .. of every 16, by two reads of 4 keys each
+        const uint32_t at_v = lds + ow * (kWaveDims / 64) * kSub + vr * 128 + (((2 * (g16 & 1) + ((n16 & 3) >> 1)) ^ swap(vr)) << 4) + (n16 & 1) * 8;
+        const int pr = lane & 31;
+        const uint32_t at_p = lds_p + pr * 64 + ((g ^ (pr >> 1 & 3)) << 4);
+        f16v o[R][kWaveDims / 32];
+        float m[R];
+        int segment = 0, begin = 0;  // begin: the segment's first step
+        const auto reset = [&]() {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                m[r] = -INFINITY;
+#pragma unroll
+                for (int d = 0; d < kWaveDims / 32; ++d) o[r][d] = zero16();
+            }
+        };
+        reset();
+        if (count > 1) arrive<kOddCopies>();
+        else arrive<0>();
 #pragma unroll 1
-                    for (int i = 0; i < kKeys; ++i) {
+        for (int i = 0; i <= count; ++i) {
+            feed.ahead(a, sm, i, count, tid);
+            if (i > 0) {  // step i - 1, at `at`
+                const int x = i - 1, buf = x % kBuffers;
+                if ((at.t + 1) * kStep > seen_by(at, 0)) {
+                    // Hidden keys: their values meet zero probabilities.  Where any of the wave's is NaN or
+                    // infinite, those are added apart, to the rows that see their keys, and then taken as zeros.
+                    u4v *v = reinterpret_cast<u4v *>(sm.row[buf][ow * (kWaveDims / 64)]);
+                    bool odd = false;
+                    for (int y = lane; y < kWaveDims / 64 * kSub / 16; y += 64) {
+                        const u4v z = v[y];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint16_t *x = sm.row[t & 1][wave] + i * 64 + ((e ^ swap(i)) << 3) + 4 * g;
-                            const u2v v = *reinterpret_cast<const u2v *>(x);
+                        for (int k = 0; k < 4; ++k) odd |= (z[k] & 0x7f80u) == 0x7f80u || (z[k] & 0x7f800000u) == 0x7f800000u;
+                    }
+                    if (__builtin_amdgcn_ballot_w64(odd) != 0) {
+                        int sees[R];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t b = (v[j / 2] >> (16 * (j & 1))) & 0xffffu;
-                                const float f = (b & 0x7f80u) == 0x7f80u ? bf16_bits_to_f32(b) : 0.0f;
+                        for (int r = 0; r < R; ++r) sees[r] = seen_by(at, 32 * r + pr);
+#pragma unroll 1
+                        for (int k = 0; k < kStep; ++k) {
 #pragma unroll
-                                for (int r = 0; r < R; ++r) o[r][e / 4][4 * (e % 4) + j] += t * kKeys + i < sees[r] ? f : 0.0f;
+                            for (int e = 0; e < kWaveDims / 8; ++e) {
+                                const uint16_t *y = sm.row[buf][ow * (kWaveDims / 64) + (e >> 3)] + k * 64 + (((e & 7) ^ swap(k)) << 3) + 4 * g;
+                                const u2v z = *reinterpret_cast<const u2v *>(y);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t b = (z[j / 2] >> (16 * (j & 1))) & 0xffffu;
+                                    const float f = (b & 0x7f80u) == 0x7f80u ? bf16_bits_to_f32(b) : 0.0f;
+#pragma unroll
+                                    for (int r = 0; r < R; ++r) o[r][e / 4][4 * (e % 4) + j] += at.t * kStep + k < sees[r] ? f : 0.0f;
+                                }
+                            }
+                        }
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        uint32_t *y = reinterpret_cast<uint32_t *>(v);
+                        for (int k = lane; k < kWaveDims / 64 * kSub / 4; k += 64) {
+                            uint32_t z = y[k];
+                            if ((z & 0x7f80u) == 0x7f80u) z &= 0xffff0000u;
+                            if ((z & 0x7f800000u) == 0x7f800000u) z &= 0x0000ffffu;
+                            y[k] = z;
+                        }
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    }
+                }
+                constexpr int kSlots = kStep / 16 * kWaveDims / 32, kAhead = 3;
+                const uint32_t v = at_v + buf * (uint32_t)sizeof(sm.row[0]);
+                const auto operand = [&](int y) {
+                    const int d = y % (kWaveDims / 32);
+                    const uint32_t z = (v ^ ((d & 1) << 6)) + (d >> 1) * kSub + y / (kWaveDims / 32) * 16 * 128;
+                    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(z));
+                    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>((z ^ 16) + 4 * 128));
+                    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                };
+                s8 p[R][2], ring[kAhead];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) p[r][ks] = read8((at_p ^ (ks << 5)) + (x & 1) * (uint32_t)sizeof(sm.p[0]) + r * 32 * 64);
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y) ring[y] = operand(y);
+#pragma unroll
+                for (int y = 0; y < kSlots; ++y) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        o[r][y % (kWaveDims / 32)] = mfma32(ring[y % kAhead], p[r][y / (kWaveDims / 32)], o[r][y % (kWaveDims / 32)]);
+                    if (y + kAhead < kSlots) ring[y % kAhead] = operand(y + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                const bool ends = at.t == at.steps - 1;
+                if (ends || i == count) {
+                    const int64_t tile = (int64_t)at.n * a.row_tiles + at.rt;
+                    const bool begins = at.t - (x - begin) == 0;  // its first step is this workgroup's, too
+                    const int64_t slot = 2 * w + (begin == 0 ? 0 : 1);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float z = sm.sum[segment & 1][0][32 * r + pr] + sm.sum[segment & 1][1][32 * r + pr];
+                        const uint32_t j = (uint32_t)(at.rt * R + r) * 32 + pr;
+                        if (begins && ends) {
+                            const float f = z == 0.0f ? 0.0f : 1.0f / z;
+                            if (j >= rows) continue;
+                            uint16_t *out = a.out + (at.n * (int64_t)rows + j) * kLat + ow * kWaveDims + 4 * g;
+#pragma unroll
+                            for (int d = 0; d < kWaveDims / 32; ++d)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const u2v y = {pack2(o[r][d][4 * e] * f, o[r][d][4 * e + 1] * f),
+                                                   pack2(o[r][d][4 * e + 2] * f, o[r][d][4 * e + 3] * f)};
+                                    *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = y;
+                                }
+                            if (a.lse && g == 0 && ow == 0)
+                                a.lse[at.n * (int64_t)rows + j] = z == 0.0f ? -INFINITY : (m[r] + __builtin_amdgcn_logf(z)) * kLn2;
+                        } else {
+                            f4 *y = reinterpret_cast<f4 *>(a.part) + ((slot * kOutWaves + ow) * R + r) * (kWaveDims / 8 * 64) + lane;
+#pragma unroll
+                            for (int d = 0; d < kWaveDims / 32; ++d)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    y[(4 * d + e) * 64] = f4{o[r][d][4 * e], o[r][d][4 * e + 1], o[r][d][4 * e + 2], o[r][d][4 * e + 3]};
+                            if (g == 0 && ow == 0) {
+                                float *st = a.part_stat + (slot * R + r) * 64 + lane;
+                                st[0] = m[r];
+                                st[32] = z;
                             }
                         }
                     }
-                    __syncthreads();
-                    uint32_t *x = reinterpret_cast<uint32_t *>(sm.row[t & 1]);
-                    for (int i = tid; i < kLat / 64 * kSub / 4; i += 512) {
-                        uint32_t v = x[i];
-                        if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-                        if ((v >> 16 & 0x7f80u) == 0x7f80u) v &= 0x0000ffffu;
-                        x[i] = v;
+                    if (lane == 0 && ow == 0 && begins) {
+                        a.seg[2 * tile] = ends ? -1 : (int32_t)slot;
+                        a.seg[2 * tile + 1] = (int32_t)((first + begin + at.steps - 1) / per);
                     }
-                    __syncthreads();
+                    reset();
+                    begin = i;
+                    ++segment;
                 }
-                // outputs
-                {
-                    constexpr int kAhead = 3;
-                    const uint32_t v = at_v + buf;
-                    const auto operand = [&](int i) {
-                        const uint32_t x = (v ^ ((i & 1) << 6)) + (i >> 1) * 16 * 128;
-                        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(x));
-                        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>((x ^ 16) + 4 * 128));
-                        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                    };
-                    s8 p[R][2], ring[kAhead];
+                advance(a, at);
+            }
+            if (i + 2 < count) arrive<kOddCopies>();
+            else arrive<0>();
+            if (i < count && sm.rise[i & 1]) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) p[r][0] = read8(at_p + r * 32 * 128);
+                for (int r = 0; r < R; ++r) {
+                    const float x = fmaxf(m[r], fmaxf(sm.top[0][32 * r + pr], sm.top[1][32 * r + pr])), f = rescale(m[r], x);
+                    m[r] = x;
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) ring[i] = operand(i);
+                    for (int d = 0; d < kWaveDims / 32; ++d)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if ((i & 1) == 0 && i < 6)
-#pragma unroll
-                            for (int r = 0; r < R; ++r) p[r][(i >> 1) + 1 & 1] = read8((at_p ^ (((i >> 1) + 1) << 5)) + r * 32 * 128);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) o[r][i & 1] = mfma32(ring[i % kAhead], p[r][i >> 1 & 1], o[r][i & 1]);
-                        if (i + kAhead < 8) ring[i % kAhead] = operand(i + kAhead);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                        for (int e = 0; e < 16; ++e) o[r][d][e] *= f;
                 }
-            }
-            if (apart || t1 * kKeys <= all_see || a.T == 1) break;
-            float odd = 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) odd = fmaf(o[r][d][i], 0.0f, odd);
-            __syncthreads();
-            if (tid == 0) sm.odd = 0;
-            __syncthreads();
-            if (!(odd == 0.0f)) sm.odd = 1;
-            __syncthreads();
-            if (!sm.odd) break;
-        }
-
-        // The sums over all keys.
-        __syncthreads();
-        const float mine = quad_sum(l);
-        if (g16 == 0) sm.sum[kg][my_row] = mine;
-        __syncthreads();
-        float z[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = 32 * r + (lane & 31);
-            z[r] = sm.sum[0][row] + sm.sum[1][row];
-            if (kKeyGroups == 4) z[r] += sm.sum[2][row] + sm.sum[3][row];
-        }
-        if (alone) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t i = (uint32_t)((rt * R + r) * 32 + (lane & 31));
-                const float f = z[r] == 0.0f ? 0.0f : 1.0f / z[r];
-                if (i >= rows) continue;
-                uint16_t *out = a.out + (n * rows + i) * kLat + wave * 64 + 4 * g;
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const u2v x = {pack2(o[r][d][4 * e] * f, o[r][d][4 * e + 1] * f), pack2(o[r][d][4 * e + 2] * f, o[r][d][4 * e + 3] * f)};
-                        *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = x;
-                    }
-                if (a.lse && g == 0 && wave == 0)
-                    a.lse[n * rows + i] = z[r] == 0.0f ? -INFINITY : (mo[r] + __builtin_amdgcn_logf(z[r])) * kLn2;
-            }
-            if (tid == 0) a.seg[2 * (n * a.row_tiles + rt)] = -1;
-        } else {
-            const int64_t slot = 2 * w + (opening ? 0 : 1);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                f4 *p = reinterpret_cast<f4 *>(a.part) + ((slot * kWaves + wave) * R + r) * (8 * 64) + lane;
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[(4 * d + e) * 64] = f4{o[r][d][4 * e], o[r][d][4 * e + 1], o[r][d][4 * e + 2], o[r][d][4 * e + 3]};
-                if (g == 0 && wave == 0) {
-                    float *st = a.part_stat + (slot * R + r) * 64 + lane;
-                    st[0] = mo[r];
-                    st[32] = z[r];
-                }
-            }
-            if (t0 == 0 && tid == 0) {
-                a.seg[2 * (n * a.row_tiles + rt)] = (int32_t)slot;
-                a.seg[2 * (n * a.row_tiles + rt) + 1] = (int32_t)((step + tiles - 1) / per);
+                lds_barrier();
             }
         }
-        step += t1 - t0;
-        rest += t1 - t0;
-        opening = false;
     }
 }
 
@@ -427,7 +527,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDeco
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n32 = lane & 31;
     const int64_t unit = base + blockIdx.x, tile = unit / (64 * R);
     const int piece = (int)(unit & 63), r = (int)(unit / 64 % R);
-    const int pw = piece >> 3, pv = piece & 7;  // wave and group of values
+    const int pw = piece >> 4, pv = piece & 15;  // wave and group of values
     const int32_t head = a.seg[2 * tile];
     if (head == -1) return;
     const int64_t rows = a.T * a.H, n = tile / a.row_tiles, rt = tile - n * a.row_tiles;
@@ -442,7 +542,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDeco
         for (int w = w0 + wave; w <= w1; w += kJoinWaves) {
             const int64_t s = (int64_t)(w == w0 ? head : 2 * w) * R + r;
             const float *st = a.part_stat + s * 64 + n32;
-            const f4 x = reinterpret_cast<const f4 *>(a.part)[((s / R * kWaves + pw) * R + r) * (8 * 64) + pv * 64 + lane];
+            const f4 x = reinterpret_cast<const f4 *>(a.part)[((s / R * kOutWaves + pw) * R + r) * (kWaveDims / 8 * 64) + pv * 64 + lane];
             const float top = fmaxf(m, st[0]), f = factor(m, top), e = factor(st[0], top);
             o = o * f + x * e;
             l = l * f + st[32] * e;
@@ -467,7 +567,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDeco
         l += sums[w][n32] * f;
     }
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *out = a.out + (n * rows + i) * kLat + pw * 64 + 32 * (pv >> 2) + 8 * (pv & 3) + 4 * (lane >> 5);
+    uint16_t *out = a.out + (n * rows + i) * kLat + pw * kWaveDims + 32 * (pv >> 2) + 8 * (pv & 3) + 4 * (lane >> 5);
     *reinterpret_cast<u2v *>(out) = u2v{pack2(o[0] * f, o[1] * f), pack2(o[2] * f, o[3] * f)};
     if (a.lse && piece == 0 && lane < 32) a.lse[n * rows + i] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
