@@ -60,23 +60,25 @@ __device__ __forceinline__ float pair_sum(float x) {
 
 // ---- tiles in LDS -----------------------------------------------------------------
 // A tile holds rows of 16-byte chunks, 8 (or a multiple) to a row, with chunk c of row
-// r at place c ^ swap(r).  Both reads are then without bank conflicts: 16 bytes of 8
-// neighbouring rows (swap takes 8 values), and the transposing read's 32 bytes of 4
-// rows (swap / 2 takes 4).
+// r at place c ^ swap(r): 16 bytes of 8 neighbouring rows then lie in 8 different places
+// of 128 bytes (swap takes 8 values), and so do the transposing read's 32 bytes of 4 rows
+// (swap / 2 takes 4).  (A swap over 256 bytes, which are what LDS delivers a cycle, leaves
+// no conflicts at all, 57% of the LDS cycles, but needs twice the addresses: the forward
+// 762 -> 865 us, the gradient 2473 -> 2620.)
 __device__ __forceinline__ int swap(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
 
 typedef const __attribute__((address_space(3))) s8 *lds_s8;
 typedef __attribute__((address_space(3))) s4 *lds_s4;
 __device__ __forceinline__ s8 read8(uint32_t at) { return *reinterpret_cast<lds_s8>(at); }
-__device__ __forceinline__ s8 read_tr(uint32_t at, uint32_t step) {
-    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(at));
-    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(at + step));
+__device__ __forceinline__ s8 read_tr(uint32_t first, uint32_t second) {
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(first));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(second));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Row operand of rows 0 .. 31 of a tile of `row` bytes a row, k-block ks: at
-// row_at(...) ^ 32 ks within 128 bytes, 128 bytes further for every 4 k-blocks, 32
-// rows further for the next rows.
+// Row operand of rows 0 .. 31 of a tile of ROW bytes a row, k-block ks: at row_at(...) ^
+// 32 ks within 128 bytes, 128 bytes further for every 4 k-blocks, 32 rows further for the
+// next rows.
 template <int ROW>
 __device__ __forceinline__ uint32_t row_at(uint32_t base, int lane) {
     const int n = lane & 31, g = lane >> 5;
@@ -86,7 +88,8 @@ template <int ROW>
 __device__ __forceinline__ s8 row_operand(uint32_t at, int rows32, int ks) {
     return read8((at ^ ((ks & 3) << 5)) + (ks >> 2) * 128 + rows32 * 32 * ROW);
 }
-// Column operand: 32 columns from 32 dt, the rows perm(s, g, j) of k-block s.
+// Column operand: 32 columns from 32 dt, the rows perm(s, g, j) of k-block s: 4 rows,
+// and 4 that are 8 further.
 template <int ROW>
 __device__ __forceinline__ uint32_t col_at(uint32_t base, int lane) {
     const int i = lane & 15, c16 = (lane >> 4) & 1, g = lane >> 5;
@@ -95,7 +98,8 @@ __device__ __forceinline__ uint32_t col_at(uint32_t base, int lane) {
 }
 template <int ROW>
 __device__ __forceinline__ s8 col_operand(uint32_t at, int s, int dt) {
-    return read_tr((at ^ ((dt & 1) << 6)) + (dt >> 1) * 128 + s * 16 * ROW, 8 * ROW);
+    const uint32_t x = (at ^ ((dt & 1) << 6)) + (dt >> 1) * 128 + s * 16 * ROW;
+    return read_tr(x, x + 8 * ROW);
 }
 
 // Copies from global memory straight into LDS, 16 bytes a lane: the wave's 64 lanes

@@ -35,13 +35,17 @@ constexpr int kWaveDims = kLat / kOutWaves;    // values of an output wave
 
 struct DecodeSmem {
     uint16_t row[kBuffers][kSubs][kStep * 64];
-    uint16_t p[2][64 * kStep];                 // [row][key], 16-byte chunk c of row r at c ^ (r / 2 % 4)
+    uint16_t p[2][64 * kStep];                 // [row][key], 16-byte chunk c of row r at c ^ (r / 4 % 4)
     int32_t entry[kEntries][64];               // page of every row of a step (32 of them)
     float top[2][64], sum[2][2][64];           // [half of the keys][row]; of two segments
     int rise[2];
     int64_t wave_sum[8];
     int64_t begin_n, begin_rest;
 };
+
+// Chunk c of row r lies at place c ^ place(r) of its 128 bytes: reads of 16 bytes of 16
+// rows, and transposing ones of 64 bytes of 4 rows, are without bank conflicts.
+__device__ __forceinline__ int place(int r) { return ((r >> 1 & 1) << 2) | ((r >> 2) & 3); }
 
 // Copies 16 bytes a lane from p + OFF into LDS from lds on.
 template <int OFF>
@@ -100,7 +104,7 @@ template <bool EVEN>
 __device__ __forceinline__ void copy_step(const LatentDecodeArgs &a, const Cursor &x, int32_t page, int row, int chunk, uint32_t lds) {
     const int pos = min(x.t * kStep + row, x.len - 1);  // rows behind the length: the last one again
     const int64_t slot = (clamp64(page, 0, a.pages - 1) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-    const uint16_t *p = a.cache + slot * kRow + ((chunk ^ swap(row)) << 3);
+    const uint16_t *p = a.cache + slot * kRow + ((chunk ^ place(row)) << 3);
     if (EVEN) {
         copy16_at<0>(p, lds);
         copy16_at<256>(p, lds + 2 * kSub);
@@ -251,7 +255,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         // ---- scores: 16 keys and 16 R rows a wave --------------------------------------
         Feed<true> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
         const int kg = wave >> 1, r0 = (wave & 1) * 16 * R;
-        const uint32_t at_k = lds + (kg * 16 + n16) * 128 + ((g16 ^ swap(n16)) << 4);
+        const uint32_t at_k = lds + (kg * 16 + n16) * 128 + ((g16 ^ place(n16)) << 4);
         s8 q[R][kRow / 32];
         int seen[R], all_see = 0, segment = 0;
         float m[R], l[R];
@@ -275,7 +279,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                     for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f(fmaf(s[r][k], c, -x));
                     part[r] = (e[0] + e[1]) + (e[2] + e[3]);
                     *reinterpret_cast<__attribute__((address_space(3))) u2v *>(
-                        put + row * 64 + (((2 * kg + (g16 >> 1)) ^ (row >> 1 & 3)) << 4) + (g16 & 1) * 8) = u2v{pack2(e[0], e[1]), pack2(e[2], e[3])};
+                        put + row * 64 + (((2 * kg + (g16 >> 1)) ^ (row >> 2 & 3)) << 4) + (g16 & 1) * 8) = u2v{pack2(e[0], e[1]), pack2(e[2], e[3])};
                     if (last) {
                         const float z = quad_sum(l[r] + part[r]);
                         if (g16 == 0) sm.sum[segment & 1][kg][row] = z;
@@ -366,9 +370,9 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         Feed<false> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
         const int ow = wave - 4;
         const int vr = 8 * g + (n16 >> 2);  // keys 8 g .. of every 16, by two reads of 4 keys each
-        const uint32_t at_v = lds + ow * (kWaveDims / 64) * kSub + vr * 128 + (((2 * (g16 & 1) + ((n16 & 3) >> 1)) ^ swap(vr)) << 4) + (n16 & 1) * 8;
+        const uint32_t at_v = lds + ow * (kWaveDims / 64) * kSub + vr * 128 + (((2 * (g16 & 1) + ((n16 & 3) >> 1)) ^ place(vr)) << 4) + (n16 & 1) * 8;
         const int pr = lane & 31;
-        const uint32_t at_p = lds_p + pr * 64 + ((g ^ (pr >> 1 & 3)) << 4);
+        const uint32_t at_p = lds_p + pr * 64 + ((g ^ (pr >> 2 & 3)) << 4);
         f16v o[R][kWaveDims / 32];
         float m[R];
         int segment = 0, begin = 0;  // begin: the segment's first step
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                         for (int k = 0; k < kStep; ++k) {
 #pragma unroll
                             for (int e = 0; e < kWaveDims / 8; ++e) {
-                                const uint16_t *y = sm.row[buf][ow * (kWaveDims / 64) + (e >> 3)] + k * 64 + (((e & 7) ^ swap(k)) << 3) + 4 * g;
+                                const uint16_t *y = sm.row[buf][ow * (kWaveDims / 64) + (e >> 3)] + k * 64 + (((e & 7) ^ place(k)) << 3) + 4 * g;
                                 const u2v z = *reinterpret_cast<const u2v *>(y);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
@@ -433,9 +437,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                 const auto operand = [&](int y) {
                     const int d = y % (kWaveDims / 32);
                     const uint32_t z = (v ^ ((d & 1) << 6)) + (d >> 1) * kSub + y / (kWaveDims / 32) * 16 * 128;
-                    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>(z));
-                    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s4>((z ^ 16) + 4 * 128));
-                    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    return read_tr(z, (z ^ 16) + 4 * 128);
                 };
                 s8 p[R][2], ring[kAhead];
 #pragma unroll

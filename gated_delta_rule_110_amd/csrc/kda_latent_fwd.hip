@@ -486,7 +486,7 @@ hipError_t kda_launch_latent_table(const LatentArgs &a, int size, int by_keys, i
     return hipGetLastError();
 }
 
-int kda_latent_block(int64_t B, int64_t T, int64_t H) { (void)B; (void)T; (void)H; return getenv("KDA_QT") && getenv("KDA_QT")[0] == '1' ? 128 : 256; }
+int kda_latent_block(int64_t B, int64_t T, int64_t H) { (void)B; (void)T; (void)H; return getenv("KDA_QT") && getenv("KDA_QT")[0] == '2' ? 256 : 128; }
 
 hipError_t kda_launch_latent_fwd(const LatentArgs &a, int block, hipStream_t s) {
     const int64_t units = a.blocks * a.B * a.H;
