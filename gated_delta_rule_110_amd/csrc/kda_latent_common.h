@@ -131,21 +131,21 @@ __device__ __forceinline__ void copies_done() {
     asm volatile("" ::: "memory");
 }
 
-// `rows` (at most 64) rows of 2 W bytes, `stride` bytes apart, into a tile: for a workgroup of 256 threads, W / 8 chunks
-// a row.  voff: tile_offset's; chunk blocks of 256 are voff + i step.
+// `rows` (at most 64) rows of 2 W bytes, `stride` bytes apart, into a tile, by the
+// workgroup's WAVES waves.  off: tile_offset's.
 template <int W>
 __device__ __forceinline__ uint32_t tile_offset(int tid, uint32_t stride) {
     constexpr int C = W / 8;
     const int r = tid / C, c = tid % C;
     return (uint32_t)r * stride + (uint32_t)((c ^ swap(r)) << 4);
 }
-template <int W>
+template <int W, int WAVES = 4>
 __device__ __forceinline__ void copy_tile(const uint16_t *p, int rows, uint32_t stride, uint32_t off, uint32_t lds, int wave) {
-    constexpr int C = W / 8, kRows = 256 / C;
+    constexpr int C = W / 8, kRows = WAVES * 64 / C;
     const i4v rsrc = buffer_of(p, rows > 0 ? (uint32_t)(rows - 1) * stride + 2 * W : 0u);
 #pragma unroll
     for (int i = 0; i < kKeys / kRows; ++i)
-        copy16(rsrc, off + (uint32_t)(i * kRows) * stride, lds + i * 4096 + wave * 1024);
+        copy16(rsrc, off + (uint32_t)(i * kRows) * stride, lds + (i * WAVES + wave) * 1024);
 }
 
 // ---- a block's sequence ----------------------------------------------------------

@@ -1,8 +1,8 @@
 // kda_latent_fwd.hip -- latent attention in its expanded form (kda_latent_fwd in
 // include/kda_latent.h), and the table of a packed batch's blocks.
 //
-// A workgroup of four waves has 128 QT queries of one head and runs once through the
-// keys they see, 64 at a time.  Scores are taken transposed, S^T = K Q^T, so that a
+// A workgroup of four or eight waves has 32 queries a wave of one head and runs once
+// through the keys they see, 64 at a time.  Scores are taken transposed, S^T = K Q^T, so that a
 // lane holds one query's: its maximum and sum are the lane's own but for one exchange
 // between lanes n and n + 32, and the accumulators, rounded to bf16, are the B operand
 // of O^T += V^T P^T as they stand.  Queries stay in registers, keys and values come by
@@ -25,11 +25,10 @@ struct FwdSmem {
     uint16_t v[2][kKeys * kVal];
 };
 
-template <int QT>
 struct FwdState {
-    s8 q[QT][kQk / 16];
-    f16v o[QT][kVal / 32];
-    float mc[QT], l[QT];  // running maximum (times scale, log2 units) and this lane's part of the sum
+    s8 q[kQk / 16];
+    f16v o[kVal / 32];
+    float mc, l;   // running maximum (times scale, log2 units) and this lane's part of the sum
 };
 
 struct FwdAddr {
@@ -49,146 +48,103 @@ __device__ __forceinline__ s8 value_operand(const FwdAddr &at, int buf, int m) {
 }
 constexpr int kKeySlots = 2 * kQk / 16, kValueSlots = 4 * kVal / 32;
 
-// Scores of keys that a query does not see become -infinity.  base: the tile's first
-// key; seen[q]: keys that the lane's query sees.
-template <int QT>
-__device__ __forceinline__ void mask(f16v (&s)[QT][2], const int (&seen)[QT], int base, int g) {
+// Scores of keys that the lane's query does not see become -infinity.  base: the tile's
+// first key; seen: keys that the query sees.
+__device__ __forceinline__ void mask(f16v (&s)[2], int seen, int base, int g) {
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int key = base + 32 * t + 8 * (i / 4) + 4 * g + i % 4;
-                s[q][t][i] = key < seen[q] ? s[q][t][i] : -INFINITY;
-            }
+        for (int i = 0; i < 16; ++i) s[t][i] = base + 32 * t + 8 * (i / 4) + 4 * g + i % 4 < seen ? s[t][i] : -INFINITY;
 }
 
-// The maximum of the lane's scores i, i + 1, .. of a query.
-template <int QT>
-__device__ __forceinline__ void maxima(const f16v (&s)[QT][2], float (&top)[QT], int first, int n) {
+// The maximum of n of the lane's scores of either half, from `first` on.
+__device__ __forceinline__ void maxima(const f16v (&s)[2], float &top, int first, int n) {
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-        for (int i = first; i < first + n; ++i) top[q] = fmaxf(fmaxf(top[q], s[q][0][i]), s[q][1][i]);
+    for (int i = first; i < first + n; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
 }
 
 // A rise of the maximum scales the accumulators.  The maximum in use may stay up to 2^8
 // below the true one: probabilities up to 256 lose nothing, and the accumulators are
 // scaled a few times a row instead of once a tile.
-template <int QT>
-__device__ __forceinline__ void rise(FwdState<QT> &f, const float (&lane_top)[QT], float c) {
+__device__ __forceinline__ void rise(FwdState &f, float lane_top, float c) {
     constexpr float kSlack = 8.0f;
-    float top[QT];
-    bool need = false;
+    const float top = pair_max(lane_top) * c;
+    if (__builtin_amdgcn_ballot_w64(top > f.mc + kSlack) == 0) return;
+    const float m = fmaxf(f.mc, top);
+    const float w = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(f.mc - m);
+    f.mc = m;
+    f.l *= w;
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-        top[q] = pair_max(lane_top[q]) * c;
-        need |= top[q] > f.mc[q] + kSlack;
-    }
-    if (__builtin_amdgcn_ballot_w64(need) != 0) {
+    for (int d = 0; d < kVal / 32; ++d)
 #pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            const float m = fmaxf(f.mc[q], top[q]);
-            const float w = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(f.mc[q] - m);
-            f.mc[q] = m;
-            f.l[q] *= w;
-#pragma unroll
-            for (int d = 0; d < kVal / 32; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f.o[q][d][i] *= w;
-        }
-    }
+        for (int i = 0; i < 16; ++i) f.o[d][i] *= w;
 }
 
-// Probability x of a tile's 32 QT in the lane, those of the first 32 keys first: entry
-// x % 16 of half x / (16 QT).  Every second one completes a word of the B operand.
-template <int QT>
+// Probability x of a tile's 32 in the lane, those of the first 32 keys first.  Every
+// second one completes a word of the B operand.
 struct Probs {
-    u4v w[QT][4];
+    u4v w[4];
     float last;
 };
-template <int QT>
-__device__ __forceinline__ void probability(FwdState<QT> &f, const f16v (&s)[QT][2], float c, const float (&m)[QT], int x, Probs<QT> &p) {
-    const int t = x / (16 * QT), q = x / 16 % QT, i = x % 16;
-    const float e = __builtin_amdgcn_exp2f(fmaf(s[q][t][i], c, -m[q]));
-    f.l[q] += e;
-    if (i & 1) p.w[q][2 * t + i / 8][i % 8 / 2] = pack2(p.last, e);
+__device__ __forceinline__ void probability(FwdState &f, const f16v (&s)[2], float c, float m, int x, Probs &p) {
+    const int t = x / 16, i = x % 16;
+    const float e = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -m));
+    f.l += e;
+    if (i & 1) p.w[2 * t + i / 8][i % 8 / 2] = pack2(p.last, e);
     else p.last = e;
 }
 
 // Tile j's probabilities and outputs; with NEXT the scores of tile j + 1 too (and their
-// maxima), whose 24 slots of QT products each come first, with QT exponentials a slot;
-// the last QT 8 are taken in the first slots of the outputs' products, which need them in
-// the last.  Operands are read kAhead slots before their use.  The order is fixed by
-// the fences: left to itself the compiler reads all operands at once and spills.
-template <int QT, bool NEXT>
-__device__ __forceinline__ void tile_step(FwdState<QT> &f, const FwdAddr &at, int buf, const f16v (&s)[QT][2], f16v (&next)[QT][2],
-                                          float (&top)[QT], float c) {
-    constexpr int kAhead = 4;
-    float m[QT];
-    Probs<QT> p;
-#pragma unroll
-    for (int q = 0; q < QT; ++q) m[q] = f.mc[q] == -INFINITY ? 0.0f : f.mc[q];
+// maxima), whose 24 products come first, with an exponential each; the last 8 are taken
+// beside the first half of the outputs' products, which need them in the second.
+// Operands are read kAhead products before their use.  The order is fixed by the
+// fences: left to itself the compiler reads all operands at once and spills.
+template <bool NEXT>
+__device__ __forceinline__ void tile_step(FwdState &f, const FwdAddr &at, int buf, const f16v (&s)[2], f16v (&next)[2], float &top, float c) {
+    constexpr int kAhead = 4, kFirst = NEXT ? 0 : kKeySlots;
+    const float m = f.mc == -INFINITY ? 0.0f : f.mc;
+    Probs p;
     s8 ring[kAhead];
-    constexpr int kFirst = NEXT ? 0 : kKeySlots;
     const auto operand = [&](int n) { return n < kKeySlots ? key_operand(at, buf ^ 1, n) : value_operand(at, buf, n - kKeySlots); };
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) ring[(kFirst + n) % kAhead] = operand(kFirst + n);
     if (NEXT) {
-#pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            next[q][0] = next[q][1] = zero16();
-            top[q] = -INFINITY;
-        }
+        next[0] = next[1] = zero16();
+        top = -INFINITY;
     } else {
 #pragma unroll
-        for (int x = 0; x < QT * kKeySlots; ++x) probability<QT>(f, s, c, m, x, p);
+        for (int x = 0; x < kKeySlots; ++x) probability(f, s, c, m, x, p);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = kFirst; n < kKeySlots + kValueSlots; ++n) {
         const s8 a = ring[n % kAhead];
         const int v = n - kKeySlots;
-#pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            if (v < 0) next[q][n & 1] = mfma32(a, f.q[q][n >> 1], next[q][n & 1]);
-            else f.o[q][v & 3] = mfma32(a, __builtin_bit_cast(s8, p.w[q][v >> 2]), f.o[q][v & 3]);
-        }
+        if (v < 0) next[n & 1] = mfma32(a, f.q[n >> 1], next[n & 1]);
+        else f.o[v & 3] = mfma32(a, __builtin_bit_cast(s8, p.w[v >> 2]), f.o[v & 3]);
         if (n + kAhead < kKeySlots + kValueSlots) ring[n % kAhead] = operand(n + kAhead);
-        if (v < kValueSlots / 2) {
-#pragma unroll
-            for (int x = n * QT; x < (n + 1) * QT; ++x) probability<QT>(f, s, c, m, x, p);
-        } else if (NEXT) {
-            maxima<QT>(next, top, 2 * (v - kValueSlots / 2), 2);
-        }
+        if (v < kValueSlots / 2) probability(f, s, c, m, n, p);
+        else if (NEXT) maxima(next, top, 2 * (v - kValueSlots / 2), 2);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <int QT>
-__device__ __forceinline__ void first_scores(const FwdState<QT> &f, const FwdAddr &at, int buf, f16v (&s)[QT][2], float (&top)[QT]) {
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-        s[q][0] = s[q][1] = zero16();
-        top[q] = -INFINITY;
-    }
+__device__ __forceinline__ void first_scores(const FwdState &f, const FwdAddr &at, int buf, f16v (&s)[2], float &top) {
+    s[0] = s[1] = zero16();
 #pragma unroll
     for (int n = 0; n < kKeySlots; ++n) {
-        const s8 a = key_operand(at, buf, n);
-#pragma unroll
-        for (int q = 0; q < QT; ++q) s[q][n & 1] = mfma32(a, f.q[q][n >> 1], s[q][n & 1]);
+        s[n & 1] = mfma32(key_operand(at, buf, n), f.q[n >> 1], s[n & 1]);
         if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
-    maxima<QT>(s, top, 0, 16);
+    top = -INFINITY;
+    maxima(s, top, 0, 16);
 }
 
 // Values that are NaN or infinite meet the zero probabilities of queries that do not see
 // them.  Where a tile has hidden keys, those values are added apart, to the queries that
 // see their keys, and then taken as zeros.
 __device__ __forceinline__ bool odd_bits(uint32_t bf16) { return (bf16 & 0x7f80u) == 0x7f80u; }
-template <int QT>
-__device__ __forceinline__ void add_odd(FwdState<QT> &f, const uint16_t *v, const int (&seen)[QT], int base, int g) {
+__device__ __forceinline__ void add_odd(FwdState &f, const uint16_t *v, int seen, int base, int g) {
 #pragma unroll 1
     for (int r = 0; r < kKeys; ++r) {
 #pragma unroll
@@ -198,15 +154,14 @@ __device__ __forceinline__ void add_odd(FwdState<QT> &f, const uint16_t *v, cons
             for (int k = 0; k < 4; ++k) {
                 const uint32_t b = (w[k / 2] >> (16 * (k & 1))) & 0xffffu;
                 const float x = odd_bits(b) ? bf16_bits_to_f32(b) : 0.0f;
-#pragma unroll
-                for (int q = 0; q < QT; ++q) f.o[q][e / 4][4 * (e % 4) + k] += base + r < seen[q] ? x : 0.0f;
+                f.o[e / 4][4 * (e % 4) + k] += base + r < seen ? x : 0.0f;
             }
         }
     }
 }
-__device__ __forceinline__ void clear_odd(uint16_t *v, int tid) {
+__device__ __forceinline__ void clear_odd(uint16_t *v, int tid, int threads) {
     uint32_t *w = reinterpret_cast<uint32_t *>(v);
-    for (int i = tid; i < kKeys * kVal / 2; i += 256) {
+    for (int i = tid; i < kKeys * kVal / 2; i += threads) {
         uint32_t x = w[i];
         if (odd_bits(x)) x &= 0xffff0000u;
         if (odd_bits(x >> 16)) x &= 0x0000ffffu;
@@ -214,24 +169,25 @@ __device__ __forceinline__ void clear_odd(uint16_t *v, int tid) {
     }
 }
 
-template <int QT>
-__global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void latent_fwd_kernel(LatentArgs a) {
+// WAVES of 32 queries each.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a) {
     __shared__ __attribute__((aligned(1024))) FwdSmem sm;
-    constexpr int kBlock = 128 * QT;
+    constexpr int kBlock = 32 * WAVES;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
     Span sp;
     if (!span_of(a, unit / a.H, a.causal, sp)) return;
-    const int q_first = sp.block * kBlock + wave * 32 * QT;  // of this wave
+    const int q_first = sp.block * kBlock + wave * 32;  // of this wave
     const int block_last = min(sp.lq, (sp.block + 1) * kBlock) - 1;
     if (block_last < sp.block * kBlock) return;
 
     const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
-    const int tiles = (sees(block_last) + kKeys - 1) / kKeys;             // of the workgroup
-    const int last = min(sp.lq - 1, q_first + 32 * QT - 1);
+    const int tiles = (sees(block_last) + kKeys - 1) / kKeys;                // of the workgroup
+    const int last = min(sp.lq - 1, q_first + 31);
     const int mine = last < q_first ? 0 : (sees(last) + kKeys - 1) / kKeys;  // of this wave
-    const int whole = sees(q_first) / kKeys;                              // of them without hidden keys
+    const int whole = sees(q_first) / kKeys;                                 // of them without hidden keys
 
     const uint16_t *kv = a.kv + sp.b * a.kvb + sp.k0 * a.kvt + h * kKvRow;
     const uint16_t *pe = a.pe + sp.b * a.peb + sp.k0 * a.pet;
@@ -240,12 +196,12 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void latent_fwd_kernel(Latent
     const uint32_t lds_kn = lds_addr(sm.kn), lds_kp = lds_addr(sm.kp), lds_v = lds_addr(sm.v);
     const auto copy_keys = [&](int j) {
         const int rows = min(kKeys, sp.lk - j * kKeys), buf = j & 1;
-        copy_tile<kNope>(kv + (int64_t)j * kKeys * a.kvt, rows, kv_bytes, off_n, lds_kn + buf * (uint32_t)sizeof(sm.kn[0]), wave);
-        copy_tile<kPe>(pe + (int64_t)j * kKeys * a.pet, rows, pe_bytes, off_p, lds_kp + buf * (uint32_t)sizeof(sm.kp[0]), wave);
+        copy_tile<kNope, WAVES>(kv + (int64_t)j * kKeys * a.kvt, rows, kv_bytes, off_n, lds_kn + buf * (uint32_t)sizeof(sm.kn[0]), wave);
+        copy_tile<kPe, WAVES>(pe + (int64_t)j * kKeys * a.pet, rows, pe_bytes, off_p, lds_kp + buf * (uint32_t)sizeof(sm.kp[0]), wave);
     };
     const auto copy_values = [&](int j) {
         const int rows = min(kKeys, sp.lk - j * kKeys), buf = j & 1;
-        copy_tile<kVal>(kv + kNope + (int64_t)j * kKeys * a.kvt, rows, kv_bytes, off_n, lds_v + buf * (uint32_t)sizeof(sm.v[0]), wave);
+        copy_tile<kVal, WAVES>(kv + kNope + (int64_t)j * kKeys * a.kvt, rows, kv_bytes, off_n, lds_v + buf * (uint32_t)sizeof(sm.v[0]), wave);
     };
     if (tiles > 0) {
         copy_keys(0);
@@ -253,72 +209,60 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void latent_fwd_kernel(Latent
         copy_values(0);
     }
 
-    FwdState<QT> f;
-    int seen[QT];
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-        const int i = q_first + 32 * q + (lane & 31);
-        seen[q] = sees(i);
+    FwdState f;
+    const int i = q_first + (lane & 31), seen = sees(i);
+    {
         const uint16_t *p = a.q + sp.b * a.qb + (sp.q0 + min(i, sp.lq - 1)) * a.qt + h * kQk + 8 * g;
 #pragma unroll
-        for (int ks = 0; ks < kQk / 16; ++ks) {
-            f.q[q][ks] = *reinterpret_cast<const s8 *>(p + 16 * ks);
-        }
+        for (int ks = 0; ks < kQk / 16; ++ks) f.q[ks] = *reinterpret_cast<const s8 *>(p + 16 * ks);
     }
     const auto reset = [&]() {
+        f.mc = -INFINITY;
+        f.l = 0.0f;
 #pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            f.mc[q] = -INFINITY;
-            f.l[q] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < kVal / 32; ++d) f.o[q][d] = zero16();
-        }
+        for (int d = 0; d < kVal / 32; ++d) f.o[d] = zero16();
     };
     reset();
     const FwdAddr at = {row_at<2 * kNope>(lds_kn, lane), row_at<2 * kPe>(lds_kp, lane), col_at<2 * kVal>(lds_v, lane)};
     const float c = a.scale * kLog2e;
 
-    // Tile j's scores are in `s`, their maxima in `top`; those of j + 1 go to `next`.
-    float top[QT];
+    // Tile j's scores are in `s`, their maximum in `top`; those of j + 1 go to `next`.
+    float top = -INFINITY;
     const auto begin = [&](int j) {
         copies_done();
         if (j + 2 < tiles) copy_keys(j + 2);
         if (j + 1 < tiles) copy_values(j + 1);
     };
-    const auto hide = [&](int j, f16v (&s)[QT][2]) {
-        mask<QT>(s, seen, j * kKeys, g);
-#pragma unroll
-        for (int q = 0; q < QT; ++q) top[q] = -INFINITY;
-        maxima<QT>(s, top, 0, 16);
+    const auto hide = [&](int j, f16v (&s)[2]) {
+        mask(s, seen, j * kKeys, g);
+        top = -INFINITY;
+        maxima(s, top, 0, 16);
     };
-    const auto step = [&](int j, f16v (&s)[QT][2], f16v (&next)[QT][2]) {
+    const auto step = [&](int j, f16v (&s)[2], f16v (&next)[2]) {
         begin(j);
         if (j >= whole) hide(j, s);
-        rise<QT>(f, top, c);
-        tile_step<QT, true>(f, at, j & 1, s, next, top, c);
+        rise(f, top, c);
+        tile_step<true>(f, at, j & 1, s, next, top, c);
     };
     if (tiles > 0) {
-        f16v s0[QT][2], s1[QT][2];
+        f16v s0[2], s1[2];
         copies_done();
         int j = 0;
         if (mine > 0) {
-            first_scores<QT>(f, at, 0, s0, top);
+            first_scores(f, at, 0, s0, top);
             for (; j + 2 < mine; j += 2) {
                 step(j, s0, s1);
                 step(j + 1, s1, s0);
             }
             if (j + 1 < mine) {
                 step(j++, s0, s1);
-#pragma unroll
-                for (int q = 0; q < QT; ++q) {
-                    s0[q][0] = s1[q][0];
-                    s0[q][1] = s1[q][1];
-                }
+                s0[0] = s1[0];
+                s0[1] = s1[1];
             }
             begin(j);
             if (j >= whole) hide(j, s0);
-            rise<QT>(f, top, c);
-            tile_step<QT, false>(f, at, j & 1, s0, s0, top, c);
+            rise(f, top, c);
+            tile_step<false>(f, at, j & 1, s0, s0, top, c);
             ++j;
         }
         for (; j < tiles; ++j) begin(j);
@@ -328,11 +272,9 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void latent_fwd_kernel(Latent
     // see.  The block runs again, tile by tile, with those apart.
     float odd = 0.0f;
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
+    for (int d = 0; d < kVal / 32; ++d)
 #pragma unroll
-        for (int d = 0; d < kVal / 32; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) odd = fmaf(f.o[q][d][i], 0.0f, odd);
+        for (int e = 0; e < 16; ++e) odd = fmaf(f.o[d][e], 0.0f, odd);
     uint32_t *flag = reinterpret_cast<uint32_t *>(sm.kn);
     copies_done();
     if (tid == 0) *flag = 0;
@@ -349,42 +291,37 @@ __global__ __launch_bounds__(256, QT == 1 ? 2 : 1) void latent_fwd_kernel(Latent
             copy_keys(j);
             copy_values(j);
             copies_done();
-            f16v s[QT][2];
+            f16v s[2];
             if (j < mine) {
-                first_scores<QT>(f, at, j & 1, s, top);
+                first_scores(f, at, j & 1, s, top);
                 hide(j, s);
-                rise<QT>(f, top, c);
+                rise(f, top, c);
             }
             if (j >= block_whole) {
-                if (j < mine) add_odd<QT>(f, sm.v[j & 1], seen, j * kKeys, g);
+                if (j < mine) add_odd(f, sm.v[j & 1], seen, j * kKeys, g);
                 __syncthreads();
-                clear_odd(sm.v[j & 1], tid);
+                clear_odd(sm.v[j & 1], tid, 64 * WAVES);
                 __syncthreads();
             }
-            if (j < mine) tile_step<QT, false>(f, at, j & 1, s, s, top, c);
+            if (j < mine) tile_step<false>(f, at, j & 1, s, s, top, c);
             __syncthreads();
         }
     }
 
+    const float l = pair_sum(f.l);
+    const float w = l == 0.0f ? 0.0f : 1.0f / l;
+    if (i >= sp.lq) return;
+    const int64_t row = (sp.b * a.T + sp.q0 + i) * a.H + h;
+    uint16_t *out = a.out + row * kVal + 4 * g;
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-        const int i = q_first + 32 * q + (lane & 31);
-        const float l = pair_sum(f.l[q]);
-        const float w = l == 0.0f ? 0.0f : 1.0f / l;
-        if (i >= sp.lq) continue;
-        const int64_t row = (sp.b * a.T + sp.q0 + i) * a.H + h;
-        uint16_t *out = a.out + row * kVal + 4 * g;
+    for (int d = 0; d < kVal / 32; ++d)
 #pragma unroll
-        for (int d = 0; d < kVal / 32; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const u2v w2 = {pack2(f.o[q][d][4 * e] * w, f.o[q][d][4 * e + 1] * w),
-                                pack2(f.o[q][d][4 * e + 2] * w, f.o[q][d][4 * e + 3] * w)};
-                *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = w2;
-            }
-        // l == 0: no key is seen
-        if (a.lse && g == 0) a.lse[row] = l == 0.0f ? -INFINITY : (f.mc[q] + __builtin_amdgcn_logf(l)) * kLn2;
-    }
+        for (int e = 0; e < 4; ++e) {
+            const u2v x = {pack2(f.o[d][4 * e] * w, f.o[d][4 * e + 1] * w), pack2(f.o[d][4 * e + 2] * w, f.o[d][4 * e + 3] * w)};
+            *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = x;
+        }
+    // l == 0: no key is seen
+    if (a.lse && g == 0) a.lse[row] = l == 0.0f ? -INFINITY : (f.mc + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // The blocks of a packed batch in order of falling length, by buckets of their tiles'
@@ -493,7 +430,7 @@ hipError_t kda_launch_latent_fwd(const LatentArgs &a, int block, hipStream_t s) 
     return launch_groups(units, a.launch_cap, [&](int64_t base, dim3 grid) {
         LatentArgs p = a;
         p.base = base;
-        if (block == 128) hipLaunchKernelGGL(latent_fwd_kernel<1>, grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(latent_fwd_kernel<2>, grid, dim3(256), 0, s, p);
+        if (block == 128) hipLaunchKernelGGL(latent_fwd_kernel<4>, grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL(latent_fwd_kernel<8>, grid, dim3(512), 0, s, p);
     });
 }
