@@ -242,7 +242,7 @@ kda_status_t plan_decode(const kda_latent_decode_desc_t *d, DecodePlan &p) {
     if (!page_ok(d->page_size)) return KDA_ERR_UNSUPPORTED;
     constexpr int64_t kMaxRows = int64_t(1) << 24;
     if (d->H > 65535 || d->T > kMaxRows / d->H || d->N > kMaxRows / (d->T * d->H)) return KDA_ERR_SHAPE;
-    if (d->pages > kMaxSeqs || d->max_pages > kMaxSeqs || d->max_pages > kMaxAttention / d->page_size) return KDA_ERR_SHAPE;
+    if (d->pages > kMaxSeqs / d->page_size || d->max_pages > kMaxSeqs || d->max_pages > kMaxAttention / d->page_size) return KDA_ERR_SHAPE;
     const int64_t strides[] = {d->ql_stride_n, d->ql_stride_t, d->ql_stride_h, d->qp_stride_n, d->qp_stride_t, d->qp_stride_h};
     for (int64_t s : strides)
         if (!stride_ok(s)) return KDA_ERR_SHAPE;

@@ -40,7 +40,8 @@ struct DecodeSmem {
     float top[2][64], sum[2][2][64];           // [half of the keys][row]; of two segments
     int rise[2];
     int64_t wave_sum[8];
-    int64_t begin_n, begin_rest;
+    int64_t begin_rest;
+    int begin_n, begin_len;
 };
 
 // Chunk c of row r lies at place c ^ place(r) of its 128 bytes: reads of 16 bytes of 16
@@ -103,8 +104,8 @@ __device__ __forceinline__ void advance(const LatentDecodeArgs &a, Cursor &x) {
 template <bool EVEN>
 __device__ __forceinline__ void copy_step(const LatentDecodeArgs &a, const Cursor &x, int32_t page, int row, int chunk, uint32_t lds) {
     const int pos = min(x.t * kStep + row, x.len - 1);  // rows behind the length: the last one again
-    const int64_t slot = (clamp64(page, 0, a.pages - 1) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-    const uint16_t *p = a.cache + slot * kRow + ((chunk ^ place(row)) << 3);
+    const uint32_t slot = ((uint32_t)min(max(page, 0), (int)a.pages - 1) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    const uint16_t *p = a.cache + (uint64_t)slot * kRow + ((chunk ^ place(row)) << 3);
     if (EVEN) {
         copy16_at<0>(p, lds);
         copy16_at<256>(p, lds + 2 * kSub);
@@ -191,14 +192,15 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
             if (first < at + t) break;
             at += t;
         }
-        sm.begin_n = n;
+        sm.begin_n = (int)n;
+        sm.begin_len = (int)clamp64(a.len[n], 0, a.max_pages << a.page_shift);
         sm.begin_rest = first - at;
     }
     __syncthreads();
     const int count = __builtin_amdgcn_readfirstlane((int)mine);
     Cursor at;
-    at.n = __builtin_amdgcn_readfirstlane((int)sm.begin_n);
-    at.len = length_of(a, at.n);
+    at.n = __builtin_amdgcn_readfirstlane(sm.begin_n);
+    at.len = __builtin_amdgcn_readfirstlane(sm.begin_len);
     at.steps = (at.len + kStep - 1) / kStep;
     {
         const int64_t rest = sm.begin_rest;
@@ -216,34 +218,30 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         return min(max(x.len - (int)a.T + 1 + (int)(i / H), 0), x.len);
     };
 
-    // The first two steps' copies, by entries that the thread reads itself; the next two's entries.
+    // The first two steps' copies, and the next two's entries: here every thread reads its row's.
     const int my_row = 8 * (wave & 3) + (lane >> 3);
-    Cursor copy = at, look;
+    Cursor copy = at, look = at;
     {
-        int32_t page[2];
-        Cursor x = at;
+        int32_t page[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+            page[i] = 0;
             if (i < count) {
-                page[i] = a.table[x.n * a.max_pages + (min(x.t * kStep + my_row, x.len - 1) >> a.page_shift)];
-                advance(a, x);
+                page[i] = a.table[look.n * a.max_pages + (min(look.t * kStep + my_row, look.len - 1) >> a.page_shift)];
+                advance(a, look);
             }
-        look = x;
-        const uint32_t place = lds + (wave & 3) * 1024;
-        for (int i = 2; i < 4 && i < count; ++i) {
-            if (tid < 64) {
-                const int pos = min(look.t * kStep + (tid & (kStep - 1)), look.len - 1);
-                sm.entry[i][tid] = a.table[look.n * a.max_pages + (pos >> a.page_shift)];
-            }
-            advance(a, look);
         }
+        const uint32_t to = lds + (wave & 3) * 1024;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (i < count) {
-                if (wave < 4) copy_step<true>(a, copy, page[i], my_row, lane & 7, place + i * (uint32_t)sizeof(sm.row[0]));
-                else copy_step<false>(a, copy, page[i], my_row, lane & 7, place + i * (uint32_t)sizeof(sm.row[0]));
+                if (wave < 4) copy_step<true>(a, copy, page[i], my_row, lane & 7, to + i * (uint32_t)sizeof(sm.row[0]));
+                else copy_step<false>(a, copy, page[i], my_row, lane & 7, to + i * (uint32_t)sizeof(sm.row[0]));
                 advance(a, copy);
             }
+        if (wave < 4 && (lane & 7) == 0)
+#pragma unroll
+            for (int i = 2; i < 4; ++i) sm.entry[i][my_row] = page[i];
     }
 
     // Probabilities use the maximum that is in use, which may stay 2^40 behind the true one

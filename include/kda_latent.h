@@ -106,7 +106,8 @@ typedef struct {
  * fp32 [N, T, H] or NULL.  Lengths are clamped to 0 .. max_pages page_size and pages
  * to 0 .. pages - 1, so that wrong ones give wrong results but no access outside the
  * tensors.  Cached rows at and behind a sequence's length are not used, whatever
- * they hold.  N T H of more than 2^24 rows are refused (KDA_ERR_SHAPE). */
+ * they hold.  Refused (KDA_ERR_SHAPE) are N T H of more than 2^24, caches of 2^31 rows
+ * and more, and N ceil(T H / 64) max_pages page_size of more than 2^43. */
 kda_status_t kda_latent_decode(const void *q_latent, const void *q_pe, const void *cache, const int64_t *lengths,
                                const int32_t *block_table, void *out, float *lse, const kda_latent_decode_desc_t *desc,
                                hipStream_t stream);
