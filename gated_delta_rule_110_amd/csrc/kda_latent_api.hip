@@ -85,7 +85,7 @@ kda_status_t table_bytes(int64_t blocks, size_t &bytes) {
 extern "C" size_t kda_latent_fwd_workspace_size(const kda_latent_desc_t *desc) {
     size_t need = 0;
     if (!desc || check_latent(desc, true) != KDA_OK) return 0;
-    const int block = kda_latent_block(desc->B, desc->T, desc->H);
+    const int block = kda_latent_block(desc->B, desc->T, desc->H, desc->num_seqs);
     return table_bytes(blocks_of(desc->T, block, desc->num_seqs, true), need) == KDA_OK ? need : 0;
 }
 
@@ -98,11 +98,12 @@ extern "C" kda_status_t kda_latent_fwd(const void *q, const void *kv, const void
     if (desc->T > 0 && !out) return KDA_ERR_NULL;
     if (!aligned(out, 16) || !aligned(lse, 4)) return KDA_ERR_ALIGN;
     const bool packed = cu_seqlens != nullptr;
-    const int block = kda_latent_block(desc->B, desc->T, desc->H);
+    const int block = kda_latent_block(desc->B, desc->T, desc->H, desc->num_seqs);
     a.blocks = blocks_of(desc->T, block, desc->num_seqs, packed);
     size_t need = 0;
     if (packed) st = table_bytes(a.blocks, need);
     if (st != KDA_OK) return st;
+    const bool counted = packed && kda_latent_counted(desc->num_seqs, a.blocks * desc->H);
     Memory m;
     latent_reads(m, q, kv, k_pe, cu_seqlens, cu_seqlens_k, desc);
     m.write(out, latent_rows(desc) * kVal * 2);
@@ -118,9 +119,9 @@ extern "C" kda_status_t kda_latent_fwd(const void *q, const void *kv, const void
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     hipError_t e = hipSuccess;
-    if (packed) {
+    if (packed && !counted) {
         int32_t *table = reinterpret_cast<int32_t *>(ws.at(0));
-        e = kda_launch_latent_table(a, block, 0, table, stream);
+        e = kda_launch_latent_table(a, block, table, a.blocks, nullptr, 0, stream);
         a.table = table;
     }
     if (e == hipSuccess) e = kda_launch_latent_fwd(a, block, stream);
@@ -207,10 +208,9 @@ extern "C" kda_status_t kda_latent_bwd(const void *q, const void *kv, const void
     a.blocks = p.q_blocks;
     k.blocks = p.k_blocks;
     hipError_t e = hipSuccess;
-    if (packed) {
+    if (packed && !kda_latent_counted(desc->num_seqs, std::max(p.q_blocks, p.k_blocks) * desc->H)) {
         int32_t *qt = reinterpret_cast<int32_t *>(ws.at(p.off_qt)), *kt = reinterpret_cast<int32_t *>(ws.at(p.off_kt));
-        e = kda_launch_latent_table(a, kLatentBwdBlock, 0, qt, stream);
-        if (e == hipSuccess) e = kda_launch_latent_table(k, kLatentBwdBlock, 1, kt, stream);
+        e = kda_launch_latent_table(a, kLatentBwdBlock, qt, p.q_blocks, kt, p.k_blocks, stream);
         a.table = qt;
         k.table = kt;
     }
@@ -371,7 +371,7 @@ kda_status_t check_pages(const kda_page_desc_t *d) {
 }  // namespace
 
 extern "C" size_t kda_page_workspace_size(const kda_page_desc_t *desc) {
-    return desc && check_pages(desc) == KDA_OK ? align_up((size_t)(desc->N + 1) * 8, 256) : 0;
+    return desc && check_pages(desc) == KDA_OK ? align_up((size_t)(2 * desc->N + 3) * 8, 256) : 0;
 }
 
 extern "C" kda_status_t kda_page_assign(const int64_t *lengths, const int64_t *new_tokens, const uint8_t *ended,
@@ -413,6 +413,7 @@ extern "C" kda_status_t kda_page_assign(const int64_t *lengths, const int64_t *n
     a.N = desc->N; a.max_pages = desc->max_pages; a.stack = desc->stack; a.tokens = desc->tokens;
     a.shift = log2_of(desc->page_size);
     a.have = reinterpret_cast<int64_t *>(ws.at(0));
-    a.base = a.have + 1;
+    a.base = a.have + 2;
+    a.back = a.base + a.N;
     return of_hip(kda_launch_pages(a, stream));
 }

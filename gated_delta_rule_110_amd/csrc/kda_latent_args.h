@@ -13,10 +13,10 @@ constexpr int kKeys = 64;                                 // keys (or queries) o
 struct LatentArgs {
     const uint16_t *q, *kv, *pe;
     int64_t qb, qt, kvb, kvt, peb, pet;
-    const int64_t *cu, *cuk;   // packed: offsets of queries and keys
+    const int64_t *cu, *cuk;   // packed: offsets of queries and keys, else nullptr
     int64_t B, T, Tk, H, seqs;
     int64_t blocks;            // blocks of queries (keys) per batch row; packed: at most, in all
-    const int32_t *table;      // packed: their number, then (sequence, block) of each, longest first
+    const int32_t *table;      // packed: their number, then (sequence, block) of each, longest first; or nullptr
     float scale;
     int causal;
     uint16_t *out;
@@ -70,17 +70,23 @@ struct PageArgs {
     int64_t *slots, *cu, *len_out, *granted, *count_out;
     int64_t N, max_pages, stack, tokens;
     int shift;                 // log2 of the page size
-    int64_t *have;             // workspace: [1] pages on the stack once all are back
-    int64_t *base;             // workspace: [N] pages that the requests before take; before that, that they give
+    // workspace
+    int64_t *have;             // [2] pages on the stack once all are back, and before
+    int64_t *base, *back;      // [N], [N + 1] pages that the requests before one take, and give back
 };
 
 }  // namespace kda
 
-// Queries per workgroup of the forward: the caller's table is made for them.
-int kda_latent_block(int64_t B, int64_t T, int64_t H);
-// The table of a packed batch: blocks of `size` queries (or keys, with by_keys) of every sequence, those with the
-// most tiles first.  table: int32 [2 + 2 blocks].
-hipError_t kda_launch_latent_table(const kda::LatentArgs &a, int size, int by_keys, int32_t *table, hipStream_t s);
+// Queries per workgroup of the forward (128 or 256), by which its table is made.
+int kda_latent_block(int64_t B, int64_t T, int64_t H, int64_t seqs);
+// Whether the workgroups (units: blocks times heads) of a packed batch count through its
+// sequences themselves: one launch less where they all run at once, so that it does not matter which
+// comes first (1000 tokens in 7 sequences x 32 heads: 31 -> 24 us).
+bool kda_latent_counted(int64_t seqs, int64_t units);
+// The tables of a packed batch: blocks of `size` queries and (where keys is given) keys of
+// every sequence, those with the most tiles first.  int32 [2 + 2 blocks].
+hipError_t kda_launch_latent_table(const kda::LatentArgs &a, int size, int32_t *queries, int64_t q_blocks, int32_t *keys,
+                                   int64_t k_blocks, hipStream_t s);
 hipError_t kda_launch_latent_fwd(const kda::LatentArgs &a, int block, hipStream_t s);
 // The gradient: dq and `stat`, then dkv and the heads' parts of dk_pe, then their sum.
 constexpr int kLatentBwdBlock = 128;  // queries or keys per workgroup

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(LatentArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
     Span sp;
-    if (!span_of(a, unit / a.H, a.causal, sp)) return;
+    if (!span_of<kBlock, false>(a, unit / a.H, a.causal, sp)) return;
     const int q_first = sp.block * kBlock + wave * 32;
     const int block_last = min(sp.lq, (sp.block + 1) * kBlock) - 1;
     if (block_last < sp.block * kBlock) return;
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
     Span sp;
-    if (!span_of(a, unit / a.H, false, sp)) return;
+    if (!span_of<kBlock, true>(a, unit / a.H, false, sp)) return;
     if (sp.block * kBlock >= sp.lk) return;
     const int k_first = sp.block * kBlock + wave * 32;
     // The first query that sees key j, and with it all behind it.

@@ -164,23 +164,50 @@ __device__ __forceinline__ void bounds_of(const int64_t *cu, int64_t n, int64_t 
     len = (int)(hi - lo);
 }
 
-// The sequence and block of unit e (a workgroup's number over the heads); false where there is none.
+// The sequence and block of unit e (a workgroup's number over the heads); false where
+// there is none.  size: tokens of a block, of the keys with BY_KEYS, else of the queries;
+// reversed: the last blocks, which see the most, come first.  Without a table the blocks
+// of a packed batch (of at most 64 sequences) are counted through by the wave.
+template <int SIZE, bool BY_KEYS>
 __device__ __forceinline__ bool span_of(const LatentArgs &a, int64_t e, bool reversed, Span &s) {
-    if (a.table) {
-        if (e >= a.table[0]) return false;
-        const int64_t n = a.table[2 + 2 * e];
-        s.block = a.table[3 + 2 * e];
-        bounds_of(a.cu, n, a.T, s.q0, s.lq);
-        bounds_of(a.cuk, n, a.Tk, s.k0, s.lk);
-        s.b = 0;
-    } else {
+    if (!a.cu) {
         s.b = e % a.B;
         s.block = (int)(e / a.B);
         if (reversed) s.block = (int)a.blocks - 1 - s.block;
         s.q0 = s.k0 = 0;
         s.lq = (int)a.T;
         s.lk = (int)a.Tk;
+        return true;
     }
+    int64_t n;
+    if (a.table) {
+        if (e >= a.table[0]) return false;
+        n = a.table[2 + 2 * e];
+        s.block = a.table[3 + 2 * e];
+    } else {
+        const int lane = threadIdx.x & 63;
+        int blocks = 0;
+        if (lane < a.seqs) {
+            int64_t first;
+            int len;
+            bounds_of(BY_KEYS ? a.cuk : a.cu, lane, BY_KEYS ? a.Tk : a.T, first, len);
+            blocks = (len + SIZE - 1) / SIZE;
+        }
+        int upto = blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
+        }
+        const uint64_t behind = __builtin_amdgcn_ballot_w64(upto > e);
+        if (behind == 0) return false;
+        n = __builtin_ctzll(behind);
+        s.block = __builtin_amdgcn_readlane(upto, (int)n) - 1 - (int)e;  // from the sequence's end
+        if (!reversed) s.block = __builtin_amdgcn_readlane(blocks, (int)n) - 1 - s.block;
+    }
+    bounds_of(a.cu, n, a.T, s.q0, s.lq);
+    bounds_of(a.cuk, n, a.Tk, s.k0, s.lk);
+    s.b = 0;
     return true;
 }
 

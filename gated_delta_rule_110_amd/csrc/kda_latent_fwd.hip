@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
     Span sp;
-    if (!span_of(a, unit / a.H, a.causal, sp)) return;
+    if (!span_of<kBlock, false>(a, unit / a.H, a.causal, sp)) return;
     const int q_first = sp.block * kBlock + wave * 32;  // of this wave
     const int block_last = min(sp.lq, (sp.block + 1) * kBlock) - 1;
     if (block_last < sp.block * kBlock) return;
@@ -335,7 +335,8 @@ struct TableArgs {
     int size, by_keys, causal;
     int32_t *table;
 };
-__global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs a) {
+__global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs by_queries, TableArgs by_keys) {
+    const TableArgs &a = blockIdx.x == 0 ? by_queries : by_keys;
     __shared__ int count[kBuckets];
     __shared__ int most, part[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -417,13 +418,22 @@ __global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs a) {
 
 using namespace kda;
 
-hipError_t kda_launch_latent_table(const LatentArgs &a, int size, int by_keys, int32_t *table, hipStream_t s) {
-    TableArgs t{a.cu, a.cuk, a.T, a.Tk, a.seqs, a.blocks, size, by_keys, a.causal, table};
-    hipLaunchKernelGGL(latent_table_kernel, dim3(1), dim3(1024), 0, s, t);
+bool kda_latent_counted(int64_t seqs, int64_t units) { return seqs <= 64 && units <= 1024; }
+
+hipError_t kda_launch_latent_table(const LatentArgs &a, int size, int32_t *queries, int64_t q_blocks, int32_t *keys, int64_t k_blocks,
+                                   hipStream_t s) {
+    const TableArgs q{a.cu, a.cuk, a.T, a.Tk, a.seqs, q_blocks, size, 0, a.causal, queries};
+    const TableArgs k{a.cu, a.cuk, a.T, a.Tk, a.seqs, k_blocks, size, 1, a.causal, keys};
+    hipLaunchKernelGGL(latent_table_kernel, dim3(keys ? 2 : 1), dim3(1024), 0, s, q, k);
     return hipGetLastError();
 }
 
-int kda_latent_block(int64_t B, int64_t T, int64_t H) { (void)B; (void)T; (void)H; return getenv("KDA_QT") && getenv("KDA_QT")[0] == '2' ? 256 : 128; }
+// With eight waves half as much is copied into LDS, but blocks are twice as long: 4096
+// and 8192 tokens x 32 heads 178 and 609 us (with four waves 187 and 621); 16384 x 4 heads, 256
+// workgroups, 437 (387); 16 sequences of 512 x 32 heads 101 (96).
+int kda_latent_block(int64_t B, int64_t T, int64_t H, int64_t seqs) {
+    return T * B / seqs >= 2048 && (T + 255) / 256 * B * H >= 512 ? 256 : 128;
+}
 
 hipError_t kda_launch_latent_fwd(const LatentArgs &a, int block, hipStream_t s) {
     const int64_t units = a.blocks * a.B * a.H;

@@ -308,12 +308,17 @@ def page_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: to
     sizes = {"slots": tokens, "cu_seqlens": N + 1, "lengths": N, "granted": N, "free_count": 1}
     given = outputs or {}
     res = {k: _output(given[k], k, (n,), torch.int64, dev) for k, n in sizes.items() if given.get(k) is not None}
-    need = [k for k in sizes if k not in res]
-    if need:  # one allocation for all of them
-        parts = torch.empty(sum(sizes[k] for k in need), dtype=torch.int64, device=dev).split([sizes[k] for k in need])
-        res.update(zip(need, parts))
     lib = _library()
-    ws = _workspace(workspace, lib.kda_page_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    need = [k for k in sizes if k not in res]
+    if workspace is None:  # one allocation for it and all outputs that are not given
+        words = lib.kda_page_workspace_size(d) // 8
+        buf = torch.empty(words + sum(sizes[k] for k in need), dtype=torch.int64, device=dev)
+        d.workspace, d.workspace_bytes = buf.data_ptr(), 8 * words
+        parts = buf.split([words] + [sizes[k] for k in need])
+        res.update(zip(need, parts[1:]))
+    else:
+        _workspace(workspace, lib.kda_page_workspace_size(d), dev, d)
+        res.update((k, torch.empty(sizes[k], dtype=torch.int64, device=dev)) for k in need)
     _call(lib.kda_page_assign, dev, lengths.data_ptr(), new_tokens.data_ptr(), _ptr(ended), block_table.data_ptr(),
           free_pages.data_ptr(), free_count.data_ptr(), *[res[k].data_ptr() for k in sizes], d)
     return {k: res[k] for k in sizes}
