@@ -39,6 +39,20 @@ __device__ __forceinline__ s8 operand_of(const uint32_t (&w)[8], int s) {
     return __builtin_bit_cast(s8, v);
 }
 
+// S and dP go to ordinary registers, where the vector instructions take them, while the
+// sums over all pairs stay in the accumulator half of the file: the compiler, which uses
+// one half for all products of a kernel, would move 128 values a tile.  What it does not
+// see is that results are there some 11 issue slots after the last product only: between a
+// unit's first products and their first use lie the 12 or 20 products of its sums, or
+// products_done.
+__device__ __forceinline__ void first_product(f16v &d, const s8 &a, const s8 &b) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void add_product(f16v &d, const s8 &a, const s8 &b) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void products_done() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+
 // ---- dq -----------------------------------------------------------------------------
 
 constexpr int kStages = 3;  // tiles in LDS: two in use, one on its way
@@ -86,10 +100,7 @@ __device__ __forceinline__ void dq_unit(DqState &f, const DqAddr &at, int buf, i
     s8 ring[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) ring[(kFirst + n) % kAhead] = operand(kFirst + n);
-    if (NEXT) {
-        s2 = zero16();
-        dp2 = zero16();
-    } else {
+    if (!NEXT) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) pair(i);
     }
@@ -99,8 +110,10 @@ __device__ __forceinline__ void dq_unit(DqState &f, const DqAddr &at, int buf, i
         const s8 a = ring[n % kAhead];
         const int m = n - kSdSlots;
         if (m >= 0) f.dq[m % (kQk / 32)] = mfma32(a, operand_of(w.e, m / (kQk / 32)), f.dq[m % (kQk / 32)]);
-        else if (is_s(n)) s2 = mfma32(a, f.q[sd_block(n)], s2);
-        else dp2 = mfma32(a, f.y[sd_block(n)], dp2);
+        else if (n == 0) first_product(s2, a, f.q[0]);
+        else if (n == 1) first_product(dp2, a, f.y[0]);
+        else if (is_s(n)) add_product(s2, a, f.q[sd_block(n)]);
+        else add_product(dp2, a, f.y[sd_block(n)]);
         if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
         if (NEXT && n < 16) pair(n);
         __builtin_amdgcn_sched_barrier(0);
@@ -186,17 +199,21 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(LatentArgs a) {
     if (tiles > 0) copies_done();
     if (mine > 0) {
         f16v s0, d0, s1, d1;
-        s0 = d0 = zero16();
 #pragma unroll
         for (int n = 0; n < kSdSlots; ++n) {
             const int ks = sd_block(n);
-            if (is_s(n))
-                s0 = mfma32(ks < kNope / 16 ? row_operand<2 * kNope>(at.kn, 0, ks) : row_operand<2 * kPe>(at.kp, 0, ks - kNope / 16),
-                            f.q[ks], s0);
-            else
-                d0 = mfma32(row_operand<2 * kVal>(at.v, 0, ks), f.y[ks], d0);
+            if (is_s(n)) {
+                const s8 x = ks < kNope / 16 ? row_operand<2 * kNope>(at.kn, 0, ks) : row_operand<2 * kPe>(at.kp, 0, ks - kNope / 16);
+                if (n == 0) first_product(s0, x, f.q[ks]);
+                else add_product(s0, x, f.q[ks]);
+            } else {
+                const s8 x = row_operand<2 * kVal>(at.v, 0, ks);
+                if (n == 1) first_product(d0, x, f.y[ks]);
+                else add_product(d0, x, f.y[ks]);
+            }
             if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
+        products_done();
         int st = 0;
         for (; t < mine - 1; ++t) {
             const int next = st == kStages - 1 ? 0 : st + 1;
@@ -287,10 +304,7 @@ __device__ __forceinline__ void dkv_unit(DkvState &f, const DkvAddr &at, int st,
     s8 ring[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) ring[(kFirst + n) % kAhead] = operand(kFirst + n);
-    if (NEXT) {
-        s2 = zero16();
-        dp2 = zero16();
-    } else {
+    if (!NEXT) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) prob(i);
     }
@@ -304,10 +318,13 @@ __device__ __forceinline__ void dkv_unit(DkvState &f, const DkvAddr &at, int st,
             f.dk[x % (kQk / 32)] = mfma32(a, operand_of(w.e, x / (kQk / 32)), f.dk[x % (kQk / 32)]);
         } else if (m >= 0) {
             f.dv[m % (kVal / 32)] = mfma32(a, operand_of(w.p, m / (kVal / 32)), f.dv[m % (kVal / 32)]);
+        } else if (n < 2) {
+            if (n == 0) first_product(s2, a, f.k[0]);
+            else first_product(dp2, a, f.v[0]);
         } else if (is_s(n)) {
-            s2 = mfma32(a, f.k[sd_block(n)], s2);
+            add_product(s2, a, f.k[sd_block(n)]);
         } else {
-            dp2 = mfma32(a, f.v[sd_block(n)], dp2);
+            add_product(dp2, a, f.v[sd_block(n)]);
         }
         if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
         if (NEXT && n < 16) prob(n);
@@ -395,18 +412,23 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentArgs a) {
     if (first < tiles) {
         f16v s0, d0, s1, d1;
         copies_done();
-        s0 = d0 = zero16();
         int st = first % kStages;
 #pragma unroll
         for (int n = 0; n < kSdSlots; ++n) {
             const int ks = sd_block(n);
             const uint32_t qn = at.qn + st * (uint32_t)sizeof(sm.qn[0]), qp = at.qp + st * (uint32_t)sizeof(sm.qp[0]);
-            if (is_s(n))
-                s0 = mfma32(ks < kNope / 16 ? row_operand<2 * kNope>(qn, 0, ks) : row_operand<2 * kPe>(qp, 0, ks - kNope / 16), f.k[ks], s0);
-            else
-                d0 = mfma32(row_operand<2 * kVal>(at.y + st * (uint32_t)sizeof(sm.y[0]), 0, ks), f.v[ks], d0);
+            if (is_s(n)) {
+                const s8 x = ks < kNope / 16 ? row_operand<2 * kNope>(qn, 0, ks) : row_operand<2 * kPe>(qp, 0, ks - kNope / 16);
+                if (n == 0) first_product(s0, x, f.k[ks]);
+                else add_product(s0, x, f.k[ks]);
+            } else {
+                const s8 x = row_operand<2 * kVal>(at.y + st * (uint32_t)sizeof(sm.y[0]), 0, ks);
+                if (n == 1) first_product(d0, x, f.v[ks]);
+                else add_product(d0, x, f.v[ks]);
+            }
             if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
+        products_done();
         for (int t = first; t < tiles - 1; ++t) {
             const int next = st == kStages - 1 ? 0 : st + 1;
             copies_done();  // tile t + 1 is there, and tile t - 1 read
