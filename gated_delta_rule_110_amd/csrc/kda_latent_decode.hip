@@ -7,8 +7,9 @@
 // 64 rows the cache's bytes are the bound, beyond that they come from L2.
 //
 // Steps (32 cached rows of one row tile) of all sequences are lined up and shared out
-// evenly among 256 workgroups, one a CU, whatever the lengths: each computes the line
-// from the lengths, so that no plan has to be made on the host or launched ahead.  A
+// evenly among 256 workgroups, one a CU, whatever the lengths (with an allowance for the
+// changes from one row tile to the next): each computes the line from the lengths, so that
+// no plan has to be made on the host or launched ahead.  A
 // row tile that ends up in several workgroups is joined by a second kernel from their
 // fp32 accumulators, maxima and sums.
 //
@@ -20,6 +21,7 @@
 // the LDS reads.)  The table's entries are copied into LDS two steps ahead of the rows.
 //
 // Precision: as in the expanded form, probabilities are rounded to bf16, all else is fp32.
+#include <type_traits>
 #include "kda_latent_common.h"
 
 namespace kda {
@@ -40,8 +42,9 @@ struct DecodeSmem {
     float top[2][64], sum[2][2][64];           // [half of the keys][row]; of two segments
     int rise[2];
     int64_t wave_sum[8];
-    int64_t begin_rest;
-    int begin_n, begin_len;
+    int wave_tiles[8];
+    int64_t begin_rest, real[2];               // steps of all workgroups ahead of this one's, and with it
+    int begin_n, begin_len, uneven;
 };
 
 // Chunk c of row r lies at place c ^ place(r) of its 128 bytes: reads of 16 bytes of 16
@@ -153,60 +156,109 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t w = blockIdx.x;
 
-    // The line of steps: sequence after sequence, row tile after row tile.  Thread t sums
-    // up an even share of the sequences.
+    // The line of steps: sequence after sequence, row tile after row tile.  Thread t sums up an even
+    // share of the sequences.
     const int64_t share = (a.N + 511) / 512, n0 = min(a.N, tid * share), n1 = min(a.N, n0 + share);
-    const auto steps_of = [&](int64_t n) {
-        return (clamp64(a.len[n], 0, a.max_pages << a.page_shift) + kStep - 1) / kStep * a.row_tiles;
-    };
+    const auto length = [&](int64_t n) { return clamp64(a.len[n], 0, a.max_pages << a.page_shift); };
+    const auto steps_of = [&](int64_t n) { return (length(n) + kStep - 1) / kStep; };  // a row tile's, below 2^26
     int64_t sum = 0;
+    int tiles = 0;
     for (int64_t n = n0; n < n1; ++n) {
         const int64_t t = steps_of(n);
-        sum += t;
-        if (t == 0 && w == 0)
+        sum += t * a.row_tiles;
+        if (t > 0) tiles += (int)a.row_tiles;
+        else if (w == 0)
             for (int64_t r = 0; r < a.row_tiles; ++r) a.seg[2 * (n * a.row_tiles + r)] = -2;
     }
     int64_t upto = sum;
+    int tiles_upto = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int64_t o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
+        const int p = __shfl_up(tiles_upto, d);
+        if (lane >= d) {
+            upto += o;
+            tiles_upto += p;
+        }
     }
-    if (lane == 63) sm.wave_sum[wave] = upto;
+    if (lane == 63) {
+        sm.wave_sum[wave] = upto;
+        sm.wave_tiles[wave] = tiles_upto;
+    }
     if (tid < 2) sm.rise[tid] = 0;
+    if (tid == 0) sm.uneven = 0;
     __syncthreads();
     int64_t total = 0;
+    int all_tiles = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (i < wave) upto += sm.wave_sum[i];
-        total += sm.wave_sum[i];
-    }
-    const int64_t per = (total + a.groups - 1) / a.groups;
-    const int64_t first = w * per;
-    const int64_t mine = min(total, first + per) - first;
-    if (mine <= 0) return;
-    if (upto - sum <= first && first < upto) {
-        int64_t at = upto - sum, n = n0;
-        for (;; ++n) {
-            const int64_t t = steps_of(n);
-            if (first < at + t) break;
-            at += t;
+        if (i < wave) {
+            upto += sm.wave_sum[i];
+            tiles_upto += sm.wave_tiles[i];
         }
-        sm.begin_n = (int)n;
-        sm.begin_len = (int)clamp64(a.len[n], 0, a.max_pages << a.page_shift);
-        sm.begin_rest = first - at;
+        total += sm.wave_sum[i];
+        all_tiles += sm.wave_tiles[i];
+    }
+    // A change to other queries within a workgroup takes about as long as kChange steps: where any has
+    // one, as many units without work lie ahead of every row tile (12 sequences of up to 15000 rows x 64: 54
+    // -> 44 us; where none has, as with two row tiles of 4096 steps, the units would make it 33 steps a
+    // workgroup instead of 32, 66 -> 70 us).
+    constexpr int kChange = R == 1 ? 3 : 5;
+    {
+        const uint32_t even = (uint32_t)((total + a.groups - 1) / a.groups);
+        for (int64_t n = n0; n < n1; ++n)
+            if ((uint32_t)steps_of(n) % even != 0) sm.uneven = 1;
     }
     __syncthreads();
-    const int count = __builtin_amdgcn_readfirstlane((int)mine);
+    const int change = sm.uneven ? kChange : 0;
+    const int64_t ahead = upto - sum + (int64_t)(tiles_upto - tiles) * change;
+    upto += (int64_t)tiles_upto * change;
+    total += (int64_t)all_tiles * change;
+    const int64_t per = (total + a.groups - 1) / a.groups;
+    const int64_t first = w * per, behind = min(total, first + per);
+    if (first >= behind) return;
+    // A point of the line: its sequence, how far it lies in it, and the steps ahead of it.
+    const auto locate = [&](int64_t point, int64_t &n, int64_t &rest) {
+        int64_t at = ahead, before = tiles_upto - tiles, t;
+        for (n = n0;; ++n) {
+            t = steps_of(n);
+            const int64_t u = t > 0 ? (t + change) * a.row_tiles : 0;
+            if (point < at + u) break;
+            at += u;
+            if (u > 0) before += a.row_tiles;
+        }
+        rest = point - at;
+        const int64_t unit = t + change, rt = rest >> 32 ? rest / unit : (uint32_t)rest / (uint32_t)unit;
+        return point - (before + rt) * change - min(rest - rt * unit, (int64_t)change);
+    };
+    if (ahead <= first && first < upto) {
+        int64_t n, rest;
+        sm.real[0] = locate(first, n, rest);
+        sm.begin_n = (int)n;
+        sm.begin_len = (int)length(n);
+        sm.begin_rest = rest;
+    }
+    if (ahead <= behind && behind < upto) {
+        int64_t n, rest;
+        sm.real[1] = locate(behind, n, rest);
+    }
+    if (tid == 0 && behind == total) sm.real[1] = total - (int64_t)all_tiles * change;
+    __syncthreads();
+    const int count = __builtin_amdgcn_readfirstlane((int)(sm.real[1] - sm.real[0]));
+    if (count == 0) return;
     Cursor at;
     at.n = __builtin_amdgcn_readfirstlane(sm.begin_n);
     at.len = __builtin_amdgcn_readfirstlane(sm.begin_len);
     at.steps = (at.len + kStep - 1) / kStep;
+    int64_t begin_unit;  // where this workgroup's first step stands in the line
     {
         const int64_t rest = sm.begin_rest;
-        const int rt = rest >> 32 ? (int)(rest / at.steps) : (int)((uint32_t)rest / (uint32_t)at.steps);  // below 2^24 / 32
+        const int unit = at.steps + change;
+        const int rt = rest >> 32 ? (int)(rest / unit) : (int)((uint32_t)rest / (uint32_t)unit);
+        const int within = (int)(rest - (int64_t)rt * unit);
         at.rt = __builtin_amdgcn_readfirstlane(rt);
-        at.t = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)rt * at.steps));
+        at.t = __builtin_amdgcn_readfirstlane(max(0, within - change));
+        begin_unit = first + max(0, change - within);
     }
 
     const uint32_t rows = (uint32_t)(a.T * a.H), H = (uint32_t)a.H;
@@ -221,28 +273,23 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
     // The first two steps' copies, and the next two's entries: here every thread reads its row's.
     const int my_row = 8 * (wave & 3) + (lane >> 3);
     Cursor copy = at, look = at;
-    {
-        int32_t page[4];
+    int32_t page[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            page[i] = 0;
-            if (i < count) {
-                page[i] = a.table[look.n * a.max_pages + (min(look.t * kStep + my_row, look.len - 1) >> a.page_shift)];
-                advance(a, look);
-            }
+    for (int i = 0; i < 4; ++i) {
+        page[i] = 0;
+        if (i < count) {
+            page[i] = a.table[look.n * a.max_pages + (min(look.t * kStep + my_row, look.len - 1) >> a.page_shift)];
+            advance(a, look);
         }
-        const uint32_t to = lds + (wave & 3) * 1024;
+    }
+    const auto first_copies = [&](auto even) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (i < count) {
-                if (wave < 4) copy_step<true>(a, copy, page[i], my_row, lane & 7, to + i * (uint32_t)sizeof(sm.row[0]));
-                else copy_step<false>(a, copy, page[i], my_row, lane & 7, to + i * (uint32_t)sizeof(sm.row[0]));
+                copy_step<decltype(even)::value>(a, copy, page[i], my_row, lane & 7, lds + (wave & 3) * 1024 + i * (uint32_t)sizeof(sm.row[0]));
                 advance(a, copy);
             }
-        if (wave < 4 && (lane & 7) == 0)
-#pragma unroll
-            for (int i = 2; i < 4; ++i) sm.entry[i][my_row] = page[i];
-    }
+    };
 
     // Probabilities use the maximum that is in use, which may stay 2^40 behind the true one
     // (bf16 has fp32's exponents, so that nothing is lost): only a larger step, as at a segment's
@@ -251,15 +298,36 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
 
     if (wave < 4) {
         // ---- scores: 16 keys and 16 R rows a wave --------------------------------------
-        Feed<true> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
         const int kg = wave >> 1, r0 = (wave & 1) * 16 * R;
         const uint32_t at_k = lds + (kg * 16 + n16) * 128 + ((g16 ^ place(n16)) << 4);
         s8 q[R][kRow / 32];
         int seen[R], all_see = 0, segment = 0;
         float m[R], l[R];
-        bool fresh = true;
-        if (count > 1) arrive<kEvenCopies>();
-        else arrive<0>();
+        const auto begin_segment = [&]() {
+            all_see = seen_by(at, 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t x = min((uint32_t)(at.rt * R * 32 + r0 + 16 * r + n16), rows - 1), tok = x / H, head = x - tok * H;
+                seen[r] = seen_by(at, r0 + 16 * r + n16);
+                m[r] = -INFINITY;
+                l[r] = 0.0f;
+                const uint16_t *ql = a.ql + at.n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + 8 * g16;
+                const uint16_t *qp = a.qp + at.n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + 8 * g16;
+#pragma unroll
+                for (int ks = 0; ks < kRow / 32; ++ks)
+                    q[r][ks] = ks < kLat / 32 ? *reinterpret_cast<const s8 *>(ql + 32 * ks)
+                                              : *reinterpret_cast<const s8 *>(qp + 32 * ks - kLat);
+            }
+        };
+        // The first segment's queries come with the first copies, and ahead of them.
+        begin_segment();
+        first_copies(std::true_type());
+        if ((lane & 7) == 0)
+#pragma unroll
+            for (int i = 2; i < 4; ++i) sm.entry[i][my_row] = page[i];
+        Feed<true> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
+        bool fresh = false;
+        arrive<0>();
 #pragma unroll 1
         for (int i = 0; i <= count; ++i) {
             feed.ahead(a, sm, i, count, tid);
@@ -286,22 +354,9 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
             };
             if (i < count) {
                 if (fresh) {
-                    all_see = seen_by(at, 0);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const uint32_t x = min((uint32_t)(at.rt * R * 32 + r0 + 16 * r + n16), rows - 1), tok = x / H, head = x - tok * H;
-                        seen[r] = seen_by(at, r0 + 16 * r + n16);
-                        m[r] = -INFINITY;
-                        l[r] = 0.0f;
-                        const uint16_t *ql = a.ql + at.n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + 8 * g16;
-                        const uint16_t *qp = a.qp + at.n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + 8 * g16;
-#pragma unroll
-                        for (int ks = 0; ks < kRow / 32; ++ks)
-                            q[r][ks] = ks < kLat / 32 ? *reinterpret_cast<const s8 *>(ql + 32 * ks)
-                                                      : *reinterpret_cast<const s8 *>(qp + 32 * ks - kLat);
-                    }
                     // Waited for here, once a segment: at their uses, every step would wait, and with
                     // them for the copies.
+                    begin_segment();
                     asm volatile("" ::: "memory");
                     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
                     asm volatile("" ::: "memory");
@@ -365,6 +420,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         }
     } else {
         // ---- outputs: 128 values of all rows a wave -------------------------------------
+        first_copies(std::false_type());
         Feed<false> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
         const int ow = wave - 4;
         const int vr = 8 * g + (n16 >> 2);  // keys 8 g .. of every 16, by two reads of 4 keys each
@@ -491,7 +547,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                     }
                     if (lane == 0 && ow == 0 && begins) {
                         a.seg[2 * tile] = ends ? -1 : (int32_t)slot;
-                        a.seg[2 * tile + 1] = (int32_t)((first + begin + at.steps - 1) / per);
+                        a.seg[2 * tile + 1] = (int32_t)((begin_unit + begin + (int64_t)segment * change + at.steps - 1) / per);
                     }
                     reset();
                     begin = i;

@@ -153,6 +153,29 @@ def test_strides_and_broadcasts():
     R.within(small.grad, d(each).sum(0, keepdim=True), R.HALF * d(each).sum(0, keepdim=True).abs() + 1e-30, "broadcast kv")
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_long_sequences(packed):
+    """Sizes at which a workgroup takes 256 queries: every head's bits are those of the head alone, which has 128, and
+    hidden values that are not finite stay where they are."""
+    T, H = 2100, 64
+    lens = [T + 30, T - 30] if packed else [T]
+    say("case latent long packed=%s" % packed)
+    a = make(1, sum(lens), sum(lens), H, seed=17)
+    cu = cu_of(lens) if packed else None
+    a["kv"][0, T - 60, 5, 130] = float("nan")
+    a["kv"][0, T - 70, 63, 3] = float("inf")
+    out, lse = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, True, cu)
+    for h in (0, 5, 31, 63):
+        q, kv = a["q"][:, :, h:h + 1].contiguous(), a["kv"][:, :, h:h + 1].contiguous()
+        one = kda.latent_fwd(q, kv, a["k_pe"], SCALE, True, cu)
+        same({"out": out[:, :, h:h + 1].contiguous(), "lse": lse[:, :, h:h + 1].contiguous()}, {"out": one[0], "lse": one[1]})
+    assert out[0, :, 5, 2].isnan().nonzero().flatten().tolist() == list(range(T - 60, lens[0]))
+    f = lambda t: d(t)[0]  # noqa: E731
+    ref = R.attention(f(a["q"][:, :, 31:32]), f(a["kv"][:, :, 31:32]), f(a["k_pe"]), SCALE, True, lens, lens)
+    R.within(out[0, :, 31:32], ref["out"], ref["tol_out"], "out")
+    R.within(lse[0, :, 31:32], ref["lse"], ref["tol_lse"], "lse")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("where", ["k", "v", "pe"])
 def test_hidden_special_values(where, bad):

@@ -59,6 +59,16 @@ def test_decode(lengths, T, H, page):
     check(a, run(a), "decode")
 
 
+@pytest.mark.parametrize("lengths,T,H", [
+    ([1024] * 16, 1, 32), ([2048, 1024, 0, 1024], 2, 40),                 # row tiles of even shares: none begins within one
+    ([6000, 4, 0, 2500, 33, 31, 4000], 4, 16), ([3000, 1, 1, 2900], 1, 32),  # several begin within a share
+    ([(37 * i) % 90 for i in range(700)], 1, 3), ([(61 * i) % 200 for i in range(600)], 2, 40)])
+def test_decode_shares(lengths, T, H):
+    say("case decode shares %s.. T=%d H=%d" % (lengths[:6], T, H))
+    a = make(lengths, T, H, 32, seed=9)
+    check(a, run(a), "shares")
+
+
 def test_decode_tokens_without_keys():
     a = make([2, 0, 5], 4, 8, 16, seed=1)
     out, lse = run(a)
