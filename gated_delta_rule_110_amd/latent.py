@@ -314,8 +314,7 @@ def page_assign(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: to
         words = lib.kda_page_workspace_size(d) // 8
         buf = torch.empty(words + sum(sizes[k] for k in need), dtype=torch.int64, device=dev)
         d.workspace, d.workspace_bytes = buf.data_ptr(), 8 * words
-        parts = buf.split([words] + [sizes[k] for k in need])
-        res.update(zip(need, parts[1:]))
+        res.update(zip(need, buf.split_with_sizes([words] + [sizes[k] for k in need])[1:]))
     else:
         _workspace(workspace, lib.kda_page_workspace_size(d), dev, d)
         res.update((k, torch.empty(sizes[k], dtype=torch.int64, device=dev)) for k in need)
