@@ -214,8 +214,7 @@ extern "C" kda_status_t kda_latent_bwd(const void *q, const void *kv, const void
         a.table = qt;
         k.table = kt;
     }
-    if (e == hipSuccess) e = kda_launch_latent_dq(a, stream);
-    if (e == hipSuccess) e = kda_launch_latent_dkv(k, stream);
+    if (e == hipSuccess) e = kda_launch_latent_pairs(a, k, stream);
     if (e == hipSuccess) e = kda_launch_latent_dpe(k, stream);
     return of_hip(e);
 }

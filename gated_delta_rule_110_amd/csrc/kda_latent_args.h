@@ -88,10 +88,10 @@ bool kda_latent_counted(int64_t seqs, int64_t units);
 hipError_t kda_launch_latent_table(const kda::LatentArgs &a, int size, int32_t *queries, int64_t q_blocks, int32_t *keys,
                                    int64_t k_blocks, hipStream_t s);
 hipError_t kda_launch_latent_fwd(const kda::LatentArgs &a, int block, hipStream_t s);
-// The gradient: dq and `stat`, then dkv and the heads' parts of dk_pe, then their sum.
+// The gradient: dq and `stat`, dkv and the heads' parts of dk_pe (q, k: the passes' blocks and
+// tables); then their sum.
 constexpr int kLatentBwdBlock = 128;  // queries or keys per workgroup
-hipError_t kda_launch_latent_dq(const kda::LatentArgs &a, hipStream_t s);
-hipError_t kda_launch_latent_dkv(const kda::LatentArgs &a, hipStream_t s);
+hipError_t kda_launch_latent_pairs(const kda::LatentArgs &q, const kda::LatentArgs &k, hipStream_t s);
 hipError_t kda_launch_latent_dpe(const kda::LatentArgs &a, hipStream_t s);
 // The absorbed form: the workgroups' parts, then their joining.
 constexpr int64_t kLatentGroups = 256;

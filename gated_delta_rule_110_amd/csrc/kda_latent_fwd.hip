@@ -9,6 +9,12 @@
 // copies straight into LDS, two tiles of each, and the scores of tile j + 1 are
 // computed beside the exponentials of tile j.
 //
+// The matrix instructions bound it: 8192 tokens x 32 heads take 598 us, 1.15 PFLOP/s, and a
+// stream of nothing but those instructions 538.  Both are held by the card's power, which
+// lowers the clock (1.7 GHz here, where they fill 64% of the cycles), so that every LDS read
+// and vector instruction costs time although there are slots for it: without exponentials
+// the kernel took 26 us less, without LDS reads 70 and without copies 84 (of 715).
+//
 // Precision: scores, maxima, sums and outputs are fp32.  Probabilities are rounded to
 // bf16 for the second product (2^-9 of each; the outputs' own rounding is as large);
 // the sum, and with it lse, takes them unrounded.

@@ -258,6 +258,21 @@ def test_launch_pieces_and_repeats():
     same(run(b, True, cu_of(lens), launch_piece=1), want)
 
 
+@pytest.mark.parametrize("lens", [[1300], [900, 0, 1, 399]])
+def test_gradient_in_one_and_in_two_launches(lens):
+    """Many blocks take a launch of queries and one of keys, few of them one launch for both: the same bits."""
+    H = 16
+    say("case latent gradient of %s x %d heads" % (lens, H))
+    a = make(1, sum(lens), sum(lens), H, seed=18)
+    cu = cu_of(lens) if len(lens) > 1 else None
+    res = run(a, True, cu)
+    check(a, res, True, lens, lens, "many")
+    for h in (0, 7, 15):
+        one = {k: (v if k == "k_pe" else v[:, :, h:h + 1].contiguous()) for k, v in a.items()}
+        got = run(one, True, cu)
+        same({k: got[k] for k in ("out", "lse", "dq", "dkv")}, {k: res[k][:, :, h:h + 1].contiguous() for k in ("out", "lse", "dq", "dkv")})
+
+
 def test_many_short_sequences():
     n = 3000
     lens = [(7 * i) % 5 for i in range(n)]
