@@ -80,13 +80,48 @@ kda_status_t table_bytes(int64_t blocks, size_t &bytes) {
     return KDA_OK;
 }
 
+struct LatentFwdPlan {
+    int block, part_tiles;
+    int64_t blocks, parts;
+    size_t off_stat, off_part, total;
+};
+// Few blocks with many keys leave CUs idle: their keys are split into parts, of at least
+// kPartTiles tiles, so that there are some 256 workgroups, and joined by a second kernel
+// (512 tokens x 8 heads over 16384 keys 280 -> 62 us, 2048 x 2 over their own 41 -> 23; with
+// 11 tiles, 700 x 1, they would take 21 instead of 18; 512 workgroups take 6% more or less).
+kda_status_t plan_latent_fwd(const kda_latent_desc_t *d, bool packed, LatentFwdPlan &p) {
+    constexpr int64_t kPartTiles = 8, kFewTiles = 12, kFewUnits = 128, kUnits = 256;
+    p = LatentFwdPlan{};
+    p.block = kda_latent_block(d->B, d->T, d->H, d->num_seqs);
+    p.blocks = blocks_of(d->T, p.block, d->num_seqs, packed);
+    p.parts = 1;
+    if (packed) {
+        const kda_status_t st = table_bytes(p.blocks, p.off_stat);
+        if (st != KDA_OK) return st;
+    }
+    p.off_part = p.total = p.off_stat;
+    const int64_t units = p.blocks * d->B * d->H, tiles = (d->Tk + kKeys - 1) / kKeys;
+    if (units > kFewUnits || tiles <= kFewTiles) return KDA_OK;
+    const int64_t even = (units * tiles + kUnits - 1) / kUnits;
+    p.part_tiles = (int)(std::max(kPartTiles, even) + 1) / 2 * 2;
+    p.parts = (tiles + p.part_tiles - 1) / p.part_tiles;
+    if (p.parts < 2) return KDA_OK;  // part_tiles may be all of them
+    p.off_part = p.off_stat + align_up((size_t)(units * p.parts) * p.block * 8, 256);
+    p.total = p.off_part + (size_t)(units * p.parts) * p.block * kVal * 4;
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" size_t kda_latent_fwd_workspace_size(const kda_latent_desc_t *desc) {
-    size_t need = 0;
-    if (!desc || check_latent(desc, true) != KDA_OK) return 0;
-    const int block = kda_latent_block(desc->B, desc->T, desc->H, desc->num_seqs);
-    return table_bytes(blocks_of(desc->T, block, desc->num_seqs, true), need) == KDA_OK ? need : 0;
+    size_t best = 0;
+    if (!desc) return 0;
+    for (bool packed : {false, true}) {
+        LatentFwdPlan p;
+        if (check_latent(desc, packed) != KDA_OK || plan_latent_fwd(desc, packed, p) != KDA_OK) continue;
+        best = std::max(best, p.total);
+    }
+    return best;
 }
 
 extern "C" kda_status_t kda_latent_fwd(const void *q, const void *kv, const void *k_pe, const int64_t *cu_seqlens,
@@ -98,33 +133,38 @@ extern "C" kda_status_t kda_latent_fwd(const void *q, const void *kv, const void
     if (desc->T > 0 && !out) return KDA_ERR_NULL;
     if (!aligned(out, 16) || !aligned(lse, 4)) return KDA_ERR_ALIGN;
     const bool packed = cu_seqlens != nullptr;
-    const int block = kda_latent_block(desc->B, desc->T, desc->H, desc->num_seqs);
-    a.blocks = blocks_of(desc->T, block, desc->num_seqs, packed);
-    size_t need = 0;
-    if (packed) st = table_bytes(a.blocks, need);
+    LatentFwdPlan p;
+    st = plan_latent_fwd(desc, packed, p);
     if (st != KDA_OK) return st;
+    a.blocks = p.blocks;
+    a.parts = p.parts;
+    a.part_tiles = p.part_tiles;
     const bool counted = packed && kda_latent_counted(desc->num_seqs, a.blocks * desc->H);
     Memory m;
     latent_reads(m, q, kv, k_pe, cu_seqlens, cu_seqlens_k, desc);
     m.write(out, latent_rows(desc) * kVal * 2);
     m.write(lse, latent_rows(desc) * 4);
-    m.write(desc->workspace, need);
+    m.write(desc->workspace, p.total);
     if (m.clash()) return KDA_ERR_OVERLAP;
     st = validate_cu(cu_seqlens, desc->num_seqs, desc->T, stream);
     if (st == KDA_OK) st = validate_cu(cu_seqlens_k, desc->num_seqs, desc->Tk, stream);
     if (st != KDA_OK) return st;
     if (desc->T == 0) return KDA_OK;
-    Workspace ws(desc->workspace, desc->workspace_bytes, need, stream);
+    Workspace ws(desc->workspace, desc->workspace_bytes, p.total, stream);
     if (ws.status() != KDA_OK) return ws.status();
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     hipError_t e = hipSuccess;
     if (packed && !counted) {
         int32_t *table = reinterpret_cast<int32_t *>(ws.at(0));
-        e = kda_launch_latent_table(a, block, table, a.blocks, nullptr, 0, stream);
+        e = kda_launch_latent_table(a, p.block, table, a.blocks, nullptr, 0, stream);
         a.table = table;
     }
-    if (e == hipSuccess) e = kda_launch_latent_fwd(a, block, stream);
+    if (p.parts > 1) {
+        a.part_stat = reinterpret_cast<float *>(ws.at(p.off_stat));
+        a.part = reinterpret_cast<float *>(ws.at(p.off_part));
+    }
+    if (e == hipSuccess) e = kda_launch_latent_fwd(a, p.block, stream);
     return of_hip(e);
 }
 

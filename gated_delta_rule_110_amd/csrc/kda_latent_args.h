@@ -22,6 +22,11 @@ struct LatentArgs {
     uint16_t *out;
     float *lse;
     int64_t launch_cap, base;  // base: first workgroup of this launch; set by the launcher
+    // forward: parts (1: none) of part_tiles tiles of keys that a block's keys may be split in; what each
+    // leaves of its 128 queries: accumulators, and (maximum, sum)
+    int64_t parts;
+    int part_tiles;
+    float *part, *part_stat;
     // gradient
     const uint16_t *o, *dy;    // out, d_out
     int64_t ob, ot, yb, yt;
@@ -87,6 +92,7 @@ bool kda_latent_counted(int64_t seqs, int64_t units);
 // every sequence, those with the most tiles first.  int32 [2 + 2 blocks].
 hipError_t kda_launch_latent_table(const kda::LatentArgs &a, int size, int32_t *queries, int64_t q_blocks, int32_t *keys,
                                    int64_t k_blocks, hipStream_t s);
+// With parts (blocks of 128 queries only) their joining too.
 hipError_t kda_launch_latent_fwd(const kda::LatentArgs &a, int block, hipStream_t s);
 // The gradient: dq and `stat`, dkv and the heads' parts of dk_pe (q, k: the passes' blocks and
 // tables); then their sum.

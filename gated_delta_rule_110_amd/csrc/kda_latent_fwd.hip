@@ -7,7 +7,8 @@
 // between lanes n and n + 32, and the accumulators, rounded to bf16, are the B operand
 // of O^T += V^T P^T as they stand.  Queries stay in registers, keys and values come by
 // copies straight into LDS, two tiles of each, and the scores of tile j + 1 are
-// computed beside the exponentials of tile j.
+// computed beside the exponentials of tile j.  Where there are few queries, workgroups
+// share a block's keys and a second kernel joins what they leave.
 //
 // The matrix instructions bound it: 8192 tokens x 32 heads take 598 us, 1.15 PFLOP/s, and a
 // stream of nothing but those instructions 538.  Both are held by the card's power, which
@@ -175,14 +176,14 @@ __device__ __forceinline__ void clear_odd(uint16_t *v, int tid, int threads) {
     }
 }
 
-// WAVES of 32 queries each.
-template <int WAVES>
+// WAVES of 32 queries each.  SPLIT: a workgroup takes a part of its block's keys.
+template <int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a) {
     __shared__ __attribute__((aligned(1024))) FwdSmem sm;
     constexpr int kBlock = 32 * WAVES;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t unit = a.base + blockIdx.x, h = unit % a.H;
+    const int64_t place = a.base + blockIdx.x, unit = SPLIT ? place / a.parts : place, h = unit % a.H;
     Span sp;
     if (!span_of<kBlock, false>(a, unit / a.H, a.causal, sp)) return;
     const int q_first = sp.block * kBlock + wave * 32;  // of this wave
@@ -190,9 +191,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
     if (block_last < sp.block * kBlock) return;
 
     const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
-    const int tiles = (sees(block_last) + kKeys - 1) / kKeys;                // of the workgroup
+    const int all = (sees(block_last) + kKeys - 1) / kKeys;                      // tiles of the block
+    const int t0 = SPLIT ? (int)(place - unit * a.parts) * a.part_tiles : 0;     // even: tile j is in buffer j % 2
+    if (SPLIT && t0 >= max(all, 1)) return;
+    const int tiles = SPLIT ? min(all, t0 + a.part_tiles) : all;                 // (behind the last) of the workgroup
     const int last = min(sp.lq - 1, q_first + 31);
-    const int mine = last < q_first ? 0 : (sees(last) + kKeys - 1) / kKeys;  // of this wave
+    const int mine = last < q_first ? 0 : min(tiles, (sees(last) + kKeys - 1) / kKeys);  // of this wave
     const int whole = sees(q_first) / kKeys;                                 // of them without hidden keys
 
     const uint16_t *kv = a.kv + sp.b * a.kvb + sp.k0 * a.kvt + h * kKvRow;
@@ -209,10 +213,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
         const int rows = min(kKeys, sp.lk - j * kKeys), buf = j & 1;
         copy_tile<kVal, WAVES>(kv + kNope + (int64_t)j * kKeys * a.kvt, rows, kv_bytes, off_n, lds_v + buf * (uint32_t)sizeof(sm.v[0]), wave);
     };
-    if (tiles > 0) {
-        copy_keys(0);
-        if (tiles > 1) copy_keys(1);
-        copy_values(0);
+    if (tiles > t0) {
+        copy_keys(t0);
+        if (tiles > t0 + 1) copy_keys(t0 + 1);
+        copy_values(t0);
     }
 
     FwdState f;
@@ -250,11 +254,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
         rise(f, top, c);
         tile_step<true>(f, at, j & 1, s, next, top, c);
     };
-    if (tiles > 0) {
+    if (tiles > t0) {
         f16v s0[2], s1[2];
         copies_done();
-        int j = 0;
-        if (mine > 0) {
+        int j = t0;
+        if (mine > t0) {
             first_scores(f, at, 0, s0, top);
             for (; j + 2 < mine; j += 2) {
                 step(j, s0, s1);
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
         reset();
         const int block_whole = sees(sp.block * kBlock) / kKeys;
 #pragma unroll 1
-        for (int j = 0; j < tiles; ++j) {
+        for (int j = t0; j < tiles; ++j) {
             copy_keys(j);
             copy_values(j);
             copies_done();
@@ -315,6 +319,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
     }
 
     const float l = pair_sum(f.l);
+    if (SPLIT && all > a.part_tiles) {
+        f4 *y = reinterpret_cast<f4 *>(a.part) + (place * WAVES + wave) * (kVal / 8 * 64) + lane;
+#pragma unroll
+        for (int d = 0; d < kVal / 32; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[(4 * d + e) * 64] = f4{f.o[d][4 * e], f.o[d][4 * e + 1], f.o[d][4 * e + 2], f.o[d][4 * e + 3]};
+        if (g == 0) {
+            float *st = a.part_stat + (place * WAVES + wave) * 64 + lane;
+            st[0] = f.mc;
+            st[32] = l;
+        }
+        return;
+    }
     const float w = l == 0.0f ? 0.0f : 1.0f / l;
     if (i >= sp.lq) return;
     const int64_t row = (sp.b * a.T + sp.q0 + i) * a.H + h;
@@ -328,6 +345,45 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
         }
     // l == 0: no key is seen
     if (a.lse && g == 0) a.lse[row] = l == 0.0f ? -INFINITY : (f.mc + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// A block's parts added up in their order: 32 queries and 32 of their values a wave.
+__global__ __launch_bounds__(64) void latent_fwd_join_kernel(LatentArgs a) {
+    constexpr int kWaves = 4, kPieces = kVal / 32;
+    const int lane = threadIdx.x, g = lane >> 5;
+    const int64_t place = a.base + blockIdx.x, unit = place / (kWaves * kPieces), h = unit % a.H;
+    const int wave = (int)(place / kPieces % kWaves), d = (int)(place % kPieces);
+    Span sp;
+    if (!span_of<32 * kWaves, false>(a, unit / a.H, a.causal, sp)) return;
+    const int q_first = sp.block * 32 * kWaves + wave * 32, block_last = min(sp.lq, (sp.block + 1) * 32 * kWaves) - 1;
+    if (q_first > block_last) return;
+    const int keys = a.causal ? max(0, min(sp.lk, block_last + 1 + sp.lk - sp.lq)) : sp.lk, all = (keys + kKeys - 1) / kKeys;
+    const int parts = (all + a.part_tiles - 1) / a.part_tiles;
+    if (parts < 2) return;
+    const auto factor = [](float from, float to) { return to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(from - to); };
+    f4 o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const int64_t s = (unit * a.parts + p) * kWaves + wave;
+        const f4 *y = reinterpret_cast<const f4 *>(a.part) + (s * kPieces + d) * 4 * 64 + lane;
+        const float *st = a.part_stat + s * 64 + (lane & 31);
+        const float top = fmaxf(m, st[0]), was = factor(m, top), is = factor(st[0], top);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = o[e] * was + y[e * 64] * is;
+        l = l * was + st[32] * is;
+        m = top;
+    }
+    const int i = q_first + (lane & 31);
+    if (i > block_last) return;
+    const float w = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t row = (sp.b * a.T + sp.q0 + i) * a.H + h;
+    uint16_t *out = a.out + row * kVal + 32 * d + 4 * g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<u2v *>(out + 8 * e) = u2v{pack2(o[e][0] * w, o[e][1] * w), pack2(o[e][2] * w, o[e][3] * w)};
+    if (a.lse && d == 0 && g == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // The blocks of a packed batch in order of falling length, by buckets of their tiles'
@@ -443,10 +499,17 @@ int kda_latent_block(int64_t B, int64_t T, int64_t H, int64_t seqs) {
 
 hipError_t kda_launch_latent_fwd(const LatentArgs &a, int block, hipStream_t s) {
     const int64_t units = a.blocks * a.B * a.H;
-    return launch_groups(units, a.launch_cap, [&](int64_t base, dim3 grid) {
+    const hipError_t e = launch_groups(units * a.parts, a.launch_cap, [&](int64_t base, dim3 grid) {
         LatentArgs p = a;
         p.base = base;
-        if (block == 128) hipLaunchKernelGGL(latent_fwd_kernel<4>, grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(latent_fwd_kernel<8>, grid, dim3(512), 0, s, p);
+        if (a.parts > 1) hipLaunchKernelGGL((latent_fwd_kernel<4, true>), grid, dim3(256), 0, s, p);
+        else if (block == 128) hipLaunchKernelGGL((latent_fwd_kernel<4, false>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((latent_fwd_kernel<8, false>), grid, dim3(512), 0, s, p);
+    });
+    if (e != hipSuccess || a.parts < 2) return e;
+    return launch_groups(units * 16, a.launch_cap, [&](int64_t base, dim3 grid) {
+        LatentArgs p = a;
+        p.base = base;
+        hipLaunchKernelGGL(latent_fwd_join_kernel, grid, dim3(64), 0, s, p);
     });
 }

@@ -76,8 +76,8 @@ def _latent_args(q, kv, k_pe, scale, causal, cu, cu_k, launch_piece=0):
 
 
 def latent_workspace_size(B: int, T: int, Tk: int, H: int, num_seqs: Optional[int] = None) -> int:
-    """Workspace bytes ``latent_fwd`` needs for these sizes as a packed batch of num_seqs sequences (0 if it is none)."""
-    return 0 if num_seqs is None else int(_library().kda_latent_fwd_workspace_size(_sizes(B, T, Tk, H, num_seqs)))
+    """Workspace bytes ``latent_fwd`` needs for these sizes (num_seqs: of a packed batch)."""
+    return int(_library().kda_latent_fwd_workspace_size(_sizes(B, T, Tk, H, B if num_seqs is None else num_seqs)))
 
 
 def _sizes(B, T, Tk, H, n):
@@ -100,9 +100,9 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: flo
     d, dev = _latent_args(q, kv, k_pe, scale, causal, cu_seqlens, cu_seqlens_k, launch_piece)
     out = _output(out, "out", (d.B, d.T, d.H, VALUE), torch.bfloat16, dev)
     lse = _output(lse, "lse", (d.B, d.T, d.H), torch.float32, dev)
-    ws = None
-    if cu_seqlens is not None:
-        ws = _workspace(workspace, _library().kda_latent_fwd_workspace_size(d), dev, d)  # noqa: F841 (held until the call)
+    need = _library().kda_latent_fwd_workspace_size(d)
+    if need:
+        ws = _workspace(workspace, need, dev, d)  # noqa: F841 (held until the call)
     _call(_library().kda_latent_fwd, dev, q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), _ptr(cu_seqlens), _ptr(cu_seqlens_k),
           out.data_ptr(), lse.data_ptr(), d)
     return out, lse

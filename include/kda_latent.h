@@ -79,7 +79,8 @@ kda_status_t kda_latent_bwd(const void *q, const void *kv, const void *k_pe, con
                             const int64_t *cu_seqlens_k, const void *out, const float *lse, const void *d_out, void *dq,
                             void *dkv, void *dk_pe, const kda_latent_desc_t *desc, hipStream_t stream);
 /* Bytes of workspace the calls need (0 if the shapes are invalid; with B = 1 enough
- * for a packed batch too).  The forward needs none but for packed batches. */
+ * for a packed batch too).  The forward needs some for packed batches and for few
+ * queries with many keys. */
 size_t kda_latent_fwd_workspace_size(const kda_latent_desc_t *desc);
 size_t kda_latent_bwd_workspace_size(const kda_latent_desc_t *desc);
 

@@ -155,7 +155,7 @@ def test_strides_and_broadcasts():
 
 @pytest.mark.parametrize("packed", [False, True])
 def test_long_sequences(packed):
-    """Sizes at which a workgroup takes 256 queries: every head's bits are those of the head alone, which has 128, and
+    """Sizes at which a workgroup takes 256 queries: the heads' bits are those of fewer heads, which take 128, and
     hidden values that are not finite stay where they are."""
     T, H = 2100, 64
     lens = [T + 30, T - 30] if packed else [T]
@@ -165,10 +165,10 @@ def test_long_sequences(packed):
     a["kv"][0, T - 60, 5, 130] = float("nan")
     a["kv"][0, T - 70, 63, 3] = float("inf")
     out, lse = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, True, cu)
-    for h in (0, 5, 31, 63):
-        q, kv = a["q"][:, :, h:h + 1].contiguous(), a["kv"][:, :, h:h + 1].contiguous()
-        one = kda.latent_fwd(q, kv, a["k_pe"], SCALE, True, cu)
-        same({"out": out[:, :, h:h + 1].contiguous(), "lse": lse[:, :, h:h + 1].contiguous()}, {"out": one[0], "lse": one[1]})
+    for h in (0, 24, 48):
+        q, kv = a["q"][:, :, h:h + 16].contiguous(), a["kv"][:, :, h:h + 16].contiguous()
+        few = kda.latent_fwd(q, kv, a["k_pe"], SCALE, True, cu)
+        same({"out": out[:, :, h:h + 16].contiguous(), "lse": lse[:, :, h:h + 16].contiguous()}, {"out": few[0], "lse": few[1]})
     assert out[0, :, 5, 2].isnan().nonzero().flatten().tolist() == list(range(T - 60, lens[0]))
     f = lambda t: d(t)[0]  # noqa: E731
     ref = R.attention(f(a["q"][:, :, 31:32]), f(a["kv"][:, :, 31:32]), f(a["k_pe"]), SCALE, True, lens, lens)
@@ -237,12 +237,15 @@ def test_offsets_beyond_32_bits():
     res = run({"q": q, "kv": kv, "k_pe": pe, "dy": dy}, True)
     for h in (0, 77, 127):
         one = {"q": q[:, :, h:h + 1], "kv": kv[:, :, h:h + 1], "k_pe": pe, "dy": dy[:, :, h:h + 1]}
-        got = run({k: v.contiguous() for k, v in one.items()}, True)
-        for k in ("out", "lse", "dq", "dkv"):
+        one = {k: v.contiguous() for k, v in one.items()}
+        got = kda.latent_bwd(one["q"], one["kv"], pe, SCALE, res["out"][:, :, h:h + 1], res["lse"][:, :, h:h + 1].contiguous(), one["dy"])
+        for k in ("dq", "dkv"):
             assert torch.equal(got[k][:, :, 0], res[k][:, :, h]), (h, k)
-    f = lambda t: d(t)[0]  # noqa: E731
-    ref = R.attention(f(q)[:, 127:], f(kv[:, :, 127:]), f(pe), SCALE, True, [T], [Tk])
-    R.within(res["out"][0, :, 127:], ref["out"], ref["tol_out"], "out")
+        f = lambda t: d(t)[0]  # noqa: E731
+        ref = R.attention(f(one["q"]), f(one["kv"]), f(pe), SCALE, True, [T], [Tk])
+        for out, lse in ((res["out"][0, :, h:h + 1], res["lse"][0, :, h:h + 1]), [t[0] for t in kda.latent_fwd(one["q"], one["kv"], pe, SCALE)]):
+            R.within(out, ref["out"], ref["tol_out"], "out")
+            R.within(lse, ref["lse"], ref["tol_lse"], "lse")
 
 
 def test_launch_pieces_and_repeats():
@@ -269,8 +272,66 @@ def test_gradient_in_one_and_in_two_launches(lens):
     check(a, res, True, lens, lens, "many")
     for h in (0, 7, 15):
         one = {k: (v if k == "k_pe" else v[:, :, h:h + 1].contiguous()) for k, v in a.items()}
-        got = run(one, True, cu)
-        same({k: got[k] for k in ("out", "lse", "dq", "dkv")}, {k: res[k][:, :, h:h + 1].contiguous() for k in ("out", "lse", "dq", "dkv")})
+        out, lse = res["out"][:, :, h:h + 1].contiguous(), res["lse"][:, :, h:h + 1].contiguous()
+        got = kda.latent_bwd(one["q"], one["kv"], one["k_pe"], SCALE, out, lse, one["dy"], True, cu)
+        same({k: got[k] for k in ("dq", "dkv")}, {k: res[k][:, :, h:h + 1].contiguous() for k in ("dq", "dkv")})
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B,T,Tk,H", [(1, 1, 5000, 1), (1, 64, 4097, 2), (2, 130, 2500, 3), (1, 1500, 1500, 1), (1, 1000, 900, 2)])
+def test_few_queries_with_many_keys(B, T, Tk, H, causal):
+    """Keys in parts, which are joined: also where the first blocks see one part or no key, and a NaN that some see."""
+    say("case latent parts %s causal=%s" % ((B, T, Tk, H), causal))
+    a = make(B, T, Tk, H, seed=19)
+    want = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal)
+    check(a, run(a, causal), causal, [T] * B, [Tk] * B, "parts")
+    for piece in (0, 8):
+        got = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal, launch_piece=piece)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    j = Tk - 1 - min(T, Tk) // 2  # seen by the last queries
+    a["kv"][0, j, 0, 200] = float("nan")
+    out, lse = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal)
+    first = max(0, j - (Tk - T)) if causal else 0
+    assert torch.equal(lse, want[1]) and out[0, first:, 0, 72].isnan().all()
+    out[0, first:, 0, 72] = want[0][0, first:, 0, 72]
+    assert torch.equal(out, want[0])
+
+
+def test_packed_parts_in_a_graph():
+    lens, ctx = [5, 200, 0, 3, 129], [2000, 0, 7, 900, 1300]
+    lens_k = [p + c for p, c in zip(lens, ctx)]
+    H, tail = 2, 6
+    a = make(1, sum(lens) + tail, sum(lens_k) + tail, H, seed=20)
+    cu, cu_k = cu_of(lens), cu_of(lens_k)
+    need = kda.latent_workspace_size(1, sum(lens) + tail, sum(lens_k) + tail, H, num_seqs=5)
+    assert need > 1 << 20
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = torch.full((1, sum(lens) + tail, H, 128), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((1, sum(lens) + tail, H), 7.0, device="cuda")
+
+    def call(cu, cu_k):
+        kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, True, cu, cu_k, out=out, lse=lse, workspace=ws)
+
+    def compare(lens, lens_k):
+        f = lambda t: d(t)[0]  # noqa: E731
+        n, m = sum(lens), sum(lens_k)
+        ref = R.attention(f(a["q"])[:n], f(a["kv"])[:m], f(a["k_pe"])[:m], SCALE, True, lens, lens_k)
+        R.within(out[0, :n], ref["out"], ref["tol_out"], "out")
+        R.within(lse[0, :n], ref["lse"], ref["tol_lse"], "lse")
+        assert (out[0, n:] == 7.0).all() and (lse[0, n:] == 7.0).all()
+    call(cu, cu_k)
+    compare(lens, lens_k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(cu, cu_k)
+    for p, k in (([5, 200, 0, 3, 129], lens_k), ([100, 1, 1, 35, 200], [100, 1, 4000, 35, 200]), ([0, 0, 0, 337, 0], [1, 2, 3, 4300, 0])):
+        cu.copy_(cu_of(p))
+        cu_k.copy_(cu_of(k))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        compare(p, k)
 
 
 def test_many_short_sequences():

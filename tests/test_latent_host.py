@@ -81,6 +81,8 @@ def test_latent_checks(lib):
 def test_latent_workspaces(lib):
     assert kda.latent_workspace_size(2, 100, 100, 4) == 0
     assert kda.latent_workspace_size(1, 1000, 1000, 4, num_seqs=9) > 0
+    # one token of one head over many keys: accumulators and statistics of 128 rows of every part
+    assert kda.latent_workspace_size(2, 1, 100000, 1) % (128 * 130 * 4) == 0 and kda.latent_workspace_size(2, 8000, 8000, 16) == 0
     assert kda.latent_bwd_workspace_size(2, 100, 300, 4) >= 2 * 300 * 4 * 64 * 4 + 2 * 100 * 4 * 8
     assert kda.latent_bwd_workspace_size(1, 200, 600, 4, num_seqs=3) > kda.latent_bwd_workspace_size(1, 200, 600, 3, num_seqs=3)
     for bad in ((0, 8, 8, 1), (1, -1, 8, 1), (1, 8, 8, 0), (2, 8, 8, 1, 3)):
