@@ -209,7 +209,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
     // workgroup instead of 32, 66 -> 70 us).
     constexpr int kChange = R == 1 ? 3 : 5;
     {
-        const uint32_t even = (uint32_t)((total + a.groups - 1) / a.groups);
+        const uint32_t even = max((uint32_t)((total + a.groups - 1) / a.groups), 1u);
         for (int64_t n = n0; n < n1; ++n)
             if ((uint32_t)steps_of(n) % even != 0) sm.uneven = 1;
     }
