@@ -170,8 +170,9 @@ extern "C" kda_status_t kda_latent_fwd(const void *q, const void *kv, const void
 
 namespace {
 struct LatentBwdPlan {
-    int64_t q_blocks, k_blocks;
-    size_t off_qt, off_kt, off_stat, off_part, total;
+    int64_t q_blocks, k_blocks, q_parts, k_parts;
+    int part_tiles;
+    size_t off_qt, off_kt, off_stat, off_part, off_q, off_k, total;
 };
 kda_status_t plan_latent_bwd(const kda_latent_desc_t *d, bool packed, LatentBwdPlan &p) {
     p = LatentBwdPlan{};
@@ -187,7 +188,20 @@ kda_status_t plan_latent_bwd(const kda_latent_desc_t *d, bool packed, LatentBwdP
     p.off_kt = qt;
     p.off_stat = p.off_kt + kt;
     p.off_part = p.off_stat + align_up(latent_rows(d) * 8, 256);
-    p.total = p.off_part + align_up(latent_keys(d) * (size_t)d->H * kPe * 4, 256);
+    p.off_q = p.off_k = p.total = p.off_part + align_up(latent_keys(d) * (size_t)d->H * kPe * 4, 256);
+    p.q_parts = p.k_parts = 1;
+    // Few blocks are split as in the forward, here by a common number of tiles of the other side, for some
+    // 256 workgroups, all that run at once (4096 tokens x 2 heads 136 -> 90 us, with 512 of them 102; 512
+    // tokens of one head over 8512 keys 209 -> 42).
+    constexpr int64_t kPartTiles = 8, kFewTiles = 12, kFewUnits = 128, kUnits = 256;
+    const int64_t q_units = p.q_blocks * d->B * d->H, k_units = p.k_blocks * d->B * d->H;
+    const int64_t q_tiles = (d->T + kKeys - 1) / kKeys, k_tiles = (d->Tk + kKeys - 1) / kKeys;
+    if (q_units + k_units > kFewUnits || std::max(q_tiles, k_tiles) <= kFewTiles) return KDA_OK;
+    p.part_tiles = (int)std::max(kPartTiles, (q_units * k_tiles + k_units * q_tiles + kUnits - 1) / kUnits);
+    p.q_parts = std::max<int64_t>(1, (k_tiles + p.part_tiles - 1) / p.part_tiles);
+    p.k_parts = std::max<int64_t>(1, (q_tiles + p.part_tiles - 1) / p.part_tiles);
+    p.off_k = p.off_q + (size_t)(q_units * p.q_parts) * kLatentBwdBlock * kQk * 4;
+    p.total = p.off_k + (size_t)(k_units * p.k_parts) * kLatentBwdBlock * (kQk + kVal) * 4;
     return KDA_OK;
 }
 }  // namespace
@@ -247,6 +261,11 @@ extern "C" kda_status_t kda_latent_bwd(const void *q, const void *kv, const void
     LatentArgs k = a;
     a.blocks = p.q_blocks;
     k.blocks = p.k_blocks;
+    a.parts = p.q_parts;
+    k.parts = p.k_parts;
+    a.part_tiles = k.part_tiles = p.part_tiles;
+    a.part = reinterpret_cast<float *>(ws.at(p.off_q));
+    k.part = reinterpret_cast<float *>(ws.at(p.off_k));
     hipError_t e = hipSuccess;
     if (packed && !kda_latent_counted(desc->num_seqs, std::max(p.q_blocks, p.k_blocks) * desc->H)) {
         int32_t *qt = reinterpret_cast<int32_t *>(ws.at(p.off_qt)), *kt = reinterpret_cast<int32_t *>(ws.at(p.off_kt));

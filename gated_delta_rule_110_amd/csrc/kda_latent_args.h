@@ -22,8 +22,8 @@ struct LatentArgs {
     uint16_t *out;
     float *lse;
     int64_t launch_cap, base;  // base: first workgroup of this launch; set by the launcher
-    // forward: parts (1: none) of part_tiles tiles of keys that a block's keys may be split in; what each
-    // leaves of its 128 queries: accumulators, and (maximum, sum)
+    // parts (1: none) of part_tiles tiles of the other side that a block's work may be split in; what each
+    // leaves of its 128 tokens: accumulators, and in the forward (maximum, sum)
     int64_t parts;
     int part_tiles;
     float *part, *part_stat;

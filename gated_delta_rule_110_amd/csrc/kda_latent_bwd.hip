@@ -13,7 +13,8 @@
 // through LDS, 64 at a time; P and dS are fed back as B operands as they stand.  A unit is
 // 32 tokens of the other side: the first products of unit u + 1 run beside the
 // exponentials of unit u.  Every head leaves its part of dk_pe in fp32; they are added up
-// in the order of the heads.
+// in the order of the heads.  Few blocks take one launch for both passes, and parts of their
+// other side each, which are added up in their order by a launch of its own.
 //
 // The matrix instructions bound it, with one wave a SIMD, whose 512 registers hold its sums:
 // 8192 tokens x 32 heads take 982 us for dq (1.12 PFLOP/s), 1212 for dkv (1.13) and 12 for
@@ -136,9 +137,22 @@ __device__ __forceinline__ Stat row_stat(const s8 (&y)[kVal / 16], const uint16_
     return {lse == -INFINITY ? 0.0f : lse * kLog2e, pair_sum(d)};
 }
 
-// unit: the block, counted over the heads.  STORE: the rows' statistics too, for dkv.
-template <bool STORE>
-__device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSmem &sm) {
+// What a workgroup leaves of its part of a block: GROUPS groups of 32 values of a wave's 32 tokens, an
+// accumulator each.
+template <int GROUPS>
+__device__ __forceinline__ f4 *part_of(const LatentArgs &a, int64_t place, int wave, int group) {
+    return reinterpret_cast<f4 *>(a.part) + ((place * 4 + wave) * GROUPS + group) * 4 * 64 + (threadIdx.x & 63);
+}
+__device__ __forceinline__ void leave(f4 *p, const f16v &v, float scale) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        p[e * 64] = f4{v[4 * e] * scale, v[4 * e + 1] * scale, v[4 * e + 2] * scale, v[4 * e + 3] * scale};
+}
+
+// place: the block, counted over the heads, with SPLIT its part.  STORE: the rows' statistics too, for dkv.
+template <bool STORE, bool SPLIT>
+__device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t place, DqSmem &sm) {
+    const int64_t unit = SPLIT ? place / a.parts : place;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t h = unit % a.H;
@@ -148,9 +162,12 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSm
     const int block_last = min(sp.lq, (sp.block + 1) * kBlock) - 1;
     if (block_last < sp.block * kBlock) return;
     const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
-    const int tiles = (sees(block_last) + kKeys - 1) / kKeys;
+    const int all = (sees(block_last) + kKeys - 1) / kKeys;
+    const int t0 = SPLIT ? (int)(place - unit * a.parts) * a.part_tiles : 0;
+    if (SPLIT && t0 >= max(all, 1)) return;
+    const int tiles = SPLIT ? min(all, t0 + a.part_tiles) : all;
     const int last = min(sp.lq - 1, q_first + 31);
-    const int mine = last < q_first ? 0 : (sees(last) + kKeys - 1) / kKeys;  // of this wave
+    const int mine = last < q_first ? 0 : min(tiles, (sees(last) + kKeys - 1) / kKeys);  // of this wave
     const int whole = sees(q_first) / 32;                                    // units without hidden keys
 
     const uint16_t *kv = a.kv + sp.b * a.kvb + sp.k0 * a.kvt + h * kKvRow;
@@ -166,8 +183,8 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSm
         copy_tile<kPe>(pe + (int64_t)j * kKeys * a.pet, rows, pe_bytes, off_p, lds_kp + buf * (uint32_t)sizeof(sm.kp[0]), wave);
         copy_tile<kVal>(p + kNope, rows, kv_bytes, off_n, lds_v + buf * (uint32_t)sizeof(sm.v[0]), wave);
     };
-    copy(0);
-    copy(1);
+    copy(t0);
+    copy(t0 + 1);
 
     DqState f;
     const int i = q_first + (lane & 31), row = min(i, sp.lq - 1);  // rows behind the last: of no effect, not stored
@@ -206,26 +223,27 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSm
         copies_done();
         copy(t + 1);
     };
-    int t = 0;
-    if (tiles > 0) copies_done();
-    if (mine > 0) {
+    int t = t0;
+    if (tiles > t0) copies_done();
+    if (mine > t0) {
         f16v s0, d0, s1, d1;
+        int st = t0 % kStages;
 #pragma unroll
         for (int n = 0; n < kSdSlots; ++n) {
             const int ks = sd_block(n);
             if (is_s(n)) {
-                const s8 x = ks < kNope / 16 ? row_operand<2 * kNope>(at.kn, 0, ks) : row_operand<2 * kPe>(at.kp, 0, ks - kNope / 16);
+                const uint32_t kn = at.kn + st * (uint32_t)sizeof(sm.kn[0]), kp = at.kp + st * (uint32_t)sizeof(sm.kp[0]);
+                const s8 x = ks < kNope / 16 ? row_operand<2 * kNope>(kn, 0, ks) : row_operand<2 * kPe>(kp, 0, ks - kNope / 16);
                 if (n == 0) first_product(s0, x, f.q[ks]);
                 else add_product(s0, x, f.q[ks]);
             } else {
-                const s8 x = row_operand<2 * kVal>(at.v, 0, ks);
+                const s8 x = row_operand<2 * kVal>(at.v + st * (uint32_t)sizeof(sm.v[0]), 0, ks);
                 if (n == 1) first_product(d0, x, f.y[ks]);
                 else add_product(d0, x, f.y[ks]);
             }
             if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
         products_done();
-        int st = 0;
         for (; t < mine - 1; ++t) {
             const int next = st == kStages - 1 ? 0 : st + 1;
             begin(t + 1);
@@ -245,6 +263,11 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSm
     }
     for (; t < tiles; ++t) begin(t);
 
+    if (SPLIT && all > a.part_tiles) {
+#pragma unroll
+        for (int d = 0; d < kQk / 32; ++d) leave(part_of<kQk / 32>(a, place, wave, d), f.dq[d], a.scale);
+        return;
+    }
     if (i >= sp.lq) return;
     uint16_t *out = a.dq + ((sp.b * a.T + sp.q0 + i) * a.H + h) * kQk + 4 * g;
 #pragma unroll
@@ -259,7 +282,7 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t unit, DqSm
 
 __global__ __launch_bounds__(256, 1) void latent_dq_kernel(LatentArgs a) {
     __shared__ __attribute__((aligned(1024))) DqSmem sm;
-    dq_block<true>(a, a.base + blockIdx.x, sm);
+    dq_block<true, false>(a, a.base + blockIdx.x, sm);
 }
 
 // ---- dkv ----------------------------------------------------------------------------
@@ -352,7 +375,10 @@ __device__ __forceinline__ void dkv_unit(DkvState &f, const DkvAddr &at, int st,
     }
 }
 
-__device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t unit, DkvSmem &sm) {
+constexpr int kDkvGroups = (kQk + kVal) / 32;
+template <bool SPLIT>
+__device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t place, DkvSmem &sm) {
+    const int64_t unit = SPLIT ? place / a.parts : place;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t h = unit % a.H;
@@ -363,8 +389,11 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t unit, Dkv
     // The first query that sees key j, and with it all behind it.
     const int lead = sp.lk - sp.lq;
     const auto seen_from = [&](int j) { return a.causal ? max(0, j - lead) : 0; };
-    const int first = seen_from(sp.block * kBlock) / kKeys;           // tiles of queries
-    const int tiles = max(first, (sp.lq + kKeys - 1) / kKeys);        // (one behind the last)
+    const int first_all = seen_from(sp.block * kBlock) / kKeys;                // tiles of queries
+    const int tiles_all = max(first_all, (sp.lq + kKeys - 1) / kKeys);         // (one behind the last)
+    const int first = SPLIT ? first_all + (int)(place - unit * a.parts) * a.part_tiles : first_all;
+    if (SPLIT && first > first_all && first >= tiles_all) return;
+    const int tiles = SPLIT ? min(tiles_all, first + a.part_tiles) : tiles_all;
     const int j = k_first + (lane & 31), row = min(j, sp.lk - 1);
     const int from = seen_from(j);                                    // of the lane's key
     const int top_key = min(k_first + 31, sp.lk - 1);
@@ -460,6 +489,13 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t unit, Dkv
         dkv_unit<false>(f, at, st, 1, 0, 0, s1, d1, s0, d0, c);
     }
 
+    if (SPLIT && tiles_all - first_all > a.part_tiles) {
+#pragma unroll
+        for (int d = 0; d < kQk / 32; ++d) leave(part_of<kDkvGroups>(a, place, wave, d), f.dk[d], a.scale);
+#pragma unroll
+        for (int d = 0; d < kVal / 32; ++d) leave(part_of<kDkvGroups>(a, place, wave, kQk / 32 + d), f.dv[d], 1.0f);
+        return;
+    }
     if (j >= sp.lk) return;
     const int64_t key = sp.b * a.Tk + sp.k0 + j;
     uint16_t *out = a.dkv + (key * a.H + h) * kKvRow + 4 * g;
@@ -489,7 +525,7 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t unit, Dkv
 
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentArgs a) {
     __shared__ __attribute__((aligned(1024))) DkvSmem sm;
-    dkv_block(a, a.base + blockIdx.x, sm);
+    dkv_block<false>(a, a.base + blockIdx.x, sm);
 }
 
 // ---- both at once -------------------------------------------------------------------
@@ -510,13 +546,63 @@ __global__ __launch_bounds__(256) void latent_stat_kernel(LatentArgs a) {
     }
 }
 
-// The blocks of queries, then those of keys.
-__global__ __launch_bounds__(256, 1) void latent_both_kernel(LatentArgs q, LatentArgs k, int64_t q_units) {
+// The blocks of queries, then those of keys; with SPLIT their parts.
+template <bool SPLIT>
+__global__ __launch_bounds__(256, 1) void latent_both_kernel(LatentArgs q, LatentArgs k, int64_t q_places) {
     __shared__ __attribute__((aligned(1024))) char sm[sizeof(DkvSmem)];
     static_assert(sizeof(DqSmem) <= sizeof(DkvSmem), "");
-    const int64_t unit = q.base + blockIdx.x;
-    if (unit < q_units) dq_block<false>(q, unit, *reinterpret_cast<DqSmem *>(sm));
-    else dkv_block(k, unit - q_units, *reinterpret_cast<DkvSmem *>(sm));
+    const int64_t place = q.base + blockIdx.x;
+    if (place < q_places) dq_block<false, SPLIT>(q, place, *reinterpret_cast<DqSmem *>(sm));
+    else dkv_block<SPLIT>(k, place - q_places, *reinterpret_cast<DkvSmem *>(sm));
+}
+
+// The parts of a block added up in their order: 32 tokens and 32 of their values a wave.
+template <bool BY_KEYS>
+__device__ __forceinline__ void join_parts(const LatentArgs &a, int64_t place) {
+    constexpr int kGroups = BY_KEYS ? kDkvGroups : kQk / 32;
+    const int lane = threadIdx.x, g = lane >> 5;
+    const int64_t unit = place / (4 * kGroups), h = unit % a.H;
+    const int wave = (int)(place / kGroups % 4), d = (int)(place % kGroups);
+    Span sp;
+    if (!span_of<kBlock, BY_KEYS>(a, unit / a.H, BY_KEYS ? false : a.causal, sp)) return;
+    const int first = sp.block * kBlock, len = BY_KEYS ? sp.lk : sp.lq;
+    if (first + wave * 32 >= len) return;
+    int tiles;
+    if (BY_KEYS) {
+        const int from = (a.causal ? max(0, first - (sp.lk - sp.lq)) : 0) / kKeys;
+        tiles = (sp.lq + kKeys - 1) / kKeys - from;
+    } else {
+        const int last = min(sp.lq, first + kBlock) - 1;
+        tiles = ((a.causal ? max(0, min(sp.lk, last + 1 + sp.lk - sp.lq)) : sp.lk) + kKeys - 1) / kKeys;
+    }
+    if (tiles <= a.part_tiles) return;
+    const int parts = (tiles + a.part_tiles - 1) / a.part_tiles;
+    f4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const f4 *x = part_of<kGroups>(a, unit * a.parts + p, wave, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e * 64];
+    }
+    const int i = first + wave * 32 + (lane & 31);
+    if (i >= len) return;
+    if (BY_KEYS && d >= kNope / 32 && d < kQk / 32) {
+        float *part = a.dpe_part + (h * a.B * a.Tk + sp.b * a.Tk + sp.k0 + i) * kPe + 32 * (d - kNope / 32) + 4 * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<f4 *>(part + 8 * e) = v[e];
+        return;
+    }
+    uint16_t *out = BY_KEYS ? a.dkv + ((sp.b * a.Tk + sp.k0 + i) * a.H + h) * kKvRow + 32 * (d < kNope / 32 ? d : d - kPe / 32)
+                            : a.dq + ((sp.b * a.T + sp.q0 + i) * a.H + h) * kQk + 32 * d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<u2v *>(out + 4 * g + 8 * e) = u2v{pack2(v[e][0], v[e][1]), pack2(v[e][2], v[e][3])};
+}
+__global__ __launch_bounds__(64) void latent_grad_join_kernel(LatentArgs q, LatentArgs k, int64_t q_places) {
+    const int64_t place = q.base + blockIdx.x;
+    if (place < q_places) join_parts<false>(q, place);
+    else join_parts<true>(k, place - q_places);
 }
 
 // dk_pe: the heads' parts added up, 4 values a thread, heads in order.
@@ -557,8 +643,16 @@ hipError_t kda_launch_latent_pairs(const LatentArgs &q, const LatentArgs &k, hip
             hipLaunchKernelGGL(latent_stat_kernel, grid, block, 0, s, p);
         });
         if (e != hipSuccess) return e;
-        return pieces(q_units + k_units, [&](dim3 grid, const LatentArgs &p, const LatentArgs &r) {
-            hipLaunchKernelGGL(latent_both_kernel, grid, block, 0, s, p, r, q_units);
+        const int64_t q_places = q_units * q.parts, k_places = k_units * k.parts;
+        const bool split = q.parts > 1 || k.parts > 1;
+        const hipError_t f = pieces(q_places + k_places, [&](dim3 grid, const LatentArgs &p, const LatentArgs &r) {
+            if (split) hipLaunchKernelGGL(latent_both_kernel<true>, grid, block, 0, s, p, r, q_places);
+            else hipLaunchKernelGGL(latent_both_kernel<false>, grid, block, 0, s, p, r, q_places);
+        });
+        if (f != hipSuccess || !split) return f;
+        const int64_t q_joins = q_units * 4 * (kQk / 32), k_joins = k_units * 4 * kDkvGroups;
+        return pieces(q_joins + k_joins, [&](dim3 grid, const LatentArgs &p, const LatentArgs &r) {
+            hipLaunchKernelGGL(latent_grad_join_kernel, grid, dim3(64), 0, s, p, r, q_joins);
         });
     }
     const hipError_t e = pieces(q_units, [&](dim3 grid, const LatentArgs &p, const LatentArgs &) {

@@ -263,18 +263,20 @@ def test_launch_pieces_and_repeats():
 
 @pytest.mark.parametrize("lens", [[1300], [900, 0, 1, 399]])
 def test_gradient_in_one_and_in_two_launches(lens):
-    """Many blocks take a launch of queries and one of keys, few of them one launch for both: the same bits."""
+    """Many blocks take a launch of queries and one of keys, few of them one launch for both, or for parts of both."""
     H = 16
     say("case latent gradient of %s x %d heads" % (lens, H))
     a = make(1, sum(lens), sum(lens), H, seed=18)
     cu = cu_of(lens) if len(lens) > 1 else None
     res = run(a, True, cu)
     check(a, res, True, lens, lens, "many")
-    for h in (0, 7, 15):
-        one = {k: (v if k == "k_pe" else v[:, :, h:h + 1].contiguous()) for k, v in a.items()}
-        out, lse = res["out"][:, :, h:h + 1].contiguous(), res["lse"][:, :, h:h + 1].contiguous()
-        got = kda.latent_bwd(one["q"], one["kv"], one["k_pe"], SCALE, out, lse, one["dy"], True, cu)
-        same({k: got[k] for k in ("dq", "dkv")}, {k: res[k][:, :, h:h + 1].contiguous() for k in ("dq", "dkv")})
+    for h, n in ((0, 8), (8, 8), (15, 1)):
+        few = {k: (v if k == "k_pe" else v[:, :, h:h + n].contiguous()) for k, v in a.items()}
+        out, lse = res["out"][:, :, h:h + n].contiguous(), res["lse"][:, :, h:h + n].contiguous()
+        got = kda.latent_bwd(few["q"], few["kv"], few["k_pe"], SCALE, out, lse, few["dy"], True, cu)
+        if n == 8:  # not in parts
+            same({k: got[k] for k in ("dq", "dkv")}, {k: res[k][:, :, h:h + n].contiguous() for k in ("dq", "dkv")})
+        check(few, {"out": out, "lse": lse} | got, True, lens, lens, "few")
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -284,10 +286,10 @@ def test_few_queries_with_many_keys(B, T, Tk, H, causal):
     say("case latent parts %s causal=%s" % ((B, T, Tk, H), causal))
     a = make(B, T, Tk, H, seed=19)
     want = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal)
-    check(a, run(a, causal), causal, [T] * B, [Tk] * B, "parts")
+    res = run(a, causal)
+    check(a, res, causal, [T] * B, [Tk] * B, "parts")
     for piece in (0, 8):
-        got = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal, launch_piece=piece)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        same(run(a, causal, launch_piece=piece), res)
     j = Tk - 1 - min(T, Tk) // 2  # seen by the last queries
     a["kv"][0, j, 0, 200] = float("nan")
     out, lse = kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, causal)
@@ -305,20 +307,22 @@ def test_packed_parts_in_a_graph():
     cu, cu_k = cu_of(lens), cu_of(lens_k)
     need = kda.latent_workspace_size(1, sum(lens) + tail, sum(lens_k) + tail, H, num_seqs=5)
     assert need > 1 << 20
+    need = max(need, kda.latent_bwd_workspace_size(1, sum(lens) + tail, sum(lens_k) + tail, H, num_seqs=5))
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     out = torch.full((1, sum(lens) + tail, H, 128), 7.0, dtype=BF, device="cuda")
     lse = torch.full((1, sum(lens) + tail, H), 7.0, device="cuda")
+    grads = {"dq": torch.full_like(a["q"], 7.0), "dkv": torch.full_like(a["kv"], 7.0), "dk_pe": torch.full_like(a["k_pe"], 7.0)}
+    res = {"out": out, "lse": lse} | grads
 
     def call(cu, cu_k):
         kda.latent_fwd(a["q"], a["kv"], a["k_pe"], SCALE, True, cu, cu_k, out=out, lse=lse, workspace=ws)
+        kda.latent_bwd(a["q"], a["kv"], a["k_pe"], SCALE, out, lse, a["dy"], True, cu, cu_k, workspace=ws, outputs=grads)
 
     def compare(lens, lens_k):
-        f = lambda t: d(t)[0]  # noqa: E731
-        n, m = sum(lens), sum(lens_k)
-        ref = R.attention(f(a["q"])[:n], f(a["kv"])[:m], f(a["k_pe"])[:m], SCALE, True, lens, lens_k)
-        R.within(out[0, :n], ref["out"], ref["tol_out"], "out")
-        R.within(lse[0, :n], ref["lse"], ref["tol_lse"], "lse")
-        assert (out[0, n:] == 7.0).all() and (lse[0, n:] == 7.0).all()
+        n = {k: sum(lens_k) if k in ("kv", "k_pe", "dkv", "dk_pe") else sum(lens) for k in list(a) + list(res)}
+        check({k: v[:, :n[k]] for k, v in a.items()}, {k: v[:, :n[k]] for k, v in res.items()}, True, lens, lens_k, "parts")
+        for k, v in res.items():
+            assert (v[:, n[k]:] == 7.0).all(), k
     call(cu, cu_k)
     compare(lens, lens_k)
     g = torch.cuda.CUDAGraph()
@@ -327,8 +331,8 @@ def test_packed_parts_in_a_graph():
     for p, k in (([5, 200, 0, 3, 129], lens_k), ([100, 1, 1, 35, 200], [100, 1, 4000, 35, 200]), ([0, 0, 0, 337, 0], [1, 2, 3, 4300, 0])):
         cu.copy_(cu_of(p))
         cu_k.copy_(cu_of(k))
-        out.fill_(7.0)
-        lse.fill_(7.0)
+        for v in res.values():
+            v.fill_(7.0)
         g.replay()
         torch.cuda.synchronize()
         compare(p, k)
