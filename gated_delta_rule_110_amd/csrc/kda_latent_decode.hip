@@ -7,8 +7,9 @@
 //
 // With 32 rows the cache's bytes are the bound: 64 requests of 4096 rows, 32 heads, take
 // 57 us for 286 MB, 8 of them until the first rows are there, and their joining 8.  With 64
-// rows it is a step's chain of scores, exponentials and barrier, 1.3 us: one request of
-// 131072 rows, 128 heads, takes 50 to 59 us and its joining 8 (its bytes 25).
+// rows a step's chain of scores, exponentials and barrier takes 1.3 us, for which its rows
+// come at 7 TB/s: enough where a sequence has one row tile; with two, one request of 131072
+// rows and 128 heads takes 50 to 59 us and its joining 8 (its bytes 25).
 //
 // Steps (32 cached rows of one row tile) of all sequences are lined up and shared out
 // evenly among 256 workgroups, one a CU, whatever the lengths (with an allowance for the
