@@ -136,7 +136,8 @@ def _workspace(t: Optional[torch.Tensor], need: int, dev: int, d) -> Optional[to
 
 def _call(fn, dev: int, *args) -> None:
     """``fn(*args, stream)`` on the current stream of device ``dev``."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    # The stream's handle alone; torch.cuda.current_stream makes an object of it (1.1 us of the 10 of a small call).
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     if torch.cuda.current_device() == dev:
         st = fn(*args, stream)
     else:
