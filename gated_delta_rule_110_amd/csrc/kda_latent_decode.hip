@@ -578,15 +578,14 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
     }
 }
 
-// The parts of a row tile added up: a workgroup has 8 of a wave's values of 32 rows, 4
-// a lane; each of its waves takes every kJoinWaves-th part, with a running maximum, and
-// the waves' sums are added in their order.
-template <int R, int kJoinWaves>
+// The parts of a row tile added up: 8 of a wave's values of 32 rows, 4 a lane, with a running
+// maximum.  With MANY parts a workgroup's eight waves take every eighth of them, and their sums
+// are added in their order; with few each of its waves has values of its own.
+constexpr int kJoinWaves = 8;
+template <int R, bool MANY>
 __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDecodeArgs a, int64_t base) {
-    __shared__ f4 acc[kJoinWaves][64];
-    __shared__ float tops[kJoinWaves][32], sums[kJoinWaves][32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n32 = lane & 31;
-    const int64_t unit = base + blockIdx.x, tile = unit / (64 * R);
+    const int64_t unit = MANY ? base + blockIdx.x : (base + blockIdx.x) * kJoinWaves + wave, tile = unit / (64 * R);
     const int piece = (int)(unit & 63), r = (int)(unit / 64 % R);
     const int pw = piece >> 4, pv = piece & 15;  // wave and group of values
     const int32_t head = a.seg[2 * tile];
@@ -600,7 +599,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDeco
     if (head >= 0) {
         const int w0 = head >> 1, w1 = a.seg[2 * tile + 1];
 #pragma unroll 8
-        for (int w = w0 + wave; w <= w1; w += kJoinWaves) {
+        for (int w = w0 + (MANY ? wave : 0); w <= w1; w += MANY ? kJoinWaves : 1) {
             const int64_t s = (int64_t)(w == w0 ? head : 2 * w) * R + r;
             const float *st = a.part_stat + s * 64 + n32;
             const f4 x = reinterpret_cast<const f4 *>(a.part)[((s / R * kOutWaves + pw) * R + r) * (kWaveDims / 8 * 64) + pv * 64 + lane];
@@ -610,23 +609,28 @@ __global__ __launch_bounds__(64 * kJoinWaves) void latent_join_kernel(LatentDeco
             m = top;
         }
     }
-    acc[wave][lane] = o;
-    if (lane < 32) {
-        tops[wave][lane] = m;
-        sums[wave][lane] = l;
-    }
-    __syncthreads();
-    if (wave > 0 || i >= rows) return;
+    if (MANY) {
+        __shared__ f4 acc[kJoinWaves][64];
+        __shared__ float tops[kJoinWaves][32], sums[kJoinWaves][32];
+        acc[wave][lane] = o;
+        if (lane < 32) {
+            tops[wave][lane] = m;
+            sums[wave][lane] = l;
+        }
+        __syncthreads();
+        if (wave > 0) return;
 #pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) m = fmaxf(m, tops[w][n32]);
-    o = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    l = 0.0f;
+        for (int w = 1; w < kJoinWaves; ++w) m = fmaxf(m, tops[w][n32]);
+        o = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWaves; ++w) {
-        const float f = factor(tops[w][n32], m);
-        o += acc[w][lane] * f;
-        l += sums[w][n32] * f;
+        for (int w = 0; w < kJoinWaves; ++w) {
+            const float f = factor(tops[w][n32], m);
+            o += acc[w][lane] * f;
+            l += sums[w][n32] * f;
+        }
     }
+    if (i >= rows) return;
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *out = a.out + (n * rows + i) * kLat + pw * kWaveDims + 32 * (pv >> 2) + 8 * (pv & 3) + 4 * (lane >> 5);
     *reinterpret_cast<u2v *>(out) = u2v{pack2(o[0] * f, o[1] * f), pack2(o[2] * f, o[3] * f)};
@@ -647,13 +651,16 @@ hipError_t kda_launch_latent_decode(const LatentDecodeArgs &a, hipStream_t s) {
 }
 
 hipError_t kda_launch_latent_join(const LatentDecodeArgs &a, hipStream_t s) {
-    // A row tile has about groups / (N row_tiles) parts: with many, eight waves take them (128 parts of 64
-    // rows: 8 us, with two waves 28), with few, two (64 row tiles of 5 parts: 8 us, with eight 12).
+    // A row tile has about groups / (N row_tiles) parts: 128 parts of 64 rows take 8 us by eight waves, 28 by
+    // two; with few parts a second wave only costs (64 row tiles of 5 parts, with the steps: 64 -> 63 us; 16
+    // sequences x 128 heads 42 -> 40).
     const bool many = a.N * a.row_tiles * 16 <= a.groups;
-    return launch_groups(a.N * a.row_tiles * a.rows32 * 64, 0, [&](int64_t base, dim3 grid) {
-        if (a.rows32 == 1 && many) hipLaunchKernelGGL((latent_join_kernel<1, 8>), grid, dim3(512), 0, s, a, base);
-        else if (a.rows32 == 1) hipLaunchKernelGGL((latent_join_kernel<1, 2>), grid, dim3(128), 0, s, a, base);
-        else if (many) hipLaunchKernelGGL((latent_join_kernel<2, 8>), grid, dim3(512), 0, s, a, base);
-        else hipLaunchKernelGGL((latent_join_kernel<2, 2>), grid, dim3(128), 0, s, a, base);
+    const int64_t units = a.N * a.row_tiles * a.rows32 * 64;
+    return launch_groups(many ? units : units / kJoinWaves, 0, [&](int64_t base, dim3 grid) {
+        const dim3 block(64 * kJoinWaves);
+        if (a.rows32 == 1 && many) hipLaunchKernelGGL((latent_join_kernel<1, true>), grid, block, 0, s, a, base);
+        else if (a.rows32 == 1) hipLaunchKernelGGL((latent_join_kernel<1, false>), grid, block, 0, s, a, base);
+        else if (many) hipLaunchKernelGGL((latent_join_kernel<2, true>), grid, block, 0, s, a, base);
+        else hipLaunchKernelGGL((latent_join_kernel<2, false>), grid, block, 0, s, a, base);
     });
 }
