@@ -6,10 +6,10 @@
 // and as values (their first 512): 1152 bytes for 2 x 64 x 1088 operations a row.
 //
 // With 32 rows the cache's bytes are the bound: 64 requests of 4096 rows, 32 heads, take
-// 57 us for 286 MB, 8 of them until the first rows are there, and their joining 8.  With 64
+// 55 us for 286 MB, 7 of them until the first rows are there, and their joining 7.  With 64
 // rows a step's chain of scores, exponentials and barrier takes 1.3 us, for which its rows
 // come at 7 TB/s: enough where a sequence has one row tile; with two, one request of 131072
-// rows and 128 heads takes 50 to 59 us and its joining 8 (its bytes 25).
+// rows and 128 heads takes 52 us and its joining 8 (its bytes 25).
 //
 // Steps (32 cached rows of one row tile) of all sequences are lined up and shared out
 // evenly among 256 workgroups, one a CU, whatever the lengths (with an allowance for the
@@ -287,6 +287,32 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
             advance(a, look);
         }
     }
+    // Ahead of them the first segment's queries, by way of the buffers that are still free: where the score
+    // waves ask for them, 16 rows a load and twice each, they come later (131072 rows x 128 heads 64 -> 60
+    // us, 12 sequences of drafted tokens 41 -> 39).
+    constexpr int kQueries = 2;  // first of the buffers
+    {
+        asm volatile("" ::"v"(page[0]), "v"(page[1]), "v"(page[2]), "v"(page[3]));  // waited for ahead of the copies, not behind them
+        const int group = R == 2 ? wave : wave & 3, row = 8 * group + (lane >> 3);
+        const uint32_t x = min((uint32_t)(at.rt * R * 32 + row), rows - 1), tok = x / H, head = x - tok * H;
+        const int chunk = ((lane & 7) ^ place(row & 31)) << 3;
+        const uint16_t *ql = a.ql + at.n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + chunk;
+        const uint16_t *qp = a.qp + at.n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + chunk;
+        const uint32_t to = lds + (kQueries + (group >> 2)) * (uint32_t)sizeof(sm.row[0]) + (group & 3) * 1024;
+        if (R == 2 || wave < 4) {
+            copy16_at<0>(ql, to);
+            copy16_at<128>(ql, to + kSub);
+            copy16_at<256>(ql, to + 2 * kSub);
+            copy16_at<384>(ql, to + 3 * kSub);
+        }
+        if (R == 2 || wave >= 4) {
+            copy16_at<512>(ql, to + 4 * kSub);
+            copy16_at<640>(ql, to + 5 * kSub);
+            copy16_at<768>(ql, to + 6 * kSub);
+            copy16_at<896>(ql, to + 7 * kSub);
+            copy16_at<0>(qp, to + 8 * kSub);
+        }
+    }
     const auto first_copies = [&](auto even) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -312,10 +338,15 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
             all_see = seen_by(at, 0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const uint32_t x = min((uint32_t)(at.rt * R * 32 + r0 + 16 * r + n16), rows - 1), tok = x / H, head = x - tok * H;
                 seen[r] = seen_by(at, r0 + 16 * r + n16);
                 m[r] = -INFINITY;
                 l[r] = 0.0f;
+            }
+        };
+        const auto load_queries = [&]() {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t x = min((uint32_t)(at.rt * R * 32 + r0 + 16 * r + n16), rows - 1), tok = x / H, head = x - tok * H;
                 const uint16_t *ql = a.ql + at.n * a.qln + (int64_t)tok * a.qlt + (int64_t)head * a.qlh + 8 * g16;
                 const uint16_t *qp = a.qp + at.n * a.qpn + (int64_t)tok * a.qpt + (int64_t)head * a.qph + 8 * g16;
 #pragma unroll
@@ -324,15 +355,24 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                                               : *reinterpret_cast<const s8 *>(qp + 32 * ks - kLat);
             }
         };
-        // The first segment's queries come with the first copies, and ahead of them.
-        begin_segment();
         first_copies(std::true_type());
+        begin_segment();
         if ((lane & 7) == 0)
 #pragma unroll
             for (int i = 2; i < 4; ++i) sm.entry[i][my_row] = page[i];
         Feed<true> feed{copy, look, my_row, lane & 7, lds + (wave & 3) * 1024};
         bool fresh = false;
-        arrive<0>();
+        if (count > 1) arrive<2 * kEvenCopies>();
+        else arrive<kEvenCopies>();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = r0 + 16 * r + n16;
+            const uint32_t at_q = lds + (kQueries + (row >> 5)) * (uint32_t)sizeof(sm.row[0]) + (row & 31) * 128 + ((g16 ^ place(row & 31)) << 4);
+#pragma unroll
+            for (int ks = 0; ks < kRow / 32; ++ks) q[r][ks] = read8((at_q ^ ((ks & 1) << 6)) + (ks >> 1) * kSub);
+        }
+        if (count > 1) arrive<kEvenCopies>();
+        else arrive<0>();
 #pragma unroll 1
         for (int i = 0; i <= count; ++i) {
             feed.ahead(a, sm, i, count, tid);
@@ -362,6 +402,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
                     // Waited for here, once a segment: at their uses, every step would wait, and with
                     // them for the copies.
                     begin_segment();
+                    load_queries();
                     asm volatile("" ::: "memory");
                     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
                     asm volatile("" ::: "memory");
@@ -444,6 +485,8 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
             }
         };
         reset();
+        if (count > 1) arrive<2 * kOddCopies>();
+        else arrive<kOddCopies>();
         if (count > 1) arrive<kOddCopies>();
         else arrive<0>();
 #pragma unroll 1
