@@ -6,10 +6,10 @@
 // and as values (their first 512): 1152 bytes for 2 x 64 x 1088 operations a row.
 //
 // With 32 rows the cache's bytes are the bound: 64 requests of 4096 rows, 32 heads, take
-// 55 us for 286 MB, 7 of them until the first rows are there, and their joining 7.  With 64
+// 57 us for 286 MB, 7 of them until the first rows are there, and their joining 7.  With 64
 // rows a step's chain of scores, exponentials and barrier takes 1.3 us, for which its rows
 // come at 7 TB/s: enough where a sequence has one row tile; with two, one request of 131072
-// rows and 128 heads takes 52 us and its joining 8 (its bytes 25).
+// rows and 128 heads takes 53 to 60 us and its joining 8 (its bytes 25).
 //
 // Steps (32 cached rows of one row tile) of all sequences are lined up and shared out
 // evenly among 256 workgroups, one a CU, whatever the lengths (with an allowance for the
