@@ -76,6 +76,9 @@ def test_latent_checks(lib):
     assert latent(lib, "bwd", out_stride_t=-8) == SHAPE and latent(lib, "bwd", d_out_stride_t=4) == ALIGN
     assert latent(lib, "bwd", workspace_bytes=256) == WORKSPACE and latent(lib, "bwd", workspace=p(20, 8)) == ALIGN
     assert latent(lib, "fwd", {"cu": p(9)}, B=1, num_seqs=2, workspace_bytes=8) == WORKSPACE
+    # few queries with many keys: the parts of their keys
+    assert latent(lib, "fwd", T=1, Tk=9000, H=1, workspace_bytes=256) == WORKSPACE
+    assert latent(lib, "fwd", T=1, Tk=9000, H=1, workspace=p(20, 8)) == ALIGN
 
 
 def test_latent_workspaces(lib):
