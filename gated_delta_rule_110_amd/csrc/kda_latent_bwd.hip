@@ -268,16 +268,12 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t place, DqS
         for (int d = 0; d < kQk / 32; ++d) leave(part_of<kQk / 32>(a, place, wave, d), f.dq[d], a.scale);
         return;
     }
-    if (i >= sp.lq) return;
-    uint16_t *out = a.dq + ((sp.b * a.T + sp.q0 + i) * a.H + h) * kQk + 4 * g;
+    __syncthreads();  // the tiles are read
+    char *stage = reinterpret_cast<char *>(&sm) + wave * 32 * 2 * kQk;
+    static_assert(sizeof(sm) >= 4 * 32 * 2 * kQk, "");
 #pragma unroll
-    for (int d = 0; d < kQk / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const u2v w = {pack2(f.dq[d][4 * e] * a.scale, f.dq[d][4 * e + 1] * a.scale),
-                           pack2(f.dq[d][4 * e + 2] * a.scale, f.dq[d][4 * e + 3] * a.scale)};
-            *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = w;
-        }
+    for (int d = 0; d < kQk / 32; ++d) stage_values<kQk / 8>(stage, lane, 4 * d, f.dq[d], a.scale);
+    store_rows<kQk / 8>(stage, lane, a.dq + ((sp.b * a.T + sp.q0 + q_first) * a.H + h) * kQk, a.H * kQk, sp.lq - q_first);
 }
 
 __global__ __launch_bounds__(256, 1) void latent_dq_kernel(LatentArgs a) {
@@ -496,30 +492,25 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t place, Dk
         for (int d = 0; d < kVal / 32; ++d) leave(part_of<kDkvGroups>(a, place, wave, kQk / 32 + d), f.dv[d], 1.0f);
         return;
     }
-    if (j >= sp.lk) return;
-    const int64_t key = sp.b * a.Tk + sp.k0 + j;
-    uint16_t *out = a.dkv + (key * a.H + h) * kKvRow + 4 * g;
-    float *part = a.dpe_part + (h * a.B * a.Tk + key) * kPe + 4 * g;
+    __syncthreads();  // the tiles are read
+    char *stage = reinterpret_cast<char *>(&sm) + wave * 32 * 2 * kKvRow;
+    static_assert(sizeof(sm) >= 4 * 32 * 2 * kKvRow, "");
+    const int64_t key = sp.b * a.Tk + sp.k0 + k_first;
 #pragma unroll
-    for (int d = 0; d < kQk / 32; ++d)
+    for (int d = 0; d < kNope / 32; ++d) stage_values<kKvRow / 8>(stage, lane, 4 * d, f.dk[d], a.scale);
+#pragma unroll
+    for (int d = 0; d < kVal / 32; ++d) stage_values<kKvRow / 8>(stage, lane, kNope / 8 + 4 * d, f.dv[d], 1.0f);
+    store_rows<kKvRow / 8>(stage, lane, a.dkv + (key * a.H + h) * kKvRow, a.H * kKvRow, sp.lk - k_first);
+    if (j >= sp.lk) return;
+    float *part = a.dpe_part + (h * a.B * a.Tk + key + (lane & 31)) * kPe + 4 * g;
+#pragma unroll
+    for (int d = 0; d < kPe / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             f4 x;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = f.dk[d][4 * e + r] * a.scale;
-            if (d < kNope / 32) {
-                const u2v w = {pack2(x[0], x[1]), pack2(x[2], x[3])};
-                *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = w;
-            } else {
-                *reinterpret_cast<f4 *>(part + 32 * (d - kNope / 32) + 8 * e) = x;
-            }
-        }
-#pragma unroll
-    for (int d = 0; d < kVal / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const u2v w = {pack2(f.dv[d][4 * e], f.dv[d][4 * e + 1]), pack2(f.dv[d][4 * e + 2], f.dv[d][4 * e + 3])};
-            *reinterpret_cast<u2v *>(out + kNope + 32 * d + 8 * e) = w;
+            for (int r = 0; r < 4; ++r) x[r] = f.dk[kNope / 32 + d][4 * e + r] * a.scale;
+            *reinterpret_cast<f4 *>(part + 32 * d + 8 * e) = x;
         }
 }
 

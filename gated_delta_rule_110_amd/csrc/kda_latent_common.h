@@ -148,6 +148,33 @@ __device__ __forceinline__ void copy_tile(const uint16_t *p, int rows, uint32_t 
         copy16(rsrc, off + (uint32_t)(i * kRows) * stride, lds + (i * WAVES + wave) * 1024);
 }
 
+// ---- rows that leave a wave ----------------------------------------------------------
+// 32 rows of CHUNKS x 16 bytes are staged in LDS (their own 512 CHUNKS bytes of it) and stored
+// whole: lanes hold 8 bytes of a row at a time, and stored as such rows took 1.3 us longer a
+// workgroup.  Chunk c of row r is at place c ^ (r % 16 or 8).
+template <int CHUNKS>
+__device__ __forceinline__ char *staged(char *stage, int r, int c) {
+    return stage + r * (16 * CHUNKS) + ((c ^ (r & (CHUNKS % 16 == 0 ? 15 : 7))) << 4);
+}
+// Accumulators of 32 values from chunk `first` on, times f, as bf16.
+template <int CHUNKS>
+__device__ __forceinline__ void stage_values(char *stage, int lane, int first, const f16v &v, float f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<u2v *>(staged<CHUNKS>(stage, lane & 31, first + e) + 8 * (lane >> 5)) =
+            u2v{pack2(v[4 * e] * f, v[4 * e + 1] * f), pack2(v[4 * e + 2] * f, v[4 * e + 3] * f)};
+}
+// The first `rows` rows to `out`, `stride` values apart.
+template <int CHUNKS>
+__device__ __forceinline__ void store_rows(char *stage, int lane, uint16_t *out, int64_t stride, int rows) {
+#pragma unroll
+    for (int k = 0; k < CHUNKS / 2; ++k) {
+        const int r = (64 * k + lane) / CHUNKS, c = (64 * k + lane) % CHUNKS;
+        const u4v x = *reinterpret_cast<const u4v *>(staged<CHUNKS>(stage, r, c));
+        if (r < rows) *reinterpret_cast<u4v *>(out + r * stride + 8 * c) = x;
+    }
+}
+
 // ---- a block's sequence ----------------------------------------------------------
 struct Span {
     int64_t q0, k0;  // first query and key, in rows of the tensors' token dimension

@@ -280,20 +280,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
 
     // NaN or infinity among the outputs: perhaps by way of keys that the query does not
     // see.  The block runs again, tile by tile, with those apart.
-    float odd = 0.0f;
+    f4 odd = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int d = 0; d < kVal / 32; ++d)
+    for (int e = 0; e < 16; ++e)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) odd = fmaf(f.o[d][e], 0.0f, odd);
-    uint32_t *flag = reinterpret_cast<uint32_t *>(sm.kn);
+        for (int d = 0; d < kVal / 32; ++d) odd[d] = fmaf(f.o[d][e], 0.0f, odd[d]);
+    static_assert(kVal / 32 == 4, "");
+    uint32_t *flag = reinterpret_cast<uint32_t *>(sm.v[1]);  // behind what the outputs are staged in
     copies_done();
-    if (tid == 0) *flag = 0;
+    const bool found = __builtin_amdgcn_ballot_w64(!((odd[0] + odd[1]) + (odd[2] + odd[3]) == 0.0f)) != 0;
+    if (lane == 0) flag[wave] = found;
     __syncthreads();
-    if (!(odd == 0.0f)) *flag = 1;
-    __syncthreads();
-    const uint32_t again = *flag;
-    __syncthreads();
+    uint32_t again = 0;
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) again |= flag[k];
     if (again) {
+        __syncthreads();
         reset();
         const int block_whole = sees(sp.block * kBlock) / kKeys;
 #pragma unroll 1
@@ -333,18 +335,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
         return;
     }
     const float w = l == 0.0f ? 0.0f : 1.0f / l;
-    if (i >= sp.lq) return;
-    const int64_t row = (sp.b * a.T + sp.q0 + i) * a.H + h;
-    uint16_t *out = a.out + row * kVal + 4 * g;
+    const int64_t row0 = (sp.b * a.T + sp.q0 + q_first) * a.H + h;
+    char *stage = reinterpret_cast<char *>(&sm) + wave * 32 * 2 * kVal;
+    static_assert(sizeof(sm.kn) + sizeof(sm.kp) + sizeof(sm.v[0]) >= 8 * 32 * 2 * kVal, "");
 #pragma unroll
-    for (int d = 0; d < kVal / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const u2v x = {pack2(f.o[d][4 * e] * w, f.o[d][4 * e + 1] * w), pack2(f.o[d][4 * e + 2] * w, f.o[d][4 * e + 3] * w)};
-            *reinterpret_cast<u2v *>(out + 32 * d + 8 * e) = x;
-        }
+    for (int d = 0; d < kVal / 32; ++d) stage_values<kVal / 8>(stage, lane, 4 * d, f.o[d], w);
+    store_rows<kVal / 8>(stage, lane, a.out + row0 * kVal, a.H * kVal, sp.lq - q_first);
     // l == 0: no key is seen
-    if (a.lse && g == 0) a.lse[row] = l == 0.0f ? -INFINITY : (f.mc + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && g == 0 && i < sp.lq) a.lse[row0 + (lane & 31) * a.H] = l == 0.0f ? -INFINITY : (f.mc + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // A block's parts added up in their order: 32 queries and 32 of their values a wave.
