@@ -17,8 +17,8 @@
 // other side each, which are added up in their order by a launch of its own.
 //
 // The matrix instructions bound it, with one wave a SIMD, whose 512 registers hold its sums:
-// 8192 tokens x 32 heads take 982 us for dq (1.12 PFLOP/s), 1212 for dkv (1.13) and 12 for
-// dk_pe; a large matrix product reaches 1.2 to 1.36.
+// 8192 tokens x 32 heads take 982 to 1022 us for dq (1.12 to 1.08 PFLOP/s), 1212 to 1241 for
+// dkv (1.13 to 1.11) and 12 for dk_pe; a large matrix product reaches 1.2 to 1.36.
 //
 // Precision: fp32 but for P and dS, rounded to bf16 for the products they enter (2^-9 of
 // each, as large as the outputs' own rounding); delta and lse are fp32.
