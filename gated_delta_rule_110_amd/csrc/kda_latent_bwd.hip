@@ -20,7 +20,7 @@
 // 8192 tokens x 32 heads take 982 to 1022 us for dq (1.12 to 1.08 PFLOP/s), 1212 to 1241 for
 // dkv (1.13 to 1.11) and 12 for dk_pe; a large matrix product reaches 1.2 to 1.36.
 //
-// Precision: fp32 but for P and dS, rounded to bf16 for the products they enter (2^-9 of
+// Precision: fp32 but for P and dS, rounded to bf16 for the products they enter (at most 2^-8 of
 // each, as large as the outputs' own rounding); delta and lse are fp32.
 #include "kda_latent_common.h"
 

@@ -17,7 +17,7 @@
 // the kernel took 26 us less, without LDS reads 70 and without copies 84 (of 715).
 //
 // Precision: scores, maxima, sums and outputs are fp32.  Probabilities are rounded to
-// bf16 for the second product (2^-9 of each; the outputs' own rounding is as large);
+// bf16 for the second product (at most 2^-8 of each; the outputs' own rounding is as large);
 // the sum, and with it lse, takes them unrounded.
 #include "kda_latent_common.h"
 
