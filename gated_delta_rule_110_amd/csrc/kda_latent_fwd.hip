@@ -386,7 +386,8 @@ __global__ __launch_bounds__(64) void latent_fwd_join_kernel(LatentArgs a) {
 
 // The blocks of a packed batch in order of falling length, by buckets of their tiles'
 // number.  Which of a bucket's blocks comes first is left to chance: it decides when
-// a block runs, not what it computes.
+// a block runs, not what it computes.  Blocks are counted in 64 bits: offsets that
+// overlap, which valid ones do not, describe up to sequences times tokens / size of them.
 constexpr int kBuckets = 1024;
 struct TableArgs {
     const int64_t *cu, *cuk;
@@ -397,8 +398,9 @@ struct TableArgs {
 };
 __global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs by_queries, TableArgs by_keys) {
     const TableArgs &a = blockIdx.x == 0 ? by_queries : by_keys;
-    __shared__ int count[kBuckets];
-    __shared__ int most, part[16];
+    __shared__ unsigned long long count[kBuckets];
+    __shared__ int64_t part[16];
+    __shared__ int most;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int i = tid; i < kBuckets; i += 1024) count[i] = 0;
     if (tid == 0) most = 1;
@@ -447,26 +449,26 @@ __global__ __launch_bounds__(1024) void latent_table_kernel(TableArgs by_queries
             }
         }
     };
-    each([&](int64_t, int lq, int lk, int i) { atomicAdd(&count[work(lq, lk, i) >> shift], 1); });
+    each([&](int64_t, int lq, int lk, int i) { atomicAdd(&count[work(lq, lk, i) >> shift], 1ull); });
     __syncthreads();
     // each bucket's first entry: the blocks of all larger ones
-    const int mine = count[kBuckets - 1 - tid];
-    int upto = mine;
+    const int64_t mine = (int64_t)count[kBuckets - 1 - tid];
+    int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(upto, d);
+        const int64_t o = __shfl_up(upto, d);
         if (lane >= d) upto += o;
     }
     if (lane == 63) part[wave] = upto;
     __syncthreads();
-    int before = 0;
+    int64_t before = 0;
     for (int w = 0; w < wave; ++w) before += part[w];
     count[kBuckets - 1 - tid] = before + upto - mine;
-    if (tid == 1023) a.table[0] = (int)min((int64_t)(before + upto), a.cap);
+    if (tid == 1023) a.table[0] = (int)min(before + upto, a.cap);
     __syncthreads();
     each([&](int64_t n, int lq, int lk, int i) {
-        const int at = atomicAdd(&count[work(lq, lk, i) >> shift], 1);
-        if (at >= a.cap) return;  // sequences that overlap, which valid offsets do not describe
+        const int64_t at = (int64_t)atomicAdd(&count[work(lq, lk, i) >> shift], 1ull);
+        if (at >= a.cap) return;  // sequences that overlap
         a.table[2 + 2 * at] = (int)n;
         a.table[3 + 2 * at] = i;
     });
