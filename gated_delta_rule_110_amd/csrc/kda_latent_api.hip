@@ -87,10 +87,11 @@ struct LatentFwdPlan {
 };
 // Few blocks with many keys leave CUs idle: their keys are split into parts, of at least
 // kPartTiles tiles, so that there are some 256 workgroups, and joined by a second kernel
-// (512 tokens x 8 heads over 16384 keys 280 -> 62 us, 2048 x 2 over their own 41 -> 23; with
-// 11 tiles, 700 x 1, they would take 21 instead of 18; 512 workgroups take 6% more or less).
+// (512 tokens x 8 heads over 16384 keys 280 -> 62 us, 2048 x 2 over their own 41 -> 23; 512
+// workgroups take 6% more or less).  A packed batch, whose lengths the host does not know, is
+// planned as if every block saw all keys; the kernels size the parts by the sequence (part_tiles_of).
 kda_status_t plan_latent_fwd(const kda_latent_desc_t *d, bool packed, LatentFwdPlan &p) {
-    constexpr int64_t kPartTiles = 8, kFewTiles = 12, kFewUnits = 128, kUnits = 256;
+    constexpr int64_t kFewUnits = 128, kUnits = 256;
     p = LatentFwdPlan{};
     p.block = kda_latent_block(d->B, d->T, d->H, d->num_seqs);
     p.blocks = blocks_of(d->T, p.block, d->num_seqs, packed);
@@ -103,7 +104,7 @@ kda_status_t plan_latent_fwd(const kda_latent_desc_t *d, bool packed, LatentFwdP
     const int64_t units = p.blocks * d->B * d->H, tiles = (d->Tk + kKeys - 1) / kKeys;
     if (units > kFewUnits || tiles <= kFewTiles) return KDA_OK;
     const int64_t even = (units * tiles + kUnits - 1) / kUnits;
-    p.part_tiles = (int)(std::max(kPartTiles, even) + 1) / 2 * 2;
+    p.part_tiles = (int)(std::max<int64_t>(kPartTiles, even) + 1) / 2 * 2;
     p.parts = (tiles + p.part_tiles - 1) / p.part_tiles;
     if (p.parts < 2) return KDA_OK;  // part_tiles may be all of them
     p.off_part = p.off_stat + align_up((size_t)(units * p.parts) * p.block * 8, 256);
@@ -193,11 +194,11 @@ kda_status_t plan_latent_bwd(const kda_latent_desc_t *d, bool packed, LatentBwdP
     // Few blocks are split as in the forward, here by a common number of tiles of the other side, for some
     // 256 workgroups, all that run at once (4096 tokens x 2 heads 136 -> 90 us, with 512 of them 102; 512
     // tokens of one head over 8512 keys 209 -> 42).
-    constexpr int64_t kPartTiles = 8, kFewTiles = 12, kFewUnits = 128, kUnits = 256;
+    constexpr int64_t kFewUnits = 128, kUnits = 256;
     const int64_t q_units = p.q_blocks * d->B * d->H, k_units = p.k_blocks * d->B * d->H;
     const int64_t q_tiles = (d->T + kKeys - 1) / kKeys, k_tiles = (d->Tk + kKeys - 1) / kKeys;
     if (q_units + k_units > kFewUnits || std::max(q_tiles, k_tiles) <= kFewTiles) return KDA_OK;
-    p.part_tiles = (int)std::max(kPartTiles, (q_units * k_tiles + k_units * q_tiles + kUnits - 1) / kUnits);
+    p.part_tiles = (int)std::max<int64_t>(kPartTiles, (q_units * k_tiles + k_units * q_tiles + kUnits - 1) / kUnits);
     p.q_parts = std::max<int64_t>(1, (k_tiles + p.part_tiles - 1) / p.part_tiles);
     p.k_parts = std::max<int64_t>(1, (q_tiles + p.part_tiles - 1) / p.part_tiles);
     p.off_k = p.off_q + (size_t)(q_units * p.q_parts) * kLatentBwdBlock * kQk * 4;

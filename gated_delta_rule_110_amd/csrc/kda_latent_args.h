@@ -9,6 +9,9 @@ constexpr int kNope = 128, kPe = 64, kQk = kNope + kPe;   // a head's own key va
 constexpr int kVal = 128, kKvRow = kNope + kVal;          // a head's values, its row of kv
 constexpr int kLat = 512, kRow = kLat + kPe;              // the latent, a cached row
 constexpr int kKeys = 64;                                 // keys (or queries) of a tile in LDS
+// Blocks of few of them have their tiles split into parts of at least kPartTiles; up to kFewTiles are
+// not worth a second kernel (700 queries of one head over their own 11 tiles would take 21 us instead of 18).
+constexpr int kPartTiles = 8, kFewTiles = 12;
 
 struct LatentArgs {
     const uint16_t *q, *kv, *pe;
@@ -22,8 +25,9 @@ struct LatentArgs {
     uint16_t *out;
     float *lse;
     int64_t launch_cap, base;  // base: first workgroup of this launch; set by the launcher
-    // parts (1: none) of part_tiles tiles of the other side that a block's work may be split in; what each
-    // leaves of its 128 tokens: accumulators, and in the forward (maximum, sum)
+    // parts (1: none) of part_tiles tiles of the other side that a block's work may be split in (packed: as
+    // many at most, of a number of tiles that goes by the sequence); what each leaves of its 128 tokens:
+    // accumulators, and in the forward (maximum, sum)
     int64_t parts;
     int part_tiles;
     float *part, *part_stat;

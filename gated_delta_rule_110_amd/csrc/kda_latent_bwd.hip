@@ -163,9 +163,10 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t place, DqS
     if (block_last < sp.block * kBlock) return;
     const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
     const int all = (sees(block_last) + kKeys - 1) / kKeys;
-    const int t0 = SPLIT ? (int)(place - unit * a.parts) * a.part_tiles : 0;
+    const int part_tiles = SPLIT ? part_tiles_of(a, (sp.lk + kKeys - 1) / kKeys) : 0;
+    const int t0 = SPLIT ? (int)(place - unit * a.parts) * part_tiles : 0;
     if (SPLIT && t0 >= max(all, 1)) return;
-    const int tiles = SPLIT ? min(all, t0 + a.part_tiles) : all;
+    const int tiles = SPLIT ? min(all, t0 + part_tiles) : all;
     const int last = min(sp.lq - 1, q_first + 31);
     const int mine = last < q_first ? 0 : min(tiles, (sees(last) + kKeys - 1) / kKeys);  // of this wave
     const int whole = sees(q_first) / 32;                                    // units without hidden keys
@@ -263,7 +264,7 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, int64_t place, DqS
     }
     for (; t < tiles; ++t) begin(t);
 
-    if (SPLIT && all > a.part_tiles) {
+    if (SPLIT && all > part_tiles) {
 #pragma unroll
         for (int d = 0; d < kQk / 32; ++d) leave(part_of<kQk / 32>(a, place, wave, d), f.dq[d], a.scale);
         return;
@@ -387,9 +388,10 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t place, Dk
     const auto seen_from = [&](int j) { return a.causal ? max(0, j - lead) : 0; };
     const int first_all = seen_from(sp.block * kBlock) / kKeys;                // tiles of queries
     const int tiles_all = max(first_all, (sp.lq + kKeys - 1) / kKeys);         // (one behind the last)
-    const int first = SPLIT ? first_all + (int)(place - unit * a.parts) * a.part_tiles : first_all;
+    const int part_tiles = SPLIT ? part_tiles_of(a, (sp.lq + kKeys - 1) / kKeys) : 0;
+    const int first = SPLIT ? first_all + (int)(place - unit * a.parts) * part_tiles : first_all;
     if (SPLIT && first > first_all && first >= tiles_all) return;
-    const int tiles = SPLIT ? min(tiles_all, first + a.part_tiles) : tiles_all;
+    const int tiles = SPLIT ? min(tiles_all, first + part_tiles) : tiles_all;
     const int j = k_first + (lane & 31), row = min(j, sp.lk - 1);
     const int from = seen_from(j);                                    // of the lane's key
     const int top_key = min(k_first + 31, sp.lk - 1);
@@ -485,7 +487,7 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, int64_t place, Dk
         dkv_unit<false>(f, at, st, 1, 0, 0, s1, d1, s0, d0, c);
     }
 
-    if (SPLIT && tiles_all - first_all > a.part_tiles) {
+    if (SPLIT && tiles_all - first_all > part_tiles) {
 #pragma unroll
         for (int d = 0; d < kQk / 32; ++d) leave(part_of<kDkvGroups>(a, place, wave, d), f.dk[d], a.scale);
 #pragma unroll
@@ -566,8 +568,9 @@ __device__ __forceinline__ void join_parts(const LatentArgs &a, int64_t place) {
         const int last = min(sp.lq, first + kBlock) - 1;
         tiles = ((a.causal ? max(0, min(sp.lk, last + 1 + sp.lk - sp.lq)) : sp.lk) + kKeys - 1) / kKeys;
     }
-    if (tiles <= a.part_tiles) return;
-    const int parts = (tiles + a.part_tiles - 1) / a.part_tiles;
+    const int part_tiles = part_tiles_of(a, ((BY_KEYS ? sp.lq : sp.lk) + kKeys - 1) / kKeys);
+    if (tiles <= part_tiles) return;
+    const int parts = (tiles + part_tiles - 1) / part_tiles;
     f4 v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = f4{0.0f, 0.0f, 0.0f, 0.0f};

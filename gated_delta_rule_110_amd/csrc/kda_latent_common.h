@@ -191,6 +191,18 @@ __device__ __forceinline__ void bounds_of(const int64_t *cu, int64_t n, int64_t 
     len = (int)(hi - lo);
 }
 
+// Tiles of a part of a block whose sequence has `tiles` of the other side.  The host plans by the
+// tiles of all sequences together, which are a batch row's own; of a packed batch each sequence is
+// cut into as many parts as one that had all tiles would be (by that one's part 8 sequences of 16 queries over
+// 8208 keys x 4 heads were not split at all: 149 -> 37 us; 4 of 1000 tokens, one head, 22 -> 20, their
+// gradient 50 -> 40).  Even, as the forward has tile j in buffer j % 2.
+__device__ __forceinline__ int part_tiles_of(const LatentArgs &a, int tiles) {
+    if (!a.cu) return a.part_tiles;
+    if (tiles <= kFewTiles) return kFewTiles;
+    const int parts = (int)a.parts;
+    return (max(kPartTiles, (tiles + parts - 1) / parts) + 1) / 2 * 2;
+}
+
 // The sequence and block of unit e (a workgroup's number over the heads); false where
 // there is none.  size: tokens of a block, of the keys with BY_KEYS, else of the queries;
 // reversed: the last blocks, which see the most, come first.  Without a table the blocks

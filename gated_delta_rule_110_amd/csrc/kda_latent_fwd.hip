@@ -192,9 +192,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
 
     const auto sees = [&](int i) { return a.causal ? max(0, min(sp.lk, i + 1 + sp.lk - sp.lq)) : sp.lk; };
     const int all = (sees(block_last) + kKeys - 1) / kKeys;                      // tiles of the block
-    const int t0 = SPLIT ? (int)(place - unit * a.parts) * a.part_tiles : 0;     // even: tile j is in buffer j % 2
+    const int part_tiles = SPLIT ? part_tiles_of(a, (sp.lk + kKeys - 1) / kKeys) : 0;
+    const int t0 = SPLIT ? (int)(place - unit * a.parts) * part_tiles : 0;       // even: tile j is in buffer j % 2
     if (SPLIT && t0 >= max(all, 1)) return;
-    const int tiles = SPLIT ? min(all, t0 + a.part_tiles) : all;                 // (behind the last) of the workgroup
+    const int tiles = SPLIT ? min(all, t0 + part_tiles) : all;                   // (behind the last) of the workgroup
     const int last = min(sp.lq - 1, q_first + 31);
     const int mine = last < q_first ? 0 : min(tiles, (sees(last) + kKeys - 1) / kKeys);  // of this wave
     const int whole = sees(q_first) / kKeys;                                 // of them without hidden keys
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_fwd_kernel(LatentArgs a)
     }
 
     const float l = pair_sum(f.l);
-    if (SPLIT && all > a.part_tiles) {
+    if (SPLIT && all > part_tiles) {
         f4 *y = reinterpret_cast<f4 *>(a.part) + (place * WAVES + wave) * (kVal / 8 * 64) + lane;
 #pragma unroll
         for (int d = 0; d < kVal / 32; ++d)
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(64) void latent_fwd_join_kernel(LatentArgs a) {
     const int q_first = sp.block * 32 * kWaves + wave * 32, block_last = min(sp.lq, (sp.block + 1) * 32 * kWaves) - 1;
     if (q_first > block_last) return;
     const int keys = a.causal ? max(0, min(sp.lk, block_last + 1 + sp.lk - sp.lq)) : sp.lk, all = (keys + kKeys - 1) / kKeys;
-    const int parts = (all + a.part_tiles - 1) / a.part_tiles;
+    const int part_tiles = part_tiles_of(a, (sp.lk + kKeys - 1) / kKeys), parts = (all + part_tiles - 1) / part_tiles;
     if (parts < 2) return;
     const auto factor = [](float from, float to) { return to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(from - to); };
     f4 o[4];
