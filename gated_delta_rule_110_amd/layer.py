@@ -134,10 +134,18 @@ def _workspace(t: Optional[torch.Tensor], need: int, dev: int, d) -> Optional[to
     return t
 
 
+def _public_stream_of(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# The handle of a device's current stream.  torch.cuda.current_stream makes an object of it first (1.1 us of the 10 of
+# a small call); the name that gives the handle alone is not a public one, so that a torch without it takes the other.
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream_of)
+
+
 def _call(fn, dev: int, *args) -> None:
     """``fn(*args, stream)`` on the current stream of device ``dev``."""
-    # The stream's handle alone; torch.cuda.current_stream makes an object of it (1.1 us of the 10 of a small call).
-    stream = torch._C._cuda_getCurrentRawStream(dev)
+    stream = _stream_of(dev)
     if torch.cuda.current_device() == dev:
         st = fn(*args, stream)
     else:
