@@ -90,7 +90,7 @@ struct PageArgs {
 int kda_latent_block(int64_t B, int64_t T, int64_t H, int64_t seqs);
 // Whether the workgroups (units: blocks times heads) of a packed batch count through its
 // sequences themselves: one launch less where they all run at once, so that it does not matter which
-// comes first (1000 tokens in 7 sequences x 32 heads: 31 -> 24 us).
+// comes first (1000 tokens in 7 sequences x 32 heads: 30 -> 25 us).
 bool kda_latent_counted(int64_t seqs, int64_t units);
 // The tables of a packed batch: blocks of `size` queries and (where keys is given) keys of
 // every sequence, those with the most tiles first.  int32 [2 + 2 blocks].

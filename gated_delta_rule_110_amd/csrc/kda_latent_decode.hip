@@ -205,7 +205,7 @@ __global__ __launch_bounds__(512, 2) void latent_decode_kernel(LatentDecodeArgs 
         all_tiles += sm.wave_tiles[i];
     }
     // A change to other queries within a workgroup takes about as long as kChange steps: where any has
-    // one, as many units without work lie ahead of every row tile (12 sequences of up to 15000 rows x 64: 54
+    // one, as many units without work lie ahead of every row tile (12 sequences of up to 15000 rows x 64: 55
     // -> 44 us; where none has, as with two row tiles of 4096 steps, the units would make it 33 steps a
     // workgroup instead of 32, 66 -> 70 us).
     constexpr int kChange = R == 1 ? 3 : 5;
@@ -695,8 +695,8 @@ hipError_t kda_launch_latent_decode(const LatentDecodeArgs &a, hipStream_t s) {
 
 hipError_t kda_launch_latent_join(const LatentDecodeArgs &a, hipStream_t s) {
     // A row tile has about groups / (N row_tiles) parts: 128 parts of 64 rows take 8 us by eight waves, 28 by
-    // two; with few parts a second wave only costs (64 row tiles of 5 parts, with the steps: 64 -> 63 us; 16
-    // sequences x 128 heads 42 -> 40).
+    // two; with few parts a second wave only costs (64 row tiles of 5 parts: this kernel's and the steps' times
+    // 64 -> 63 us, of a call that takes 68; 16 sequences x 128 heads 42 -> 40).
     const bool many = a.N * a.row_tiles * 16 <= a.groups;
     const int64_t units = a.N * a.row_tiles * a.rows32 * 64;
     return launch_groups(many ? units : units / kJoinWaves, 0, [&](int64_t base, dim3 grid) {

@@ -17,7 +17,12 @@
  * and released on the stream), packed batches described by a device int64
  * cu_seqlens, strides in elements, written tensors contiguous and apart from
  * everything else that the call touches (KDA_ERR_OVERLAP).  Results do not depend
- * on the order in which workgroups run.
+ * on the order in which workgroups run: the same call gives the same bits.  The order in
+ * which a token's sums are added up goes by the sizes of the call, though (batch, heads,
+ * tokens, sequences), so that their last bits may differ from those of a call of other sizes.
+ * Sums are fp32 of probabilities that may stand a common factor of up to 2^8 (expanded form)
+ * or 2^40 (absorbed form) above their value until the sum's end: values (cached latents) of up to
+ * 2^56 in magnitude are safe, larger ones may come out infinite.
  *
  * Activations are bf16.  They are read 16 bytes at a time, at addresses that are
  * multiples of 16 bytes, with strides that are multiples of 8 elements
