@@ -9,7 +9,7 @@ constexpr int kNope = 128, kPe = 64, kQk = kNope + kPe;   // a head's own key va
 constexpr int kVal = 128, kKvRow = kNope + kVal;          // a head's values, its row of kv
 constexpr int kLat = 512, kRow = kLat + kPe;              // the latent, a cached row
 constexpr int kKeys = 64;                                 // keys (or queries) of a tile in LDS
-// Blocks of few of them have their tiles split into parts of at least kPartTiles; up to kFewTiles are
+// Few blocks have their tiles split into parts of at least kPartTiles; up to kFewTiles in all are
 // not worth a second kernel (700 queries of one head over their own 11 tiles would take 21 us instead of 18).
 constexpr int kPartTiles = 8, kFewTiles = 12;
 

@@ -195,10 +195,10 @@ __device__ __forceinline__ void bounds_of(const int64_t *cu, int64_t n, int64_t 
 // tiles of all sequences together, which are a batch row's own; of a packed batch each sequence is
 // cut into as many parts as one that had all tiles would be (by that one's part 8 sequences of 16 queries over
 // 8208 keys x 4 heads were not split at all: 149 -> 37 us; 4 of 1000 tokens, one head, 22 -> 20, their
-// gradient 50 -> 40).  Even, as the forward has tile j in buffer j % 2.
+// gradient 50 -> 40).  (Sequences of up to kFewTiles, too: the joining is launched for all of them; 5 of
+// 768 tokens, one head, take 20.0 us, whole 22.9.)  Even, as the forward has tile j in buffer j % 2.
 __device__ __forceinline__ int part_tiles_of(const LatentArgs &a, int tiles) {
     if (!a.cu) return a.part_tiles;
-    if (tiles <= kFewTiles) return kFewTiles;
     const int parts = (int)a.parts;
     return (max(kPartTiles, (tiles + parts - 1) / parts) + 1) / 2 * 2;
 }
